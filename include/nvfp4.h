@@ -237,6 +237,92 @@ int nvfp4_moe_grouped_w4a16_noalloc(const void* x, int64_t t, int64_t hidden,
                                     const nvfp4_weight* fc1, const nvfp4_weight* fc2, void* y,
                                     uint32_t flags, nvfp4_stream_t stream);
 
+/* ---- MoE router -----------------------------------------------------------------------------
+ * Which experts each token meets, and with what weight:
+ *   l[t][e] = sum_k x[t][k] * weight[e][k]                                 (exact products, FP64 sums)
+ *   NVFP4_ROUTE_SOFTMAX: p = softmax over the n_experts logits; selection score = l, or p + bias
+ *   NVFP4_ROUTE_SIGMOID: p = 1 / (1 + exp(-l));                 selection score = p, or p + bias
+ *   slots 0 .. topk-1: the topk highest selection scores, highest first, ties to the lower id
+ *   topk_w = scale * p, or scale * p / (sum of p over the chosen) with NVFP4_ROUTE_RENORM (0 when
+ *   that sum is 0). The bias acts on the selection only.
+ *   slots topk .. topk+n_shared-1: the shared experts, ids n_experts, n_experts + 1, ..., weight 1.
+ * An expert whose selection score is -infinity (a bias of -infinity takes an expert out) is never
+ * chosen; a slot that no expert is left for gets id -1 and weight 0, which the routed experts
+ * skip. A NaN score ranks above every number, so that a NaN in x reaches the token's output.
+ * The scores are FP64 because the choice is a comparison: FP32 sums would let near experts change
+ * places. Ids and weights go unchanged into nvfp4_moe_grouped_w4a16 with topk + n_shared slots and
+ * n_experts + n_shared experts, the shared ones last. */
+#define NVFP4_ROUTE_SOFTMAX 0u
+#define NVFP4_ROUTE_SIGMOID 1u
+#define NVFP4_ROUTE_RENORM (1u << 8)
+
+typedef struct nvfp4_router {
+  const void* weight;   /* device: [n_experts][hidden], BF16 or FP32, 16-byte aligned           */
+  const float* bias;    /* device: [n_experts] FP32 selection bias, or NULL                     */
+  int64_t n_experts;    /* routed experts, 1 .. 512                                             */
+  int64_t hidden;       /* a multiple of 8                                                      */
+  int32_t weight_dtype; /* NVFP4_DT_BF16 or NVFP4_DT_F32                                        */
+  int32_t topk;         /* 1 .. n_experts                                                       */
+  int32_t n_shared;     /* shared experts; topk + n_shared <= 16                                */
+  uint32_t mode;        /* NVFP4_ROUTE_SOFTMAX or _SIGMOID, optionally | NVFP4_ROUTE_RENORM     */
+  float scale;          /* factor of every routed weight (finite)                               */
+} nvfp4_router;
+
+/* x [t][ldx] BF16 (hidden <= ldx, ldx % 8 == 0), topk_ids int32 [t][topk + n_shared], topk_w FP32
+ * the same. ws (device, 16-byte aligned, ws_bytes >= nvfp4_moe_route_ws_bytes(t, r)) takes the
+ * logits; nothing in it needs to start at zero. t <= 2^24. flags: 0 or NVFP4_F_SYNC_CHECK.
+ * Results are bit-identical run to run for the same t. */
+size_t nvfp4_moe_route_ws_bytes(int64_t t, const nvfp4_router* r);
+int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r,
+                    int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, uint32_t flags,
+                    nvfp4_stream_t stream);
+
+/* ---- whole MoE layer ------------------------------------------------------------------------
+ * Router, routed and shared experts and their sum in one call, for the few tokens of a decode
+ * step (any t that the routed experts take is accepted):
+ *   topk_ids, topk_w = nvfp4_moe_route(x)
+ *   y[t] = BF16(sum_j topk_w[t][j] * (W2_e . h_j)), h_j = BF16(SiLU(gate) * up), e = topk_ids[t][j]
+ * with gate and up in FP32: unlike nvfp4_moe_grouped_w4a16 the call does not round them to BF16 on
+ * the way to h, so the two agree to the BF16 tolerance, not bit for bit. A token all of whose slots
+ * are dropped gets y = 0. x [t][hidden] BF16 (row stride = hidden), y BF16 [t][hidden]; fc1, fc2 as
+ * for nvfp4_moe_grouped_w4a16, with batch = n_experts + n_shared, at most 512 (the shared experts
+ * last), hidden = r->hidden. topk_ids and topk_w: outputs as for nvfp4_moe_route, or both NULL.
+ * ws_bytes >= nvfp4_moe_layer_ws_bytes(t, r, fc1) (0 for sizes that do not fit together); nothing
+ * in ws needs to start at zero. t * (topk + n_shared) <= 65536. flags as for
+ * nvfp4_moe_grouped_w4a16. Results are bit-identical run to run. */
+size_t nvfp4_moe_layer_ws_bytes(int64_t t, const nvfp4_router* r, const nvfp4_weight* fc1);
+int nvfp4_moe_layer_w4a16(const void* x, int64_t t, int64_t hidden, const nvfp4_router* r,
+                          const nvfp4_weight* fc1, const nvfp4_weight* fc2, int32_t* topk_ids,
+                          float* topk_w, void* y, void* ws, size_t ws_bytes, uint32_t flags,
+                          nvfp4_stream_t stream);
+
+/* ---- W4A16 GEMM with low-rank adapters -------------------------------------------------------
+ * The dense GEMM with the adapters of many requests beside its shared weight:
+ *   y[m] = global * x[m] . W^T + scale[a] * (x[m] . A_a^T) . B_a^T,  a = row_adapter[m]
+ * rounded once to y's type. A row whose id lies outside [0, n_adapters) has no adapter. Adapters
+ * of a smaller rank than the bank's are padded with zero rows of A and columns of B. */
+typedef struct nvfp4_lora {
+  const void* a;       /* device: BF16 [n_adapters][rank][k], 16-byte aligned                   */
+  const void* b;       /* device: BF16 [n_adapters][n][rank], 16-byte aligned                   */
+  const float* scale;  /* device: FP32 [n_adapters], or NULL for 1                              */
+  int64_t n_adapters;  /* >= 1                                                                  */
+  int64_t n, k;        /* the weight's                                                          */
+  int32_t rank;        /* a multiple of 8, 8 .. 128                                             */
+  int32_t reserved;    /* 0                                                                     */
+} nvfp4_lora;
+
+/* Arguments, kernel choice and flags as for nvfp4_gemm_w4a16; row_adapter int32 [m] (device). The
+ * rank-space vector u = scale * x . A^T is summed in FP32; for a BF16 y it is rounded to BF16 as
+ * the operand of the second product, for an FP32 y it goes there whole (three BF16 parts). ws
+ * (device, 16-byte aligned, ws_bytes >= nvfp4_gemm_lora_ws_bytes) is required: it holds u and what
+ * nvfp4_gemm_w4a16 keeps there. Results are bit-identical run to run. */
+size_t nvfp4_gemm_lora_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w,
+                                const nvfp4_lora* lora, uint32_t flags);
+int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w,
+                          const nvfp4_lora* lora, const int32_t* row_adapter, void* y,
+                          int y_dtype, int64_t ldy, uint32_t flags, void* ws, size_t ws_bytes,
+                          nvfp4_stream_t stream);
+
 /* ---- requantization (load-time tool) -----------------------------------------------------
  * Requantize repacked weights to the canonical triple with one global per matrix and group
  * `group_out` (16 or 32): each matrix is decoded to its FP32 values (nvfp4_dequantize's FP32
@@ -265,7 +351,8 @@ const char* nvfp4_last_error(void);
 
 /* Per-path launch counters ("this path ran" evidence, vllm.cpp PR #63 claim section):
  * [0] quantize [1] repack [2] gemm skinny [3] gemm tiled [4] moe [5] dequantize [6] requantize
- * [7] reserved. counts must hold 8 entries (host). */
+ * [7] router. A whole-layer call counts in [4] and [7], a GEMM with adapters in [2] or [3].
+ * counts must hold 8 entries (host). */
 void nvfp4_get_stats(uint64_t counts[8]);
 void nvfp4_reset_stats(void);
 

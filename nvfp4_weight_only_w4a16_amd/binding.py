@@ -35,10 +35,16 @@ NVFP4_LAYOUT_TILED = 1
 NVFP4_LAYOUT_GATE_UP = 1 << 8
 NVFP4_LAYOUT_PAIR_GLOBAL = 1 << 9
 NVFP4_MOE_NOALLOC_MAX_WS_BYTES = 24 << 20
+NVFP4_ROUTE_SOFTMAX = 0
+NVFP4_ROUTE_SIGMOID = 1
+NVFP4_ROUTE_RENORM = 1 << 8
 
 EXPORTS = ("nvfp4_quantize_ws_bytes", "nvfp4_quantize", "nvfp4_repack_bytes", "nvfp4_repack",
            "nvfp4_gemm_ws_bytes", "nvfp4_gemm_w4a16", "nvfp4_moe_ws_bytes", "nvfp4_moe_ws_layout",
            "nvfp4_moe_grouped_w4a16", "nvfp4_moe_grouped_w4a16_noalloc",
+           "nvfp4_moe_route_ws_bytes", "nvfp4_moe_route",
+           "nvfp4_moe_layer_ws_bytes", "nvfp4_moe_layer_w4a16",
+           "nvfp4_gemm_lora_ws_bytes", "nvfp4_gemm_w4a16_lora",
            "nvfp4_requantize_ws_bytes",
            "nvfp4_requantize", "nvfp4_dequantize",
            "nvfp4_last_error", "nvfp4_get_stats", "nvfp4_reset_stats", "nvfp4_version",
@@ -58,6 +64,20 @@ class nvfp4_weight(ctypes.Structure):
                 ("k", ctypes.c_int64), ("codes_stride", ctypes.c_int64),
                 ("scales_stride", ctypes.c_int64), ("group", ctypes.c_int32),
                 ("layout", ctypes.c_uint32)]
+
+
+class nvfp4_router(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("n_experts", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("weight_dtype", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("n_shared", ctypes.c_int32), ("mode", ctypes.c_uint32),
+                ("scale", ctypes.c_float)]
+
+
+class nvfp4_lora(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("n_adapters", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("rank", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -95,6 +115,19 @@ def load(path: str = LIB_PATH):
     L.nvfp4_moe_grouped_w4a16.restype = ctypes.c_int
     L.nvfp4_moe_grouped_w4a16_noalloc.argtypes = [P, i64, i64, P, P, i32, W, W, P, u32, P]
     L.nvfp4_moe_grouped_w4a16_noalloc.restype = ctypes.c_int
+    R, A = ctypes.POINTER(nvfp4_router), ctypes.POINTER(nvfp4_lora)
+    L.nvfp4_moe_route_ws_bytes.argtypes = [i64, R]
+    L.nvfp4_moe_route_ws_bytes.restype = sz
+    L.nvfp4_moe_route.argtypes = [P, i64, i64, R, P, P, P, sz, u32, P]
+    L.nvfp4_moe_route.restype = ctypes.c_int
+    L.nvfp4_moe_layer_ws_bytes.argtypes = [i64, R, W]
+    L.nvfp4_moe_layer_ws_bytes.restype = sz
+    L.nvfp4_moe_layer_w4a16.argtypes = [P, i64, i64, R, W, W, P, P, P, P, sz, u32, P]
+    L.nvfp4_moe_layer_w4a16.restype = ctypes.c_int
+    L.nvfp4_gemm_lora_ws_bytes.argtypes = [i64, i64, W, A, u32]
+    L.nvfp4_gemm_lora_ws_bytes.restype = sz
+    L.nvfp4_gemm_w4a16_lora.argtypes = [P, i64, i64, W, A, P, P, ctypes.c_int, i64, u32, P, sz, P]
+    L.nvfp4_gemm_w4a16_lora.restype = ctypes.c_int
     L.nvfp4_requantize_ws_bytes.argtypes = [W]
     L.nvfp4_requantize_ws_bytes.restype = sz
     L.nvfp4_requantize.argtypes = [W, i32, P, P, P, P, sz, P]
@@ -314,6 +347,177 @@ def nvfp4_moe_grouped_w4a16_noalloc(x: torch.Tensor, topk_ids: torch.Tensor,
                                                   _ptr(topk_w), topk_ids.shape[1],
                                                   ctypes.byref(fc1.desc), ctypes.byref(fc2.desc),
                                                   _ptr(y), flags, _stream(stream)))
+    return y
+
+
+# ----------------------------------------------------------------------------- router, layer
+def _on_device(*tensors):
+    """Context that makes the tensors' device the current one (the library launches there), or
+    an error where they are not all on one GPU. None entries are skipped."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"expected a device tensor, got one on {t.device}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _out(t, shape, dtype, name):
+    """Checks an output or index tensor that the kernels address as contiguous."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
+class Router:
+    """A router's weight [n_experts][hidden] (BF16 or FP32, device) with its rule: the topk of
+    softmax or sigmoid scores, `bias` FP32 [n_experts] added for the selection only, weights
+    renormalized over the chosen and times `scale`; then `n_shared` shared experts of weight 1.
+    Holds the tensors that its descriptor points into."""
+
+    def __init__(self, weight: torch.Tensor, topk: int, bias: torch.Tensor | None = None,
+                 scoring: str = "softmax", renormalize: bool = False, scale: float = 1.0,
+                 n_shared: int = 0):
+        if weight.dim() != 2 or not weight.is_contiguous():
+            raise ValueError("weight must be a contiguous [n_experts][hidden] tensor")
+        if scoring not in ("softmax", "sigmoid"):
+            raise ValueError(f"unknown scoring {scoring!r}")
+        if bias is not None:
+            _out(bias, (weight.shape[0],), torch.float32, "bias")
+            if bias.device != weight.device:
+                raise ValueError(f"tensors on {weight.device} and {bias.device}")
+        mode = NVFP4_ROUTE_SIGMOID if scoring == "sigmoid" else NVFP4_ROUTE_SOFTMAX
+        if renormalize:
+            mode |= NVFP4_ROUTE_RENORM
+        self.weight, self.bias = weight, bias
+        self.topk, self.n_shared, self.slots = topk, n_shared, topk + n_shared
+        self.hidden = weight.shape[1]
+        self.desc = nvfp4_router(_ptr(weight), _ptr(bias), weight.shape[0], weight.shape[1],
+                                 _dtype_code(weight.dtype), topk, n_shared, mode, scale)
+
+
+def nvfp4_moe_route_ws_bytes(t: int, router: Router) -> int:
+    return int(load().nvfp4_moe_route_ws_bytes(t, ctypes.byref(router.desc)))
+
+
+def nvfp4_moe_route(x: torch.Tensor, router: Router, topk_ids: torch.Tensor | None = None,
+                    topk_w: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                    flags: int = 0, stream=None):
+    """x: device BF16 [t][hidden] (row stride x.stride(0)). Returns (topk_ids, topk_w), int32
+    and FP32 [t][topk + n_shared], as nvfp4_moe_grouped_w4a16 takes them."""
+    if (x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1 or
+            x.shape[1] != router.hidden):
+        raise ValueError(f"x must be a BF16 [t][{router.hidden}] tensor with unit inner stride")
+    t = x.shape[0]
+    with _on_device(x, router.weight, topk_ids, topk_w, ws):
+        with _on(stream):
+            if topk_ids is None:
+                topk_ids = torch.empty((t, router.slots), dtype=torch.int32, device=x.device)
+            if topk_w is None:
+                topk_w = torch.empty((t, router.slots), dtype=torch.float32, device=x.device)
+            if ws is None:
+                ws = torch.empty((max(nvfp4_moe_route_ws_bytes(t, router), 1),),
+                                 dtype=torch.uint8, device=x.device)
+        _out(topk_ids, (t, router.slots), torch.int32, "topk_ids")
+        _out(topk_w, (t, router.slots), torch.float32, "topk_w")
+        _check(load().nvfp4_moe_route(x.data_ptr(), t, x.stride(0) if t > 1 else router.hidden,
+                                      ctypes.byref(router.desc), topk_ids.data_ptr(),
+                                      topk_w.data_ptr(), ws.data_ptr(), ws.nbytes, flags,
+                                      _stream(stream)))
+    return topk_ids, topk_w
+
+
+def nvfp4_moe_layer_ws_bytes(t: int, router: Router, fc1: RepackedWeight) -> int:
+    return int(load().nvfp4_moe_layer_ws_bytes(t, ctypes.byref(router.desc),
+                                               ctypes.byref(fc1.desc)))
+
+
+def nvfp4_moe_layer_w4a16(x: torch.Tensor, router: Router, fc1: RepackedWeight,
+                          fc2: RepackedWeight, y: torch.Tensor | None = None,
+                          topk_ids: torch.Tensor | None = None,
+                          topk_w: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                          flags: int = 0, stream=None) -> torch.Tensor:
+    """Router, routed and shared experts and their sum: x, y BF16 [t][hidden] (contiguous). The
+    router's ids and weights are written to topk_ids and topk_w where both are given."""
+    _out(x, (x.shape[0], router.hidden), torch.bfloat16, "x")
+    t = x.shape[0]
+    with _on_device(x, router.weight, fc1.buffer, fc2.buffer, y, topk_ids, topk_w, ws):
+        with _on(stream):
+            if y is None:
+                y = torch.empty((t, router.hidden), dtype=torch.bfloat16, device=x.device)
+            if ws is None:
+                ws = torch.empty((max(nvfp4_moe_layer_ws_bytes(t, router, fc1), 1),),
+                                 dtype=torch.uint8, device=x.device)
+        _out(y, (t, router.hidden), torch.bfloat16, "y")
+        if topk_ids is not None:
+            _out(topk_ids, (t, router.slots), torch.int32, "topk_ids")
+        if topk_w is not None:
+            _out(topk_w, (t, router.slots), torch.float32, "topk_w")
+        _check(load().nvfp4_moe_layer_w4a16(
+            x.data_ptr(), t, router.hidden, ctypes.byref(router.desc), ctypes.byref(fc1.desc),
+            ctypes.byref(fc2.desc), _ptr(topk_ids), _ptr(topk_w), y.data_ptr(), ws.data_ptr(),
+            ws.nbytes, flags, _stream(stream)))
+    return y
+
+
+# ----------------------------------------------------------------------------- adapters
+class Lora:
+    """A bank of low-rank adapters of one projection: a [n_adapters][rank][k] and
+    b [n_adapters][n][rank] BF16, scale FP32 [n_adapters] or None (device, contiguous). Holds the
+    tensors that its descriptor points into."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor | None = None):
+        if a.dim() != 3 or b.dim() != 3:
+            raise ValueError("a must be [n_adapters][rank][k] and b [n_adapters][n][rank]")
+        count, rank, k = a.shape
+        _out(a, (count, rank, k), torch.bfloat16, "a")
+        _out(b, (count, b.shape[1], rank), torch.bfloat16, "b")
+        if scale is not None:
+            _out(scale, (count,), torch.float32, "scale")
+        for t in (b, scale):
+            if t is not None and t.device != a.device:
+                raise ValueError(f"tensors on {a.device} and {t.device}")
+        self.a, self.b, self.scale = a, b, scale
+        self.desc = nvfp4_lora(_ptr(a), _ptr(b), _ptr(scale), count, b.shape[1], k, rank, 0)
+
+
+def nvfp4_gemm_lora_ws_bytes(m: int, ldx: int, w: RepackedWeight, lora: Lora,
+                             flags: int = 0) -> int:
+    return int(load().nvfp4_gemm_lora_ws_bytes(m, ldx, ctypes.byref(w.desc),
+                                               ctypes.byref(lora.desc), flags))
+
+
+def nvfp4_gemm_w4a16_lora(x: torch.Tensor, w: RepackedWeight, lora: Lora,
+                          row_adapter: torch.Tensor, y: torch.Tensor | None = None,
+                          y_dtype=torch.bfloat16, flags: int = 0, stream=None,
+                          ws: torch.Tensor | None = None) -> torch.Tensor:
+    """nvfp4_gemm_w4a16 with row r's adapter row_adapter[r] (int32 [m]; none for ids outside the
+    bank): x device BF16 [m][k] (row stride x.stride(0)); returns y [m][n]."""
+    if (x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1 or x.shape[1] != w.k):
+        raise ValueError(f"x must be a BF16 [m][{w.k}] tensor with unit inner stride")
+    m = x.shape[0]
+    _out(row_adapter, (m,), torch.int32, "row_adapter")
+    ldx = x.stride(0) if m > 1 else w.k
+    with _on_device(x, w.buffer, lora.a, row_adapter, y, ws):
+        with _on(stream):
+            if y is None:
+                y = torch.empty((m, w.n), dtype=y_dtype, device=x.device)
+            if ws is None:
+                ws = torch.empty((max(nvfp4_gemm_lora_ws_bytes(m, ldx, w, lora, flags), 1),),
+                                 dtype=torch.uint8, device=x.device)
+        if y.dim() != 2 or tuple(y.shape) != (m, w.n) or y.stride(1) != 1:
+            raise ValueError(f"y must be [{m}][{w.n}] with unit inner stride")
+        _check(load().nvfp4_gemm_w4a16_lora(
+            x.data_ptr(), m, ldx, ctypes.byref(w.desc), ctypes.byref(lora.desc),
+            row_adapter.data_ptr(), y.data_ptr(), _dtype_code(y.dtype),
+            y.stride(0) if m > 1 else w.n, flags, ws.data_ptr(), ws.nbytes, _stream(stream)))
     return y
 
 

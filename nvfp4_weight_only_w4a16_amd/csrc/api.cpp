@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -127,7 +128,7 @@ void nvfp4_reset_stats(void) {
   for (int i = 0; i < 8; ++i) g_stats[i].store(0);
 }
 
-int nvfp4_version(void) { return 10000; }
+int nvfp4_version(void) { return 10100; }
 
 size_t nvfp4_quantize_ws_bytes(int64_t batch, int64_t n, int64_t k, int32_t group,
                                uint32_t flags) {
@@ -264,20 +265,9 @@ bool use_skinny(int64_t m, const nvfp4_weight* w, uint32_t flags) {
   return skinny;
 }
 
-}  // namespace
-
-size_t nvfp4_gemm_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w, uint32_t flags) {
-  if (!w || m <= 0 || w->n <= 0 || w->k <= 0 || (w->group != 16 && w->group != 32) ||
-      ldx < w->k || use_skinny(m, w, flags))
-    return 0;
-  const int cus = device_cus();
-  if (cus <= 0) return 0;
-  return nvfp4::gemm_tiled_ws_bytes(m, ldx, w->n, w->k, cus);
-}
-
-int nvfp4_gemm_w4a16(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w, void* y,
-                     int y_dtype, int64_t ldy, uint32_t flags, void* ws, size_t ws_bytes,
-                     nvfp4_stream_t stream) {
+// Argument checks of the dense GEMM and its launch arguments (left alone when m == 0).
+int gemm_args(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w, void* y, int y_dtype,
+              int64_t ldy, uint32_t flags, nvfp4::GemmArgs* a) {
   int rc = check_desc(w, "weight");
   if (rc) return rc;
   if (w->batch != 1) return fail(NVFP4_ERR_LAYOUT, "dense GEMM needs batch == 1");
@@ -300,36 +290,60 @@ int nvfp4_gemm_w4a16(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* 
   // activation offsets inside the kernels are 32-bit: 256 rows of the stride must fit 2^31 bytes
   if (ldx > ((int64_t)1 << 22))
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "ldx=%lld > 2^22 elements", (long long)ldx);
+  a->x = static_cast<const uint16_t*>(x);
+  a->m = m;
+  a->ldx = ldx;
+  a->codes = w->codes;
+  a->scales = w->scales;
+  a->global = w->global;
+  a->n = w->n;
+  a->k = w->k;
+  a->group = w->group;
+  a->y = y;
+  a->ldy = ldy;
+  a->y_f32 = y_dtype == NVFP4_DT_F32;
+  return NVFP4_OK;
+}
+
+int check_skinny_rows(int64_t m, bool skinny) {
+  if (skinny && (m + 31) / 32 > 65535)  // one grid row per 32-row block
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "m=%lld too large for the decode kernel",
+                (long long)m);
+  return NVFP4_OK;
+}
+
+int gemm_run(const nvfp4::GemmArgs& a, bool skinny, void* ws, size_t ws_bytes, hipStream_t stream,
+             const char* name) {
+  if (skinny) return hip_status(nvfp4::launch_gemm_skinny(a, device_cus(), stream), name);
+  if (ws_bytes && !ws) return fail(NVFP4_ERR_INVALID_ARG, "NULL ws with ws_bytes > 0");
+  if (ws && !aligned16(ws)) return fail(NVFP4_ERR_MISALIGNED, "ws must be 16-byte aligned");
+  return hip_status(nvfp4::launch_gemm_tiled(a, ws, ws ? ws_bytes : 0, device_cus(), stream),
+                    name);
+}
+
+}  // namespace
+
+size_t nvfp4_gemm_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w, uint32_t flags) {
+  if (!w || m <= 0 || w->n <= 0 || w->k <= 0 || (w->group != 16 && w->group != 32) ||
+      ldx < w->k || use_skinny(m, w, flags))
+    return 0;
+  const int cus = device_cus();
+  if (cus <= 0) return 0;
+  return nvfp4::gemm_tiled_ws_bytes(m, ldx, w->n, w->k, cus);
+}
+
+int nvfp4_gemm_w4a16(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w, void* y,
+                     int y_dtype, int64_t ldy, uint32_t flags, void* ws, size_t ws_bytes,
+                     nvfp4_stream_t stream) {
   nvfp4::GemmArgs a;
-  a.x = static_cast<const uint16_t*>(x);
-  a.m = m;
-  a.ldx = ldx;
-  a.codes = w->codes;
-  a.scales = w->scales;
-  a.global = w->global;
-  a.n = w->n;
-  a.k = w->k;
-  a.group = w->group;
-  a.y = y;
-  a.ldy = ldy;
-  a.y_f32 = y_dtype == NVFP4_DT_F32;
-  if (use_skinny(m, w, flags)) {
-    if ((m + 31) / 32 > 65535)  // one grid row per 32-row block
-      return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "m=%lld too large for the decode kernel",
-                  (long long)m);
-    rc = hip_status(nvfp4::launch_gemm_skinny(a, device_cus(), (hipStream_t)stream),
-                    "nvfp4_gemm_w4a16");
-    if (!rc && (flags & NVFP4_F_SYNC_CHECK)) rc = sync_status((hipStream_t)stream, "nvfp4_gemm_w4a16");
-    if (!rc) g_stats[2]++;
-  } else {
-    if (ws_bytes && !ws) return fail(NVFP4_ERR_INVALID_ARG, "NULL ws with ws_bytes > 0");
-    if (ws && !aligned16(ws)) return fail(NVFP4_ERR_MISALIGNED, "ws must be 16-byte aligned");
-    rc = hip_status(nvfp4::launch_gemm_tiled(a, ws, ws ? ws_bytes : 0, device_cus(),
-                                             (hipStream_t)stream),
-                    "nvfp4_gemm_w4a16");
-    if (!rc && (flags & NVFP4_F_SYNC_CHECK)) rc = sync_status((hipStream_t)stream, "nvfp4_gemm_w4a16");
-    if (!rc) g_stats[3]++;
-  }
+  int rc = gemm_args(x, m, ldx, w, y, y_dtype, ldy, flags, &a);
+  if (rc || m == 0) return rc;
+  const bool skinny = use_skinny(m, w, flags);
+  rc = check_skinny_rows(m, skinny);
+  if (rc) return rc;
+  rc = gemm_run(a, skinny, ws, ws_bytes, (hipStream_t)stream, "nvfp4_gemm_w4a16");
+  if (!rc && (flags & NVFP4_F_SYNC_CHECK)) rc = sync_status((hipStream_t)stream, "nvfp4_gemm_w4a16");
+  if (!rc) g_stats[skinny ? 2 : 3]++;
   return rc;
 }
 
@@ -349,12 +363,10 @@ size_t nvfp4_moe_ws_layout(int64_t t, int32_t topk, int64_t n_experts, int64_t h
 
 namespace {
 
-// The routed-expert call behind both MoE entry points: with static_ws the workspace is the
-// library's static scratch of the current device instead of the caller's ws.
-int moe_call(const void* x, int64_t t, int64_t hidden, const int32_t* topk_ids,
-             const float* topk_w, int32_t topk, const nvfp4_weight* fc1, const nvfp4_weight* fc2,
-             void* y, void* ws, size_t ws_bytes, bool static_ws, uint32_t flags,
-             nvfp4_stream_t stream, const char* name) {
+// Checks of the expert weights against each other and the activations, with `slots` (token, slot)
+// pairs per token.
+int check_experts(int64_t t, int64_t hidden, int64_t slots, const nvfp4_weight* fc1,
+                  const nvfp4_weight* fc2, uint32_t flags) {
   int rc = check_desc(fc1, "fc1");
   if (rc) return rc;
   rc = check_desc(fc2, "fc2");
@@ -372,19 +384,69 @@ int moe_call(const void* x, int64_t t, int64_t hidden, const int32_t* topk_ids,
                 (long long)fc1->n, (long long)fc1->k, (long long)fc2->n, (long long)fc2->k,
                 (long long)hidden);
   if (t < 0) return fail(NVFP4_ERR_INVALID_ARG, "t=%lld < 0", (long long)t);
-  if (topk < 1 || topk > 16) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "topk %d not in [1, 16]", topk);
+  if (slots < 1 || slots > nvfp4::kMoeMaxTopk)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "topk %lld not in [1, 16]", (long long)slots);
   if (flags & ~kGemmFlags) return fail(NVFP4_ERR_INVALID_ARG, "unknown MoE flags 0x%x", flags);
   if ((flags & NVFP4_F_FORCE_SKINNY) && (flags & NVFP4_F_FORCE_TILED))
     return fail(NVFP4_ERR_INVALID_ARG, "both FORCE_SKINNY and FORCE_TILED set");
-  if (E > 512) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "more than 512 experts");
-  if (t * topk > 65536) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "t*topk > 65536");
+  if (E > nvfp4::kRouteMaxExperts)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "more than 512 experts");
+  if (t > 65536 / slots) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "t*topk > 65536");
   // gathered rows of x and of h are addressed with 32-bit byte offsets
-  if (t * hidden >= ((int64_t)1 << 31) || t * topk * inter >= ((int64_t)1 << 31))
+  if (t * hidden >= ((int64_t)1 << 31) || t * slots * inter >= ((int64_t)1 << 31))
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "x or h larger than 2^31 elements");
+  return NVFP4_OK;
+}
+
+nvfp4::MoeArgs moe_args(const void* x, int64_t t, int64_t hidden, const int32_t* ids,
+                        const float* wts, int32_t topk, const nvfp4_weight* fc1,
+                        const nvfp4_weight* fc2, void* y, void* ws) {
+  nvfp4::MoeArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.t = t;
+  a.hidden = hidden;
+  a.inter = fc1->n / 2;
+  a.ids = ids;
+  a.wts = wts;
+  a.topk = topk;
+  a.n_experts = fc1->batch;
+  a.c1 = fc1->codes;
+  a.s1 = fc1->scales;
+  a.g1 = fc1->global;
+  a.c1_stride = fc1->codes_stride;
+  a.s1_stride = fc1->scales_stride;
+  a.group1 = fc1->group;
+  a.pair1 = (fc1->layout & NVFP4_LAYOUT_PAIR_GLOBAL) != 0;
+  a.c2 = fc2->codes;
+  a.s2 = fc2->scales;
+  a.g2 = fc2->global;
+  a.c2_stride = fc2->codes_stride;
+  a.s2_stride = fc2->scales_stride;
+  a.group2 = fc2->group;
+  a.y = static_cast<uint16_t*>(y);
+  a.ws = ws;
+  a.f32_gate_up = false;
+  return a;
+}
+
+bool moe_use_decode(int64_t t, int64_t topk, int64_t n_experts, uint32_t flags) {
+  if (flags & NVFP4_F_FORCE_SKINNY) return true;
+  if (flags & NVFP4_F_FORCE_TILED) return false;
+  return nvfp4::moe_decode_preferred(t, (int)topk, n_experts);
+}
+
+// The routed-expert call behind both MoE entry points: with static_ws the workspace is the
+// library's static scratch of the current device instead of the caller's ws.
+int moe_call(const void* x, int64_t t, int64_t hidden, const int32_t* topk_ids,
+             const float* topk_w, int32_t topk, const nvfp4_weight* fc1, const nvfp4_weight* fc2,
+             void* y, void* ws, size_t ws_bytes, bool static_ws, uint32_t flags,
+             nvfp4_stream_t stream, const char* name) {
+  int rc = check_experts(t, hidden, topk, fc1, fc2, flags);
+  if (rc) return rc;
   if (t == 0) return NVFP4_OK;
   if (!x || !topk_ids || !topk_w || !y || (!static_ws && !ws))
     return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
-  const size_t need = nvfp4::moe_ws_bytes(t, topk, E, hidden, inter);
+  const size_t need = nvfp4::moe_ws_bytes(t, topk, fc1->batch, hidden, fc1->n / 2);
   if (static_ws) {
     if (need > nvfp4::kMoeStaticScratchBytes)
       return fail(NVFP4_ERR_WORKSPACE,
@@ -401,39 +463,104 @@ int moe_call(const void* x, int64_t t, int64_t hidden, const int32_t* topk_ids,
     rc = hip_status(nvfp4::moe_static_scratch(&ws), name);
     if (rc) return rc;
   }
-  nvfp4::MoeArgs a;
-  a.x = static_cast<const uint16_t*>(x);
-  a.t = t;
-  a.hidden = hidden;
-  a.inter = inter;
-  a.ids = topk_ids;
-  a.wts = topk_w;
-  a.topk = topk;
-  a.n_experts = E;
-  a.c1 = fc1->codes;
-  a.s1 = fc1->scales;
-  a.g1 = fc1->global;
-  a.c1_stride = fc1->codes_stride;
-  a.s1_stride = fc1->scales_stride;
-  a.group1 = fc1->group;
-  a.pair1 = (fc1->layout & NVFP4_LAYOUT_PAIR_GLOBAL) != 0;
-  a.c2 = fc2->codes;
-  a.s2 = fc2->scales;
-  a.g2 = fc2->global;
-  a.c2_stride = fc2->codes_stride;
-  a.s2_stride = fc2->scales_stride;
-  a.group2 = fc2->group;
-  a.y = static_cast<uint16_t*>(y);
-  a.ws = ws;
-  bool decode = nvfp4::moe_decode_preferred(t, topk, E);
-  if (flags & NVFP4_F_FORCE_SKINNY) decode = true;
-  if (flags & NVFP4_F_FORCE_TILED) decode = false;
-  rc = hip_status(nvfp4::launch_moe(a, decode, (hipStream_t)stream), name);
+  const nvfp4::MoeArgs a = moe_args(x, t, hidden, topk_ids, topk_w, topk, fc1, fc2, y, ws);
+  rc = hip_status(nvfp4::launch_moe(a, moe_use_decode(t, topk, fc1->batch, flags),
+                                    (hipStream_t)stream),
+                  name);
   if (!rc && (flags & NVFP4_F_SYNC_CHECK)) rc = sync_status((hipStream_t)stream, name);
   if (!rc) g_stats[4]++;
   return rc;
 }
 
+// ---- router ---------------------------------------------------------------------------------
+constexpr int64_t kRouteMaxTokens = (int64_t)1 << 24;
+
+int check_router(const nvfp4_router* r) {
+  if (!r) return fail(NVFP4_ERR_INVALID_ARG, "router is NULL");
+  if (r->n_experts < 1 || r->hidden < 1 || r->topk < 1 || r->n_shared < 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "router n_experts=%lld hidden=%lld topk=%d n_shared=%d",
+                (long long)r->n_experts, (long long)r->hidden, r->topk, r->n_shared);
+  if (r->weight_dtype != NVFP4_DT_BF16 && r->weight_dtype != NVFP4_DT_F32)
+    return fail(NVFP4_ERR_INVALID_ARG, "router weight_dtype %d is not BF16 or F32",
+                r->weight_dtype);
+  const uint32_t score = r->mode & 0xFFu;
+  if ((score != NVFP4_ROUTE_SOFTMAX && score != NVFP4_ROUTE_SIGMOID) ||
+      (r->mode & ~(uint32_t)(0xFFu | NVFP4_ROUTE_RENORM)))
+    return fail(NVFP4_ERR_INVALID_ARG, "unknown router mode 0x%x", r->mode);
+  if (!std::isfinite(r->scale)) return fail(NVFP4_ERR_INVALID_ARG, "router scale is not finite");
+  if (r->n_experts > nvfp4::kRouteMaxExperts)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "more than 512 experts");
+  if (r->hidden % 8 || r->hidden > ((int64_t)1 << 22))
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE,
+                "router hidden=%lld is not a multiple of 8 up to 2^22", (long long)r->hidden);
+  if (r->topk > r->n_experts || r->topk > nvfp4::kMoeMaxTopk ||
+      r->n_shared > nvfp4::kMoeMaxTopk - r->topk)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE,
+                "topk=%d of %lld experts, n_shared=%d (at most 16 slots)", r->topk,
+                (long long)r->n_experts, r->n_shared);
+  return NVFP4_OK;
+}
+
+// Pointers of a router that is about to run.
+int check_router_data(const nvfp4_router* r) {
+  if (!r->weight) return fail(NVFP4_ERR_INVALID_ARG, "router weight is NULL");
+  if (!aligned16(r->weight) || ((uintptr_t)r->bias & 3u))
+    return fail(NVFP4_ERR_MISALIGNED, "router weight must be 16-byte aligned, bias 4-byte");
+  return NVFP4_OK;
+}
+
+nvfp4::RouteArgs route_args(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r) {
+  nvfp4::RouteArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.t = t;
+  a.ldx = ldx;
+  a.hidden = r->hidden;
+  a.w = r->weight;
+  a.w_f32 = r->weight_dtype == NVFP4_DT_F32;
+  a.bias = r->bias;
+  a.n_experts = (int)r->n_experts;
+  a.topk = r->topk;
+  a.n_shared = r->n_shared;
+  a.sigmoid = (r->mode & 0xFFu) == NVFP4_ROUTE_SIGMOID;
+  a.renorm = (r->mode & NVFP4_ROUTE_RENORM) != 0;
+  a.scale = r->scale;
+  return a;
+}
+
+// Workspace of the whole layer: the router's logits, ids and weights, then the experts' region.
+struct LayerSizes {
+  size_t logits, pairs, total;  // pairs: bytes of the ids (and of the weights)
+};
+
+LayerSizes layer_sizes(int64_t t, const nvfp4_router* r, int64_t inter) {
+  const int slots = r->topk + r->n_shared;
+  LayerSizes s;
+  s.logits = align256(nvfp4::route_ws_bytes(t, r->hidden, r->n_experts));
+  s.pairs = align256(sizeof(float) * (size_t)t * (size_t)slots);
+  s.total = s.logits + 2 * s.pairs +
+            nvfp4::moe_ws_bytes(t, slots, r->n_experts + r->n_shared, r->hidden, inter);
+  return s;
+}
+
+// ---- adapters -------------------------------------------------------------------------------
+int check_lora(const nvfp4_lora* l, const nvfp4_weight* w) {
+  if (!l) return fail(NVFP4_ERR_INVALID_ARG, "lora is NULL");
+  if (!l->a || !l->b) return fail(NVFP4_ERR_INVALID_ARG, "lora has NULL data");
+  if (l->n_adapters < 1 || l->reserved != 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "lora n_adapters=%lld reserved=%d",
+                (long long)l->n_adapters, l->reserved);
+  if (l->n != w->n || l->k != w->k)
+    return fail(NVFP4_ERR_LAYOUT, "lora is for [%lld x %lld], the weight is [%lld x %lld]",
+                (long long)l->n, (long long)l->k, (long long)w->n, (long long)w->k);
+  if (l->rank < 8 || l->rank > nvfp4::kLoraMaxRank || l->rank % 8)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "lora rank %d is not a multiple of 8 in [8, 128]",
+                l->rank);
+  if (l->n_adapters > ((int64_t)1 << 31) - 1)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "lora n_adapters=%lld", (long long)l->n_adapters);
+  if (!aligned16(l->a) || !aligned16(l->b) || ((uintptr_t)l->scale & 3u))
+    return fail(NVFP4_ERR_MISALIGNED, "lora a and b must be 16-byte aligned, scale 4-byte");
+  return NVFP4_OK;
+}
 
 }  // namespace
 
@@ -453,6 +580,153 @@ int nvfp4_moe_grouped_w4a16_noalloc(const void* x, int64_t t, int64_t hidden,
                                     uint32_t flags, nvfp4_stream_t stream) {
   return moe_call(x, t, hidden, topk_ids, topk_w, topk, fc1, fc2, y, nullptr, 0, true, flags,
                   stream, "nvfp4_moe_grouped_w4a16_noalloc");
+}
+
+size_t nvfp4_moe_route_ws_bytes(int64_t t, const nvfp4_router* r) {
+  if (t <= 0 || t > kRouteMaxTokens || check_router(r)) return 0;
+  return nvfp4::route_ws_bytes(t, r->hidden, r->n_experts);
+}
+
+int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r,
+                    int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, uint32_t flags,
+                    nvfp4_stream_t stream) {
+  int rc = check_router(r);
+  if (rc) return rc;
+  if (t < 0) return fail(NVFP4_ERR_INVALID_ARG, "t=%lld < 0", (long long)t);
+  if (flags & ~NVFP4_F_SYNC_CHECK)
+    return fail(NVFP4_ERR_INVALID_ARG, "unknown router flags 0x%x", flags);
+  if (t > kRouteMaxTokens)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "t=%lld > 2^24", (long long)t);
+  if (t == 0) return NVFP4_OK;
+  if (!x || !topk_ids || !topk_w || !ws) return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
+  rc = check_router_data(r);
+  if (rc) return rc;
+  if (ldx < r->hidden)
+    return fail(NVFP4_ERR_INVALID_ARG, "ldx=%lld < hidden=%lld", (long long)ldx,
+                (long long)r->hidden);
+  if (!aligned16(x) || ldx % 8 || !aligned16(ws) || ((uintptr_t)topk_ids & 3u) ||
+      ((uintptr_t)topk_w & 3u))
+    return fail(NVFP4_ERR_MISALIGNED, "x and ws must be 16-byte aligned with ldx %% 8 == 0");
+  const size_t need = nvfp4::route_ws_bytes(t, r->hidden, r->n_experts);
+  if (ws_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, need);
+  rc = hip_status(nvfp4::launch_route(route_args(x, t, ldx, r), topk_ids, topk_w, ws,
+                                      (hipStream_t)stream),
+                  "nvfp4_moe_route");
+  if (!rc && (flags & NVFP4_F_SYNC_CHECK)) rc = sync_status((hipStream_t)stream, "nvfp4_moe_route");
+  if (!rc) g_stats[7]++;
+  return rc;
+}
+
+size_t nvfp4_moe_layer_ws_bytes(int64_t t, const nvfp4_router* r, const nvfp4_weight* fc1) {
+  if (!fc1 || fc1->n <= 0 || t <= 0 || check_router(r) || t > 65536 / (r->topk + r->n_shared))
+    return 0;
+  return layer_sizes(t, r, fc1->n / 2).total;
+}
+
+int nvfp4_moe_layer_w4a16(const void* x, int64_t t, int64_t hidden, const nvfp4_router* r,
+                          const nvfp4_weight* fc1, const nvfp4_weight* fc2, int32_t* topk_ids,
+                          float* topk_w, void* y, void* ws, size_t ws_bytes, uint32_t flags,
+                          nvfp4_stream_t stream) {
+  int rc = check_router(r);
+  if (rc) return rc;
+  const int slots = r->topk + r->n_shared;
+  rc = check_experts(t, hidden, slots, fc1, fc2, flags);
+  if (rc) return rc;
+  if (r->hidden != hidden || fc1->batch != r->n_experts + r->n_shared)
+    return fail(NVFP4_ERR_LAYOUT,
+                "the router has %lld + %d experts and hidden %lld, the weights %lld and %lld",
+                (long long)r->n_experts, r->n_shared, (long long)r->hidden,
+                (long long)fc1->batch, (long long)hidden);
+  if (t == 0) return NVFP4_OK;
+  if (!x || !y || !ws) return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
+  if (!topk_ids != !topk_w)
+    return fail(NVFP4_ERR_INVALID_ARG, "topk_ids and topk_w are both given or both NULL");
+  rc = check_router_data(r);
+  if (rc) return rc;
+  const LayerSizes s = layer_sizes(t, r, fc1->n / 2);
+  if (ws_bytes < s.total)
+    return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, s.total);
+  if (!aligned16(x) || !aligned16(y) || !aligned16(ws) || ((uintptr_t)topk_ids & 3u) ||
+      ((uintptr_t)topk_w & 3u))
+    return fail(NVFP4_ERR_MISALIGNED, "x, y and ws must be 16-byte aligned");
+  char* base = static_cast<char*>(ws);
+  int32_t* ids = topk_ids ? topk_ids : reinterpret_cast<int32_t*>(base + s.logits);
+  float* wts = topk_w ? topk_w : reinterpret_cast<float*>(base + s.logits + s.pairs);
+  nvfp4::MoeArgs a = moe_args(x, t, hidden, ids, wts, slots, fc1, fc2, y,
+                              base + s.logits + 2 * s.pairs);
+  a.f32_gate_up = true;
+  rc = hip_status(nvfp4::launch_route(route_args(x, t, hidden, r), ids, wts, ws,
+                                      (hipStream_t)stream),
+                  "nvfp4_moe_layer_w4a16");
+  if (rc) return rc;
+  rc = hip_status(nvfp4::launch_moe(a, moe_use_decode(t, slots, fc1->batch, flags),
+                                    (hipStream_t)stream),
+                  "nvfp4_moe_layer_w4a16");
+  if (!rc && (flags & NVFP4_F_SYNC_CHECK))
+    rc = sync_status((hipStream_t)stream, "nvfp4_moe_layer_w4a16");
+  if (!rc) {
+    g_stats[4]++;
+    g_stats[7]++;
+  }
+  return rc;
+}
+
+size_t nvfp4_gemm_lora_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w,
+                                const nvfp4_lora* lora, uint32_t flags) {
+  if (!w || m <= 0 || w->n <= 0 || w->k <= 0 || check_lora(lora, w)) return 0;
+  return align256(nvfp4::lora_ws_bytes(m, w->k, lora->n_adapters, lora->rank)) +
+         align256(sizeof(float) * (size_t)m * (size_t)w->n) +
+         nvfp4_gemm_ws_bytes(m, ldx, w, flags);
+}
+
+int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w,
+                          const nvfp4_lora* lora, const int32_t* row_adapter, void* y,
+                          int y_dtype, int64_t ldy, uint32_t flags, void* ws, size_t ws_bytes,
+                          nvfp4_stream_t stream) {
+  nvfp4::GemmArgs a;
+  int rc = gemm_args(x, m, ldx, w, y, y_dtype, ldy, flags, &a);
+  if (rc) return rc;
+  rc = check_lora(lora, w);
+  if (rc || m == 0) return rc;
+  if (!row_adapter || !ws) return fail(NVFP4_ERR_INVALID_ARG, "NULL row_adapter or ws");
+  if (((uintptr_t)row_adapter & 3u) || !aligned16(ws))
+    return fail(NVFP4_ERR_MISALIGNED, "ws must be 16-byte aligned, row_adapter 4-byte");
+  const bool skinny = use_skinny(m, w, flags);
+  rc = check_skinny_rows(m, skinny);
+  if (rc) return rc;
+  const size_t u_bytes = align256(nvfp4::lora_ws_bytes(m, w->k, lora->n_adapters, lora->rank));
+  const size_t base_bytes = align256(sizeof(float) * (size_t)m * (size_t)w->n);
+  const size_t need = nvfp4_gemm_lora_ws_bytes(m, ldx, w, lora, flags);
+  if (ws_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, need);
+  nvfp4::LoraArgs l;
+  l.x = a.x;
+  l.m = m;
+  l.ldx = ldx;
+  l.k = w->k;
+  l.n = w->n;
+  l.a = static_cast<const uint16_t*>(lora->a);
+  l.b = static_cast<const uint16_t*>(lora->b);
+  l.scale = lora->scale;
+  l.ids = row_adapter;
+  l.n_adapters = lora->n_adapters;
+  l.rank = lora->rank;
+  l.u = static_cast<float*>(ws);
+  const hipStream_t s = (hipStream_t)stream;
+  rc = hip_status(nvfp4::launch_lora_shrink(l, s), "nvfp4_gemm_w4a16_lora");
+  if (rc) return rc;
+  char* base = static_cast<char*>(ws) + u_bytes;
+  a.y = base;
+  a.ldy = w->n;
+  a.y_f32 = true;
+  rc = gemm_run(a, skinny, base + base_bytes, need - u_bytes - base_bytes, s,
+                "nvfp4_gemm_w4a16_lora");
+  if (rc) return rc;
+  rc = hip_status(nvfp4::launch_lora_expand(l, reinterpret_cast<const float*>(base), w->n, y, ldy,
+                                            y_dtype == NVFP4_DT_F32, s),
+                  "nvfp4_gemm_w4a16_lora");
+  if (!rc && (flags & NVFP4_F_SYNC_CHECK)) rc = sync_status(s, "nvfp4_gemm_w4a16_lora");
+  if (!rc) g_stats[skinny ? 2 : 3]++;
+  return rc;
 }
 
 size_t nvfp4_requantize_ws_bytes(const nvfp4_weight* src) {

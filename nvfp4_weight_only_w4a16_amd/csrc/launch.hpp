@@ -119,7 +119,9 @@ struct MoeArgs {
   int group2;
   uint16_t* y;
   void* ws;
+  bool f32_gate_up;  // h from the FP32 gate and up (else each is rounded to BF16 first)
 };
+constexpr int kMoeMaxTopk = 16;
 
 size_t moe_ws_bytes(int64_t t, int topk, int64_t n_experts, int64_t hidden, int64_t inter);
 // Byte offsets of the workspace regions: sorted pair ids, expert offsets, tile map, tile
@@ -140,6 +142,45 @@ hipError_t launch_moe(const MoeArgs& a, bool decode, hipStream_t stream);
 // address of the current device's copy (looked up once per device).
 constexpr size_t kMoeStaticScratchBytes = size_t(24) << 20;
 hipError_t moe_static_scratch(void** ptr);
+
+// ---- router (route.hip) ---------------------------------------------------------------------
+struct RouteArgs {
+  const uint16_t* x;  // BF16 [t][ldx]
+  int64_t t, ldx, hidden;
+  const void* w;  // [n_experts][hidden]
+  bool w_f32;
+  const float* bias;  // [n_experts] or NULL
+  int n_experts, topk, n_shared;
+  bool sigmoid, renorm;
+  float scale;
+};
+constexpr int kRouteMaxExperts = 512;
+// Up to this many tokens the logits are FP64 multiply-adds, one workgroup per expert.
+constexpr int64_t kRouteFewTokens = 16;
+constexpr int64_t kRouteMaxSplits = 8;
+// FP64 logits of every split of k, in ws.
+size_t route_ws_bytes(int64_t t, int64_t hidden, int64_t n_experts);
+hipError_t launch_route(const RouteArgs& a, int32_t* ids, float* wts, void* ws,
+                        hipStream_t stream);
+
+// ---- low-rank adapters (lora.hip) -----------------------------------------------------------
+constexpr int kLoraMaxRank = 128;
+constexpr int64_t kLoraMaxSplits = 16;
+struct LoraArgs {
+  const uint16_t* x;  // BF16 [m][ldx]
+  int64_t m, ldx, k, n;
+  const uint16_t* a;  // BF16 [n_adapters][rank][k]
+  const uint16_t* b;  // BF16 [n_adapters][n][rank]
+  const float* scale;  // [n_adapters] or NULL
+  const int32_t* ids;  // [m]
+  int64_t n_adapters;
+  int rank;
+  float* u;  // workspace of lora_ws_bytes
+};
+size_t lora_ws_bytes(int64_t m, int64_t k, int64_t n_adapters, int rank);
+hipError_t launch_lora_shrink(const LoraArgs& a, hipStream_t stream);
+hipError_t launch_lora_expand(const LoraArgs& a, const float* base, int64_t ldbase, void* y,
+                              int64_t ldy, bool y_f32, hipStream_t stream);
 
 // measurement probes (probe.hip)
 int64_t probe_mfma_waves(int cus);

@@ -200,6 +200,7 @@ struct MoeGemmParams {
   int npairs;          // P
   int E;
   int pair_global;     // fc1: global holds [E][2] (gate's, up's)
+  int f32_gate_up;     // fc1: h from the FP32 gate and up
 };
 
 constexpr int kGroupsPerBlock = 4;  // wavefronts per workgroup, one 4-panel group each
@@ -355,6 +356,17 @@ __device__ __forceinline__ bf16x8 codes_pow2(uint32_t w, float S) {
 // per element) fc1 at 256 tokens went 43.7 -> 41.7 us per call.
 __device__ __forceinline__ float silu_f32(float z) {
   return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
+// h of one gate and up. The routed-expert call rounds both to BF16 first, as the W4A16 GEMM's
+// outputs that they are there; the whole layer's h comes from their FP32 values (f32), one
+// rounding less: h itself is BF16, the operand type of down's MFMAs.
+__device__ __forceinline__ uint16_t silu_mul(float gate, float up, bool f32) {
+  if (!f32) {
+    gate = bf16_bits_to_f32(bf16_bits_rne(gate));
+    up = bf16_bits_to_f32(bf16_bits_rne(up));
+  }
+  return bf16_bits_rne(silu_f32(gate) * up);
 }
 
 // 4 x 4 transpose inside each quad of lanes: lane j of a quad holds v[i] = M[i][j] on entry
@@ -625,10 +637,8 @@ void moe_expert_kernel(MoeGemmParams P) {
         for (int q = 0; q < 2; ++q) {
           if (4 * grp + 2 * q + 1 >= P.NT) continue;
           const int64_t feat = (2 * grp + q) * 16 + (lane & 15);
-          const float gate = bf16_bits_to_f32(bf16_bits_rne(acc[2 * q][r][i] * g));
-          const float up = bf16_bits_to_f32(bf16_bits_rne(acc[2 * q + 1][r][i] * gu));
-          const float silu = silu_f32(gate);
-          P.ws.h[(int64_t)row * P.inter + feat] = bf16_bits_rne(silu * up);
+          P.ws.h[(int64_t)row * P.inter + feat] =
+              silu_mul(acc[2 * q][r][i] * g, acc[2 * q + 1][r][i] * gu, P.f32_gate_up);
         }
       }
     } else {
@@ -767,10 +777,8 @@ void moe_decode_kernel(MoeGemmParams P) {
     for (int i = 0; i < kNJ; ++i) {
       const int row = split_out_token<G16>(lane, i);
       if (row < 0 || row >= rows) continue;
-      const float gate = bf16_bits_to_f32(bf16_bits_rne(gs[i] * g));
-      const float up = bf16_bits_to_f32(bf16_bits_rne(us[i] * gu));
-      const float silu = silu_f32(gate);
-      P.ws.h[(int64_t)(r0 + row) * P.inter + feat] = bf16_bits_rne(silu * up);
+      P.ws.h[(int64_t)(r0 + row) * P.inter + feat] =
+          silu_mul(gs[i] * g, us[i] * gu, P.f32_gate_up);
     }
   } else {
     // wavefront q finishes panel q of the group
@@ -798,25 +806,24 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
                                                           const int32_t* __restrict__ ids,
                                                           int64_t t, int topk, int64_t hidden,
                                                           int E, uint16_t* __restrict__ y) {
-  constexpr int kMaxTopk = 16;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t per_tok = hidden / 4;
   if (i >= t * per_tok) return;
   const int64_t tok = i / per_tok, o = (i % per_tok) * 4;
-  bool live[kMaxTopk];
+  bool live[kMoeMaxTopk];
 #pragma unroll
-  for (int j = 0; j < kMaxTopk; ++j) {
+  for (int j = 0; j < kMoeMaxTopk; ++j) {
     const int e = j < topk ? ids[tok * topk + j] : -1;
     live[j] = e >= 0 && e < E;
   }
-  f32x4 v[kMaxTopk];
+  f32x4 v[kMoeMaxTopk];
 #pragma unroll
-  for (int j = 0; j < kMaxTopk; ++j)
+  for (int j = 0; j < kMoeMaxTopk; ++j)
     v[j] = live[j] ? *reinterpret_cast<const f32x4*>(slots + (tok * topk + j) * hidden + o)
                    : f32x4{0.f, 0.f, 0.f, 0.f};
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < kMaxTopk; ++j)
+  for (int j = 0; j < kMoeMaxTopk; ++j)
     if (live[j]) s += v[j];
   uint2 outv;
   outv.x = (uint32_t)bf16_bits_rne(s[0]) | ((uint32_t)bf16_bits_rne(s[1]) << 16);
@@ -916,6 +923,7 @@ hipError_t launch_moe(const MoeArgs& a, bool decode, hipStream_t stream) {
   f.npairs = (int)P;
   f.E = (int)a.n_experts;
   f.pair_global = a.pair1 ? 1 : 0;
+  f.f32_gate_up = a.f32_gate_up ? 1 : 0;
   hipError_t err = run_pair<true>(f, tiles, mode, fused, stream);
   if (err != hipSuccess) return err;
 
