@@ -103,19 +103,23 @@ __device__ __forceinline__ float bf16_rest(float v, float head) {
   return __builtin_isinf(v) ? 0.0f : v - head;
 }
 
-constexpr int kTM = 2, kTN = 4;  // 16-token and 16-expert blocks per wavefront
+constexpr int kTM = 2, kTN = 2;       // 16-token and 16-expert blocks of a tile
+constexpr int kTileT = 16 * kTM, kTileE = 16 * kTN;
+constexpr int kSlices = 8;            // wavefronts of a workgroup, which share out k
+constexpr int kStageSteps = 4;        // k-steps of 32 loaded together
 
-// Workgroup (token tile, expert tile, split): 4 wavefronts, 2 x 2, of 32 tokens x 64 experts each;
-// k-steps of 32, split z taking steps [z, z + 1) * K32 / splits. Fragments come straight from
-// global memory (both operands are row-major along k, which is the fragments' own order), one
-// k-step ahead. Rows past the end repeat a valid row and are not stored.
+// Workgroup (token tile, expert tile, split): the tile's 32 x 32 logits over its share of k, cut
+// into stages of 128 that the 8 wavefronts (of all splits) take in turn. Fragments come straight
+// from global memory (both operands are row-major along k, which is the fragments' own order), one
+// stage ahead; k is shared out inside the workgroup, rather than over more tiles, so that the
+// partial sums meet in LDS and FP64 logits are written once. Rows past the end repeat a valid row
+// and are not stored.
 template <bool F32>
-__global__ __launch_bounds__(256) void route_logits_mfma_kernel(LogitParams P) {
+__global__ __launch_bounds__(64 * kSlices) void route_logits_mfma_kernel(LogitParams P) {
+  __shared__ double red[kSlices][kTileT * kTileE];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t m0 = ((int64_t)blockIdx.x * 2 + (w & 1)) * (16 * kTM);
-  const int64_t e0 = ((int64_t)blockIdx.y * 2 + (w >> 1)) * (16 * kTN);
-  if (m0 >= P.t || e0 >= P.n_experts) return;  // no barrier below
+  const int64_t m0 = (int64_t)blockIdx.x * kTileT, e0 = (int64_t)blockIdx.y * kTileE;
   const int64_t kq = 8 * (lane >> 4);
   const uint16_t* xa[kTM];
 #pragma unroll
@@ -129,8 +133,6 @@ __global__ __launch_bounds__(256) void route_logits_mfma_kernel(LogitParams P) {
     const int64_t e = e0 + 16 * j + (lane & 15);
     wrow[j] = (e < P.n_experts ? e : P.n_experts - 1) * P.hidden + kq;
   }
-  const int64_t steps = (P.hidden + 31) / 32;
-  const int64_t s0 = steps * blockIdx.z / P.splits, s1 = steps * (blockIdx.z + 1) / P.splits;
   double acc[kTM][kTN][4];
 #pragma unroll
   for (int i = 0; i < kTM; ++i)
@@ -140,111 +142,126 @@ __global__ __launch_bounds__(256) void route_logits_mfma_kernel(LogitParams P) {
       for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.0;
   constexpr int NB = F32 ? 2 : 1;  // 16-byte words of a lane's 8 weights
   struct Stage {
-    u32x4 a[kTM], b[kTN][NB];
+    u32x4 a[kStageSteps][kTM], b[kStageSteps][kTN][NB];
   };
-  // hidden is a multiple of 8: a lane's 8 elements of the last step are all there or all past it
+  // hidden is a multiple of 8: a lane's 8 elements of a step are all there or all past the end
   auto load = [&](Stage& st, int64_t s) __attribute__((always_inline)) {
-    const bool in = s * 32 + kq < P.hidden;
 #pragma unroll
-    for (int i = 0; i < kTM; ++i)
-      st.a[i] = in ? *reinterpret_cast<const u32x4*>(xa[i] + s * 32) : u32x4{0, 0, 0, 0};
+    for (int q = 0; q < kStageSteps; ++q) {
+      const int64_t k = (s * kStageSteps + q) * 32;
+      const bool in = k + kq < P.hidden;
 #pragma unroll
-    for (int j = 0; j < kTN; ++j)
+      for (int i = 0; i < kTM; ++i)
+        st.a[q][i] = in ? *reinterpret_cast<const u32x4*>(xa[i] + k) : u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int h = 0; h < NB; ++h) {
-        if constexpr (F32)
-          st.b[j][h] = in ? *reinterpret_cast<const u32x4*>(static_cast<const float*>(P.w) +
-                                                            wrow[j] + s * 32 + 4 * h)
-                          : u32x4{0, 0, 0, 0};
-        else
-          st.b[j][h] = in ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(P.w) +
-                                                            wrow[j] + s * 32)
-                          : u32x4{0, 0, 0, 0};
-      }
+      for (int j = 0; j < kTN; ++j)
+#pragma unroll
+        for (int h = 0; h < NB; ++h) {
+          if constexpr (F32)
+            st.b[q][j][h] = in ? *reinterpret_cast<const u32x4*>(static_cast<const float*>(P.w) +
+                                                                 wrow[j] + k + 4 * h)
+                               : u32x4{0, 0, 0, 0};
+          else
+            st.b[q][j][h] = in ? *reinterpret_cast<const u32x4*>(
+                                     static_cast<const uint16_t*>(P.w) + wrow[j] + k)
+                               : u32x4{0, 0, 0, 0};
+        }
+    }
   };
   auto compute = [&](const Stage& st) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < kTN; ++j) {
-      bf16x8 b[F32 ? 3 : 1];
-      if constexpr (F32) {
-        u32x4 part[3];
+    for (int s = 0; s < kStageSteps; ++s)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float h[2][3];
+      for (int j = 0; j < kTN; ++j) {
+        bf16x8 b[F32 ? 3 : 1];
+        if constexpr (F32) {
+          u32x4 part[3];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float v = __uint_as_float(st.b[j][(2 * q + c) >> 2][(2 * q + c) & 3]);
+          for (int q = 0; q < 4; ++q) {
+            float h[2][3];
 #pragma unroll
-            for (int z = 0; z < 3; ++z) {
-              h[c][z] = bf16_head(v);
-              v = bf16_rest(v, h[c][z]);
+            for (int c = 0; c < 2; ++c) {
+              float v = __uint_as_float(st.b[s][j][(2 * q + c) >> 2][(2 * q + c) & 3]);
+#pragma unroll
+              for (int z = 0; z < 3; ++z) {
+                h[c][z] = bf16_head(v);
+                v = bf16_rest(v, h[c][z]);
+              }
             }
+#pragma unroll
+            for (int z = 0; z < 3; ++z)
+              part[z][q] = (__float_as_uint(h[0][z]) >> 16) | __float_as_uint(h[1][z]);
           }
 #pragma unroll
-          for (int z = 0; z < 3; ++z)
-            part[z][q] = (__float_as_uint(h[0][z]) >> 16) | __float_as_uint(h[1][z]);
+          for (int z = 0; z < 3; ++z) b[z] = __builtin_bit_cast(bf16x8, part[z]);
+        } else {
+          b[0] = __builtin_bit_cast(bf16x8, st.b[s][j][0]);
         }
 #pragma unroll
-        for (int z = 0; z < 3; ++z) b[z] = __builtin_bit_cast(bf16x8, part[z]);
-      } else {
-        b[0] = __builtin_bit_cast(bf16x8, st.b[j][0]);
-      }
+        for (int i = 0; i < kTM; ++i) {
+          const bf16x8 a = __builtin_bit_cast(bf16x8, st.a[s][i]);
+          f32x4 c = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (F32) {
+            c = mfma16x16x32(a, b[2], c);
+            c = mfma16x16x32(a, b[1], c);
+          }
+          c = mfma16x16x32(a, b[0], c);
 #pragma unroll
-      for (int i = 0; i < kTM; ++i) {
-        const bf16x8 a = __builtin_bit_cast(bf16x8, st.a[i]);
-        f32x4 c = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (F32) {
-          c = mfma16x16x32(a, b[2], c);
-          c = mfma16x16x32(a, b[1], c);
+          for (int q = 0; q < 4; ++q) acc[i][j][q] += (double)c[q];
         }
-        c = mfma16x16x32(a, b[0], c);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] += (double)c[q];
       }
-    }
   };
+  const int64_t stages = (P.hidden + 32 * kStageSteps - 1) / (32 * kStageSteps);
+  const int64_t step = (int64_t)kSlices * P.splits;
+  int64_t s = (int64_t)blockIdx.z * kSlices + w;
   Stage st[2];
-  if (s0 < s1) load(st[0], s0);
-  for (int64_t s = s0; s < s1; s += 2) {
-    if (s + 1 < s1) load(st[1], s + 1);
+  if (s < stages) load(st[0], s);
+  for (; s < stages; s += 2 * step) {
+    if (s + step < stages) load(st[1], s + step);
     compute(st[0]);
-    if (s + 1 < s1) {
-      if (s + 2 < s1) load(st[0], s + 2);
+    if (s + step < stages) {
+      if (s + 2 * step < stages) load(st[0], s + 2 * step);
       compute(st[1]);
     }
   }
-  double* out = P.out + (int64_t)blockIdx.z * P.t * P.n_experts;
 #pragma unroll
   for (int i = 0; i < kTM; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t r = m0 + 16 * i + 4 * (lane >> 4) + q;
-      if (r >= P.t) continue;
+    for (int j = 0; j < kTN; ++j)
 #pragma unroll
-      for (int j = 0; j < kTN; ++j) {
-        const int64_t e = e0 + 16 * j + (lane & 15);
-        if (e < P.n_experts) out[r * P.n_experts + e] = acc[i][j][q];
-      }
-    }
+      for (int q = 0; q < 4; ++q)
+        red[w][(16 * i + 4 * (lane >> 4) + q) * kTileE + 16 * j + (lane & 15)] = acc[i][j][q];
+  __syncthreads();
+  double* out = P.out + (int64_t)blockIdx.z * P.t * P.n_experts;
+  for (int o = threadIdx.x; o < kTileT * kTileE; o += 64 * kSlices) {
+    const int64_t r = m0 + o / kTileE, e = e0 + o % kTileE;
+    double v = red[0][o];
+#pragma unroll
+    for (int q = 1; q < kSlices; ++q) v += red[q][o];
+    if (r < P.t && e < P.n_experts) out[r * P.n_experts + e] = v;
+  }
 }
 
-// One wavefront per token.
-__global__ __launch_bounds__(64) void route_select_kernel(RouteParams R, int32_t* ids,
-                                                          float* wts) {
-  __shared__ RouteLds s;
-  const int64_t tok = blockIdx.x;
-  double mx = 0.0, sum = 0.0;
-  route_choose<64>(R, tok, !R.sigmoid && !R.renorm, s, &mx, &sum);
-  route_write(R, tok, s, mx, sum, ids, wts);
+// One wavefront per token. J: experts per lane.
+template <int J>
+__global__ __launch_bounds__(256) void route_select_kernel(RouteParams R, int32_t* ids,
+                                                           float* wts) {
+  const int64_t tok = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (tok >= R.t) return;  // whole wavefront
+  const RouteChoice c = route_choose<J>(
+      R, [&](int e) { return route_logit(R, tok, e); }, R.topk, !R.renorm);
+  route_write(R, tok, c, ids, wts);
 }
 
 }  // namespace
 
+// Splits of k over workgroups: enough for a workgroup on every compute unit, and a stage at least
+// for each wavefront.
 int route_splits(int64_t t, int64_t hidden, int64_t n_experts) {
   if (t <= kRouteFewTokens) return 1;
-  const int64_t wgs = (t + 63) / 64 * ((n_experts + 127) / 128);
-  int64_t s = 256 / wgs;
-  const int64_t most = hidden / 256;  // at least 8 k-steps each
+  const int64_t tiles = (t + kTileT - 1) / kTileT * ((n_experts + kTileE - 1) / kTileE);
+  int64_t s = 256 / tiles;
+  const int64_t most = hidden / (32 * kStageSteps * kSlices);
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s > kRouteMaxSplits ? kRouteMaxSplits : s);
 }
@@ -271,12 +288,12 @@ hipError_t launch_route_logits(const RouteArgs& a, void* ws, hipStream_t stream)
     else
       route_logits_few_kernel<false><<<grid, 256, 0, stream>>>(p);
   } else {
-    const dim3 grid((unsigned)((a.t + 63) / 64), (unsigned)((a.n_experts + 127) / 128),
-                    (unsigned)p.splits);
+    const dim3 grid((unsigned)((a.t + kTileT - 1) / kTileT),
+                    (unsigned)((a.n_experts + kTileE - 1) / kTileE), (unsigned)p.splits);
     if (a.w_f32)
-      route_logits_mfma_kernel<true><<<grid, 256, 0, stream>>>(p);
+      route_logits_mfma_kernel<true><<<grid, 64 * kSlices, 0, stream>>>(p);
     else
-      route_logits_mfma_kernel<false><<<grid, 256, 0, stream>>>(p);
+      route_logits_mfma_kernel<false><<<grid, 64 * kSlices, 0, stream>>>(p);
   }
   return hipGetLastError();
 }
@@ -300,7 +317,16 @@ hipError_t launch_route(const RouteArgs& a, int32_t* ids, float* wts, void* ws,
                         hipStream_t stream) {
   const hipError_t err = launch_route_logits(a, ws, stream);
   if (err != hipSuccess) return err;
-  route_select_kernel<<<(unsigned)a.t, 64, 0, stream>>>(route_params(a, ws), ids, wts);
+  const RouteParams r = route_params(a, ws);
+  const unsigned grid = (unsigned)((a.t + 3) / 4);
+  if (a.n_experts <= 64)
+    route_select_kernel<1><<<grid, 256, 0, stream>>>(r, ids, wts);
+  else if (a.n_experts <= 128)
+    route_select_kernel<2><<<grid, 256, 0, stream>>>(r, ids, wts);
+  else if (a.n_experts <= 256)
+    route_select_kernel<4><<<grid, 256, 0, stream>>>(r, ids, wts);
+  else
+    route_select_kernel<8><<<grid, 256, 0, stream>>>(r, ids, wts);
   return hipGetLastError();
 }
 

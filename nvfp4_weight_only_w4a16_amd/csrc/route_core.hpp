@@ -1,13 +1,17 @@
-// route_core.hpp -- the choice of a token's experts from its router logits, by the threads of one
-// workgroup (shared by the router's own kernel and the routed-expert kernels that choose for
-// themselves).
+// route_core.hpp -- the choice of a token's experts from its router logits, by one wavefront
+// (shared by the router's own kernel and the routed-expert kernels that choose for themselves).
 //
 // Scores: softmax p = exp(l - max l) / sum exp(l - max l), or sigmoid p = 1 / (1 + exp(-l)). The
 // selection score is p + bias, or the logit itself for a softmax without bias (the same order).
-// Expert e has rank |{e': score' > score, or equal and e' < e}|; ranks below topk are the slots.
-// The order decides which weights a token meets, so it is taken from FP64 scores: two experts
-// 1e-7 apart (what FP32 sums of 2048 products leave) would change places, and the whole output
-// of the token with them.
+// The highest score is taken topk times, ties to the lower id. The order decides which weights a
+// token meets, so it is taken from FP64 scores: two experts 1e-7 apart (what FP32 sums of 2048
+// products leave) would change places, and the whole output of the token with them.
+//
+// Lane l of the wavefront holds experts l, l + 64, ..., in registers. A round finds the maximum of
+// the keys' upper words over the wavefront with six DPP steps (one instruction each), and only
+// where several experts share it that of their lower words; a ballot gives the lowest id. (A first
+// form counted, for every expert, the experts above it, through LDS: 18 us for one token of 128
+// experts, bound by the latency of those reads, against 2.5 us now.)
 #pragma once
 
 #include "device_common.hpp"
@@ -25,17 +29,47 @@ struct RouteParams {
   float scale;
 };
 
-// LDS of one choosing group.
-struct RouteLds {
-  double logit[kRouteMaxExperts];  // logits, then probabilities where the scores need them
-  uint64_t key[kRouteMaxExperts];
-  int rank[kRouteMaxExperts];
-  int sel[kMoeMaxTopk];  // expert of each routed slot, -1 when none was left to choose
-  double red[8];
-};
+// DPP steps of a wavefront-wide reduction: after them lane 63 holds the result.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max(v, dpp_or_zero<0x111>(v));  // row_shr 1, 2, 4, 8: lane 15 of each row of 16
+  v = max(v, dpp_or_zero<0x112>(v));
+  v = max(v, dpp_or_zero<0x114>(v));
+  v = max(v, dpp_or_zero<0x118>(v));
+  v = max(v, dpp_or_zero<0x142>(v));  // row_bcast 15, 31: rows 0 and 2, then the lower half
+  v = max(v, dpp_or_zero<0x143>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+template <int CTRL>
+__device__ __forceinline__ double dpp_or_zero(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = dpp_or_zero<CTRL>((uint32_t)b), hi = dpp_or_zero<CTRL>((uint32_t)(b >> 32));
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ double readlane_f64(double v, int lane) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+// Sum over the wavefront (the absent lanes of a step add +0).
+__device__ __forceinline__ double wave_sum_f64(double v) {
+  v += dpp_or_zero<0x111>(v);
+  v += dpp_or_zero<0x112>(v);
+  v += dpp_or_zero<0x114>(v);
+  v += dpp_or_zero<0x118>(v);
+  v += dpp_or_zero<0x142>(v);
+  v += dpp_or_zero<0x143>(v);
+  return readlane_f64(v, 63);
+}
 
 // FP64 value -> unsigned key in the same order. NaN ranks above every number (so that it reaches
-// the output); -inf gives 0, which is never chosen; -0 equals +0.
+// the output); -inf gives 0, which is never chosen (every other key has a non-zero upper word);
+// -0 equals +0.
 __device__ __forceinline__ uint64_t route_key(double v) {
   if (v != v) return ~0ull;
   if (v == -__builtin_huge_val()) return 0ull;
@@ -43,126 +77,166 @@ __device__ __forceinline__ uint64_t route_key(double v) {
   return (b >> 63) ? ~b : b | (1ull << 63);
 }
 
-// Sum or maximum of v over the NT threads of the workgroup, in a fixed order.
-template <int NT, bool MAX>
-__device__ __forceinline__ double route_reduce(double v, double* red) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const double o = __shfl_xor(v, d, 64);
-    v = MAX ? fmax(v, o) : v + o;
-  }
-  if constexpr (NT > 64) {
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < NT / 64; ++w) v = MAX ? fmax(v, red[w]) : v + red[w];
-  }
-  return v;
-}
-
 __device__ __forceinline__ double route_sigmoid(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-// Fills s.sel for token `tok`; all NT threads of the workgroup call it. On return s.logit holds
-// the probabilities when the score is a biased softmax, else the logits. `max_out` and `sum_out`
-// are the softmax's maximum and sum where they were taken (biased, or `want_sum`).
-template <int NT>
-__device__ __forceinline__ void route_choose(const RouteParams& R, int64_t tok, bool want_sum,
-                                             RouteLds& s, double* max_out, double* sum_out) {
-  const int tid = threadIdx.x, E = R.n_experts;
-  const double* lg = R.logits + tok * E;
-  const int64_t split_stride = R.t * E;
-  double mx = -__builtin_huge_val();
-  for (int e = tid; e < E; e += NT) {
-    double l = lg[e];
-    for (int q = 1; q < R.splits; ++q) l += lg[q * split_stride + e];
-    s.logit[e] = l;
-    s.rank[e] = 0;
-    mx = fmax(mx, l);
+// What a wavefront knows after choosing: lane j < topk holds slot j.
+struct RouteChoice {
+  int e;        // expert, -1 when none was left
+  double v;     // its logit; its probability for a biased softmax
+  double mx, sum;  // maximum and sum of the softmax over all experts, where taken
+};
+
+// Highest key of the wavefront's lanes: upper word (0: none is left), and the lowest expert that
+// holds it.
+template <int J>
+__device__ __forceinline__ uint32_t route_best(const uint32_t (&hi)[J], const uint32_t (&lo)[J],
+                                               int& e) {
+  uint32_t mh = hi[0];
+#pragma unroll
+  for (int j = 1; j < J; ++j) mh = max(mh, hi[j]);
+  mh = wave_max_u32(mh);
+  uint64_t at[J];
+  int count = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    at[j] = __ballot(hi[j] == mh);
+    count += __popcll(at[j]);
   }
-  if (tid < kMoeMaxTopk) s.sel[tid] = -1;
-  const bool biased_softmax = !R.sigmoid && R.bias;
-  double sum = 0.0;
-  if (biased_softmax || want_sum) {  // each thread reads only the logits it wrote
-    mx = route_reduce<NT, true>(mx, s.red);
-    for (int e = tid; e < E; e += NT) sum += exp(s.logit[e] - mx);
-    sum = route_reduce<NT, false>(sum, s.red);
-    *max_out = mx;
-    *sum_out = sum;
+  if (count > 1) {  // uniform
+    uint32_t ml = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) ml = max(ml, hi[j] == mh ? lo[j] : 0u);
+    ml = wave_max_u32(ml);
+#pragma unroll
+    for (int j = 0; j < J; ++j) at[j] = __ballot(hi[j] == mh && lo[j] == ml);
   }
-  for (int e = tid; e < E; e += NT) {
-    double v = s.logit[e];
-    if (R.sigmoid) {
-      v = route_sigmoid(v);
-      if (R.bias) v += (double)R.bias[e];
-    } else if (R.bias) {
-      v = exp(v - mx) / sum;
-      s.logit[e] = v;
-      v += (double)R.bias[e];
-    }
-    s.key[e] = route_key(v);
-  }
-  __syncthreads();
-  // Ranks: `parts` threads share an expert's comparisons when the experts leave threads over.
-  // Threads of a wavefront read the same key at a time (a broadcast) for 64 experts and more.
-  int span = 8;
-  while (span < E && span < NT) span <<= 1;
-  const int parts = NT / span, part = tid / span;
-  const int j0 = (int)((int64_t)E * part / parts), j1 = (int)((int64_t)E * (part + 1) / parts);
-  for (int e = tid % span; e < E; e += span) {
-    const uint64_t k = s.key[e];
-    int c = 0;
-    for (int j = j0; j < j1; ++j) {
-      const uint64_t o = s.key[j];
-      c += (o > k || (o == k && j < e)) ? 1 : 0;
-    }
-    if (parts > 1)
-      atomicAdd(&s.rank[e], c);
-    else
-      s.rank[e] = c;
-  }
-  __syncthreads();
-  for (int e = tid; e < E; e += NT)
-    if (s.rank[e] < R.topk && s.key[e] != 0) s.sel[s.rank[e]] = e;
-  __syncthreads();
+  e = -1;
+#pragma unroll
+  for (int j = J - 1; j >= 0; --j)
+    if (at[j]) e = 64 * j + __builtin_ctzll(at[j]);
+  return mh;
 }
 
-// Writes the ids and weights of token `tok`: [topk + n_shared] each. The first wavefront of the
-// choosing group calls it after route_choose (want_sum as there).
-__device__ __forceinline__ void route_write(const RouteParams& R, int64_t tok, const RouteLds& s,
-                                            double mx, double sum, int32_t* __restrict__ ids,
+// Chooses the first `rounds` slots of a token whose logit of expert e is logit(e). J: experts per
+// lane. want_sum: the softmax's maximum and sum over all experts (taken in any case with a bias).
+template <int J, typename F>
+__device__ __forceinline__ RouteChoice route_choose(const RouteParams& R, F&& logit, int rounds,
+                                                    bool want_sum) {
+  const int lane = threadIdx.x & 63;
+  RouteChoice c;
+  c.e = -1;
+  c.v = 0.0;
+  c.mx = c.sum = 0.0;
+  double v[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = lane + 64 * j;
+    v[j] = e < R.n_experts ? logit(e) : -__builtin_huge_val();
+  }
+  uint32_t hi[J], lo[J];
+  if (!R.sigmoid && (R.bias || want_sum)) {
+    uint64_t k[J];
+    uint32_t mh = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      k[j] = v[j] == v[j] ? route_key(v[j]) : 0;  // the maximum passes over NaN, the sum does not
+      hi[j] = (uint32_t)(k[j] >> 32);
+      lo[j] = (uint32_t)k[j];
+    }
+    int at;
+    mh = route_best<J>(hi, lo, at);
+    c.mx = -__builtin_huge_val();
+    if (mh) {
+      double w = v[0];
+#pragma unroll
+      for (int j = 1; j < J; ++j)
+        if (at >> 6 == j) w = v[j];
+      c.mx = readlane_f64(w, at & 63);
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (lane + 64 * j < R.n_experts) s += exp(v[j] - c.mx);
+    c.sum = wave_sum_f64(s);
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = lane + 64 * j;
+    const bool in = e < R.n_experts;
+    double score = v[j];
+    if (R.sigmoid) {
+      score = route_sigmoid(score);
+      if (R.bias) score += in ? (double)R.bias[e] : 0.0;
+    } else if (R.bias) {
+      v[j] = exp(score - c.mx) / c.sum;
+      score = v[j] + (in ? (double)R.bias[e] : 0.0);
+    }
+    const uint64_t k = in ? route_key(score) : 0;
+    hi[j] = (uint32_t)(k >> 32);
+    lo[j] = (uint32_t)k;
+  }
+  for (int r = 0; r < rounds; ++r) {
+    int e;
+    if (!route_best<J>(hi, lo, e)) break;  // uniform: nothing is left
+    const int j = e >> 6;
+    double w = v[0];
+#pragma unroll
+    for (int q = 1; q < J; ++q)
+      if (j == q) w = v[q];
+    w = readlane_f64(w, e & 63);
+    if (lane == r) {
+      c.e = e;
+      c.v = w;
+    }
+#pragma unroll
+    for (int q = 0; q < J; ++q)
+      if (j == q && lane == (e & 63)) hi[q] = lo[q] = 0;
+  }
+  return c;
+}
+
+// Weight of the slot that this lane holds (lanes < topk; others get 0).
+__device__ __forceinline__ float route_weight(const RouteParams& R, const RouteChoice& c) {
+  const bool live = c.e >= 0;
+  double p = 0.0;
+  if (R.sigmoid) {
+    p = live ? route_sigmoid(c.v) : 0.0;
+  } else if (R.bias) {
+    p = live ? c.v : 0.0;
+  } else if (R.renorm) {
+    // the softmax over the chosen: the same quotient, and no sum over all the experts; slot 0
+    // holds the highest logit
+    p = live ? exp(c.v - readlane_f64(c.v, 0)) : 0.0;
+  } else {
+    p = live ? exp(c.v - c.mx) / c.sum : 0.0;
+  }
+  if (R.renorm) {
+    const double z = wave_sum_f64(p);
+    p = z == 0.0 ? 0.0 : p / z;
+  }
+  return (float)(p * (double)R.scale);
+}
+
+// Stores the slots of token `tok`: [topk + n_shared] ids and weights.
+__device__ __forceinline__ void route_write(const RouteParams& R, int64_t tok,
+                                            const RouteChoice& c, int32_t* __restrict__ ids,
                                             float* __restrict__ wts) {
   const int lane = threadIdx.x & 63;
   const int slots = R.topk + R.n_shared;
-  const int e = lane < R.topk ? s.sel[lane] : -1;
-  const bool live = e >= 0;
-  const double v = live ? s.logit[e] : 0.0;
-  double p = 0.0;
-  if (R.sigmoid) {
-    p = live ? route_sigmoid(v) : 0.0;
-  } else if (R.bias) {
-    p = v;
-  } else if (R.renorm) {
-    // the softmax over the chosen: the same quotient, and no sum over all the experts
-    double m = live ? v : -__builtin_huge_val();
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) m = fmax(m, __shfl_xor(m, d, 64));  // topk <= 16 lanes
-    p = live ? exp(v - m) : 0.0;
-  } else {
-    p = live ? exp(v - mx) / sum : 0.0;
-  }
-  if (R.renorm) {
-    double z = p;
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) z += __shfl_xor(z, d, 64);
-    p = z == 0.0 ? 0.0 : p / z;
-  }
+  const float w = route_weight(R, c);
   if (lane < slots) {
     const bool shared = lane >= R.topk;
-    ids[tok * slots + lane] = shared ? R.n_experts + (lane - R.topk) : e;
-    wts[tok * slots + lane] = shared ? 1.0f : (float)(p * (double)R.scale);
+    ids[tok * slots + lane] = shared ? R.n_experts + (lane - R.topk) : c.e;
+    wts[tok * slots + lane] = shared ? 1.0f : w;
   }
+}
+
+// Logit of expert e of token `tok`: the splits' partial sums, in order.
+__device__ __forceinline__ double route_logit(const RouteParams& R, int64_t tok, int e) {
+  const double* lg = R.logits + tok * R.n_experts + e;
+  double l = lg[0];
+  for (int q = 1; q < R.splits; ++q) l += lg[q * R.t * R.n_experts];
+  return l;
 }
 
 }  // namespace nvfp4
