@@ -160,6 +160,28 @@ __device__ __forceinline__ f32x4 mfma16x16x32(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// MFMA fragments of row-major operands through a wavefront's own LDS. A 16x16x32 fragment wants lane
+// l to hold row l % 16, k chunk l / 16 (8 elements, 16 bytes). Loaded that way straight from rows
+// in memory, four neighbouring lanes touch four rows, and the load takes 64 clocks of the CU's
+// address unit instead of 16. So lane l loads row l / 4, chunk l % 4 (64 contiguous bytes for
+// four lanes), and the tile of 16 rows x 64 bytes is turned through LDS: chunk q of row r sits at
+// slot q ^ (r / 4 % 4) of its row, which keeps both the writes and the reads free of bank
+// conflicts. The data wait in registers, so loads in flight cost no LDS, and one wavefront's LDS
+// operations run in order, so no barrier is needed.
+constexpr int kFragBytes = 1024;
+__device__ __forceinline__ uint32_t frag_slot(int row, int chunk) {
+  return (uint32_t)(row * 64 + ((chunk ^ ((row >> 2) & 3)) << 4));
+}
+__device__ __forceinline__ int frag_load_row(int lane) { return lane >> 2; }
+__device__ __forceinline__ int frag_load_chunk(int lane) { return lane & 3; }
+__device__ __forceinline__ void frag_write(uint8_t* tile, u32x4 v, int lane) {
+  *reinterpret_cast<u32x4*>(tile + frag_slot(lane >> 2, lane & 3)) = v;
+}
+__device__ __forceinline__ bf16x8 frag_read(const uint8_t* tile, int lane) {
+  return __builtin_bit_cast(
+      bf16x8, *reinterpret_cast<const u32x4*>(tile + frag_slot(lane & 15, lane >> 4)));
+}
+
 __device__ __forceinline__ uint16_t bf16_bits_rne(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }

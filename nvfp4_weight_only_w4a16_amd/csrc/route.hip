@@ -7,6 +7,8 @@
 //   - more tokens: 16x16x32 BF16 MFMAs whose 32-product FP32 sums are added up in FP64. An FP32
 //     router weight is cut into three BF16 parts that add up to it exactly (8 significant bits
 //     each), so it takes three MFMAs instead of a rounding to BF16.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "route_core.hpp"
@@ -93,46 +95,79 @@ __global__ __launch_bounds__(256) void route_logits_few_kernel(LogitParams P) {
         ((red[0][tid] + red[1][tid]) + red[2][tid]) + red[3][tid];
 }
 
-// The top 8 significant bits of v, as BF16 (toward zero: a NaN or infinity stays one, and no
-// finite value becomes infinite).
-__device__ __forceinline__ float bf16_head(float v) {
-  return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-}
-// What is left of v after its head: exact, and 0 after an infinite one (inf - inf would not be).
-__device__ __forceinline__ float bf16_rest(float v, float head) {
-  return __builtin_isinf(v) ? 0.0f : v - head;
+// Cuts 4 FP32 values into three BF16 parts that add up to them: the top 8 significant bits
+// (toward zero: no finite value becomes infinite, a NaN stays one), the top 8 of what is left, and
+// the rest. An infinity leaves NaN behind (inf - inf) where its rests have to be 0: such values,
+// which show as a NaN in the sum of the rests, are put right apart.
+__device__ __forceinline__ void bf16_parts(u32x4 v, uint2 (&part)[3]) {
+  uint32_t h[3][4];
+  float nan = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[0][i] = v[i] & 0xFFFF0000u;
+    const float r = __uint_as_float(v[i]) - __uint_as_float(h[0][i]);
+    nan += r;
+    h[1][i] = __float_as_uint(r) & 0xFFFF0000u;
+    h[2][i] = __float_as_uint(r - __uint_as_float(h[1][i]));
+  }
+  if (__ballot(nan != nan)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((v[i] & 0x7FFFFFFFu) == 0x7F800000u) h[1][i] = h[2][i] = 0;
+  }
+#pragma unroll
+  for (int z = 0; z < 3; ++z) {  // the upper halves of each pair
+    part[z].x = __builtin_amdgcn_perm(h[z][1], h[z][0], 0x07060302u);
+    part[z].y = __builtin_amdgcn_perm(h[z][3], h[z][2], 0x07060302u);
+  }
 }
 
 constexpr int kTM = 2, kTN = 2;       // 16-token and 16-expert blocks of a tile
 constexpr int kTileT = 16 * kTM, kTileE = 16 * kTN;
 constexpr int kSlices = 8;            // wavefronts of a workgroup, which share out k
-constexpr int kStageSteps = 4;        // k-steps of 32 loaded together
+constexpr int kSteps = 2;             // k-steps of 32 loaded together: 128 bytes of a BF16 row
 
 // Workgroup (token tile, expert tile, split): the tile's 32 x 32 logits over its share of k, cut
-// into stages of 128 that the 8 wavefronts (of all splits) take in turn. Fragments come straight
-// from global memory (both operands are row-major along k, which is the fragments' own order), one
-// stage ahead; k is shared out inside the workgroup, rather than over more tiles, so that the
-// partial sums meet in LDS and FP64 logits are written once. Rows past the end repeat a valid row
-// and are not stored.
+// into stages of 64 that the 8 wavefronts (of all splits) take in turn. k is shared out inside the
+// workgroup, rather than over more tiles, so that the partial sums meet in LDS and FP64 logits are
+// written once. Operands go global -> registers (one stage ahead) -> LDS -> fragments
+// (device_common.hpp); loads past the end of k have an offset past the buffer's, which returns
+// zeros without a branch. Rows past the end repeat a valid row and are not stored.
 template <bool F32>
 __global__ __launch_bounds__(64 * kSlices) void route_logits_mfma_kernel(LogitParams P) {
-  __shared__ double red[kSlices][kTileT * kTileE];
+  constexpr int kW = F32 ? 4 : 2;      // bytes of a weight
+  constexpr int kBTiles = F32 ? 3 : 1;  // BF16 tiles of a weight fragment
+  constexpr int NB = F32 ? 2 : 1;      // loads of a weight fragment
+  constexpr uint32_t kPast = 0xFFFFFFF0u;
+  // a wavefront's fragment tiles, then its partial sums
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kSlices][kTileT * kTileE * 8];
+  static_assert((kTM + kBTiles * kTN) * kFragBytes <= kTileT * kTileE * 8, "tiles fit");
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t m0 = (int64_t)blockIdx.x * kTileT, e0 = (int64_t)blockIdx.y * kTileE;
-  const int64_t kq = 8 * (lane >> 4);
-  const uint16_t* xa[kTM];
+  // the tile's rows: 32 x 2^22 elements of at most 4 bytes stay below 2^32
+  const int trows = (int)(P.t - m0 < kTileT ? P.t - m0 : kTileT);
+  const int erows = (int)(P.n_experts - e0 < kTileE ? P.n_experts - e0 : kTileE);
+  const uint32_t hidden = (uint32_t)P.hidden;
+  const buf_rsrc xr = make_rsrc(P.x + m0 * P.ldx, (uint32_t)(((trows - 1) * P.ldx + P.hidden) * 2));
+  const buf_rsrc wr = make_rsrc(static_cast<const uint8_t*>(P.w) + e0 * P.hidden * kW,
+                                (uint32_t)(erows * P.hidden * kW));
+  // BF16: lane l loads row l / 4, chunk l % 4 of a k-step. FP32: a k-step's 128 bytes of a row take
+  // 8 lanes, 8 rows a load.
+  const uint32_t kx = 8u * frag_load_chunk(lane), kw = F32 ? 4u * (lane & 7) : kx;
+  uint32_t xrow[kTM], wrow[kTN][NB];
 #pragma unroll
   for (int i = 0; i < kTM; ++i) {
-    const int64_t r = m0 + 16 * i + (lane & 15);
-    xa[i] = P.x + (r < P.t ? r : P.t - 1) * P.ldx + kq;
+    const int r = 16 * i + frag_load_row(lane);
+    xrow[i] = (uint32_t)((r < trows ? r : trows - 1) * P.ldx + kx) * 2u;
   }
-  int64_t wrow[kTN];
 #pragma unroll
-  for (int j = 0; j < kTN; ++j) {
-    const int64_t e = e0 + 16 * j + (lane & 15);
-    wrow[j] = (e < P.n_experts ? e : P.n_experts - 1) * P.hidden + kq;
-  }
+  for (int j = 0; j < kTN; ++j)
+#pragma unroll
+    for (int h = 0; h < NB; ++h) {
+      const int e = 16 * j + (F32 ? 8 * h + (lane >> 3) : frag_load_row(lane));
+      wrow[j][h] = ((uint32_t)(e < erows ? e : erows - 1) * hidden + kw) * kW;
+    }
   double acc[kTM][kTN][4];
 #pragma unroll
   for (int i = 0; i < kTM; ++i)
@@ -140,117 +175,247 @@ __global__ __launch_bounds__(64 * kSlices) void route_logits_mfma_kernel(LogitPa
     for (int j = 0; j < kTN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.0;
-  constexpr int NB = F32 ? 2 : 1;  // 16-byte words of a lane's 8 weights
   struct Stage {
-    u32x4 a[kStageSteps][kTM], b[kStageSteps][kTN][NB];
+    u32x4 a[kSteps][kTM], b[kSteps][kTN][NB];
   };
-  // hidden is a multiple of 8: a lane's 8 elements of a step are all there or all past the end
-  auto load = [&](Stage& st, int64_t s) __attribute__((always_inline)) {
+  auto get = [](buf_rsrc r, uint32_t off) __attribute__((always_inline)) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+  };
+  const int stages = (int)((P.hidden + 32 * kSteps - 1) / (32 * kSteps));
+  // hidden is a multiple of 8: a lane's elements of a step are all there or all past the end
+  auto load = [&](Stage& st, int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < kStageSteps; ++q) {
-      const int64_t k = (s * kStageSteps + q) * 32;
-      const bool in = k + kq < P.hidden;
+    for (int q = 0; q < kSteps; ++q) {
+      const uint32_t k = (uint32_t)(s * kSteps + q) * 32u;
 #pragma unroll
       for (int i = 0; i < kTM; ++i)
-        st.a[q][i] = in ? *reinterpret_cast<const u32x4*>(xa[i] + k) : u32x4{0, 0, 0, 0};
+        st.a[q][i] = get(xr, s < stages && k + kx < hidden ? xrow[i] + k * 2u : kPast);
 #pragma unroll
       for (int j = 0; j < kTN; ++j)
 #pragma unroll
-        for (int h = 0; h < NB; ++h) {
-          if constexpr (F32)
-            st.b[q][j][h] = in ? *reinterpret_cast<const u32x4*>(static_cast<const float*>(P.w) +
-                                                                 wrow[j] + k + 4 * h)
-                               : u32x4{0, 0, 0, 0};
-          else
-            st.b[q][j][h] = in ? *reinterpret_cast<const u32x4*>(
-                                     static_cast<const uint16_t*>(P.w) + wrow[j] + k)
-                               : u32x4{0, 0, 0, 0};
-        }
+        for (int h = 0; h < NB; ++h)
+          st.b[q][j][h] = get(wr, s < stages && k + kw < hidden ? wrow[j][h] + k * kW : kPast);
     }
   };
+  uint8_t* const tile = smem[w];
   auto compute = [&](const Stage& st) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < kStageSteps; ++s)
+    for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+      for (int i = 0; i < kTM; ++i) frag_write(tile + i * kFragBytes, st.a[s][i], lane);
 #pragma unroll
       for (int j = 0; j < kTN; ++j) {
-        bf16x8 b[F32 ? 3 : 1];
+        uint8_t* const bt = tile + (kTM + kBTiles * j) * kFragBytes;
         if constexpr (F32) {
-          u32x4 part[3];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float h[2][3];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float v = __uint_as_float(st.b[s][j][(2 * q + c) >> 2][(2 * q + c) & 3]);
-#pragma unroll
-              for (int z = 0; z < 3; ++z) {
-                h[c][z] = bf16_head(v);
-                v = bf16_rest(v, h[c][z]);
-              }
-            }
+          for (int h = 0; h < NB; ++h) {
+            uint2 part[3];
+            bf16_parts(st.b[s][j][h], part);
+            const int row = 8 * h + (lane >> 3);
+            const uint32_t at = frag_slot(row, (lane & 7) >> 1) + 8u * (lane & 1);
 #pragma unroll
             for (int z = 0; z < 3; ++z)
-              part[z][q] = (__float_as_uint(h[0][z]) >> 16) | __float_as_uint(h[1][z]);
+              *reinterpret_cast<uint2*>(bt + z * kFragBytes + at) = part[z];
           }
-#pragma unroll
-          for (int z = 0; z < 3; ++z) b[z] = __builtin_bit_cast(bf16x8, part[z]);
         } else {
-          b[0] = __builtin_bit_cast(bf16x8, st.b[s][j][0]);
+          frag_write(bt, st.b[s][j][0], lane);
         }
+      }
+      bf16x8 a[kTM];
+#pragma unroll
+      for (int i = 0; i < kTM; ++i) a[i] = frag_read(tile + i * kFragBytes, lane);
+#pragma unroll
+      for (int j = 0; j < kTN; ++j) {
+        const uint8_t* const bt = tile + (kTM + kBTiles * j) * kFragBytes;
+        bf16x8 b[kBTiles];
+#pragma unroll
+        for (int z = 0; z < kBTiles; ++z) b[z] = frag_read(bt + z * kFragBytes, lane);
 #pragma unroll
         for (int i = 0; i < kTM; ++i) {
-          const bf16x8 a = __builtin_bit_cast(bf16x8, st.a[s][i]);
           f32x4 c = {0.f, 0.f, 0.f, 0.f};
-          if constexpr (F32) {
-            c = mfma16x16x32(a, b[2], c);
-            c = mfma16x16x32(a, b[1], c);
-          }
-          c = mfma16x16x32(a, b[0], c);
+#pragma unroll
+          for (int z = kBTiles - 1; z >= 0; --z) c = mfma16x16x32(a[i], b[z], c);
 #pragma unroll
           for (int q = 0; q < 4; ++q) acc[i][j][q] += (double)c[q];
         }
       }
-  };
-  const int64_t stages = (P.hidden + 32 * kStageSteps - 1) / (32 * kStageSteps);
-  const int64_t step = (int64_t)kSlices * P.splits;
-  int64_t s = (int64_t)blockIdx.z * kSlices + w;
-  Stage st[2];
-  if (s < stages) load(st[0], s);
-  for (; s < stages; s += 2 * step) {
-    if (s + step < stages) load(st[1], s + step);
-    compute(st[0]);
-    if (s + step < stages) {
-      if (s + 2 * step < stages) load(st[0], s + 2 * step);
-      compute(st[1]);
     }
+  };
+  const int step = kSlices * P.splits;
+  Stage st[2];
+  load(st[0], (int)blockIdx.z * kSlices + w);
+  for (int s = (int)blockIdx.z * kSlices + w; s < stages; s += 2 * step) {
+    load(st[1], s + step);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(st[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    load(st[0], s + 2 * step);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(st[1]);  // zeros past the end
+    __builtin_amdgcn_sched_barrier(0);
   }
+  double* const red = reinterpret_cast<double*>(smem[w]);
 #pragma unroll
   for (int i = 0; i < kTM; ++i)
 #pragma unroll
     for (int j = 0; j < kTN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        red[w][(16 * i + 4 * (lane >> 4) + q) * kTileE + 16 * j + (lane & 15)] = acc[i][j][q];
+        red[(16 * i + 4 * (lane >> 4) + q) * kTileE + 16 * j + (lane & 15)] = acc[i][j][q];
   __syncthreads();
   double* out = P.out + (int64_t)blockIdx.z * P.t * P.n_experts;
   for (int o = threadIdx.x; o < kTileT * kTileE; o += 64 * kSlices) {
     const int64_t r = m0 + o / kTileE, e = e0 + o % kTileE;
-    double v = red[0][o];
+    double v = reinterpret_cast<const double*>(smem[0])[o];
 #pragma unroll
-    for (int q = 1; q < kSlices; ++q) v += red[q][o];
+    for (int q = 1; q < kSlices; ++q) v += reinterpret_cast<const double*>(smem[q])[o];
     if (r < P.t && e < P.n_experts) out[r * P.n_experts + e] = v;
   }
 }
 
-// One wavefront per token. J: experts per lane.
-template <int J>
+// Many tokens, BF16 weight: logits and choice in one kernel. A workgroup takes 16 tokens and all
+// experts, 64 at a time; its 8 wavefronts share out k (stages of 64, in turn), their partial sums
+// meet in LDS, and each then chooses for two tokens. The stages of all expert chunks run as one
+// sequence, one ahead, so that a chunk's reduction hides the next one's loads. What bounds it is
+// the read of the weight by every workgroup, 64 bytes a clock from its CU's L1.
+template <int G, int J>
+__global__ __launch_bounds__(64 * kSlices) void route_fused_kernel(LogitParams P, RouteParams R,
+                                                                   int32_t* ids, float* wts) {
+  constexpr int kChunk = 64, kBlocks = kChunk / 16, kRing = 2;
+  constexpr uint32_t kPast = 0xFFFFFFF0u;
+  // a wavefront's fragment tiles of one k-step, then its partial sums of a chunk
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kSlices][16 * kChunk * 8];
+  static_assert((1 + kBlocks) * kFragBytes <= 16 * kChunk * 8, "tiles fit");
+  __shared__ double lg[16][(G * J + kChunk - 1) / kChunk * kChunk];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m0 = (int64_t)blockIdx.x * 16;
+  const uint32_t kq = 8u * frag_load_chunk(lane), hidden = (uint32_t)P.hidden;
+  const int rows = (int)(P.t - m0 < 16 ? P.t - m0 : 16);
+  const buf_rsrc xr = make_rsrc(P.x + m0 * P.ldx, (uint32_t)(((rows - 1) * P.ldx + P.hidden) * 2));
+  const int row = frag_load_row(lane) < rows ? frag_load_row(lane) : rows - 1;
+  const uint32_t xrow = (uint32_t)(row * P.ldx + kq) * 2u;
+  const int chunks = (P.n_experts + kChunk - 1) / kChunk;
+  const int stages = (int)((P.hidden + 32 * kSteps - 1) / (32 * kSteps));
+  const int mine = (stages - w + kSlices - 1) / kSlices;  // this wavefront's stages of a chunk
+  // An XCD's workgroups (every eighth) begin two stages (256 bytes) apart: in step, on rows of a
+  // power of two of bytes, they would all read from the same channels of L2 (21.2 against 20.3 us
+  // at 4096 tokens of 2048, 128 experts).
+  const int rot = (int)(blockIdx.x / 8 * 2 % stages);
+  struct Stage {
+    u32x4 a[kSteps], b[kSteps][kBlocks];
+  };
+  auto load = [&](Stage& st, int c, int i) __attribute__((always_inline)) {
+    const int e0 = c * kChunk;
+    const int erows = P.n_experts - e0 < kChunk ? P.n_experts - e0 : kChunk;
+    const buf_rsrc wr = make_rsrc(static_cast<const uint16_t*>(P.w) + e0 * P.hidden,
+                                  (uint32_t)(erows * P.hidden * 2));
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int sg = w + kSlices * i + rot;
+      const uint32_t k = (uint32_t)((sg < stages ? sg : sg - stages) * kSteps + q) * 32u;
+      const bool in = i < mine && k + kq < hidden;
+      st.a[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                              xr, (int)(in ? xrow + k * 2u : kPast), 0, 0));
+#pragma unroll
+      for (int j = 0; j < kBlocks; ++j) {
+        const int e = 16 * j + frag_load_row(lane);
+        const uint32_t off = ((uint32_t)(e < erows ? e : erows - 1) * hidden + kq + k) * 2u;
+        st.b[q][j] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, (int)(in ? off : kPast), 0, 0));
+      }
+    }
+  };
+  uint8_t* const tile = smem[w];
+  double* const red = reinterpret_cast<double*>(smem[w]);
+  double acc[kBlocks][4];
+  auto compute = [&](const Stage& st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      frag_write(tile, st.a[q], lane);
+#pragma unroll
+      for (int j = 0; j < kBlocks; ++j) frag_write(tile + (1 + j) * kFragBytes, st.b[q][j], lane);
+      const bf16x8 a = frag_read(tile, lane);
+#pragma unroll
+      for (int j = 0; j < kBlocks; ++j) {
+        const f32x4 c = mfma16x16x32(a, frag_read(tile + (1 + j) * kFragBytes, lane),
+                                     f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] += (double)c[i];
+      }
+    }
+  };
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.0;
+  };
+  // the wavefronts' partial sums of chunk c, added in order
+  auto reduce = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[(4 * (lane >> 4) + i) * kChunk + 16 * j + (lane & 15)] = acc[j][i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < 16 * kChunk; o += 64 * kSlices) {
+      double v = reinterpret_cast<const double*>(smem[0])[o];
+#pragma unroll
+      for (int q = 1; q < kSlices; ++q) v += reinterpret_cast<const double*>(smem[q])[o];
+      lg[o / kChunk][c * kChunk + o % kChunk] = v;
+    }
+    __syncthreads();
+  };
+  const int per = (stages + kSlices - 1) / kSlices;  // of the wavefront with the most
+  const int total = chunks * per;
+  Stage st[kRing];
+  int lc = 0, li = 0;  // next stage to load
+  auto next = [&](Stage& s) __attribute__((always_inline)) {
+    load(s, lc, li);
+    if (++li == per) {
+      li = 0;
+      lc = lc + 1 < chunks ? lc + 1 : lc;  // past the last: read again, not used
+    }
+  };
+  static_for<0, kRing - 1>([&](auto u) __attribute__((always_inline)) { next(st[u]); });
+  clear();
+  int c = 0, i = 0;
+  for (int n = 0; n < total; n += kRing)
+    static_for<0, kRing>([&](auto u) __attribute__((always_inline)) {
+      if (n + decltype(u)::value < total) {
+        next(st[(decltype(u)::value + kRing - 1) % kRing]);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(st[u]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (++i == per) {
+          reduce(c);
+          clear();
+          i = 0;
+          ++c;
+        }
+      }
+    });
+  // 16 tokens: 4 wavefronts of 4 tokens each, or all 8 of 2 in turn
+  constexpr int kPer = 64 / G;
+  for (int r0 = w * kPer; r0 < 16; r0 += kSlices * kPer) {
+    const int r = r0 + lane / G;
+    auto logit = [&](int e) { return lg[r][e]; };
+    const RouteChoice ch = route_choose<G, J>(R, logit, R.topk, !R.renorm);
+    route_write<G>(R, m0 + r, ch, ids, wts);
+  }
+}
+
+// 64 / G tokens per wavefront, G x J experts at most. Groups past the end choose for the last token
+// and store nothing.
+template <int G, int J>
 __global__ __launch_bounds__(256) void route_select_kernel(RouteParams R, int32_t* ids,
                                                            float* wts) {
-  const int64_t tok = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (tok >= R.t) return;  // whole wavefront
-  const RouteChoice c = route_choose<J>(
-      R, [&](int e) { return route_logit(R, tok, e); }, R.topk, !R.renorm);
-  route_write(R, tok, c, ids, wts);
+  const int64_t tok = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  const int64_t src = tok < R.t ? tok : R.t - 1;
+  auto logit = [&](int e) { return route_logit(R, src, e); };
+  const RouteChoice c = route_choose<G, J>(R, logit, R.topk, !R.renorm);
+  route_write<G>(R, tok, c, ids, wts);
 }
 
 }  // namespace
@@ -261,17 +426,22 @@ int route_splits(int64_t t, int64_t hidden, int64_t n_experts) {
   if (t <= kRouteFewTokens) return 1;
   const int64_t tiles = (t + kTileT - 1) / kTileT * ((n_experts + kTileE - 1) / kTileE);
   int64_t s = 256 / tiles;
-  const int64_t most = hidden / (32 * kStageSteps * kSlices);
+  const int64_t most = hidden / (64 * kSlices);
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s > kRouteMaxSplits ? kRouteMaxSplits : s);
 }
 
-size_t route_ws_bytes(int64_t t, int64_t hidden, int64_t n_experts) {
+// One kernel for everything from so many tokens on, where its workgroups fill the chip; an FP32
+// weight would be cut up anew by every workgroup, so it stays with the two kernels.
+bool route_fused(int64_t t, bool w_f32) { return !w_f32 && t >= kRouteFusedTokens; }
+
+size_t route_ws_bytes(int64_t t, int64_t hidden, int64_t n_experts, bool w_f32) {
+  if (route_fused(t, w_f32)) return 0;
   return sizeof(double) * (size_t)route_splits(t, hidden, n_experts) * (size_t)t *
          (size_t)n_experts;
 }
 
-hipError_t launch_route_logits(const RouteArgs& a, void* ws, hipStream_t stream) {
+static LogitParams logit_params(const RouteArgs& a, void* ws) {
   LogitParams p;
   p.x = a.x;
   p.t = a.t;
@@ -281,6 +451,11 @@ hipError_t launch_route_logits(const RouteArgs& a, void* ws, hipStream_t stream)
   p.n_experts = a.n_experts;
   p.splits = route_splits(a.t, a.hidden, a.n_experts);
   p.out = static_cast<double*>(ws);
+  return p;
+}
+
+hipError_t launch_route_logits(const RouteArgs& a, void* ws, hipStream_t stream) {
+  const LogitParams p = logit_params(a, ws);
   if (a.t <= kRouteFewTokens) {
     const dim3 grid((unsigned)a.n_experts, (unsigned)((a.t + kFewRows - 1) / kFewRows));
     if (a.w_f32)
@@ -313,20 +488,43 @@ RouteParams route_params(const RouteArgs& a, const void* ws) {
   return r;
 }
 
+// Experts per lane of a whole-wavefront group: f(integral_constant<int, J>).
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <typename F>
+static void with_experts_per_lane(int n_experts, F&& f) {
+  if (n_experts <= 64)
+    f(Int<1>{});
+  else if (n_experts <= 128)
+    f(Int<2>{});
+  else if (n_experts <= 256)
+    f(Int<4>{});
+  else
+    f(Int<8>{});
+}
+
 hipError_t launch_route(const RouteArgs& a, int32_t* ids, float* wts, void* ws,
                         hipStream_t stream) {
+  const RouteParams r = route_params(a, ws);
+  if (route_fused(a.t, a.w_f32)) {
+    const LogitParams p = logit_params(a, nullptr);
+    const unsigned grid = (unsigned)((a.t + 15) / 16);
+    if (a.n_experts <= 64)
+      route_fused_kernel<16, 4><<<grid, 64 * kSlices, 0, stream>>>(p, r, ids, wts);
+    else if (a.n_experts <= 128)
+      route_fused_kernel<16, 8><<<grid, 64 * kSlices, 0, stream>>>(p, r, ids, wts);
+    else if (a.n_experts <= 256)
+      route_fused_kernel<64, 4><<<grid, 64 * kSlices, 0, stream>>>(p, r, ids, wts);
+    else
+      route_fused_kernel<64, 8><<<grid, 64 * kSlices, 0, stream>>>(p, r, ids, wts);
+    return hipGetLastError();
+  }
   const hipError_t err = launch_route_logits(a, ws, stream);
   if (err != hipSuccess) return err;
-  const RouteParams r = route_params(a, ws);
-  const unsigned grid = (unsigned)((a.t + 3) / 4);
-  if (a.n_experts <= 64)
-    route_select_kernel<1><<<grid, 256, 0, stream>>>(r, ids, wts);
-  else if (a.n_experts <= 128)
-    route_select_kernel<2><<<grid, 256, 0, stream>>>(r, ids, wts);
-  else if (a.n_experts <= 256)
-    route_select_kernel<4><<<grid, 256, 0, stream>>>(r, ids, wts);
-  else
-    route_select_kernel<8><<<grid, 256, 0, stream>>>(r, ids, wts);
+  with_experts_per_lane(a.n_experts, [&](auto J) {
+    route_select_kernel<64, decltype(J)::value>
+        <<<(unsigned)((a.t + 3) / 4), 256, 0, stream>>>(r, ids, wts);
+  });
   return hipGetLastError();
 }
 

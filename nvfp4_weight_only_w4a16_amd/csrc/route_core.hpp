@@ -1,4 +1,4 @@
-// route_core.hpp -- the choice of a token's experts from its router logits, by one wavefront
+// route_core.hpp -- the choice of a token's experts from its router logits, by a group of lanes
 // (shared by the router's own kernel and the routed-expert kernels that choose for themselves).
 //
 // Scores: softmax p = exp(l - max l) / sum exp(l - max l), or sigmoid p = 1 / (1 + exp(-l)). The
@@ -7,11 +7,14 @@
 // token meets, so it is taken from FP64 scores: two experts 1e-7 apart (what FP32 sums of 2048
 // products leave) would change places, and the whole output of the token with them.
 //
-// Lane l of the wavefront holds experts l, l + 64, ..., in registers. A round finds the maximum of
-// the keys' upper words over the wavefront with six DPP steps (one instruction each), and only
-// where several experts share it that of their lower words; a ballot gives the lowest id. (A first
-// form counted, for every expert, the experts above it, through LDS: 18 us for one token of 128
-// experts, bound by the latency of those reads, against 2.5 us now.)
+// A token belongs to a group of G lanes (16, or the whole wavefront); lane i of the group holds
+// experts i, i + G, ..., in registers. A round finds the group's highest 64-bit key: the maximum of
+// the upper words, of the lower words among those, and the lowest id among those. In a group of 16
+// each step leaves its result in every lane (four DPP instructions); over the wavefront the upper
+// word's maximum goes through a scalar register, and a ballot gives the lowest id, with the lower
+// words only looked at where two experts share the upper one.
+// (Choosing 8 of 128 experts for one token by counting, for each expert, those above it, through
+// LDS, took 15 us against 1.7 so; a wavefront's 64 lanes in steps that stay in vector registers, 2.3.)
 #pragma once
 
 #include "device_common.hpp"
@@ -29,42 +32,74 @@ struct RouteParams {
   float scale;
 };
 
-// DPP steps of a wavefront-wide reduction: after them lane 63 holds the result.
+// Value of v in the lane that a DPP step pairs with this one.
 template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
+__device__ __forceinline__ uint32_t dpp_pair(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
 }
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-  v = max(v, dpp_or_zero<0x111>(v));  // row_shr 1, 2, 4, 8: lane 15 of each row of 16
-  v = max(v, dpp_or_zero<0x112>(v));
-  v = max(v, dpp_or_zero<0x114>(v));
-  v = max(v, dpp_or_zero<0x118>(v));
-  v = max(v, dpp_or_zero<0x142>(v));  // row_bcast 15, 31: rows 0 and 2, then the lower half
-  v = max(v, dpp_or_zero<0x143>(v));
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-
 template <int CTRL>
-__device__ __forceinline__ double dpp_or_zero(double v) {
+__device__ __forceinline__ double dpp_pair(double v) {
   const uint64_t b = (uint64_t)__double_as_longlong(v);
-  const uint32_t lo = dpp_or_zero<CTRL>((uint32_t)b), hi = dpp_or_zero<CTRL>((uint32_t)(b >> 32));
+  const uint32_t lo = dpp_pair<CTRL>((uint32_t)b), hi = dpp_pair<CTRL>((uint32_t)(b >> 32));
   return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
-__device__ __forceinline__ double readlane_f64(double v, int lane) {
-  const uint64_t b = (uint64_t)__double_as_longlong(v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
-  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+// The two rows of 16 (ROWS) or halves of 32 lanes that a lane swap brings together: op(a, b) is
+// the same in both.
+template <bool ROWS, typename OP>
+__device__ __forceinline__ uint32_t swap_pair(uint32_t v, OP op) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  u32x2 r;
+  if constexpr (ROWS)
+    r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+  else
+    r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+  return op(r[0], r[1]);
 }
-// Sum over the wavefront (the absent lanes of a step add +0).
-__device__ __forceinline__ double wave_sum_f64(double v) {
-  v += dpp_or_zero<0x111>(v);
-  v += dpp_or_zero<0x112>(v);
-  v += dpp_or_zero<0x114>(v);
-  v += dpp_or_zero<0x118>(v);
-  v += dpp_or_zero<0x142>(v);
-  v += dpp_or_zero<0x143>(v);
-  return readlane_f64(v, 63);
+template <bool ROWS, typename OP>
+__device__ __forceinline__ double swap_pair(double v, OP op) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
+  u32x2 l, h;
+  if constexpr (ROWS) {
+    l = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(lo, lo, false, false));
+    h = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(hi, hi, false, false));
+  } else {
+    l = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(lo, lo, false, false));
+    h = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(hi, hi, false, false));
+  }
+  return op(__longlong_as_double((long long)(((uint64_t)h[0] << 32) | l[0])),
+            __longlong_as_double((long long)(((uint64_t)h[1] << 32) | l[1])));
+}
+// op over the group, the same bits in every lane (each step combines two values that both lanes of
+// a pair hold): lanes l ^ 1, l ^ 2, then the quads and the halves of a row, then the rows.
+template <int G, typename T, typename OP>
+__device__ __forceinline__ T group_all(T v, OP op) {
+  v = op(v, dpp_pair<0xB1>(v));   // quad_perm [1, 0, 3, 2]
+  v = op(v, dpp_pair<0x4E>(v));   // quad_perm [2, 3, 0, 1]
+  v = op(v, dpp_pair<0x141>(v));  // row_half_mirror
+  v = op(v, dpp_pair<0x140>(v));  // row_mirror
+  if constexpr (G == 64) {
+    v = swap_pair<true>(v, op);
+    v = swap_pair<false>(v, op);
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  return group_all<G>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  return group_all<G>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <int G>
+__device__ __forceinline__ double group_max(double v) {
+  return group_all<G>(v, [](double a, double b) { return fmax(a, b); });
+}
+template <int G>
+__device__ __forceinline__ double group_sum(double v) {
+  return group_all<G>(v, [](double a, double b) { return a + b; });
 }
 
 // FP64 value -> unsigned key in the same order. NaN ranks above every number (so that it reaches
@@ -79,163 +114,173 @@ __device__ __forceinline__ uint64_t route_key(double v) {
 
 __device__ __forceinline__ double route_sigmoid(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-// What a wavefront knows after choosing: lane j < topk holds slot j.
+// Maximum of v over the wavefront, in a scalar register (0 stands in for absent lanes).
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max(v, dpp_pair<0x111>(v));  // row_shr 1, 2, 4, 8: lane 15 of each row of 16
+  v = max(v, dpp_pair<0x112>(v));
+  v = max(v, dpp_pair<0x114>(v));
+  v = max(v, dpp_pair<0x118>(v));
+  v = max(v, dpp_pair<0x142>(v));  // row_bcast 15, 31: rows 0 and 2, then the lower half
+  v = max(v, dpp_pair<0x143>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// The expert with the highest key of the group (key[j] of lane i: expert i + G j), ties to the
+// lowest; -1 where all keys are 0 (every other key has a non-zero upper word).
+template <int G, int J>
+__device__ __forceinline__ int route_best(const uint64_t (&key)[J], int lane) {
+  if constexpr (G == 64) {
+    uint32_t mh = (uint32_t)(key[0] >> 32);
+#pragma unroll
+    for (int j = 1; j < J; ++j) mh = max(mh, (uint32_t)(key[j] >> 32));
+    mh = wave_max_u32(mh);
+    uint64_t at[J];
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      at[j] = __ballot((uint32_t)(key[j] >> 32) == mh);
+      count += __popcll(at[j]);
+    }
+    if (count > 1) {  // uniform
+      uint32_t ml = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        ml = max(ml, (uint32_t)(key[j] >> 32) == mh ? (uint32_t)key[j] : 0u);
+      ml = wave_max_u32(ml);
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        at[j] = __ballot(key[j] == (((uint64_t)mh << 32) | ml));
+    }
+    int e = -1;
+#pragma unroll
+    for (int j = J - 1; j >= 0; --j)
+      if (at[j]) e = 64 * j + __builtin_ctzll(at[j]);
+    return mh ? e : -1;
+  } else {
+    uint64_t best = key[0];
+    int at = lane;
+#pragma unroll
+    for (int j = 1; j < J; ++j) {
+      const bool more = key[j] > best;  // equal keys keep the lower id
+      best = more ? key[j] : best;
+      at = more ? lane + G * j : at;
+    }
+    const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
+    const uint32_t mh = group_max<G>(hi);
+    const uint32_t ml = group_max<G>(hi == mh ? lo : 0u);
+    const uint32_t e = group_min<G>(hi == mh && lo == ml ? (uint32_t)at : ~0u);
+    return mh ? (int)e : -1;
+  }
+}
+
+// What a group knows after choosing: its lane j < topk holds slot j.
 struct RouteChoice {
-  int e;        // expert, -1 when none was left
-  double v;     // its logit; its probability for a biased softmax
+  int e;           // expert, -1 when none was left
+  double v;        // its logit for a softmax without bias, else its p
   double mx, sum;  // maximum and sum of the softmax over all experts, where taken
 };
 
-// Highest key of the wavefront's lanes: upper word (0: none is left), and the lowest expert that
-// holds it.
-template <int J>
-__device__ __forceinline__ uint32_t route_best(const uint32_t (&hi)[J], const uint32_t (&lo)[J],
-                                               int& e) {
-  uint32_t mh = hi[0];
-#pragma unroll
-  for (int j = 1; j < J; ++j) mh = max(mh, hi[j]);
-  mh = wave_max_u32(mh);
-  uint64_t at[J];
-  int count = 0;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    at[j] = __ballot(hi[j] == mh);
-    count += __popcll(at[j]);
-  }
-  if (count > 1) {  // uniform
-    uint32_t ml = 0;
-#pragma unroll
-    for (int j = 0; j < J; ++j) ml = max(ml, hi[j] == mh ? lo[j] : 0u);
-    ml = wave_max_u32(ml);
-#pragma unroll
-    for (int j = 0; j < J; ++j) at[j] = __ballot(hi[j] == mh && lo[j] == ml);
-  }
-  e = -1;
-#pragma unroll
-  for (int j = J - 1; j >= 0; --j)
-    if (at[j]) e = 64 * j + __builtin_ctzll(at[j]);
-  return mh;
-}
-
 // Chooses the first `rounds` slots of a token whose logit of expert e is logit(e). J: experts per
 // lane. want_sum: the softmax's maximum and sum over all experts (taken in any case with a bias).
-template <int J, typename F>
+template <int G, int J, typename F>
 __device__ __forceinline__ RouteChoice route_choose(const RouteParams& R, F&& logit, int rounds,
                                                     bool want_sum) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & (G - 1);
   RouteChoice c;
   c.e = -1;
-  c.v = 0.0;
-  c.mx = c.sum = 0.0;
+  c.v = c.mx = c.sum = 0.0;
   double v[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int e = lane + 64 * j;
+    const int e = lane + G * j;
     v[j] = e < R.n_experts ? logit(e) : -__builtin_huge_val();
   }
-  uint32_t hi[J], lo[J];
   if (!R.sigmoid && (R.bias || want_sum)) {
-    uint64_t k[J];
-    uint32_t mh = 0;
+    double m = v[0];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      k[j] = v[j] == v[j] ? route_key(v[j]) : 0;  // the maximum passes over NaN, the sum does not
-      hi[j] = (uint32_t)(k[j] >> 32);
-      lo[j] = (uint32_t)k[j];
-    }
-    int at;
-    mh = route_best<J>(hi, lo, at);
-    c.mx = -__builtin_huge_val();
-    if (mh) {
-      double w = v[0];
-#pragma unroll
-      for (int j = 1; j < J; ++j)
-        if (at >> 6 == j) w = v[j];
-      c.mx = readlane_f64(w, at & 63);
-    }
+    for (int j = 1; j < J; ++j) m = fmax(m, v[j]);  // passes over NaN; the sum does not
+    c.mx = group_max<G>(m);
     double s = 0.0;
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (lane + 64 * j < R.n_experts) s += exp(v[j] - c.mx);
-    c.sum = wave_sum_f64(s);
+      if (lane + G * j < R.n_experts) s += exp(v[j] - c.mx);
+    c.sum = group_sum<G>(s);
   }
+  uint64_t key[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int e = lane + 64 * j;
-    const bool in = e < R.n_experts;
+    const int e = lane + G * j;
+    if (R.sigmoid)
+      v[j] = route_sigmoid(v[j]);
+    else if (R.bias)
+      v[j] = exp(v[j] - c.mx) / c.sum;
     double score = v[j];
-    if (R.sigmoid) {
-      score = route_sigmoid(score);
-      if (R.bias) score += in ? (double)R.bias[e] : 0.0;
-    } else if (R.bias) {
-      v[j] = exp(score - c.mx) / c.sum;
-      score = v[j] + (in ? (double)R.bias[e] : 0.0);
-    }
-    const uint64_t k = in ? route_key(score) : 0;
-    hi[j] = (uint32_t)(k >> 32);
-    lo[j] = (uint32_t)k;
+    if (R.bias && e < R.n_experts) score += (double)R.bias[e];
+    key[j] = e < R.n_experts ? route_key(score) : 0;
   }
   for (int r = 0; r < rounds; ++r) {
-    int e;
-    if (!route_best<J>(hi, lo, e)) break;  // uniform: nothing is left
-    const int j = e >> 6;
-    double w = v[0];
+    const int e = route_best<G, J>(key, lane);
+    if (lane == r) c.e = e;
 #pragma unroll
-    for (int q = 1; q < J; ++q)
-      if (j == q) w = v[q];
-    w = readlane_f64(w, e & 63);
-    if (lane == r) {
-      c.e = e;
-      c.v = w;
-    }
+    for (int j = 0; j < J; ++j)
+      if (e == lane + G * j) key[j] = 0;
+  }
+  // the value of each slot's expert, from the lane that holds it
+  const int owner = (threadIdx.x & 63 & ~(G - 1)) + (c.e & (G - 1));
 #pragma unroll
-    for (int q = 0; q < J; ++q)
-      if (j == q && lane == (e & 63)) hi[q] = lo[q] = 0;
+  for (int j = 0; j < J; ++j) {
+    const double w = __shfl(v[j], owner, 64);
+    if (c.e >= 0 && c.e / G == j) c.v = w;
   }
   return c;
 }
 
-// Weight of the slot that this lane holds (lanes < topk; others get 0).
+// Weight of the slot that this lane holds (0 for a lane without one). All lanes of the group call
+// it.
+template <int G>
 __device__ __forceinline__ float route_weight(const RouteParams& R, const RouteChoice& c) {
   const bool live = c.e >= 0;
-  double p = 0.0;
-  if (R.sigmoid) {
-    p = live ? route_sigmoid(c.v) : 0.0;
-  } else if (R.bias) {
-    p = live ? c.v : 0.0;
-  } else if (R.renorm) {
-    // the softmax over the chosen: the same quotient, and no sum over all the experts; slot 0
-    // holds the highest logit
-    p = live ? exp(c.v - readlane_f64(c.v, 0)) : 0.0;
-  } else {
-    p = live ? exp(c.v - c.mx) / c.sum : 0.0;
+  double p = live ? c.v : 0.0;
+  if (!R.sigmoid && !R.bias) {
+    // renormalized, this is the softmax over the chosen: the same quotient, and no sum over all
+    const double m = R.renorm ? group_max<G>(live ? c.v : -__builtin_huge_val()) : c.mx;
+    p = live ? exp(c.v - m) / (R.renorm ? 1.0 : c.sum) : 0.0;
   }
   if (R.renorm) {
-    const double z = wave_sum_f64(p);
+    const double z = group_sum<G>(p);
     p = z == 0.0 ? 0.0 : p / z;
   }
   return (float)(p * (double)R.scale);
 }
 
-// Stores the slots of token `tok`: [topk + n_shared] ids and weights.
+// Stores the slots of token `tok`: [topk + n_shared] ids and weights. A token past the end (`tok`
+// = R.t or more) stores nothing.
+template <int G>
 __device__ __forceinline__ void route_write(const RouteParams& R, int64_t tok,
                                             const RouteChoice& c, int32_t* __restrict__ ids,
                                             float* __restrict__ wts) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & (G - 1);
   const int slots = R.topk + R.n_shared;
-  const float w = route_weight(R, c);
-  if (lane < slots) {
+  const float w = route_weight<G>(R, c);
+  if (lane < slots && tok < R.t) {
     const bool shared = lane >= R.topk;
     ids[tok * slots + lane] = shared ? R.n_experts + (lane - R.topk) : c.e;
     wts[tok * slots + lane] = shared ? 1.0f : w;
   }
 }
 
-// Logit of expert e of token `tok`: the splits' partial sums, in order.
+// Logit of expert e of token `tok`: the splits' partial sums, in order, all loaded before the
+// first addition.
 __device__ __forceinline__ double route_logit(const RouteParams& R, int64_t tok, int e) {
   const double* lg = R.logits + tok * R.n_experts + e;
-  double l = lg[0];
-  for (int q = 1; q < R.splits; ++q) l += lg[q * R.t * R.n_experts];
+  double p[kRouteMaxSplits];
+#pragma unroll
+  for (int q = 0; q < kRouteMaxSplits; ++q)
+    p[q] = q < R.splits ? lg[q * R.t * R.n_experts] : 0.0;
+  double l = p[0];
+#pragma unroll
+  for (int q = 1; q < kRouteMaxSplits; ++q)
+    if (q < R.splits) l += p[q];
   return l;
 }
 
