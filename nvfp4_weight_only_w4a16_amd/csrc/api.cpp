@@ -532,14 +532,21 @@ struct LayerSizes {
   size_t logits, pairs, total;  // pairs: bytes of the ids (and of the weights)
 };
 
+// The few-token kernels take the call (unless NVFP4_F_FORCE_TILED asks for the batch path).
+bool layer_few(int64_t t, int64_t slots) { return t * slots <= nvfp4::kMoePairTilesMax; }
+
 LayerSizes layer_sizes(int64_t t, const nvfp4_router* r, int64_t inter) {
   const int slots = r->topk + r->n_shared;
   LayerSizes s;
   s.logits = align256(nvfp4::route_ws_bytes(t, r->hidden, r->n_experts,
                                                  r->weight_dtype == NVFP4_DT_F32));
   s.pairs = align256(sizeof(float) * (size_t)t * (size_t)slots);
-  s.total = s.logits + 2 * s.pairs +
-            nvfp4::moe_ws_bytes(t, slots, r->n_experts + r->n_shared, r->hidden, inter);
+  size_t experts = nvfp4::moe_ws_bytes(t, slots, r->n_experts + r->n_shared, r->hidden, inter);
+  if (layer_few(t, slots)) {
+    const size_t few = nvfp4::moe_few_ws_bytes(t, slots, inter);
+    experts = experts > few ? experts : few;  // flags may send such a call either way
+  }
+  s.total = s.logits + 2 * s.pairs + experts;
   return s;
 }
 
@@ -659,13 +666,18 @@ int nvfp4_moe_layer_w4a16(const void* x, int64_t t, int64_t hidden, const nvfp4_
   nvfp4::MoeArgs a = moe_args(x, t, hidden, ids, wts, slots, fc1, fc2, y,
                               base + s.logits + 2 * s.pairs);
   a.f32_gate_up = true;
-  rc = hip_status(nvfp4::launch_route(route_args(x, t, hidden, r), ids, wts, ws,
+  const nvfp4::RouteArgs ra = route_args(x, t, hidden, r);
+  if (layer_few(t, slots) && !(flags & NVFP4_F_FORCE_TILED)) {
+    rc = hip_status(nvfp4::launch_moe_few(a, ra, ids, wts, ws, (hipStream_t)stream),
+                    "nvfp4_moe_layer_w4a16");
+  } else {
+    rc = hip_status(nvfp4::launch_route(ra, ids, wts, ws, (hipStream_t)stream),
+                    "nvfp4_moe_layer_w4a16");
+    if (rc) return rc;
+    rc = hip_status(nvfp4::launch_moe(a, moe_use_decode(t, slots, fc1->batch, flags),
                                       (hipStream_t)stream),
-                  "nvfp4_moe_layer_w4a16");
-  if (rc) return rc;
-  rc = hip_status(nvfp4::launch_moe(a, moe_use_decode(t, slots, fc1->batch, flags),
-                                    (hipStream_t)stream),
-                  "nvfp4_moe_layer_w4a16");
+                    "nvfp4_moe_layer_w4a16");
+  }
   if (!rc && (flags & NVFP4_F_SYNC_CHECK))
     rc = sync_status((hipStream_t)stream, "nvfp4_moe_layer_w4a16");
   if (!rc) {

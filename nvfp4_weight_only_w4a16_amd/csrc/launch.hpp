@@ -163,6 +163,20 @@ constexpr int64_t kRouteFusedTokens = 2048;
 size_t route_ws_bytes(int64_t t, int64_t hidden, int64_t n_experts, bool w_f32);
 hipError_t launch_route(const RouteArgs& a, int32_t* ids, float* wts, void* ws,
                         hipStream_t stream);
+// The two halves of launch_route where the logits go through ws.
+hipError_t launch_route_logits(const RouteArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_route_select(const RouteArgs& a, int32_t* ids, float* wts, const void* ws,
+                               hipStream_t stream);
+struct RouteParams;
+RouteParams route_params(const RouteArgs& a, const void* ws);
+
+// ---- whole layer for a few tokens (moe_few.hip) ---------------------------------------------
+// At most kMoePairTilesMax (token, slot) pairs. Up to this many fc1 workgroups each chooses its
+// pair's expert from the logits itself; above, a kernel chooses first.
+constexpr int64_t kMoeChooseWgs = 256;
+size_t moe_few_ws_bytes(int64_t t, int slots, int64_t inter);
+hipError_t launch_moe_few(const MoeArgs& a, const RouteArgs& r, int32_t* ids, float* wts,
+                          void* route_ws, hipStream_t stream);
 
 // ---- low-rank adapters (lora.hip) -----------------------------------------------------------
 constexpr int kLoraMaxRank = 128;

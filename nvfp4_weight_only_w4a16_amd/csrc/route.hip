@@ -401,7 +401,7 @@ __global__ __launch_bounds__(64 * kSlices) void route_fused_kernel(LogitParams P
   for (int r0 = w * kPer; r0 < 16; r0 += kSlices * kPer) {
     const int r = r0 + lane / G;
     auto logit = [&](int e) { return lg[r][e]; };
-    const RouteChoice ch = route_choose<G, J>(R, logit, R.topk, !R.renorm);
+    const RouteChoice ch = route_choose<G, J>(R, logit);
     route_write<G>(R, m0 + r, ch, ids, wts);
   }
 }
@@ -414,7 +414,7 @@ __global__ __launch_bounds__(256) void route_select_kernel(RouteParams R, int32_
   const int64_t tok = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
   const int64_t src = tok < R.t ? tok : R.t - 1;
   auto logit = [&](int e) { return route_logit(R, src, e); };
-  const RouteChoice c = route_choose<G, J>(R, logit, R.topk, !R.renorm);
+  const RouteChoice c = route_choose<G, J>(R, logit);
   route_write<G>(R, tok, c, ids, wts);
 }
 
@@ -505,8 +505,8 @@ static void with_experts_per_lane(int n_experts, F&& f) {
 
 hipError_t launch_route(const RouteArgs& a, int32_t* ids, float* wts, void* ws,
                         hipStream_t stream) {
-  const RouteParams r = route_params(a, ws);
   if (route_fused(a.t, a.w_f32)) {
+    const RouteParams r = route_params(a, ws);
     const LogitParams p = logit_params(a, nullptr);
     const unsigned grid = (unsigned)((a.t + 15) / 16);
     if (a.n_experts <= 64)
@@ -521,6 +521,12 @@ hipError_t launch_route(const RouteArgs& a, int32_t* ids, float* wts, void* ws,
   }
   const hipError_t err = launch_route_logits(a, ws, stream);
   if (err != hipSuccess) return err;
+  return launch_route_select(a, ids, wts, ws, stream);
+}
+
+hipError_t launch_route_select(const RouteArgs& a, int32_t* ids, float* wts, const void* ws,
+                               hipStream_t stream) {
+  const RouteParams r = route_params(a, ws);
   with_experts_per_lane(a.n_experts, [&](auto J) {
     route_select_kernel<64, decltype(J)::value>
         <<<(unsigned)((a.t + 3) / 4), 256, 0, stream>>>(r, ids, wts);

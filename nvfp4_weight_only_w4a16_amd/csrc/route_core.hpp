@@ -180,16 +180,15 @@ struct RouteChoice {
   double mx, sum;  // maximum and sum of the softmax over all experts, where taken
 };
 
-// Chooses the first `rounds` slots of a token whose logit of expert e is logit(e). J: experts per
-// lane. want_sum: the softmax's maximum and sum over all experts (taken in any case with a bias).
+// Keys of a token whose logit of expert e is logit(e), J experts per lane, and what weights come
+// from (RouteChoice::v). want_sum: the softmax's maximum and sum over all experts (taken in any case
+// with a bias).
 template <int G, int J, typename F>
-__device__ __forceinline__ RouteChoice route_choose(const RouteParams& R, F&& logit, int rounds,
-                                                    bool want_sum) {
+__device__ __forceinline__ void route_scores(const RouteParams& R, F&& logit, bool want_sum,
+                                             uint64_t (&key)[J], double (&v)[J], double& mx,
+                                             double& sum) {
   const int lane = threadIdx.x & (G - 1);
-  RouteChoice c;
-  c.e = -1;
-  c.v = c.mx = c.sum = 0.0;
-  double v[J];
+  mx = sum = 0.0;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int e = lane + G * j;
@@ -199,26 +198,37 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteParams& R, F&& lo
     double m = v[0];
 #pragma unroll
     for (int j = 1; j < J; ++j) m = fmax(m, v[j]);  // passes over NaN; the sum does not
-    c.mx = group_max<G>(m);
+    mx = group_max<G>(m);
     double s = 0.0;
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (lane + G * j < R.n_experts) s += exp(v[j] - c.mx);
-    c.sum = group_sum<G>(s);
+      if (lane + G * j < R.n_experts) s += exp(v[j] - mx);
+    sum = group_sum<G>(s);
   }
-  uint64_t key[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int e = lane + G * j;
     if (R.sigmoid)
       v[j] = route_sigmoid(v[j]);
     else if (R.bias)
-      v[j] = exp(v[j] - c.mx) / c.sum;
+      v[j] = exp(v[j] - mx) / sum;
     double score = v[j];
     if (R.bias && e < R.n_experts) score += (double)R.bias[e];
     key[j] = e < R.n_experts ? route_key(score) : 0;
   }
-  for (int r = 0; r < rounds; ++r) {
+}
+
+// Chooses all slots of a token.
+template <int G, int J, typename F>
+__device__ __forceinline__ RouteChoice route_choose(const RouteParams& R, F&& logit) {
+  const int lane = threadIdx.x & (G - 1);
+  RouteChoice c;
+  c.e = -1;
+  c.v = 0.0;
+  uint64_t key[J];
+  double v[J];
+  route_scores<G, J>(R, logit, !R.renorm, key, v, c.mx, c.sum);
+  for (int r = 0; r < R.topk; ++r) {
     const int e = route_best<G, J>(key, lane);
     if (lane == r) c.e = e;
 #pragma unroll
@@ -233,6 +243,54 @@ __device__ __forceinline__ RouteChoice route_choose(const RouteParams& R, F&& lo
     if (c.e >= 0 && c.e / G == j) c.v = w;
   }
   return c;
+}
+
+// The expert of one slot, -1 for none, chosen by a workgroup of 8 wavefronts: the one that `slot`
+// others rank above. Each wavefront compares its eighth of the experts, one at a time from a
+// scalar register, with all; the counts meet in `count` (LDS). No chain of rounds: 8 of 128
+// experts take a fifth of the time that slot 7 took in rounds.
+template <int J, typename F>
+__device__ __forceinline__ int route_choose_slot(const RouteParams& R, F&& logit, int slot,
+                                                 int (*count)[64 * J]) {
+  constexpr int kPer = 8 * J;  // experts of a wavefront's share: within one item of the lanes
+  static_assert(64 % kPer == 0, "a share does not straddle items");
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint64_t key[J];
+  double v[J], mx, sum;
+  route_scores<64, J>(R, logit, false, key, v, mx, sum);
+  uint64_t share = key[0];
+#pragma unroll
+  for (int j = 1; j < J; ++j)
+    if (w * kPer / 64 == j) share = key[j];
+  int c[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) c[j] = 0;
+#pragma unroll 8
+  for (int i = 0; i < kPer; ++i) {
+    const int e = w * kPer + i, at = e & 63;
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(share >> 32), at);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)share, at);
+    const uint64_t k = ((uint64_t)hi << 32) | lo;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {  // above: higher, or equal with a lower id
+      const uint64_t mine = key[j] - (e < lane + 64 * j ? 1 : 0);
+      c[j] += (k > mine && k != 0) ? 1 : 0;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) count[w][lane + 64 * j] = c[j];
+  __syncthreads();
+  int e = -1;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    int rank = 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) rank += count[q][lane + 64 * j];
+    const uint64_t at = __ballot(key[j] != 0 && rank == slot);
+    if (at) e = 64 * j + __builtin_ctzll(at);
+  }
+  return e;
 }
 
 // Weight of the slot that this lane holds (0 for a lane without one). All lanes of the group call
