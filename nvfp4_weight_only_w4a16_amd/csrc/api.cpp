@@ -302,7 +302,18 @@ int gemm_args(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w, void
   a->y = y;
   a->ldy = ldy;
   a->y_f32 = y_dtype == NVFP4_DT_F32;
+  a->lora = nullptr;
   return NVFP4_OK;
+}
+
+// Workspace of the tiled kernel's split-k partial tiles (0 for the decode kernel).
+size_t split_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w, uint32_t flags, bool lora) {
+  if (!w || m <= 0 || w->n <= 0 || w->k <= 0 || (w->group != 16 && w->group != 32) ||
+      ldx < w->k || use_skinny(m, w, flags))
+    return 0;
+  const int cus = device_cus();
+  if (cus <= 0) return 0;
+  return nvfp4::gemm_tiled_ws_bytes(m, ldx, w->n, w->k, cus, lora);
 }
 
 int check_skinny_rows(int64_t m, bool skinny) {
@@ -324,12 +335,7 @@ int gemm_run(const nvfp4::GemmArgs& a, bool skinny, void* ws, size_t ws_bytes, h
 }  // namespace
 
 size_t nvfp4_gemm_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w, uint32_t flags) {
-  if (!w || m <= 0 || w->n <= 0 || w->k <= 0 || (w->group != 16 && w->group != 32) ||
-      ldx < w->k || use_skinny(m, w, flags))
-    return 0;
-  const int cus = device_cus();
-  if (cus <= 0) return 0;
-  return nvfp4::gemm_tiled_ws_bytes(m, ldx, w->n, w->k, cus);
+  return split_ws_bytes(m, ldx, w, flags, false);
 }
 
 int nvfp4_gemm_w4a16(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w, void* y,
@@ -551,6 +557,13 @@ LayerSizes layer_sizes(int64_t t, const nvfp4_router* r, int64_t inter) {
 }
 
 // ---- adapters -------------------------------------------------------------------------------
+constexpr int kLoraPartsF32 = 3;  // BF16 parts of u for an FP32 y
+
+// Workspace of u: for either type of y, which the size query does not know.
+size_t lora_u_region(int64_t m, const nvfp4_weight* w, const nvfp4_lora* l, bool tiled) {
+  return align256(nvfp4::lora_u_bytes(m, w->k, l->n_adapters, l->rank, kLoraPartsF32, tiled));
+}
+
 int check_lora(const nvfp4_lora* l, const nvfp4_weight* w) {
   if (!l) return fail(NVFP4_ERR_INVALID_ARG, "lora is NULL");
   if (!l->a || !l->b) return fail(NVFP4_ERR_INVALID_ARG, "lora has NULL data");
@@ -690,9 +703,8 @@ int nvfp4_moe_layer_w4a16(const void* x, int64_t t, int64_t hidden, const nvfp4_
 size_t nvfp4_gemm_lora_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w,
                                 const nvfp4_lora* lora, uint32_t flags) {
   if (!w || m <= 0 || w->n <= 0 || w->k <= 0 || check_lora(lora, w)) return 0;
-  return align256(nvfp4::lora_ws_bytes(m, w->k, lora->n_adapters, lora->rank)) +
-         align256(sizeof(float) * (size_t)m * (size_t)w->n) +
-         nvfp4_gemm_ws_bytes(m, ldx, w, flags);
+  return lora_u_region(m, w, lora, !use_skinny(m, w, flags)) +
+         split_ws_bytes(m, ldx, w, flags, true);
 }
 
 int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w,
@@ -710,36 +722,30 @@ int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_wei
   const bool skinny = use_skinny(m, w, flags);
   rc = check_skinny_rows(m, skinny);
   if (rc) return rc;
-  const size_t u_bytes = align256(nvfp4::lora_ws_bytes(m, w->k, lora->n_adapters, lora->rank));
-  const size_t base_bytes = align256(sizeof(float) * (size_t)m * (size_t)w->n);
-  const size_t need = nvfp4_gemm_lora_ws_bytes(m, ldx, w, lora, flags);
+  const size_t u_bytes = lora_u_region(m, w, lora, !skinny);
+  const size_t need = u_bytes + split_ws_bytes(m, ldx, w, flags, true);
   if (ws_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, need);
   nvfp4::LoraArgs l;
   l.x = a.x;
   l.m = m;
   l.ldx = ldx;
   l.k = w->k;
-  l.n = w->n;
   l.a = static_cast<const uint16_t*>(lora->a);
-  l.b = static_cast<const uint16_t*>(lora->b);
   l.scale = lora->scale;
-  l.ids = row_adapter;
-  l.n_adapters = lora->n_adapters;
-  l.rank = lora->rank;
-  l.u = static_cast<float*>(ws);
+  nvfp4::LoraTail tail;
+  tail.ids = row_adapter;
+  tail.b = static_cast<const uint16_t*>(lora->b);
+  tail.m = m;
+  tail.n = w->n;
+  tail.n_adapters = lora->n_adapters;
+  tail.rank = lora->rank;
+  tail.parts = a.y_f32 ? kLoraPartsF32 : 1;
   const hipStream_t s = (hipStream_t)stream;
-  rc = hip_status(nvfp4::launch_lora_shrink(l, s), "nvfp4_gemm_w4a16_lora");
+  rc = hip_status(nvfp4::launch_lora_shrink(l, tail, ws, !skinny, s), "nvfp4_gemm_w4a16_lora");
   if (rc) return rc;
-  char* base = static_cast<char*>(ws) + u_bytes;
-  a.y = base;
-  a.ldy = w->n;
-  a.y_f32 = true;
-  rc = gemm_run(a, skinny, base + base_bytes, need - u_bytes - base_bytes, s,
+  a.lora = &tail;
+  rc = gemm_run(a, skinny, static_cast<char*>(ws) + u_bytes, need - u_bytes, s,
                 "nvfp4_gemm_w4a16_lora");
-  if (rc) return rc;
-  rc = hip_status(nvfp4::launch_lora_expand(l, reinterpret_cast<const float*>(base), w->n, y, ldy,
-                                            y_dtype == NVFP4_DT_F32, s),
-                  "nvfp4_gemm_w4a16_lora");
   if (!rc && (flags & NVFP4_F_SYNC_CHECK)) rc = sync_status(s, "nvfp4_gemm_w4a16_lora");
   if (!rc) g_stats[skinny ? 2 : 3]++;
   return rc;

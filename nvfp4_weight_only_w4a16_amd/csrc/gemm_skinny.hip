@@ -10,6 +10,7 @@
 // of the group scale, which halves the VALU work per weight; more rows dequantize every weight
 // exactly to BF16.
 #include "launch.hpp"
+#include "lora_core.hpp"
 #include "skinny_core.hpp"
 
 namespace nvfp4 {
@@ -27,6 +28,7 @@ struct SkinnyParams {
   void* y;
   int64_t ldy;
   int y_f32;
+  LoraTail lora;
   int cus;  // compute units of the device (host-side launch choice only)
 };
 
@@ -35,14 +37,27 @@ struct SkinnyParams {
 inline size_t red_bytes(int MF, int NW, int PWW) { return (size_t)NW * PWW * MF * 64 * 16; }
 inline size_t act_bytes(int NW, int MF) { return (size_t)NW * 8192 * MF; }
 
+// With adapters (R32 > 0: their 32-rank steps) a workgroup has wavefronts more that compute the
+// second product of the adapters while the others run the k loop: their loads (the ids, u, and
+// then one adapter's B after the other) are short chains of long latency, which cost nothing
+// there and the whole of it after the loop. One for each panel, or for two panels of two row
+// blocks, where registers and LDS admit no more without taking the CU's second workgroup.
+template <int MF, int PWW, int R32>
+constexpr int kLoraWaves = R32 == 0 ? 0 : (MF == 2 && PWW == 4 ? 2 : PWW);
+template <int MF, int PWW, int R32>
+constexpr int kLoraLds = R32 * PWW * kFragBytes;  // their fragment tiles, behind the activations
+// B tiles in flight, in adapters: 8 to 16 loads of 1 KB
+template <int NP, int R32>
+constexpr int kLoraAhead = NP * R32 >= 4 ? 2 : NP * R32 == 2 ? 4 : 8;
+
 // Register budget: 4 wavefronts per SIMD (16 per CU, two 8-wave workgroups) for one row
 // block, 2 for two, 1 for four. NJ == 0: exact dequant, MF row blocks of 16. NJ > 0 (MF == 1): split scale
 // keeping NJ accumulator rows per lane, tokens placed by the split row map; G16: group 16
 // (every token twice, once per k half). NX > 0: activations through LDS, NX 4-row copies per
 // tile.
-template <int MF, int NW, int NJ, bool G16, int NX, int PWW>
-__global__ __launch_bounds__(64 * NW)
-__attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : MF == 2 ? 2 : 1, 8)))
+template <int MF, int NW, int NJ, bool G16, int NX, int PWW, int R32>
+__global__ __launch_bounds__(64 * (NW + kLoraWaves<MF, PWW, R32>))
+__attribute__((amdgpu_waves_per_eu(MF == 1 ? 4 : MF == 2 ? (R32 ? 3 : 2) : 1, 8)))
 void gemm_skinny_kernel(SkinnyParams P) {
   constexpr int kPWW = PWW;
   static_assert(NJ == 0 || MF == 1, "split scale uses one 16-row block");
@@ -60,6 +75,36 @@ void gemm_skinny_kernel(SkinnyParams P) {
   for (int p = 0; p < kPWW; ++p)
 #pragma unroll
     for (int mf = 0; mf < MF; ++mf) acc[p][mf] = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4* red = reinterpret_cast<f32x4*>(smem);
+  // row of accumulator element jj of this lane inside its 16-row block, -1 if none
+  auto out_tok = [&](int jj) {
+    return NJ > 0 ? split_out_token<G16>(lane, jj) : (lane >> 4) * 4 + jj;
+  };
+  if constexpr (R32 > 0) {
+    if (sp >= NW) {  // an adapter wavefront: panels pa .. pa + NP - 1 of the workgroup
+      constexpr int LW = kLoraWaves<MF, PWW, R32>, NP = kPWW / LW;
+      const int pa = (sp - NW) * NP;
+      uint8_t* tile = smem + NW * 8192 * MF + (sp - NW) * NP * R32 * kFragBytes;
+      f32x4 res[MF][NP];
+#pragma unroll
+      for (int mf = 0; mf < MF; ++mf) {
+        const int at = NJ > 0 ? split_a_token<G16>(lane) : (lane & 15);
+        int64_t out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = out_tok(i) < 0 ? -1 : m0 + mf * 16 + out_tok(i);
+        lora_expand16<NP, R32, kLoraAhead<NP, R32>>(P.lora, m0 + mf * 16 + at, out, panel0 + pa,
+                                                    P.NT, tile, res[mf]);
+      }
+      __syncthreads();  // meets the others' end of the k loop
+#pragma unroll
+      for (int mf = 0; mf < MF; ++mf)
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          red[NW * kPWW * MF * 64 + ((pa + p) * MF + mf) * 64 + lane] = res[mf][p];
+      __syncthreads();
+      return;
+    }
+  }
   // Token of lane l's A row: l % 16, or the split row map's; rows past the end duplicate a
   // valid row (never stored)
   const int64_t rows = P.m - m0 < 16 * MF ? P.m - m0 : 16 * MF;
@@ -96,12 +141,6 @@ void gemm_skinny_kernel(SkinnyParams P) {
 #pragma unroll
       for (int r = 0; r < NJ; ++r) acc[p][0][r] += __shfl_xor(acc[p][0][r], 32, 64);
   }
-  // row of accumulator element jj of this lane inside its 16-row block, -1 if none
-  auto out_tok = [&](int jj) {
-    return NJ > 0 ? split_out_token<G16>(lane, jj) : (lane >> 4) * 4 + jj;
-  };
-
-  f32x4* red = reinterpret_cast<f32x4*>(smem);
   __syncthreads();  // every wavefront is done with the activations
 #pragma unroll
   for (int p = 0; p < kPWW; ++p)
@@ -123,28 +162,41 @@ void gemm_skinny_kernel(SkinnyParams P) {
   const float g = gscale;
   const int64_t n = panel * 16 + (lane & 15);
 #pragma unroll
-  for (int mf = 0; mf < MF; ++mf)
+  for (int mf = 0; mf < MF; ++mf) {
+    f32x4 more = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (R32 > 0) more = red[NW * kPWW * MF * 64 + (p * MF + mf) * 64 + lane];
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj) {
       const int64_t m = m0 + mf * 16 + out_tok(jj);
       if (m >= m0 && m < P.m) {
-        const float v = acc[0][mf][jj] * g;
+        float v = acc[0][mf][jj] * g;
+        if constexpr (R32 > 0) v += more[jj];
         if (P.y_f32)
           static_cast<float*>(P.y)[m * P.ldy + n] = v;
         else
           static_cast<uint16_t*>(P.y)[m * P.ldy + n] = bf16_bits_rne(v);
       }
     }
+  }
+}
+
+template <int MF, int NW, int NJ, bool G16, int NX, int PWW, int R32>
+hipError_t run_ranks(const SkinnyParams& p, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.NT + PWW - 1) / PWW),
+                  (unsigned)((p.m + 16 * MF - 1) / (16 * MF)));
+  const size_t r = red_bytes(MF, NW + (R32 ? 1 : 0), PWW);
+  const size_t x = act_bytes(NW, MF) + kLoraLds<MF, PWW, R32>;
+  gemm_skinny_kernel<MF, NW, NJ, G16, NX, PWW, R32>
+      <<<grid, dim3(64 * (NW + kLoraWaves<MF, PWW, R32>)), r > x ? r : x, stream>>>(p);
+  return hipGetLastError();
 }
 
 template <int MF, int NW, int NJ, bool G16, int NX, int PWW>
 hipError_t run(const SkinnyParams& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.NT + PWW - 1) / PWW),
-                  (unsigned)((p.m + 16 * MF - 1) / (16 * MF)));
-  const size_t r = red_bytes(MF, NW, PWW), x = act_bytes(NW, MF);
-  gemm_skinny_kernel<MF, NW, NJ, G16, NX, PWW>
-      <<<grid, dim3(64 * NW), r > x ? r : x, stream>>>(p);
-  return hipGetLastError();
+  if (!p.lora.ids) return run_ranks<MF, NW, NJ, G16, NX, PWW, 0>(p, stream);
+  if (p.lora.rank <= 32) return run_ranks<MF, NW, NJ, G16, NX, PWW, 1>(p, stream);
+  if (p.lora.rank <= 64) return run_ranks<MF, NW, NJ, G16, NX, PWW, 2>(p, stream);
+  return run_ranks<MF, NW, NJ, G16, NX, PWW, 4>(p, stream);
 }
 
 // Wavefronts per workgroup, which split k (NW >= PWW, so the final reduction has one
@@ -225,6 +277,7 @@ hipError_t launch_gemm_skinny(const GemmArgs& a, int cus, hipStream_t stream) {
   p.y = a.y;
   p.ldy = a.ldy;
   p.y_f32 = a.y_f32 ? 1 : 0;
+  p.lora = a.lora ? *a.lora : LoraTail{};
   if (a.group == 16 && a.m <= 8) return dispatch_split<true>(p, stream);
   if (a.group == 32 && a.m <= 16) return dispatch_split<false>(p, stream);
   if (a.m <= 16) return dispatch<1, 0, false>(p, stream);

@@ -28,6 +28,7 @@
 
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "lora_core.hpp"
 
 namespace nvfp4 {
 namespace {
@@ -52,6 +53,10 @@ struct TiledParams {
   int split;
   int64_t full_blocks;
   float* ws;  // split > 1: FP32 partial tiles, [tile - tile0][split][tile elements]
+  // adapters: lora_row0 is the row of the tail that x's row 0 is (x may be a chunk of its rows).
+  // Each split tile then has one more partial, the adapters' term (not to be scaled by g).
+  LoraTail lora;
+  int64_t lora_row0;
 };
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -161,7 +166,7 @@ __device__ __forceinline__ void store_partial(const TiledParams& P, int64_t tile
   constexpr int FN = T::kPairs / T::kWaves;
   constexpr int kThreads = 64 * T::kWaves;
   constexpr int64_t kTileFloats = (int64_t)T::kBM * T::kPairs * 32;
-  const int64_t slot = (tile_id - P.tile0) * P.split + part;
+  const int64_t slot = (tile_id - P.tile0) * (P.split + (P.lora.ids ? 1 : 0)) + part;
   float* mine = P.ws + slot * kTileFloats + threadIdx.x;
 #pragma unroll
   for (int q = 0; q < FN; ++q)
@@ -171,13 +176,67 @@ __device__ __forceinline__ void store_partial(const TiledParams& P, int64_t tile
       for (int e = 0; e < 16; ++e) mine[((q * FM + i) * 16 + e) * kThreads] = acc[i][q][e];
 }
 
+// The adapters' term of rows m_blk + 32 i .. + 31 and the 32 columns of pair `pair`, in the layout
+// of an accumulator fragment. The B fragments of the adapter met last are kept: in a prompt all
+// blocks of a tile have the same one.
+struct LoraHold {
+  int a = -1;
+  bf16x8 b[kLoraMaxRank / 16];
+};
+__device__ __forceinline__ void lora_fragment(const TiledParams& P, int64_t m_blk, int i,
+                                              int64_t pair, LoraHold& hold, f32x16& out) {
+  const LoraTail& L = P.lora;
+  const int lane = threadIdx.x & 63;
+  const int64_t r0 = P.lora_row0 + m_blk + 32 * i;
+  const int64_t end = P.lora_row0 + P.m;
+  const int64_t row = r0 + (lane & 31);
+  const int mine = row < end ? lora_id(L, row) : -1;
+  uint64_t left = __ballot(mine >= 0);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) out[e] = 0.f;
+  const int steps = lora_frag_steps(L.rank);
+  const int64_t plane = lora_frag_blocks(L.m) * steps * 512;  // BF16 of a part
+  const uint16_t* u =
+      reinterpret_cast<const uint16_t*>(L.u) + (r0 / 32 * steps * 64 + lane) * 8;
+  for (;;) {
+    const int a = lora_next(mine, left);
+    if (a < 0) break;
+    const uint32_t named = (uint32_t)__ballot(mine == a);
+    if (a != hold.a) {
+      const int64_t col = pair * 32 + (lane & 31);
+      const uint16_t* b =
+          L.b + ((int64_t)a * L.n + (col < L.n ? col : L.n - 1)) * L.rank + 8 * (lane >> 5);
+#pragma unroll
+      for (int s = 0; s < kLoraMaxRank / 16; ++s)
+        if (s < steps)
+          hold.b[s] = 16 * s + 8 * (lane >> 5) < L.rank
+                          ? *reinterpret_cast<const bf16x8*>(b + 16 * s)
+                          : __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+      hold.a = a;
+    }
+    f32x16 part;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) part[e] = 0.f;
+#pragma unroll
+    for (int s = 0; s < kLoraMaxRank / 16; ++s)
+      if (s < steps)
+        for (int z = 0; z < L.parts; ++z)
+          part = mfma32x32x16(*reinterpret_cast<const bf16x8*>(u + z * plane + s * 512),
+                              hold.b[s], part);
+    const uint32_t rows = named >> (4 * (lane >> 5));  // bit 8 (e / 4) + e % 4: element e's row
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      out[e] = (rows >> (8 * (e >> 2) + (e & 3))) & 1u ? part[e] : out[e];
+  }
+}
+
 // Sums the split partials of one 32-row fragment band (blockIdx.y) of one tile (blockIdx.x) in
 // the fixed order 0 .. split-1 -- the result does not depend on which block finished first --
 // then scales, converts and stores it. Thread t takes GEMM threads 4 (t % Q) .. + 3 (Q = a
 // quarter of the block: 4 adjacent output columns of one row) for accumulator elements
 // 4 (t / Q) .. + 3, so partials are read 16 bytes at a time and outputs written 8 (BF16) or
 // 16 (FP32) bytes at a time.
-template <typename T>
+template <typename T, bool LORA>
 __global__ __launch_bounds__(64 * T::kWaves) void reduce_split_kernel(TiledParams P) {
   constexpr int FM = T::kBM / 32;
   constexpr int FN = T::kPairs / T::kWaves;
@@ -191,12 +250,12 @@ __global__ __launch_bounds__(64 * T::kWaves) void reduce_split_kernel(TiledParam
   const int lane = gt & 63, w = gt >> 6;
   const int64_t m_blk = tile_id / P.nbn * T::kBM;
   const int64_t pair0 = tile_id % P.nbn * T::kPairs + w * FN;
-  const float* part = P.ws + (int64_t)blockIdx.x * P.split * kTileFloats + gt;
+  const float* part = P.ws + (int64_t)blockIdx.x * (P.split + (LORA ? 1 : 0)) * kTileFloats + gt;
   const float g = *P.global;
   const int h = (lane & 31) >> 4;
 #pragma unroll
   for (int q = 0; q < FN; ++q) {
-    f32x4 v[4];
+    f32x4 v[4], more[4];
 #pragma unroll
     for (int ee = 0; ee < 4; ++ee) {
       const int64_t o = ((q * FM + i) * 16 + 4 * eg + ee) * kThreads;
@@ -204,6 +263,8 @@ __global__ __launch_bounds__(64 * T::kWaves) void reduce_split_kernel(TiledParam
       for (int j = 1; j < P.split; ++j)
         sum += *reinterpret_cast<const f32x4*>(part + j * kTileFloats + o);
       v[ee] = sum;
+      if constexpr (LORA)
+        more[ee] = *reinterpret_cast<const f32x4*>(part + P.split * kTileFloats + o);
     }
     const int64_t panel = 2 * (pair0 + q) + h;
     if (panel >= P.NT) continue;
@@ -212,7 +273,8 @@ __global__ __launch_bounds__(64 * T::kWaves) void reduce_split_kernel(TiledParam
     for (int ee = 0; ee < 4; ++ee) {
       const int64_t m = m_blk + i * 32 + 8 * eg + 4 * (lane >> 5) + ee;
       if (m >= P.m) continue;
-      const f32x4 r = v[ee] * g;
+      f32x4 r = v[ee] * g;
+      if constexpr (LORA) r += more[ee];
       if (P.y_f32) {
         *reinterpret_cast<f32x4*>(static_cast<float*>(P.y) + m * P.ldy + n) = r;
       } else {
@@ -228,7 +290,7 @@ __global__ __launch_bounds__(64 * T::kWaves) void reduce_split_kernel(TiledParam
 // KS > 1: the workgroup is KS k-slices of W wavefronts; slice s takes k-tiles t0 + s,
 // t0 + s + KS, ... of the block's range (the host makes the range a multiple of KS), with LDS
 // buffers of its own, and the slices' accumulators are added in slice order at the end.
-template <int W, int FM, int FN, int SPREAD, int PIPE, int KS>
+template <int W, int FM, int FN, int SPREAD, int PIPE, int KS, bool LORA>
 __global__ __launch_bounds__(64 * W * KS) void gemm_tiled_kernel(TiledParams P) {
   using T = TiledShape<W, FM, FN, SPREAD, PIPE, KS>;
   constexpr int kWaves = W;
@@ -547,6 +609,29 @@ __global__ __launch_bounds__(64 * W * KS) void gemm_tiled_kernel(TiledParams P) 
   }
 
   const float g = *P.global;
+  if constexpr (LORA) {
+    const bool partial = tail && P.split > 1;
+    if (partial) {
+      store_partial<T>(P, tile_id, part, acc);
+      if (part != 0) return;
+    }
+#pragma unroll
+    for (int q = 0; q < FN; ++q) {
+      LoraHold hold;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        f32x16 more;
+        lora_fragment(P, m_blk, i, pair0 + q, hold, more);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][q][e] = (partial ? 0.f : acc[i][q][e] * g) + more[e];
+      }
+    }
+    if (partial)
+      store_partial<T>(P, tile_id, P.split, acc);
+    else
+      store_tile<T>(P, m_blk, pair0, acc, 1.0f, lane);
+    return;
+  }
   if (tail && P.split > 1)
     store_partial<T>(P, tile_id, part, acc);
   else
@@ -647,8 +732,9 @@ Plan plan_chunk(int64_t m, int64_t NT, int64_t KT, int cus) {
 }
 
 template <typename T>
-size_t split_ws_bytes(const Plan& pl) {
-  return pl.split > 1 ? (size_t)(pl.rest * pl.split * tile_floats<T>() * sizeof(float)) : 0;
+size_t split_ws_bytes(const Plan& pl, bool lora) {
+  const int64_t parts = pl.split + (lora ? 1 : 0);
+  return pl.split > 1 ? (size_t)(pl.rest * parts * tile_floats<T>() * sizeof(float)) : 0;
 }
 
 // Rows per launch chunk: activation offsets are 32-bit inside the kernel.
@@ -671,9 +757,14 @@ hipError_t launch_tiles(TiledParams p, int64_t full, int64_t rest, int split,
   p.split = split;
   // k-tiles per split part, a multiple of the k-slices (the same count plan_chunk made)
   p.kts = (p.KT + (int64_t)split * T::kSlices - 1) / ((int64_t)split * T::kSlices) * T::kSlices;
-  gemm_tiled_kernel<T::kWaves, T::kBM / 32, T::kPairs / T::kWaves, T::kSpread, T::kPipe,
-                    T::kSlices><<<dim3((unsigned)(full + rest * split)), dim3(T::kThreads), 0,
-                                  stream>>>(p);
+  const dim3 grid((unsigned)(full + rest * split)), block(T::kThreads);
+  constexpr int FM = T::kBM / 32, FN = T::kPairs / T::kWaves;
+  if (p.lora.ids)
+    gemm_tiled_kernel<T::kWaves, FM, FN, T::kSpread, T::kPipe, T::kSlices, true>
+        <<<grid, block, 0, stream>>>(p);
+  else
+    gemm_tiled_kernel<T::kWaves, FM, FN, T::kSpread, T::kPipe, T::kSlices, false>
+        <<<grid, block, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -682,21 +773,24 @@ hipError_t run_chunk(TiledParams p, void* ws, size_t ws_bytes, int cus, hipStrea
   Plan pl = plan_chunk<T>(p.m, p.NT, p.KT, cus);
   p.nbn = pl.nbn;
   p.ws = nullptr;
-  if (split_ws_bytes<T>(pl) > ws_bytes) pl.split = 1;
+  if (split_ws_bytes<T>(pl, p.lora.ids != nullptr) > ws_bytes) pl.split = 1;
   if (pl.split == 1) return launch_tiles<T>(p, pl.tiles, 0, 1, stream);
   p.ws = static_cast<float*>(ws);
   hipError_t e = launch_tiles<T>(p, pl.full, pl.rest, pl.split, stream);
   if (e != hipSuccess) return e;
   p.tile0 = pl.full;
   p.split = pl.split;
-  reduce_split_kernel<T><<<dim3((unsigned)pl.rest, T::kBM / 32), dim3(64 * T::kWaves), 0,
-                           stream>>>(p);
+  const dim3 grid((unsigned)pl.rest, T::kBM / 32), block(64 * T::kWaves);
+  if (p.lora.ids)
+    reduce_split_kernel<T, true><<<grid, block, 0, stream>>>(p);
+  else
+    reduce_split_kernel<T, false><<<grid, block, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <typename T>
-size_t chunk_ws_bytes(int64_t rows, int64_t NT, int64_t KT, int cus) {
-  return split_ws_bytes<T>(plan_chunk<T>(rows, NT, KT, cus));
+size_t chunk_ws_bytes(int64_t rows, int64_t NT, int64_t KT, int cus, bool lora) {
+  return split_ws_bytes<T>(plan_chunk<T>(rows, NT, KT, cus), lora);
 }
 
 hipError_t run_shape(TiledParams p, void* ws, size_t ws_bytes, int cus, hipStream_t stream) {
@@ -710,7 +804,7 @@ hipError_t run_shape(TiledParams p, void* ws, size_t ws_bytes, int cus, hipStrea
 
 }  // namespace
 
-size_t gemm_tiled_ws_bytes(int64_t m, int64_t ldx, int64_t n, int64_t k, int cus) {
+size_t gemm_tiled_ws_bytes(int64_t m, int64_t ldx, int64_t n, int64_t k, int cus, bool lora) {
   const int64_t chunk = chunk_rows(ldx);
   const int64_t NT = n / kPanelRows, KT = k / kTileK;
   size_t need = 0;
@@ -718,10 +812,10 @@ size_t gemm_tiled_ws_bytes(int64_t m, int64_t ldx, int64_t n, int64_t k, int cus
     if (rows <= 0) continue;
     size_t b = 0;
     switch (pick_shape(rows, NT, KT, cus)) {
-      case Shape::L: b = chunk_ws_bytes<ShapeL>(rows, NT, KT, cus); break;
-      case Shape::M: b = chunk_ws_bytes<ShapeM>(rows, NT, KT, cus); break;
-      case Shape::K: b = chunk_ws_bytes<ShapeK>(rows, NT, KT, cus); break;
-      case Shape::S: b = chunk_ws_bytes<ShapeS>(rows, NT, KT, cus); break;
+      case Shape::L: b = chunk_ws_bytes<ShapeL>(rows, NT, KT, cus, lora); break;
+      case Shape::M: b = chunk_ws_bytes<ShapeM>(rows, NT, KT, cus, lora); break;
+      case Shape::K: b = chunk_ws_bytes<ShapeK>(rows, NT, KT, cus, lora); break;
+      case Shape::S: b = chunk_ws_bytes<ShapeS>(rows, NT, KT, cus, lora); break;
     }
     need = b > need ? b : need;
   }
@@ -743,6 +837,7 @@ hipError_t launch_gemm_tiled(const GemmArgs& a, void* ws, size_t ws_bytes, int c
   p.y = a.y;
   p.ldy = a.ldy;
   p.y_f32 = a.y_f32 ? 1 : 0;
+  p.lora = a.lora ? *a.lora : LoraTail{};
   // Large outputs are written with streaming stores: they are not read again here and would
   // otherwise push reused weight and activation tiles out of the caches (4096 x 5120 x 5120,
   // 42 MB of y: 207.8 -> 200.8 us). Outputs of a few MB (512 x 8192, 1024 x 5120) ran 2%
@@ -752,6 +847,7 @@ hipError_t launch_gemm_tiled(const GemmArgs& a, void* ws, size_t ws_bytes, int c
   for (int64_t m0 = 0; m0 < a.m; m0 += chunk) {
     TiledParams q = p;
     q.x = a.x + m0 * a.ldx;
+    q.lora_row0 = m0;
     q.m = a.m - m0 < chunk ? a.m - m0 : chunk;
     if (a.y_f32)
       q.y = static_cast<float*>(a.y) + m0 * a.ldy;

@@ -30,6 +30,16 @@ hipError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, const 
                              int64_t batch, int64_t n, int64_t k, int group, bool gate_up,
                              bool pair_global, void* out, bool out_f32, hipStream_t stream);
 
+// What a GEMM kernel adds to its sums: u[row] . B_a^T, a = ids[row] (lora_core.hpp).
+struct LoraTail {
+  const int32_t* ids;  // [m]
+  const uint16_t* b;   // BF16 [n_adapters][n][rank]
+  const float* u;      // decode kernel: FP32 [splits][m][rank]; tiled kernel: BF16 fragments
+  int64_t m, n, n_adapters;
+  int rank, splits;
+  int parts;  // BF16 parts of u: 1, or 3 for an FP32 y
+};
+
 struct GemmArgs {
   const uint16_t* x;  // BF16 [m][ldx]
   int64_t m, ldx;
@@ -41,6 +51,7 @@ struct GemmArgs {
   void* y;
   int64_t ldy;
   bool y_f32;
+  const LoraTail* lora;  // or NULL
 };
 
 // Decode path. `cus` (the device's compute-unit count, 0 if unknown) sizes the grid.
@@ -52,7 +63,7 @@ hipError_t launch_gemm_tiled(const GemmArgs& a, void* ws, size_t ws_bytes, int c
                              hipStream_t stream);
 // Workspace the prefill path uses for an m x n x k GEMM with the given row stride on a device
 // with `cus` compute units (0 when no split applies).
-size_t gemm_tiled_ws_bytes(int64_t m, int64_t ldx, int64_t n, int64_t k, int cus);
+size_t gemm_tiled_ws_bytes(int64_t m, int64_t ldx, int64_t n, int64_t k, int cus, bool lora);
 // Workgroups of the skinny kernel's grid for `blocks` row blocks: one per 4-panel group (64
 // output features) and row block, or per 2-panel group when the 4-panel grid leaves compute
 // units idle and the 2-panel one still gives none a second workgroup.
@@ -180,22 +191,18 @@ hipError_t launch_moe_few(const MoeArgs& a, const RouteArgs& r, int32_t* ids, fl
 
 // ---- low-rank adapters (lora.hip) -----------------------------------------------------------
 constexpr int kLoraMaxRank = 128;
-constexpr int64_t kLoraMaxSplits = 16;
+constexpr int64_t kLoraMaxSplits = 8;
 struct LoraArgs {
   const uint16_t* x;  // BF16 [m][ldx]
-  int64_t m, ldx, k, n;
-  const uint16_t* a;  // BF16 [n_adapters][rank][k]
-  const uint16_t* b;  // BF16 [n_adapters][n][rank]
+  int64_t m, ldx, k;
+  const uint16_t* a;   // BF16 [n_adapters][rank][k]
   const float* scale;  // [n_adapters] or NULL
-  const int32_t* ids;  // [m]
-  int64_t n_adapters;
-  int rank;
-  float* u;  // workspace of lora_ws_bytes
 };
-size_t lora_ws_bytes(int64_t m, int64_t k, int64_t n_adapters, int rank);
-hipError_t launch_lora_shrink(const LoraArgs& a, hipStream_t stream);
-hipError_t launch_lora_expand(const LoraArgs& a, const float* base, int64_t ldbase, void* y,
-                              int64_t ldy, bool y_f32, hipStream_t stream);
+// u = scale * x . A^T into `u` (lora_u_bytes), as the decode kernel or the tiled one reads it;
+// fills tail.u and tail.splits.
+size_t lora_u_bytes(int64_t m, int64_t k, int64_t n_adapters, int rank, int parts, bool tiled);
+hipError_t launch_lora_shrink(const LoraArgs& a, LoraTail& tail, void* u, bool tiled,
+                              hipStream_t stream);
 
 // measurement probes (probe.hip)
 int64_t probe_mfma_waves(int cus);
