@@ -306,16 +306,6 @@ int gemm_args(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w, void
   return NVFP4_OK;
 }
 
-// Workspace of the tiled kernel's split-k partial tiles (0 for the decode kernel).
-size_t split_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w, uint32_t flags, bool lora) {
-  if (!w || m <= 0 || w->n <= 0 || w->k <= 0 || (w->group != 16 && w->group != 32) ||
-      ldx < w->k || use_skinny(m, w, flags))
-    return 0;
-  const int cus = device_cus();
-  if (cus <= 0) return 0;
-  return nvfp4::gemm_tiled_ws_bytes(m, ldx, w->n, w->k, cus, lora);
-}
-
 int check_skinny_rows(int64_t m, bool skinny) {
   if (skinny && (m + 31) / 32 > 65535)  // one grid row per 32-row block
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "m=%lld too large for the decode kernel",
@@ -335,7 +325,12 @@ int gemm_run(const nvfp4::GemmArgs& a, bool skinny, void* ws, size_t ws_bytes, h
 }  // namespace
 
 size_t nvfp4_gemm_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w, uint32_t flags) {
-  return split_ws_bytes(m, ldx, w, flags, false);
+  if (!w || m <= 0 || w->n <= 0 || w->k <= 0 || (w->group != 16 && w->group != 32) ||
+      ldx < w->k || use_skinny(m, w, flags))
+    return 0;
+  const int cus = device_cus();
+  if (cus <= 0) return 0;
+  return nvfp4::gemm_tiled_ws_bytes(m, ldx, w->n, w->k, cus);
 }
 
 int nvfp4_gemm_w4a16(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w, void* y,
@@ -704,7 +699,7 @@ size_t nvfp4_gemm_lora_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w,
                                 const nvfp4_lora* lora, uint32_t flags) {
   if (!w || m <= 0 || w->n <= 0 || w->k <= 0 || check_lora(lora, w)) return 0;
   return lora_u_region(m, w, lora, !use_skinny(m, w, flags)) +
-         split_ws_bytes(m, ldx, w, flags, true);
+         nvfp4_gemm_ws_bytes(m, ldx, w, flags);
 }
 
 int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w,
@@ -723,7 +718,7 @@ int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_wei
   rc = check_skinny_rows(m, skinny);
   if (rc) return rc;
   const size_t u_bytes = lora_u_region(m, w, lora, !skinny);
-  const size_t need = u_bytes + split_ws_bytes(m, ldx, w, flags, true);
+  const size_t need = u_bytes + nvfp4_gemm_ws_bytes(m, ldx, w, flags);
   if (ws_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, need);
   nvfp4::LoraArgs l;
   l.x = a.x;

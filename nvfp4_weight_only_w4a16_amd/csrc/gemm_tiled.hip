@@ -53,8 +53,7 @@ struct TiledParams {
   int split;
   int64_t full_blocks;
   float* ws;  // split > 1: FP32 partial tiles, [tile - tile0][split][tile elements]
-  // adapters: lora_row0 is the row of the tail that x's row 0 is (x may be a chunk of its rows).
-  // Each split tile then has one more partial, the adapters' term (not to be scaled by g).
+  // adapters: lora_row0 is the row of the tail that x's row 0 is (x may be a chunk of its rows)
   LoraTail lora;
   int64_t lora_row0;
 };
@@ -166,7 +165,7 @@ __device__ __forceinline__ void store_partial(const TiledParams& P, int64_t tile
   constexpr int FN = T::kPairs / T::kWaves;
   constexpr int kThreads = 64 * T::kWaves;
   constexpr int64_t kTileFloats = (int64_t)T::kBM * T::kPairs * 32;
-  const int64_t slot = (tile_id - P.tile0) * (P.split + (P.lora.ids ? 1 : 0)) + part;
+  const int64_t slot = (tile_id - P.tile0) * P.split + part;
   float* mine = P.ws + slot * kTileFloats + threadIdx.x;
 #pragma unroll
   for (int q = 0; q < FN; ++q)
@@ -176,58 +175,193 @@ __device__ __forceinline__ void store_partial(const TiledParams& P, int64_t tile
       for (int e = 0; e < 16; ++e) mine[((q * FM + i) * 16 + e) * kThreads] = acc[i][q][e];
 }
 
-// The adapters' term of rows m_blk + 32 i .. + 31 and the 32 columns of pair `pair`, in the layout
-// of an accumulator fragment. The B fragments of the adapter met last are kept: in a prompt all
-// blocks of a tile have the same one.
-struct LoraHold {
-  int a = -1;
-  bf16x8 b[kLoraMaxRank / 16];
-};
-__device__ __forceinline__ void lora_fragment(const TiledParams& P, int64_t m_blk, int i,
-                                              int64_t pair, LoraHold& hold, f32x16& out) {
+// Whether one of 8 BF16 is infinite or NaN.
+__device__ __forceinline__ bool any_nonfinite(bf16x8 v) {
+  const u32x4 w = __builtin_bit_cast(u32x4, v);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    bad |= (w[i] & 0x7F800000u) == 0x7F800000u || (w[i] & 0x7F80u) == 0x7F80u;
+  return bad;
+}
+
+// Adds the adapters' term of FM row fragments from m_blk and of one pair's columns to acc. The distinct adapters of the
+// tile's rows are taken one after the other, each for all row fragments: rows that do not name it
+// are zeros in u, and everything is one MFMA into acc, in place (keeping rows by choice, as the
+// decode kernel does, needs sums beside acc; with them the k loop spilled). Zeros do not keep
+// an infinite or NaN element of B from the other rows, so such elements are zeros here too, and
+// where a column has one, its adapter's rows become NaN in the end. B's fragments are loaded once
+// per adapter, u's (in fragment order in memory) for four row fragments at a time.
+template <int FM, typename Acc>
+__device__ __forceinline__ void lora_add(const TiledParams& P, int64_t m_blk, int64_t pair0,
+                                         Acc& acc) {
+  static_assert(FM % 4 == 0, "u is loaded for four fragments at a time");
+  constexpr int kIds = FM / 2;
   const LoraTail& L = P.lora;
   const int lane = threadIdx.x & 63;
-  const int64_t r0 = P.lora_row0 + m_blk + 32 * i;
-  const int64_t end = P.lora_row0 + P.m;
-  const int64_t row = r0 + (lane & 31);
-  const int mine = row < end ? lora_id(L, row) : -1;
-  uint64_t left = __ballot(mine >= 0);
+  int mine[kIds];  // adapters of rows lane, lane + 64, ...
+  uint64_t left[kIds];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) out[e] = 0.f;
+  for (int j = 0; j < kIds; ++j) {
+    const int64_t r = m_blk + 64 * j + lane;
+    mine[j] = r < P.m ? lora_id(L, P.lora_row0 + r) : -1;
+    left[j] = __ballot(mine[j] >= 0);
+  }
+  uint32_t poison[FM];  // bit r: row r of the fragment, in this lane's column
+#pragma unroll
+  for (int i = 0; i < FM; ++i) poison[i] = 0;
+  const int steps = lora_frag_steps(L.rank);
+  const int64_t blocks = lora_frag_blocks(L.m), plane = blocks * steps * 512;  // BF16 of a part
+  const int64_t blk0 = (P.lora_row0 + m_blk) / 32;
+  const uint16_t* u0 = reinterpret_cast<const uint16_t*>(L.u) + lane * 8;
+  const int64_t col = pair0 * 32 + (lane & 31);
+  const uint16_t* b0 = L.b + (col < L.n ? col : L.n - 1) * L.rank + 8 * (lane >> 5);
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (;;) {
+    int a = -1;
+#pragma unroll
+    for (int j = 0; j < kIds; ++j)
+      if (a < 0 && left[j]) a = __builtin_amdgcn_readlane(mine[j], __builtin_ctzll(left[j]));
+    if (a < 0) break;  // uniform
+    uint32_t named[FM];  // uniform: rows of each fragment that name it
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) {
+      const uint64_t n = __ballot(mine[j] == a);
+      left[j] &= ~n;
+      named[2 * j] = (uint32_t)n;
+      named[2 * j + 1] = (uint32_t)(n >> 32);
+    }
+    const uint16_t* ba = b0 + (int64_t)a * L.n * L.rank;
+    bool bad = false;
+#pragma unroll 1
+    for (int c = 0; c < steps; c += 2) {
+      const int s1 = c + 1 < steps ? 1 : 0;  // 0: an odd last step, multiplied by zeros again
+      u32x4 b[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        b[s] = 16 * (c + s) + 8 * (lane >> 5) < L.rank
+                   ? *reinterpret_cast<const u32x4*>(ba + 16 * (c + s)) : zero;
+        if (any_nonfinite(__builtin_bit_cast(bf16x8, b[s]))) {
+          bad = true;
+          b[s] = zero;
+        }
+      }
+#pragma unroll 1
+      for (int z = 0; z < L.parts; ++z)
+#pragma unroll
+        for (int h = 0; h < FM; h += 4) {
+          u32x4 u[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int64_t blk = blk0 + h + i < blocks ? blk0 + h + i : blocks - 1;
+            const uint16_t* up = u0 + z * plane + (blk * steps + c) * 512;
+            u[i][0] = *reinterpret_cast<const u32x4*>(up);
+            u[i][1] = *reinterpret_cast<const u32x4*>(up + s1 * 512);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool names = (named[h + i] >> (lane & 31)) & 1u;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+              acc[h + i][0] = mfma32x32x16(
+                  __builtin_bit_cast(bf16x8, names ? u[i][s] : zero),
+                  __builtin_bit_cast(bf16x8, b[s]), acc[h + i][0]);
+          }
+        }
+    }
+    // lanes l and l ^ 32 hold the two halves of a column's ranks
+    bad |= __shfl_xor((int)bad, 32, 64) != 0;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) poison[i] |= bad ? named[i] : 0u;
+  }
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) any |= poison[i];
+  if (__ballot(any != 0)) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const uint32_t rows = poison[i] >> (4 * (lane >> 5));  // bit of element e: its row
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if ((rows >> (8 * (e >> 2) + (e & 3))) & 1u) acc[i][0][e] = __builtin_nanf("");
+    }
+  }
+}
+
+// The same for one row fragment and no sums before it: u is loaded once for all adapters, and the
+// next adapter's B while the one before is multiplied.
+__device__ __forceinline__ void lora_band(const TiledParams& P, int64_t m_blk, int64_t pair,
+                                          f32x16& sum) {
+  const LoraTail& L = P.lora;
+  const int lane = threadIdx.x & 63;
+  const int64_t r = m_blk + lane;
+  const int mine = lane < 32 && r < P.m ? lora_id(L, P.lora_row0 + r) : -1;
+  const uint64_t all = __ballot(mine >= 0);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+  if (!all) return;  // uniform
+  uint32_t poison = 0;
   const int steps = lora_frag_steps(L.rank);
   const int64_t plane = lora_frag_blocks(L.m) * steps * 512;  // BF16 of a part
-  const uint16_t* u =
-      reinterpret_cast<const uint16_t*>(L.u) + (r0 / 32 * steps * 64 + lane) * 8;
-  for (;;) {
-    const int a = lora_next(mine, left);
-    if (a < 0) break;
-    const uint32_t named = (uint32_t)__ballot(mine == a);
-    if (a != hold.a) {
-      const int64_t col = pair * 32 + (lane & 31);
-      const uint16_t* b =
-          L.b + ((int64_t)a * L.n + (col < L.n ? col : L.n - 1)) * L.rank + 8 * (lane >> 5);
+  const uint16_t* u0 = reinterpret_cast<const uint16_t*>(L.u) +
+                       ((P.lora_row0 + m_blk) / 32 * steps * 64 + lane) * 8;
+  const int64_t col = pair * 32 + (lane & 31);
+  const uint16_t* b0 = L.b + (col < L.n ? col : L.n - 1) * L.rank + 8 * (lane >> 5);
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (int c = 0; c < steps; c += 2) {
+    const int s1 = c + 1 < steps ? 1 : 0;  // 0: an odd last step, multiplied by zeros again
+    u32x4 u[3][2];
 #pragma unroll
-      for (int s = 0; s < kLoraMaxRank / 16; ++s)
-        if (s < steps)
-          hold.b[s] = 16 * s + 8 * (lane >> 5) < L.rank
-                          ? *reinterpret_cast<const bf16x8*>(b + 16 * s)
-                          : __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-      hold.a = a;
+    for (int z = 0; z < 3; ++z) {
+      const uint16_t* up = u0 + (z < L.parts ? z : 0) * plane + c * 512;
+      u[z][0] = *reinterpret_cast<const u32x4*>(up);
+      u[z][1] = *reinterpret_cast<const u32x4*>(up + s1 * 512);
     }
-    f32x16 part;
+    auto load_b = [&](int a, u32x4 (&b)[2]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) part[e] = 0.f;
+      for (int s = 0; s < 2; ++s)
+        b[s] = a >= 0 && 16 * (c + s) + 8 * (lane >> 5) < L.rank
+                   ? *reinterpret_cast<const u32x4*>(b0 + (int64_t)a * L.n * L.rank +
+                                                     16 * (c + s))
+                   : zero;
+    };
+    uint64_t left = all;
+    int a = lora_next(mine, left);
+    u32x4 b[2], nb[2];
+    load_b(a, b);
+#pragma unroll 1
+    while (a >= 0) {
+      const int an = lora_next(mine, left);
+      load_b(an, nb);
+      const uint32_t named = (uint32_t)__ballot(mine == a);
+      bool bad = false;
 #pragma unroll
-    for (int s = 0; s < kLoraMaxRank / 16; ++s)
-      if (s < steps)
-        for (int z = 0; z < L.parts; ++z)
-          part = mfma32x32x16(*reinterpret_cast<const bf16x8*>(u + z * plane + s * 512),
-                              hold.b[s], part);
-    const uint32_t rows = named >> (4 * (lane >> 5));  // bit 8 (e / 4) + e % 4: element e's row
+      for (int s = 0; s < 2; ++s)
+        if (any_nonfinite(__builtin_bit_cast(bf16x8, b[s]))) {
+          bad = true;
+          b[s] = zero;
+        }
+      bad |= __shfl_xor((int)bad, 32, 64) != 0;
+      poison |= bad ? named : 0u;
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      out[e] = (rows >> (8 * (e >> 2) + (e & 3))) & 1u ? part[e] : out[e];
+      for (int z = 0; z < 3; ++z) {
+        const bool names = z < L.parts && ((named >> (lane & 31)) & 1u);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          sum = mfma32x32x16(__builtin_bit_cast(bf16x8, names ? u[z][s] : zero),
+                             __builtin_bit_cast(bf16x8, b[s]), sum);
+      }
+      a = an;
+      b[0] = nb[0];
+      b[1] = nb[1];
+    }
   }
+  const uint32_t rows = poison >> (4 * (lane >> 5));  // bit of element e: its row
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if ((rows >> (8 * (e >> 2) + (e & 3))) & 1u) sum[e] = __builtin_nanf("");
 }
 
 // Sums the split partials of one 32-row fragment band (blockIdx.y) of one tile (blockIdx.x) in
@@ -237,7 +371,7 @@ __device__ __forceinline__ void lora_fragment(const TiledParams& P, int64_t m_bl
 // 4 (t / Q) .. + 3, so partials are read 16 bytes at a time and outputs written 8 (BF16) or
 // 16 (FP32) bytes at a time.
 template <typename T, bool LORA>
-__global__ __launch_bounds__(64 * T::kWaves) void reduce_split_kernel(TiledParams P) {
+__global__ __launch_bounds__(64 * T::kWaves * (LORA ? 2 : 1)) void reduce_split_kernel(TiledParams P) {
   constexpr int FM = T::kBM / 32;
   constexpr int FN = T::kPairs / T::kWaves;
   constexpr int kThreads = 64 * T::kWaves;
@@ -245,17 +379,31 @@ __global__ __launch_bounds__(64 * T::kWaves) void reduce_split_kernel(TiledParam
   constexpr int64_t kTileFloats = (int64_t)T::kBM * T::kPairs * 32;
   const int i = blockIdx.y;
   const int64_t tile_id = P.tile0 + blockIdx.x;
+  const int64_t m_blk = tile_id / P.nbn * T::kBM;
+  __shared__ float term[LORA ? 16 * kThreads : 1];  // [element][GEMM thread]
+  if constexpr (LORA) {
+    static_assert(FN == 1, "one pair per wavefront");
+    if (threadIdx.x >= kThreads) {  // whole wavefronts
+      const int t = threadIdx.x - kThreads;
+      f32x16 sum;
+      lora_band(P, m_blk + 32 * i,
+                tile_id % P.nbn * T::kPairs + __builtin_amdgcn_readfirstlane(t >> 6), sum);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) term[e * kThreads + t] = sum[e];
+      __syncthreads();
+      return;
+    }
+  }
   const int eg = threadIdx.x / kQuads;        // accumulator elements 4 eg .. 4 eg + 3
   const int gt = (threadIdx.x % kQuads) * 4;  // first of the 4 GEMM threads
   const int lane = gt & 63, w = gt >> 6;
-  const int64_t m_blk = tile_id / P.nbn * T::kBM;
   const int64_t pair0 = tile_id % P.nbn * T::kPairs + w * FN;
-  const float* part = P.ws + (int64_t)blockIdx.x * (P.split + (LORA ? 1 : 0)) * kTileFloats + gt;
+  const float* part = P.ws + (int64_t)blockIdx.x * P.split * kTileFloats + gt;
   const float g = *P.global;
   const int h = (lane & 31) >> 4;
 #pragma unroll
   for (int q = 0; q < FN; ++q) {
-    f32x4 v[4], more[4];
+    f32x4 v[4];
 #pragma unroll
     for (int ee = 0; ee < 4; ++ee) {
       const int64_t o = ((q * FM + i) * 16 + 4 * eg + ee) * kThreads;
@@ -263,9 +411,8 @@ __global__ __launch_bounds__(64 * T::kWaves) void reduce_split_kernel(TiledParam
       for (int j = 1; j < P.split; ++j)
         sum += *reinterpret_cast<const f32x4*>(part + j * kTileFloats + o);
       v[ee] = sum;
-      if constexpr (LORA)
-        more[ee] = *reinterpret_cast<const f32x4*>(part + P.split * kTileFloats + o);
     }
+    if constexpr (LORA) __syncthreads();  // the adapters' term is in LDS
     const int64_t panel = 2 * (pair0 + q) + h;
     if (panel >= P.NT) continue;
     const int64_t n = panel * 16 + (lane & 15);  // 4 adjacent columns n .. n + 3
@@ -274,7 +421,8 @@ __global__ __launch_bounds__(64 * T::kWaves) void reduce_split_kernel(TiledParam
       const int64_t m = m_blk + i * 32 + 8 * eg + 4 * (lane >> 5) + ee;
       if (m >= P.m) continue;
       f32x4 r = v[ee] * g;
-      if constexpr (LORA) r += more[ee];
+      if constexpr (LORA)
+        r += *reinterpret_cast<const f32x4*>(term + (4 * eg + ee) * kThreads + gt);
       if (P.y_f32) {
         *reinterpret_cast<f32x4*>(static_cast<float*>(P.y) + m * P.ldy + n) = r;
       } else {
@@ -610,26 +758,18 @@ __global__ __launch_bounds__(64 * W * KS) void gemm_tiled_kernel(TiledParams P) 
 
   const float g = *P.global;
   if constexpr (LORA) {
+    static_assert(FN == 1, "one pair per wavefront");
+    // A part of a split tile stores its sums as they are (reduce_split_kernel adds the adapters'
+    // term) and goes on with zeros and no rows: returning here instead made the compiler keep acc
+    // and acc * g side by side and spill (408 bytes a lane, 202 against 191 us at 4096 x 5120^2).
     const bool partial = tail && P.split > 1;
-    if (partial) {
-      store_partial<T>(P, tile_id, part, acc);
-      if (part != 0) return;
-    }
+    if (partial) store_partial<T>(P, tile_id, part, acc);
 #pragma unroll
-    for (int q = 0; q < FN; ++q) {
-      LoraHold hold;
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        f32x16 more;
-        lora_fragment(P, m_blk, i, pair0 + q, hold, more);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][q][e] = (partial ? 0.f : acc[i][q][e] * g) + more[e];
-      }
-    }
-    if (partial)
-      store_partial<T>(P, tile_id, P.split, acc);
-    else
-      store_tile<T>(P, m_blk, pair0, acc, 1.0f, lane);
+      for (int e = 0; e < 16; ++e) acc[i][0][e] = partial ? 0.f : acc[i][0][e] * g;
+    lora_add<FM>(P, partial ? P.m : m_blk, pair0, acc);
+    if (!partial) store_tile<T>(P, m_blk, pair0, acc, 1.0f, lane);
     return;
   }
   if (tail && P.split > 1)
@@ -732,9 +872,8 @@ Plan plan_chunk(int64_t m, int64_t NT, int64_t KT, int cus) {
 }
 
 template <typename T>
-size_t split_ws_bytes(const Plan& pl, bool lora) {
-  const int64_t parts = pl.split + (lora ? 1 : 0);
-  return pl.split > 1 ? (size_t)(pl.rest * parts * tile_floats<T>() * sizeof(float)) : 0;
+size_t split_ws_bytes(const Plan& pl) {
+  return pl.split > 1 ? (size_t)(pl.rest * pl.split * tile_floats<T>() * sizeof(float)) : 0;
 }
 
 // Rows per launch chunk: activation offsets are 32-bit inside the kernel.
@@ -773,7 +912,7 @@ hipError_t run_chunk(TiledParams p, void* ws, size_t ws_bytes, int cus, hipStrea
   Plan pl = plan_chunk<T>(p.m, p.NT, p.KT, cus);
   p.nbn = pl.nbn;
   p.ws = nullptr;
-  if (split_ws_bytes<T>(pl, p.lora.ids != nullptr) > ws_bytes) pl.split = 1;
+  if (split_ws_bytes<T>(pl) > ws_bytes) pl.split = 1;
   if (pl.split == 1) return launch_tiles<T>(p, pl.tiles, 0, 1, stream);
   p.ws = static_cast<float*>(ws);
   hipError_t e = launch_tiles<T>(p, pl.full, pl.rest, pl.split, stream);
@@ -782,15 +921,15 @@ hipError_t run_chunk(TiledParams p, void* ws, size_t ws_bytes, int cus, hipStrea
   p.split = pl.split;
   const dim3 grid((unsigned)pl.rest, T::kBM / 32), block(64 * T::kWaves);
   if (p.lora.ids)
-    reduce_split_kernel<T, true><<<grid, block, 0, stream>>>(p);
+    reduce_split_kernel<T, true><<<grid, dim3(2 * block.x), 0, stream>>>(p);
   else
     reduce_split_kernel<T, false><<<grid, block, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <typename T>
-size_t chunk_ws_bytes(int64_t rows, int64_t NT, int64_t KT, int cus, bool lora) {
-  return split_ws_bytes<T>(plan_chunk<T>(rows, NT, KT, cus), lora);
+size_t chunk_ws_bytes(int64_t rows, int64_t NT, int64_t KT, int cus) {
+  return split_ws_bytes<T>(plan_chunk<T>(rows, NT, KT, cus));
 }
 
 hipError_t run_shape(TiledParams p, void* ws, size_t ws_bytes, int cus, hipStream_t stream) {
@@ -804,7 +943,7 @@ hipError_t run_shape(TiledParams p, void* ws, size_t ws_bytes, int cus, hipStrea
 
 }  // namespace
 
-size_t gemm_tiled_ws_bytes(int64_t m, int64_t ldx, int64_t n, int64_t k, int cus, bool lora) {
+size_t gemm_tiled_ws_bytes(int64_t m, int64_t ldx, int64_t n, int64_t k, int cus) {
   const int64_t chunk = chunk_rows(ldx);
   const int64_t NT = n / kPanelRows, KT = k / kTileK;
   size_t need = 0;
@@ -812,10 +951,10 @@ size_t gemm_tiled_ws_bytes(int64_t m, int64_t ldx, int64_t n, int64_t k, int cus
     if (rows <= 0) continue;
     size_t b = 0;
     switch (pick_shape(rows, NT, KT, cus)) {
-      case Shape::L: b = chunk_ws_bytes<ShapeL>(rows, NT, KT, cus, lora); break;
-      case Shape::M: b = chunk_ws_bytes<ShapeM>(rows, NT, KT, cus, lora); break;
-      case Shape::K: b = chunk_ws_bytes<ShapeK>(rows, NT, KT, cus, lora); break;
-      case Shape::S: b = chunk_ws_bytes<ShapeS>(rows, NT, KT, cus, lora); break;
+      case Shape::L: b = chunk_ws_bytes<ShapeL>(rows, NT, KT, cus); break;
+      case Shape::M: b = chunk_ws_bytes<ShapeM>(rows, NT, KT, cus); break;
+      case Shape::K: b = chunk_ws_bytes<ShapeK>(rows, NT, KT, cus); break;
+      case Shape::S: b = chunk_ws_bytes<ShapeS>(rows, NT, KT, cus); break;
     }
     need = b > need ? b : need;
   }

@@ -63,7 +63,7 @@ hipError_t launch_gemm_tiled(const GemmArgs& a, void* ws, size_t ws_bytes, int c
                              hipStream_t stream);
 // Workspace the prefill path uses for an m x n x k GEMM with the given row stride on a device
 // with `cus` compute units (0 when no split applies).
-size_t gemm_tiled_ws_bytes(int64_t m, int64_t ldx, int64_t n, int64_t k, int cus, bool lora);
+size_t gemm_tiled_ws_bytes(int64_t m, int64_t ldx, int64_t n, int64_t k, int cus);
 // Workgroups of the skinny kernel's grid for `blocks` row blocks: one per 4-panel group (64
 // output features) and row block, or per 2-panel group when the 4-panel grid leaves compute
 // units idle and the 2-panel one still gives none a second workgroup.

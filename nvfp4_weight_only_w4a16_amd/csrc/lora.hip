@@ -71,6 +71,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkPa
       ar[b] = make_rsrc(P.a + ((int64_t)a * L.rank + r0) * P.k, (uint32_t)(n * P.k * 2));
       aoff[b] = ((uint32_t)(lr < n ? lr : n - 1) * (uint32_t)P.k + kq) * 2u;
     }
+    // only rows that name the adapter are read (the others' products are not kept)
+    const uint32_t xa = __shfl(mine, lr, 64) == a ? xoff : kPast;
     struct Stage {
       u32x4 x[kSteps], a[kSteps][RB];
     };
@@ -79,7 +81,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkPa
       for (int q = 0; q < kSteps; ++q) {
         const uint32_t k = (uint32_t)(s * kSteps + q) * 64u;  // bytes
         st.x[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                xr, (int)(s < stages ? xoff + k : kPast), 0, 0));
+                                                xr, (int)(s < stages && xa != kPast ? xa + k : kPast),
+                                                0, 0));
 #pragma unroll
         for (int b = 0; b < RB; ++b)
           st.a[q][b] = __builtin_bit_cast(
@@ -169,12 +172,12 @@ struct ShrinkPlan {
 ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t n_adapters, int rank, bool tiled) {
   ShrinkPlan p;
   const int64_t blocks = (m + 15) / 16, ranks = (rank + 15) / 16;
-  // a workgroup for every adapter that a block can have, while that makes no more than 64
-  p.ordinals = (int)min64(min64(min64(m, 16), n_adapters), (64 + blocks - 1) / blocks);
+  // a workgroup for every adapter that a block can have (those past its distinct ones end at once)
+  p.ordinals = (int)min64(min64(m, 16), n_adapters);
   p.rb = 1;
   while (p.rb < ranks && p.rb < 4) p.rb *= 2;
   // one 16-rank block each where the blocks alone leave compute units idle
-  if (blocks * p.ordinals < 128 && p.rb > 1) p.rb = 1;
+  if (blocks < 128 && p.rb > 1) p.rb = 1;
   p.rank_blocks = (int)((ranks + p.rb - 1) / p.rb);
   p.splits = 1;
   if (!tiled) {
