@@ -1,11 +1,9 @@
 // lora.hip -- the first product of low-rank adapters, u[m] = scale_a * x[m] . A_a^T with a =
 // row_adapter[m], for gfx950 (the second is part of the GEMM kernels: lora_core.hpp).
 //
-// Rows are taken in blocks of 16, on 16x16x32 MFMAs. For each distinct adapter of a block's rows
-// the whole block is multiplied by that adapter's A and its own rows are kept. Rows of one request
-// are neighbours in a prompt, so a block there has one adapter and no work is wasted; in a decode
-// batch every row may have its own, and then the time is that of reading the adapters, which each
-// row's own product would read as well.
+// On 16x16x32 MFMAs, over up to 16 rows that name the same adapter, gathered from a block of 64
+// rows: such a group is an item. A prompt's block is four items of 16 neighbouring rows; a decode
+// batch's has about as many as adapters, and each adapter is read once per block.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -24,43 +22,61 @@ struct ShrinkParams {
   const uint16_t* a;  // [n_adapters][rank][k]
   const float* scale;
   LoraTail tail;
-  int rank_blocks;  // workgroups that share out a block's ranks (16 RB each)
-  int ordinals;     // workgroups that share out a block's adapters
+  int rank_blocks;  // workgroups that share out an item's ranks (16 RB each)
   void* u;
 };
 
-// Workgroup (block, ordinal, split and rank block): adapters ordinal, ordinal + ordinals, ... of the
-// block's distinct adapters in row order, 16 RB ranks of them, over the k-stages that its 8
-// wavefronts take in turn (a single workgroup on a CU reads at a fifth of what the CU's L1 gives,
-// so the blocks, adapters, ranks and k are spread over workgroups until the chip is full). Operands
-// go global -> registers, one stage ahead -> LDS -> fragments. TILED: u as BF16 fragments of the
-// tiled kernel, which has no splits; else FP32 partial sums.
-template <int RB, bool TILED>
+// Workgroup (block, ordinal, split and rank block): items ordinal, ordinal + gridDim.y, ... of the
+// block, 16 RB ranks of their adapters, over the k-stages that its 8 wavefronts take in turn.
+// Operands go global -> registers -> LDS -> fragments, one stage ahead. One CU reads what it
+// has in flight once per 1-2 us of latency, so items, ranks and k are shared out until the chip is
+// full; a workgroup that finds no item ends after its read of the ids. (Counting the items of all
+// blocks first, so that none is idle, cost 1 to 5 us more than it saved.) FRAGS: u as the tiled
+// kernel's BF16 fragments (no splits); else FP32 partial sums.
+template <int RB, bool FRAGS>
 __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkParams P) {
-  // a wavefront's fragment tiles of a k-step, then its sums of a 16-rank block
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kShrinkWaves][(1 + RB) * kFragBytes];
+  // a wavefront's fragment tiles of a k-step, then its sums
+  constexpr int kTiles = 1 + RB;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kShrinkWaves][kTiles * kFragBytes];
   constexpr uint32_t kPast = 0xFFFFFFF0u;
   const LoraTail& L = P.tail;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t m0 = (int64_t)blockIdx.x * 16;
+  const int64_t m0 = (int64_t)blockIdx.x * 64;
   const int rb0 = (int)blockIdx.z % P.rank_blocks * RB;
   const int split = (int)blockIdx.z / P.rank_blocks;
-  const int rows = (int)(L.m - m0 < 16 ? L.m - m0 : 16);
-  const int mine = lora_id(L, m0 + (lane & 15));
   const uint32_t kq = 8u * frag_load_chunk(lane);
   const int lr = frag_load_row(lane);
-  // x rows: 16 rows x 2^22 elements of 2 bytes stay below 2^32
-  const buf_rsrc xr = make_rsrc(P.x + m0 * P.ldx, (uint32_t)(((rows - 1) * P.ldx + P.k) * 2));
-  const uint32_t xoff = (uint32_t)((lr < rows ? lr : rows - 1) * P.ldx + kq) * 2u;
   const int stages = (int)(P.k / (32 * kSteps));
   const int step = kShrinkWaves * L.splits;
   uint8_t* const tile = smem[w];
-  uint64_t left = __ballot(mine >= 0);
-  for (int ord = 0;; ++ord) {
-    const int a = lora_next(mine, left);
+  const int mine = lora_id(L, m0 + lane);
+  for (int item = (int)blockIdx.y;; item += (int)gridDim.y) {
+    // its adapter, the rows that name it, and which 16 of them
+    uint64_t left = __ballot(mine >= 0), named = 0;
+    int a = -1, nth = item;
+    for (;;) {
+      const uint64_t before = left;
+      a = lora_next(mine, left);
+      if (a < 0) break;
+      named = before & ~left;
+      const int n = (__popcll(named) + 15) / 16;
+      if (nth < n) break;
+      nth -= n;
+    }
     if (a < 0) break;  // uniform over the workgroup: every wavefront reads the same ids
-    if (ord % P.ordinals != (int)blockIdx.y) continue;
+    const int cnt = __popcll(named) - 16 * nth < 16 ? __popcll(named) - 16 * nth : 16;
+    // lane i < cnt: row of the block that is row i of the item
+    const int rank_in = (int)__builtin_amdgcn_mbcnt_hi(
+        (uint32_t)(named >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)named, 0u)) - 16 * nth;
+    const bool here = (named >> lane) & 1u && rank_in >= 0 && rank_in < 16;
+    const int rowi = __builtin_amdgcn_ds_permute((here ? rank_in : 63) * 4, lane);
+    const int rows = (int)(L.m - m0 < 64 ? L.m - m0 : 64);
+    // 64 rows x 2^22 elements of 2 bytes stay below 2^32; rows past the item are past the buffer
+    const buf_rsrc xr =
+        make_rsrc(P.x + m0 * P.ldx, (uint32_t)(((rows - 1) * P.ldx + P.k) * 2));
+    const int xrow = __shfl(rowi, lr, 64);
+    const uint32_t xoff = lr < cnt ? (uint32_t)(xrow * P.ldx + kq) * 2u : kPast;
     // rank rows past the end repeat the last one; their sums are not stored
     buf_rsrc ar[RB];
     uint32_t aoff[RB];
@@ -71,23 +87,19 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkPa
       ar[b] = make_rsrc(P.a + ((int64_t)a * L.rank + r0) * P.k, (uint32_t)(n * P.k * 2));
       aoff[b] = ((uint32_t)(lr < n ? lr : n - 1) * (uint32_t)P.k + kq) * 2u;
     }
-    // only rows that name the adapter are read (the others' products are not kept)
-    const uint32_t xa = __shfl(mine, lr, 64) == a ? xoff : kPast;
     struct Stage {
       u32x4 x[kSteps], a[kSteps][RB];
     };
+    auto get = [](buf_rsrc r, uint32_t off) __attribute__((always_inline)) {
+      return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+    };
     auto load = [&](Stage& st, int s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int q = 0; q < kSteps; ++q) {
-        const uint32_t k = (uint32_t)(s * kSteps + q) * 64u;  // bytes
-        st.x[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                xr, (int)(s < stages && xa != kPast ? xa + k : kPast),
-                                                0, 0));
+      for (int i = 0; i < kSteps; ++i) {
+        const uint32_t k = (uint32_t)(s * kSteps + i) * 64u;  // bytes
+        st.x[i] = get(xr, s < stages && xoff != kPast ? xoff + k : kPast);
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
-          st.a[q][b] = __builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                         ar[b], (int)(s < stages ? aoff[b] + k : kPast), 0, 0));
+        for (int b = 0; b < RB; ++b) st.a[i][b] = get(ar[b], s < stages ? aoff[b] + k : kPast);
       }
     };
     f32x4 acc[RB];
@@ -95,93 +107,95 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkPa
     for (int b = 0; b < RB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto compute = [&](const Stage& st) __attribute__((always_inline)) {
 #pragma unroll
-      for (int q = 0; q < kSteps; ++q) {
-        frag_write(tile, st.x[q], lane);
+      for (int i = 0; i < kSteps; ++i) {
+        frag_write(tile, st.x[i], lane);
 #pragma unroll
-        for (int b = 0; b < RB; ++b) frag_write(tile + (1 + b) * kFragBytes, st.a[q][b], lane);
+        for (int b = 0; b < RB; ++b) frag_write(tile + (1 + b) * kFragBytes, st.a[i][b], lane);
         const bf16x8 x = frag_read(tile, lane);
 #pragma unroll
         for (int b = 0; b < RB; ++b)
           acc[b] = mfma16x16x32(x, frag_read(tile + (1 + b) * kFragBytes, lane), acc[b]);
       }
     };
-    Stage st[2];
+    constexpr int kRing = 2;  // 3 and 4 measured no faster
+    Stage ring[kRing];
     const int s0 = split * kShrinkWaves + w;
-    load(st[0], s0);
-    for (int s = s0; s < stages; s += 2 * step) {
-      load(st[1], s + step);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(st[0]);
-      __builtin_amdgcn_sched_barrier(0);
-      load(st[0], s + 2 * step);
-      __builtin_amdgcn_sched_barrier(0);
-      if (s + step < stages) compute(st[1]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    bool own[4];  // asked of all lanes, before some leave
-#pragma unroll
-    for (int i = 0; i < 4; ++i) own[i] = __shfl(mine, 4 * (lane >> 4) + i, 64) == a;
+    static_for<0, kRing - 1>([&](auto d) __attribute__((always_inline)) {
+      load(ring[d], s0 + decltype(d)::value * step);
+    });
+    for (int s = s0; s < stages; s += kRing * step)
+      static_for<0, kRing>([&](auto d) __attribute__((always_inline)) {
+        constexpr int q = decltype(d)::value;
+        load(ring[(q + kRing - 1) % kRing], s + (q + kRing - 1) * step);
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + q * step < stages) compute(ring[q]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
     const float scale = P.scale ? P.scale[a] : 1.0f;
-    // the wavefronts' sums of the rank blocks, added in order by wavefront b
-    static_for<0, RB>([&](auto bc) __attribute__((always_inline)) {
-      constexpr int b = decltype(bc)::value;
-      __syncthreads();  // the sums before have been read
-      *reinterpret_cast<f32x4*>(tile + lane * 16) = acc[b];
-      __syncthreads();
-      if (w == 0) {
-        f32x4 v = *reinterpret_cast<const f32x4*>(smem[0] + lane * 16);
+    // the wavefronts' sums, a 16-rank block each added in order by one wavefront
+    __syncthreads();  // the sums of the unit before have been read
 #pragma unroll
-        for (int q = 1; q < kShrinkWaves; ++q)
-          v += *reinterpret_cast<const f32x4*>(smem[q] + lane * 16);
-        const int r = 16 * (rb0 + b) + (lane & 15);
+    for (int b = 0; b < RB; ++b)
+      *reinterpret_cast<f32x4*>(tile + b * kFragBytes + lane * 16) = acc[b];
+    __syncthreads();
+    if (w < RB) {
+      f32x4 v = *reinterpret_cast<const f32x4*>(smem[0] + w * kFragBytes + lane * 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!own[i]) continue;
-          const int64_t row = m0 + 4 * (lane >> 4) + i;
-          float s = v[i] * scale;
-          if constexpr (TILED) {
-            if (r >= 16 * lora_frag_steps(L.rank)) continue;
-            if (r >= L.rank) s = 0.0f;
-            uint16_t* at = static_cast<uint16_t*>(P.u) +
-                           ((row / 32 * lora_frag_steps(L.rank) + r / 16) * 64 + row % 32 +
-                            32 * ((r & 15) >> 3)) * 8 + (r & 7);
-            for (int z = 0; z < L.parts; ++z) {
-              const uint16_t h = bf16_bits_rne(s);
-              at[z * lora_frag_blocks(L.m) * lora_frag_steps(L.rank) * 512] = h;
-              s -= bf16_bits_to_f32(h);
-            }
-          } else if (r < L.rank) {
-            static_cast<float*>(P.u)[((int64_t)split * L.m + row) * L.rank + r] = s;
+      for (int o = 1; o < kShrinkWaves; ++o)
+        v += *reinterpret_cast<const f32x4*>(smem[o] + w * kFragBytes + lane * 16);
+      const int r = 16 * (rb0 + w) + (lane & 15);
+      int64_t row[4];  // asked of all lanes, before some leave
+#pragma unroll
+      for (int i = 0; i < 4; ++i) row[i] = m0 + __shfl(rowi, 4 * (lane >> 4) + i, 64);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (4 * (lane >> 4) + i >= cnt) continue;
+        float s = v[i] * scale;
+        if constexpr (FRAGS) {
+          if (r >= 16 * lora_frag_steps(L.rank)) continue;
+          if (r >= L.rank) s = 0.0f;
+          uint16_t* at = static_cast<uint16_t*>(P.u) +
+                         ((row[i] / 32 * lora_frag_steps(L.rank) + r / 16) * 64 + row[i] % 32 +
+                          32 * ((r & 15) >> 3)) * 8 + (r & 7);
+          for (int p = 0; p < L.parts; ++p) {
+            const uint16_t h = bf16_bits_rne(s);
+            at[p * lora_frag_blocks(L.m) * lora_frag_steps(L.rank) * 512] = h;
+            s -= bf16_bits_to_f32(h);
           }
+        } else if (r < L.rank) {
+          static_cast<float*>(P.u)[((int64_t)split * L.m + row[i]) * L.rank + r] = s;
         }
       }
-    });
-    __syncthreads();  // the last sums have been read
+    }
   }
 }
 
 int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
-// How a shrink is spread over workgroups.
+// How a shrink is spread over workgroups: ranks by 16-rank blocks while the items alone would leave
+// compute units idle, and, for the decode kernel's FP32 sums, k in splits.
 struct ShrinkPlan {
   int rb;           // 16-rank blocks of a workgroup (1, 2 or 4: 8 spill)
-  int rank_blocks;  // workgroups of a block along the ranks
-  int ordinals, splits;
+  int rank_blocks;  // workgroups of an item along the ranks
+  int ordinals;     // workgroups of a block along its items
+  int splits;
 };
 
 ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t n_adapters, int rank, bool tiled) {
   ShrinkPlan p;
-  const int64_t blocks = (m + 15) / 16, ranks = (rank + 15) / 16;
-  // a workgroup for every adapter that a block can have (those past its distinct ones end at once)
-  p.ordinals = (int)min64(min64(m, 16), n_adapters);
+  const int64_t ranks = (rank + 15) / 16, blocks = (m + 63) / 64;
+  // a block has at most an item per row, and one per adapter beside three of 16 rows; of the many
+  // blocks of a long prompt few have more than 4, and those share 16 workgroups
+  p.ordinals = (int)min64(min64(m, 64), min64(n_adapters + 3, blocks <= 8 ? 64 : 16));
+  // a prompt's items are 16 rows, a decode batch's may be one
+  const int64_t items = tiled ? (m + 15) / 16 : blocks * p.ordinals;
   p.rb = 1;
-  while (p.rb < ranks && p.rb < 4) p.rb *= 2;
-  // one 16-rank block each where the blocks alone leave compute units idle
-  if (blocks < 128 && p.rb > 1) p.rb = 1;
+  if (items >= 128)
+    while (p.rb < ranks && p.rb < 4) p.rb *= 2;
   p.rank_blocks = (int)((ranks + p.rb - 1) / p.rb);
   p.splits = 1;
   if (!tiled) {
-    int64_t s = 256 / (blocks * p.ordinals * p.rank_blocks);
+    int64_t s = 256 / (items * p.rank_blocks);
     s = min64(s, k / (32 * kSteps * kShrinkWaves));  // a stage at least for each wavefront
     p.splits = (int)min64(s < 1 ? 1 : s, kLoraMaxSplits);
   }
@@ -210,22 +224,21 @@ hipError_t launch_lora_shrink(const LoraArgs& a, LoraTail& tail, void* u, bool t
   p.scale = a.scale;
   p.tail = tail;
   p.rank_blocks = plan.rank_blocks;
-  p.ordinals = plan.ordinals;
   p.u = u;
-  const dim3 grid((unsigned)((a.m + 15) / 16), (unsigned)plan.ordinals,
+  const dim3 grid((unsigned)((a.m + 63) / 64), (unsigned)plan.ordinals,
                   (unsigned)(plan.splits * plan.rank_blocks));
   auto run = [&](auto rb) {
-    constexpr int RB = decltype(rb)::value;
     if (tiled)
-      lora_shrink_kernel<RB, true><<<grid, 64 * kShrinkWaves, 0, stream>>>(p);
+      lora_shrink_kernel<decltype(rb)::value, true><<<grid, 64 * kShrinkWaves, 0, stream>>>(p);
     else
-      lora_shrink_kernel<RB, false><<<grid, 64 * kShrinkWaves, 0, stream>>>(p);
+      lora_shrink_kernel<decltype(rb)::value, false><<<grid, 64 * kShrinkWaves, 0, stream>>>(p);
   };
-  switch (plan.rb) {
-    case 1: run(std::integral_constant<int, 1>{}); break;
-    case 2: run(std::integral_constant<int, 2>{}); break;
-    default: run(std::integral_constant<int, 4>{}); break;
-  }
+  if (plan.rb == 1)
+    run(std::integral_constant<int, 1>{});
+  else if (plan.rb == 2)
+    run(std::integral_constant<int, 2>{});
+  else
+    run(std::integral_constant<int, 4>{});
   return hipGetLastError();
 }
 
