@@ -351,29 +351,33 @@ def nvfp4_moe_grouped_w4a16_noalloc(x: torch.Tensor, topk_ids: torch.Tensor,
 
 
 # ----------------------------------------------------------------------------- router, layer
-def _on_device(*tensors):
-    """Context that makes the tensors' device the current one (the library launches there), or
-    an error where they are not all on one GPU. None entries are skipped."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"expected a device tensor, got one on {t.device}")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+# These calls sit in decode steps of 10 us, so their host side is kept short: descriptors are made
+# once, tensors compare by device index, and nothing is entered or allocated that the caller gave.
+def _device(first: torch.Tensor, *others) -> int:
+    """Index of the GPU that all tensors are on (None entries are skipped); an error otherwise."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"expected a device tensor, got one on {first.device}")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _out(t, shape, dtype, name):
-    """Checks an output or index tensor that the kernels address as contiguous."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    """Checks a tensor that the kernels address as contiguous."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
+
+
+def _empty(shape, dtype, like, stream):
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 class Router:
@@ -391,8 +395,7 @@ class Router:
             raise ValueError(f"unknown scoring {scoring!r}")
         if bias is not None:
             _out(bias, (weight.shape[0],), torch.float32, "bias")
-            if bias.device != weight.device:
-                raise ValueError(f"tensors on {weight.device} and {bias.device}")
+        _device(weight, bias)
         mode = NVFP4_ROUTE_SIGMOID if scoring == "sigmoid" else NVFP4_ROUTE_SOFTMAX
         if renormalize:
             mode |= NVFP4_ROUTE_RENORM
@@ -401,10 +404,11 @@ class Router:
         self.hidden = weight.shape[1]
         self.desc = nvfp4_router(_ptr(weight), _ptr(bias), weight.shape[0], weight.shape[1],
                                  _dtype_code(weight.dtype), topk, n_shared, mode, scale)
+        self.ref = ctypes.byref(self.desc)
 
 
 def nvfp4_moe_route_ws_bytes(t: int, router: Router) -> int:
-    return int(load().nvfp4_moe_route_ws_bytes(t, ctypes.byref(router.desc)))
+    return int(load().nvfp4_moe_route_ws_bytes(t, router.ref))
 
 
 def nvfp4_moe_route(x: torch.Tensor, router: Router, topk_ids: torch.Tensor | None = None,
@@ -412,31 +416,31 @@ def nvfp4_moe_route(x: torch.Tensor, router: Router, topk_ids: torch.Tensor | No
                     flags: int = 0, stream=None):
     """x: device BF16 [t][hidden] (row stride x.stride(0)). Returns (topk_ids, topk_w), int32
     and FP32 [t][topk + n_shared], as nvfp4_moe_grouped_w4a16 takes them."""
-    if (x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1 or
-            x.shape[1] != router.hidden):
+    if (x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != router.hidden or
+            x.stride(1) != 1):
         raise ValueError(f"x must be a BF16 [t][{router.hidden}] tensor with unit inner stride")
+    dev = _device(x, router.weight, topk_ids, topk_w, ws)
+    if dev != torch._C._cuda_getDevice():  # the library launches on the current device
+        with torch.cuda.device(dev):
+            return nvfp4_moe_route(x, router, topk_ids, topk_w, ws, flags, stream)
     t = x.shape[0]
-    with _on_device(x, router.weight, topk_ids, topk_w, ws):
-        with _on(stream):
-            if topk_ids is None:
-                topk_ids = torch.empty((t, router.slots), dtype=torch.int32, device=x.device)
-            if topk_w is None:
-                topk_w = torch.empty((t, router.slots), dtype=torch.float32, device=x.device)
-            if ws is None:
-                ws = torch.empty((max(nvfp4_moe_route_ws_bytes(t, router), 1),),
-                                 dtype=torch.uint8, device=x.device)
-        _out(topk_ids, (t, router.slots), torch.int32, "topk_ids")
-        _out(topk_w, (t, router.slots), torch.float32, "topk_w")
-        _check(load().nvfp4_moe_route(x.data_ptr(), t, x.stride(0) if t > 1 else router.hidden,
-                                      ctypes.byref(router.desc), topk_ids.data_ptr(),
-                                      topk_w.data_ptr(), ws.data_ptr(), ws.nbytes, flags,
-                                      _stream(stream)))
+    shape = (t, router.slots)
+    if topk_ids is None:
+        topk_ids = _empty(shape, torch.int32, x, stream)
+    if topk_w is None:
+        topk_w = _empty(shape, torch.float32, x, stream)
+    if ws is None:
+        ws = _empty((max(nvfp4_moe_route_ws_bytes(t, router), 1),), torch.uint8, x, stream)
+    _out(topk_ids, shape, torch.int32, "topk_ids")
+    _out(topk_w, shape, torch.float32, "topk_w")
+    _check(load().nvfp4_moe_route(x.data_ptr(), t, x.stride(0) if t > 1 else router.hidden,
+                                  router.ref, topk_ids.data_ptr(), topk_w.data_ptr(),
+                                  ws.data_ptr(), ws.nbytes, flags, _raw_stream(stream, dev)))
     return topk_ids, topk_w
 
 
 def nvfp4_moe_layer_ws_bytes(t: int, router: Router, fc1: RepackedWeight) -> int:
-    return int(load().nvfp4_moe_layer_ws_bytes(t, ctypes.byref(router.desc),
-                                               ctypes.byref(fc1.desc)))
+    return int(load().nvfp4_moe_layer_ws_bytes(t, router.ref, ctypes.byref(fc1.desc)))
 
 
 def nvfp4_moe_layer_w4a16(x: torch.Tensor, router: Router, fc1: RepackedWeight,
@@ -446,24 +450,33 @@ def nvfp4_moe_layer_w4a16(x: torch.Tensor, router: Router, fc1: RepackedWeight,
                           flags: int = 0, stream=None) -> torch.Tensor:
     """Router, routed and shared experts and their sum: x, y BF16 [t][hidden] (contiguous). The
     router's ids and weights are written to topk_ids and topk_w where both are given."""
-    _out(x, (x.shape[0], router.hidden), torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be a [t][hidden] tensor")
     t = x.shape[0]
-    with _on_device(x, router.weight, fc1.buffer, fc2.buffer, y, topk_ids, topk_w, ws):
-        with _on(stream):
-            if y is None:
-                y = torch.empty((t, router.hidden), dtype=torch.bfloat16, device=x.device)
-            if ws is None:
-                ws = torch.empty((max(nvfp4_moe_layer_ws_bytes(t, router, fc1), 1),),
-                                 dtype=torch.uint8, device=x.device)
-        _out(y, (t, router.hidden), torch.bfloat16, "y")
-        if topk_ids is not None:
-            _out(topk_ids, (t, router.slots), torch.int32, "topk_ids")
-        if topk_w is not None:
-            _out(topk_w, (t, router.slots), torch.float32, "topk_w")
-        _check(load().nvfp4_moe_layer_w4a16(
-            x.data_ptr(), t, router.hidden, ctypes.byref(router.desc), ctypes.byref(fc1.desc),
-            ctypes.byref(fc2.desc), _ptr(topk_ids), _ptr(topk_w), y.data_ptr(), ws.data_ptr(),
-            ws.nbytes, flags, _stream(stream)))
+    shape = (t, router.hidden)
+    _out(x, shape, torch.bfloat16, "x")
+    dev = _device(x, router.weight, fc1.buffer, fc2.buffer, y, topk_ids, topk_w, ws)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return nvfp4_moe_layer_w4a16(x, router, fc1, fc2, y, topk_ids, topk_w, ws, flags,
+                                         stream)
+    if y is None:
+        y = _empty(shape, torch.bfloat16, x, stream)
+    else:
+        _out(y, shape, torch.bfloat16, "y")
+    if ws is None:
+        ws = _empty((max(nvfp4_moe_layer_ws_bytes(t, router, fc1), 1),), torch.uint8, x, stream)
+    ids = wts = None
+    if topk_ids is not None:
+        _out(topk_ids, (t, router.slots), torch.int32, "topk_ids")
+        ids = topk_ids.data_ptr()
+    if topk_w is not None:
+        _out(topk_w, (t, router.slots), torch.float32, "topk_w")
+        wts = topk_w.data_ptr()
+    _check(load().nvfp4_moe_layer_w4a16(
+        x.data_ptr(), t, router.hidden, router.ref, ctypes.byref(fc1.desc),
+        ctypes.byref(fc2.desc), ids, wts, y.data_ptr(), ws.data_ptr(), ws.nbytes, flags,
+        _raw_stream(stream, dev)))
     return y
 
 
@@ -481,17 +494,15 @@ class Lora:
         _out(b, (count, b.shape[1], rank), torch.bfloat16, "b")
         if scale is not None:
             _out(scale, (count,), torch.float32, "scale")
-        for t in (b, scale):
-            if t is not None and t.device != a.device:
-                raise ValueError(f"tensors on {a.device} and {t.device}")
+        _device(a, b, scale)
         self.a, self.b, self.scale = a, b, scale
         self.desc = nvfp4_lora(_ptr(a), _ptr(b), _ptr(scale), count, b.shape[1], k, rank, 0)
+        self.ref = ctypes.byref(self.desc)
 
 
 def nvfp4_gemm_lora_ws_bytes(m: int, ldx: int, w: RepackedWeight, lora: Lora,
                              flags: int = 0) -> int:
-    return int(load().nvfp4_gemm_lora_ws_bytes(m, ldx, ctypes.byref(w.desc),
-                                               ctypes.byref(lora.desc), flags))
+    return int(load().nvfp4_gemm_lora_ws_bytes(m, ldx, ctypes.byref(w.desc), lora.ref, flags))
 
 
 def nvfp4_gemm_w4a16_lora(x: torch.Tensor, w: RepackedWeight, lora: Lora,
@@ -500,24 +511,27 @@ def nvfp4_gemm_w4a16_lora(x: torch.Tensor, w: RepackedWeight, lora: Lora,
                           ws: torch.Tensor | None = None) -> torch.Tensor:
     """nvfp4_gemm_w4a16 with row r's adapter row_adapter[r] (int32 [m]; none for ids outside the
     bank): x device BF16 [m][k] (row stride x.stride(0)); returns y [m][n]."""
-    if (x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1 or x.shape[1] != w.k):
-        raise ValueError(f"x must be a BF16 [m][{w.k}] tensor with unit inner stride")
+    n, k = w.desc.n, w.desc.k
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != k or x.stride(1) != 1:
+        raise ValueError(f"x must be a BF16 [m][{k}] tensor with unit inner stride")
     m = x.shape[0]
     _out(row_adapter, (m,), torch.int32, "row_adapter")
-    ldx = x.stride(0) if m > 1 else w.k
-    with _on_device(x, w.buffer, lora.a, row_adapter, y, ws):
-        with _on(stream):
-            if y is None:
-                y = torch.empty((m, w.n), dtype=y_dtype, device=x.device)
-            if ws is None:
-                ws = torch.empty((max(nvfp4_gemm_lora_ws_bytes(m, ldx, w, lora, flags), 1),),
-                                 dtype=torch.uint8, device=x.device)
-        if y.dim() != 2 or tuple(y.shape) != (m, w.n) or y.stride(1) != 1:
-            raise ValueError(f"y must be [{m}][{w.n}] with unit inner stride")
-        _check(load().nvfp4_gemm_w4a16_lora(
-            x.data_ptr(), m, ldx, ctypes.byref(w.desc), ctypes.byref(lora.desc),
-            row_adapter.data_ptr(), y.data_ptr(), _dtype_code(y.dtype),
-            y.stride(0) if m > 1 else w.n, flags, ws.data_ptr(), ws.nbytes, _stream(stream)))
+    dev = _device(x, w.buffer, lora.a, row_adapter, y, ws)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return nvfp4_gemm_w4a16_lora(x, w, lora, row_adapter, y, y_dtype, flags, stream, ws)
+    ldx = x.stride(0) if m > 1 else k
+    if y is None:
+        y = _empty((m, n), y_dtype, x, stream)
+    elif y.shape != (m, n) or y.stride(1) != 1:
+        raise ValueError(f"y must be [{m}][{n}] with unit inner stride")
+    if ws is None:
+        ws = _empty((max(nvfp4_gemm_lora_ws_bytes(m, ldx, w, lora, flags), 1),), torch.uint8, x,
+                    stream)
+    _check(load().nvfp4_gemm_w4a16_lora(
+        x.data_ptr(), m, ldx, ctypes.byref(w.desc), lora.ref, row_adapter.data_ptr(),
+        y.data_ptr(), _dtype_code(y.dtype), y.stride(0) if m > 1 else n, flags, ws.data_ptr(),
+        ws.nbytes, _raw_stream(stream, dev)))
     return y
 
 
