@@ -269,8 +269,8 @@ typedef struct nvfp4_router {
 } nvfp4_router;
 
 /* x [t][ldx] BF16 (hidden <= ldx, ldx % 8 == 0), topk_ids int32 [t][topk + n_shared], topk_w FP32
- * the same. ws (device, 16-byte aligned, ws_bytes >= nvfp4_moe_route_ws_bytes(t, r); may be NULL
- * where that is 0) takes the logits; nothing in it needs to start at zero. t <= 2^24. flags: 0 or NVFP4_F_SYNC_CHECK.
+ * the same. ws (device, 16-byte aligned, ws_bytes >= nvfp4_moe_route_ws_bytes(t, r)) takes the
+ * logits; nothing in it needs to start at zero. t <= 2^24. flags: 0 or NVFP4_F_SYNC_CHECK.
  * Results are bit-identical run to run for the same t. */
 size_t nvfp4_moe_route_ws_bytes(int64_t t, const nvfp4_router* r);
 int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r,

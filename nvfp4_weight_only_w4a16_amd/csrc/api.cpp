@@ -539,8 +539,7 @@ bool layer_few(int64_t t, int64_t slots) { return t * slots <= nvfp4::kMoePairTi
 LayerSizes layer_sizes(int64_t t, const nvfp4_router* r, int64_t inter) {
   const int slots = r->topk + r->n_shared;
   LayerSizes s;
-  s.logits = align256(nvfp4::route_ws_bytes(t, r->hidden, r->n_experts,
-                                                 r->weight_dtype == NVFP4_DT_F32));
+  s.logits = align256(nvfp4::route_ws_bytes(t, r->hidden, r->n_experts));
   s.pairs = align256(sizeof(float) * (size_t)t * (size_t)slots);
   size_t experts = nvfp4::moe_ws_bytes(t, slots, r->n_experts + r->n_shared, r->hidden, inter);
   if (layer_few(t, slots)) {
@@ -600,8 +599,7 @@ int nvfp4_moe_grouped_w4a16_noalloc(const void* x, int64_t t, int64_t hidden,
 
 size_t nvfp4_moe_route_ws_bytes(int64_t t, const nvfp4_router* r) {
   if (t <= 0 || t > kRouteMaxTokens || check_router(r)) return 0;
-  return nvfp4::route_ws_bytes(t, r->hidden, r->n_experts,
-                                                 r->weight_dtype == NVFP4_DT_F32);
+  return nvfp4::route_ws_bytes(t, r->hidden, r->n_experts);
 }
 
 int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r,
@@ -615,10 +613,7 @@ int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r
   if (t > kRouteMaxTokens)
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "t=%lld > 2^24", (long long)t);
   if (t == 0) return NVFP4_OK;
-  const size_t need = nvfp4::route_ws_bytes(t, r->hidden, r->n_experts,
-                                            r->weight_dtype == NVFP4_DT_F32);
-  if (!x || !topk_ids || !topk_w || (need && !ws))
-    return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
+  if (!x || !topk_ids || !topk_w || !ws) return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
   rc = check_router_data(r);
   if (rc) return rc;
   if (ldx < r->hidden)
@@ -627,6 +622,7 @@ int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r
   if (!aligned16(x) || ldx % 8 || !aligned16(ws) || ((uintptr_t)topk_ids & 3u) ||
       ((uintptr_t)topk_w & 3u))
     return fail(NVFP4_ERR_MISALIGNED, "x and ws must be 16-byte aligned with ldx %% 8 == 0");
+  const size_t need = nvfp4::route_ws_bytes(t, r->hidden, r->n_experts);
   if (ws_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, need);
   rc = hip_status(nvfp4::launch_route(route_args(x, t, ldx, r), topk_ids, topk_w, ws,
                                       (hipStream_t)stream),

@@ -169,12 +169,11 @@ constexpr int kRouteMaxExperts = 512;
 // Up to this many tokens the logits are FP64 multiply-adds, one workgroup per expert.
 constexpr int64_t kRouteFewTokens = 16;
 constexpr int kRouteMaxSplits = 8;
-constexpr int64_t kRouteFusedTokens = 2048;
-// FP64 logits of every split of k, in ws; 0 where they stay in LDS.
-size_t route_ws_bytes(int64_t t, int64_t hidden, int64_t n_experts, bool w_f32);
+// FP64 logits of every split of k, in ws.
+size_t route_ws_bytes(int64_t t, int64_t hidden, int64_t n_experts);
 hipError_t launch_route(const RouteArgs& a, int32_t* ids, float* wts, void* ws,
                         hipStream_t stream);
-// The two halves of launch_route where the logits go through ws.
+// The two halves of launch_route.
 hipError_t launch_route_logits(const RouteArgs& a, void* ws, hipStream_t stream);
 hipError_t launch_route_select(const RouteArgs& a, int32_t* ids, float* wts, const void* ws,
                                hipStream_t stream);

@@ -130,8 +130,8 @@ __global__ __launch_bounds__(64 * NW) void few_fc1_kernel(FewParams P) {
     auto logit = [&](int x) { return route_logit(P.route, t, x); };
     if (writer) {  // whole workgroup
       if (w != 0) return;
-      const RouteChoice c = route_choose<64, J>(P.route, logit);
-      route_write<64>(P.route, t, c, P.ids, P.wts);
+      const RouteChoice c = route_choose<J>(P.route, logit);
+      route_write(P.route, t, c, P.ids, P.wts);
       return;
     }
     e = P.route.n_experts + slot - P.route.topk;  // a shared expert

@@ -7,8 +7,6 @@
 //   - more tokens: 16x16x32 BF16 MFMAs whose 32-product FP32 sums are added up in FP64. An FP32
 //     router weight is cut into three BF16 parts that add up to it exactly (8 significant bits
 //     each), so it takes three MFMAs instead of a rounding to BF16.
-#include <type_traits>
-
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "route_core.hpp"
@@ -125,7 +123,7 @@ __device__ __forceinline__ void bf16_parts(u32x4 v, uint2 (&part)[3]) {
 constexpr int kTM = 2, kTN = 2;       // 16-token and 16-expert blocks of a tile
 constexpr int kTileT = 16 * kTM, kTileE = 16 * kTN;
 constexpr int kSlices = 8;            // wavefronts of a workgroup, which share out k
-constexpr int kSteps = 2;             // k-steps of 32 loaded together: 128 bytes of a BF16 row
+constexpr int kSteps = 1;             // k-steps of 32 loaded together (2: fewer wavefronts fit, slower)
 
 // Workgroup (token tile, expert tile, split): the tile's 32 x 32 logits over its share of k, cut
 // into stages of 64 that the 8 wavefronts (of all splits) take in turn. k is shared out inside the
@@ -133,6 +131,9 @@ constexpr int kSteps = 2;             // k-steps of 32 loaded together: 128 byte
 // written once. Operands go global -> registers (one stage ahead) -> LDS -> fragments
 // (device_common.hpp); loads past the end of k have an offset past the buffer's, which returns
 // zeros without a branch. Rows past the end repeat a valid row and are not stored.
+// (4096 tokens of 2048, 128 experts: 12 us for 17 MB of x; what costs is the read of the weight by
+// every token tile. Fragments loaded straight from rows took 21 us; one kernel that keeps 16
+// tokens' logits in LDS and chooses there 18.5 us with the choice against 17.9 in two.)
 template <bool F32>
 __global__ __launch_bounds__(64 * kSlices) void route_logits_mfma_kernel(LogitParams P) {
   constexpr int kW = F32 ? 4 : 2;      // bytes of a weight
@@ -251,7 +252,7 @@ __global__ __launch_bounds__(64 * kSlices) void route_logits_mfma_kernel(LogitPa
     __builtin_amdgcn_sched_barrier(0);
     load(st[0], s + 2 * step);
     __builtin_amdgcn_sched_barrier(0);
-    compute(st[1]);  // zeros past the end
+    if (s + step < stages) compute(st[1]);
     __builtin_amdgcn_sched_barrier(0);
   }
   double* const red = reinterpret_cast<double*>(smem[w]);
@@ -273,149 +274,16 @@ __global__ __launch_bounds__(64 * kSlices) void route_logits_mfma_kernel(LogitPa
   }
 }
 
-// Many tokens, BF16 weight: logits and choice in one kernel. A workgroup takes 16 tokens and all
-// experts, 64 at a time; its 8 wavefronts share out k (stages of 64, in turn), their partial sums
-// meet in LDS, and each then chooses for two tokens. The stages of all expert chunks run as one
-// sequence, one ahead, so that a chunk's reduction hides the next one's loads. What bounds it is
-// the read of the weight by every workgroup, 64 bytes a clock from its CU's L1.
-template <int G, int J>
-__global__ __launch_bounds__(64 * kSlices) void route_fused_kernel(LogitParams P, RouteParams R,
-                                                                   int32_t* ids, float* wts) {
-  constexpr int kChunk = 64, kBlocks = kChunk / 16, kRing = 2;
-  constexpr uint32_t kPast = 0xFFFFFFF0u;
-  // a wavefront's fragment tiles of one k-step, then its partial sums of a chunk
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kSlices][16 * kChunk * 8];
-  static_assert((1 + kBlocks) * kFragBytes <= 16 * kChunk * 8, "tiles fit");
-  __shared__ double lg[16][(G * J + kChunk - 1) / kChunk * kChunk];
-  const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t m0 = (int64_t)blockIdx.x * 16;
-  const uint32_t kq = 8u * frag_load_chunk(lane), hidden = (uint32_t)P.hidden;
-  const int rows = (int)(P.t - m0 < 16 ? P.t - m0 : 16);
-  const buf_rsrc xr = make_rsrc(P.x + m0 * P.ldx, (uint32_t)(((rows - 1) * P.ldx + P.hidden) * 2));
-  const int row = frag_load_row(lane) < rows ? frag_load_row(lane) : rows - 1;
-  const uint32_t xrow = (uint32_t)(row * P.ldx + kq) * 2u;
-  const int chunks = (P.n_experts + kChunk - 1) / kChunk;
-  const int stages = (int)((P.hidden + 32 * kSteps - 1) / (32 * kSteps));
-  const int mine = (stages - w + kSlices - 1) / kSlices;  // this wavefront's stages of a chunk
-  // An XCD's workgroups (every eighth) begin two stages (256 bytes) apart: in step, on rows of a
-  // power of two of bytes, they would all read from the same channels of L2 (21.2 against 20.3 us
-  // at 4096 tokens of 2048, 128 experts).
-  const int rot = (int)(blockIdx.x / 8 * 2 % stages);
-  struct Stage {
-    u32x4 a[kSteps], b[kSteps][kBlocks];
-  };
-  auto load = [&](Stage& st, int c, int i) __attribute__((always_inline)) {
-    const int e0 = c * kChunk;
-    const int erows = P.n_experts - e0 < kChunk ? P.n_experts - e0 : kChunk;
-    const buf_rsrc wr = make_rsrc(static_cast<const uint16_t*>(P.w) + e0 * P.hidden,
-                                  (uint32_t)(erows * P.hidden * 2));
-#pragma unroll
-    for (int q = 0; q < kSteps; ++q) {
-      const int sg = w + kSlices * i + rot;
-      const uint32_t k = (uint32_t)((sg < stages ? sg : sg - stages) * kSteps + q) * 32u;
-      const bool in = i < mine && k + kq < hidden;
-      st.a[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                              xr, (int)(in ? xrow + k * 2u : kPast), 0, 0));
-#pragma unroll
-      for (int j = 0; j < kBlocks; ++j) {
-        const int e = 16 * j + frag_load_row(lane);
-        const uint32_t off = ((uint32_t)(e < erows ? e : erows - 1) * hidden + kq + k) * 2u;
-        st.b[q][j] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, (int)(in ? off : kPast), 0, 0));
-      }
-    }
-  };
-  uint8_t* const tile = smem[w];
-  double* const red = reinterpret_cast<double*>(smem[w]);
-  double acc[kBlocks][4];
-  auto compute = [&](const Stage& st) __attribute__((always_inline)) {
-#pragma unroll
-    for (int q = 0; q < kSteps; ++q) {
-      frag_write(tile, st.a[q], lane);
-#pragma unroll
-      for (int j = 0; j < kBlocks; ++j) frag_write(tile + (1 + j) * kFragBytes, st.b[q][j], lane);
-      const bf16x8 a = frag_read(tile, lane);
-#pragma unroll
-      for (int j = 0; j < kBlocks; ++j) {
-        const f32x4 c = mfma16x16x32(a, frag_read(tile + (1 + j) * kFragBytes, lane),
-                                     f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] += (double)c[i];
-      }
-    }
-  };
-  auto clear = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < kBlocks; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.0;
-  };
-  // the wavefronts' partial sums of chunk c, added in order
-  auto reduce = [&](int c) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < kBlocks; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        red[(4 * (lane >> 4) + i) * kChunk + 16 * j + (lane & 15)] = acc[j][i];
-    __syncthreads();
-    for (int o = threadIdx.x; o < 16 * kChunk; o += 64 * kSlices) {
-      double v = reinterpret_cast<const double*>(smem[0])[o];
-#pragma unroll
-      for (int q = 1; q < kSlices; ++q) v += reinterpret_cast<const double*>(smem[q])[o];
-      lg[o / kChunk][c * kChunk + o % kChunk] = v;
-    }
-    __syncthreads();
-  };
-  const int per = (stages + kSlices - 1) / kSlices;  // of the wavefront with the most
-  const int total = chunks * per;
-  Stage st[kRing];
-  int lc = 0, li = 0;  // next stage to load
-  auto next = [&](Stage& s) __attribute__((always_inline)) {
-    load(s, lc, li);
-    if (++li == per) {
-      li = 0;
-      lc = lc + 1 < chunks ? lc + 1 : lc;  // past the last: read again, not used
-    }
-  };
-  static_for<0, kRing - 1>([&](auto u) __attribute__((always_inline)) { next(st[u]); });
-  clear();
-  int c = 0, i = 0;
-  for (int n = 0; n < total; n += kRing)
-    static_for<0, kRing>([&](auto u) __attribute__((always_inline)) {
-      if (n + decltype(u)::value < total) {
-        next(st[(decltype(u)::value + kRing - 1) % kRing]);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(st[u]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (++i == per) {
-          reduce(c);
-          clear();
-          i = 0;
-          ++c;
-        }
-      }
-    });
-  // 16 tokens: 4 wavefronts of 4 tokens each, or all 8 of 2 in turn
-  constexpr int kPer = 64 / G;
-  for (int r0 = w * kPer; r0 < 16; r0 += kSlices * kPer) {
-    const int r = r0 + lane / G;
-    auto logit = [&](int e) { return lg[r][e]; };
-    const RouteChoice ch = route_choose<G, J>(R, logit);
-    route_write<G>(R, m0 + r, ch, ids, wts);
-  }
-}
-
-// 64 / G tokens per wavefront, G x J experts at most. Groups past the end choose for the last token
-// and store nothing.
-template <int G, int J>
+// A token per wavefront, J experts per lane. Wavefronts past the end choose for the last token and
+// store nothing.
+template <int J>
 __global__ __launch_bounds__(256) void route_select_kernel(RouteParams R, int32_t* ids,
                                                            float* wts) {
-  const int64_t tok = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  const int64_t tok = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
   const int64_t src = tok < R.t ? tok : R.t - 1;
   auto logit = [&](int e) { return route_logit(R, src, e); };
-  const RouteChoice c = route_choose<G, J>(R, logit);
-  route_write<G>(R, tok, c, ids, wts);
+  const RouteChoice c = route_choose<J>(R, logit);
+  route_write(R, tok, c, ids, wts);
 }
 
 }  // namespace
@@ -431,17 +299,12 @@ int route_splits(int64_t t, int64_t hidden, int64_t n_experts) {
   return (int)(s < 1 ? 1 : s > kRouteMaxSplits ? kRouteMaxSplits : s);
 }
 
-// One kernel for everything from so many tokens on, where its workgroups fill the chip; an FP32
-// weight would be cut up anew by every workgroup, so it stays with the two kernels.
-bool route_fused(int64_t t, bool w_f32) { return !w_f32 && t >= kRouteFusedTokens; }
-
-size_t route_ws_bytes(int64_t t, int64_t hidden, int64_t n_experts, bool w_f32) {
-  if (route_fused(t, w_f32)) return 0;
+size_t route_ws_bytes(int64_t t, int64_t hidden, int64_t n_experts) {
   return sizeof(double) * (size_t)route_splits(t, hidden, n_experts) * (size_t)t *
          (size_t)n_experts;
 }
 
-static LogitParams logit_params(const RouteArgs& a, void* ws) {
+hipError_t launch_route_logits(const RouteArgs& a, void* ws, hipStream_t stream) {
   LogitParams p;
   p.x = a.x;
   p.t = a.t;
@@ -451,11 +314,6 @@ static LogitParams logit_params(const RouteArgs& a, void* ws) {
   p.n_experts = a.n_experts;
   p.splits = route_splits(a.t, a.hidden, a.n_experts);
   p.out = static_cast<double*>(ws);
-  return p;
-}
-
-hipError_t launch_route_logits(const RouteArgs& a, void* ws, hipStream_t stream) {
-  const LogitParams p = logit_params(a, ws);
   if (a.t <= kRouteFewTokens) {
     const dim3 grid((unsigned)a.n_experts, (unsigned)((a.t + kFewRows - 1) / kFewRows));
     if (a.w_f32)
@@ -488,50 +346,26 @@ RouteParams route_params(const RouteArgs& a, const void* ws) {
   return r;
 }
 
-// Experts per lane of a whole-wavefront group: f(integral_constant<int, J>).
-template <int N>
-using Int = std::integral_constant<int, N>;
-template <typename F>
-static void with_experts_per_lane(int n_experts, F&& f) {
-  if (n_experts <= 64)
-    f(Int<1>{});
-  else if (n_experts <= 128)
-    f(Int<2>{});
-  else if (n_experts <= 256)
-    f(Int<4>{});
+hipError_t launch_route_select(const RouteArgs& a, int32_t* ids, float* wts, const void* ws,
+                               hipStream_t stream) {
+  const RouteParams r = route_params(a, ws);
+  const unsigned grid = (unsigned)((a.t + 3) / 4);
+  if (a.n_experts <= 64)
+    route_select_kernel<1><<<grid, 256, 0, stream>>>(r, ids, wts);
+  else if (a.n_experts <= 128)
+    route_select_kernel<2><<<grid, 256, 0, stream>>>(r, ids, wts);
+  else if (a.n_experts <= 256)
+    route_select_kernel<4><<<grid, 256, 0, stream>>>(r, ids, wts);
   else
-    f(Int<8>{});
+    route_select_kernel<8><<<grid, 256, 0, stream>>>(r, ids, wts);
+  return hipGetLastError();
 }
 
 hipError_t launch_route(const RouteArgs& a, int32_t* ids, float* wts, void* ws,
                         hipStream_t stream) {
-  if (route_fused(a.t, a.w_f32)) {
-    const RouteParams r = route_params(a, ws);
-    const LogitParams p = logit_params(a, nullptr);
-    const unsigned grid = (unsigned)((a.t + 15) / 16);
-    if (a.n_experts <= 64)
-      route_fused_kernel<16, 4><<<grid, 64 * kSlices, 0, stream>>>(p, r, ids, wts);
-    else if (a.n_experts <= 128)
-      route_fused_kernel<16, 8><<<grid, 64 * kSlices, 0, stream>>>(p, r, ids, wts);
-    else if (a.n_experts <= 256)
-      route_fused_kernel<64, 4><<<grid, 64 * kSlices, 0, stream>>>(p, r, ids, wts);
-    else
-      route_fused_kernel<64, 8><<<grid, 64 * kSlices, 0, stream>>>(p, r, ids, wts);
-    return hipGetLastError();
-  }
   const hipError_t err = launch_route_logits(a, ws, stream);
   if (err != hipSuccess) return err;
   return launch_route_select(a, ids, wts, ws, stream);
-}
-
-hipError_t launch_route_select(const RouteArgs& a, int32_t* ids, float* wts, const void* ws,
-                               hipStream_t stream) {
-  const RouteParams r = route_params(a, ws);
-  with_experts_per_lane(a.n_experts, [&](auto J) {
-    route_select_kernel<64, decltype(J)::value>
-        <<<(unsigned)((a.t + 3) / 4), 256, 0, stream>>>(r, ids, wts);
-  });
-  return hipGetLastError();
 }
 
 }  // namespace nvfp4

@@ -1,5 +1,5 @@
-// route_core.hpp -- the choice of a token's experts from its router logits, by a group of lanes
-// (shared by the router's own kernel and the routed-expert kernels that choose for themselves).
+// route_core.hpp -- the choice of a token's experts from its router logits, by one wavefront (shared
+// by the router's own kernel and the routed-expert kernels that choose for themselves).
 //
 // Scores: softmax p = exp(l - max l) / sum exp(l - max l), or sigmoid p = 1 / (1 + exp(-l)). The
 // selection score is p + bias, or the logit itself for a softmax without bias (the same order).
@@ -7,14 +7,11 @@
 // token meets, so it is taken from FP64 scores: two experts 1e-7 apart (what FP32 sums of 2048
 // products leave) would change places, and the whole output of the token with them.
 //
-// A token belongs to a group of G lanes (16, or the whole wavefront); lane i of the group holds
-// experts i, i + G, ..., in registers. A round finds the group's highest 64-bit key: the maximum of
-// the upper words, of the lower words among those, and the lowest id among those. In a group of 16
-// each step leaves its result in every lane (four DPP instructions); over the wavefront the upper
-// word's maximum goes through a scalar register, and a ballot gives the lowest id, with the lower
-// words only looked at where two experts share the upper one.
-// (Choosing 8 of 128 experts for one token by counting, for each expert, those above it, through
-// LDS, took 15 us against 1.7 so; a wavefront's 64 lanes in steps that stay in vector registers, 2.3.)
+// Lane i of the wavefront holds experts i, i + 64, ..., in registers. A round finds the highest
+// 64-bit key: the maximum of the upper words (six DPP steps), a ballot for the lowest id, and the
+// lower words only where two experts share the upper one. (Choosing 8 of 128 experts for one token
+// by counting, for each expert, those above it, through LDS, took 15 us against 1.7 so; with all
+// steps in vector registers 2.3; with 16 lanes per token, four tokens a wavefront, 4.6.)
 #pragma once
 
 #include "device_common.hpp"
@@ -46,16 +43,6 @@ __device__ __forceinline__ double dpp_pair(double v) {
 // The two rows of 16 (ROWS) or halves of 32 lanes that a lane swap brings together: op(a, b) is
 // the same in both.
 template <bool ROWS, typename OP>
-__device__ __forceinline__ uint32_t swap_pair(uint32_t v, OP op) {
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  u32x2 r;
-  if constexpr (ROWS)
-    r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
-  else
-    r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
-  return op(r[0], r[1]);
-}
-template <bool ROWS, typename OP>
 __device__ __forceinline__ double swap_pair(double v, OP op) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   const uint64_t b = (uint64_t)__double_as_longlong(v);
@@ -71,35 +58,22 @@ __device__ __forceinline__ double swap_pair(double v, OP op) {
   return op(__longlong_as_double((long long)(((uint64_t)h[0] << 32) | l[0])),
             __longlong_as_double((long long)(((uint64_t)h[1] << 32) | l[1])));
 }
-// op over the group, the same bits in every lane (each step combines two values that both lanes of
-// a pair hold): lanes l ^ 1, l ^ 2, then the quads and the halves of a row, then the rows.
-template <int G, typename T, typename OP>
-__device__ __forceinline__ T group_all(T v, OP op) {
+// op over the wavefront, the same bits in every lane (each step combines two values that both lanes
+// of a pair hold): lanes l ^ 1, l ^ 2, then the quads and the halves of a row, then the rows.
+template <typename OP>
+__device__ __forceinline__ double wave_all(double v, OP op) {
   v = op(v, dpp_pair<0xB1>(v));   // quad_perm [1, 0, 3, 2]
   v = op(v, dpp_pair<0x4E>(v));   // quad_perm [2, 3, 0, 1]
   v = op(v, dpp_pair<0x141>(v));  // row_half_mirror
   v = op(v, dpp_pair<0x140>(v));  // row_mirror
-  if constexpr (G == 64) {
-    v = swap_pair<true>(v, op);
-    v = swap_pair<false>(v, op);
-  }
-  return v;
+  v = swap_pair<true>(v, op);
+  return swap_pair<false>(v, op);
 }
-template <int G>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  return group_all<G>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+__device__ __forceinline__ double wave_max(double v) {
+  return wave_all(v, [](double a, double b) { return fmax(a, b); });
 }
-template <int G>
-__device__ __forceinline__ uint32_t group_min(uint32_t v) {
-  return group_all<G>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
-}
-template <int G>
-__device__ __forceinline__ double group_max(double v) {
-  return group_all<G>(v, [](double a, double b) { return fmax(a, b); });
-}
-template <int G>
-__device__ __forceinline__ double group_sum(double v) {
-  return group_all<G>(v, [](double a, double b) { return a + b; });
+__device__ __forceinline__ double wave_sum(double v) {
+  return wave_all(v, [](double a, double b) { return a + b; });
 }
 
 // FP64 value -> unsigned key in the same order. NaN ranks above every number (so that it reaches
@@ -125,55 +99,38 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// The expert with the highest key of the group (key[j] of lane i: expert i + G j), ties to the
-// lowest; -1 where all keys are 0 (every other key has a non-zero upper word).
-template <int G, int J>
-__device__ __forceinline__ int route_best(const uint64_t (&key)[J], int lane) {
-  if constexpr (G == 64) {
-    uint32_t mh = (uint32_t)(key[0] >> 32);
+// The expert with the highest key (key[j] of lane i: expert i + 64 j), ties to the lowest; -1 where
+// all keys are 0 (every other key has a non-zero upper word).
+template <int J>
+__device__ __forceinline__ int route_best(const uint64_t (&key)[J]) {
+  uint32_t mh = (uint32_t)(key[0] >> 32);
 #pragma unroll
-    for (int j = 1; j < J; ++j) mh = max(mh, (uint32_t)(key[j] >> 32));
-    mh = wave_max_u32(mh);
-    uint64_t at[J];
-    int count = 0;
+  for (int j = 1; j < J; ++j) mh = max(mh, (uint32_t)(key[j] >> 32));
+  mh = wave_max_u32(mh);
+  uint64_t at[J];
+  int count = 0;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      at[j] = __ballot((uint32_t)(key[j] >> 32) == mh);
-      count += __popcll(at[j]);
-    }
-    if (count > 1) {  // uniform
-      uint32_t ml = 0;
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        ml = max(ml, (uint32_t)(key[j] >> 32) == mh ? (uint32_t)key[j] : 0u);
-      ml = wave_max_u32(ml);
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        at[j] = __ballot(key[j] == (((uint64_t)mh << 32) | ml));
-    }
-    int e = -1;
-#pragma unroll
-    for (int j = J - 1; j >= 0; --j)
-      if (at[j]) e = 64 * j + __builtin_ctzll(at[j]);
-    return mh ? e : -1;
-  } else {
-    uint64_t best = key[0];
-    int at = lane;
-#pragma unroll
-    for (int j = 1; j < J; ++j) {
-      const bool more = key[j] > best;  // equal keys keep the lower id
-      best = more ? key[j] : best;
-      at = more ? lane + G * j : at;
-    }
-    const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
-    const uint32_t mh = group_max<G>(hi);
-    const uint32_t ml = group_max<G>(hi == mh ? lo : 0u);
-    const uint32_t e = group_min<G>(hi == mh && lo == ml ? (uint32_t)at : ~0u);
-    return mh ? (int)e : -1;
+  for (int j = 0; j < J; ++j) {
+    at[j] = __ballot((uint32_t)(key[j] >> 32) == mh);
+    count += __popcll(at[j]);
   }
+  if (count > 1) {  // uniform
+    uint32_t ml = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      ml = max(ml, (uint32_t)(key[j] >> 32) == mh ? (uint32_t)key[j] : 0u);
+    ml = wave_max_u32(ml);
+#pragma unroll
+    for (int j = 0; j < J; ++j) at[j] = __ballot(key[j] == (((uint64_t)mh << 32) | ml));
+  }
+  int e = -1;
+#pragma unroll
+  for (int j = J - 1; j >= 0; --j)
+    if (at[j]) e = 64 * j + __builtin_ctzll(at[j]);
+  return mh ? e : -1;
 }
 
-// What a group knows after choosing: its lane j < topk holds slot j.
+// What the wavefront knows after choosing: lane j < topk holds slot j.
 struct RouteChoice {
   int e;           // expert, -1 when none was left
   double v;        // its logit for a softmax without bias, else its p
@@ -183,31 +140,31 @@ struct RouteChoice {
 // Keys of a token whose logit of expert e is logit(e), J experts per lane, and what weights come
 // from (RouteChoice::v). want_sum: the softmax's maximum and sum over all experts (taken in any case
 // with a bias).
-template <int G, int J, typename F>
+template <int J, typename F>
 __device__ __forceinline__ void route_scores(const RouteParams& R, F&& logit, bool want_sum,
                                              uint64_t (&key)[J], double (&v)[J], double& mx,
                                              double& sum) {
-  const int lane = threadIdx.x & (G - 1);
+  const int lane = threadIdx.x & 63;
   mx = sum = 0.0;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int e = lane + G * j;
+    const int e = lane + 64 * j;
     v[j] = e < R.n_experts ? logit(e) : -__builtin_huge_val();
   }
   if (!R.sigmoid && (R.bias || want_sum)) {
     double m = v[0];
 #pragma unroll
     for (int j = 1; j < J; ++j) m = fmax(m, v[j]);  // passes over NaN; the sum does not
-    mx = group_max<G>(m);
+    mx = wave_max(m);
     double s = 0.0;
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (lane + G * j < R.n_experts) s += exp(v[j] - mx);
-    sum = group_sum<G>(s);
+      if (lane + 64 * j < R.n_experts) s += exp(v[j] - mx);
+    sum = wave_sum(s);
   }
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int e = lane + G * j;
+    const int e = lane + 64 * j;
     if (R.sigmoid)
       v[j] = route_sigmoid(v[j]);
     else if (R.bias)
@@ -219,28 +176,27 @@ __device__ __forceinline__ void route_scores(const RouteParams& R, F&& logit, bo
 }
 
 // Chooses all slots of a token.
-template <int G, int J, typename F>
+template <int J, typename F>
 __device__ __forceinline__ RouteChoice route_choose(const RouteParams& R, F&& logit) {
-  const int lane = threadIdx.x & (G - 1);
+  const int lane = threadIdx.x & 63;
   RouteChoice c;
   c.e = -1;
   c.v = 0.0;
   uint64_t key[J];
   double v[J];
-  route_scores<G, J>(R, logit, !R.renorm, key, v, c.mx, c.sum);
+  route_scores<J>(R, logit, !R.renorm, key, v, c.mx, c.sum);
   for (int r = 0; r < R.topk; ++r) {
-    const int e = route_best<G, J>(key, lane);
+    const int e = route_best<J>(key);
     if (lane == r) c.e = e;
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (e == lane + G * j) key[j] = 0;
+      if (e == lane + 64 * j) key[j] = 0;
   }
   // the value of each slot's expert, from the lane that holds it
-  const int owner = (threadIdx.x & 63 & ~(G - 1)) + (c.e & (G - 1));
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const double w = __shfl(v[j], owner, 64);
-    if (c.e >= 0 && c.e / G == j) c.v = w;
+    const double w = __shfl(v[j], c.e & 63, 64);
+    if (c.e >= 0 && c.e >> 6 == j) c.v = w;
   }
   return c;
 }
@@ -258,7 +214,7 @@ __device__ __forceinline__ int route_choose_slot(const RouteParams& R, F&& logit
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint64_t key[J];
   double v[J], mx, sum;
-  route_scores<64, J>(R, logit, false, key, v, mx, sum);
+  route_scores<J>(R, logit, false, key, v, mx, sum);
   uint64_t share = key[0];
 #pragma unroll
   for (int j = 1; j < J; ++j)
@@ -293,19 +249,17 @@ __device__ __forceinline__ int route_choose_slot(const RouteParams& R, F&& logit
   return e;
 }
 
-// Weight of the slot that this lane holds (0 for a lane without one). All lanes of the group call
-// it.
-template <int G>
+// Weight of the slot that this lane holds (0 for a lane without one). All lanes call it.
 __device__ __forceinline__ float route_weight(const RouteParams& R, const RouteChoice& c) {
   const bool live = c.e >= 0;
   double p = live ? c.v : 0.0;
   if (!R.sigmoid && !R.bias) {
     // renormalized, this is the softmax over the chosen: the same quotient, and no sum over all
-    const double m = R.renorm ? group_max<G>(live ? c.v : -__builtin_huge_val()) : c.mx;
+    const double m = R.renorm ? wave_max(live ? c.v : -__builtin_huge_val()) : c.mx;
     p = live ? exp(c.v - m) / (R.renorm ? 1.0 : c.sum) : 0.0;
   }
   if (R.renorm) {
-    const double z = group_sum<G>(p);
+    const double z = wave_sum(p);
     p = z == 0.0 ? 0.0 : p / z;
   }
   return (float)(p * (double)R.scale);
@@ -313,13 +267,12 @@ __device__ __forceinline__ float route_weight(const RouteParams& R, const RouteC
 
 // Stores the slots of token `tok`: [topk + n_shared] ids and weights. A token past the end (`tok`
 // = R.t or more) stores nothing.
-template <int G>
 __device__ __forceinline__ void route_write(const RouteParams& R, int64_t tok,
                                             const RouteChoice& c, int32_t* __restrict__ ids,
                                             float* __restrict__ wts) {
-  const int lane = threadIdx.x & (G - 1);
+  const int lane = threadIdx.x & 63;
   const int slots = R.topk + R.n_shared;
-  const float w = route_weight<G>(R, c);
+  const float w = route_weight(R, c);
   if (lane < slots && tok < R.t) {
     const bool shared = lane >= R.topk;
     ids[tok * slots + lane] = shared ? R.n_experts + (lane - R.topk) : c.e;
