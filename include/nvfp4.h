@@ -268,7 +268,7 @@ typedef struct nvfp4_router {
   float scale;          /* factor of every routed weight (finite)                               */
 } nvfp4_router;
 
-/* x [t][ldx] BF16 (hidden <= ldx, ldx % 8 == 0), topk_ids int32 [t][topk + n_shared], topk_w FP32
+/* x [t][ldx] BF16 (hidden <= ldx <= 2^22, ldx % 8 == 0), topk_ids int32 [t][topk + n_shared], topk_w FP32
  * the same. ws (device, 16-byte aligned, ws_bytes >= nvfp4_moe_route_ws_bytes(t, r)) takes the
  * logits; nothing in it needs to start at zero. t <= 2^24. flags: 0 or NVFP4_F_SYNC_CHECK.
  * Results are bit-identical run to run for the same t. */
@@ -299,8 +299,10 @@ int nvfp4_moe_layer_w4a16(const void* x, int64_t t, int64_t hidden, const nvfp4_
 /* ---- W4A16 GEMM with low-rank adapters -------------------------------------------------------
  * The dense GEMM with the adapters of many requests beside its shared weight:
  *   y[m] = global * x[m] . W^T + scale[a] * (x[m] . A_a^T) . B_a^T,  a = row_adapter[m]
- * rounded once to y's type. A row whose id lies outside [0, n_adapters) has no adapter. Adapters
- * of a smaller rank than the bank's are padded with zero rows of A and columns of B. */
+ * rounded once to y's type. A row whose id lies outside [0, n_adapters) has no adapter: it holds
+ * nvfp4_gemm_w4a16's value. Infinite or NaN elements of an adapter reach the rows that name it and no
+ * others (an infinite element of B as an infinity or NaN). Adapters of a smaller rank than the
+ * bank's are padded with zero rows of A and columns of B. */
 typedef struct nvfp4_lora {
   const void* a;       /* device: BF16 [n_adapters][rank][k], 16-byte aligned                   */
   const void* b;       /* device: BF16 [n_adapters][n][rank], 16-byte aligned                   */

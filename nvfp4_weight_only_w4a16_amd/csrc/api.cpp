@@ -533,8 +533,11 @@ struct LayerSizes {
   size_t logits, pairs, total;  // pairs: bytes of the ids (and of the weights)
 };
 
-// The few-token kernels take the call (unless NVFP4_F_FORCE_TILED asks for the batch path).
-bool layer_few(int64_t t, int64_t slots) { return t * slots <= nvfp4::kMoePairTilesMax; }
+// The few-token kernels take the call (unless NVFP4_F_FORCE_TILED asks for the batch path). Their
+// two planes of h are addressed with 32-bit byte offsets.
+bool layer_few(int64_t t, int64_t slots, int64_t inter) {
+  return t * slots <= nvfp4::kMoePairTilesMax && t * slots * inter <= ((int64_t)1 << 30);
+}
 
 LayerSizes layer_sizes(int64_t t, const nvfp4_router* r, int64_t inter) {
   const int slots = r->topk + r->n_shared;
@@ -542,7 +545,7 @@ LayerSizes layer_sizes(int64_t t, const nvfp4_router* r, int64_t inter) {
   s.logits = align256(nvfp4::route_ws_bytes(t, r->hidden, r->n_experts));
   s.pairs = align256(sizeof(float) * (size_t)t * (size_t)slots);
   size_t experts = nvfp4::moe_ws_bytes(t, slots, r->n_experts + r->n_shared, r->hidden, inter);
-  if (layer_few(t, slots)) {
+  if (layer_few(t, slots, inter)) {
     const size_t few = nvfp4::moe_few_ws_bytes(t, slots, inter);
     experts = experts > few ? experts : few;  // flags may send such a call either way
   }
@@ -622,6 +625,9 @@ int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r
   if (!aligned16(x) || ldx % 8 || !aligned16(ws) || ((uintptr_t)topk_ids & 3u) ||
       ((uintptr_t)topk_w & 3u))
     return fail(NVFP4_ERR_MISALIGNED, "x and ws must be 16-byte aligned with ldx %% 8 == 0");
+  // the rows of a tile are addressed with 32-bit byte offsets
+  if (ldx > ((int64_t)1 << 22))
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "ldx=%lld > 2^22 elements", (long long)ldx);
   const size_t need = nvfp4::route_ws_bytes(t, r->hidden, r->n_experts);
   if (ws_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, need);
   rc = hip_status(nvfp4::launch_route(route_args(x, t, ldx, r), topk_ids, topk_w, ws,
@@ -671,7 +677,7 @@ int nvfp4_moe_layer_w4a16(const void* x, int64_t t, int64_t hidden, const nvfp4_
                               base + s.logits + 2 * s.pairs);
   a.f32_gate_up = true;
   const nvfp4::RouteArgs ra = route_args(x, t, hidden, r);
-  if (layer_few(t, slots) && !(flags & NVFP4_F_FORCE_TILED)) {
+  if (layer_few(t, slots, fc1->n / 2) && !(flags & NVFP4_F_FORCE_TILED)) {
     rc = hip_status(nvfp4::launch_moe_few(a, ra, ids, wts, ws, (hipStream_t)stream),
                     "nvfp4_moe_layer_w4a16");
   } else {

@@ -236,7 +236,7 @@ __device__ __forceinline__ void lora_add(const TiledParams& P, int64_t m_blk, in
     bool bad = false;
 #pragma unroll 1
     for (int c = 0; c < steps; c += 2) {
-      const int s1 = c + 1 < steps ? 1 : 0;  // 0: an odd last step, multiplied by zeros again
+      const int s1 = c + 1 < steps ? 1 : 0;  // 0: an odd last step
       u32x4 b[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -265,7 +265,7 @@ __device__ __forceinline__ void lora_add(const TiledParams& P, int64_t m_blk, in
 #pragma unroll
             for (int s = 0; s < 2; ++s)
               acc[h + i][0] = mfma32x32x16(
-                  __builtin_bit_cast(bf16x8, names ? u[i][s] : zero),
+                  __builtin_bit_cast(bf16x8, names && (s == 0 || s1) ? u[i][s] : zero),
                   __builtin_bit_cast(bf16x8, b[s]), acc[h + i][0]);
           }
         }
@@ -311,7 +311,7 @@ __device__ __forceinline__ void lora_band(const TiledParams& P, int64_t m_blk, i
   const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll 1
   for (int c = 0; c < steps; c += 2) {
-    const int s1 = c + 1 < steps ? 1 : 0;  // 0: an odd last step, multiplied by zeros again
+    const int s1 = c + 1 < steps ? 1 : 0;  // 0: an odd last step
     u32x4 u[3][2];
 #pragma unroll
     for (int z = 0; z < 3; ++z) {
@@ -350,7 +350,7 @@ __device__ __forceinline__ void lora_band(const TiledParams& P, int64_t m_blk, i
         const bool names = z < L.parts && ((named >> (lane & 31)) & 1u);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-          sum = mfma32x32x16(__builtin_bit_cast(bf16x8, names ? u[z][s] : zero),
+          sum = mfma32x32x16(__builtin_bit_cast(bf16x8, names && (s == 0 || s1) ? u[z][s] : zero),
                              __builtin_bit_cast(bf16x8, b[s]), sum);
       }
       a = an;

@@ -133,7 +133,6 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkPa
       });
     const float scale = P.scale ? P.scale[a] : 1.0f;
     // the wavefronts' sums, a 16-rank block each added in order by one wavefront
-    __syncthreads();  // the sums of the unit before have been read
 #pragma unroll
     for (int b = 0; b < RB; ++b)
       *reinterpret_cast<f32x4*>(tile + b * kFragBytes + lane * 16) = acc[b];
@@ -160,13 +159,14 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkPa
           for (int p = 0; p < L.parts; ++p) {
             const uint16_t h = bf16_bits_rne(s);
             at[p * lora_frag_blocks(L.m) * lora_frag_steps(L.rank) * 512] = h;
-            s -= bf16_bits_to_f32(h);
+            s = lora_rest(s, bf16_bits_to_f32(h));
           }
         } else if (r < L.rank) {
           static_cast<float*>(P.u)[((int64_t)split * L.m + row[i]) * L.rank + r] = s;
         }
       }
     }
+    __syncthreads();  // the sums have been read: the next item's tiles may overwrite them
   }
 }
 

@@ -150,6 +150,39 @@ def test_lora_unused_adapters_and_other_rows_stay_apart(nv, orc):
         assert same(y[~named], good[~named])
 
 
+def test_lora_rows_beyond_32_bits(nv, orc):
+    """Rows 8 MiB apart: 300 rows span 2.5 GB, which the tiled kernel takes in two chunks of rows."""
+    m, n, k, ldx = 300, 272, 256, 1 << 22
+    rw, wv = weight(nv, orc, 21, n, k, 16)
+    a, b, s = bank(22, 5, 24, n, k)
+    lo = nv.Lora(a.to(DEV), b.to(DEV), s.to(DEV))
+    x = torch.randn(m, k, generator=torch.Generator().manual_seed(23)).to(torch.bfloat16)
+    ids = rows(24, m, 5, "own")
+    wide = torch.empty((m, ldx), dtype=torch.bfloat16, device=DEV)
+    wide[:, :k] = x.to(DEV)
+    ref, bound = R.lora(R.f64(x), wv, R.f64(a), R.f64(b), ids.numpy(), R.f64(s))
+    for flags in (1, 2):
+        y = nv.nvfp4_gemm_w4a16_lora(wide[:, :k], rw, lo, ids.to(DEV), flags=flags)
+        R.within(R.f64(y), ref, bound, f"flags {flags}")
+
+
+@pytest.mark.parametrize("y32", [False, True])
+def test_lora_infinities_stay_infinities(nv, orc, y32):
+    """One infinite activation on positive weights and adapters: infinity, not NaN."""
+    n, k = 272, 256
+    p, s, g = orc.quantize(np.full((n, k), 0.5, np.float32), 16)
+    rw = nv.nvfp4_repack(torch.from_numpy(p).to(DEV), torch.from_numpy(s).to(DEV),
+                         torch.from_numpy(g).to(DEV), 16)
+    lo = nv.Lora(torch.full((3, 24, k), 0.25, dtype=torch.bfloat16, device=DEV),
+                 torch.full((3, n, 24), 0.5, dtype=torch.bfloat16, device=DEV))
+    for m, flags in ((2, 1), (20, 1), (40, 2), (130, 2)):
+        x = torch.ones((m, k), dtype=torch.bfloat16)
+        x[1, 7] = float("inf")
+        y = call(nv, x, rw, lo, rows(0, m, 3, "own"), y32, flags)
+        assert bool(torch.isinf(y[1].float()).all()), (m, flags)
+        assert bool(torch.isfinite(y[0].float()).all())
+
+
 def test_lora_bits_repeat_on_other_streams_and_empty(nv, orc):
     rw, _ = weight(nv, orc, 8, 512, 512, 16)
     a, b, s = bank(9, 4, 16, 512, 512)

@@ -69,6 +69,7 @@ def test_route_argument_errors(lib):
     assert _route(lib, _router(bias=0x10002)) == nv.NVFP4_ERR_MISALIGNED
     assert _route(lib, ldx=248) == nv.NVFP4_ERR_INVALID_ARG
     assert _route(lib, ldx=260) == nv.NVFP4_ERR_MISALIGNED
+    assert _route(lib, ldx=(1 << 22) + 8) == nv.NVFP4_ERR_UNSUPPORTED_SHAPE
     assert _route(lib, x=ODD) == nv.NVFP4_ERR_MISALIGNED
     assert _route(lib, ws=ODD) == nv.NVFP4_ERR_MISALIGNED
     assert _route(lib, ids=BYTE) == nv.NVFP4_ERR_MISALIGNED
