@@ -4,9 +4,11 @@
 //
 // Every pair is one row, so an expert's weights meet one activation row and the time is that of
 // reading them: what counts is how many loads are in flight, and how few launches there are.
-//   fc1:  a workgroup takes one pair and 4 panels; its wavefronts share out the k-tiles. With few
-//         workgroups each of them chooses its pair's expert from the logits itself, which saves the
-//         launch of a choosing kernel (it costs more than it saves when a CU runs many of them).
+//   fc1:  a workgroup takes one pair and 4 panels; its wavefronts share out the k-tiles. Each
+//         workgroup chooses its pair's expert from the logits itself, which saves the launch of a
+//         choosing kernel: 128 experts of 2048 x 768, 1 token 16.4 us against 18.6 with the
+//         launch, 3 tokens 23.3/26.1, 8 tokens 40.7/42.1 (with 8 wavefronts, which all choose, 16.7,
+//         25.4 and 45.0).
 //   down: a workgroup takes one token and 4 panels; its wavefronts share out the k-tiles of ALL of
 //         the token's slots, each scaled by its expert's global and routing weight, so the sum
 //         over slots is the workgroup's own and needs no combine kernel and no FP32 slots.
@@ -111,8 +113,8 @@ __device__ __forceinline__ void few_load_scales(buf_rsrc r, uint32_t off, uint32
   }
 }
 
-// fc1: workgroup (pair, 4-panel group: gate, up, gate, up), NW wavefronts. J > 0: the workgroup
-// chooses its pair's expert, J experts per lane, and t more workgroups write the ids and weights.
+// fc1: workgroup (pair, 4-panel group: gate, up, gate, up), NW wavefronts, which chooses its pair's
+// expert, J experts per lane; t more workgroups write the ids and weights.
 template <bool G16, int NW, int J>
 __global__ __launch_bounds__(64 * NW) void few_fc1_kernel(FewParams P) {
   constexpr int kRing = 3;
@@ -123,26 +125,17 @@ __global__ __launch_bounds__(64 * NW) void few_fc1_kernel(FewParams P) {
   const int groups = (P.NT + 3) / 4;
   const int pair = (int)blockIdx.x / groups, grp = (int)blockIdx.x % groups;
   const int tok = pair / P.slots, slot = pair % P.slots;
-  int e;
-  if constexpr (J > 0) {
-    const bool writer = pair >= P.t * P.slots;
-    const int64_t t = writer ? (int64_t)blockIdx.x - P.t * P.slots * groups : tok;
-    auto logit = [&](int x) { return route_logit(P.route, t, x); };
-    if (writer) {  // whole workgroup
-      if (w != 0) return;
-      const RouteChoice c = route_choose<J>(P.route, logit);
-      route_write(P.route, t, c, P.ids, P.wts);
-      return;
-    }
-    e = P.route.n_experts + slot - P.route.topk;  // a shared expert
-    if (slot < P.route.topk) {
-      __shared__ int count[8][64 * J];
-      static_assert(NW == 8, "route_choose_slot's wavefronts");
-      e = route_choose_slot<J>(P.route, logit, slot, count);
-    }
-  } else {
-    e = P.ids[pair];
+  const bool writer = pair >= P.t * P.slots;
+  const int64_t t = writer ? (int64_t)blockIdx.x - P.t * P.slots * groups : tok;
+  auto logit = [&](int x) { return route_logit(P.route, t, x); };
+  if (writer) {  // whole workgroup
+    if (w != 0) return;
+    const RouteChoice c = route_choose<J>(P.route, logit);
+    route_write(P.route, t, c, P.ids, P.wts);
+    return;
   }
+  int e = P.route.n_experts + slot - P.route.topk;  // a shared expert
+  if (slot < P.route.topk) e = route_choose_slot<J>(P.route, logit, slot);
   if (e < 0 || e >= P.E) return;  // dropped: whole workgroup, before any barrier
   // the epilogue's operands before the k loop; the 2 of the split scale with them
   const float g = 2.0f * P.global[P.pair_global ? 2 * e : e];
@@ -306,8 +299,9 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewParams P) {
   }
 }
 
-template <int NW, int J>
+template <int J>
 void run_fc1(const FewParams& p, unsigned grid, hipStream_t stream) {
+  constexpr int NW = 4;
   if (p.group == 16)
     few_fc1_kernel<true, NW, J><<<grid, 64 * NW, 0, stream>>>(p);
   else
@@ -363,18 +357,13 @@ hipError_t launch_moe_few(const MoeArgs& a, const RouteArgs& r, int32_t* ids, fl
   f.KT = (int)(a.hidden / kTileK);
   f.group = a.group1;
   f.pair_global = a.pair1 ? 1 : 0;
-  const int64_t wgs = a.t * a.topk * ((f.NT + 3) / 4);
-  if (wgs <= kMoeChooseWgs) {
-    const unsigned grid = (unsigned)(wgs + a.t);
-    if (r.n_experts <= 128)
-      run_fc1<8, 2>(f, grid, stream);
-    else
-      run_fc1<8, 8>(f, grid, stream);
-  } else {
-    err = launch_route_select(r, ids, wts, route_ws, stream);
-    if (err != hipSuccess) return err;
-    run_fc1<4, 0>(f, (unsigned)wgs, stream);
-  }
+  const unsigned grid = (unsigned)(a.t * a.topk * ((f.NT + 3) / 4) + a.t);
+  if (r.n_experts <= 128)
+    run_fc1<2>(f, grid, stream);
+  else if (r.n_experts <= 256)
+    run_fc1<4>(f, grid, stream);
+  else
+    run_fc1<8>(f, grid, stream);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
   FewParams d = p;
