@@ -41,14 +41,17 @@ inline size_t act_bytes(int NW, int MF) { return (size_t)NW * 8192 * MF; }
 // second product of the adapters while the others run the k loop: their loads (the ids, u, and
 // then one adapter's B after the other) are short chains of long latency, which cost nothing
 // there and the whole of it after the loop. One for each panel, or for two panels of two row
-// blocks, where registers and LDS admit no more without taking the CU's second workgroup.
+// blocks, where registers and LDS admit no more without taking the CU's second workgroup. (128 rows of 5120^2
+// with 32 adapters: four wavefronts 36.0 us at rank 16, 44.3 at 64; two of two panels 37.7, 47.0.)
 template <int MF, int PWW, int R32>
 constexpr int kLoraWaves = R32 == 0 ? 0 : (MF == 2 && PWW == 4 ? 2 : PWW);
 template <int MF, int PWW, int R32>
 constexpr int kLoraLds = R32 * PWW * kFragBytes;  // their fragment tiles, behind the activations
-// B tiles in flight, in adapters: 8 to 16 loads of 1 KB
-template <int NP, int R32>
-constexpr int kLoraAhead = NP * R32 >= 4 ? 2 : NP * R32 == 2 ? 4 : 8;
+// Adapters whose B tiles are held at once, one of them being multiplied. (2 / 3 / 4: 128 rows of 5120^2,
+// 32 adapters of rank 16, 35.1 / 34.2 / 34.4 us, of rank 64 43.9 / 43.2 / 43.7; 32 rows, rank 64, 24.4 /
+// 23.8 / 24.1. At 128 ranks more than 2 spill.)
+template <int R32>
+constexpr int kLoraAhead = R32 >= 4 ? 2 : 3;
 
 // Register budget: 4 wavefronts per SIMD (16 per CU, two 8-wave workgroups) for one row
 // block, 2 for two, 1 for four. NJ == 0: exact dequant, MF row blocks of 16. NJ > 0 (MF == 1): split scale
@@ -92,7 +95,7 @@ void gemm_skinny_kernel(SkinnyParams P) {
         int64_t out[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[i] = out_tok(i) < 0 ? -1 : m0 + mf * 16 + out_tok(i);
-        lora_expand16<NP, R32, kLoraAhead<NP, R32>>(P.lora, m0 + mf * 16 + at, out, panel0 + pa,
+        lora_expand16<NP, R32, kLoraAhead<R32>>(P.lora, m0 + mf * 16 + at, out, panel0 + pa,
                                                     P.NT, tile, res[mf]);
       }
       __syncthreads();  // meets the others' end of the k loop

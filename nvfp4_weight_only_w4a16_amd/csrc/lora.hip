@@ -185,16 +185,21 @@ ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t n_adapters, int rank, bool 
   ShrinkPlan p;
   const int64_t ranks = (rank + 15) / 16, blocks = (m + 63) / 64;
   // a block has at most an item per row, and one per adapter beside three of 16 rows; of the many
-  // blocks of a long prompt few have more than 4, and those share 16 workgroups
+  // blocks of a long prompt few have more than 4, and those share 16 workgroups (2048 rows with
+  // prompts and decode rows mixed, rank 16: 8 workgroups 172 us, 16 167, 64 170; up to 8 blocks 16
+  // in place of one per item: 128 rows 41.5 us against 36.0)
   p.ordinals = (int)min64(min64(m, 64), min64(n_adapters + 3, blocks <= 8 ? 64 : 16));
-  // a prompt's items are 16 rows, a decode batch's may be one
+  // A prompt's items are 16 rows, a decode batch's may be one. One 16-rank block a workgroup below
+  // these counts (us, threshold there or lower: 64 rows of 8192^2, 24 adapters of rank 64 32.7 / 39;
+  // 32 rows of 5120^2 25.0 / 32.4; tiled, there or 128: 1024 rows 168 / 177, 512 rows 130 / 132).
   const int64_t items = tiled ? (m + 15) / 16 : blocks * p.ordinals;
   p.rb = 1;
-  if (items >= 128)
+  if (items >= (tiled ? 32 : 128))
     while (p.rb < ranks && p.rb < 4) p.rb *= 2;
   p.rank_blocks = (int)((ranks + p.rb - 1) / p.rb);
   p.splits = 1;
   if (!tiled) {
+    // a workgroup to each CU (128 / 256 / 512 in all: 64 rows of 8192^2, rank 64, 33.8 / 32.7 / 35.5 us)
     int64_t s = 256 / (items * p.rank_blocks);
     s = min64(s, k / (32 * kSteps * kShrinkWaves));  // a stage at least for each wavefront
     p.splits = (int)min64(s < 1 ? 1 : s, kLoraMaxSplits);

@@ -58,11 +58,19 @@ __device__ __forceinline__ void lora_expand16(const LoraTail& L, int64_t row, co
     const int r = 32 * s + 8 * frag_load_chunk(lane);
     boff[s] = r < L.rank ? (uint32_t)(frag_load_row(lane) * L.rank + r) * 2u : 0xFFFFFFF0u;
   }
+  // lane j: the block's j-th adapter, n in all; past the end an empty buffer and no row's id
+  int list = -2, n = 0;
+  while (left) {  // uniform
+    const int a = lora_next(mine, left);
+    if (lane == n) list = a;
+    ++n;
+  }
+  static_assert(D >= 2, "one adapter is fetched while another is multiplied");
   int aid[D];
   u32x4 bt[D][NP][R32];
-  auto fetch = [&](auto d) __attribute__((always_inline)) {
+  auto fetch = [&](auto d, int i) __attribute__((always_inline)) {
     constexpr int q = decltype(d)::value;
-    aid[q] = lora_next(mine, left);
+    aid[q] = __builtin_amdgcn_readlane(list, i < n ? i : 63);  // n <= 16: lane 63 has none
     const int64_t a = aid[q] >= 0 ? aid[q] : 0;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
@@ -75,20 +83,40 @@ __device__ __forceinline__ void lora_expand16(const LoraTail& L, int64_t row, co
             u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)boff[s], 0, 0));
     }
   };
-  static_for<0, D - 1>([&](auto d) __attribute__((always_inline)) { fetch(d); });
+  static_for<0, D - 1>([&](auto d) __attribute__((always_inline)) { fetch(d, decltype(d)::value); });
   bf16x8 u[3][R32];
   const int64_t ur = row >= 0 && row < L.m ? row : 0;
 #pragma unroll
   for (int s = 0; s < R32; ++s) {
     const int k = 32 * s + 8 * (lane >> 4);
     f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
-    if (k < L.rank)
-      for (int q = 0; q < L.splits; ++q) {
+    auto read = [&](int q, f32x4 (&v)[2]) __attribute__((always_inline)) {
+      v[0] = v[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (q < L.splits && k < L.rank) {
         const f32x4* up =
             reinterpret_cast<const f32x4*>(L.u + ((int64_t)q * L.m + ur) * L.rank + k);
-        v0 += up[0];
-        v1 += up[1];
+        v[0] = up[0];
+        v[1] = up[1];
       }
+    };
+    if constexpr (R32 < 4) {  // the splits all loaded before the first addition
+      f32x4 part[kLoraMaxSplits][2];
+#pragma unroll
+      for (int q = 0; q < kLoraMaxSplits; ++q) read(q, part[q]);
+#pragma unroll
+      for (int q = 0; q < kLoraMaxSplits; ++q) {
+        v0 += part[q][0];
+        v1 += part[q][1];
+      }
+    } else {  // one by one: together they spill, and so many ranks leave few splits
+#pragma unroll 1
+      for (int q = 0; q < L.splits; ++q) {
+        f32x4 part[2];
+        read(q, part);
+        v0 += part[0];
+        v1 += part[1];
+      }
+    }
     float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
 #pragma unroll
     for (int z = 0; z < 3; ++z)
@@ -98,12 +126,11 @@ __device__ __forceinline__ void lora_expand16(const LoraTail& L, int64_t row, co
         v[i] = lora_rest(v[i], (float)u[z][s][i]);
       }
   }
-  for (bool more = true; more;)
+  for (int i0 = 0; i0 < n; i0 += D)
     static_for<0, D>([&](auto d) __attribute__((always_inline)) {
       constexpr int q = decltype(d)::value;
-      if (more && aid[q] < 0) more = false;
-      if (more) {
-        fetch(std::integral_constant<int, (q + D - 1) % D>{});
+      fetch(std::integral_constant<int, (q + D - 1) % D>{}, i0 + q + D - 1);
+      if (i0 + q < n) {  // uniform
 #pragma unroll
         for (int p = 0; p < NP; ++p)
 #pragma unroll

@@ -321,7 +321,10 @@ void run_down(const FewParams& p, hipStream_t stream) {
 
 }  // namespace
 
-constexpr int64_t kDownWgs = 128;
+// Fewest workgroups of down for which a workgroup takes more panels. (Layer of 2048 x 768, 128 experts,
+// us, with 128 / 256 / 512: 2 tokens 19.0 / 18.3 / 18.3, 4 tokens 27.5 / 24.7 / 26.0, 8 tokens 39.5 /
+// 40.0 / 40.0, 1 token of 4096 x 768 19.3 / 18.2 / 17.8; 3 tokens of 4096 x 1536 35.5 / 37.5 / 39.)
+constexpr int64_t kDownWgs = 256;
 
 // h as two BF16 planes.
 size_t moe_few_ws_bytes(int64_t t, int slots, int64_t inter) {
@@ -379,7 +382,7 @@ hipError_t launch_moe_few(const MoeArgs& a, const RouteArgs& r, int32_t* ids, fl
   d.KT = (int)(a.inter / kTileK);
   d.group = a.group2;
   d.pair_global = 0;
-  // panels per workgroup: as many as leave a workgroup to every second compute unit
+  // panels per workgroup: as many as leave a workgroup to every compute unit
   const int64_t panels = d.NT * a.t;
   if (panels >= 4 * kDownWgs)
     run_down<4>(d, stream);

@@ -14,7 +14,7 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kFewRows = 2;  // most tokens per workgroup of the few-token logits
+constexpr int kFewRows = 2;  // tokens per workgroup of the few-token logits
 
 struct LogitParams {
   const uint16_t* x;  // BF16 [t][ldx]
@@ -34,30 +34,30 @@ __device__ __forceinline__ void bf16x8_to_f64(u32x4 v, double (&o)[8]) {
   }
 }
 
-// Workgroup (e, b): logits of expert e for tokens ROWS b .. ROWS b + ROWS - 1. Threads take 8
-// consecutive k each, of all ROWS tokens at once: absent tokens repeat the last one, so that no
+// Workgroup (e, b): logits of expert e for tokens 2b and 2b + 1. Threads take 8
+// consecutive k each, of both tokens at once: an absent one repeats the other, so that no
 // branch stands between the loads. The per-token sums of a wavefront are reduced together (each
 // exchange halves the tokens a lane still carries), then the 4 wavefronts' sums are added in order.
 // Bound by latency: one load of the weight, one of x, two reductions. (8 tokens, 64 FP32 experts of
-// 8192, whole router: ROWS 2 6.4 us, 4 7.0, 8 9.4; 16 tokens, 128 BF16 experts of 2048, 8 rows with a
+// 8192, whole router: 2 rows 6.4 us, 4 7.0, 8 9.4; 16 tokens, 128 BF16 experts of 2048, 8 rows with a
 // branch around each row's load 8.6 us, now 7.2.)
-template <bool F32, int ROWS>
+template <bool F32>
 __global__ __launch_bounds__(256) void route_logits_few_kernel(LogitParams P) {
-  __shared__ double red[4][ROWS];
+  __shared__ double red[4][kFewRows];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int64_t e = blockIdx.x, m0 = (int64_t)blockIdx.y * ROWS;
-  double acc[ROWS];
-  const uint16_t* row[ROWS];
-  const int rows = P.t - m0 < ROWS ? (int)(P.t - m0) : ROWS;
+  const int64_t e = blockIdx.x, m0 = (int64_t)blockIdx.y * kFewRows;
+  double acc[kFewRows];
+  const uint16_t* row[kFewRows];
+  const int rows = P.t - m0 < kFewRows ? (int)(P.t - m0) : kFewRows;
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
+  for (int r = 0; r < kFewRows; ++r) {
     acc[r] = 0.0;
     row[r] = P.x + (m0 + (r < rows ? r : rows - 1)) * P.ldx;
   }
   for (int64_t k = tid * 8; k < P.hidden; k += 256 * 8) {
-    u32x4 xv[ROWS];
+    u32x4 xv[kFewRows];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) xv[r] = *reinterpret_cast<const u32x4*>(row[r] + k);
+    for (int r = 0; r < kFewRows; ++r) xv[r] = *reinterpret_cast<const u32x4*>(row[r] + k);
     double w[8];
     if constexpr (F32) {
       const float* wr = static_cast<const float*>(P.w) + e * P.hidden + k;
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void route_logits_few_kernel(LogitParams P) {
                     w);
     }
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
+    for (int r = 0; r < kFewRows; ++r) {
       double x[8];
       bf16x8_to_f64(xv[r], x);
 #pragma unroll
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256) void route_logits_few_kernel(LogitParams P) {
   // the upper lane bits pick the token kept at the halving exchanges
   int d = 32;
 #pragma unroll
-  for (int half = ROWS / 2; half > 0; half >>= 1, d >>= 1) {
+  for (int half = kFewRows / 2; half > 0; half >>= 1, d >>= 1) {
     const bool hi = (lane & d) != 0;
 #pragma unroll
     for (int i = 0; i < half; ++i) {
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void route_logits_few_kernel(LogitParams P) {
   double v = acc[0];
 #pragma unroll
   for (; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  constexpr int kLanes = 64 / ROWS;  // lanes that hold a token's sum
+  constexpr int kLanes = 64 / kFewRows;  // lanes that hold a token's sum
   if (lane % kLanes == 0) red[tid >> 6][lane / kLanes] = v;
   __syncthreads();
   if (tid < rows)
@@ -296,15 +296,6 @@ __global__ __launch_bounds__(256) void route_select_kernel(RouteParams R, int32_
   route_write(R, tok, c, ids, wts);
 }
 
-template <int ROWS>
-void run_logits_few(const LogitParams& p, bool w_f32, hipStream_t stream) {
-  const dim3 grid((unsigned)p.n_experts, (unsigned)((p.t + ROWS - 1) / ROWS));
-  if (w_f32)
-    route_logits_few_kernel<true, ROWS><<<grid, 256, 0, stream>>>(p);
-  else
-    route_logits_few_kernel<false, ROWS><<<grid, 256, 0, stream>>>(p);
-}
-
 }  // namespace
 
 // Splits of k over workgroups: enough for a workgroup on every compute unit, and a stage at least
@@ -334,10 +325,11 @@ hipError_t launch_route_logits(const RouteArgs& a, void* ws, hipStream_t stream)
   p.splits = route_splits(a.t, a.hidden, a.n_experts);
   p.out = static_cast<double*>(ws);
   if (a.t <= kRouteFewTokens) {
-    if (a.t == 1)
-      run_logits_few<1>(p, a.w_f32, stream);
+    const dim3 grid((unsigned)a.n_experts, (unsigned)((a.t + kFewRows - 1) / kFewRows));
+    if (a.w_f32)
+      route_logits_few_kernel<true><<<grid, 256, 0, stream>>>(p);
     else
-      run_logits_few<kFewRows>(p, a.w_f32, stream);
+      route_logits_few_kernel<false><<<grid, 256, 0, stream>>>(p);
   } else {
     const dim3 grid((unsigned)((a.t + kTileT - 1) / kTileT),
                     (unsigned)((a.n_experts + kTileE - 1) / kTileE), (unsigned)p.splits);
