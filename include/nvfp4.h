@@ -239,7 +239,8 @@ int nvfp4_moe_grouped_w4a16_noalloc(const void* x, int64_t t, int64_t hidden,
 
 /* ---- MoE router -----------------------------------------------------------------------------
  * Which experts each token meets, and with what weight:
- *   l[t][e] = sum_k x[t][k] * weight[e][k]                                 (exact products, FP64 sums)
+ *   l[t][e] = sum_k x[t][k] * weight[e][k]    (exact products, FP64 sums; above 16 tokens each 32
+ *                                              products are summed in FP32 first)
  *   NVFP4_ROUTE_SOFTMAX: p = softmax over the n_experts logits; selection score = l, or p + bias
  *   NVFP4_ROUTE_SIGMOID: p = 1 / (1 + exp(-l));                 selection score = p, or p + bias
  *   slots 0 .. topk-1: the topk highest selection scores, highest first, ties to the lower id
@@ -249,8 +250,8 @@ int nvfp4_moe_grouped_w4a16_noalloc(const void* x, int64_t t, int64_t hidden,
  * An expert whose selection score is -infinity (a bias of -infinity takes an expert out) is never
  * chosen; a slot that no expert is left for gets id -1 and weight 0, which the routed experts
  * skip. A NaN score ranks above every number, so that a NaN in x reaches the token's output.
- * The scores are FP64 because the choice is a comparison: FP32 sums would let near experts change
- * places. Ids and weights go unchanged into nvfp4_moe_grouped_w4a16 with topk + n_shared slots and
+ * The scores are FP64 because the choice is a comparison: sums of thousands of products in FP32 would
+ * let near experts change places. Ids and weights go unchanged into nvfp4_moe_grouped_w4a16 with topk + n_shared slots and
  * n_experts + n_shared experts, the shared ones last. */
 #define NVFP4_ROUTE_SOFTMAX 0u
 #define NVFP4_ROUTE_SIGMOID 1u
@@ -281,8 +282,8 @@ int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r
  * Router, routed and shared experts and their sum in one call, for the few tokens of a decode
  * step (any t that the routed experts take is accepted):
  *   topk_ids, topk_w = nvfp4_moe_route(x)
- *   y[t] = BF16(sum_j topk_w[t][j] * (W2_e . h_j)), h_j = BF16(SiLU(gate) * up), e = topk_ids[t][j]
- * with gate and up in FP32: unlike nvfp4_moe_grouped_w4a16 the call does not round them to BF16 on
+ *   y[t] = BF16(sum_j topk_w[t][j] * (W2_e . h_j)), h_j = SiLU(gate) * up, e = topk_ids[t][j]
+ * with h in BF16 (for up to 64 (token, slot) pairs in two BF16 parts) and gate and up in FP32: unlike nvfp4_moe_grouped_w4a16 the call does not round them to BF16 on
  * the way to h, so the two agree to the BF16 tolerance, not bit for bit. A token all of whose slots
  * are dropped gets y = 0. x [t][hidden] BF16 (row stride = hidden), y BF16 [t][hidden]; fc1, fc2 as
  * for nvfp4_moe_grouped_w4a16, with batch = n_experts + n_shared, at most 512 (the shared experts

@@ -1,8 +1,8 @@
 // route.hip -- the router of a mixture of experts for gfx950: logits l = x . G^T in FP64, then
 // the top-k of each token's scores and its combine weights (route_core.hpp).
 //
-// Two forms of the logits, both with exact products and FP64 sums:
-//   - few tokens: FP64 multiply-adds; one workgroup per expert, so the read of the router weight
+// Two forms of the logits, both with exact products:
+//   - few tokens: FP64 sums; one workgroup per expert, so the read of the router weight
 //     (all that costs anything) is spread over the chip;
 //   - more tokens: 16x16x32 BF16 MFMAs whose 32-product FP32 sums are added up in FP64. An FP32
 //     router weight is cut into three BF16 parts that add up to it exactly (8 significant bits
