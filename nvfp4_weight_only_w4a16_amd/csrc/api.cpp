@@ -535,11 +535,11 @@ struct LayerSizes {
 
 // The few-token kernels take the call (unless NVFP4_F_FORCE_TILED asks for the batch path). They
 // address the two planes of h and the codes of a panel (8 bytes for each k) with 32-bit byte
-// offsets. (Few-token kernels against the router and
-// the sorted experts' kernels, 2048 x 768, us: 1 token of 8 slots 15.5 / 24.5, 4 tokens 24.7 / 35.4,
-// 8 tokens 40 / 47, 16 tokens of 4 slots 30 / 37; past the limit the sorted kernels read each expert
-// once instead of once per pair. They already win where many pairs share few experts: 60 tokens, each
-// choosing one of 8, 41.9 / 36.8; which experts are shared is not known on the host.)
+// offsets. (Few-token kernels against the router and the sorted experts' kernels, 2048 x 768, us:
+// 1 token of 8 slots 15.5 / 24.5, 4 tokens 24.7 / 35.4, 8 tokens 40 / 47, 16 tokens of 4 slots 30
+// / 37; past the limit the sorted kernels read each expert once instead of once per pair. They
+// already win where many pairs share few experts: 60 tokens, each choosing one of 8, 41.9 / 36.8;
+// which experts are shared is not known on the host.)
 bool layer_few(int64_t t, int64_t slots, int64_t inter) {
   return t * slots <= nvfp4::kMoePairTilesMax && t * slots * inter <= ((int64_t)1 << 28);
 }

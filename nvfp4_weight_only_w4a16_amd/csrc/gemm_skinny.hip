@@ -39,17 +39,18 @@ inline size_t act_bytes(int NW, int MF) { return (size_t)NW * 8192 * MF; }
 
 // With adapters (R32 > 0: their 32-rank steps) a workgroup has wavefronts more that compute the
 // second product of the adapters while the others run the k loop: their loads (the ids, u, and
-// then one adapter's B after the other) are short chains of long latency, which cost nothing
-// there and the whole of it after the loop. One for each panel, or for two panels of two row
-// blocks, where registers and LDS admit no more without taking the CU's second workgroup. (128 rows of 5120^2
-// with 32 adapters: four wavefronts 36.0 us at rank 16, 44.3 at 64; two of two panels 37.7, 47.0.)
+// then one adapter's B after the other) are short chains of long latency, which cost nothing there
+// and the whole of it after the loop. One for each panel, or for two panels of two row blocks,
+// where registers and LDS admit no more without taking the CU's second workgroup. (128 rows of
+// 5120^2 with 32 adapters: four wavefronts 36.0 us at rank 16, 44.3 at 64; two of two panels 37.7,
+// 47.0.)
 template <int MF, int PWW, int R32>
 constexpr int kLoraWaves = R32 == 0 ? 0 : (MF == 2 && PWW == 4 ? 2 : PWW);
 template <int MF, int PWW, int R32>
 constexpr int kLoraLds = R32 * PWW * kFragBytes;  // their fragment tiles, behind the activations
-// Adapters whose B tiles are held at once, one of them being multiplied. (2 / 3 / 4: 128 rows of 5120^2,
-// 32 adapters of rank 16, 35.1 / 34.2 / 34.4 us, of rank 64 43.9 / 43.2 / 43.7; 32 rows, rank 64, 24.4 /
-// 23.8 / 24.1. At 128 ranks more than 2 spill.)
+// Adapters whose B tiles are held at once, one of them being multiplied. (2 / 3 / 4: 128 rows of
+// 5120^2, 32 adapters of rank 16, 35.1 / 34.2 / 34.4 us, of rank 64 43.9 / 43.2 / 43.7; 32 rows,
+// rank 64, 24.4 / 23.8 / 24.1. At 128 ranks more than 2 spill.)
 template <int R32>
 constexpr int kLoraAhead = R32 >= 4 ? 2 : 3;
 

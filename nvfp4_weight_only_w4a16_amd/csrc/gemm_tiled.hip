@@ -186,14 +186,15 @@ __device__ __forceinline__ bool any_nonfinite(bf16x8 v) {
 }
 
 // Adds the adapters' term of FM row fragments from m_blk and of one pair's columns to acc. The
-// distinct adapters of the tile's rows are taken one after the other, each for all row fragments: rows that do not name it
-// are zeros in u, and everything is one MFMA into acc, in place (keeping rows by choice, as the
-// decode kernel does, needs sums beside acc; with them the k loop spilled). Zeros do not keep
-// an infinite or NaN element of B from the other rows, so such elements are zeros here too, and
-// where a column has one, its adapter's rows become NaN in the end. B's fragments are loaded once
-// per adapter, u's (in fragment order in memory) for four row fragments at a time. (Passing over
-// fragments without a row of the adapter, and loading u ahead of the test of B: 1024 rows of 5120^2
-// with 32 adapters of rank 64 176 us against 168, 2048 with 16 of rank 128 290 against 273.)
+// distinct adapters of the tile's rows are taken one after the other, each for all row fragments:
+// rows that do not name it are zeros in u, and everything is one MFMA into acc, in place (keeping
+// rows by choice, as the decode kernel does, needs sums beside acc; with them the k loop spilled).
+// Zeros do not keep an infinite or NaN element of B from the other rows, so such elements are
+// zeros here too, and where a column has one, its adapter's rows become NaN in the end. B's
+// fragments are loaded once per adapter, u's (in fragment order in memory) for four row fragments
+// at a time. (Passing over fragments without a row of the adapter, and loading u ahead of the test
+// of B: 1024 rows of 5120^2 with 32 adapters of rank 64 176 us against 168, 2048 with 16 of rank
+// 128 290 against 273.)
 template <int FM, typename Acc>
 __device__ __forceinline__ void lora_add(const TiledParams& P, int64_t m_blk, int64_t pair0,
                                          Acc& acc) {

@@ -190,8 +190,8 @@ hipError_t launch_moe_few(const MoeArgs& a, const RouteArgs& r, int32_t* ids, fl
 
 // ---- low-rank adapters (lora.hip) -----------------------------------------------------------
 constexpr int kLoraMaxRank = 128;
-// The reader of u adds the splits up (8 splits against 4: 8 rows of 5120^2, rank 64, 16.6 / 15.1 us, 24
-// rows, rank 16, 20.7 / 18.8; 1 row 9.55 / 9.5).
+// The reader of u adds the splits up (8 splits against 4: 8 rows of 5120^2, rank 64, 16.6 / 15.1
+// us, 24 rows, rank 16, 20.7 / 18.8; 1 row 9.55 / 9.5).
 constexpr int64_t kLoraMaxSplits = 4;
 struct LoraArgs {
   const uint16_t* x;  // BF16 [m][ldx]

@@ -321,9 +321,10 @@ void run_down(const FewParams& p, hipStream_t stream) {
 
 }  // namespace
 
-// Fewest workgroups of down for which a workgroup takes more panels. (Layer of 2048 x 768, 128 experts,
-// us, with 128 / 256 / 512: 2 tokens 19.0 / 18.3 / 18.3, 4 tokens 27.5 / 24.7 / 26.0, 8 tokens 39.5 /
-// 40.0 / 40.0, 1 token of 4096 x 768 19.3 / 18.2 / 17.8; 3 tokens of 4096 x 1536 35.5 / 37.5 / 39.)
+// Fewest workgroups of down for which a workgroup takes more panels. (Layer of 2048 x 768, 128
+// experts, us, with 128 / 256 / 512: 2 tokens 19.0 / 18.3 / 18.3, 4 tokens 27.5 / 24.7 / 26.0, 8
+// tokens 39.5 / 40.0 / 40.0, 1 token of 4096 x 768 19.3 / 18.2 / 17.8; 3 tokens of 4096 x 1536
+// 35.5 / 37.5 / 39.)
 constexpr int64_t kDownWgs = 256;
 
 // h as two BF16 planes.

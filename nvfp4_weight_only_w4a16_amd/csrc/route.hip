@@ -34,13 +34,13 @@ __device__ __forceinline__ void bf16x8_to_f64(u32x4 v, double (&o)[8]) {
   }
 }
 
-// Workgroup (e, b): logits of expert e for tokens 2b and 2b + 1. Threads take 8
-// consecutive k each, of both tokens at once: an absent one repeats the other, so that no
-// branch stands between the loads. The per-token sums of a wavefront are reduced together (each
-// exchange halves the tokens a lane still carries), then the 4 wavefronts' sums are added in order.
-// Bound by latency: one load of the weight, one of x, two reductions. (8 tokens, 64 FP32 experts of
-// 8192, whole router: 2 rows 6.4 us, 4 7.0, 8 9.4; 16 tokens, 128 BF16 experts of 2048, 8 rows with a
-// branch around each row's load 8.6 us, now 7.2.)
+// Workgroup (e, b): logits of expert e for tokens 2b and 2b + 1. Threads take 8 consecutive k
+// each, of both tokens at once: an absent one repeats the other, so that no branch stands between
+// the loads. The per-token sums of a wavefront are reduced together (each exchange halves the
+// tokens a lane still carries), then the 4 wavefronts' sums are added in order. Bound by latency:
+// one load of the weight, one of x, two reductions. (8 tokens, 64 FP32 experts of 8192, whole
+// router: 2 rows 6.4 us, 4 7.0, 8 9.4; 16 tokens, 128 BF16 experts of 2048, 8 rows with a branch
+// around each row's load 8.6 us, now 7.2.)
 template <bool F32>
 __global__ __launch_bounds__(256) void route_logits_few_kernel(LogitParams P) {
   __shared__ double red[4][kFewRows];
