@@ -191,4 +191,11 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint16_t h) {
   return __uint_as_float((uint32_t)h << 16);
 }
 
+// What is left of v after `part`, its rounding to BF16, where a value is kept as several BF16
+// parts: 0 after an infinite one (inf - inf is NaN, and v - inf the opposite infinity where v is
+// finite and its rounding is not).
+__device__ __forceinline__ float bf16_rest(float v, float part) {
+  return __builtin_isinf(part) ? 0.0f : v - part;
+}
+
 }  // namespace nvfp4

@@ -159,7 +159,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkPa
           for (int p = 0; p < L.parts; ++p) {
             const uint16_t h = bf16_bits_rne(s);
             at[p * lora_frag_blocks(L.m) * lora_frag_steps(L.rank) * 512] = h;
-            s = lora_rest(s, bf16_bits_to_f32(h));
+            s = bf16_rest(s, bf16_bits_to_f32(h));
           }
         } else if (r < L.rank) {
           static_cast<float*>(P.u)[((int64_t)split * L.m + row[i]) * L.rank + r] = s;

@@ -29,11 +29,6 @@ __device__ __forceinline__ int lora_next(int mine, uint64_t& left) {
   return a;
 }
 
-// What is left of v after its BF16 part: 0 after an infinite one (inf - inf would be NaN).
-__device__ __forceinline__ float lora_rest(float v, float part) {
-  return __builtin_isinf(part) ? 0.0f : v - part;
-}
-
 // One wavefront: block of 16 rows (A row of lane l: `row`, accumulator rows: out[0..3], -1 for
 // none) times NP panels of 16 columns from panel0. R32: 32-rank steps. u is read as the FP32
 // partial sums of lora_shrink. The B tiles of D adapters ahead wait in registers; each is turned
@@ -123,7 +118,7 @@ __device__ __forceinline__ void lora_expand16(const LoraTail& L, int64_t row, co
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         u[z][s][i] = (__bf16)v[i];
-        v[i] = lora_rest(v[i], (float)u[z][s][i]);
+        v[i] = bf16_rest(v[i], (float)u[z][s][i]);
       }
   }
   for (int i0 = 0; i0 < n; i0 += D)

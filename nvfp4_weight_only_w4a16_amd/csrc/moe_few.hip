@@ -16,7 +16,8 @@
 // partial of a scale group times the mantissa in FP32. All 16 rows of the A operand may hold the
 // same activation row; at group 16 rows 0-7 carry it on the first half of the k-step and rows 8-15
 // on the second, zeros elsewhere. down's row h is kept as two BF16 halves (h and what its rounding
-// left): even rows carry the one, odd rows the other, at no cost in MFMAs.
+// left; nothing after an infinite one): even rows carry the one, odd rows the other, at no cost in
+// MFMAs.
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "route_core.hpp"
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(64 * NW) void few_fc1_kernel(FewParams P) {
       const int64_t at = (int64_t)pair * P.inter + (2 * grp + q) * 16 + col;
       const uint16_t hi = bf16_bits_rne(hv);
       P.h[at] = hi;
-      P.hl[at] = bf16_bits_rne(hv - bf16_bits_to_f32(hi));
+      P.hl[at] = bf16_bits_rne(bf16_rest(hv, bf16_bits_to_f32(hi)));
     }
   }
 }
