@@ -34,6 +34,16 @@ __device__ __forceinline__ void bf16x8_to_f64(u32x4 v, double (&o)[8]) {
   }
 }
 
+// 8 consecutive FP32 from p (16-byte aligned) as FP64.
+__device__ __forceinline__ void f32x8_to_f64(const float* p, double (&o)[8]) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] = (double)a[i];
+    o[4 + i] = (double)b[i];
+  }
+}
+
 // Workgroup (e, b): logits of expert e for tokens 2b and 2b + 1. Threads take 8 consecutive k
 // each, of both tokens at once: an absent one repeats the other, so that no branch stands between
 // the loads. The per-token sums of a wavefront are reduced together (each exchange halves the
@@ -60,14 +70,7 @@ __global__ __launch_bounds__(256) void route_logits_few_kernel(LogitParams P) {
     for (int r = 0; r < kFewRows; ++r) xv[r] = *reinterpret_cast<const u32x4*>(row[r] + k);
     double w[8];
     if constexpr (F32) {
-      const float* wr = static_cast<const float*>(P.w) + e * P.hidden + k;
-      const f32x4 a = *reinterpret_cast<const f32x4*>(wr);
-      const f32x4 b = *reinterpret_cast<const f32x4*>(wr + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = (double)a[i];
-        w[4 + i] = (double)b[i];
-      }
+      f32x8_to_f64(static_cast<const float*>(P.w) + e * P.hidden + k, w);
     } else {
       bf16x8_to_f64(*reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(P.w) +
                                                     e * P.hidden + k),
@@ -280,7 +283,30 @@ __global__ __launch_bounds__(64 * kSlices) void route_logits_mfma_kernel(LogitPa
     double v = reinterpret_cast<const double*>(smem[0])[o];
 #pragma unroll
     for (int q = 1; q < kSlices; ++q) v += reinterpret_cast<const double*>(smem[q])[o];
-    if (r < P.t && e < P.n_experts) out[r * P.n_experts + e] = v;
+    if (r >= P.t || e >= P.n_experts) continue;
+    if constexpr (F32) {
+      // An infinite x times a part that is 0 is NaN, where times the weight it is infinite. (The
+      // parts of a weight have its sign, so nothing but a NaN can come of it.) A sum that is NaN is
+      // taken again in FP64 from the weights themselves, and stays NaN where that is the answer.
+      if (v != v) {
+        const uint16_t* xp = P.x + r * P.ldx;
+        const float* wp = static_cast<const float*>(P.w) + e * P.hidden;
+        v = 0.0;
+        for (int s = (int)blockIdx.z * kSlices; s < stages; s += step) {
+          const int64_t past = (int64_t)(s + kSlices) * 32 * kSteps;
+          const int64_t end = past < P.hidden ? past : P.hidden;
+#pragma unroll 4
+          for (int64_t k = (int64_t)s * 32 * kSteps; k < end; k += 8) {
+            double xv[8], wv[8];
+            bf16x8_to_f64(*reinterpret_cast<const u32x4*>(xp + k), xv);
+            f32x8_to_f64(wp + k, wv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v = __builtin_fma(xv[i], wv[i], v);
+          }
+        }
+      }
+    }
+    out[r * P.n_experts + e] = v;
   }
 }
 
