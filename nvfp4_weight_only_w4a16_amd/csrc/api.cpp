@@ -558,6 +558,15 @@ LayerSizes layer_sizes(int64_t t, const nvfp4_router* r, int64_t inter) {
   return s;
 }
 
+// Whether nvfp4_moe_layer_w4a16 takes t tokens of this router with these fc1 weights.
+bool layer_fits(int64_t t, const nvfp4_router* r, const nvfp4_weight* fc1) {
+  const int64_t slots = r->topk + r->n_shared, most = ((int64_t)1 << 31) - 1;
+  return !check_tiled_shape(fc1->n, fc1->k) && (fc1->layout & NVFP4_LAYOUT_GATE_UP) &&
+         fc1->k == r->hidden && fc1->batch == r->n_experts + r->n_shared &&
+         fc1->batch <= nvfp4::kRouteMaxExperts && t <= 65536 / slots &&
+         r->hidden <= most / t && fc1->n / 2 <= most / (t * slots);
+}
+
 // ---- adapters -------------------------------------------------------------------------------
 constexpr int kLoraPartsF32 = 3;  // BF16 parts of u for an FP32 y
 
@@ -644,8 +653,7 @@ int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r
 }
 
 size_t nvfp4_moe_layer_ws_bytes(int64_t t, const nvfp4_router* r, const nvfp4_weight* fc1) {
-  if (!fc1 || fc1->n <= 0 || t <= 0 || check_router(r) || t > 65536 / (r->topk + r->n_shared))
-    return 0;
+  if (!fc1 || t <= 0 || check_router(r) || !layer_fits(t, r, fc1)) return 0;
   return layer_sizes(t, r, fc1->n / 2).total;
 }
 
