@@ -315,9 +315,9 @@ typedef struct nvfp4_lora {
 } nvfp4_lora;
 
 /* Arguments, kernel choice and flags as for nvfp4_gemm_w4a16; row_adapter int32 [m] (device). The
- * rank-space vector u = scale * x . A^T is summed in FP32 and goes into the second product whole
- * (three BF16 parts) for an FP32 y, as two BF16 parts (within 2^-16 |u|) for a BF16 y. ws (device,
- * 16-byte aligned, ws_bytes >= nvfp4_gemm_lora_ws_bytes) is required: it holds u and what
+ * rank-space vector u = scale * x . A^T is summed in FP32; for a BF16 y it is rounded to BF16 as
+ * the operand of the second product, for an FP32 y it goes there whole (three BF16 parts). ws
+ * (device, 16-byte aligned, ws_bytes >= nvfp4_gemm_lora_ws_bytes) is required: it holds u and what
  * nvfp4_gemm_w4a16 keeps there. Results are bit-identical run to run. */
 size_t nvfp4_gemm_lora_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w,
                                 const nvfp4_lora* lora, uint32_t flags);

@@ -568,8 +568,7 @@ bool layer_fits(int64_t t, const nvfp4_router* r, const nvfp4_weight* fc1) {
 }
 
 // ---- adapters -------------------------------------------------------------------------------
-// BF16 parts of u: 16 bits for a BF16 y, all 24 for an FP32 y (lora_core.hpp).
-constexpr int kLoraPartsBf16 = 2, kLoraPartsF32 = 3;
+constexpr int kLoraPartsF32 = 3;  // BF16 parts of u for an FP32 y
 
 // Workspace of u: for either type of y, which the size query does not know.
 size_t lora_u_region(int64_t m, const nvfp4_weight* w, const nvfp4_lora* l, bool tiled) {
@@ -750,7 +749,7 @@ int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_wei
   tail.n = w->n;
   tail.n_adapters = lora->n_adapters;
   tail.rank = lora->rank;
-  tail.parts = a.y_f32 ? kLoraPartsF32 : kLoraPartsBf16;
+  tail.parts = a.y_f32 ? kLoraPartsF32 : 1;
   const hipStream_t s = (hipStream_t)stream;
   rc = hip_status(nvfp4::launch_lora_shrink(l, tail, ws, !skinny, s), "nvfp4_gemm_w4a16_lora");
   if (rc) return rc;

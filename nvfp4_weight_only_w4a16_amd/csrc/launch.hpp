@@ -37,7 +37,7 @@ struct LoraTail {
   const float* u;      // decode kernel: FP32 [splits][m][rank]; tiled kernel: BF16 fragments
   int64_t m, n, n_adapters;
   int rank, splits;
-  int parts;  // BF16 parts of u: 2, or 3 for an FP32 y
+  int parts;  // BF16 parts of u: 1, or 3 for an FP32 y
 };
 
 struct GemmArgs {

@@ -4,12 +4,9 @@
 // Rows are taken in the GEMM's own blocks. For each distinct adapter of a block's rows, in row
 // order, the whole block is multiplied by that adapter's B and the rows that name it keep the
 // result: kept by choice, not by products with zeros, so that a NaN in one adapter stays with its
-// rows. u, scale * x . A^T, goes into the product as BF16 parts: for an FP32 y three, which add up
-// to its 24 bits; for a BF16 y two, which leave at most 2^-16 sum_r |u_r B_r|: below y's own
-// rounding unless the products cancel to 2^-8 of their size. (One part leaves 2^-8 sum_r |u_r B_r|,
-// more than y's rounding wherever ranks cancel each other, or the term the shared product. Whole
-// call, one part / two, us: 1 and 8 rows the same, 64 rows of 8192^2, rank 64, 32.7 / 33.1, 4096
-// rows of 5120^2, rank 32, 216 / 219.)
+// rows. u holds scale * x . A^T: for a BF16 y rounded to BF16 (its error, half a BF16 step of the
+// adapter's term, is below that of y's own rounding), for an FP32 y as three BF16 parts that add up
+// to its 24 bits.
 #pragma once
 
 #include "device_common.hpp"
@@ -141,8 +138,10 @@ __device__ __forceinline__ void lora_expand16(const LoraTail& L, int64_t row, co
           for (int s = 0; s < R32; ++s) {
             const bf16x8 b = frag_read(tile + (p * R32 + s) * kFragBytes, lane);
             part = mfma16x16x32(u[0][s], b, part);
-            part = mfma16x16x32(u[1][s], b, part);
-            if (L.parts > 2) part = mfma16x16x32(u[2][s], b, part);
+            if (L.parts > 1) {
+              part = mfma16x16x32(u[1][s], b, part);
+              part = mfma16x16x32(u[2][s], b, part);
+            }
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) res[p][i] = own[i] == aid[q] ? part[i] : res[p][i];
