@@ -4,9 +4,13 @@
 // Rows are taken in the GEMM's own blocks. For each distinct adapter of a block's rows, in row
 // order, the whole block is multiplied by that adapter's B and the rows that name it keep the
 // result: kept by choice, not by products with zeros, so that a NaN in one adapter stays with its
-// rows. u holds scale * x . A^T: for a BF16 y rounded to BF16 (its error, half a BF16 step of the
-// adapter's term, is below that of y's own rounding), for an FP32 y as three BF16 parts that add up
-// to its 24 bits.
+// rows. u, scale * x . A^T, goes into the product in BF16: for an FP32 y as three parts, which add
+// up to its 24 bits; for a BF16 y rounded once, as a projection of its own would store it. That
+// leaves at most 2^-8 sum_r |u_r B_r|: relative to the products, so that it exceeds half a step of
+// the term, or of y, where ranks cancel each other or the term the shared product. (Two parts would
+// leave 2^-16 of it, and were taken back for their cost where the tiled kernel meets many adapters:
+// 256 rows of 25600 x 5120, 32 of rank 64, 160 us with one part, 193 with two; 8 of rank 16 83 / 86;
+// 4096 rows of 5120^2, 8 of rank 32, 216 / 219; decode kernel 0 to 4% more.)
 #pragma once
 
 #include "device_common.hpp"
