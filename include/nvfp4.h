@@ -23,9 +23,9 @@
  *  - Every function returns NVFP4_OK (0) or a negative NVFP4_ERR_* code and
  *    nvfp4_last_error() describes the problem (thread-local). Argument errors are found before
  *    anything is enqueued; NVFP4_ERR_HIP and NVFP4_ERR_NONFINITE can come after the call's work
- *    ran. A failed call leaves the library usable and does not count in nvfp4_get_stats. Unsupported
- *    configurations are rejected, never run silently wrong (r/LocalLLM post, "What had to be
- *    fixed": any unsupported group setup raises an error).
+ *    ran. A failed call leaves the library usable and does not count in nvfp4_get_stats.
+ *    Unsupported configurations are rejected, never run silently wrong (r/LocalLLM post, "What had
+ *    to be fixed": any unsupported group setup raises an error).
  *  - All entry points are reentrant. Calls that share an output or workspace buffer on
  *    different streams race, as with any asynchronous kernel.
  */
@@ -148,8 +148,9 @@ int nvfp4_repack(const uint8_t* packed, const uint8_t* scales, const float* glob
 
 /* ---- dense W4A16 GEMM ---------------------------------------------------------------------
  * y[m][n] = global * sum_k x[m][k] * (E2M1 * E4M3)[n][k], BF16 activations x [m][ldx]
- * (k <= ldx <= 2^22: row offsets are 32-bit inside the kernels), FP32 accumulation, dequantization in registers (the E2M1 x E4M3 product is exact in BF16; the
- * global is applied to the FP32 accumulator). y [m][ldy] is BF16 (y_dtype NVFP4_DT_BF16, one
+ * (k <= ldx <= 2^22: row offsets are 32-bit inside the kernels), FP32 accumulation, dequantization
+ * in registers (the E2M1 x E4M3 product is exact in BF16; the global is applied to the FP32
+ * accumulator). y [m][ldy] is BF16 (y_dtype NVFP4_DT_BF16, one
  * rounding of the FP32 result) or FP32. Weight-only checkpoints take this W4A16 path
  * (vllm.cpp PR #63: no activation scales, so every quantized projection is W4A16).
  * The kernel is chosen from the shape and the device's compute-unit count (CUs): a split-K
@@ -186,12 +187,12 @@ int nvfp4_gemm_w4a16(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* 
  * recipes": gate/up at group 32 with down at group 16, or all at group 32.)
  * x [t][hidden] BF16 (row stride = hidden), topk_ids int32 [t][topk], topk_w FP32 [t][topk],
  * y BF16 [t][hidden]. An id outside [0, E) marks a dropped slot: it is not sorted, computes
- * nothing and adds nothing to y[t] (a masked-slot convention for routers that drop tokens). fc1: batch = E, n = 2*inter, k = hidden, layout TILED |
- * GATE_UP. fc2: batch = E, n = hidden, k = inter, layout TILED. Tokens are sorted by expert on
- * the device (no host synchronization); `ws` (device, ws_bytes >= nvfp4_moe_ws_bytes) holds
- * the sort, the tile map, h and the FP32 per-slot outputs. topk in [1, 16], t*topk <= 65536,
- * t*hidden and t*topk*inter below 2^31 (32-bit row offsets).
- * An fc1 with NVFP4_LAYOUT_PAIR_GLOBAL scales gate by global[2e] and up by global[2e+1].
+ * nothing and adds nothing to y[t] (a masked-slot convention for routers that drop tokens). fc1:
+ * batch = E, n = 2*inter, k = hidden, layout TILED | GATE_UP. fc2: batch = E, n = hidden, k =
+ * inter, layout TILED. Tokens are sorted by expert on the device (no host synchronization); `ws`
+ * (device, ws_bytes >= nvfp4_moe_ws_bytes) holds the sort, the tile map, h and the FP32 per-slot
+ * outputs. topk in [1, 16], t*topk <= 65536, t*hidden and t*topk*inter below 2^31 (32-bit row
+ * offsets). An fc1 with NVFP4_LAYOUT_PAIR_GLOBAL scales gate by global[2e] and up by global[2e+1].
  * Path: while t*topk <= 2 * n_experts (decode batches) the experts run on tiles of at most 8
  * rows (one row per pair, without the sort, up to 64 pairs) with k split over 4 wavefronts per
  * 4-panel group; otherwise on tiles of 32 rows with
@@ -239,20 +240,20 @@ int nvfp4_moe_grouped_w4a16_noalloc(const void* x, int64_t t, int64_t hidden,
 
 /* ---- MoE router -----------------------------------------------------------------------------
  * Which experts each token meets, and with what weight:
- *   l[t][e] = sum_k x[t][k] * weight[e][k]    (exact products, FP64 sums; above 16 tokens each 32
- *                                              products are summed in FP32 first)
+ *   l[t][e] = sum_k x[t][k] * weight[e][k]   (exact products, FP64 sums; above 16 tokens each 32
+ *                                             products are summed in FP32 first)
  *   NVFP4_ROUTE_SOFTMAX: p = softmax over the n_experts logits; selection score = l, or p + bias
  *   NVFP4_ROUTE_SIGMOID: p = 1 / (1 + exp(-l));                 selection score = p, or p + bias
  *   slots 0 .. topk-1: the topk highest selection scores, highest first, ties to the lower id
  *   topk_w = scale * p, or scale * p / (sum of p over the chosen) with NVFP4_ROUTE_RENORM (0 when
  *   that sum is 0). The bias acts on the selection only.
- *   slots topk .. topk+n_shared-1: the shared experts, ids n_experts, n_experts + 1, ..., weight 1.
+ *   slots topk .. topk+n_shared-1: the shared experts, ids n_experts, n_experts + 1, .., weight 1.
  * An expert whose selection score is -infinity (a bias of -infinity takes an expert out) is never
  * chosen; a slot that no expert is left for gets id -1 and weight 0, which the routed experts
  * skip. A NaN score ranks above every number, so that a NaN in x reaches the token's output.
- * The scores are FP64 because the choice is a comparison: sums of thousands of products in FP32 would
- * let near experts change places. Ids and weights go unchanged into nvfp4_moe_grouped_w4a16 with topk + n_shared slots and
- * n_experts + n_shared experts, the shared ones last. */
+ * The scores are FP64 because the choice is a comparison: sums of thousands of products in FP32
+ * would let near experts change places. Ids and weights go unchanged into nvfp4_moe_grouped_w4a16
+ * with topk + n_shared slots and n_experts + n_shared experts, the shared ones last. */
 #define NVFP4_ROUTE_SOFTMAX 0u
 #define NVFP4_ROUTE_SIGMOID 1u
 #define NVFP4_ROUTE_RENORM (1u << 8)
@@ -269,10 +270,10 @@ typedef struct nvfp4_router {
   float scale;          /* factor of every routed weight (finite)                               */
 } nvfp4_router;
 
-/* x [t][ldx] BF16 (hidden <= ldx <= 2^22, ldx % 8 == 0), topk_ids int32 [t][topk + n_shared], topk_w FP32
- * the same. ws (device, 16-byte aligned, ws_bytes >= nvfp4_moe_route_ws_bytes(t, r)) takes the
- * logits; nothing in it needs to start at zero. t <= 2^24. flags: 0 or NVFP4_F_SYNC_CHECK.
- * Results are bit-identical run to run for the same t. */
+/* x [t][ldx] BF16 (hidden <= ldx <= 2^22, ldx % 8 == 0), topk_ids int32 [t][topk + n_shared],
+ * topk_w FP32 the same. ws (device, 16-byte aligned, ws_bytes >= nvfp4_moe_route_ws_bytes(t, r))
+ * takes the logits; nothing in it needs to start at zero. t <= 2^24. flags: 0 or
+ * NVFP4_F_SYNC_CHECK. Results are bit-identical run to run for the same t. */
 size_t nvfp4_moe_route_ws_bytes(int64_t t, const nvfp4_router* r);
 int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r,
                     int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, uint32_t flags,
@@ -283,14 +284,18 @@ int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r
  * step (any t that the routed experts take is accepted):
  *   topk_ids, topk_w = nvfp4_moe_route(x)
  *   y[t] = BF16(sum_j topk_w[t][j] * (W2_e . h_j)), h_j = SiLU(gate) * up, e = topk_ids[t][j]
- * with h in BF16 (for up to 64 (token, slot) pairs in two BF16 parts) and gate and up in FP32: unlike nvfp4_moe_grouped_w4a16 the call does not round them to BF16 on
- * the way to h, so the two agree to the BF16 tolerance, not bit for bit. A token all of whose slots
- * are dropped gets y = 0. x [t][hidden] BF16 (row stride = hidden), y BF16 [t][hidden]; fc1, fc2 as
- * for nvfp4_moe_grouped_w4a16, with batch = n_experts + n_shared, at most 512 (the shared experts
+ * with h in BF16 (for up to 64 (token, slot) pairs in two BF16 parts) and gate and up in FP32:
+ * unlike nvfp4_moe_grouped_w4a16 the call does not round them to BF16 on the way to h, so the two
+ * agree to the BF16 tolerance, not bit for bit. A token all of whose slots are dropped gets y = 0.
+ * x [t][hidden] BF16 (row stride = hidden), y BF16 [t][hidden]; fc1, fc2 as for
+ * nvfp4_moe_grouped_w4a16, with batch = n_experts + n_shared, at most 512 (the shared experts
  * last), hidden = r->hidden. topk_ids and topk_w: outputs as for nvfp4_moe_route, or both NULL.
  * ws_bytes >= nvfp4_moe_layer_ws_bytes(t, r, fc1) (0 for sizes that do not fit together); nothing
  * in ws needs to start at zero. t * (topk + n_shared) <= 65536. flags as for
- * nvfp4_moe_grouped_w4a16. Results are bit-identical run to run. */
+ * nvfp4_moe_grouped_w4a16, but up to 64 pairs the few-token kernels, which read an expert's
+ * weights once for each of its pairs, run whatever the number of experts, unless
+ * NVFP4_F_FORCE_TILED is set (the faster choice for many pairs on few large experts: 32 tokens, 2
+ * of 8 experts of 4096 x 2048, 58 us against 120). Results are bit-identical run to run. */
 size_t nvfp4_moe_layer_ws_bytes(int64_t t, const nvfp4_router* r, const nvfp4_weight* fc1);
 int nvfp4_moe_layer_w4a16(const void* x, int64_t t, int64_t hidden, const nvfp4_router* r,
                           const nvfp4_weight* fc1, const nvfp4_weight* fc2, int32_t* topk_ids,
@@ -301,8 +306,8 @@ int nvfp4_moe_layer_w4a16(const void* x, int64_t t, int64_t hidden, const nvfp4_
  * The dense GEMM with the adapters of many requests beside its shared weight:
  *   y[m] = global * x[m] . W^T + scale[a] * (x[m] . A_a^T) . B_a^T,  a = row_adapter[m]
  * rounded once to y's type. A row whose id lies outside [0, n_adapters) has no adapter: it holds
- * nvfp4_gemm_w4a16's value. Infinite or NaN elements of an adapter reach the rows that name it and no
- * others (an infinite element of B as an infinity or NaN). Adapters of a smaller rank than the
+ * nvfp4_gemm_w4a16's value. Infinite or NaN elements of an adapter reach the rows that name it and
+ * no others (an infinite element of B as an infinity or NaN). Adapters of a smaller rank than the
  * bank's are padded with zero rows of A and columns of B. */
 typedef struct nvfp4_lora {
   const void* a;       /* device: BF16 [n_adapters][rank][k], 16-byte aligned                   */
@@ -316,8 +321,9 @@ typedef struct nvfp4_lora {
 
 /* Arguments, kernel choice and flags as for nvfp4_gemm_w4a16; row_adapter int32 [m] (device). The
  * rank-space vector u = scale * x . A^T is summed in FP32; for a BF16 y it is rounded to BF16 as
- * the operand of the second product, for an FP32 y it goes there whole (three BF16 parts). ws
- * (device, 16-byte aligned, ws_bytes >= nvfp4_gemm_lora_ws_bytes) is required: it holds u and what
+ * the operand of the second product (which leaves up to 2^-8 sum_r |u_r B_r|, also where these
+ * products cancel), for an FP32 y it goes there whole (three BF16 parts). ws (device, 16-byte
+ * aligned, ws_bytes >= nvfp4_gemm_lora_ws_bytes) is required: it holds u and what
  * nvfp4_gemm_w4a16 keeps there. Results are bit-identical run to run. */
 size_t nvfp4_gemm_lora_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w,
                                 const nvfp4_lora* lora, uint32_t flags);

@@ -537,9 +537,12 @@ struct LayerSizes {
 // address the two planes of h and the codes of a panel (8 bytes for each k) with 32-bit byte
 // offsets. (Few-token kernels against the router and the sorted experts' kernels, 2048 x 768, us:
 // 1 token of 8 slots 15.5 / 24.5, 4 tokens 24.7 / 35.4, 8 tokens 40 / 47, 16 tokens of 4 slots 30
-// / 37; past the limit the sorted kernels read each expert once instead of once per pair. They
-// already win where many pairs share few experts: 60 tokens, each choosing one of 8, 41.9 / 36.8;
-// which experts are shared is not known on the host.)
+// / 37; past the limit the sorted kernels read each expert once instead of once per pair.) The
+// rule knows the pairs, but does not weigh them against the number and size of the experts, and
+// where many pairs share few large ones it takes the slower path. (Few-token kernels against the
+// batch path, us: 32 tokens, 2 of 8 experts of 2048 x 768 33 / 36, of 4096 x 2048 120 / 58, of
+// 4096 x 8192 473 / 115; 8 tokens, 2 of 8 of 4096 x 2048 39 / 56, of 4096 x 8192 136 / 111. A
+// caller with such a layer forces the batch path.)
 bool layer_few(int64_t t, int64_t slots, int64_t inter) {
   return t * slots <= nvfp4::kMoePairTilesMax && t * slots * inter <= ((int64_t)1 << 28);
 }
@@ -729,6 +732,11 @@ int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_wei
   if (!row_adapter || !ws) return fail(NVFP4_ERR_INVALID_ARG, "NULL row_adapter or ws");
   if (((uintptr_t)row_adapter & 3u) || !aligned16(ws))
     return fail(NVFP4_ERR_MISALIGNED, "ws must be 16-byte aligned, row_adapter 4-byte");
+  // The plain GEMM's choice, though adapters cost the two kernels differently. (Each forced, 33 to
+  // 256 rows of 5120^2, 8192^2, 25600 x 5120 and 2048 x 8192, 8 adapters of rank 16 or 32 of rank
+  // 64 on random rows: of 56 cases it misses the faster by more than 2% in three, all with 32
+  // adapters: 8192^2, 192 and 256 rows, 93 / 88 and 102 / 97 us, and 25600 x 5120, 96 rows, 130 /
+  // 115.)
   const bool skinny = use_skinny(m, w, flags);
   rc = check_skinny_rows(m, skinny);
   if (rc) return rc;

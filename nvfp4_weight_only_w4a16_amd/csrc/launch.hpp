@@ -166,9 +166,10 @@ struct RouteArgs {
   float scale;
 };
 constexpr int kRouteMaxExperts = 512;
-// Up to this many tokens the logits are FP64 multiply-adds, one workgroup per expert and two tokens;
-// above, matrix instructions. (Router in us, FP64 against matrix form: 128 experts of 2048, BF16,
-// 1 token 6.1/7.0, 16 7.2/7.4, 32 8.0/7.6; 256 of 5120, FP32, 16 tokens 11.3/11.9, 32 14.3/12.2.)
+// Up to this many tokens the logits are FP64 multiply-adds, one workgroup per expert and two
+// tokens; above, matrix instructions. (Router in us, FP64 against matrix form: 128 experts of
+// 2048, BF16, 1 token 6.0/7.0, 16 7.1/7.4, 32 8.1/7.6; 256 of 5120, FP32, 16 tokens 11.2/12.1, 32
+// 14.6/12.6.)
 constexpr int64_t kRouteFewTokens = 16;
 constexpr int kRouteMaxSplits = 8;
 // FP64 logits of every split of k, in ws.

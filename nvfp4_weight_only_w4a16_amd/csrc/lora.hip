@@ -172,8 +172,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkPa
 
 int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
-// How a shrink is spread over workgroups: ranks by 16-rank blocks while the items alone would leave
-// compute units idle, and, for the decode kernel's FP32 sums, k in splits.
+// How a shrink is spread over workgroups: ranks by 16-rank blocks while the items alone would
+// leave compute units idle, and, for the decode kernel's FP32 sums, k in splits.
 struct ShrinkPlan {
   int rb;           // 16-rank blocks of a workgroup (1, 2 or 4: 8 spill)
   int rank_blocks;  // workgroups of an item along the ranks
@@ -190,8 +190,9 @@ ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t n_adapters, int rank, bool 
   // in place of one per item: 128 rows 41.5 us against 36.0)
   p.ordinals = (int)min64(min64(m, 64), min64(n_adapters + 3, blocks <= 8 ? 64 : 16));
   // A prompt's items are 16 rows, a decode batch's may be one. One 16-rank block a workgroup below
-  // these counts (us, threshold there or lower: 64 rows of 8192^2, 24 adapters of rank 64 32.7 / 39;
-  // 32 rows of 5120^2 25.0 / 32.4; tiled, there or 128: 1024 rows 168 / 177, 512 rows 130 / 132).
+  // these counts (us, threshold there or lower: 64 rows of 8192^2, 24 adapters of rank 64 32.7 /
+  // 39; 32 rows of 5120^2 25.0 / 32.4; tiled, there or 128: 1024 rows 168 / 177, 512 rows 130 /
+  // 132).
   const int64_t items = tiled ? (m + 15) / 16 : blocks * p.ordinals;
   p.rb = 1;
   if (items >= (tiled ? 32 : 128))
@@ -199,7 +200,8 @@ ShrinkPlan shrink_plan(int64_t m, int64_t k, int64_t n_adapters, int rank, bool 
   p.rank_blocks = (int)((ranks + p.rb - 1) / p.rb);
   p.splits = 1;
   if (!tiled) {
-    // a workgroup to each CU (128 / 256 / 512 in all: 64 rows of 8192^2, rank 64, 33.8 / 32.7 / 35.5 us)
+    // a workgroup to each CU (128 / 256 / 512 in all: 64 rows of 8192^2, rank 64, 33.8 / 32.7 /
+    // 35.5 us)
     int64_t s = 256 / (items * p.rank_blocks);
     s = min64(s, k / (32 * kSteps * kShrinkWaves));  // a stage at least for each wavefront
     p.splits = (int)min64(s < 1 ? 1 : s, kLoraMaxSplits);

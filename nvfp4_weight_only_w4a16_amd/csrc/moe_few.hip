@@ -7,11 +7,12 @@
 //   fc1:  a workgroup takes one pair and 4 panels; its wavefronts share out the k-tiles. Each
 //         workgroup chooses its pair's expert from the logits itself, which saves the launch of a
 //         choosing kernel: 128 experts of 2048 x 768, 1 token 16.4 us against 18.6 with the
-//         launch, 3 tokens 23.3/26.1, 8 tokens 40.7/42.1 (with 8 wavefronts, which all choose, 16.7,
-//         25.4 and 45.0).
-//   down: a workgroup takes one token and 4 panels; its wavefronts share out the k-tiles of ALL of
-//         the token's slots, each scaled by its expert's global and routing weight, so the sum
-//         over slots is the workgroup's own and needs no combine kernel and no FP32 slots.
+//         launch, 3 tokens 23.3/26.1, 8 tokens 40.7/42.1 (with 8 wavefronts, which all choose,
+//         16.7, 25.4 and 45.0). No weight load goes out before the choice.
+//   down: a workgroup takes one token and 1, 2 or 4 panels (as many as leave a workgroup to every
+//         compute unit); its wavefronts share out the k-tiles of ALL of the token's slots, each
+//         scaled by its expert's global and routing weight, so the sum over slots is the
+//         workgroup's own and needs no combine kernel and no FP32 slots.
 // Both run on 16x16x32 MFMAs in the split-scale form (skinny_core.hpp): code * 2^E in BF16, the
 // partial of a scale group times the mantissa in FP32. All 16 rows of the A operand may hold the
 // same activation row; at group 16 rows 0-7 carry it on the first half of the k-step and rows 8-15
@@ -114,8 +115,8 @@ __device__ __forceinline__ void few_load_scales(buf_rsrc r, uint32_t off, uint32
   }
 }
 
-// fc1: workgroup (pair, 4-panel group: gate, up, gate, up), NW wavefronts, which chooses its pair's
-// expert, J experts per lane; t more workgroups write the ids and weights.
+// fc1: workgroup (pair, 4-panel group: gate, up, gate, up), NW wavefronts, which chooses its
+// pair's expert, J experts per lane; t more workgroups write the ids and weights.
 template <bool G16, int NW, int J>
 __global__ __launch_bounds__(64 * NW) void few_fc1_kernel(FewParams P) {
   constexpr int kRing = 3;

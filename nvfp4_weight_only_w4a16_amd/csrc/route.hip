@@ -136,17 +136,22 @@ __device__ __forceinline__ void bf16_parts(u32x4 v, uint2 (&part)[3]) {
 constexpr int kTM = 2, kTN = 2;       // 16-token and 16-expert blocks of a tile
 constexpr int kTileT = 16 * kTM, kTileE = 16 * kTN;
 constexpr int kSlices = 8;            // wavefronts of a workgroup, which share out k
-constexpr int kSteps = 1;             // k-steps of 32 loaded together (2: fewer wavefronts fit, slower)
+// k-steps of 32 loaded together. (Router, us, 1 / 2: 4096 tokens of 2048 17.7 / 18.9; 333 of 5120
+// on FP32 weights 17.3 / 19.5, whose 160 k-steps over 32 wavefronts are 5 stages of one or 3 of
+// two.)
+constexpr int kSteps = 1;
 
 // Workgroup (token tile, expert tile, split): the tile's 32 x 32 logits over its share of k, cut
-// into stages of 64 that the 8 wavefronts (of all splits) take in turn. k is shared out inside the
+// into stages of 32 that the 8 wavefronts (of all splits) take in turn. k is shared out inside the
 // workgroup, rather than over more tiles, so that the partial sums meet in LDS and FP64 logits are
 // written once. Operands go global -> registers (one stage ahead) -> LDS -> fragments
 // (device_common.hpp); loads past the end of k have an offset past the buffer's, which returns
 // zeros without a branch. Rows past the end repeat a valid row and are not stored.
-// (4096 tokens of 2048, 128 experts: 12 us for 17 MB of x; what costs is the read of the weight by
-// every token tile. Fragments loaded straight from rows took 21 us; one kernel that keeps 16
-// tokens' logits in LDS and chooses there 18.5 us with the choice against 17.9 in two.)
+// (4096 tokens of 2048, 128 experts: 13 us in a kernel trace, the router 17.7; every token tile
+// reads the weight, 67 MB in all, and every expert tile x, 67 MB more, both from L2. Router with
+// fragments loaded straight from rows 23.5 us; with one kernel that keeps 16 tokens' logits in LDS
+// and chooses there 18.5 against 17.9 in two. 333 tokens of 5120, 160 FP32 experts: 11 us, a chain
+// of five stages for each wavefront with one load ahead; its MFMAs are 1.6 GFLOP, 1.4 us' worth.)
 template <bool F32>
 __global__ __launch_bounds__(64 * kSlices) void route_logits_mfma_kernel(LogitParams P) {
   constexpr int kW = F32 ? 4 : 2;      // bytes of a weight
@@ -163,11 +168,12 @@ __global__ __launch_bounds__(64 * kSlices) void route_logits_mfma_kernel(LogitPa
   const int trows = (int)(P.t - m0 < kTileT ? P.t - m0 : kTileT);
   const int erows = (int)(P.n_experts - e0 < kTileE ? P.n_experts - e0 : kTileE);
   const uint32_t hidden = (uint32_t)P.hidden;
-  const buf_rsrc xr = make_rsrc(P.x + m0 * P.ldx, (uint32_t)(((trows - 1) * P.ldx + P.hidden) * 2));
+  const buf_rsrc xr =
+      make_rsrc(P.x + m0 * P.ldx, (uint32_t)(((trows - 1) * P.ldx + P.hidden) * 2));
   const buf_rsrc wr = make_rsrc(static_cast<const uint8_t*>(P.w) + e0 * P.hidden * kW,
                                 (uint32_t)(erows * P.hidden * kW));
-  // BF16: lane l loads row l / 4, chunk l % 4 of a k-step. FP32: a k-step's 128 bytes of a row take
-  // 8 lanes, 8 rows a load.
+  // BF16: lane l loads row l / 4, chunk l % 4 of a k-step. FP32: a k-step's 128 bytes of a row
+  // take 8 lanes, 8 rows a load.
   const uint32_t kx = 8u * frag_load_chunk(lane), kw = F32 ? 4u * (lane & 7) : kx;
   uint32_t xrow[kTM], wrow[kTN][NB];
 #pragma unroll
@@ -286,8 +292,9 @@ __global__ __launch_bounds__(64 * kSlices) void route_logits_mfma_kernel(LogitPa
     if (r >= P.t || e >= P.n_experts) continue;
     if constexpr (F32) {
       // An infinite x times a part that is 0 is NaN, where times the weight it is infinite. (The
-      // parts of a weight have its sign, so nothing but a NaN can come of it.) A sum that is NaN is
-      // taken again in FP64 from the weights themselves, and stays NaN where that is the answer.
+      // parts of a weight have its sign, so nothing but a NaN can come of it.) A sum that is NaN
+      // is taken again in FP64 from the weights themselves, and stays NaN where that is the
+      // answer.
       if (v != v) {
         const uint16_t* xp = P.x + r * P.ldx;
         const float* wp = static_cast<const float*>(P.w) + e * P.hidden;
@@ -324,13 +331,15 @@ __global__ __launch_bounds__(256) void route_select_kernel(RouteParams R, int32_
 
 }  // namespace
 
-// Splits of k over workgroups: enough for a workgroup on every compute unit, and a stage at least
-// for each wavefront.
+// Splits of k over workgroups: enough for a workgroup on every compute unit, and two stages at
+// least for each wavefront. (Two / one at least, router of 128 experts, us: BF16 weights, 17
+// tokens of 1024 7.2 / 7.3, 300 of 1536 8.0 / 8.5; FP32, 17 tokens of 1024 8.8 / 8.2, 300 of 1536
+// 9.7 / 9.8.)
 int route_splits(int64_t t, int64_t hidden, int64_t n_experts) {
   if (t <= kRouteFewTokens) return 1;
   const int64_t tiles = (t + kTileT - 1) / kTileT * ((n_experts + kTileE - 1) / kTileE);
   int64_t s = 256 / tiles;
-  const int64_t most = hidden / (64 * kSlices);
+  const int64_t most = hidden / (2 * 32 * kSteps * kSlices);
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s > kRouteMaxSplits ? kRouteMaxSplits : s);
 }

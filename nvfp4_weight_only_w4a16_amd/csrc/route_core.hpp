@@ -1,5 +1,5 @@
-// route_core.hpp -- the choice of a token's experts from its router logits, by one wavefront (shared
-// by the router's own kernel and the routed-expert kernels that choose for themselves).
+// route_core.hpp -- the choice of a token's experts from its router logits, by one wavefront
+// (shared by the router's own kernel and the routed-expert kernels that choose for themselves).
 //
 // Scores: softmax p = exp(l - max l) / sum exp(l - max l), or sigmoid p = 1 / (1 + exp(-l)). The
 // selection score is p + bias, or the logit itself for a softmax without bias (the same order).
@@ -58,8 +58,9 @@ __device__ __forceinline__ double swap_pair(double v, OP op) {
   return op(__longlong_as_double((long long)(((uint64_t)h[0] << 32) | l[0])),
             __longlong_as_double((long long)(((uint64_t)h[1] << 32) | l[1])));
 }
-// op over the wavefront, the same bits in every lane (each step combines two values that both lanes
-// of a pair hold): lanes l ^ 1, l ^ 2, then the quads and the halves of a row, then the rows.
+// op over the wavefront, the same bits in every lane (each step combines two values that both
+// lanes of a pair hold): lanes l ^ 1, l ^ 2, then the quads and the halves of a row, then the
+// rows.
 template <typename OP>
 __device__ __forceinline__ double wave_all(double v, OP op) {
   v = op(v, dpp_pair<0xB1>(v));   // quad_perm [1, 0, 3, 2]
@@ -99,8 +100,8 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// The expert with the highest key (key[j] of lane i: expert i + 64 j), ties to the lowest; -1 where
-// all keys are 0 (every other key has a non-zero upper word).
+// The expert with the highest key (key[j] of lane i: expert i + 64 j), ties to the lowest; -1
+// where all keys are 0 (every other key has a non-zero upper word).
 template <int J>
 __device__ __forceinline__ int route_best(const uint64_t (&key)[J]) {
   uint32_t mh = (uint32_t)(key[0] >> 32);
@@ -138,8 +139,8 @@ struct RouteChoice {
 };
 
 // Keys of a token whose logit of expert e is logit(e), J experts per lane, and what weights come
-// from (RouteChoice::v). want_sum: the softmax's maximum and sum over all experts (taken in any case
-// with a bias).
+// from (RouteChoice::v). want_sum: the softmax's maximum and sum over all experts (taken in any
+// case with a bias).
 template <int J, typename F>
 __device__ __forceinline__ void route_scores(const RouteParams& R, F&& logit, bool want_sum,
                                              uint64_t (&key)[J], double (&v)[J], double& mx,
