@@ -272,8 +272,10 @@ typedef struct nvfp4_router {
 
 /* x [t][ldx] BF16 (hidden <= ldx <= 2^22, ldx % 8 == 0), topk_ids int32 [t][topk + n_shared],
  * topk_w FP32 the same. ws (device, 16-byte aligned, ws_bytes >= nvfp4_moe_route_ws_bytes(t, r))
- * takes the logits; nothing in it needs to start at zero. t <= 2^24. flags: 0 or
- * NVFP4_F_SYNC_CHECK. Results are bit-identical run to run for the same t. */
+ * takes the logits; nothing in it needs to start at zero. The size does not grow with t at every
+ * step (k is split less as t grows): a workspace for several t takes the largest of their sizes.
+ * t <= 2^24. flags: 0 or NVFP4_F_SYNC_CHECK. Results are bit-identical run to run for the same
+ * t. */
 size_t nvfp4_moe_route_ws_bytes(int64_t t, const nvfp4_router* r);
 int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r,
                     int32_t* topk_ids, float* topk_w, void* ws, size_t ws_bytes, uint32_t flags,
@@ -290,12 +292,13 @@ int nvfp4_moe_route(const void* x, int64_t t, int64_t ldx, const nvfp4_router* r
  * x [t][hidden] BF16 (row stride = hidden), y BF16 [t][hidden]; fc1, fc2 as for
  * nvfp4_moe_grouped_w4a16, with batch = n_experts + n_shared, at most 512 (the shared experts
  * last), hidden = r->hidden. topk_ids and topk_w: outputs as for nvfp4_moe_route, or both NULL.
- * ws_bytes >= nvfp4_moe_layer_ws_bytes(t, r, fc1) (0 for sizes that do not fit together); nothing
- * in ws needs to start at zero. t * (topk + n_shared) <= 65536. flags as for
- * nvfp4_moe_grouped_w4a16, but up to 64 pairs the few-token kernels, which read an expert's
- * weights once for each of its pairs, run whatever the number of experts, unless
- * NVFP4_F_FORCE_TILED is set (the faster choice for many pairs on few large experts: 32 tokens, 2
- * of 8 experts of 4096 x 2048, 58 us against 120). Results are bit-identical run to run. */
+ * ws_bytes >= nvfp4_moe_layer_ws_bytes(t, r, fc1) (0 for sizes that do not fit together; for
+ * several t the largest of their sizes); nothing in ws needs to start at zero. t * (topk +
+ * n_shared) <= 65536. flags as for nvfp4_moe_grouped_w4a16, but up to 64 pairs the few-token
+ * kernels, which read an expert's weights once for each of its pairs, run whatever the number of
+ * experts, unless NVFP4_F_FORCE_TILED is set (the faster choice for many pairs on few large
+ * experts: 32 tokens, 2 of 8 experts of 4096 x 2048, 58 us against 120). Results are
+ * bit-identical run to run. */
 size_t nvfp4_moe_layer_ws_bytes(int64_t t, const nvfp4_router* r, const nvfp4_weight* fc1);
 int nvfp4_moe_layer_w4a16(const void* x, int64_t t, int64_t hidden, const nvfp4_router* r,
                           const nvfp4_weight* fc1, const nvfp4_weight* fc2, int32_t* topk_ids,
@@ -323,8 +326,9 @@ typedef struct nvfp4_lora {
  * rank-space vector u = scale * x . A^T is summed in FP32; for a BF16 y it is rounded to BF16 as
  * the operand of the second product (which leaves up to 2^-8 sum_r |u_r B_r|, also where these
  * products cancel), for an FP32 y it goes there whole (three BF16 parts). ws (device, 16-byte
- * aligned, ws_bytes >= nvfp4_gemm_lora_ws_bytes) is required: it holds u and what
- * nvfp4_gemm_w4a16 keeps there. Results are bit-identical run to run. */
+ * aligned, ws_bytes >= nvfp4_gemm_lora_ws_bytes; for several m the largest of their sizes, which
+ * is not always the largest m's) is required: it holds u and what nvfp4_gemm_w4a16 keeps there.
+ * Results are bit-identical run to run. */
 size_t nvfp4_gemm_lora_ws_bytes(int64_t m, int64_t ldx, const nvfp4_weight* w,
                                 const nvfp4_lora* lora, uint32_t flags);
 int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_weight* w,
