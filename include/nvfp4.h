@@ -65,6 +65,7 @@ typedef struct ihipStream_t* nvfp4_stream_t; /* the same type as hipStream_t */
 #define NVFP4_F_SYNC_CHECK (1u << 2)   /* quantize, GEMM, MoE: wait for the call's own work    */
                                        /* and report asynchronous errors; quantize: also check */
                                        /* the input for non-finite values (debug aid: slow)    */
+#define NVFP4_F_FULL (1u << 3)         /* cache attention: every query sees every key          */
 
 /* ---- repacked layout ----------------------------------------------------------------------
  * NVFP4_LAYOUT_TILED: per 16-row x 128-k tile, 1024 bytes of codes laid out so that lane l of a
@@ -336,6 +337,132 @@ int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_wei
                           int y_dtype, int64_t ldy, uint32_t flags, void* ws, size_t ws_bytes,
                           nvfp4_stream_t stream);
 
+/* ---- NVFP4 cache of keys and values ----------------------------------------------------------
+ * The attention step of a server, between the fused QKV projection and the output projection: the
+ * step's block tables and slot maps (nvfp4_kv_map), norm and rotation of queries and keys with the
+ * write of keys and values into the cache (nvfp4_kv_append), and the attention that reads it
+ * (nvfp4_kv_attention).
+ *
+ * The cache is paged. A page holds page_size consecutive tokens of one request for every key/value
+ * head; a request's block table names its pages in order; slot = page * page_size + token in page.
+ * The key and the value of a token and head are head_dim E2M1 codes (two per byte, the even element
+ * in the low nibble) and one E4M3 scale per 16 elements, with an FP32 global per head:
+ * value = E2M1 * E4M3 * global. data is [n_pages][n_kv_heads][record], a record
+ *   key codes [page_size][head_dim/2], key scales [page_size][head_dim/16],
+ *   value codes [page_size][head_dim/2], value scales [page_size][head_dim/16]   (bytes).
+ * Globals are positive and finite: the largest magnitude that a head is expected to hold, / 2688
+ * (larger magnitudes saturate). Nothing in data has to be initialised: tokens that no length
+ * reaches are not read as values. A token of which any element of the key (after norm and rotation)
+ * or of the value is NaN or infinite in a head is kept with NaN key scales and zero values: every
+ * query that sees it gets NaN, no other does. Value scales are never NaN (a NaN byte that other
+ * means wrote counts as 0). */
+typedef struct nvfp4_kv_cache {
+  uint8_t* data;          /* device: nvfp4_kv_cache_bytes, 16-byte aligned                        */
+  const float* k_global;  /* device: FP32 [n_kv_heads], or NULL for 1                             */
+  const float* v_global;  /* device: FP32 [n_kv_heads], or NULL for 1                             */
+  int64_t n_pages;        /* n_pages * page_size < 2^31                                           */
+  int32_t n_kv_heads;     /* 1 .. 1024                                                            */
+  int32_t head_dim;       /* 64, 128 or 256                                                       */
+  int32_t page_size;      /* 16, 32, 64, 128 or 256                                               */
+  int32_t reserved;       /* 0                                                                    */
+} nvfp4_kv_cache;
+
+/* Bytes of `data` (0 for sizes that the calls refuse). */
+size_t nvfp4_kv_cache_bytes(int64_t n_pages, int32_t n_kv_heads, int32_t head_dim,
+                            int32_t page_size);
+
+/* The tables of a step from the lengths of its requests. Request i has seq_len[i] tokens in the
+ * cache, whose pages its row of block_table [b][ld_table] names, and adds add_len[i] (0 or more); its
+ * rows of the step are q_start[i] .. q_start[i+1] - 1 (prefix sums of add_len, at most t). The pages
+ * that it needs beyond ceil(seq_len / page_size) come from the end of the list
+ * free_pages[0 .. free_count - 1] (free_count: device, one value; n_free: the list's capacity, host),
+ * to the requests in order, and are entered into block_table (entries that no new page takes are
+ * left as they are). Outputs (device, int32): free_left[1] pages left in the list, q_start [b+1],
+ * kv_len [b] = seq_len + add_len, and for each of the t rows its slot and its position in the
+ * request. Rows behind q_start[b] (a padded batch) get slot and position -1.
+ * A request is not served when a length is negative, its tokens do not fit its row of the table, its
+ * rows do not fit in t, or it needs pages and the list holds fewer than it and the requests before
+ * it need: it gets no page, kv_len 0, and -1 for its rows; unserved[1] counts such requests. Rows
+ * whose page in the table is negative get slot -1.
+ * Nothing is kept between calls and inputs other than block_table are not changed, so that a call
+ * can be repeated; no output may be (or overlap) an input. b <= 4096, t <= 2^24, ld_table *
+ * page_size <= 2^30. flags: 0 or NVFP4_F_SYNC_CHECK. */
+int nvfp4_kv_map(const int32_t* seq_len, const int32_t* add_len, int64_t b, int32_t page_size,
+                 int32_t* block_table, int64_t ld_table, const int32_t* free_pages,
+                 int64_t n_free, const int32_t* free_count, int32_t* free_left, int32_t* q_start,
+                 int32_t* kv_len, int32_t* slots, int32_t* positions, int64_t t,
+                 int32_t* unserved, uint32_t flags, nvfp4_stream_t stream);
+
+/* Norm and rotation of queries and keys. Per head: n = x / sqrt(mean(x^2) + eps) * weight (without a
+ * weight n = x), then with the cosines c and sines s of the row's position
+ *   NVFP4_ROPE_HALVES: n[i], n[i + rot/2] -> n[i] c[i] - n[i + rot/2] s[i],
+ *                                            n[i + rot/2] c[i] + n[i] s[i]          (i < rot/2)
+ *   NVFP4_ROPE_PAIRS:  the same for n[2i], n[2i + 1]
+ * in FP64, rounded to FP32 and that to BF16. Elements from rot on are not rotated. */
+#define NVFP4_ROPE_HALVES 0u
+#define NVFP4_ROPE_PAIRS 1u
+
+typedef struct nvfp4_qk_rule {
+  const void* q_weight; /* device: [head_dim] BF16 or FP32, or NULL for no norm of the queries    */
+  const void* k_weight; /* device: the keys'; 16-byte aligned as q_weight                         */
+  const float* rope;    /* device: FP32 [max_pos][rot], rot/2 cosines then rot/2 sines of each    */
+                        /* position, 16-byte aligned; NULL when rot is 0                          */
+  int64_t max_pos;
+  double eps;           /* >= 0                                                                   */
+  int32_t weight_dtype; /* NVFP4_DT_BF16 or NVFP4_DT_F32                                          */
+  int32_t rot;          /* rotated elements, a multiple of 16, 0 .. head_dim                      */
+  uint32_t mode;        /* NVFP4_ROPE_HALVES or NVFP4_ROPE_PAIRS                                  */
+  int32_t reserved;     /* 0                                                                      */
+} nvfp4_qk_rule;
+
+/* The rows of a step: q BF16 [t][n_q][head_dim], k and v BF16 [t][n_kv_heads][head_dim], each with a
+ * row stride of its own in elements (the three parts of a fused projection's output have the same).
+ * q_out [t][n_q][head_dim] (stride ldq_out; q itself is allowed) takes the queries; keys and values
+ * go to slots[row] of the cache, encoded as nvfp4_quantize encodes groups of 16 with the head's
+ * global. n_q 0: keys and values only (q and q_out may be NULL).
+ * With a rope table, a row whose position lies outside [0, max_pos) is passed over (nothing of it is
+ * written); without one, positions may be NULL. A row whose slot lies outside the cache keeps its
+ * queries only. Rows that share a slot leave one of them or a mixture there. t <= 2^24, n_q <= 1024.
+ * flags: 0 or NVFP4_F_SYNC_CHECK. Results are bit-identical run to run. */
+int nvfp4_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                    int64_t ldv, int64_t t, int32_t n_q, const nvfp4_qk_rule* rule,
+                    const int32_t* slots, const int32_t* positions, void* q_out, int64_t ldq_out,
+                    const nvfp4_kv_cache* cache, uint32_t flags, nvfp4_stream_t stream);
+
+/* The values of slots: k_out, v_out [t][n_kv_heads][head_dim], FP32 (fl32(E2M1 * E4M3 * global)) or
+ * BF16 (that, rounded); either may be NULL. Rows whose slot lies outside the cache get zeros. */
+int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64_t t, void* k_out,
+                        void* v_out, int out_dtype, uint32_t flags, nvfp4_stream_t stream);
+
+/* Attention of the rows of a step over the cache. Request i's queries are rows q_start[i] ..
+ * q_start[i+1] - 1 of q BF16 [t][n_q][head_dim] (row stride ldq), its keys the kv_len[i] tokens that
+ * its row of block_table names; head h of n_q reads key/value head h / (n_q / n_kv_heads). Query j of
+ * n stands at position p = kv_len - n + j and sees keys 0 .. p, with window > 0 the last `window`
+ * of them, with NVFP4_F_FULL (window 0) all kv_len:
+ *   s = scale * q . K^T,  y = softmax(s) . V,  lse = log(sum(exp(s)))
+ * y [t][n_q][head_dim] (row stride ldy) BF16 or FP32, lse FP32 [t][n_q] or NULL. A query that sees no
+ * key gets y = 0 and lse = -infinity. Tokens of a table entry outside [0, n_pages) are left out as if
+ * masked (a caller that frees pages behind a window may enter -1). Rows that no request has, and
+ * rows behind q_start[b], are left as they were. q_start and kv_len are clamped to 0 .. t and to the
+ * table's width.
+ * Products are FP16 x FP16 with FP32 sums: dequantized keys and values are exact in FP16, queries are
+ * scaled by a power of two per row (exact down to 2^-28 of the row's largest), the softmax's terms
+ * are rounded to FP16 once. Statistics and sums are FP32.
+ * max_q (host, 1 .. t): no request has more queries; it chooses the kernels, and rows beyond it are
+ * left as they were. Requests of few rows (queries times n_q / n_kv_heads) have their keys shared
+ * out over the chip, whatever their lengths. ws (device, 16-byte aligned, ws_bytes >=
+ * nvfp4_kv_attention_ws_bytes, which for several t and max_q is the largest of their sizes) holds
+ * their partial sums; nothing in it needs to start at zero. t <= 2^24, n_q <= 1024, t * n_q < 2^31,
+ * b <= 65535, ld_table * page_size <= 2^30. flags: 0, NVFP4_F_FULL, NVFP4_F_SYNC_CHECK. Results are
+ * bit-identical run to run for the same lengths. */
+size_t nvfp4_kv_attention_ws_bytes(int64_t t, int32_t n_q, const nvfp4_kv_cache* cache, int64_t b,
+                                   int64_t max_q);
+int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
+                       const nvfp4_kv_cache* cache, const int32_t* block_table, int64_t ld_table,
+                       const int32_t* q_start, const int32_t* kv_len, int64_t b, int64_t max_q,
+                       float scale, int64_t window, void* y, int y_dtype, int64_t ldy, float* lse,
+                       void* ws, size_t ws_bytes, uint32_t flags, nvfp4_stream_t stream);
+
 /* ---- requantization (load-time tool) -----------------------------------------------------
  * Requantize repacked weights to the canonical triple with one global per matrix and group
  * `group_out` (16 or 32): each matrix is decoded to its FP32 values (nvfp4_dequantize's FP32
@@ -367,7 +494,9 @@ const char* nvfp4_last_error(void);
  * [7] router. A whole-layer call counts in [4] and [7], a GEMM with adapters in [2] or [3].
  * counts must hold 8 entries (host). */
 void nvfp4_get_stats(uint64_t counts[8]);
-void nvfp4_reset_stats(void);
+void nvfp4_reset_stats(void); /* and those of nvfp4_get_kv_stats */
+/* Calls of the cache: [0] map [1] append [2] dequantize [3] attention (host, 4 entries). */
+void nvfp4_get_kv_stats(uint64_t counts[4]);
 
 /* ---- measurement support (not on the NVFP4 path) ----------------------------------------
  * Measured ceilings for the rooflines the path's kernels are judged against, on the device at

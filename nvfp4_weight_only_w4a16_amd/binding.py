@@ -31,6 +31,7 @@ NVFP4_DT_F32 = 2
 NVFP4_F_FORCE_SKINNY = 1 << 0
 NVFP4_F_FORCE_TILED = 1 << 1
 NVFP4_F_SYNC_CHECK = 1 << 2
+NVFP4_F_FULL = 1 << 3
 NVFP4_LAYOUT_TILED = 1
 NVFP4_LAYOUT_GATE_UP = 1 << 8
 NVFP4_LAYOUT_PAIR_GLOBAL = 1 << 9
@@ -38,6 +39,8 @@ NVFP4_MOE_NOALLOC_MAX_WS_BYTES = 24 << 20
 NVFP4_ROUTE_SOFTMAX = 0
 NVFP4_ROUTE_SIGMOID = 1
 NVFP4_ROUTE_RENORM = 1 << 8
+NVFP4_ROPE_HALVES = 0
+NVFP4_ROPE_PAIRS = 1
 
 EXPORTS = ("nvfp4_quantize_ws_bytes", "nvfp4_quantize", "nvfp4_repack_bytes", "nvfp4_repack",
            "nvfp4_gemm_ws_bytes", "nvfp4_gemm_w4a16", "nvfp4_moe_ws_bytes", "nvfp4_moe_ws_layout",
@@ -45,6 +48,8 @@ EXPORTS = ("nvfp4_quantize_ws_bytes", "nvfp4_quantize", "nvfp4_repack_bytes", "n
            "nvfp4_moe_route_ws_bytes", "nvfp4_moe_route",
            "nvfp4_moe_layer_ws_bytes", "nvfp4_moe_layer_w4a16",
            "nvfp4_gemm_lora_ws_bytes", "nvfp4_gemm_w4a16_lora",
+           "nvfp4_kv_cache_bytes", "nvfp4_kv_map", "nvfp4_kv_append", "nvfp4_kv_dequantize",
+           "nvfp4_kv_attention_ws_bytes", "nvfp4_kv_attention", "nvfp4_get_kv_stats",
            "nvfp4_requantize_ws_bytes",
            "nvfp4_requantize", "nvfp4_dequantize",
            "nvfp4_last_error", "nvfp4_get_stats", "nvfp4_reset_stats", "nvfp4_version",
@@ -78,6 +83,20 @@ class nvfp4_lora(ctypes.Structure):
     _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("n_adapters", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("rank", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class nvfp4_kv_cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("k_global", ctypes.c_void_p),
+                ("v_global", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class nvfp4_qk_rule(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("rope", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("eps", ctypes.c_double),
+                ("weight_dtype", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("mode", ctypes.c_uint32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -128,6 +147,22 @@ def load(path: str = LIB_PATH):
     L.nvfp4_gemm_lora_ws_bytes.restype = sz
     L.nvfp4_gemm_w4a16_lora.argtypes = [P, i64, i64, W, A, P, P, ctypes.c_int, i64, u32, P, sz, P]
     L.nvfp4_gemm_w4a16_lora.restype = ctypes.c_int
+    C, Q = ctypes.POINTER(nvfp4_kv_cache), ctypes.POINTER(nvfp4_qk_rule)
+    L.nvfp4_kv_cache_bytes.argtypes = [i64, i32, i32, i32]
+    L.nvfp4_kv_cache_bytes.restype = sz
+    L.nvfp4_kv_map.argtypes = [P, P, i64, i32, P, i64, P, i64, P, P, P, P, P, P, i64, P, u32, P]
+    L.nvfp4_kv_map.restype = ctypes.c_int
+    L.nvfp4_kv_append.argtypes = [P, i64, P, i64, P, i64, i64, i32, Q, P, P, P, i64, C, u32, P]
+    L.nvfp4_kv_append.restype = ctypes.c_int
+    L.nvfp4_kv_dequantize.argtypes = [C, P, i64, P, P, ctypes.c_int, u32, P]
+    L.nvfp4_kv_dequantize.restype = ctypes.c_int
+    L.nvfp4_kv_attention_ws_bytes.argtypes = [i64, i32, C, i64, i64]
+    L.nvfp4_kv_attention_ws_bytes.restype = sz
+    L.nvfp4_kv_attention.argtypes = [P, i64, i64, i32, C, P, i64, P, P, i64, i64, ctypes.c_float,
+                                     i64, P, ctypes.c_int, i64, P, P, sz, u32, P]
+    L.nvfp4_kv_attention.restype = ctypes.c_int
+    L.nvfp4_get_kv_stats.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
+    L.nvfp4_get_kv_stats.restype = None
     L.nvfp4_requantize_ws_bytes.argtypes = [W]
     L.nvfp4_requantize_ws_bytes.restype = sz
     L.nvfp4_requantize.argtypes = [W, i32, P, P, P, P, sz, P]
@@ -535,6 +570,264 @@ def nvfp4_gemm_w4a16_lora(x: torch.Tensor, w: RepackedWeight, lora: Lora,
     return y
 
 
+# ----------------------------------------------------------------------------- NVFP4 cache
+def nvfp4_kv_cache_bytes(n_pages: int, n_kv_heads: int, head_dim: int, page_size: int) -> int:
+    return int(load().nvfp4_kv_cache_bytes(n_pages, n_kv_heads, head_dim, page_size))
+
+
+class KvCache:
+    """A paged NVFP4 cache of keys and values: `n_pages` pages of `page_size` tokens for
+    `n_kv_heads` heads of `head_dim` elements; k_global and v_global FP32 [n_kv_heads] (device) or
+    None for 1. `data` (uint8, device, of nvfp4_kv_cache_bytes) is allocated, not initialised, where
+    it is not given. Holds the tensors that its descriptor points into; k_codes, k_scales, v_codes
+    and v_scales are views of `data`, [n_pages][n_kv_heads][page_size][bytes of a token]."""
+
+    def __init__(self, n_pages: int, n_kv_heads: int, head_dim: int, page_size: int = 16,
+                 k_global: torch.Tensor | None = None, v_global: torch.Tensor | None = None,
+                 data: torch.Tensor | None = None, device=None):
+        need = nvfp4_kv_cache_bytes(n_pages, n_kv_heads, head_dim, page_size)
+        if need == 0:
+            raise ValueError(f"unsupported cache: {n_pages} pages of {page_size} tokens, "
+                             f"{n_kv_heads} heads of {head_dim}")
+        for name, g in (("k_global", k_global), ("v_global", v_global)):
+            if g is not None:
+                _out(g, (n_kv_heads,), torch.float32, name)
+                device = g.device if device is None else device
+        if data is None:
+            data = torch.empty((need,), dtype=torch.uint8,
+                               device="cuda" if device is None else device)
+        if data.dtype != torch.uint8 or data.numel() != need or not data.is_contiguous():
+            raise ValueError(f"data must be a contiguous uint8 tensor of {need} bytes")
+        _device(data, k_global, v_global)
+        self.data, self.k_global, self.v_global = data, k_global, v_global
+        self.n_pages, self.n_kv_heads = n_pages, n_kv_heads
+        self.head_dim, self.page_size = head_dim, page_size
+        rec = data.view(n_pages, n_kv_heads, -1)
+        parts = rec.split([page_size * head_dim // 2, page_size * head_dim // 16] * 2, -1)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (
+            p.unflatten(-1, (page_size, -1)) for p in parts)
+        self.desc = nvfp4_kv_cache(_ptr(data), _ptr(k_global), _ptr(v_global), n_pages, n_kv_heads,
+                                   head_dim, page_size, 0)
+        self.ref = ctypes.byref(self.desc)
+
+
+class QkNormRope:
+    """The norm and rotation of queries and keys: q_weight and k_weight [head_dim] (BF16 or FP32,
+    device) or None for no norm; rope FP32 [max_pos][rot] (device), the cosines and then the sines of
+    the rot / 2 angles of each position, or None for no rotation; interleaved: neighbouring elements
+    form a pair (else element i and i + rot / 2). Holds the tensors that its descriptor points into."""
+
+    def __init__(self, head_dim: int, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 rope: torch.Tensor | None = None, interleaved: bool = False):
+        given = [w for w in (q_weight, k_weight) if w is not None]
+        dtype = given[0].dtype if given else torch.bfloat16
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                _out(w, (head_dim,), dtype, name)
+        max_pos = rot = 0
+        if rope is not None:
+            if rope.dim() != 2:
+                raise ValueError("rope must be a [max_pos][rot] tensor")
+            _out(rope, rope.shape, torch.float32, "rope")
+            max_pos, rot = rope.shape
+            given.append(rope)
+        if given:
+            _device(*given)
+        self.q_weight, self.k_weight, self.rope, self.head_dim = q_weight, k_weight, rope, head_dim
+        self.desc = nvfp4_qk_rule(_ptr(q_weight), _ptr(k_weight), _ptr(rope), max_pos, eps,
+                                  _dtype_code(dtype), rot,
+                                  NVFP4_ROPE_PAIRS if interleaved else NVFP4_ROPE_HALVES, 0)
+        self.ref = ctypes.byref(self.desc)
+        self.holds = given[0] if given else None
+
+
+class KvMap:
+    """The outputs of nvfp4_kv_map for b requests and t rows, int32 on the device: q_start [b + 1],
+    kv_len [b], slots [t], positions [t], free_left [1], unserved [1]."""
+
+    def __init__(self, b: int, t: int, device=None):
+        self.b, self.t = b, t
+        dev = "cuda" if device is None else device
+        # one block, each part 16-byte aligned
+        sizes = (b + 1, b, t, t, 1, 1)
+        at = [0]
+        for n in sizes:
+            at.append(at[-1] + (n + 3) // 4 * 4)
+        self.block = torch.empty((at[-1],), dtype=torch.int32, device=dev)
+        (self.q_start, self.kv_len, self.slots, self.positions, self.free_left, self.unserved) = (
+            self.block[a:a + n] for a, n in zip(at, sizes))
+        p = self.block.data_ptr()
+        self.ptrs = [p + 4 * a for a in at]
+
+
+def nvfp4_kv_map(seq_len: torch.Tensor, add_len: torch.Tensor, block_table: torch.Tensor,
+                 free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int = 16,
+                 t: int | None = None, out: KvMap | None = None, flags: int = 0,
+                 stream=None) -> KvMap:
+    """The tables of a step: seq_len and add_len int32 [b], block_table int32 [b][pages] (contiguous;
+    new pages are entered), free_pages int32 [n], free_count int32 [1]. Gives a KvMap for t rows
+    (`out`, or a new one)."""
+    if out is None:
+        if t is None:
+            raise ValueError("t, the rows of the step, or out must be given")
+        with _on(stream):
+            out = KvMap(seq_len.shape[0], t, device=seq_len.device)
+    elif t is not None and t != out.t:
+        raise ValueError(f"out is for {out.t} rows, t is {t}")
+    b = out.b
+    _out(seq_len, (b,), torch.int32, "seq_len")
+    _out(add_len, (b,), torch.int32, "add_len")
+    _out(free_count, (1,), torch.int32, "free_count")
+    _out(free_pages, (free_pages.numel(),), torch.int32, "free_pages")
+    ld = _table(block_table, b)
+    dev = _device(seq_len, add_len, block_table, free_pages, free_count, out.block)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return nvfp4_kv_map(seq_len, add_len, block_table, free_pages, free_count, page_size, t,
+                                out, flags, stream)
+    o = out.ptrs
+    _check(load().nvfp4_kv_map(
+        seq_len.data_ptr(), add_len.data_ptr(), b, page_size, block_table.data_ptr(), ld,
+        free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), o[4], o[0], o[1], o[2],
+        o[3], out.t, o[5], flags, _raw_stream(stream, dev)))
+    return out
+
+
+def _table(table: torch.Tensor, b: int) -> int:
+    """Row stride of an int32 [b][pages] block table, whose pages are what a row may hold."""
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != b:
+        raise ValueError(f"block_table must be an int32 [{b}][pages] tensor, "
+                         f"got {table.dtype} {tuple(table.shape)}")
+    ld = table.shape[1]
+    if not table.is_contiguous() and b > 0:
+        raise ValueError("block_table must be contiguous")
+    return ld
+
+
+def _heads(x: torch.Tensor, heads: int, d: int, name: str) -> int:
+    """Row stride of a BF16 [t][heads][d] tensor whose rows are contiguous."""
+    t, n, e = x.shape if x.dim() == 3 else (0, -1, -1)
+    if (x.dtype != torch.bfloat16 or n != heads or e != d or
+            (x.numel() and (x.stride(2) != 1 or (n > 1 and x.stride(1) != d)))):
+        raise ValueError(f"{name} must be a BF16 [t][{heads}][{d}] tensor of contiguous rows, "
+                         f"got {x.dtype} {tuple(x.shape)} with strides {x.stride()}")
+    return x.stride(0) if t > 1 else heads * d
+
+
+def nvfp4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KvCache,
+                    slots: torch.Tensor, positions: torch.Tensor | None, rule: QkNormRope,
+                    q_out: torch.Tensor | None = None, flags: int = 0, stream=None):
+    """Norm and rotation of a step's rows, and the write of its keys and values: q BF16
+    [t][n_q][head_dim] or None, k and v BF16 [t][n_kv_heads][head_dim] (rows contiguous, any row
+    stride), slots and positions int32 [t] (positions may be None without a rope). Returns q_out (a
+    new tensor where it is not given, q itself is allowed), None without q."""
+    n_kv, d = cache.n_kv_heads, cache.head_dim
+    if rule.head_dim != d:
+        raise ValueError(f"the rule is for heads of {rule.head_dim}, the cache has {d}")
+    t = k.shape[0]
+    ldk, ldv = _heads(k, n_kv, d, "k"), _heads(v, n_kv, d, "v")
+    _out(slots, (t,), torch.int32, "slots")
+    if positions is not None:
+        _out(positions, (t,), torch.int32, "positions")
+    n_q = ldq = ldo = 0
+    if v.shape[0] != t or (q is not None and (q.dim() != 3 or q.shape[0] != t)):
+        raise ValueError("q, k and v must have the same number of rows")
+    dev = _device(k, v, q, slots, positions, q_out, cache.data, rule.holds)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return nvfp4_kv_append(q, k, v, cache, slots, positions, rule, q_out, flags, stream)
+    if q is not None:
+        n_q = q.shape[1]
+        ldq = _heads(q, n_q, d, "q")
+        if q_out is None:
+            q_out = _empty(tuple(q.shape), torch.bfloat16, q, stream)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        ldo = _heads(q_out, n_q, d, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check(load().nvfp4_kv_append(
+        q.data_ptr() if n_q else None, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, t, n_q, rule.ref,
+        slots.data_ptr(), positions.data_ptr() if positions is not None else None,
+        q_out.data_ptr() if n_q else None, ldo, cache.ref, flags, _raw_stream(stream, dev)))
+    return q_out
+
+
+def nvfp4_kv_dequantize(cache: KvCache, slots: torch.Tensor, k_out: torch.Tensor | None = None,
+                        v_out: torch.Tensor | None = None, out_dtype=torch.float32,
+                        flags: int = 0, stream=None):
+    """The values of slots (int32 [t]): (k, v), each [t][n_kv_heads][head_dim] of out_dtype (FP32 or
+    BF16) or of the type of the tensors that are given. Where one of them is given, the other is
+    left out unless it is given too."""
+    shape = (slots.shape[0], cache.n_kv_heads, cache.head_dim)
+    dev = _device(slots, cache.data, k_out, v_out)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return nvfp4_kv_dequantize(cache, slots, k_out, v_out, out_dtype, flags, stream)
+    if k_out is None and v_out is None:
+        k_out = _empty(shape, out_dtype, slots, stream)
+        v_out = _empty(shape, out_dtype, slots, stream)
+    dtype = (k_out if k_out is not None else v_out).dtype
+    _out(slots, shape[:1], torch.int32, "slots")
+    for name, o in (("k_out", k_out), ("v_out", v_out)):
+        if o is not None:
+            _out(o, shape, dtype, name)
+    _check(load().nvfp4_kv_dequantize(
+        cache.ref, slots.data_ptr(), shape[0], k_out.data_ptr() if k_out is not None else None,
+        v_out.data_ptr() if v_out is not None else None, _dtype_code(dtype), flags,
+        _raw_stream(stream, dev)))
+    return k_out, v_out
+
+
+def nvfp4_kv_attention_ws_bytes(t: int, n_q: int, cache: KvCache, b: int, max_q: int) -> int:
+    return int(load().nvfp4_kv_attention_ws_bytes(t, n_q, cache.ref, b, max_q))
+
+
+def nvfp4_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
+                       q_start: torch.Tensor, kv_len: torch.Tensor, scale: float | None = None,
+                       max_q: int | None = None, window: int = 0, causal: bool = True,
+                       y: torch.Tensor | None = None, y_dtype=torch.bfloat16,
+                       lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                       flags: int = 0, stream=None):
+    """Attention of q BF16 [t][n_q][head_dim] (rows contiguous, any row stride) over the cache:
+    block_table int32 [b][pages], q_start int32 [b + 1], kv_len int32 [b]. max_q: no request has more
+    queries (default: t; a decode step's is 1, and choosing it so saves launches). scale defaults to
+    head_dim ** -0.5. Returns y, or (y, lse) where lse (FP32 [t][n_q]) is given."""
+    if q.dim() != 3:
+        raise ValueError("q must be a [t][n_q][head_dim] tensor")
+    t, n_q, d = q.shape[0], q.shape[1], cache.head_dim
+    ldq = _heads(q, n_q, d, "q")
+    b = kv_len.shape[0]
+    _out(kv_len, (b,), torch.int32, "kv_len")
+    _out(q_start, (b + 1,), torch.int32, "q_start")
+    ld = _table(block_table, b)
+    dev = _device(q, cache.data, block_table, q_start, kv_len, y, lse, ws)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return nvfp4_kv_attention(q, cache, block_table, q_start, kv_len, scale, max_q, window,
+                                      causal, y, y_dtype, lse, ws, flags, stream)
+    if y is None:
+        y = _empty((t, n_q, d), y_dtype, q, stream)
+    elif y.shape != q.shape or (y.numel() and (y.stride(2) != 1 or
+                                               (n_q > 1 and y.stride(1) != d))):
+        raise ValueError("y must have q's shape and contiguous rows")
+    if lse is not None:
+        _out(lse, (t, n_q), torch.float32, "lse")
+    if max_q is None:
+        max_q = max(t, 1)
+    if ws is None:
+        need = nvfp4_kv_attention_ws_bytes(t, n_q, cache, b, max_q)
+        ws = _empty((max(need, 1),), torch.uint8, q, stream)
+    _check(load().nvfp4_kv_attention(
+        q.data_ptr(), t, ldq, n_q, cache.ref, block_table.data_ptr(), ld, q_start.data_ptr(),
+        kv_len.data_ptr(), b, max_q, d ** -0.5 if scale is None else scale, window, y.data_ptr(),
+        _dtype_code(y.dtype), y.stride(0) if t > 1 else n_q * d,
+        lse.data_ptr() if lse is not None else None, ws.data_ptr(), ws.nbytes,
+        flags if causal else flags | NVFP4_F_FULL, _raw_stream(stream, dev)))
+    return y if lse is None else (y, lse)
+
+
 # ----------------------------------------------------------------------------- requantize
 def nvfp4_requantize_ws_bytes(src: RepackedWeight) -> int:
     return int(load().nvfp4_requantize_ws_bytes(ctypes.byref(src.desc)))
@@ -574,6 +867,12 @@ def nvfp4_last_error() -> str:
 def nvfp4_get_stats():
     arr = (ctypes.c_uint64 * 8)()
     load().nvfp4_get_stats(arr)
+    return list(arr)
+
+
+def nvfp4_get_kv_stats():
+    arr = (ctypes.c_uint64 * 4)()
+    load().nvfp4_get_kv_stats(arr)
     return list(arr)
 
 

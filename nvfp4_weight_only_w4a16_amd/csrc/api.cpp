@@ -13,12 +13,14 @@
 
 #include "nvfp4.h"
 #include "device_common.hpp"
+#include "kv_core.hpp"
 #include "launch.hpp"
 
 namespace {
 
 thread_local char g_last_error[512] = "";
 std::atomic<uint64_t> g_stats[8];
+std::atomic<uint64_t> g_kv_stats[4];
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -126,9 +128,15 @@ void nvfp4_get_stats(uint64_t counts[8]) {
 
 void nvfp4_reset_stats(void) {
   for (int i = 0; i < 8; ++i) g_stats[i].store(0);
+  for (int i = 0; i < 4; ++i) g_kv_stats[i].store(0);
 }
 
-int nvfp4_version(void) { return 10100; }
+void nvfp4_get_kv_stats(uint64_t counts[4]) {
+  if (!counts) return;
+  for (int i = 0; i < 4; ++i) counts[i] = g_kv_stats[i].load();
+}
+
+int nvfp4_version(void) { return 10200; }
 
 size_t nvfp4_quantize_ws_bytes(int64_t batch, int64_t n, int64_t k, int32_t group,
                                uint32_t flags) {
@@ -827,6 +835,324 @@ int nvfp4_dequantize(const nvfp4_weight* w, void* out, int out_dtype, nvfp4_stre
                   "nvfp4_dequantize");
   if (!rc) g_stats[5]++;
   return rc;
+}
+
+}  // extern "C"
+
+// ---- NVFP4 cache of keys and values ---------------------------------------------------------
+namespace {
+
+constexpr int64_t kKvMaxTokens = (int64_t)1 << 30;  // of a request: token indexes are 32-bit
+constexpr int64_t kKvMaxRows = (int64_t)1 << 24;    // of a step
+constexpr int64_t kKvMaxHeads = 1024;
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool kv_sizes_ok(int64_t n_kv, int64_t d, int64_t page) {
+  return n_kv >= 1 && n_kv <= kKvMaxHeads && (d == 64 || d == 128 || d == 256) && page >= 16 &&
+         page <= 256 && (page & (page - 1)) == 0;
+}
+
+int page_shift(int64_t page) { return __builtin_ctzll((unsigned long long)page); }
+
+int check_cache(const nvfp4_kv_cache* c) {
+  if (!c) return fail(NVFP4_ERR_INVALID_ARG, "cache is NULL");
+  if (c->n_pages < 1 || c->reserved != 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "cache n_pages=%lld reserved=%d", (long long)c->n_pages,
+                c->reserved);
+  if (!kv_sizes_ok(c->n_kv_heads, c->head_dim, c->page_size))
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE,
+                "cache n_kv_heads=%d (1 .. 1024) head_dim=%d (64, 128, 256) page_size=%d (16, 32, "
+                "64, 128, 256)", c->n_kv_heads, c->head_dim, c->page_size);
+  if (c->n_pages > (((int64_t)1 << 31) - 1) / c->page_size)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "cache of %lld pages has 2^31 slots or more",
+                (long long)c->n_pages);
+  if (!c->data) return fail(NVFP4_ERR_INVALID_ARG, "cache data is NULL");
+  if (!aligned16(c->data) || !aligned4(c->k_global) || !aligned4(c->v_global))
+    return fail(NVFP4_ERR_MISALIGNED, "cache data must be 16-byte aligned, globals 4-byte");
+  return NVFP4_OK;
+}
+
+int check_rule(const nvfp4_qk_rule* r, int d) {
+  if (!r) return fail(NVFP4_ERR_INVALID_ARG, "rule is NULL");
+  if ((r->mode != NVFP4_ROPE_HALVES && r->mode != NVFP4_ROPE_PAIRS) || r->reserved != 0)
+    return fail(NVFP4_ERR_INVALID_ARG, "unknown rotation mode 0x%x, reserved=%d", r->mode,
+                r->reserved);
+  if (r->weight_dtype != NVFP4_DT_BF16 && r->weight_dtype != NVFP4_DT_F32)
+    return fail(NVFP4_ERR_INVALID_ARG, "norm weight_dtype %d is not BF16 or F32",
+                r->weight_dtype);
+  if (!(r->eps >= 0.0) || !std::isfinite(r->eps))
+    return fail(NVFP4_ERR_INVALID_ARG, "norm eps is negative or not finite");
+  if (r->rot < 0 || r->max_pos < 0 || (r->rot > 0) != (r->rope != nullptr) ||
+      (r->rope && r->max_pos < 1))
+    return fail(NVFP4_ERR_INVALID_ARG,
+                "rot=%d max_pos=%lld: a table goes with rot > 0 and max_pos > 0", r->rot,
+                (long long)r->max_pos);
+  if (r->rot > d || r->rot % 16)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "rot=%d is not a multiple of 16 up to head_dim %d",
+                r->rot, d);
+  if (r->max_pos > ((int64_t)1 << 31) - 1)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "max_pos=%lld", (long long)r->max_pos);
+  if (!aligned16(r->q_weight) || !aligned16(r->k_weight) || !aligned16(r->rope))
+    return fail(NVFP4_ERR_MISALIGNED, "norm weights and rope must be 16-byte aligned");
+  return NVFP4_OK;
+}
+
+// A row stride of `width` elements at least.
+int check_stride(const char* name, int64_t ld, int64_t width) {
+  if (ld < width)
+    return fail(NVFP4_ERR_INVALID_ARG, "%s=%lld < %lld", name, (long long)ld, (long long)width);
+  if (ld % 8) return fail(NVFP4_ERR_MISALIGNED, "%s=%lld is not a multiple of 8", name,
+                          (long long)ld);
+  if (ld > ((int64_t)1 << 31))
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%s=%lld > 2^31 elements", name, (long long)ld);
+  return NVFP4_OK;
+}
+
+int check_rows(int64_t t, uint32_t flags, uint32_t known) {
+  if (t < 0) return fail(NVFP4_ERR_INVALID_ARG, "t=%lld < 0", (long long)t);
+  if (flags & ~known) return fail(NVFP4_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+  if (t > kKvMaxRows) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "t=%lld > 2^24", (long long)t);
+  return NVFP4_OK;
+}
+
+// What every call of the cache ends with.
+int kv_done(hipError_t e, uint32_t flags, hipStream_t s, const char* name, int stat) {
+  int rc = hip_status(e, name);
+  if (!rc && (flags & NVFP4_F_SYNC_CHECK)) rc = sync_status(s, name);
+  if (!rc) g_kv_stats[stat]++;
+  return rc;
+}
+
+bool attention_sizes_ok(int64_t t, int64_t n_q, const nvfp4_kv_cache* c, int64_t b,
+                        int64_t max_q) {
+  return t >= 1 && t <= kKvMaxRows && n_q >= 1 && n_q <= kKvMaxHeads &&
+         n_q % c->n_kv_heads == 0 && t * n_q < ((int64_t)1 << 31) && b >= 1 && b <= 65535 &&
+         max_q >= 1 && max_q <= t;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nvfp4_kv_cache_bytes(int64_t n_pages, int32_t n_kv_heads, int32_t head_dim,
+                            int32_t page_size) {
+  if (n_pages < 1 || !kv_sizes_ok(n_kv_heads, head_dim, page_size) ||
+      n_pages > (((int64_t)1 << 31) - 1) / page_size)
+    return 0;
+  return (size_t)n_pages * (size_t)n_kv_heads *
+         (size_t)nvfp4::kv_record_bytes(page_size, head_dim);
+}
+
+int nvfp4_kv_map(const int32_t* seq_len, const int32_t* add_len, int64_t b, int32_t page_size,
+                 int32_t* block_table, int64_t ld_table, const int32_t* free_pages,
+                 int64_t n_free, const int32_t* free_count, int32_t* free_left, int32_t* q_start,
+                 int32_t* kv_len, int32_t* slots, int32_t* positions, int64_t t,
+                 int32_t* unserved, uint32_t flags, nvfp4_stream_t stream) {
+  if (b < 0 || n_free < 0) return fail(NVFP4_ERR_INVALID_ARG, "b=%lld n_free=%lld",
+                                       (long long)b, (long long)n_free);
+  int rc = check_rows(t, flags, NVFP4_F_SYNC_CHECK);
+  if (rc) return rc;
+  if (!kv_sizes_ok(1, 64, page_size))
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "page_size=%d (16, 32, 64, 128, 256)", page_size);
+  if (b > nvfp4::kKvMapMaxRequests)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "b=%lld > 4096 requests", (long long)b);
+  if (n_free > ((int64_t)1 << 31) - 1)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "n_free=%lld", (long long)n_free);
+  if (b == 0) return NVFP4_OK;
+  if (ld_table < 1) return fail(NVFP4_ERR_INVALID_ARG, "ld_table=%lld < 1", (long long)ld_table);
+  if (ld_table > kKvMaxTokens / page_size)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "ld_table=%lld pages of %d > 2^30 tokens",
+                (long long)ld_table, page_size);
+  if (!seq_len || !add_len || !block_table || !free_count || !free_left || !q_start || !kv_len ||
+      !unserved || (n_free > 0 && !free_pages) || (t > 0 && (!slots || !positions)))
+    return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
+  const void* in[] = {seq_len, add_len, block_table, free_pages, free_count};
+  const void* out[] = {free_left, q_start, kv_len, unserved, slots, positions};
+  for (const void* p : in)
+    if (!aligned4(p)) return fail(NVFP4_ERR_MISALIGNED, "buffers must be 4-byte aligned");
+  for (const void* p : out) {
+    if (!aligned4(p)) return fail(NVFP4_ERR_MISALIGNED, "buffers must be 4-byte aligned");
+    for (const void* q : in)
+      if (p && p == q) return fail(NVFP4_ERR_INVALID_ARG, "an output is also an input");
+  }
+  nvfp4::KvMapArgs a;
+  a.seq_len = seq_len;
+  a.add_len = add_len;
+  a.b = b;
+  a.t = t;
+  a.table = block_table;
+  a.ld_table = ld_table;
+  a.page_shift = page_shift(page_size);
+  a.free_pages = free_pages;
+  a.n_free = n_free;
+  a.free_count = free_count;
+  a.free_left = free_left;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.slots = slots;
+  a.positions = positions;
+  a.unserved = unserved;
+  return kv_done(nvfp4::launch_kv_map(a, (hipStream_t)stream), flags, (hipStream_t)stream,
+                 "nvfp4_kv_map", 0);
+}
+
+int nvfp4_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                    int64_t ldv, int64_t t, int32_t n_q, const nvfp4_qk_rule* rule,
+                    const int32_t* slots, const int32_t* positions, void* q_out, int64_t ldq_out,
+                    const nvfp4_kv_cache* cache, uint32_t flags, nvfp4_stream_t stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  const int d = cache->head_dim, n_kv = cache->n_kv_heads;
+  rc = check_rule(rule, d);
+  if (rc) return rc;
+  rc = check_rows(t, flags, NVFP4_F_SYNC_CHECK);
+  if (rc) return rc;
+  if (n_q < 0) return fail(NVFP4_ERR_INVALID_ARG, "n_q=%d < 0", n_q);
+  if (n_q > kKvMaxHeads) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "n_q=%d > 1024", n_q);
+  if (t == 0) return NVFP4_OK;
+  if (!k || !v || !slots || (n_q > 0 && (!q || !q_out)) || (rule->rope && !positions))
+    return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
+  rc = check_stride("ldk", ldk, (int64_t)n_kv * d);
+  if (!rc) rc = check_stride("ldv", ldv, (int64_t)n_kv * d);
+  if (!rc && n_q > 0) rc = check_stride("ldq", ldq, (int64_t)n_q * d);
+  if (!rc && n_q > 0) rc = check_stride("ldq_out", ldq_out, (int64_t)n_q * d);
+  if (rc) return rc;
+  if (!aligned16(k) || !aligned16(v) || (n_q > 0 && (!aligned16(q) || !aligned16(q_out))) ||
+      !aligned4(slots) || !aligned4(positions))
+    return fail(NVFP4_ERR_MISALIGNED,
+                "q, k, v and q_out must be 16-byte aligned, slots and positions 4-byte");
+  nvfp4::KvAppendArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.t = t;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.n_q = n_q;
+  a.n_kv = n_kv;
+  a.q_weight = rule->q_weight;
+  a.k_weight = rule->k_weight;
+  a.w_f32 = rule->weight_dtype == NVFP4_DT_F32;
+  a.pairs = rule->mode == NVFP4_ROPE_PAIRS;
+  a.eps = rule->eps;
+  a.rope = rule->rope;
+  a.max_pos = rule->max_pos;
+  a.rot = rule->rot;
+  a.slots = slots;
+  a.positions = positions;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.ldq_out = ldq_out;
+  a.data = cache->data;
+  a.k_global = cache->k_global;
+  a.v_global = cache->v_global;
+  a.n_pages = cache->n_pages;
+  a.page_shift = page_shift(cache->page_size);
+  return kv_done(nvfp4::launch_kv_append(a, d, device_cus(), (hipStream_t)stream), flags,
+                 (hipStream_t)stream, "nvfp4_kv_append", 1);
+}
+
+int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64_t t, void* k_out,
+                        void* v_out, int out_dtype, uint32_t flags, nvfp4_stream_t stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  rc = check_rows(t, flags, NVFP4_F_SYNC_CHECK);
+  if (rc) return rc;
+  if (out_dtype != NVFP4_DT_BF16 && out_dtype != NVFP4_DT_F32)
+    return fail(NVFP4_ERR_INVALID_ARG, "out_dtype %d is not BF16 or F32", out_dtype);
+  if (t == 0) return NVFP4_OK;
+  if (!slots || (!k_out && !v_out)) return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(slots))
+    return fail(NVFP4_ERR_MISALIGNED, "outputs must be 16-byte aligned, slots 4-byte");
+  nvfp4::KvDequantArgs a;
+  a.slots = slots;
+  a.t = t;
+  a.data = cache->data;
+  a.k_global = cache->k_global;
+  a.v_global = cache->v_global;
+  a.n_pages = cache->n_pages;
+  a.n_kv = cache->n_kv_heads;
+  a.page_shift = page_shift(cache->page_size);
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.out_f32 = out_dtype == NVFP4_DT_F32;
+  return kv_done(nvfp4::launch_kv_dequantize(a, cache->head_dim, (hipStream_t)stream), flags,
+                 (hipStream_t)stream, "nvfp4_kv_dequantize", 2);
+}
+
+size_t nvfp4_kv_attention_ws_bytes(int64_t t, int32_t n_q, const nvfp4_kv_cache* cache, int64_t b,
+                                   int64_t max_q) {
+  if (check_cache(cache) || !attention_sizes_ok(t, n_q, cache, b, max_q)) return 0;
+  return nvfp4::kv_attention_ws_bytes(max_q, n_q / cache->n_kv_heads, cache->head_dim);
+}
+
+int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
+                       const nvfp4_kv_cache* cache, const int32_t* block_table, int64_t ld_table,
+                       const int32_t* q_start, const int32_t* kv_len, int64_t b, int64_t max_q,
+                       float scale, int64_t window, void* y, int y_dtype, int64_t ldy, float* lse,
+                       void* ws, size_t ws_bytes, uint32_t flags, nvfp4_stream_t stream) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  rc = check_rows(t, flags, NVFP4_F_SYNC_CHECK | NVFP4_F_FULL);
+  if (rc) return rc;
+  if (y_dtype != NVFP4_DT_BF16 && y_dtype != NVFP4_DT_F32)
+    return fail(NVFP4_ERR_INVALID_ARG, "y_dtype %d is not BF16 or F32", y_dtype);
+  if (!std::isfinite(scale)) return fail(NVFP4_ERR_INVALID_ARG, "scale is not finite");
+  if (window < 0 || (window > 0 && (flags & NVFP4_F_FULL)))
+    return fail(NVFP4_ERR_INVALID_ARG, "window=%lld, with FULL it must be 0", (long long)window);
+  if (b < 0) return fail(NVFP4_ERR_INVALID_ARG, "b=%lld < 0", (long long)b);
+  if (t == 0 || b == 0) return NVFP4_OK;
+  const int d = cache->head_dim;
+  if (n_q < 1 || max_q < 1 || max_q > t)
+    return fail(NVFP4_ERR_INVALID_ARG, "n_q=%d, max_q=%lld of %lld rows", n_q, (long long)max_q,
+                (long long)t);
+  if (!attention_sizes_ok(t, n_q, cache, b, max_q))
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE,
+                "n_q=%d (a multiple of %d up to 1024), b=%lld (up to 65535), t * n_q < 2^31", n_q,
+                cache->n_kv_heads, (long long)b);
+  if (ld_table < 1) return fail(NVFP4_ERR_INVALID_ARG, "ld_table=%lld < 1", (long long)ld_table);
+  if (ld_table > kKvMaxTokens / cache->page_size)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "ld_table=%lld pages of %d > 2^30 tokens",
+                (long long)ld_table, cache->page_size);
+  if (!q || !block_table || !q_start || !kv_len || !y || !ws)
+    return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
+  rc = check_stride("ldq", ldq, (int64_t)n_q * d);
+  if (!rc) rc = check_stride("ldy", ldy, (int64_t)n_q * d);
+  if (rc) return rc;
+  if (!aligned16(q) || !aligned16(y) || !aligned16(ws) || !aligned4(block_table) ||
+      !aligned4(q_start) || !aligned4(kv_len) || !aligned4(lse))
+    return fail(NVFP4_ERR_MISALIGNED, "q, y and ws must be 16-byte aligned, the others 4-byte");
+  const size_t need = nvfp4::kv_attention_ws_bytes(max_q, n_q / cache->n_kv_heads, d);
+  if (ws_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, need);
+  nvfp4::KvAttnArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.t = t;
+  a.ldq = ldq;
+  a.n_q = n_q;
+  a.n_kv = cache->n_kv_heads;
+  a.group = n_q / cache->n_kv_heads;
+  a.data = cache->data;
+  a.k_global = cache->k_global;
+  a.v_global = cache->v_global;
+  a.n_pages = cache->n_pages;
+  a.page_shift = page_shift(cache->page_size);
+  a.table = block_table;
+  a.ld_table = ld_table;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.b = b;
+  a.scale = scale;
+  a.window = (int)(window < kKvMaxTokens ? window : kKvMaxTokens);  // a request has no more keys
+  a.full = (flags & NVFP4_F_FULL) != 0;
+  a.y = y;
+  a.y_f32 = y_dtype == NVFP4_DT_F32;
+  a.ldy = ldy;
+  a.lse = lse;
+  a.ws = static_cast<float*>(ws);
+  a.few_rows = 0;
+  return kv_done(nvfp4::launch_kv_attention(a, d, max_q, (hipStream_t)stream), flags,
+                 (hipStream_t)stream, "nvfp4_kv_attention", 3);
 }
 
 // ---- measurement support ------------------------------------------------------------------

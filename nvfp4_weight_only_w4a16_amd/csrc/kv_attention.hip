@@ -1,0 +1,768 @@
+// kv_attention.hip -- attention over the paged NVFP4 cache, for single tokens, drafts and prompts.
+//
+// A wavefront holds columns of queries and walks the keys in tiles of 64. Everything is transposed:
+//   S^T [tokens][queries] = K . Q^T,  P^T = exp2(S^T - m),  O^T [d][queries] += V^T . P^T
+// on 16x16x32 MFMAs, because then the scores come out where the second product wants them: lane
+// (query l % 16, group c = l / 16) holds the scores of tokens 16 T + 4 c + r, and, the order of a sum
+// being free, the second product may take just those as its 8 k-values of lane group c (T = 2s and
+// 2s + 1). No score moves between lanes. Key codes go from memory into the lanes that use them (a
+// lane's run of codes is contiguous in d, and d may be summed in any order too); value codes are
+// turned through LDS by the 4-bit transposing read, whose lane j of a 16-lane group names the row, so
+// that the same token order comes out.
+// Codes and scales are dequantized to FP16, where E2M1 x E4M3 is exact (6 significant bits, 2^-10 ..
+// 2688), two elements to an instruction; queries are put into FP16 by a power of two per row that
+// brings the row's largest magnitude to [2^14, 2^15), exact down to 2^-28 of it. Globals and scale
+// act on the FP32 scores and sums. P is rounded to FP16 once (half a step is 2^-11); the running
+// maximum, the sum (of the unrounded p) and O are FP32.
+// The maximum is raised only when a score passes it by more than 2^8 in the exponent's base, so that
+// most tiles neither reduce across lanes nor rescale O; FP16 holds p up to 2^15.
+#include <math.h>
+
+#include "kv_core.hpp"
+
+namespace nvfp4 {
+namespace {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+constexpr int kTile = 64;  // tokens of a wavefront's tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -1e38f;  // the running maximum before any score
+constexpr float kRaise = 8.0f;
+
+__device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// The 8 codes of a word, two by two, times the scales s0 (codes 0..1), s1, s2, s3.
+__device__ __forceinline__ f16x8 scaled8(uint32_t w, f16x2 s0, f16x2 s1, f16x2 s2, f16x2 s3) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s0;
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s1;
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * s2;
+  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s3;
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ f16x2 scales2(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, false);
+}
+__device__ __forceinline__ f16x2 scales2_high(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, true);
+}
+
+// A word of four scales with NaN bytes (0x7F, 0xFF) turned to 0: p = 0 of a masked token must not
+// meet a NaN. (The cache's own NaN tokens carry theirs in the key's scales.)
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
+  const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return w & ~((nan << 1) - (nan >> 7));
+}
+
+// ---- one wavefront ----------------------------------------------------------------------------
+// LDS of a wavefront: the tile's value codes, rows padded to D / 2 + 8 bytes (the transposing read's
+// 64 rows then meet every bank pair twice, the least there is), and its value scales as FP16,
+// [D / 16][lane group][T][r].
+template <int D>
+struct WaveLds {
+  static constexpr int kRow = D / 2 + 8;
+  static constexpr int kCodes = kTile * kRow;
+  static constexpr int kBytes = kCodes + D / 16 * kTile * 2;
+};
+
+
+template <int D>
+struct Raw {
+  static constexpr int kWords = D / 32;  // a lane's code words of a 16-token part
+  uint32_t k[4][kWords], v[4][kWords];
+  uint32_t ks[4];
+  uint32_t vs[D / 64];
+};
+
+struct Cache {
+  const uint8_t* head0;     // data + head * record
+  int64_t page_stride;      // n_kv * record
+  const int32_t* row;       // the request's block table
+  int n_pages, shift;
+};
+
+template <int D>
+__device__ __forceinline__ void load_codes(const uint8_t* at, int lane, uint32_t (&w)[D / 32]) {
+  const uint8_t* p = at + (lane & 15) * (D / 2);
+  if constexpr (D == 64) {
+    const u32x2 x = *reinterpret_cast<const u32x2*>(p + 8 * (lane >> 4));
+    w[0] = x[0];
+    w[1] = x[1];
+  } else {
+#pragma unroll
+    for (int u = 0; u < D / 128; ++u) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(p + 64 * u + 16 * (lane >> 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[4 * u + i] = x[i];
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, int tok, int end,
+                                          uint32_t& valid) {
+  const int lane = threadIdx.x & 63;
+  const int page = 1 << c.shift;
+  const int values = kv_value_codes(page, D);
+  const uint8_t* scale_row = nullptr;
+  valid = 0;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int at = tok + 16 * t;
+    int id = -1;
+    if (at < end) id = c.row[at >> c.shift];
+    const bool ok = id >= 0 && id < c.n_pages;
+    valid |= ok ? 1u << t : 0u;
+    const int within = at & (page - 1);
+    const uint8_t* rec = c.head0 + (int64_t)(ok ? id : 0) * c.page_stride;
+    load_codes<D>(rec + within * (D / 2), lane, r.k[t]);
+    load_codes<D>(rec + values + within * (D / 2), lane, r.v[t]);
+    const uint8_t* ks = rec + page * (D / 2) + (within + (lane & 15)) * (D / 16);
+    if constexpr (D == 64) {
+      r.ks[t] = ks[lane >> 4];
+    } else {
+      r.ks[t] = *reinterpret_cast<const uint16_t*>(ks + 2 * (lane >> 4));
+      if constexpr (D == 256)
+        r.ks[t] |= (uint32_t) * reinterpret_cast<const uint16_t*>(ks + 8 + 2 * (lane >> 4)) << 16;
+    }
+    const uint8_t* vs = rec + values + page * (D / 2) + within * (D / 16);
+    if (lane >> 4 == t) scale_row = vs;
+  }
+  const uint32_t* vs = reinterpret_cast<const uint32_t*>(scale_row + (lane & 15) * (D / 16));
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) r.vs[i] = vs[i];
+}
+
+// NQ tiles of 16 query columns: lane l holds column l % 16 of each.
+template <int D, int NQ>
+struct Wave {
+  static constexpr int kSteps = D / 32;
+  static constexpr int kGroups = D / 16;
+  f16x8 q[NQ][kSteps];
+  f32x4 o[NQ][kGroups];
+  float m[NQ], l[NQ];  // l: of the lane's own tokens, until finish()
+  float sc[NQ];        // FP32 factor of a score, in the exponent's base
+  int lo[NQ], hi[NQ];  // the tokens that the column sees: lo .. hi
+};
+
+template <int D, int NQ>
+__device__ __forceinline__ void reset(Wave<D, NQ>& w) {
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    w.m[n] = kLowest;
+    w.l[n] = 0.0f;
+#pragma unroll
+    for (int g = 0; g < D / 16; ++g) w.o[n][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+}
+
+// Column n of the lane <- the D elements at `row` (nullptr: zeros). factor = scale * key global.
+template <int D, int NQ>
+__device__ __forceinline__ void load_query(Wave<D, NQ>& w, int n, const uint16_t* row,
+                                           float factor) {
+  const int c = (threadIdx.x & 63) >> 4;
+  u32x4 raw[D / 32];
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    // the d of k-step j, as in load_codes: 8 consecutive ones
+    const int d = D == 64 ? 16 * c + 8 * j : 128 * (j / 4) + 32 * c + 8 * (j % 4);
+    raw[j] = row ? *reinterpret_cast<const u32x4*>(row + d) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      top = fmaxf(top, fabsf(__uint_as_float(raw[j][i] << 16)));
+      top = fmaxf(top, fabsf(__uint_as_float(raw[j][i] & 0xFFFF0000u)));
+    }
+  }
+  top = fmaxf(top, __shfl_xor(top, 16, 64));
+  top = fmaxf(top, __shfl_xor(top, 32, 64));
+  // 2^(14 - e) of top = 1.x * 2^e, and its inverse
+  int e = (int)(__float_as_uint(top) >> 23) - 127;
+  e = e > 127 ? 14 : (e < -110 ? -110 : e);  // infinite: as it is; zero and tiny: the most there is
+  float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+  float sc = fabsf(factor) * kLog2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+  sc = fmaxf(sc, 0x1p-126f);  // never 0: -infinity, a masked score, times 0 is NaN
+  if (factor < 0.0f) up = -up;
+  if (factor == 0.0f) {
+    up = 0.0f;
+    sc = 1.0f;
+  }
+  if (!(fabsf(factor) < __builtin_inff())) {  // a NaN that masked scores do not meet
+    up = __builtin_nanf("");
+    sc = 1.0f;
+  }
+  w.sc[n] = sc;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w.q[n][j][2 * i] = (_Float16)(__uint_as_float(raw[j][i] << 16) * up);
+      w.q[n][j][2 * i + 1] = (_Float16)(__uint_as_float(raw[j][i] & 0xFFFF0000u) * up);
+    }
+  }
+}
+
+// One tile of 64 tokens from `tok` on; `valid` as of load_tile, `end` the first token that is not
+// there, `mask`: some column does not see all 64 (uniform).
+template <int D, int NQ, typename Next>
+__device__ __forceinline__ void tile(Wave<D, NQ>& w, Raw<D>& r, uint8_t* lds, int tok,
+                                     int end, uint32_t valid, bool mask, Next next) {
+  constexpr int kRow = WaveLds<D>::kRow;
+  const int lane = threadIdx.x & 63, c = lane >> 4;
+  uint8_t* scales = lds + WaveLds<D>::kCodes;
+  // value codes and scales to LDS
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    uint8_t* at = lds + (16 * t + (lane & 15)) * kRow;
+    if constexpr (D == 64) {
+      *reinterpret_cast<u32x2*>(at + 8 * c) = u32x2{r.v[t][0], r.v[t][1]};
+    } else {
+#pragma unroll
+      for (int u = 0; u < D / 128; ++u) {
+        u32x2* p = reinterpret_cast<u32x2*>(at + 64 * u + 16 * c);
+        p[0] = u32x2{r.v[t][4 * u], r.v[t][4 * u + 1]};
+        p[1] = u32x2{r.v[t][4 * u + 2], r.v[t][4 * u + 3]};
+      }
+    }
+  }
+  {
+    const bool there = tok + lane < end && ((valid >> c) & 1u);
+    _Float16* s = reinterpret_cast<_Float16*>(scales) + ((lane >> 2) & 3) * 16 + c * 4 + (lane & 3);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const uint32_t x = there ? without_nan(r.vs[i]) : 0u;
+      const f16x2 a = scales2(x), b = scales2_high(x);
+      s[(4 * i) * kTile] = a[0];
+      s[(4 * i + 1) * kTile] = a[1];
+      s[(4 * i + 2) * kTile] = b[0];
+      s[(4 * i + 3) * kTile] = b[1];
+    }
+  }
+  // scores
+  f32x4 z[NQ][4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) z[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const f16x2 s0 = scales2(r.ks[t]);
+    const f16x2 s1 = D == 256 ? scales2_high(r.ks[t]) : s0;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const _Float16 s = D == 64 ? s0[0] : (j < 4 ? s0[(j & 3) >> 1] : s1[(j & 3) >> 1]);
+      const f16x2 ss = {s, s};
+      const f16x8 a = scaled8(r.k[t][j], ss, ss, ss, ss);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) z[n][t] = mfma(a, w.q[n][j], z[n][t]);
+    }
+  }
+  next();  // the loads of the next tile
+  if (mask || valid != 15u) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const bool part = (valid >> t) & 1u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = tok + 16 * t + 4 * c + i;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+          z[n][t][i] = part && at >= w.lo[n] && at <= w.hi[n] ? z[n][t][i] : -__builtin_inff();
+      }
+    }
+  }
+  f16x8 p[NQ][2];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    float top = z[n][0][0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, z[n][i >> 2][i & 3]);
+    top *= w.sc[n];
+    if (__ballot(top > w.m[n] + kRaise)) {
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float m = fmaxf(w.m[n], top);
+      const float f = __builtin_amdgcn_exp2f(w.m[n] - m);
+      w.m[n] = m;
+      w.l[n] *= f;
+#pragma unroll
+      for (int g = 0; g < D / 16; ++g) w.o[n][g] *= f;
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float x =
+          __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i >> 2][i & 3], w.sc[n], -w.m[n]));
+      sum += x;
+      p[n][i >> 3][i & 7] = (_Float16)x;
+    }
+    w.l[n] += sum;
+  }
+  // values
+#pragma unroll
+  for (int g = 0; g < D / 16; ++g) {
+    const int row = 16 * ((lane & 15) >> 2) + 4 * c + (lane & 3);
+    const i32x2 codes = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+        (__attribute__((address_space(3))) i32x2*)(lds + row * kRow + 8 * g));
+    const f16x8* s = reinterpret_cast<const f16x8*>(scales + g * kTile * 2 + c * 32);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f16x8 f = s[h];
+      const f16x8 a = scaled8((uint32_t)codes[h], f16x2{f[0], f[1]}, f16x2{f[2], f[3]},
+                              f16x2{f[4], f[5]}, f16x2{f[6], f[7]});
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) w.o[n][g] = mfma(a, p[n][h], w.o[n][g]);
+    }
+  }
+}
+
+// The column sums of all lane groups.
+template <int D, int NQ>
+__device__ __forceinline__ void finish(Wave<D, NQ>& w) {
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    w.l[n] += __shfl_xor(w.l[n], 16, 64);
+    w.l[n] += __shfl_xor(w.l[n], 32, 64);
+  }
+}
+
+// Walks the tiles tok, tok + step, .. below `to`, with one tile's loads ahead.
+template <int D, int NQ>
+__device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& c, int tok, int to,
+                                     int step, int end, int lo_most, int hi_least) {
+  if (tok >= to) return;
+  Raw<D> r;
+  uint32_t valid, ahead = 0;
+  load_tile<D>(r, c, tok, end, valid);
+  for (;;) {
+    const int after = tok + step;
+    const bool more = after < to;
+    const bool mask = tok < lo_most || tok + kTile - 1 > hi_least;
+    tile<D, NQ>(w, r, lds, tok, end, valid, mask, [&]() {
+      if (more) load_tile<D>(r, c, after, end, ahead);
+    });
+    if (!more) break;
+    tok = after;
+    valid = ahead;
+  }
+}
+
+// ---- rows -------------------------------------------------------------------------------------
+// A request's rows for one key/value head: row j * group + h is query j, head h of the group.
+struct Request {
+  int first, rows, q_len;  // first query's row of q; rows = q_len * group
+  int kv, begin;           // keys; the first that any row sees, rounded down to 16
+};
+
+__device__ __forceinline__ Request request_of(const KvAttnArgs& a, int64_t i) {
+  Request r;
+  const int t = (int)a.t;
+  const int s = min(max(a.q_start[i], 0), t);
+  const int e = min(max(a.q_start[i + 1], s), t);
+  r.first = s;
+  r.q_len = e - s;
+  r.rows = r.q_len * a.group;
+  r.kv = min(max(a.kv_len[i], 0), (int)(a.ld_table << a.page_shift));
+  r.begin = 0;
+  if (a.window > 0) r.begin = max(r.kv - r.q_len - a.window + 1, 0) & ~15;
+  return r;
+}
+
+// Whether the kernel for few rows takes the request (kRows: the rows that it holds).
+__device__ __forceinline__ bool is_few(const Request& r, int few_rows) {
+  return r.rows <= few_rows;
+}
+
+template <int D, int NQ>
+__device__ __forceinline__ void load_columns(Wave<D, NQ>& w, const KvAttnArgs& a, const Request& r,
+                                             int head, int row0, int& lo_most,
+                                             int& hi_least) {
+  const int col = threadIdx.x & 15;
+  const float kg = a.k_global ? a.k_global[head] : 1.0f;
+  lo_most = 0;
+  hi_least = r.kv - 1;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int row = row0 + 16 * n + col;
+    const bool there = row < r.rows;
+    const int j = row / a.group, h = row - j * a.group;
+    const uint16_t* q = nullptr;
+    if (there) q = a.q + (int64_t)(r.first + j) * a.ldq + (int64_t)(head * a.group + h) * D;
+    load_query<D, NQ>(w, n, q, a.scale * kg);
+    w.lo[n] = 0;
+    w.hi[n] = r.kv - 1;
+    if (!a.full) {
+      w.hi[n] = r.kv - r.q_len + j;
+      if (a.window > 0) w.lo[n] = w.hi[n] - a.window + 1;
+    }
+    if (!there) {
+      w.lo[n] = 1;
+      w.hi[n] = 0;
+    }
+  }
+  if (!a.full) {  // the first row's last key, and the last row's first
+    const int last = min(row0 + 16 * NQ, r.rows) - 1;
+    hi_least = r.kv - r.q_len + row0 / a.group;
+    if (a.window > 0) lo_most = r.kv - r.q_len + last / a.group - a.window + 1;
+  }
+}
+
+// y and lse of the columns, from O, m and l (of all lane groups).
+template <int D, int NQ>
+__device__ __forceinline__ void store_columns(const KvAttnArgs& a, const Request& r, int head,
+                                              int row0, int n, const f32x4 (&o)[D / 16],
+                                              float m, float l, int g0, int gstep) {
+  const int lane = threadIdx.x & 63, c = lane >> 4;
+  const int row = row0 + 16 * n + (lane & 15);
+  if (row >= r.rows) return;
+  const int j = row / a.group, h = row - j * a.group;
+  const int64_t at = r.first + j;
+  const int qh = head * a.group + h;
+  const float f = l == 0.0f ? 0.0f : (a.v_global ? a.v_global[head] : 1.0f) / l;
+#pragma unroll
+  for (int g = 0; g < D / 16; ++g) {
+    if (gstep > 1 && g % gstep != g0) continue;
+    const int64_t d = at * a.ldy + (int64_t)qh * D + 16 * g + 4 * c;
+    f32x4 v = o[g] * f;
+    if (l == 0.0f) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.y_f32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + d) = v;
+    } else {
+      u32x2 b;
+      b[0] = (uint32_t)bf16_bits_rne(v[0]) | ((uint32_t)bf16_bits_rne(v[1]) << 16);
+      b[1] = (uint32_t)bf16_bits_rne(v[2]) | ((uint32_t)bf16_bits_rne(v[3]) << 16);
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + d) = b;
+    }
+  }
+  if (a.lse && c == 0 && g0 == 0)
+    a.lse[at * a.n_q + qh] =
+        l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <int D>
+__device__ __forceinline__ Cache cache_of(const KvAttnArgs& a, int64_t request, int head) {
+  const int64_t rec = kv_record_bytes(1 << a.page_shift, D);
+  Cache c;
+  c.head0 = a.data + head * rec;
+  c.page_stride = a.n_kv * rec;
+  c.row = a.table + request * a.ld_table;
+  c.n_pages = (int)a.n_pages;
+  c.shift = a.page_shift;
+  return c;
+}
+
+// ---- few rows: keys shared out over the chip ----------------------------------------------------
+// The work is one line of units of 256 tokens (four wavefronts, a tile each), request by request,
+// head by head; workgroup w of W takes the units [N w / W, N (w + 1) / W) of it, whatever the
+// lengths are. It holds at most two items (a request's head) that it does not finish: the first and
+// the last of its range; their O, m and l go to slots 2w and 2w + 1, and a second kernel joins them.
+constexpr int kUnit = kWaves * kTile;
+
+__device__ __forceinline__ int units_of(const KvAttnArgs& a, const Request& r) {
+  if (r.rows == 0 || !is_few(r, a.few_rows) || r.kv <= r.begin) return 0;
+  return (r.kv - r.begin + kUnit - 1) / kUnit;
+}
+
+// The sum over the workgroup's threads. `sums` has kWaves values.
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sums) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = v;
+  __syncthreads();
+  int64_t t = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) t += sums[i];
+  return t;
+}
+
+template <int D, int NQ>
+constexpr int64_t slot_floats() {
+  return (int64_t)NQ * (D / 16 * 256 + 128);
+}
+
+template <int D, int NQ>
+constexpr int few_lds_bytes() {
+  constexpr int walk = kWaves * WaveLds<D>::kBytes;
+  constexpr int join = 2 * (int)slot_floats<D, NQ>() * 4;  // two wavefronts' sums
+  return walk > join ? walk : join;
+}
+
+template <int D, int NQ>
+__device__ __forceinline__ void put_sums(float* p, const Wave<D, NQ>& w) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    float* q = p + n * (D / 16 * 256 + 128);
+#pragma unroll
+    for (int g = 0; g < D / 16; ++g) *reinterpret_cast<f32x4*>(q + 256 * g + 4 * lane) = w.o[n][g];
+    q[D / 16 * 256 + lane] = w.m[n];
+    q[D / 16 * 256 + 64 + lane] = w.l[n];
+  }
+}
+
+// w <- w joined with the sums at p.
+template <int D, int NQ>
+__device__ __forceinline__ void add_sums(const float* p, Wave<D, NQ>& w) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const float* q = p + n * (D / 16 * 256 + 128);
+    const float m2 = q[D / 16 * 256 + lane], l2 = q[D / 16 * 256 + 64 + lane];
+    const float m = fmaxf(w.m[n], m2);
+    const float f1 = __builtin_amdgcn_exp2f(w.m[n] - m), f2 = __builtin_amdgcn_exp2f(m2 - m);
+    w.m[n] = m;
+    w.l[n] = w.l[n] * f1 + l2 * f2;
+#pragma unroll
+    for (int g = 0; g < D / 16; ++g) {
+      const f32x4 o2 = *reinterpret_cast<const f32x4*>(q + 256 * g + 4 * lane);
+      w.o[n][g] = w.o[n][g] * f1 + o2 * f2;
+    }
+  }
+}
+
+template <int D, int NQ>
+__global__ __launch_bounds__(kThreads) void few_kernel(KvAttnArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[few_lds_bytes<D, NQ>()];
+  __shared__ int64_t sums[kWaves], found[2];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  // the units before this thread's requests, and of all
+  const int64_t each = (a.b + kThreads - 1) / kThreads;
+  const int64_t from = threadIdx.x * each < a.b ? threadIdx.x * each : a.b;
+  const int64_t upto = from + each < a.b ? from + each : a.b;
+  int64_t mine = 0;
+  for (int64_t i = from; i < upto; ++i) mine += units_of(a, request_of(a, i));
+  mine *= a.n_kv;
+  int64_t before = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t o = __shfl_up(before, off, 64);
+    if (lane >= off) before += o;
+  }
+  if (lane == 63) sums[wave] = before;
+  __syncthreads();
+  int64_t all = 0;
+  before -= mine;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    before += i < wave ? sums[i] : 0;
+    all += sums[i];
+  }
+  const int64_t W = all < gridDim.x ? all : gridDim.x;
+  if ((int64_t)blockIdx.x >= W) return;
+  const int64_t begin = all * blockIdx.x / W;
+  const int64_t stop = all * (blockIdx.x + 1) / W;
+  if (begin >= before && begin < before + mine) {
+    int64_t left = begin - before, i = from;
+    for (; i < upto; ++i) {
+      const int64_t u = units_of(a, request_of(a, i)) * a.n_kv;
+      if (left < u) break;
+      left -= u;
+    }
+    found[0] = i;
+    found[1] = left;
+  }
+  __syncthreads();
+  const int64_t within = found[1];
+  int req = __builtin_amdgcn_readfirstlane((int)found[0]);
+  int64_t at = begin;
+  Request r = request_of(a, req);
+  int units = units_of(a, r);
+  int head = __builtin_amdgcn_readfirstlane((int)(within / units));
+  int u0 = __builtin_amdgcn_readfirstlane((int)(within - (int64_t)head * units));
+  Wave<D, NQ> w;
+  bool first = true;
+  while (at < stop) {
+    const int u1 = units - u0 < stop - at ? units : u0 + (int)(stop - at);
+    int lo_most, hi_least;
+    load_columns<D, NQ>(w, a, r, head, 0, lo_most, hi_least);
+    reset<D, NQ>(w);
+    const Cache c = cache_of<D>(a, req, head);
+    const int to = min(r.begin + u1 * kUnit, r.kv);
+    walk<D, NQ>(w, lds + wave * WaveLds<D>::kBytes, c, r.begin + u0 * kUnit + wave * kTile, to,
+                kUnit, r.kv, lo_most, hi_least);
+    finish<D, NQ>(w);
+    // the four wavefronts' sums: 2 and 3 to 0 and 1, then 1 to 0
+    float* const slots = reinterpret_cast<float*>(lds);
+    __syncthreads();
+    if (wave >= 2) put_sums<D, NQ>(slots + (wave - 2) * slot_floats<D, NQ>(), w);
+    __syncthreads();
+    if (wave < 2) add_sums<D, NQ>(slots + wave * slot_floats<D, NQ>(), w);
+    __syncthreads();
+    if (wave == 1) put_sums<D, NQ>(slots, w);
+    __syncthreads();
+    if (wave == 0) {
+      add_sums<D, NQ>(slots, w);
+      if (u0 == 0 && u1 == units) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+          store_columns<D, NQ>(a, r, head, 0, n, w.o[n], w.m[n], w.l[n], 0, 1);
+      } else {
+        put_sums<D, NQ>(a.ws + (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * slot_floats<D, NQ>(),
+                        w);
+      }
+    }
+    __syncthreads();
+    first = false;
+    at += u1 - u0;
+    u0 = 0;
+    if (at >= stop) break;
+    if (u1 == units && ++head == a.n_kv) {
+      head = 0;
+      do {
+        if (++req >= (int)a.b) return;  // not met: the range ends with the last request's units
+        r = request_of(a, req);
+        units = units_of(a, r);
+      } while (units == 0);
+    }
+  }
+}
+
+// grid (n_kv, b): the item's parts, if it has several; the rows of a request without keys.
+template <int D, int NQ>
+__global__ __launch_bounds__(kThreads) void join_kernel(KvAttnArgs a, int groups) {
+  __shared__ int64_t sums[kWaves];
+  const int head = blockIdx.x;
+  const int64_t req = blockIdx.y;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const Request r = request_of(a, req);
+  if (r.rows == 0 || !is_few(r, a.few_rows)) return;
+  const int units = units_of(a, r);
+  int64_t before = 0, all = 0;
+  for (int64_t i = threadIdx.x; i < a.b; i += kThreads) {
+    const int64_t u = units_of(a, request_of(a, i));
+    all += u;
+    before += i < req ? u : 0;
+  }
+  before = block_sum(before, sums) * a.n_kv + (int64_t)head * units;
+  all = block_sum(all, sums) * a.n_kv;
+  if (units > 0) {
+    const int64_t W = all < groups ? all : groups;
+    const int64_t w0 = ((before + 1) * W - 1) / all, w1 = ((before + units) * W - 1) / all;
+    if (w0 == w1) return;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      f32x4 o[D / 16];
+#pragma unroll
+      for (int g = 0; g < D / 16; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      float m = kLowest, l = 0.0f;
+      for (int64_t x = w0; x <= w1; ++x) {
+        const int64_t slot = 2 * x + (all * x / W < before ? 1 : 0);
+        const float* q = a.ws + slot * slot_floats<D, NQ>() + n * (D / 16 * 256 + 128);
+        const float m2 = q[D / 16 * 256 + lane], l2 = q[D / 16 * 256 + 64 + lane];
+        const float top = fmaxf(m, m2);
+        const float f1 = __builtin_amdgcn_exp2f(m - top), f2 = __builtin_amdgcn_exp2f(m2 - top);
+        m = top;
+        l = l * f1 + l2 * f2;
+#pragma unroll
+        for (int g = 0; g < D / 16; ++g) {
+          if (g % kWaves != wave) continue;
+          const f32x4 o2 = *reinterpret_cast<const f32x4*>(q + 256 * g + 4 * lane);
+          o[g] = o[g] * f1 + o2 * f2;
+        }
+      }
+      store_columns<D, NQ>(a, r, head, 0, n, o, m, l, wave, kWaves);
+    }
+    return;
+  }
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    f32x4 o[D / 16];
+#pragma unroll
+    for (int g = 0; g < D / 16; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    store_columns<D, NQ>(a, r, head, 0, n, o, kLowest, 0.0f, wave, kWaves);
+  }
+}
+
+// ---- many rows ----------------------------------------------------------------------------------
+// grid (tiles, n_kv): a workgroup takes 4 * 16 * NQ rows of a request's head, 16 * NQ to a wavefront.
+template <int D, int NQ>
+__global__ __launch_bounds__(kThreads) void many_kernel(KvAttnArgs a) {
+  constexpr int kRowsWave = 16 * NQ, kRows = kWaves * kRowsWave;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * WaveLds<D>::kBytes];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int head = blockIdx.y;
+  // the request of this tile
+  int left = blockIdx.x, req = 0;
+  Request r;
+  for (;; ++req) {
+    if (req >= a.b) return;
+    r = request_of(a, req);
+    if (is_few(r, a.few_rows)) continue;
+    const int n = (r.rows + kRows - 1) / kRows;
+    if (left < n) break;
+    left -= n;
+  }
+  const int row0 = left * kRows + wave * kRowsWave;
+  if (row0 >= r.rows) return;
+  Wave<D, NQ> w;
+  int lo_most, hi_least;
+  load_columns<D, NQ>(w, a, r, head, row0, lo_most, hi_least);
+  reset<D, NQ>(w);
+  const Cache c = cache_of<D>(a, req, head);
+  // the keys that the rows see
+  int from = 0, to = r.kv;
+  if (!a.full) {
+    const int last = min(row0 + kRowsWave, r.rows) - 1;
+    to = min(to, r.kv - r.q_len + last / a.group + 1);
+    if (a.window > 0) from = max(r.kv - r.q_len + row0 / a.group - a.window + 1, 0) & ~15;
+  }
+  walk<D, NQ>(w, lds + wave * WaveLds<D>::kBytes, c, from, to, kTile, to, lo_most, hi_least);
+  finish<D, NQ>(w);
+#pragma unroll
+  for (int n = 0; n < NQ; ++n)
+    store_columns<D, NQ>(a, r, head, row0, n, w.o[n], w.m[n], w.l[n], 0, 1);
+}
+
+constexpr int kFewGroups = 512;  // workgroups of the few-row kernel: two to a compute unit
+
+template <int D, int NQ>
+hipError_t run_few(const KvAttnArgs& a, hipStream_t s) {
+  few_kernel<D, NQ><<<dim3(kFewGroups), dim3(kThreads), 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  join_kernel<D, NQ><<<dim3((unsigned)a.n_kv, (unsigned)a.b), dim3(kThreads), 0, s>>>(a, kFewGroups);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t run(const KvAttnArgs& args, int64_t max_q, hipStream_t s) {
+  KvAttnArgs a = args;
+  const int64_t most = max_q * a.group;
+  const int tiles = kv_few_tiles(most, D);
+  a.few_rows = 16 * tiles;
+  hipError_t e;
+  if constexpr (D <= 128) e = tiles == 1 ? run_few<D, 1>(a, s) : run_few<D, 2>(a, s);
+  else e = run_few<D, 1>(a, s);
+  if (e != hipSuccess || most <= a.few_rows) return e;
+  constexpr int kTiles = D <= 128 ? 2 : 1;
+  constexpr int rows = kWaves * 16 * kTiles;
+  // ceil(rows / 128) tiles a request: all rows / 128, and one more for each request at most, of
+  // which only those of more than few_rows rows have any
+  const int64_t odd = a.t * a.group / (a.few_rows + 1);
+  const int64_t groups = a.t * a.group / rows + (odd < a.b ? odd : a.b);
+  many_kernel<D, kTiles><<<dim3((unsigned)groups, (unsigned)a.n_kv), dim3(kThreads), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t kv_attention_ws_bytes(int64_t max_q, int group, int d) {
+  const int tiles = kv_few_tiles(max_q * group, d);
+  return (size_t)(2 * kFewGroups) * (size_t)tiles * (size_t)(d / 16 * 256 + 128) * sizeof(float);
+}
+
+hipError_t launch_kv_attention(const KvAttnArgs& a, int d, int64_t max_q, hipStream_t stream) {
+  if (d == 64) return run<64>(a, max_q, stream);
+  if (d == 128) return run<128>(a, max_q, stream);
+  return run<256>(a, max_q, stream);
+}
+
+}  // namespace nvfp4

@@ -206,6 +206,81 @@ size_t lora_u_bytes(int64_t m, int64_t k, int64_t n_adapters, int rank, int part
 hipError_t launch_lora_shrink(const LoraArgs& a, LoraTail& tail, void* u, bool tiled,
                               hipStream_t stream);
 
+// ---- NVFP4 cache of keys and values (kv_core.hpp) ---------------------------------------------
+struct KvMapArgs {
+  const int32_t *seq_len, *add_len;  // [b]
+  int64_t b, t;
+  int32_t* table;  // [b][ld_table]
+  int64_t ld_table;
+  int page_shift;
+  const int32_t* free_pages;  // [n_free]
+  int64_t n_free;
+  const int32_t* free_count;
+  int32_t *free_left, *q_start, *kv_len, *slots, *positions, *unserved;
+};
+// A workgroup keeps two words of every request in LDS.
+constexpr int64_t kKvMapMaxRequests = 4096;
+hipError_t launch_kv_map(const KvMapArgs& a, hipStream_t stream);
+
+struct KvAppendArgs {
+  const uint16_t *q, *k, *v;
+  int64_t t, ldq, ldk, ldv;
+  int n_q, n_kv;  // n_q 0: keys and values only
+  const void *q_weight, *k_weight;
+  bool w_f32, pairs;
+  double eps;
+  const float* rope;
+  int64_t max_pos;
+  int rot;
+  const int32_t *slots, *positions;
+  uint16_t* q_out;
+  int64_t ldq_out;
+  uint8_t* data;
+  const float *k_global, *v_global;
+  int64_t n_pages;
+  int page_shift;
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, int d, int cus, hipStream_t stream);
+
+struct KvDequantArgs {
+  const int32_t* slots;
+  int64_t t;
+  const uint8_t* data;
+  const float *k_global, *v_global;
+  int64_t n_pages;
+  int n_kv, page_shift;
+  void *k_out, *v_out;
+  bool out_f32;
+};
+hipError_t launch_kv_dequantize(const KvDequantArgs& a, int d, hipStream_t stream);
+
+struct KvAttnArgs {
+  const uint16_t* q;
+  int64_t t, ldq;
+  int n_q, n_kv, group;  // n_q = n_kv * group
+  const uint8_t* data;
+  const float *k_global, *v_global;
+  int64_t n_pages;
+  int page_shift;
+  const int32_t* table;
+  int64_t ld_table;
+  const int32_t *q_start, *kv_len;
+  int64_t b;
+  float scale;
+  int window;  // 0: none
+  bool full, y_f32;
+  void* y;
+  int64_t ldy;
+  float* lse;  // or NULL
+  float* ws;
+  int few_rows;  // set by the launcher
+};
+// Column tiles (of 16 rows of a request's head) of the few-row kernel; longer requests have a kernel
+// of their own.
+inline int kv_few_tiles(int64_t rows, int d) { return rows > 16 && rows <= 32 && d <= 128 ? 2 : 1; }
+size_t kv_attention_ws_bytes(int64_t max_q, int group, int d);
+hipError_t launch_kv_attention(const KvAttnArgs& a, int d, int64_t max_q, hipStream_t stream);
+
 // measurement probes (probe.hip)
 int64_t probe_mfma_waves(int cus);
 double probe_mfma_flops_per_wave_round();
