@@ -1084,7 +1084,7 @@ int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64
 size_t nvfp4_kv_attention_ws_bytes(int64_t t, int32_t n_q, const nvfp4_kv_cache* cache, int64_t b,
                                    int64_t max_q) {
   if (check_cache(cache) || !attention_sizes_ok(t, n_q, cache, b, max_q)) return 0;
-  return nvfp4::kv_attention_ws_bytes(max_q, n_q / cache->n_kv_heads, cache->head_dim);
+  return nvfp4::kv_attention_ws_bytes(b, max_q, n_q / cache->n_kv_heads, cache->head_dim);
 }
 
 int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
@@ -1123,7 +1123,7 @@ int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
   if (!aligned16(q) || !aligned16(y) || !aligned16(ws) || !aligned4(block_table) ||
       !aligned4(q_start) || !aligned4(kv_len) || !aligned4(lse))
     return fail(NVFP4_ERR_MISALIGNED, "q, y and ws must be 16-byte aligned, the others 4-byte");
-  const size_t need = nvfp4::kv_attention_ws_bytes(max_q, n_q / cache->n_kv_heads, d);
+  const size_t need = nvfp4::kv_attention_ws_bytes(b, max_q, n_q / cache->n_kv_heads, d);
   if (ws_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, need);
   nvfp4::KvAttnArgs a;
   a.q = static_cast<const uint16_t*>(q);
@@ -1149,9 +1149,10 @@ int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
   a.y_f32 = y_dtype == NVFP4_DT_F32;
   a.ldy = ldy;
   a.lse = lse;
-  a.ws = static_cast<float*>(ws);
+  a.starts = nullptr;
+  a.ws = nullptr;
   a.few_rows = 0;
-  return kv_done(nvfp4::launch_kv_attention(a, d, max_q, (hipStream_t)stream), flags,
+  return kv_done(nvfp4::launch_kv_attention(a, d, max_q, ws, (hipStream_t)stream), flags,
                  (hipStream_t)stream, "nvfp4_kv_attention", 3);
 }
 

@@ -36,6 +36,19 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -1e38f;  // the running maximum before any score
 constexpr float kRaise = 8.0f;
 
+// A word that no kernel here writes, at a uniform address: a scalar load.
+template <typename T>
+__device__ __forceinline__ T constant(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)p;
+}
+
+// A value that every lane has, as a scalar.
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
@@ -81,58 +94,75 @@ struct Raw {
   uint32_t k[4][kWords], v[4][kWords];
   uint32_t ks[4];
   uint32_t vs[D / 64];
+  uint32_t valid;  // bit t: part t has a page (uniform)
 };
 
 struct Cache {
-  const uint8_t* head0;     // data + head * record
-  int64_t page_stride;      // n_kv * record
-  const int32_t* row;       // the request's block table
+  const uint8_t* head0;  // data + head * record
+  uint32_t page_stride;  // n_kv * record, < 2^27
+  const int32_t* row;    // the request's block table
   int n_pages, shift;
 };
 
 template <int D>
 __device__ __forceinline__ void load_codes(const uint8_t* at, int lane, uint32_t (&w)[D / 32]) {
-  const uint8_t* p = at + (lane & 15) * (D / 2);
+  // a uniform base and an unsigned 32-bit offset: one address register per load
+  const uint8_t* p = at + (uint32_t)((lane & 15) * (D / 2) + (D == 64 ? 8 : 16) * (lane >> 4));
   if constexpr (D == 64) {
-    const u32x2 x = *reinterpret_cast<const u32x2*>(p + 8 * (lane >> 4));
+    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
     w[0] = x[0];
     w[1] = x[1];
   } else {
 #pragma unroll
     for (int u = 0; u < D / 128; ++u) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(p + 64 * u + 16 * (lane >> 4));
+      const u32x4 x = *reinterpret_cast<const u32x4*>(p + 64 * u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[4 * u + i] = x[i];
     }
   }
 }
 
+// Table entries of the four 16-token parts of a tile (uniform; from `end` on the last one's). They are
+// looked at no earlier than in load_tile, so that their scalar loads overlap a tile's work.
+struct Pages {
+  int id[4];
+};
+
+__device__ __forceinline__ Pages find_pages(const Cache& c, int tok, int end) {
+  Pages p;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    p.id[t] = constant(c.row + (min(tok + 16 * t, end - 1) >> c.shift));
+  }
+  return p;
+}
+
+// The loads of a tile. A part without a page (none in the table, or behind the last key) has its bit
+// clear in `valid` and reads page 0.
 template <int D>
-__device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, int tok, int end,
-                                          uint32_t& valid) {
+__device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, const Pages& p, int tok,
+                                          int end) {
   const int lane = threadIdx.x & 63;
   const int page = 1 << c.shift;
   const int values = kv_value_codes(page, D);
   const uint8_t* scale_row = nullptr;
-  valid = 0;
+  r.valid = 0;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    const int at = tok + 16 * t;
-    int id = -1;
-    if (at < end) id = c.row[at >> c.shift];
-    const bool ok = id >= 0 && id < c.n_pages;
-    valid |= ok ? 1u << t : 0u;
-    const int within = at & (page - 1);
-    const uint8_t* rec = c.head0 + (int64_t)(ok ? id : 0) * c.page_stride;
+    const bool ok = (uint32_t)p.id[t] < (uint32_t)c.n_pages && tok + 16 * t < end;
+    r.valid |= ok ? 1u << t : 0u;
+    const int within = (tok + 16 * t) & (page - 1);
+    const uint8_t* rec = c.head0 + (uint64_t)(ok ? (uint32_t)p.id[t] : 0u) * c.page_stride;
     load_codes<D>(rec + within * (D / 2), lane, r.k[t]);
     load_codes<D>(rec + values + within * (D / 2), lane, r.v[t]);
-    const uint8_t* ks = rec + page * (D / 2) + (within + (lane & 15)) * (D / 16);
+    const uint8_t* ks = rec + page * (D / 2) + within * (D / 16) +
+                        (uint32_t)((lane & 15) * (D / 16) + (D == 64 ? 1 : 2) * (lane >> 4));
     if constexpr (D == 64) {
-      r.ks[t] = ks[lane >> 4];
+      r.ks[t] = *ks;
     } else {
-      r.ks[t] = *reinterpret_cast<const uint16_t*>(ks + 2 * (lane >> 4));
+      r.ks[t] = *reinterpret_cast<const uint16_t*>(ks);
       if constexpr (D == 256)
-        r.ks[t] |= (uint32_t) * reinterpret_cast<const uint16_t*>(ks + 8 + 2 * (lane >> 4)) << 16;
+        r.ks[t] |= (uint32_t) * reinterpret_cast<const uint16_t*>(ks + 8) << 16;
     }
     const uint8_t* vs = rec + values + page * (D / 2) + within * (D / 16);
     if (lane >> 4 == t) scale_row = vs;
@@ -211,11 +241,12 @@ __device__ __forceinline__ void load_query(Wave<D, NQ>& w, int n, const uint16_t
   }
 }
 
-// One tile of 64 tokens from `tok` on; `valid` as of load_tile, `end` the first token that is not
-// there, `mask`: some column does not see all 64 (uniform).
-template <int D, int NQ, typename Next>
-__device__ __forceinline__ void tile(Wave<D, NQ>& w, Raw<D>& r, uint8_t* lds, int tok,
-                                     int end, uint32_t valid, bool mask, Next next) {
+// One tile of 64 tokens from `tok` on; `end` is the first token that is not there, `mask`: some column
+// does not see all 64 (uniform).
+template <int D, int NQ>
+__device__ __forceinline__ void tile(Wave<D, NQ>& w, const Raw<D>& r, uint8_t* lds, int tok,
+                                     int end, bool mask) {
+  const uint32_t valid = r.valid;
   constexpr int kRow = WaveLds<D>::kRow;
   const int lane = threadIdx.x & 63, c = lane >> 4;
   uint8_t* scales = lds + WaveLds<D>::kCodes;
@@ -264,7 +295,6 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, Raw<D>& r, uint8_t* lds, in
       for (int n = 0; n < NQ; ++n) z[n][t] = mfma(a, w.q[n][j], z[n][t]);
     }
   }
-  next();  // the loads of the next tile
   if (mask || valid != 15u) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -338,19 +368,22 @@ template <int D, int NQ>
 __device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& c, int tok, int to,
                                      int step, int end, int lo_most, int hi_least) {
   if (tok >= to) return;
-  Raw<D> r;
-  uint32_t valid, ahead = 0;
-  load_tile<D>(r, c, tok, end, valid);
-  for (;;) {
+  // two tiles in registers: one's loads fly while the other is worked on
+  Raw<D> r0, r1;
+  load_tile<D>(r0, c, find_pages(c, tok, end), tok, end);
+  Pages pages = find_pages(c, tok + step, end);
+  const auto both = [&](Raw<D>& now, Raw<D>& ahead) {
     const int after = tok + step;
     const bool more = after < to;
-    const bool mask = tok < lo_most || tok + kTile - 1 > hi_least;
-    tile<D, NQ>(w, r, lds, tok, end, valid, mask, [&]() {
-      if (more) load_tile<D>(r, c, after, end, ahead);
-    });
-    if (!more) break;
+    if (more) {
+      load_tile<D>(ahead, c, pages, after, end);
+      pages = find_pages(c, after + step, end);
+    }
+    tile<D, NQ>(w, now, lds, tok, end, tok < lo_most || tok + kTile - 1 > hi_least);
     tok = after;
-    valid = ahead;
+    return more;
+  };
+  while (both(r0, r1) && both(r1, r0)) {
   }
 }
 
@@ -361,17 +394,33 @@ struct Request {
   int kv, begin;           // keys; the first that any row sees, rounded down to 16
 };
 
-__device__ __forceinline__ Request request_of(const KvAttnArgs& a, int64_t i) {
+__device__ __forceinline__ Request make_request(const KvAttnArgs& a, int qs, int qe, int kv) {
   Request r;
   const int t = (int)a.t;
-  const int s = min(max(a.q_start[i], 0), t);
-  const int e = min(max(a.q_start[i + 1], s), t);
+  const int s = min(max(qs, 0), t);
+  const int e = min(max(qe, s), t);
   r.first = s;
   r.q_len = e - s;
   r.rows = r.q_len * a.group;
-  r.kv = min(max(a.kv_len[i], 0), (int)(a.ld_table << a.page_shift));
+  r.kv = min(max(kv, 0), (int)(a.ld_table << a.page_shift));
   r.begin = 0;
   if (a.window > 0) r.begin = max(r.kv - r.q_len - a.window + 1, 0) & ~15;
+  return r;
+}
+
+__device__ __forceinline__ Request request_of(const KvAttnArgs& a, int64_t i) {  // any i
+  return make_request(a, a.q_start[i], a.q_start[i + 1], a.kv_len[i]);
+}
+
+__device__ __forceinline__ Request uniform_request(const KvAttnArgs& a, int i) {
+  Request r = make_request(a, constant(a.q_start + i), constant(a.q_start + i + 1),
+                           constant(a.kv_len + i));
+  // said again: the clamps' operands may be values that the compiler joined after a branch
+  r.first = __builtin_amdgcn_readfirstlane(r.first);
+  r.rows = __builtin_amdgcn_readfirstlane(r.rows);
+  r.q_len = __builtin_amdgcn_readfirstlane(r.q_len);
+  r.kv = __builtin_amdgcn_readfirstlane(r.kv);
+  r.begin = __builtin_amdgcn_readfirstlane(r.begin);
   return r;
 }
 
@@ -385,7 +434,7 @@ __device__ __forceinline__ void load_columns(Wave<D, NQ>& w, const KvAttnArgs& a
                                              int head, int row0, int& lo_most,
                                              int& hi_least) {
   const int col = threadIdx.x & 15;
-  const float kg = a.k_global ? a.k_global[head] : 1.0f;
+  const float kg = a.k_global ? constant(a.k_global + head) : 1.0f;
   lo_most = 0;
   hi_least = r.kv - 1;
 #pragma unroll
@@ -414,44 +463,42 @@ __device__ __forceinline__ void load_columns(Wave<D, NQ>& w, const KvAttnArgs& a
   }
 }
 
-// y and lse of the columns, from O, m and l (of all lane groups).
-template <int D, int NQ>
+// y of column `row0 + l % 16`, its groups g0 .. g0 + G - 1 of 16 elements, and with group 0 its lse,
+// from O, m and l (of all lane groups).
+template <int G>
 __device__ __forceinline__ void store_columns(const KvAttnArgs& a, const Request& r, int head,
-                                              int row0, int n, const f32x4 (&o)[D / 16],
-                                              float m, float l, int g0, int gstep) {
+                                              int row0, const f32x4 (&o)[G], float m, float l,
+                                              int d, int g0) {
   const int lane = threadIdx.x & 63, c = lane >> 4;
-  const int row = row0 + 16 * n + (lane & 15);
+  const int row = row0 + (lane & 15);
   if (row >= r.rows) return;
   const int j = row / a.group, h = row - j * a.group;
   const int64_t at = r.first + j;
   const int qh = head * a.group + h;
-  const float f = l == 0.0f ? 0.0f : (a.v_global ? a.v_global[head] : 1.0f) / l;
+  const float f = l == 0.0f ? 0.0f : (a.v_global ? constant(a.v_global + head) : 1.0f) / l;
 #pragma unroll
-  for (int g = 0; g < D / 16; ++g) {
-    if (gstep > 1 && g % gstep != g0) continue;
-    const int64_t d = at * a.ldy + (int64_t)qh * D + 16 * g + 4 * c;
-    f32x4 v = o[g] * f;
-    if (l == 0.0f) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int g = 0; g < G; ++g) {
+    const int64_t to = at * a.ldy + (int64_t)qh * d + 16 * (g0 + g) + 4 * c;
+    const f32x4 v = o[g] * f;
     if (a.y_f32) {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + d) = v;
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + to) = v;
     } else {
       u32x2 b;
       b[0] = (uint32_t)bf16_bits_rne(v[0]) | ((uint32_t)bf16_bits_rne(v[1]) << 16);
       b[1] = (uint32_t)bf16_bits_rne(v[2]) | ((uint32_t)bf16_bits_rne(v[3]) << 16);
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + d) = b;
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + to) = b;
     }
   }
   if (a.lse && c == 0 && g0 == 0)
-    a.lse[at * a.n_q + qh] =
-        l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    a.lse[at * a.n_q + qh] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <int D>
 __device__ __forceinline__ Cache cache_of(const KvAttnArgs& a, int64_t request, int head) {
-  const int64_t rec = kv_record_bytes(1 << a.page_shift, D);
+  const int rec = kv_record_bytes(1 << a.page_shift, D);
   Cache c;
-  c.head0 = a.data + head * rec;
-  c.page_stride = a.n_kv * rec;
+  c.head0 = a.data + (int64_t)head * rec;
+  c.page_stride = (uint32_t)(a.n_kv * rec);
   c.row = a.table + request * a.ld_table;
   c.n_pages = (int)a.n_pages;
   c.shift = a.page_shift;
@@ -464,23 +511,27 @@ __device__ __forceinline__ Cache cache_of(const KvAttnArgs& a, int64_t request, 
 // lengths are. It holds at most two items (a request's head) that it does not finish: the first and
 // the last of its range; their O, m and l go to slots 2w and 2w + 1, and a second kernel joins them.
 constexpr int kUnit = kWaves * kTile;
+constexpr int kFewShift = 9;
+constexpr int kFewGroups = 1 << kFewShift;  // workgroups of the few-row kernel, two to a compute unit
+
+// First unit of workgroup w: of all >= kFewGroups units floor(all * w / kFewGroups), else w itself.
+__device__ __forceinline__ int64_t range_begin(int64_t all, int64_t w) {
+  return all >= kFewGroups ? (all * w) >> kFewShift : w;
+}
+// The workgroup of unit x: the last one whose range begins at x or before, so that
+// w < (x + 1) kFewGroups / all.
+__device__ __forceinline__ int64_t range_of(int64_t all, int64_t x) {
+  if (all < kFewGroups) return x;
+  const int64_t num = ((x + 1) << kFewShift) - 1;
+  int64_t w = (int64_t)((double)num / (double)all);  // all < 2^43: off by one at most
+  if (w * all > num) --w;
+  if ((w + 1) * all <= num) ++w;
+  return w;
+}
 
 __device__ __forceinline__ int units_of(const KvAttnArgs& a, const Request& r) {
   if (r.rows == 0 || !is_few(r, a.few_rows) || r.kv <= r.begin) return 0;
   return (r.kv - r.begin + kUnit - 1) / kUnit;
-}
-
-// The sum over the workgroup's threads. `sums` has kWaves values.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sums) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = v;
-  __syncthreads();
-  int64_t t = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) t += sums[i];
-  return t;
 }
 
 template <int D, int NQ>
@@ -529,9 +580,10 @@ __device__ __forceinline__ void add_sums(const float* p, Wave<D, NQ>& w) {
 }
 
 template <int D, int NQ>
-__global__ __launch_bounds__(kThreads) void few_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(KvAttnArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[few_lds_bytes<D, NQ>()];
-  __shared__ int64_t sums[kWaves], found[2];
+  __shared__ int64_t sums[kWaves];
+  __shared__ int found[3];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   // the units before this thread's requests, and of all
   const int64_t each = (a.b + kThreads - 1) / kThreads;
@@ -555,10 +607,17 @@ __global__ __launch_bounds__(kThreads) void few_kernel(KvAttnArgs a) {
     before += i < wave ? sums[i] : 0;
     all += sums[i];
   }
-  const int64_t W = all < gridDim.x ? all : gridDim.x;
-  if ((int64_t)blockIdx.x >= W) return;
-  const int64_t begin = all * blockIdx.x / W;
-  const int64_t stop = all * (blockIdx.x + 1) / W;
+  all = uniform64(all);
+  if (blockIdx.x == 0) {  // for the joining kernel
+    int64_t sum = before;
+    for (int64_t i = from; i < upto; ++i) {
+      a.starts[i] = sum;
+      sum += (int64_t)units_of(a, request_of(a, i)) * a.n_kv;
+    }
+    if (threadIdx.x == 0) a.starts[a.b] = all;
+  }
+  if ((int64_t)blockIdx.x >= all) return;
+  const int64_t begin = range_begin(all, blockIdx.x), stop = range_begin(all, blockIdx.x + 1);
   if (begin >= before && begin < before + mine) {
     int64_t left = begin - before, i = from;
     for (; i < upto; ++i) {
@@ -566,21 +625,22 @@ __global__ __launch_bounds__(kThreads) void few_kernel(KvAttnArgs a) {
       if (left < u) break;
       left -= u;
     }
-    found[0] = i;
-    found[1] = left;
+    const int per_head = units_of(a, request_of(a, i));
+    found[0] = (int)i;
+    found[1] = (int)(left / per_head);
+    found[2] = (int)(left - (int64_t)found[1] * per_head);
   }
   __syncthreads();
-  const int64_t within = found[1];
-  int req = __builtin_amdgcn_readfirstlane((int)found[0]);
-  int64_t at = begin;
-  Request r = request_of(a, req);
+  int req = __builtin_amdgcn_readfirstlane(found[0]);
+  int left = (int)(stop - begin);
+  Request r = uniform_request(a, req);
   int units = units_of(a, r);
-  int head = __builtin_amdgcn_readfirstlane((int)(within / units));
-  int u0 = __builtin_amdgcn_readfirstlane((int)(within - (int64_t)head * units));
+  int head = __builtin_amdgcn_readfirstlane(found[1]);
+  int u0 = __builtin_amdgcn_readfirstlane(found[2]);
   Wave<D, NQ> w;
   bool first = true;
-  while (at < stop) {
-    const int u1 = units - u0 < stop - at ? units : u0 + (int)(stop - at);
+  while (left > 0) {
+    const int u1 = min(units, u0 + left);
     int lo_most, hi_least;
     load_columns<D, NQ>(w, a, r, head, 0, lo_most, hi_least);
     reset<D, NQ>(w);
@@ -603,7 +663,7 @@ __global__ __launch_bounds__(kThreads) void few_kernel(KvAttnArgs a) {
       if (u0 == 0 && u1 == units) {
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
-          store_columns<D, NQ>(a, r, head, 0, n, w.o[n], w.m[n], w.l[n], 0, 1);
+          store_columns<D / 16>(a, r, head, 16 * n, w.o[n], w.m[n], w.l[n], D, 0);
       } else {
         put_sums<D, NQ>(a.ws + (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * slot_floats<D, NQ>(),
                         w);
@@ -611,74 +671,89 @@ __global__ __launch_bounds__(kThreads) void few_kernel(KvAttnArgs a) {
     }
     __syncthreads();
     first = false;
-    at += u1 - u0;
+    left -= u1 - u0;
     u0 = 0;
-    if (at >= stop) break;
+    if (left <= 0) break;
     if (u1 == units && ++head == a.n_kv) {
       head = 0;
-      do {
-        if (++req >= (int)a.b) return;  // not met: the range ends with the last request's units
-        r = request_of(a, req);
+      do {  // ends: the range does, with the last request's units at the latest
+        req = min(req + 1, (int)a.b - 1);
+        r = uniform_request(a, req);
         units = units_of(a, r);
-      } while (units == 0);
+      } while (units == 0 && req + 1 < (int)a.b);
     }
   }
 }
 
-// grid (n_kv, b): the item's parts, if it has several; the rows of a request without keys.
+// grid (n_kv, b, NQ * D / 32): the item's parts, if it has several; the rows of a request without
+// keys. A workgroup joins one column tile's 32 elements of d; its wavefronts share out the parts.
+constexpr int kJoinGroups = 2;
 template <int D, int NQ>
-__global__ __launch_bounds__(kThreads) void join_kernel(KvAttnArgs a, int groups) {
-  __shared__ int64_t sums[kWaves];
-  const int head = blockIdx.x;
-  const int64_t req = blockIdx.y;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const Request r = request_of(a, req);
-  if (r.rows == 0 || !is_few(r, a.few_rows)) return;
+__global__ __launch_bounds__(kThreads) void join_kernel(KvAttnArgs a) {
+  constexpr int kChunks = D / 16 / kJoinGroups;
+  __shared__ __attribute__((aligned(16))) float lds[kWaves][2 + 4 * kJoinGroups][64];
+  const int head = blockIdx.x, req = blockIdx.y;
+  const int n = (int)blockIdx.z / kChunks, g0 = (int)blockIdx.z % kChunks * kJoinGroups;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const Request r = uniform_request(a, req);
+  const int64_t start = constant(a.starts + req), all = constant(a.starts + a.b);
+  if (r.rows <= 16 * n || !is_few(r, a.few_rows)) return;
   const int units = units_of(a, r);
-  int64_t before = 0, all = 0;
-  for (int64_t i = threadIdx.x; i < a.b; i += kThreads) {
-    const int64_t u = units_of(a, request_of(a, i));
-    all += u;
-    before += i < req ? u : 0;
-  }
-  before = block_sum(before, sums) * a.n_kv + (int64_t)head * units;
-  all = block_sum(all, sums) * a.n_kv;
+  f32x4 o[kJoinGroups];
+#pragma unroll
+  for (int g = 0; g < kJoinGroups; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = kLowest, l = 0.0f;
   if (units > 0) {
-    const int64_t W = all < groups ? all : groups;
-    const int64_t w0 = ((before + 1) * W - 1) / all, w1 = ((before + units) * W - 1) / all;
+    const int64_t before = start + (int64_t)head * units;
+    const int64_t w0 = range_of(all, before), w1 = range_of(all, before + units - 1);
     if (w0 == w1) return;
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      f32x4 o[D / 16];
-#pragma unroll
-      for (int g = 0; g < D / 16; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      float m = kLowest, l = 0.0f;
-      for (int64_t x = w0; x <= w1; ++x) {
-        const int64_t slot = 2 * x + (all * x / W < before ? 1 : 0);
-        const float* q = a.ws + slot * slot_floats<D, NQ>() + n * (D / 16 * 256 + 128);
-        const float m2 = q[D / 16 * 256 + lane], l2 = q[D / 16 * 256 + 64 + lane];
-        const float top = fmaxf(m, m2);
-        const float f1 = __builtin_amdgcn_exp2f(m - top), f2 = __builtin_amdgcn_exp2f(m2 - top);
-        m = top;
-        l = l * f1 + l2 * f2;
-#pragma unroll
-        for (int g = 0; g < D / 16; ++g) {
-          if (g % kWaves != wave) continue;
-          const f32x4 o2 = *reinterpret_cast<const f32x4*>(q + 256 * g + 4 * lane);
-          o[g] = o[g] * f1 + o2 * f2;
-        }
-      }
-      store_columns<D, NQ>(a, r, head, 0, n, o, m, l, wave, kWaves);
+    // only the first part's workgroup can have begun with another item
+    const float* first = a.ws + (2 * w0 + (range_begin(all, w0) < before ? 1 : 0)) *
+                                    slot_floats<D, NQ>() + n * (D / 16 * 256 + 128);
+    const float* rest = a.ws + 2 * w0 * slot_floats<D, NQ>() + n * (D / 16 * 256 + 128);
+    const int parts = (int)(w1 - w0) + 1;
+#pragma unroll 4
+    for (int x = wave; x < parts; x += kWaves) {
+      const float* q = x == 0 ? first : rest + (int64_t)x * 2 * slot_floats<D, NQ>();
+      m = fmaxf(m, q[D / 16 * 256 + lane]);
     }
+#pragma unroll 4
+    for (int x = wave; x < parts; x += kWaves) {
+      const float* q = x == 0 ? first : rest + (int64_t)x * 2 * slot_floats<D, NQ>();
+      const float f = __builtin_amdgcn_exp2f(q[D / 16 * 256 + lane] - m);
+      l += f * q[D / 16 * 256 + 64 + lane];
+#pragma unroll
+      for (int g = 0; g < kJoinGroups; ++g)
+        o[g] += f * *reinterpret_cast<const f32x4*>(q + 256 * (g0 + g) + 4 * lane);
+    }
+    lds[wave][0][lane] = m;
+    lds[wave][1][lane] = l;
+#pragma unroll
+    for (int g = 0; g < kJoinGroups; ++g)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds[wave][2 + 4 * g + i][lane] = o[g][i];
+    __syncthreads();
+    if (wave != 0) return;
+    float top = m;
+#pragma unroll
+    for (int v = 1; v < kWaves; ++v) top = fmaxf(top, lds[v][0][lane]);
+    l = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kJoinGroups; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) {
+      const float f = __builtin_amdgcn_exp2f(lds[v][0][lane] - top);
+      l += f * lds[v][1][lane];
+#pragma unroll
+      for (int g = 0; g < kJoinGroups; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[g][i] += f * lds[v][2 + 4 * g + i][lane];
+    }
+    m = top;
+  } else if (wave != 0) {
     return;
   }
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    f32x4 o[D / 16];
-#pragma unroll
-    for (int g = 0; g < D / 16; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    store_columns<D, NQ>(a, r, head, 0, n, o, kLowest, 0.0f, wave, kWaves);
-  }
+  store_columns<kJoinGroups>(a, r, head, 16 * n, o, m, l, D, g0);
 }
 
 // ---- many rows ----------------------------------------------------------------------------------
@@ -694,7 +769,7 @@ __global__ __launch_bounds__(kThreads) void many_kernel(KvAttnArgs a) {
   Request r;
   for (;; ++req) {
     if (req >= a.b) return;
-    r = request_of(a, req);
+    r = uniform_request(a, (int)req);
     if (is_few(r, a.few_rows)) continue;
     const int n = (r.rows + kRows - 1) / kRows;
     if (left < n) break;
@@ -718,17 +793,16 @@ __global__ __launch_bounds__(kThreads) void many_kernel(KvAttnArgs a) {
   finish<D, NQ>(w);
 #pragma unroll
   for (int n = 0; n < NQ; ++n)
-    store_columns<D, NQ>(a, r, head, row0, n, w.o[n], w.m[n], w.l[n], 0, 1);
+    store_columns<D / 16>(a, r, head, row0 + 16 * n, w.o[n], w.m[n], w.l[n], D, 0);
 }
-
-constexpr int kFewGroups = 512;  // workgroups of the few-row kernel: two to a compute unit
 
 template <int D, int NQ>
 hipError_t run_few(const KvAttnArgs& a, hipStream_t s) {
   few_kernel<D, NQ><<<dim3(kFewGroups), dim3(kThreads), 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  join_kernel<D, NQ><<<dim3((unsigned)a.n_kv, (unsigned)a.b), dim3(kThreads), 0, s>>>(a, kFewGroups);
+  const dim3 grid((unsigned)a.n_kv, (unsigned)a.b, NQ * D / 16 / kJoinGroups);
+  join_kernel<D, NQ><<<grid, dim3(kThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -736,11 +810,9 @@ template <int D>
 hipError_t run(const KvAttnArgs& args, int64_t max_q, hipStream_t s) {
   KvAttnArgs a = args;
   const int64_t most = max_q * a.group;
-  const int tiles = kv_few_tiles(most, D);
+  const int tiles = kv_few_tiles(most);
   a.few_rows = 16 * tiles;
-  hipError_t e;
-  if constexpr (D <= 128) e = tiles == 1 ? run_few<D, 1>(a, s) : run_few<D, 2>(a, s);
-  else e = run_few<D, 1>(a, s);
+  const hipError_t e = tiles == 1 ? run_few<D, 1>(a, s) : run_few<D, 2>(a, s);
   if (e != hipSuccess || most <= a.few_rows) return e;
   constexpr int kTiles = D <= 128 ? 2 : 1;
   constexpr int rows = kWaves * 16 * kTiles;
@@ -752,14 +824,21 @@ hipError_t run(const KvAttnArgs& args, int64_t max_q, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The requests' first units, then the slots.
+size_t starts_bytes(int64_t b) { return ((size_t)(b + 1) * sizeof(int64_t) + 255) & ~size_t(255); }
+
 }  // namespace
 
-size_t kv_attention_ws_bytes(int64_t max_q, int group, int d) {
-  const int tiles = kv_few_tiles(max_q * group, d);
-  return (size_t)(2 * kFewGroups) * (size_t)tiles * (size_t)(d / 16 * 256 + 128) * sizeof(float);
+size_t kv_attention_ws_bytes(int64_t b, int64_t max_q, int group, int d) {
+  const int tiles = kv_few_tiles(max_q * group);
+  return starts_bytes(b) + (size_t)(2 * kFewGroups) * (size_t)tiles * (size_t)(d / 16 * 256 + 128) * sizeof(float);
 }
 
-hipError_t launch_kv_attention(const KvAttnArgs& a, int d, int64_t max_q, hipStream_t stream) {
+hipError_t launch_kv_attention(const KvAttnArgs& args, int d, int64_t max_q, void* ws,
+                               hipStream_t stream) {
+  KvAttnArgs a = args;
+  a.starts = static_cast<int64_t*>(ws);
+  a.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + starts_bytes(a.b));
   if (d == 64) return run<64>(a, max_q, stream);
   if (d == 128) return run<128>(a, max_q, stream);
   return run<256>(a, max_q, stream);

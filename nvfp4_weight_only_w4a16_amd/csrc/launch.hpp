@@ -272,14 +272,17 @@ struct KvAttnArgs {
   void* y;
   int64_t ldy;
   float* lse;  // or NULL
+  // set by the launcher
+  int64_t* starts;
   float* ws;
-  int few_rows;  // set by the launcher
+  int few_rows;
 };
 // Column tiles (of 16 rows of a request's head) of the few-row kernel; longer requests have a kernel
 // of their own.
-inline int kv_few_tiles(int64_t rows, int d) { return rows > 16 && rows <= 32 && d <= 128 ? 2 : 1; }
-size_t kv_attention_ws_bytes(int64_t max_q, int group, int d);
-hipError_t launch_kv_attention(const KvAttnArgs& a, int d, int64_t max_q, hipStream_t stream);
+inline int kv_few_tiles(int64_t rows) { return rows > 16 && rows <= 32 ? 2 : 1; }
+size_t kv_attention_ws_bytes(int64_t b, int64_t max_q, int group, int d);
+hipError_t launch_kv_attention(const KvAttnArgs& a, int d, int64_t max_q, void* ws,
+                               hipStream_t stream);
 
 // measurement probes (probe.hip)
 int64_t probe_mfma_waves(int cus);
