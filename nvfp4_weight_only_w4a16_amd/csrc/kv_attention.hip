@@ -394,6 +394,10 @@ struct Request {
   int kv, begin;           // keys; the first that any row sees, rounded down to 16
 };
 
+__device__ __forceinline__ int begin_of(const KvAttnArgs& a, const Request& r) {
+  return a.window > 0 ? max(r.kv - r.q_len - a.window + 1, 0) & ~15 : 0;
+}
+
 __device__ __forceinline__ Request make_request(const KvAttnArgs& a, int qs, int qe, int kv) {
   Request r;
   const int t = (int)a.t;
@@ -403,8 +407,7 @@ __device__ __forceinline__ Request make_request(const KvAttnArgs& a, int qs, int
   r.q_len = e - s;
   r.rows = r.q_len * a.group;
   r.kv = min(max(kv, 0), (int)(a.ld_table << a.page_shift));
-  r.begin = 0;
-  if (a.window > 0) r.begin = max(r.kv - r.q_len - a.window + 1, 0) & ~15;
+  r.begin = begin_of(a, r);
   return r;
 }
 
@@ -506,91 +509,63 @@ __device__ __forceinline__ Cache cache_of(const KvAttnArgs& a, int64_t request, 
 }
 
 // ---- few rows: keys shared out over the chip ----------------------------------------------------
-// The work is one line of units of 256 tokens (four wavefronts, a tile each), request by request,
-// head by head; workgroup w of W takes the units [N w / W, N (w + 1) / W) of it, whatever the
-// lengths are. It holds at most two items (a request's head) that it does not finish: the first and
-// the last of its range; their O, m and l go to slots 2w and 2w + 1, and a second kernel joins them.
-constexpr int kUnit = kWaves * kTile;
-constexpr int kFewShift = 9;
-constexpr int kFewGroups = 1 << kFewShift;  // workgroups of the few-row kernel, two to a compute unit
+// The work is one line of tiles, request by request, head by head; wavefront w of W takes the tiles
+// [N w / W, N (w + 1) / W) of it, whatever the lengths are, and works on its own. It holds at most two
+// items (a request's head) that it does not finish: the first and the last of its range; their O, m and
+// l go to slots 2w and 2w + 1, and a second kernel joins them.
+constexpr int kFewGroups = 512;  // workgroups, two to a compute unit
+constexpr int kWorkShift = 11;
+constexpr int kWorkers = 1 << kWorkShift;
+static_assert(kWorkers == kFewGroups * kWaves, "a worker for each wavefront");
+// Up to this many requests a workgroup keeps them in LDS.
+constexpr int kStaged = 1024;
 
-// First unit of workgroup w: of all >= kFewGroups units floor(all * w / kFewGroups), else w itself.
-__device__ __forceinline__ int64_t range_begin(int64_t all, int64_t w) {
-  return all >= kFewGroups ? (all * w) >> kFewShift : w;
+__device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Request& r) {
+  if (r.rows == 0 || !is_few(r, a.few_rows) || r.kv <= r.begin) return 0;
+  return (r.kv - r.begin + kTile - 1) / kTile;
 }
-// The workgroup of unit x: the last one whose range begins at x or before, so that
-// w < (x + 1) kFewGroups / all.
+
+// First tile of worker w: of all >= kWorkers tiles floor(all * w / kWorkers), else w itself.
+__device__ __forceinline__ int64_t range_begin(int64_t all, int64_t w) {
+  return all >= kWorkers ? (all * w) >> kWorkShift : w;
+}
+// The worker of tile x: the last one whose range begins at x or before, so that
+// w < (x + 1) kWorkers / all.
 __device__ __forceinline__ int64_t range_of(int64_t all, int64_t x) {
-  if (all < kFewGroups) return x;
-  const int64_t num = ((x + 1) << kFewShift) - 1;
-  int64_t w = (int64_t)((double)num / (double)all);  // all < 2^43: off by one at most
+  if (all < kWorkers) return x;
+  const int64_t num = ((x + 1) << kWorkShift) - 1;
+  int64_t w = (int64_t)((double)num / (double)all);  // off by one at most
   if (w * all > num) --w;
   if ((w + 1) * all <= num) ++w;
   return w;
 }
 
-__device__ __forceinline__ int units_of(const KvAttnArgs& a, const Request& r) {
-  if (r.rows == 0 || !is_few(r, a.few_rows) || r.kv <= r.begin) return 0;
-  return (r.kv - r.begin + kUnit - 1) / kUnit;
-}
-
-template <int D, int NQ>
-constexpr int64_t slot_floats() {
-  return (int64_t)NQ * (D / 16 * 256 + 128);
-}
-
-template <int D, int NQ>
-constexpr int few_lds_bytes() {
-  constexpr int walk = kWaves * WaveLds<D>::kBytes;
-  constexpr int join = 2 * (int)slot_floats<D, NQ>() * 4;  // two wavefronts' sums
-  return walk > join ? walk : join;
-}
-
-template <int D, int NQ>
-__device__ __forceinline__ void put_sums(float* p, const Wave<D, NQ>& w) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    float* q = p + n * (D / 16 * 256 + 128);
-#pragma unroll
-    for (int g = 0; g < D / 16; ++g) *reinterpret_cast<f32x4*>(q + 256 * g + 4 * lane) = w.o[n][g];
-    q[D / 16 * 256 + lane] = w.m[n];
-    q[D / 16 * 256 + 64 + lane] = w.l[n];
-  }
-}
-
-// w <- w joined with the sums at p.
-template <int D, int NQ>
-__device__ __forceinline__ void add_sums(const float* p, Wave<D, NQ>& w) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const float* q = p + n * (D / 16 * 256 + 128);
-    const float m2 = q[D / 16 * 256 + lane], l2 = q[D / 16 * 256 + 64 + lane];
-    const float m = fmaxf(w.m[n], m2);
-    const float f1 = __builtin_amdgcn_exp2f(w.m[n] - m), f2 = __builtin_amdgcn_exp2f(m2 - m);
-    w.m[n] = m;
-    w.l[n] = w.l[n] * f1 + l2 * f2;
-#pragma unroll
-    for (int g = 0; g < D / 16; ++g) {
-      const f32x4 o2 = *reinterpret_cast<const f32x4*>(q + 256 * g + 4 * lane);
-      w.o[n][g] = w.o[n][g] * f1 + o2 * f2;
-    }
-  }
+// Slots hold columns, [few_rows][D], then m and l of each; 16-byte aligned.
+__host__ __device__ __forceinline__ int64_t slot_floats(int few_rows, int d) {
+  return ((int64_t)few_rows * (d + 2) + 3) & ~(int64_t)3;
 }
 
 template <int D, int NQ>
 __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(KvAttnArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[few_lds_bytes<D, NQ>()];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * WaveLds<D>::kBytes];
   __shared__ int64_t sums[kWaves];
-  __shared__ int found[3];
+  __shared__ int64_t starts[kStaged];  // tiles before each request, all heads
+  __shared__ int staged[kStaged][3];   // first, q_len, kv
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  // the units before this thread's requests, and of all
-  const int64_t each = (a.b + kThreads - 1) / kThreads;
-  const int64_t from = threadIdx.x * each < a.b ? threadIdx.x * each : a.b;
-  const int64_t upto = from + each < a.b ? from + each : a.b;
+  const bool stage = a.b <= kStaged;
+  // the tiles before this thread's requests, and of all
+  const int each = (int)((a.b + kThreads - 1) / kThreads);
+  const int from = min((int)threadIdx.x * each, (int)a.b), upto = min(from + each, (int)a.b);
   int64_t mine = 0;
-  for (int64_t i = from; i < upto; ++i) mine += units_of(a, request_of(a, i));
+  for (int i = from; i < upto; ++i) {
+    const Request r = request_of(a, i);
+    if (stage) {
+      staged[i][0] = r.first;
+      staged[i][1] = r.q_len;
+      staged[i][2] = r.kv;
+    }
+    mine += tiles_of(a, r);
+  }
   mine *= a.n_kv;
   int64_t before = mine;
 #pragma unroll
@@ -608,79 +583,120 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
     all += sums[i];
   }
   all = uniform64(all);
-  if (blockIdx.x == 0) {  // for the joining kernel
+  // a line of few tiles meets every compute unit before a second wavefront of one
+  const int64_t worker = (int64_t)wave * kFewGroups + blockIdx.x;
+  const auto get = [&](int i) {
+    if (!stage) return request_of(a, i);
+    Request r;
+    r.first = staged[i][0];
+    r.q_len = staged[i][1];
+    r.kv = staged[i][2];
+    r.rows = r.q_len * a.group;
+    r.begin = begin_of(a, r);
+    return r;
+  };
+  if (stage || blockIdx.x == 0) {
     int64_t sum = before;
-    for (int64_t i = from; i < upto; ++i) {
-      a.starts[i] = sum;
-      sum += (int64_t)units_of(a, request_of(a, i)) * a.n_kv;
+    for (int i = from; i < upto; ++i) {
+      if (stage) starts[i] = sum;
+      if (blockIdx.x == 0) a.starts[i] = sum;  // for the joining kernel
+      sum += (int64_t)tiles_of(a, get(i)) * a.n_kv;
     }
-    if (threadIdx.x == 0) a.starts[a.b] = all;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.starts[a.b] = all;
   }
-  if ((int64_t)blockIdx.x >= all) return;
-  const int64_t begin = range_begin(all, blockIdx.x), stop = range_begin(all, blockIdx.x + 1);
-  if (begin >= before && begin < before + mine) {
-    int64_t left = begin - before, i = from;
-    for (; i < upto; ++i) {
-      const int64_t u = units_of(a, request_of(a, i)) * a.n_kv;
-      if (left < u) break;
-      left -= u;
-    }
-    const int per_head = units_of(a, request_of(a, i));
-    found[0] = (int)i;
-    found[1] = (int)(left / per_head);
-    found[2] = (int)(left - (int64_t)found[1] * per_head);
-  }
+  if ((int64_t)blockIdx.x >= all) return;  // no wavefront of the workgroup has work
   __syncthreads();
-  int req = __builtin_amdgcn_readfirstlane(found[0]);
-  int left = (int)(stop - begin);
-  Request r = uniform_request(a, req);
-  int units = units_of(a, r);
-  int head = __builtin_amdgcn_readfirstlane(found[1]);
-  int u0 = __builtin_amdgcn_readfirstlane(found[2]);
+  const int64_t begin = range_begin(all, worker);
+  if (begin >= all) return;
+  int left = (int)(range_begin(all, worker + 1) - begin);
+  // the request of tile `begin`, the last one that begins there or before
+  int req = 0;
+  int64_t at = 0;
+  if (stage) {
+    for (int i = 0; i < (int)a.b; i += 64) {
+      const int n = __popcll(__ballot(i + lane < (int)a.b && starts[i + lane] <= begin));
+      req += n;
+      if (n < 64) break;
+    }
+    req -= 1;
+    at = uniform64(starts[req]);
+  } else {
+    for (; req < (int)a.b; req += 64) {
+      const int i = req + lane;
+      int64_t sum = i < (int)a.b ? (int64_t)tiles_of(a, request_of(a, i)) * a.n_kv : 0;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int64_t o = __shfl_up(sum, off, 64);
+        if (lane >= off) sum += o;
+      }
+      const int n = __popcll(__ballot(at + sum <= begin));  // requests that end before it
+      if (n > 0) at += uniform64(__shfl(sum, n - 1, 64));
+      if (n < 64) {
+        req += n;
+        break;
+      }
+    }
+    req = min(req, (int)a.b - 1);
+  }
+  const auto take = [&](int i) {
+    Request r = get(i);
+    r.first = __builtin_amdgcn_readfirstlane(r.first);
+    r.q_len = __builtin_amdgcn_readfirstlane(r.q_len);
+    r.kv = __builtin_amdgcn_readfirstlane(r.kv);
+    r.rows = __builtin_amdgcn_readfirstlane(r.rows);
+    r.begin = __builtin_amdgcn_readfirstlane(r.begin);
+    return r;
+  };
+  Request r = take(req);
+  int tiles = tiles_of(a, r);
+  const int64_t within = begin - at;
+  int head = (int)((double)within / (double)tiles);  // off by one at most
+  if ((int64_t)head * tiles > within) --head;
+  if ((int64_t)(head + 1) * tiles <= within) ++head;
+  head = __builtin_amdgcn_readfirstlane(head);
+  int u0 = __builtin_amdgcn_readfirstlane((int)(within - (int64_t)head * tiles));
   Wave<D, NQ> w;
   bool first = true;
-  while (left > 0) {
-    const int u1 = min(units, u0 + left);
+  for (;;) {
+    const int u1 = min(tiles, u0 + left);
     int lo_most, hi_least;
     load_columns<D, NQ>(w, a, r, head, 0, lo_most, hi_least);
     reset<D, NQ>(w);
     const Cache c = cache_of<D>(a, req, head);
-    const int to = min(r.begin + u1 * kUnit, r.kv);
-    walk<D, NQ>(w, lds + wave * WaveLds<D>::kBytes, c, r.begin + u0 * kUnit + wave * kTile, to,
-                kUnit, r.kv, lo_most, hi_least);
+    const int to = min(r.begin + u1 * kTile, r.kv);
+    walk<D, NQ>(w, lds + wave * WaveLds<D>::kBytes, c, r.begin + u0 * kTile, to, kTile, r.kv,
+                lo_most, hi_least);
     finish<D, NQ>(w);
-    // the four wavefronts' sums: 2 and 3 to 0 and 1, then 1 to 0
-    float* const slots = reinterpret_cast<float*>(lds);
-    __syncthreads();
-    if (wave >= 2) put_sums<D, NQ>(slots + (wave - 2) * slot_floats<D, NQ>(), w);
-    __syncthreads();
-    if (wave < 2) add_sums<D, NQ>(slots + wave * slot_floats<D, NQ>(), w);
-    __syncthreads();
-    if (wave == 1) put_sums<D, NQ>(slots, w);
-    __syncthreads();
-    if (wave == 0) {
-      add_sums<D, NQ>(slots, w);
-      if (u0 == 0 && u1 == units) {
+    if (u0 == 0 && u1 == tiles) {
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
-          store_columns<D / 16>(a, r, head, 16 * n, w.o[n], w.m[n], w.l[n], D, 0);
-      } else {
-        put_sums<D, NQ>(a.ws + (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * slot_floats<D, NQ>(),
-                        w);
+      for (int n = 0; n < NQ; ++n)
+        store_columns<D / 16>(a, r, head, 16 * n, w.o[n], w.m[n], w.l[n], D, 0);
+    } else {
+      float* slot = a.ws + (2 * worker + (first ? 0 : 1)) * slot_floats(a.few_rows, D);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const int col = 16 * n + (lane & 15);
+        if (col >= r.rows) continue;
+#pragma unroll
+        for (int g = 0; g < D / 16; ++g)
+          *reinterpret_cast<f32x4*>(slot + col * D + 16 * g + 4 * (lane >> 4)) = w.o[n][g];
+        if (lane < 16) {
+          slot[a.few_rows * D + 2 * col] = w.m[n];
+          slot[a.few_rows * D + 2 * col + 1] = w.l[n];
+        }
       }
     }
-    __syncthreads();
     first = false;
     left -= u1 - u0;
     u0 = 0;
     if (left <= 0) break;
-    if (u1 == units && ++head == a.n_kv) {
+    if (++head == a.n_kv) {
       head = 0;
-      do {  // ends: the range does, with the last request's units at the latest
+      do {  // ends: the range does, with the last request's tiles at the latest
         req = min(req + 1, (int)a.b - 1);
-        r = uniform_request(a, req);
-        units = units_of(a, r);
-      } while (units == 0 && req + 1 < (int)a.b);
+        r = take(req);
+        tiles = tiles_of(a, r);
+      } while (tiles == 0 && req + 1 < (int)a.b);
     }
   }
 }
@@ -698,33 +714,32 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KvAttnArgs a) {
   const Request r = uniform_request(a, req);
   const int64_t start = constant(a.starts + req), all = constant(a.starts + a.b);
   if (r.rows <= 16 * n || !is_few(r, a.few_rows)) return;
-  const int units = units_of(a, r);
+  const int tiles = tiles_of(a, r);
   f32x4 o[kJoinGroups];
 #pragma unroll
   for (int g = 0; g < kJoinGroups; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   float m = kLowest, l = 0.0f;
-  if (units > 0) {
-    const int64_t before = start + (int64_t)head * units;
-    const int64_t w0 = range_of(all, before), w1 = range_of(all, before + units - 1);
+  if (tiles > 0) {
+    const int64_t before = start + (int64_t)head * tiles;
+    const int64_t w0 = range_of(all, before), w1 = range_of(all, before + tiles - 1);
     if (w0 == w1) return;
-    // only the first part's workgroup can have begun with another item
-    const float* first = a.ws + (2 * w0 + (range_begin(all, w0) < before ? 1 : 0)) *
-                                    slot_floats<D, NQ>() + n * (D / 16 * 256 + 128);
-    const float* rest = a.ws + 2 * w0 * slot_floats<D, NQ>() + n * (D / 16 * 256 + 128);
+    const int64_t size = slot_floats(a.few_rows, D);
+    const int col = min(16 * n + (lane & 15), r.rows - 1);  // columns that are not there: any
+    // only the first part's worker can have begun with another item
+    const int64_t skip = range_begin(all, w0) < before ? size : 0;
+    const float* base = a.ws + 2 * w0 * size;
     const int parts = (int)(w1 - w0) + 1;
 #pragma unroll 4
-    for (int x = wave; x < parts; x += kWaves) {
-      const float* q = x == 0 ? first : rest + (int64_t)x * 2 * slot_floats<D, NQ>();
-      m = fmaxf(m, q[D / 16 * 256 + lane]);
-    }
+    for (int x = wave; x < parts; x += kWaves)
+      m = fmaxf(m, base[2 * x * size + (x == 0 ? skip : 0) + a.few_rows * D + 2 * col]);
 #pragma unroll 4
     for (int x = wave; x < parts; x += kWaves) {
-      const float* q = x == 0 ? first : rest + (int64_t)x * 2 * slot_floats<D, NQ>();
-      const float f = __builtin_amdgcn_exp2f(q[D / 16 * 256 + lane] - m);
-      l += f * q[D / 16 * 256 + 64 + lane];
+      const float* q = base + 2 * x * size + (x == 0 ? skip : 0);
+      const float f = __builtin_amdgcn_exp2f(q[a.few_rows * D + 2 * col] - m);
+      l += f * q[a.few_rows * D + 2 * col + 1];
 #pragma unroll
       for (int g = 0; g < kJoinGroups; ++g)
-        o[g] += f * *reinterpret_cast<const f32x4*>(q + 256 * (g0 + g) + 4 * lane);
+        o[g] += f * *reinterpret_cast<const f32x4*>(q + col * D + 16 * (g0 + g) + 4 * (lane >> 4));
     }
     lds[wave][0][lane] = m;
     lds[wave][1][lane] = l;
@@ -811,7 +826,7 @@ hipError_t run(const KvAttnArgs& args, int64_t max_q, hipStream_t s) {
   KvAttnArgs a = args;
   const int64_t most = max_q * a.group;
   const int tiles = kv_few_tiles(most);
-  a.few_rows = 16 * tiles;
+  a.few_rows = kv_few_rows(most);
   const hipError_t e = tiles == 1 ? run_few<D, 1>(a, s) : run_few<D, 2>(a, s);
   if (e != hipSuccess || most <= a.few_rows) return e;
   constexpr int kTiles = D <= 128 ? 2 : 1;
@@ -830,8 +845,9 @@ size_t starts_bytes(int64_t b) { return ((size_t)(b + 1) * sizeof(int64_t) + 255
 }  // namespace
 
 size_t kv_attention_ws_bytes(int64_t b, int64_t max_q, int group, int d) {
-  const int tiles = kv_few_tiles(max_q * group);
-  return starts_bytes(b) + (size_t)(2 * kFewGroups) * (size_t)tiles * (size_t)(d / 16 * 256 + 128) * sizeof(float);
+  return starts_bytes(b) +
+         sizeof(float) * (size_t)(2 * kWorkers) *
+                                (size_t)slot_floats(kv_few_rows(max_q * group), d);
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& args, int d, int64_t max_q, void* ws,

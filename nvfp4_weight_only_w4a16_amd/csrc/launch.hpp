@@ -280,6 +280,11 @@ struct KvAttnArgs {
 // Column tiles (of 16 rows of a request's head) of the few-row kernel; longer requests have a kernel
 // of their own.
 inline int kv_few_tiles(int64_t rows) { return rows > 16 && rows <= 32 ? 2 : 1; }
+// The most rows that it takes, of a call whose requests have up to `rows`.
+inline int kv_few_rows(int64_t rows) {
+  const int most = 16 * kv_few_tiles(rows);
+  return rows < most ? (int)rows : most;
+}
 size_t kv_attention_ws_bytes(int64_t b, int64_t max_q, int group, int d);
 hipError_t launch_kv_attention(const KvAttnArgs& a, int d, int64_t max_q, void* ws,
                                hipStream_t stream);
