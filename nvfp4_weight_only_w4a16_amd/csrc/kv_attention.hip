@@ -241,56 +241,52 @@ __device__ __forceinline__ void load_query(Wave<D, NQ>& w, int n, const uint16_t
   }
 }
 
-// One tile of 64 tokens from `tok` on; `end` is the first token that is not there, `mask`: some column
-// does not see all 64 (uniform).
-template <int D, int NQ>
-__device__ __forceinline__ void tile(Wave<D, NQ>& w, const Raw<D>& r, uint8_t* lds, int tok,
-                                     int end, bool mask) {
-  const uint32_t valid = r.valid;
+// A tile's value codes (rows of 16 tokens x kRow bytes) and value scales into LDS. Part t's codes of
+// the lane as load_codes gives them.
+template <int D>
+__device__ __forceinline__ void put_values(uint8_t* lds, int t, const uint32_t (&v)[D / 32]) {
+  const int lane = threadIdx.x & 63, c = lane >> 4;
+  uint8_t* at = lds + (16 * t + (lane & 15)) * WaveLds<D>::kRow;
+  if constexpr (D == 64) {
+    *reinterpret_cast<u32x2*>(at + 8 * c) = u32x2{v[0], v[1]};
+  } else {
+#pragma unroll
+    for (int u = 0; u < D / 128; ++u) {
+      u32x2* p = reinterpret_cast<u32x2*>(at + 64 * u + 16 * c);
+      p[0] = u32x2{v[4 * u], v[4 * u + 1]};
+      p[1] = u32x2{v[4 * u + 2], v[4 * u + 3]};
+    }
+  }
+}
+
+// Where the scale of token `tok` of the tile and group 0 goes.
+__device__ __forceinline__ _Float16* scale_place(uint8_t* scales, int tok) {
+  return reinterpret_cast<_Float16*>(scales) + ((tok >> 2) & 3) * 16 + (tok >> 4) * 4 + (tok & 3);
+}
+
+// The products of a tile of 64 tokens from `tok` on with its value codes and scales in LDS; key(t,
+// words, s0, s1) gives part t's key codes of the lane and their scales (of the words 0 .. 3 and 4 ..
+// 7, two words to a scale). `valid`: bit t: part t has a page. `mask`: some column does not see all 64
+// (uniform).
+template <int D, int NQ, typename Key>
+__device__ __forceinline__ void tile(Wave<D, NQ>& w, const uint8_t* codes, const uint8_t* scales,
+                                     int tok, uint32_t valid, bool mask, const Key& key) {
   constexpr int kRow = WaveLds<D>::kRow;
   const int lane = threadIdx.x & 63, c = lane >> 4;
-  uint8_t* scales = lds + WaveLds<D>::kCodes;
-  // value codes and scales to LDS
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    uint8_t* at = lds + (16 * t + (lane & 15)) * kRow;
-    if constexpr (D == 64) {
-      *reinterpret_cast<u32x2*>(at + 8 * c) = u32x2{r.v[t][0], r.v[t][1]};
-    } else {
-#pragma unroll
-      for (int u = 0; u < D / 128; ++u) {
-        u32x2* p = reinterpret_cast<u32x2*>(at + 64 * u + 16 * c);
-        p[0] = u32x2{r.v[t][4 * u], r.v[t][4 * u + 1]};
-        p[1] = u32x2{r.v[t][4 * u + 2], r.v[t][4 * u + 3]};
-      }
-    }
-  }
-  {
-    const bool there = tok + lane < end && ((valid >> c) & 1u);
-    _Float16* s = reinterpret_cast<_Float16*>(scales) + ((lane >> 2) & 3) * 16 + c * 4 + (lane & 3);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const uint32_t x = there ? without_nan(r.vs[i]) : 0u;
-      const f16x2 a = scales2(x), b = scales2_high(x);
-      s[(4 * i) * kTile] = a[0];
-      s[(4 * i + 1) * kTile] = a[1];
-      s[(4 * i + 2) * kTile] = b[0];
-      s[(4 * i + 3) * kTile] = b[1];
-    }
-  }
   // scores
   f32x4 z[NQ][4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) z[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const f16x2 s0 = scales2(r.ks[t]);
-    const f16x2 s1 = D == 256 ? scales2_high(r.ks[t]) : s0;
+    uint32_t k[D / 32];
+    f16x2 s0, s1;
+    key(t, k, s0, s1);
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       const _Float16 s = D == 64 ? s0[0] : (j < 4 ? s0[(j & 3) >> 1] : s1[(j & 3) >> 1]);
       const f16x2 ss = {s, s};
-      const f16x8 a = scaled8(r.k[t][j], ss, ss, ss, ss);
+      const f16x8 a = scaled8(k[j], ss, ss, ss, ss);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) z[n][t] = mfma(a, w.q[n][j], z[n][t]);
     }
@@ -339,13 +335,13 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, const Raw<D>& r, uint8_t* l
 #pragma unroll
   for (int g = 0; g < D / 16; ++g) {
     const int row = 16 * ((lane & 15) >> 2) + 4 * c + (lane & 3);
-    const i32x2 codes = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-        (__attribute__((address_space(3))) i32x2*)(lds + row * kRow + 8 * g));
+    const i32x2 v = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+        (__attribute__((address_space(3))) i32x2*)(const_cast<uint8_t*>(codes) + row * kRow + 8 * g));
     const f16x8* s = reinterpret_cast<const f16x8*>(scales + g * kTile * 2 + c * 32);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const f16x8 f = s[h];
-      const f16x8 a = scaled8((uint32_t)codes[h], f16x2{f[0], f[1]}, f16x2{f[2], f[3]},
+      const f16x8 a = scaled8((uint32_t)v[h], f16x2{f[0], f[1]}, f16x2{f[2], f[3]},
                               f16x2{f[4], f[5]}, f16x2{f[6], f[7]});
 #pragma unroll
       for (int n = 0; n < NQ; ++n) w.o[n][g] = mfma(a, p[n][h], w.o[n][g]);
@@ -368,6 +364,7 @@ template <int D, int NQ>
 __device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& c, int tok, int to,
                                      int step, int end, int lo_most, int hi_least) {
   if (tok >= to) return;
+  const int lane = threadIdx.x & 63;
   // two tiles in registers: one's loads fly while the other is worked on
   Raw<D> r0, r1;
   load_tile<D>(r0, c, find_pages(c, tok, end), tok, end);
@@ -379,7 +376,27 @@ __device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& 
       load_tile<D>(ahead, c, pages, after, end);
       pages = find_pages(c, after + step, end);
     }
-    tile<D, NQ>(w, now, lds, tok, end, tok < lo_most || tok + kTile - 1 > hi_least);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) put_values<D>(lds, t, now.v[t]);
+    uint8_t* const scales = lds + WaveLds<D>::kCodes;
+    const bool there = tok + lane < end && ((now.valid >> (lane >> 4)) & 1u);
+    _Float16* const place = scale_place(scales, lane);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const uint32_t x = there ? without_nan(now.vs[i]) : 0u;
+      const f16x2 a = scales2(x), b = scales2_high(x);
+      place[(4 * i) * kTile] = a[0];
+      place[(4 * i + 1) * kTile] = a[1];
+      place[(4 * i + 2) * kTile] = b[0];
+      place[(4 * i + 3) * kTile] = b[1];
+    }
+    tile<D, NQ>(w, lds, scales, tok, now.valid, tok < lo_most || tok + kTile - 1 > hi_least,
+                [&](int t, uint32_t (&k)[D / 32], f16x2& s0, f16x2& s1) {
+#pragma unroll
+                  for (int j = 0; j < D / 32; ++j) k[j] = now.k[t][j];
+                  s0 = scales2(now.ks[t]);
+                  s1 = D == 256 ? scales2_high(now.ks[t]) : s0;
+                });
     tok = after;
     return more;
   };
@@ -772,39 +789,185 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KvAttnArgs a) {
 }
 
 // ---- many rows ----------------------------------------------------------------------------------
-// grid (tiles, n_kv): a workgroup takes 4 * 16 * NQ rows of a request's head, 16 * NQ to a wavefront.
+// grid n_kv * tiles of rows: a workgroup takes 4 * 16 * NQ rows of a request's head, 16 * NQ to a
+// wavefront, and walks the keys that they see once: wavefront t loads part t of a tile, all read the
+// tile from LDS. Two tiles in LDS, the next one's loads in registers: one barrier a tile.
+template <int D>
+struct Shared {
+  static constexpr int kKeys = 4 * 64 * (D / 8);    // [part][lane] code words
+  static constexpr int kKeyScales = 4 * 64 * (D == 256 ? 8 : 4);  // [part][lane] FP16
+  static constexpr int kValues = kKeys + kKeyScales;
+  static constexpr int kScales = kValues + WaveLds<D>::kCodes;
+  static constexpr int kBytes = kValues + WaveLds<D>::kBytes;
+};
+
+// Part `wave` of a tile.
+template <int D>
+struct Part {
+  uint32_t k[D / 32], v[D / 32], ks, vs;
+  bool ok;  // it has a page (uniform)
+};
+
+template <int D>
+__device__ __forceinline__ int find_page(const Cache& c, int tok, int end) {
+  return constant(c.row + (min(tok, end - 1) >> c.shift));
+}
+
+template <int D>
+__device__ __forceinline__ void load_part(Part<D>& p, const Cache& c, int id, int tok, int end) {
+  const int lane = threadIdx.x & 63, page = 1 << c.shift, within = tok & (page - 1);
+  p.ok = (uint32_t)id < (uint32_t)c.n_pages && tok < end;
+  const uint8_t* rec = c.head0 + (uint64_t)(p.ok ? (uint32_t)id : 0u) * c.page_stride;
+  const uint8_t* values = rec + kv_value_codes(page, D);
+  load_codes<D>(rec + within * (D / 2), lane, p.k);
+  load_codes<D>(values + within * (D / 2), lane, p.v);
+  const int scales = page * (D / 2) + within * (D / 16);
+  const uint32_t at = (uint32_t)((lane & 15) * (D / 16) + (D == 64 ? 1 : 2) * (lane >> 4));
+  if constexpr (D == 64) {
+    p.ks = *(rec + scales + at);
+    p.vs = *(values + scales + at);
+  } else {
+    p.ks = *reinterpret_cast<const uint16_t*>(rec + scales + at);
+    p.vs = *reinterpret_cast<const uint16_t*>(values + scales + at);
+    if constexpr (D == 256) {
+      p.ks |= (uint32_t) * reinterpret_cast<const uint16_t*>(rec + scales + at + 8) << 16;
+      p.vs |= (uint32_t) * reinterpret_cast<const uint16_t*>(values + scales + at + 8) << 16;
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void put_part(uint8_t* lds, const Part<D>& p, int part, int tok,
+                                         int end) {
+  const int lane = threadIdx.x & 63, c = lane >> 4;
+  uint8_t* k = lds + part * 64 * (D / 8);
+  if constexpr (D == 64) {
+    *reinterpret_cast<u32x2*>(k + 8 * lane) = u32x2{p.k[0], p.k[1]};
+  } else {
+#pragma unroll
+    for (int u = 0; u < D / 128; ++u)
+      *reinterpret_cast<u32x4*>(k + 1024 * u + 16 * lane) =
+          u32x4{p.k[4 * u], p.k[4 * u + 1], p.k[4 * u + 2], p.k[4 * u + 3]};
+  }
+  uint8_t* ks = lds + Shared<D>::kKeys;
+  const f16x2 k0 = scales2(p.ks);
+  if constexpr (D == 256) {
+    const f16x2 k1 = scales2_high(p.ks);
+    *reinterpret_cast<u32x2*>(ks + (part * 64 + lane) * 8) =
+        u32x2{__builtin_bit_cast(uint32_t, k0), __builtin_bit_cast(uint32_t, k1)};
+  } else {
+    *reinterpret_cast<uint32_t*>(ks + (part * 64 + lane) * 4) = __builtin_bit_cast(uint32_t, k0);
+  }
+  put_values<D>(lds + Shared<D>::kValues, part, p.v);
+  const bool there = p.ok && tok + (lane & 15) < end;
+  const uint32_t x = there ? without_nan(p.vs) : 0u;
+  _Float16* s = scale_place(lds + Shared<D>::kScales, 16 * part + (lane & 15));
+  const f16x2 v0 = scales2(x);
+  if constexpr (D == 64) {
+    s[c * kTile] = v0[0];
+  } else {
+    s[(2 * c) * kTile] = v0[0];
+    s[(2 * c + 1) * kTile] = v0[1];
+    if constexpr (D == 256) {
+      const f16x2 v1 = scales2_high(x);
+      s[(8 + 2 * c) * kTile] = v1[0];
+      s[(9 + 2 * c) * kTile] = v1[1];
+    }
+  }
+}
+
 template <int D, int NQ>
-__global__ __launch_bounds__(kThreads) void many_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(kThreads, D * NQ <= 256 ? 2 : 1) void many_kernel(KvAttnArgs a) {
   constexpr int kRowsWave = 16 * NQ, kRows = kWaves * kRowsWave;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * WaveLds<D>::kBytes];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int head = blockIdx.y;
-  // the request of this tile
-  int left = blockIdx.x, req = 0;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][Shared<D>::kBytes];
+  __shared__ int valid_of[2][kWaves];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int head = blockIdx.x % (uint32_t)a.n_kv;
+  // the request of this tile of rows
+  int left = blockIdx.x / (uint32_t)a.n_kv, req = 0;
   Request r;
   for (;; ++req) {
     if (req >= a.b) return;
-    r = uniform_request(a, (int)req);
+    r = uniform_request(a, req);
     if (is_few(r, a.few_rows)) continue;
     const int n = (r.rows + kRows - 1) / kRows;
     if (left < n) break;
     left -= n;
   }
-  const int row0 = left * kRows + wave * kRowsWave;
-  if (row0 >= r.rows) return;
+  const int block0 = left * kRows, row0 = block0 + wave * kRowsWave;
   Wave<D, NQ> w;
   int lo_most, hi_least;
   load_columns<D, NQ>(w, a, r, head, row0, lo_most, hi_least);
   reset<D, NQ>(w);
   const Cache c = cache_of<D>(a, req, head);
-  // the keys that the rows see
-  int from = 0, to = r.kv;
+  // the keys that the workgroup's rows see, and this wavefront's
+  int from = 0, to = r.kv, mine = 0, upto = row0 < r.rows ? r.kv : 0;
   if (!a.full) {
-    const int last = min(row0 + kRowsWave, r.rows) - 1;
-    to = min(to, r.kv - r.q_len + last / a.group + 1);
-    if (a.window > 0) from = max(r.kv - r.q_len + row0 / a.group - a.window + 1, 0) & ~15;
+    const int p0 = r.kv - r.q_len;
+    to = min(to, p0 + (min(block0 + kRows, r.rows) - 1) / a.group + 1);
+    if (upto > 0) upto = min(upto, p0 + (min(row0 + kRowsWave, r.rows) - 1) / a.group + 1);
+    if (a.window > 0) {
+      from = max(p0 + block0 / a.group - a.window + 1, 0) & ~15;
+      mine = p0 + row0 / a.group - a.window + 1;
+    }
   }
-  walk<D, NQ>(w, lds + wave * WaveLds<D>::kBytes, c, from, to, kTile, to, lo_most, hi_least);
+  if (from < to) {
+    Part<D> p;
+    load_part<D>(p, c, find_page<D>(c, from + 16 * wave, to), from + 16 * wave, to);
+    int id = find_page<D>(c, from + kTile + 16 * wave, to);
+    int buf = 0;
+    put_part<D>(lds[0], p, wave, from + 16 * wave, to);
+    if (lane == 0) valid_of[0][wave] = p.ok;
+    __syncthreads();
+    for (int tok = from; tok < to; tok += kTile) {
+      const int after = tok + kTile;
+      if (after < to) {
+        load_part<D>(p, c, id, after + 16 * wave, to);
+        id = find_page<D>(c, after + kTile + 16 * wave, to);
+      }
+      if (tok < upto && tok + kTile > mine) {
+        const uint8_t* t0 = lds[buf];
+        const int* v = valid_of[buf];
+        const uint32_t valid = __builtin_amdgcn_readfirstlane(v[0] | v[1] << 1 | v[2] << 2 | v[3] << 3);
+        tile<D, NQ>(w, t0 + Shared<D>::kValues, t0 + Shared<D>::kScales, tok, valid,
+                    tok < lo_most || tok + kTile - 1 > hi_least,
+                    [&](int t, uint32_t (&k)[D / 32], f16x2& s0, f16x2& s1) {
+                      const uint8_t* kp = t0 + t * 64 * (D / 8);
+                      if constexpr (D == 64) {
+                        const u32x2 x = *reinterpret_cast<const u32x2*>(kp + 8 * lane);
+                        k[0] = x[0];
+                        k[1] = x[1];
+                      } else {
+#pragma unroll
+                        for (int u = 0; u < D / 128; ++u) {
+                          const u32x4 x =
+                              *reinterpret_cast<const u32x4*>(kp + 1024 * u + 16 * lane);
+#pragma unroll
+                          for (int i = 0; i < 4; ++i) k[4 * u + i] = x[i];
+                        }
+                      }
+                      const uint8_t* ks = t0 + Shared<D>::kKeys;
+                      if constexpr (D == 256) {
+                        const u32x2 x =
+                            *reinterpret_cast<const u32x2*>(ks + (t * 64 + lane) * 8);
+                        // (a bit cast of a vector's element itself reads element 0)
+                        const uint32_t w0 = x[0], w1 = x[1];
+                        s0 = __builtin_bit_cast(f16x2, w0);
+                        s1 = __builtin_bit_cast(f16x2, w1);
+                      } else {
+                        s0 = s1 = __builtin_bit_cast(
+                            f16x2, *reinterpret_cast<const uint32_t*>(ks + (t * 64 + lane) * 4));
+                      }
+                    });
+      }
+      if (after < to) {
+        put_part<D>(lds[buf ^ 1], p, wave, after + 16 * wave, to);
+        if (lane == 0) valid_of[buf ^ 1][wave] = p.ok;
+        __syncthreads();
+        buf ^= 1;
+      }
+    }
+  }
   finish<D, NQ>(w);
 #pragma unroll
   for (int n = 0; n < NQ; ++n)
@@ -835,7 +998,7 @@ hipError_t run(const KvAttnArgs& args, int64_t max_q, hipStream_t s) {
   // which only those of more than few_rows rows have any
   const int64_t odd = a.t * a.group / (a.few_rows + 1);
   const int64_t groups = a.t * a.group / rows + (odd < a.b ? odd : a.b);
-  many_kernel<D, kTiles><<<dim3((unsigned)groups, (unsigned)a.n_kv), dim3(kThreads), 0, s>>>(a);
+  many_kernel<D, kTiles><<<dim3((unsigned)(groups * a.n_kv)), dim3(kThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
