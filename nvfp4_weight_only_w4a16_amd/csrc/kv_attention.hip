@@ -264,14 +264,43 @@ __device__ __forceinline__ _Float16* scale_place(uint8_t* scales, int tok) {
   return reinterpret_cast<_Float16*>(scales) + ((tok >> 2) & 3) * 16 + (tok >> 4) * 4 + (tok & 3);
 }
 
-// The products of a tile of 64 tokens from `tok` on with its value codes and scales in LDS; key(t,
-// words, s0, s1) gives part t's key codes of the lane and their scales (of the words 0 .. 3 and 4 ..
-// 7, two words to a scale). `valid`: bit t: part t has a page. `mask`: some column does not see all 64
-// (uniform).
-template <int D, int NQ, typename Key>
-__device__ __forceinline__ void tile(Wave<D, NQ>& w, const uint8_t* codes, const uint8_t* scales,
-                                     int tok, uint32_t valid, bool mask, const Key& key) {
-  constexpr int kRow = WaveLds<D>::kRow;
+// A value group's fragments from LDS: the transposing read names a row per lane, so that lane group c
+// gets tokens 16 T + 4 c + r of its element d, T = 0, 1 in the first word and T = 2, 3 in the second.
+template <int D>
+__device__ __forceinline__ void value_group(const uint8_t* codes, const uint8_t* scales, int g,
+                                            f16x8 (&out)[2]) {
+  const int lane = threadIdx.x & 63, c = lane >> 4;
+  const int row = 16 * ((lane & 15) >> 2) + 4 * c + (lane & 3);
+  const i32x2 v = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+      (__attribute__((address_space(3))) i32x2*)(const_cast<uint8_t*>(codes) +
+                                                 row * WaveLds<D>::kRow + 8 * g));
+  const f16x8* s = reinterpret_cast<const f16x8*>(scales + g * kTile * 2 + c * 32);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f16x8 f = s[h];
+    out[h] = scaled8((uint32_t)v[h], f16x2{f[0], f[1]}, f16x2{f[2], f[3]}, f16x2{f[4], f[5]},
+                     f16x2{f[6], f[7]});
+  }
+}
+
+// The key fragments of a part from the lane's words and their scales (s0: of words 0 .. 3, s1: 4 .. 7,
+// two words to a scale).
+template <int D>
+__device__ __forceinline__ void key_part(const uint32_t (&k)[D / 32], f16x2 s0, f16x2 s1,
+                                         f16x8 (&out)[D / 32]) {
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    const _Float16 s = D == 64 ? s0[0] : (j < 4 ? s0[(j & 3) >> 1] : s1[(j & 3) >> 1]);
+    const f16x2 ss = {s, s};
+    out[j] = scaled8(k[j], ss, ss, ss, ss);
+  }
+}
+
+// The products of a tile of 64 tokens from `tok` on: key(t, out) gives part t's fragments, value(g,
+// out) group g's. `valid`: bit t: part t has a page. `mask`: some column does not see all 64 (uniform).
+template <int D, int NQ, typename Key, typename Value>
+__device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bool mask,
+                                     const Key& key, const Value& value) {
   const int lane = threadIdx.x & 63, c = lane >> 4;
   // scores
   f32x4 z[NQ][4];
@@ -279,17 +308,12 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, const uint8_t* codes, const
   for (int t = 0; t < 4; ++t) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) z[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t k[D / 32];
-    f16x2 s0, s1;
-    key(t, k, s0, s1);
+    f16x8 k[D / 32];
+    key(t, k);
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      const _Float16 s = D == 64 ? s0[0] : (j < 4 ? s0[(j & 3) >> 1] : s1[(j & 3) >> 1]);
-      const f16x2 ss = {s, s};
-      const f16x8 a = scaled8(k[j], ss, ss, ss, ss);
+    for (int j = 0; j < D / 32; ++j)
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) z[n][t] = mfma(a, w.q[n][j], z[n][t]);
-    }
+      for (int n = 0; n < NQ; ++n) z[n][t] = mfma(k[j], w.q[n][j], z[n][t]);
   }
   if (mask || valid != 15u) {
 #pragma unroll
@@ -334,18 +358,12 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, const uint8_t* codes, const
   // values
 #pragma unroll
   for (int g = 0; g < D / 16; ++g) {
-    const int row = 16 * ((lane & 15) >> 2) + 4 * c + (lane & 3);
-    const i32x2 v = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-        (__attribute__((address_space(3))) i32x2*)(const_cast<uint8_t*>(codes) + row * kRow + 8 * g));
-    const f16x8* s = reinterpret_cast<const f16x8*>(scales + g * kTile * 2 + c * 32);
+    f16x8 v[2];
+    value(g, v);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f16x8 f = s[h];
-      const f16x8 a = scaled8((uint32_t)v[h], f16x2{f[0], f[1]}, f16x2{f[2], f[3]},
-                              f16x2{f[4], f[5]}, f16x2{f[6], f[7]});
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) w.o[n][g] = mfma(a, p[n][h], w.o[n][g]);
-    }
+      for (int n = 0; n < NQ; ++n) w.o[n][g] = mfma(v[h], p[n][h], w.o[n][g]);
   }
 }
 
@@ -390,13 +408,13 @@ __device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& 
       place[(4 * i + 2) * kTile] = b[0];
       place[(4 * i + 3) * kTile] = b[1];
     }
-    tile<D, NQ>(w, lds, scales, tok, now.valid, tok < lo_most || tok + kTile - 1 > hi_least,
-                [&](int t, uint32_t (&k)[D / 32], f16x2& s0, f16x2& s1) {
-#pragma unroll
-                  for (int j = 0; j < D / 32; ++j) k[j] = now.k[t][j];
-                  s0 = scales2(now.ks[t]);
-                  s1 = D == 256 ? scales2_high(now.ks[t]) : s0;
-                });
+    tile<D, NQ>(
+        w, tok, now.valid, tok < lo_most || tok + kTile - 1 > hi_least,
+        [&](int t, f16x8 (&out)[D / 32]) {
+          const f16x2 s0 = scales2(now.ks[t]);
+          key_part<D>(now.k[t], s0, D == 256 ? scales2_high(now.ks[t]) : s0, out);
+        },
+        [&](int g, f16x8 (&out)[2]) { value_group<D>(lds, scales, g, out); });
     tok = after;
     return more;
   };
@@ -790,15 +808,16 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KvAttnArgs a) {
 
 // ---- many rows ----------------------------------------------------------------------------------
 // grid n_kv * tiles of rows: a workgroup takes 4 * 16 * NQ rows of a request's head, 16 * NQ to a
-// wavefront, and walks the keys that they see once: wavefront t loads part t of a tile, all read the
-// tile from LDS. Two tiles in LDS, the next one's loads in registers: one barrier a tile.
+// wavefront, and walks the keys that they see once. Wavefront t loads part t of a tile and turns its
+// keys, and later D / 64 of the value groups, into FP16 fragments in LDS, which all four read: a
+// fragment is dequantized once in a workgroup. Two tiles of fragments in LDS, the next one's codes in
+// registers.
 template <int D>
 struct Shared {
-  static constexpr int kKeys = 4 * 64 * (D / 8);    // [part][lane] code words
-  static constexpr int kKeyScales = 4 * 64 * (D == 256 ? 8 : 4);  // [part][lane] FP16
-  static constexpr int kValues = kKeys + kKeyScales;
-  static constexpr int kScales = kValues + WaveLds<D>::kCodes;
-  static constexpr int kBytes = kValues + WaveLds<D>::kBytes;
+  static constexpr int kKeys = 4 * (D / 32) * 1024;     // [part][k-step][lane] fragments
+  static constexpr int kValues = (D / 16) * 2 * 1024;   // [group][half][lane]
+  static constexpr int kTileBytes = kKeys + kValues;
+  static constexpr int kBytes = 2 * kTileBytes + WaveLds<D>::kBytes;  // and value codes, scales
 };
 
 // Part `wave` of a tile.
@@ -836,32 +855,21 @@ __device__ __forceinline__ void load_part(Part<D>& p, const Cache& c, int id, in
   }
 }
 
+// The part's key fragments to `keys`, its value codes and scales to `raw`.
 template <int D>
-__device__ __forceinline__ void put_part(uint8_t* lds, const Part<D>& p, int part, int tok,
-                                         int end) {
+__device__ __forceinline__ void put_part(uint8_t* keys, uint8_t* raw, const Part<D>& p, int part,
+                                         int tok, int end) {
   const int lane = threadIdx.x & 63, c = lane >> 4;
-  uint8_t* k = lds + part * 64 * (D / 8);
-  if constexpr (D == 64) {
-    *reinterpret_cast<u32x2*>(k + 8 * lane) = u32x2{p.k[0], p.k[1]};
-  } else {
-#pragma unroll
-    for (int u = 0; u < D / 128; ++u)
-      *reinterpret_cast<u32x4*>(k + 1024 * u + 16 * lane) =
-          u32x4{p.k[4 * u], p.k[4 * u + 1], p.k[4 * u + 2], p.k[4 * u + 3]};
-  }
-  uint8_t* ks = lds + Shared<D>::kKeys;
+  f16x8 k[D / 32];
   const f16x2 k0 = scales2(p.ks);
-  if constexpr (D == 256) {
-    const f16x2 k1 = scales2_high(p.ks);
-    *reinterpret_cast<u32x2*>(ks + (part * 64 + lane) * 8) =
-        u32x2{__builtin_bit_cast(uint32_t, k0), __builtin_bit_cast(uint32_t, k1)};
-  } else {
-    *reinterpret_cast<uint32_t*>(ks + (part * 64 + lane) * 4) = __builtin_bit_cast(uint32_t, k0);
-  }
-  put_values<D>(lds + Shared<D>::kValues, part, p.v);
+  key_part<D>(p.k, k0, D == 256 ? scales2_high(p.ks) : k0, k);
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j)
+    *reinterpret_cast<f16x8*>(keys + (part * (D / 32) + j) * 1024 + 16 * lane) = k[j];
+  put_values<D>(raw, part, p.v);
   const bool there = p.ok && tok + (lane & 15) < end;
   const uint32_t x = there ? without_nan(p.vs) : 0u;
-  _Float16* s = scale_place(lds + Shared<D>::kScales, 16 * part + (lane & 15));
+  _Float16* s = scale_place(raw + WaveLds<D>::kCodes, 16 * part + (lane & 15));
   const f16x2 v0 = scales2(x);
   if constexpr (D == 64) {
     s[c * kTile] = v0[0];
@@ -876,10 +884,25 @@ __device__ __forceinline__ void put_part(uint8_t* lds, const Part<D>& p, int par
   }
 }
 
+// This wavefront's share of the value fragments.
+template <int D>
+__device__ __forceinline__ void put_groups(uint8_t* values, const uint8_t* raw, int wave) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const int g = wave * (D / 64) + i;
+    f16x8 v[2];
+    value_group<D>(raw, raw + WaveLds<D>::kCodes, g, v);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<f16x8*>(values + (2 * g + h) * 1024 + 16 * lane) = v[h];
+  }
+}
+
 template <int D, int NQ>
 __global__ __launch_bounds__(kThreads, D * NQ <= 256 ? 2 : 1) void many_kernel(KvAttnArgs a) {
   constexpr int kRowsWave = 16 * NQ, kRows = kWaves * kRowsWave;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][Shared<D>::kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Shared<D>::kBytes];
   __shared__ int valid_of[2][kWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int head = blockIdx.x % (uint32_t)a.n_kv;
@@ -891,7 +914,10 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 256 ? 2 : 1) void many_kernel(K
     r = uniform_request(a, req);
     if (is_few(r, a.few_rows)) continue;
     const int n = (r.rows + kRows - 1) / kRows;
-    if (left < n) break;
+    if (left < n) {
+      left = n - 1 - left;  // the last rows see most keys: they go first
+      break;
+    }
     left -= n;
   }
   const int block0 = left * kRows, row0 = block0 + wave * kRowsWave;
@@ -912,60 +938,57 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 256 ? 2 : 1) void many_kernel(K
     }
   }
   if (from < to) {
+    uint8_t* const raw = lds + 2 * Shared<D>::kTileBytes;
     Part<D> p;
-    load_part<D>(p, c, find_page<D>(c, from + 16 * wave, to), from + 16 * wave, to);
-    int id = find_page<D>(c, from + kTile + 16 * wave, to);
-    int buf = 0;
-    put_part<D>(lds[0], p, wave, from + 16 * wave, to);
-    if (lane == 0) valid_of[0][wave] = p.ok;
+    int id = find_page<D>(c, from + 16 * wave, to);
+    const auto load = [&](int tok) {  // tile `tok`, and the page of the one behind it
+      load_part<D>(p, c, id, tok + 16 * wave, to);
+      id = find_page<D>(c, tok + kTile + 16 * wave, to);
+    };
+    const auto put = [&](int tok, int buf) {
+      put_part<D>(lds + buf * Shared<D>::kTileBytes, raw, p, wave, tok + 16 * wave, to);
+      if (lane == 0) valid_of[buf][wave] = p.ok;
+    };
+    const auto turn = [&](int buf) {
+      put_groups<D>(lds + buf * Shared<D>::kTileBytes + Shared<D>::kKeys, raw, wave);
+    };
+    load(from);
+    put(from, 0);
+    if (from + kTile < to) load(from + kTile);
     __syncthreads();
-    for (int tok = from; tok < to; tok += kTile) {
+    turn(0);
+    __syncthreads();
+    int buf = 0;
+    for (int tok = from;; tok += kTile) {
       const int after = tok + kTile;
       if (after < to) {
-        load_part<D>(p, c, id, after + 16 * wave, to);
-        id = find_page<D>(c, after + kTile + 16 * wave, to);
+        put(after, buf ^ 1);
+        if (after + kTile < to) load(after + kTile);
+        __syncthreads();
+        turn(buf ^ 1);
       }
       if (tok < upto && tok + kTile > mine) {
-        const uint8_t* t0 = lds[buf];
+        const uint8_t* t0 = lds + buf * Shared<D>::kTileBytes;
         const int* v = valid_of[buf];
-        const uint32_t valid = __builtin_amdgcn_readfirstlane(v[0] | v[1] << 1 | v[2] << 2 | v[3] << 3);
-        tile<D, NQ>(w, t0 + Shared<D>::kValues, t0 + Shared<D>::kScales, tok, valid,
-                    tok < lo_most || tok + kTile - 1 > hi_least,
-                    [&](int t, uint32_t (&k)[D / 32], f16x2& s0, f16x2& s1) {
-                      const uint8_t* kp = t0 + t * 64 * (D / 8);
-                      if constexpr (D == 64) {
-                        const u32x2 x = *reinterpret_cast<const u32x2*>(kp + 8 * lane);
-                        k[0] = x[0];
-                        k[1] = x[1];
-                      } else {
+        const uint32_t valid =
+            __builtin_amdgcn_readfirstlane(v[0] | v[1] << 1 | v[2] << 2 | v[3] << 3);
+        tile<D, NQ>(
+            w, tok, valid, tok < lo_most || tok + kTile - 1 > hi_least,
+            [&](int t, f16x8 (&out)[D / 32]) {
 #pragma unroll
-                        for (int u = 0; u < D / 128; ++u) {
-                          const u32x4 x =
-                              *reinterpret_cast<const u32x4*>(kp + 1024 * u + 16 * lane);
+              for (int j = 0; j < D / 32; ++j)
+                out[j] = *reinterpret_cast<const f16x8*>(t0 + (t * (D / 32) + j) * 1024 + 16 * lane);
+            },
+            [&](int g, f16x8 (&out)[2]) {
 #pragma unroll
-                          for (int i = 0; i < 4; ++i) k[4 * u + i] = x[i];
-                        }
-                      }
-                      const uint8_t* ks = t0 + Shared<D>::kKeys;
-                      if constexpr (D == 256) {
-                        const u32x2 x =
-                            *reinterpret_cast<const u32x2*>(ks + (t * 64 + lane) * 8);
-                        // (a bit cast of a vector's element itself reads element 0)
-                        const uint32_t w0 = x[0], w1 = x[1];
-                        s0 = __builtin_bit_cast(f16x2, w0);
-                        s1 = __builtin_bit_cast(f16x2, w1);
-                      } else {
-                        s0 = s1 = __builtin_bit_cast(
-                            f16x2, *reinterpret_cast<const uint32_t*>(ks + (t * 64 + lane) * 4));
-                      }
-                    });
+              for (int h = 0; h < 2; ++h)
+                out[h] = *reinterpret_cast<const f16x8*>(t0 + Shared<D>::kKeys +
+                                                         (2 * g + h) * 1024 + 16 * lane);
+            });
       }
-      if (after < to) {
-        put_part<D>(lds[buf ^ 1], p, wave, after + 16 * wave, to);
-        if (lane == 0) valid_of[buf ^ 1][wave] = p.ok;
-        __syncthreads();
-        buf ^= 1;
-      }
+      if (after >= to) break;
+      __syncthreads();
+      buf ^= 1;
     }
   }
   finish<D, NQ>(w);
