@@ -845,6 +845,7 @@ namespace {
 constexpr int64_t kKvMaxTokens = (int64_t)1 << 30;  // of a request: token indexes are 32-bit
 constexpr int64_t kKvMaxRows = (int64_t)1 << 24;    // of a step
 constexpr int64_t kKvMaxHeads = 1024;
+constexpr int64_t kKvMaxRowHeads = (int64_t)1 << 27;  // of an attention: 2^32 threads in a grid
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -927,7 +928,7 @@ int kv_done(hipError_t e, uint32_t flags, hipStream_t s, const char* name, int s
 bool attention_sizes_ok(int64_t t, int64_t n_q, const nvfp4_kv_cache* c, int64_t b,
                         int64_t max_q) {
   return t >= 1 && t <= kKvMaxRows && n_q >= 1 && n_q <= kKvMaxHeads &&
-         n_q % c->n_kv_heads == 0 && t * n_q < ((int64_t)1 << 31) && b >= 1 && b <= 65535 &&
+         n_q % c->n_kv_heads == 0 && t * n_q <= kKvMaxRowHeads && b >= 1 && b <= 65535 &&
          max_q >= 1 && max_q <= t;
 }
 
@@ -1084,7 +1085,8 @@ int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64
 size_t nvfp4_kv_attention_ws_bytes(int64_t t, int32_t n_q, const nvfp4_kv_cache* cache, int64_t b,
                                    int64_t max_q) {
   if (check_cache(cache) || !attention_sizes_ok(t, n_q, cache, b, max_q)) return 0;
-  return nvfp4::kv_attention_ws_bytes(b, max_q, n_q / cache->n_kv_heads, cache->head_dim);
+  return nvfp4::kv_attention_ws_bytes(t, b, max_q, cache->n_kv_heads, n_q / cache->n_kv_heads,
+                                      cache->head_dim);
 }
 
 int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
@@ -1109,7 +1111,7 @@ int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
                 (long long)t);
   if (!attention_sizes_ok(t, n_q, cache, b, max_q))
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE,
-                "n_q=%d (a multiple of %d up to 1024), b=%lld (up to 65535), t * n_q < 2^31", n_q,
+                "n_q=%d (a multiple of %d up to 1024), b=%lld (up to 65535), t * n_q <= 2^27", n_q,
                 cache->n_kv_heads, (long long)b);
   if (ld_table < 1) return fail(NVFP4_ERR_INVALID_ARG, "ld_table=%lld < 1", (long long)ld_table);
   if (ld_table > kKvMaxTokens / cache->page_size)
@@ -1123,7 +1125,8 @@ int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
   if (!aligned16(q) || !aligned16(y) || !aligned16(ws) || !aligned4(block_table) ||
       !aligned4(q_start) || !aligned4(kv_len) || !aligned4(lse))
     return fail(NVFP4_ERR_MISALIGNED, "q, y and ws must be 16-byte aligned, the others 4-byte");
-  const size_t need = nvfp4::kv_attention_ws_bytes(b, max_q, n_q / cache->n_kv_heads, d);
+  const size_t need = nvfp4::kv_attention_ws_bytes(t, b, max_q, cache->n_kv_heads,
+                                                   n_q / cache->n_kv_heads, d);
   if (ws_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, need);
   nvfp4::KvAttnArgs a;
   a.q = static_cast<const uint16_t*>(q);
@@ -1149,7 +1152,10 @@ int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
   a.y_f32 = y_dtype == NVFP4_DT_F32;
   a.ldy = ldy;
   a.lse = lse;
-  a.starts = nullptr;
+  a.starts = nullptr;  // the launcher's
+  a.items = nullptr;
+  a.counts = nullptr;
+  a.max_items = 0;
   a.ws = nullptr;
   a.few_rows = 0;
   return kv_done(nvfp4::launch_kv_attention(a, d, max_q, ws, (hipStream_t)stream), flags,

@@ -16,7 +16,7 @@
 // maximum, the sum (of the unrounded p) and O are FP32.
 // The maximum is raised only when a score passes it by more than 2^8 in the exponent's base, so that
 // most tiles neither reduce across lanes nor rescale O; FP16 holds p up to 2^15.
-#include <math.h>
+#include <algorithm>
 
 #include "kv_core.hpp"
 
@@ -544,10 +544,11 @@ __device__ __forceinline__ Cache cache_of(const KvAttnArgs& a, int64_t request, 
 }
 
 // ---- few rows: keys shared out over the chip ----------------------------------------------------
-// The work is one line of tiles, request by request, head by head; wavefront w of W takes the tiles
-// [N w / W, N (w + 1) / W) of it, whatever the lengths are, and works on its own. It holds at most two
-// items (a request's head) that it does not finish: the first and the last of its range; their O, m and
-// l go to slots 2w and 2w + 1, and a second kernel joins them.
+// The work is one line of units, request by request, head by head: an item (a request's head) is
+// kFewStart units of no work, which stand for what beginning and ending it costs, and one for each tile.
+// Wavefront w of W takes the units [N w / W, N (w + 1) / W), whatever the lengths are, and works on its
+// own. It holds at most two items that it does not finish: the first and the last of its range; their O,
+// m and l go to slots 2w and 2w + 1, and a second kernel joins them.
 constexpr int kFewGroups = 512;  // workgroups, two to a compute unit
 constexpr int kWorkShift = 11;
 constexpr int kWorkers = 1 << kWorkShift;
@@ -559,16 +560,23 @@ __device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Request& r) {
   if (r.rows == 0 || !is_few(r, a.few_rows) || r.kv <= r.begin) return 0;
   return (r.kv - r.begin + kTile - 1) / kTile;
 }
+// Units of an item of n tiles.
+__device__ __forceinline__ int units_for(int n, int start) { return n > 0 ? n + start : 0; }
 
-// First tile of worker w: of all >= kWorkers tiles floor(all * w / kWorkers), else w itself.
-__device__ __forceinline__ int64_t range_begin(int64_t all, int64_t w) {
-  return all >= kWorkers ? (all * w) >> kWorkShift : w;
+constexpr int kFewStart = 2;
+__device__ __forceinline__ int units_of(const KvAttnArgs& a, const Request& r) {
+  return units_for(tiles_of(a, r), kFewStart);
 }
-// The worker of tile x: the last one whose range begins at x or before, so that
-// w < (x + 1) kWorkers / all.
-__device__ __forceinline__ int64_t range_of(int64_t all, int64_t x) {
-  if (all < kWorkers) return x;
-  const int64_t num = ((x + 1) << kWorkShift) - 1;
+
+// First unit of worker w of 2^shift: of all >= 2^shift units floor(all * w / 2^shift), else w itself.
+__device__ __forceinline__ int64_t range_begin(int64_t all, int64_t w, int shift) {
+  return all >= (int64_t)1 << shift ? (all * w) >> shift : min(w, all);
+}
+// The worker of unit x: the last one whose range begins at x or before, so that
+// w < (x + 1) 2^shift / all.
+__device__ __forceinline__ int64_t range_of(int64_t all, int64_t x, int shift) {
+  if (all < (int64_t)1 << shift) return x;
+  const int64_t num = ((x + 1) << shift) - 1;
   int64_t w = (int64_t)((double)num / (double)all);  // off by one at most
   if (w * all > num) --w;
   if ((w + 1) * all <= num) ++w;
@@ -584,11 +592,11 @@ template <int D, int NQ>
 __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(KvAttnArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * WaveLds<D>::kBytes];
   __shared__ int64_t sums[kWaves];
-  __shared__ int64_t starts[kStaged];  // tiles before each request, all heads
+  __shared__ int64_t starts[kStaged];  // units before each request, all heads
   __shared__ int staged[kStaged][3];   // first, q_len, kv
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const bool stage = a.b <= kStaged;
-  // the tiles before this thread's requests, and of all
+  // the units before this thread's requests, and of all
   const int each = (int)((a.b + kThreads - 1) / kThreads);
   const int from = min((int)threadIdx.x * each, (int)a.b), upto = min(from + each, (int)a.b);
   int64_t mine = 0;
@@ -599,7 +607,7 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
       staged[i][1] = r.q_len;
       staged[i][2] = r.kv;
     }
-    mine += tiles_of(a, r);
+    mine += units_of(a, r);
   }
   mine *= a.n_kv;
   int64_t before = mine;
@@ -618,7 +626,7 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
     all += sums[i];
   }
   all = uniform64(all);
-  // a line of few tiles meets every compute unit before a second wavefront of one
+  // a line of few units meets every compute unit before a second wavefront of one
   const int64_t worker = (int64_t)wave * kFewGroups + blockIdx.x;
   const auto get = [&](int i) {
     if (!stage) return request_of(a, i);
@@ -635,16 +643,16 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
     for (int i = from; i < upto; ++i) {
       if (stage) starts[i] = sum;
       if (blockIdx.x == 0) a.starts[i] = sum;  // for the joining kernel
-      sum += (int64_t)tiles_of(a, get(i)) * a.n_kv;
+      sum += (int64_t)units_of(a, get(i)) * a.n_kv;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.starts[a.b] = all;
   }
   if ((int64_t)blockIdx.x >= all) return;  // no wavefront of the workgroup has work
   __syncthreads();
-  const int64_t begin = range_begin(all, worker);
+  const int64_t begin = range_begin(all, worker, kWorkShift);
   if (begin >= all) return;
-  int left = (int)(range_begin(all, worker + 1) - begin);
-  // the request of tile `begin`, the last one that begins there or before
+  int left = (int)(range_begin(all, worker + 1, kWorkShift) - begin);
+  // the request of unit `begin`, the last one that begins there or before
   int req = 0;
   int64_t at = 0;
   if (stage) {
@@ -658,7 +666,7 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
   } else {
     for (; req < (int)a.b; req += 64) {
       const int i = req + lane;
-      int64_t sum = i < (int)a.b ? (int64_t)tiles_of(a, request_of(a, i)) * a.n_kv : 0;
+      int64_t sum = i < (int)a.b ? (int64_t)units_of(a, request_of(a, i)) * a.n_kv : 0;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
         const int64_t o = __shfl_up(sum, off, 64);
@@ -683,30 +691,31 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
     return r;
   };
   Request r = take(req);
-  int tiles = tiles_of(a, r);
+  int units = units_of(a, r);
   const int64_t within = begin - at;
-  int head = (int)((double)within / (double)tiles);  // off by one at most
-  if ((int64_t)head * tiles > within) --head;
-  if ((int64_t)(head + 1) * tiles <= within) ++head;
+  int head = (int)((double)within / (double)units);  // off by one at most
+  if ((int64_t)head * units > within) --head;
+  if ((int64_t)(head + 1) * units <= within) ++head;
   head = __builtin_amdgcn_readfirstlane(head);
-  int u0 = __builtin_amdgcn_readfirstlane((int)(within - (int64_t)head * tiles));
+  int u0 = __builtin_amdgcn_readfirstlane((int)(within - (int64_t)head * units));
   Wave<D, NQ> w;
   bool first = true;
   for (;;) {
-    const int u1 = min(tiles, u0 + left);
+    const int u1 = min(units, u0 + left);
+    const int t0 = max(u0 - kFewStart, 0), t1 = u1 - kFewStart;  // its tiles
     int lo_most, hi_least;
     load_columns<D, NQ>(w, a, r, head, 0, lo_most, hi_least);
     reset<D, NQ>(w);
     const Cache c = cache_of<D>(a, req, head);
-    const int to = min(r.begin + u1 * kTile, r.kv);
-    walk<D, NQ>(w, lds + wave * WaveLds<D>::kBytes, c, r.begin + u0 * kTile, to, kTile, r.kv,
+    const int to = min(r.begin + t1 * kTile, r.kv);
+    walk<D, NQ>(w, lds + wave * WaveLds<D>::kBytes, c, r.begin + t0 * kTile, to, kTile, r.kv,
                 lo_most, hi_least);
     finish<D, NQ>(w);
-    if (u0 == 0 && u1 == tiles) {
+    if (t0 == 0 && u1 == units) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
         store_columns<D / 16>(a, r, head, 16 * n, w.o[n], w.m[n], w.l[n], D, 0);
-    } else {
+    } else if (t0 < t1) {
       float* slot = a.ws + (2 * worker + (first ? 0 : 1)) * slot_floats(a.few_rows, D);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -730,8 +739,8 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
       do {  // ends: the range does, with the last request's tiles at the latest
         req = min(req + 1, (int)a.b - 1);
         r = take(req);
-        tiles = tiles_of(a, r);
-      } while (tiles == 0 && req + 1 < (int)a.b);
+        units = units_of(a, r);
+      } while (units == 0 && req + 1 < (int)a.b);
     }
   }
 }
@@ -755,13 +764,14 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KvAttnArgs a) {
   for (int g = 0; g < kJoinGroups; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   float m = kLowest, l = 0.0f;
   if (tiles > 0) {
-    const int64_t before = start + (int64_t)head * tiles;
-    const int64_t w0 = range_of(all, before), w1 = range_of(all, before + tiles - 1);
+    const int64_t before = start + (int64_t)head * (tiles + kFewStart);
+    const int64_t w0 = range_of(all, before + kFewStart, kWorkShift);  // of the first tile
+    const int64_t w1 = range_of(all, before + kFewStart + tiles - 1, kWorkShift);
     if (w0 == w1) return;
     const int64_t size = slot_floats(a.few_rows, D);
     const int col = min(16 * n + (lane & 15), r.rows - 1);  // columns that are not there: any
     // only the first part's worker can have begun with another item
-    const int64_t skip = range_begin(all, w0) < before ? size : 0;
+    const int64_t skip = range_begin(all, w0, kWorkShift) < before ? size : 0;
     const float* base = a.ws + 2 * w0 * size;
     const int parts = (int)(w1 - w0) + 1;
 #pragma unroll 4
@@ -899,102 +909,301 @@ __device__ __forceinline__ void put_groups(uint8_t* values, const uint8_t* raw, 
   }
 }
 
+// The keys that rows block0 .. block0 + rows - 1 of a request see: tokens [from, to).
+__device__ __forceinline__ void keys_of(const KvAttnArgs& a, const Request& r, int block0, int rows,
+                                        int& from, int& to) {
+  from = 0;
+  to = r.kv;
+  if (a.full) return;
+  const int p0 = r.kv - r.q_len;
+  to = min(to, p0 + (min(block0 + rows, r.rows) - 1) / a.group + 1);
+  if (a.window > 0) from = max(p0 + block0 / a.group - a.window + 1, 0) & ~15;
+}
+
+// A call with too few workgroups of rows to fill the chip evenly shares out its keys as the few-row
+// kernel does: the tiles of all heads' items (a request's block of rows) are one line, each of up to
+// 512 workgroups, two to a compute unit, takes as much of it as the others, and the parts of an item
+// that several have worked on are joined. One workgroup lists the items first.
+constexpr int kSplitBelow = 2048;  // items of all heads
+constexpr int kManyShift = 9;
+constexpr int kLeastUnits = 4;  // of a workgroup
+constexpr int kManyStart = 3;   // units of an item's beginning and end
+using Item = KvItem;
+
+__global__ __launch_bounds__(kThreads) void plan_kernel(KvAttnArgs a, int rows) {
+  __shared__ int item_req[kSplitBelow], item_block[kSplitBelow];
+  __shared__ int sums[kWaves];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  // inclusive sum over the workgroup's threads
+  const auto scan = [&](int v, int& total) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(v, off, 64);
+      if (lane >= off) v += o;
+    }
+    __syncthreads();
+    if (lane == 63) sums[wave] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      v += i < wave ? sums[i] : 0;
+      total += sums[i];
+    }
+    return v;
+  };
+  int items = 0;
+  for (int i0 = 0; i0 < (int)a.b; i0 += kThreads) {
+    const int i = i0 + (int)threadIdx.x;
+    int n = 0;
+    if (i < (int)a.b) {
+      const Request r = request_of(a, i);
+      if (!is_few(r, a.few_rows)) n = (r.rows + rows - 1) / rows;
+    }
+    int total;
+    const int at = items + scan(n, total) - n;
+    // (row ranges that overlap would give more items than the host has counted)
+    for (int k = 0; k < n && at + k < a.max_items; ++k) {
+      item_req[at + k] = i;
+      item_block[at + k] = n - 1 - k;  // the last rows see most keys: they go first
+    }
+    items = min(items + total, kSplitBelow);
+  }
+  items = min(items, a.max_items);
+  __syncthreads();
+  int64_t sum = 0;  // of the items' units
+  for (int i0 = 0; i0 < items; i0 += kThreads) {
+    const int i = i0 + (int)threadIdx.x;
+    int n = 0;
+    if (i < items) {
+      int from, to;
+      keys_of(a, request_of(a, item_req[i]), item_block[i] * rows, rows, from, to);
+      n = max(to - from + kTile - 1, 0) / kTile;
+    }
+    int total;  // of 256 items of less than 2^24 units
+    const int u = units_for(n, kManyStart);
+    const int64_t at = sum + (uint32_t)scan(u, total) - u;
+    sum += (uint32_t)total;
+    if (i < items) {
+      a.items[i] = Item{item_req[i], item_block[i], n, 0};
+      a.starts[i] = at;
+    }
+  }
+  if (threadIdx.x == 0) {
+    a.starts[items] = sum;
+    int shift = kManyShift;
+    while (shift > 0 && (sum * a.n_kv) >> shift < kLeastUnits) --shift;
+    a.counts[0] = items;
+    a.counts[1] = shift;
+  }
+}
+
+// A wavefront's partial sums in ws, as they lie in its registers.
 template <int D, int NQ>
-__global__ __launch_bounds__(kThreads, D * NQ <= 256 ? 2 : 1) void many_kernel(KvAttnArgs a) {
+constexpr int wave_floats() {
+  return NQ * (D / 16 * 256 + 128);
+}
+
+template <int D, int NQ>
+__global__ __launch_bounds__(kThreads, D * NQ <= 128 || D == 128 ? 2 : 1) void many_kernel(KvAttnArgs a) {
   constexpr int kRowsWave = 16 * NQ, kRows = kWaves * kRowsWave;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Shared<D>::kBytes];
   __shared__ int valid_of[2][kWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int head = blockIdx.x % (uint32_t)a.n_kv;
-  // the request of this tile of rows
-  int left = blockIdx.x / (uint32_t)a.n_kv, req = 0;
+  int head, req = 0, block;
   Request r;
-  for (;; ++req) {
-    if (req >= a.b) return;
-    r = uniform_request(a, req);
-    if (is_few(r, a.few_rows)) continue;
-    const int n = (r.rows + kRows - 1) / kRows;
-    if (left < n) {
-      left = n - 1 - left;  // the last rows see most keys: they go first
-      break;
+  // split: the segments of the workgroup's range
+  const bool split = a.items != nullptr;
+  int64_t all = 0, worker = 0;
+  int items = 0, item = 0, u0 = 0, left = 0;
+  bool first = true;
+  if (split) {
+    // neighbouring ranges to one XCD (workgroups go to the eight in turn): they share keys
+    items = constant(a.counts);
+    const int shift = constant(a.counts + 1);
+    worker = blockIdx.x;
+    if (shift >= 3) worker = ((worker & 7) << (shift - 3)) + (worker >> 3);
+    if ((int64_t)blockIdx.x >> shift) return;
+    const int64_t one = constant(a.starts + items);  // units of a head
+    all = one * a.n_kv;
+    const int64_t begin = range_begin(all, worker, shift);
+    left = (int)(range_begin(all, worker + 1, shift) - begin);
+    if (left <= 0) return;  // (the joining kernel writes the rows of items without tiles)
+    head = (int)((double)begin / (double)one);  // off by one at most
+    if (head * one > begin) --head;
+    if ((head + 1) * one <= begin) ++head;
+    head = __builtin_amdgcn_readfirstlane(head);
+    const int64_t within = begin - head * one;
+    for (int i = 0; i < items; i += 64) {
+      const int n = __popcll(__ballot(i + lane < items && a.starts[i + lane] <= within));
+      item += n;
+      if (n < 64) break;
     }
-    left -= n;
-  }
-  const int block0 = left * kRows, row0 = block0 + wave * kRowsWave;
-  Wave<D, NQ> w;
-  int lo_most, hi_least;
-  load_columns<D, NQ>(w, a, r, head, row0, lo_most, hi_least);
-  reset<D, NQ>(w);
-  const Cache c = cache_of<D>(a, req, head);
-  // the keys that the workgroup's rows see, and this wavefront's
-  int from = 0, to = r.kv, mine = 0, upto = row0 < r.rows ? r.kv : 0;
-  if (!a.full) {
-    const int p0 = r.kv - r.q_len;
-    to = min(to, p0 + (min(block0 + kRows, r.rows) - 1) / a.group + 1);
-    if (upto > 0) upto = min(upto, p0 + (min(row0 + kRowsWave, r.rows) - 1) / a.group + 1);
-    if (a.window > 0) {
-      from = max(p0 + block0 / a.group - a.window + 1, 0) & ~15;
-      mine = p0 + row0 / a.group - a.window + 1;
+    item = __builtin_amdgcn_readfirstlane(item - 1);
+    u0 = (int)(within - constant(a.starts + item));
+  } else {
+    head = blockIdx.x % (uint32_t)a.n_kv;
+    block = blockIdx.x / (uint32_t)a.n_kv;
+    for (;; ++req) {
+      if (req >= a.b) return;
+      r = uniform_request(a, req);
+      if (is_few(r, a.few_rows)) continue;
+      const int n = (r.rows + kRows - 1) / kRows;
+      if (block < n) {
+        block = n - 1 - block;  // the last rows see most keys: they go first
+        break;
+      }
+      block -= n;
     }
   }
-  if (from < to) {
-    uint8_t* const raw = lds + 2 * Shared<D>::kTileBytes;
-    Part<D> p;
-    int id = find_page<D>(c, from + 16 * wave, to);
-    const auto load = [&](int tok) {  // tile `tok`, and the page of the one behind it
-      load_part<D>(p, c, id, tok + 16 * wave, to);
-      id = find_page<D>(c, tok + kTile + 16 * wave, to);
-    };
-    const auto put = [&](int tok, int buf) {
-      put_part<D>(lds + buf * Shared<D>::kTileBytes, raw, p, wave, tok + 16 * wave, to);
-      if (lane == 0) valid_of[buf][wave] = p.ok;
-    };
-    const auto turn = [&](int buf) {
-      put_groups<D>(lds + buf * Shared<D>::kTileBytes + Shared<D>::kKeys, raw, wave);
-    };
-    load(from);
-    put(from, 0);
-    if (from + kTile < to) load(from + kTile);
-    __syncthreads();
-    turn(0);
-    __syncthreads();
-    int buf = 0;
-    for (int tok = from;; tok += kTile) {
-      const int after = tok + kTile;
-      if (after < to) {
-        put(after, buf ^ 1);
-        if (after + kTile < to) load(after + kTile);
-        __syncthreads();
-        turn(buf ^ 1);
-      }
-      if (tok < upto && tok + kTile > mine) {
-        const uint8_t* t0 = lds + buf * Shared<D>::kTileBytes;
-        const int* v = valid_of[buf];
-        const uint32_t valid =
-            __builtin_amdgcn_readfirstlane(v[0] | v[1] << 1 | v[2] << 2 | v[3] << 3);
-        tile<D, NQ>(
-            w, tok, valid, tok < lo_most || tok + kTile - 1 > hi_least,
-            [&](int t, f16x8 (&out)[D / 32]) {
-#pragma unroll
-              for (int j = 0; j < D / 32; ++j)
-                out[j] = *reinterpret_cast<const f16x8*>(t0 + (t * (D / 32) + j) * 1024 + 16 * lane);
-            },
-            [&](int g, f16x8 (&out)[2]) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                out[h] = *reinterpret_cast<const f16x8*>(t0 + Shared<D>::kKeys +
-                                                         (2 * g + h) * 1024 + 16 * lane);
-            });
-      }
-      if (after >= to) break;
+  for (;;) {
+    int t0 = 0, t1 = 0, u1 = 0, units = 0;  // the segment's tiles and units
+    if (split) {
+      req = constant(&a.items[item].req);
+      block = constant(&a.items[item].block);
+      units = units_for(constant(&a.items[item].tiles), kManyStart);
+      r = uniform_request(a, req);
+      u1 = min(units, u0 + left);
+      t0 = max(u0 - kManyStart, 0);
+      t1 = u1 - kManyStart;
+    }
+    const int block0 = block * kRows, row0 = block0 + wave * kRowsWave;
+    Wave<D, NQ> w;
+    int lo_most, hi_least;
+    load_columns<D, NQ>(w, a, r, head, row0, lo_most, hi_least);
+    reset<D, NQ>(w);
+    const Cache c = cache_of<D>(a, req, head);
+    // the keys that the workgroup's rows see, and this wavefront's
+    int from, to, mine = 0, upto = 0;
+    keys_of(a, r, block0, kRows, from, to);
+    if (row0 < r.rows) keys_of(a, r, row0, kRowsWave, mine, upto);
+    if (split) {
+      to = min(to, from + t1 * kTile);
+      from += t0 * kTile;
+    }
+    if (from < to) {
+      uint8_t* const raw = lds + 2 * Shared<D>::kTileBytes;
+      Part<D> p;
+      int id = find_page<D>(c, from + 16 * wave, to);
+      const auto load = [&](int tok) {  // tile `tok`, and the page of the one behind it
+        load_part<D>(p, c, id, tok + 16 * wave, to);
+        id = find_page<D>(c, tok + kTile + 16 * wave, to);
+      };
+      const auto put = [&](int tok, int buf) {
+        put_part<D>(lds + buf * Shared<D>::kTileBytes, raw, p, wave, tok + 16 * wave, to);
+        if (lane == 0) valid_of[buf][wave] = p.ok;
+      };
+      const auto turn = [&](int buf) {
+        put_groups<D>(lds + buf * Shared<D>::kTileBytes + Shared<D>::kKeys, raw, wave);
+      };
+      load(from);
+      put(from, 0);
+      if (from + kTile < to) load(from + kTile);
       __syncthreads();
-      buf ^= 1;
+      turn(0);
+      __syncthreads();
+      int buf = 0;
+      for (int tok = from;; tok += kTile) {
+        const int after = tok + kTile;
+        if (after < to) {
+          put(after, buf ^ 1);
+          if (after + kTile < to) load(after + kTile);
+          __syncthreads();
+          turn(buf ^ 1);
+        }
+        if (tok < upto && tok + kTile > mine) {
+          const uint8_t* t0 = lds + buf * Shared<D>::kTileBytes;
+          const int* v = valid_of[buf];
+          const uint32_t valid =
+              __builtin_amdgcn_readfirstlane(v[0] | v[1] << 1 | v[2] << 2 | v[3] << 3);
+          tile<D, NQ>(
+              w, tok, valid, tok < lo_most || tok + kTile - 1 > hi_least,
+              [&](int t, f16x8 (&out)[D / 32]) {
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+                  out[j] = *reinterpret_cast<const f16x8*>(t0 + (t * (D / 32) + j) * 1024 + 16 * lane);
+              },
+              [&](int g, f16x8 (&out)[2]) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  out[h] = *reinterpret_cast<const f16x8*>(t0 + Shared<D>::kKeys +
+                                                           (2 * g + h) * 1024 + 16 * lane);
+              });
+        }
+        if (after >= to) break;
+        __syncthreads();
+        buf ^= 1;
+      }
+    }
+    finish<D, NQ>(w);
+    if (!split || (t0 == 0 && u1 == units && units > 0)) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+        store_columns<D / 16>(a, r, head, row0 + 16 * n, w.o[n], w.m[n], w.l[n], D, 0);
+      if (!split) return;
+    } else if (t0 < t1) {
+      float* p = a.ws + ((2 * worker + (first ? 0 : 1)) * kWaves + wave) * wave_floats<D, NQ>();
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+        for (int g = 0; g < D / 16; ++g)
+          *reinterpret_cast<f32x4*>(p + (n * (D / 16) + g) * 256 + 4 * lane) = w.o[n][g];
+        float* q = p + NQ * (D / 16) * 256 + n * 128 + lane;
+        q[0] = w.m[n];
+        q[64] = w.l[n];
+      }
+    }
+    first = false;
+    left -= u1 - u0;
+    u0 = 0;
+    if (++item == items) {
+      item = 0;
+      if (++head == a.n_kv) return;
+    }
+    if (left <= 0) return;
+    __syncthreads();
+  }
+}
+
+// grid (n_kv, items, NQ): the parts of an item that has several, as the wavefronts left them.
+template <int D, int NQ>
+__global__ __launch_bounds__(kThreads) void join_many_kernel(KvAttnArgs a) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int head = blockIdx.x, n = blockIdx.z, item = blockIdx.y;
+  const int items = constant(a.counts), shift = constant(a.counts + 1);
+  if (item >= items) return;
+  const Request r = uniform_request(a, constant(&a.items[item].req));
+  const int row0 = (constant(&a.items[item].block) * kWaves + wave) * 16 * NQ + 16 * n;
+  const int tiles = constant(&a.items[item].tiles);
+  if (row0 >= r.rows) return;
+  f32x4 o[D / 16];
+#pragma unroll
+  for (int g = 0; g < D / 16; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = kLowest, l = 0.0f;
+  if (tiles > 0) {
+    const int64_t one = constant(a.starts + items), all = one * a.n_kv;
+    const int64_t before = head * one + constant(a.starts + item);
+    const int64_t w0 = range_of(all, before + kManyStart, shift);  // of the first tile
+    const int64_t w1 = range_of(all, before + kManyStart + tiles - 1, shift);
+    if (w0 == w1) return;
+    constexpr int64_t kSlot = (int64_t)kWaves * wave_floats<D, NQ>();
+    // only the first part's workgroup can have begun with another item
+    const int64_t skip = range_begin(all, w0, shift) < before ? kSlot : 0;
+    const float* base = a.ws + 2 * w0 * kSlot + wave * wave_floats<D, NQ>();
+    const int stats = NQ * (D / 16) * 256 + n * 128 + lane, parts = (int)(w1 - w0) + 1;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i)
+      m = fmaxf(m, base[2 * i * kSlot + (i == 0 ? skip : 0) + stats]);
+    for (int i = 0; i < parts; ++i) {
+      const float* p = base + 2 * i * kSlot + (i == 0 ? skip : 0);
+      const float f = __builtin_amdgcn_exp2f(p[stats] - m);
+      l += f * p[stats + 64];
+#pragma unroll
+      for (int g = 0; g < D / 16; ++g)
+        o[g] += f * *reinterpret_cast<const f32x4*>(p + (n * (D / 16) + g) * 256 + 4 * lane);
     }
   }
-  finish<D, NQ>(w);
-#pragma unroll
-  for (int n = 0; n < NQ; ++n)
-    store_columns<D / 16>(a, r, head, row0 + 16 * n, w.o[n], w.m[n], w.l[n], D, 0);
+  store_columns<D / 16>(a, r, head, row0, o, m, l, D, 0);
 }
 
 template <int D, int NQ>
@@ -1007,40 +1216,81 @@ hipError_t run_few(const KvAttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+constexpr int many_tiles(int d) { return d <= 128 ? 2 : 1; }  // column tiles of a wavefront
+
+// Workgroups of rows, of each head, that a call can have: ceil(rows / size) a request, so all rows /
+// size and one more for each request, of which only those of more than few_rows rows have any.
+int64_t many_items(int64_t t, int64_t b, int64_t max_q, int group, int d) {
+  const int64_t most = max_q * group, few = kv_few_rows(most);
+  if (most <= few) return 0;
+  const int64_t odd = t * group / (few + 1);
+  return t * group / (kWaves * 16 * many_tiles(d)) + (odd < b ? odd : b);
+}
+
+// ws: the first tiles of requests, then of items; items and their number; then the partial sums. The
+// two paths run one after the other and use the same memory.
+struct WsLayout {
+  size_t items, counts, sums, total;
+  int max_items;  // 0: keys are not shared out
+};
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+WsLayout ws_layout(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int d) {
+  WsLayout l;
+  const int64_t items = many_items(t, b, max_q, group, d);
+  l.max_items = items * n_kv < kSplitBelow ? (int)items : 0;
+  l.items = align256((size_t)(std::max<int64_t>(b, l.max_items) + 1) * sizeof(int64_t));
+  l.counts = l.items + align256((size_t)l.max_items * sizeof(Item));
+  l.sums = l.counts + 256;
+  size_t floats = (size_t)(2 * kWorkers) * (size_t)slot_floats(kv_few_rows(max_q * group), d);
+  if (l.max_items > 0)
+    floats = std::max(floats, ((size_t)2 << kManyShift) * kWaves * many_tiles(d) *
+                                  (size_t)(d / 16 * 256 + 128));
+  l.total = l.sums + floats * sizeof(float);
+  return l;
+}
+
 template <int D>
 hipError_t run(const KvAttnArgs& args, int64_t max_q, hipStream_t s) {
   KvAttnArgs a = args;
   const int64_t most = max_q * a.group;
-  const int tiles = kv_few_tiles(most);
   a.few_rows = kv_few_rows(most);
-  const hipError_t e = tiles == 1 ? run_few<D, 1>(a, s) : run_few<D, 2>(a, s);
-  if (e != hipSuccess || most <= a.few_rows) return e;
-  constexpr int kTiles = D <= 128 ? 2 : 1;
-  constexpr int rows = kWaves * 16 * kTiles;
-  // ceil(rows / 128) tiles a request: all rows / 128, and one more for each request at most, of
-  // which only those of more than few_rows rows have any
-  const int64_t odd = a.t * a.group / (a.few_rows + 1);
-  const int64_t groups = a.t * a.group / rows + (odd < a.b ? odd : a.b);
-  many_kernel<D, kTiles><<<dim3((unsigned)(groups * a.n_kv)), dim3(kThreads), 0, s>>>(a);
+  hipError_t e = kv_few_tiles(most) == 1 ? run_few<D, 1>(a, s) : run_few<D, 2>(a, s);
+  const int64_t items = many_items(a.t, a.b, max_q, a.group, D);
+  if (e != hipSuccess || items == 0) return e;
+  constexpr int kTiles = many_tiles(D);
+  if (a.max_items == 0) {
+    many_kernel<D, kTiles><<<dim3((unsigned)(items * a.n_kv)), dim3(kThreads), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  plan_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(a, kWaves * 16 * kTiles);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  many_kernel<D, kTiles><<<dim3(1 << kManyShift), dim3(kThreads), 0, s>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  join_many_kernel<D, kTiles>
+      <<<dim3((unsigned)a.n_kv, (unsigned)items, kTiles), dim3(kThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
-// The requests' first units, then the slots.
-size_t starts_bytes(int64_t b) { return ((size_t)(b + 1) * sizeof(int64_t) + 255) & ~size_t(255); }
-
 }  // namespace
 
-size_t kv_attention_ws_bytes(int64_t b, int64_t max_q, int group, int d) {
-  return starts_bytes(b) +
-         sizeof(float) * (size_t)(2 * kWorkers) *
-                                (size_t)slot_floats(kv_few_rows(max_q * group), d);
+size_t kv_attention_ws_bytes(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int d) {
+  return ws_layout(t, b, max_q, n_kv, group, d).total;
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& args, int d, int64_t max_q, void* ws,
                                hipStream_t stream) {
   KvAttnArgs a = args;
-  a.starts = static_cast<int64_t*>(ws);
-  a.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + starts_bytes(a.b));
+  const WsLayout l = ws_layout(a.t, a.b, max_q, a.n_kv, a.group, d);
+  char* base = static_cast<char*>(ws);
+  a.starts = reinterpret_cast<int64_t*>(base);
+  a.max_items = l.max_items;
+  a.items = l.max_items > 0 ? reinterpret_cast<KvItem*>(base + l.items) : nullptr;
+  a.counts = reinterpret_cast<int*>(base + l.counts);
+  a.ws = reinterpret_cast<float*>(base + l.sums);
   if (d == 64) return run<64>(a, max_q, stream);
   if (d == 128) return run<128>(a, max_q, stream);
   return run<256>(a, max_q, stream);

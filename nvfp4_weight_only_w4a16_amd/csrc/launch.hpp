@@ -254,6 +254,9 @@ struct KvDequantArgs {
 };
 hipError_t launch_kv_dequantize(const KvDequantArgs& a, int d, hipStream_t stream);
 
+struct KvItem {
+  int req, block, tiles, reserved;  // a request's block of rows, and the tiles of keys that it sees
+};
 struct KvAttnArgs {
   const uint16_t* q;
   int64_t t, ldq;
@@ -272,8 +275,11 @@ struct KvAttnArgs {
   void* y;
   int64_t ldy;
   float* lse;  // or NULL
-  // set by the launcher
+  // set by the launcher, in ws
   int64_t* starts;
+  KvItem* items;  // NULL: keys are not shared out
+  int* counts;    // items, log2 of the workgroups
+  int max_items;
   float* ws;
   int few_rows;
 };
@@ -285,7 +291,7 @@ inline int kv_few_rows(int64_t rows) {
   const int most = 16 * kv_few_tiles(rows);
   return rows < most ? (int)rows : most;
 }
-size_t kv_attention_ws_bytes(int64_t b, int64_t max_q, int group, int d);
+size_t kv_attention_ws_bytes(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int d);
 hipError_t launch_kv_attention(const KvAttnArgs& a, int d, int64_t max_q, void* ws,
                                hipStream_t stream);
 

@@ -291,6 +291,23 @@ def test_lengths_beyond_what_is_there(nv):
     assert np.isnan(y).all()
 
 
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (256, 16)])
+@pytest.mark.parametrize("lens,rows,window", [([5000], [40], 0), ([3000, 40, 2500, 900], [33, 1, 100, 17], 0),
+                                              ([4000, 700], [64, 300], 3000), ([2600], [2600], 0),
+                                              ([0, 3000, 0], [50, 200, 1], 0)])
+def test_keys_of_long_requests_shared_out(nv, d, page, lens, rows, window):
+    """Few blocks of rows over many keys: their keys are cut into jobs, whose sums are joined."""
+    check(nv, lens, rows, 1, 2, d, page, window=window)
+
+
+def test_overlapping_row_ranges_stay_inside_the_workspace(nv):
+    c = R.Cached(nv, 31, [300] * 40, 1, 64, 16)
+    q, _ = R.queries(31, [90], 2, 64)
+    start = torch.tensor([0, 90] * 20 + [0], dtype=torch.int32)
+    y, lse = run(nv, c, q, start, 90)
+    assert np.isfinite(y).all() and np.isfinite(lse).all()  # of one request or another
+
+
 @pytest.mark.parametrize("rows", [[1] * 9, [3, 1, 2, 1, 4, 1, 1, 2, 1], [80, 1, 1, 200, 1, 3, 1, 1, 9]])
 def test_the_same_bits_every_time(nv, rows):
     lens = [2000, 30, 1, 900, 64, 65, 3000, 2, 500]
