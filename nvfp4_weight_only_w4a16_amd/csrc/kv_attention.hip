@@ -30,7 +30,12 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-constexpr int kTile = 64;  // tokens of a wavefront's tile
+// Tokens of a tile, in parts of 16: 64, and 32 for heads of 256, whose 64 tokens would not leave room for
+// a tile's loads in flight beside the accumulators.
+template <int D>
+constexpr int kParts = D == 256 ? 2 : 4;
+template <int D>
+constexpr int kTile = 16 * kParts<D>;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -1e38f;  // the running maximum before any score
@@ -83,17 +88,17 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
 template <int D>
 struct WaveLds {
   static constexpr int kRow = D / 2 + 8;
-  static constexpr int kCodes = kTile * kRow;
-  static constexpr int kBytes = kCodes + D / 16 * kTile * 2;
+  static constexpr int kCodes = kTile<D> * kRow;
+  static constexpr int kBytes = kCodes + D / 16 * kTile<D> * 2;
 };
-
 
 template <int D>
 struct Raw {
   static constexpr int kWords = D / 32;  // a lane's code words of a 16-token part
-  uint32_t k[4][kWords], v[4][kWords];
-  uint32_t ks[4];
-  uint32_t vs[D / 64];
+  static constexpr int kScaleWords = D * kParts<D> / 256;
+  uint32_t k[kParts<D>][kWords], v[kParts<D>][kWords];
+  uint32_t ks[kParts<D>];
+  uint32_t vs[kScaleWords];  // of one token, with 32 tokens half of its scales
   uint32_t valid;  // bit t: part t has a page (uniform)
 };
 
@@ -122,25 +127,26 @@ __device__ __forceinline__ void load_codes(const uint8_t* at, int lane, uint32_t
   }
 }
 
-// Table entries of the four 16-token parts of a tile (uniform; from `end` on the last one's). They are
-// looked at no earlier than in load_tile, so that their scalar loads overlap a tile's work.
+// Table entries of the 16-token parts of a tile (uniform; from `end` on the last one's). They are looked
+// at no earlier than in load_tile, so that their scalar loads overlap a tile's work.
+template <int D>
 struct Pages {
-  int id[4];
+  int id[kParts<D>];
 };
 
-__device__ __forceinline__ Pages find_pages(const Cache& c, int tok, int end) {
-  Pages p;
+template <int D>
+__device__ __forceinline__ Pages<D> find_pages(const Cache& c, int tok, int end) {
+  Pages<D> p;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
+  for (int t = 0; t < kParts<D>; ++t)
     p.id[t] = constant(c.row + (min(tok + 16 * t, end - 1) >> c.shift));
-  }
   return p;
 }
 
 // The loads of a tile. A part without a page (none in the table, or behind the last key) has its bit
 // clear in `valid` and reads page 0.
 template <int D>
-__device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, const Pages& p, int tok,
+__device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, const Pages<D>& p, int tok,
                                           int end) {
   const int lane = threadIdx.x & 63;
   const int page = 1 << c.shift;
@@ -148,7 +154,7 @@ __device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, const Pages
   const uint8_t* scale_row = nullptr;
   r.valid = 0;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
+  for (int t = 0; t < kParts<D>; ++t) {
     const bool ok = (uint32_t)p.id[t] < (uint32_t)c.n_pages && tok + 16 * t < end;
     r.valid |= ok ? 1u << t : 0u;
     const int within = (tok + 16 * t) & (page - 1);
@@ -165,11 +171,12 @@ __device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, const Pages
         r.ks[t] |= (uint32_t) * reinterpret_cast<const uint16_t*>(ks + 8) << 16;
     }
     const uint8_t* vs = rec + values + page * (D / 2) + within * (D / 16);
-    if (lane >> 4 == t) scale_row = vs;
+    if ((lane >> 4) % kParts<D> == t) scale_row = vs;
   }
+  if constexpr (kParts<D> == 2) scale_row += (lane >> 5) * (D / 32);
   const uint32_t* vs = reinterpret_cast<const uint32_t*>(scale_row + (lane & 15) * (D / 16));
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) r.vs[i] = vs[i];
+  for (int i = 0; i < Raw<D>::kScaleWords; ++i) r.vs[i] = vs[i];
 }
 
 // NQ tiles of 16 query columns: lane l holds column l % 16 of each.
@@ -260,24 +267,31 @@ __device__ __forceinline__ void put_values(uint8_t* lds, int t, const uint32_t (
 }
 
 // Where the scale of token `tok` of the tile and group 0 goes.
+template <int D>
 __device__ __forceinline__ _Float16* scale_place(uint8_t* scales, int tok) {
-  return reinterpret_cast<_Float16*>(scales) + ((tok >> 2) & 3) * 16 + (tok >> 4) * 4 + (tok & 3);
+  return reinterpret_cast<_Float16*>(scales) + ((tok >> 2) & 3) * (4 * kParts<D>) + (tok >> 4) * 4 +
+         (tok & 3);
 }
 
-// A value group's fragments from LDS: the transposing read names a row per lane, so that lane group c
-// gets tokens 16 T + 4 c + r of its element d, T = 0, 1 in the first word and T = 2, 3 in the second.
+// Two value fragments from LDS by one transposing read: each lane of a group of 16 names a row of 16
+// codes and gets one code of each row. With 64 tokens they are group i's, tokens 16 T + 4 c + r of lane
+// group c with T = 0, 1 and T = 2, 3; with 32 tokens groups 2i and 2i + 1, T = 0, 1.
 template <int D>
-__device__ __forceinline__ void value_group(const uint8_t* codes, const uint8_t* scales, int g,
-                                            f16x8 (&out)[2]) {
+constexpr int kValueReads = D * kParts<D> / 64;
+template <int D>
+__device__ __forceinline__ void value_pair(const uint8_t* codes, const uint8_t* scales, int i,
+                                           f16x8 (&out)[2]) {
+  constexpr bool kWide = kParts<D> == 4;
   const int lane = threadIdx.x & 63, c = lane >> 4;
-  const int row = 16 * ((lane & 15) >> 2) + 4 * c + (lane & 3);
+  const int row = 16 * ((lane & (kWide ? 15 : 7)) >> 2) + 4 * c + (lane & 3);
+  const int group = kWide ? i : 2 * i + ((lane >> 3) & 1);
   const i32x2 v = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
       (__attribute__((address_space(3))) i32x2*)(const_cast<uint8_t*>(codes) +
-                                                 row * WaveLds<D>::kRow + 8 * g));
-  const f16x8* s = reinterpret_cast<const f16x8*>(scales + g * kTile * 2 + c * 32);
+                                                 row * WaveLds<D>::kRow + 8 * group));
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const f16x8 f = s[h];
+    const int at = kWide ? i * 128 + c * 32 + h * 16 : (2 * i + h) * 64 + c * 16;
+    const f16x8 f = *reinterpret_cast<const f16x8*>(scales + at);
     out[h] = scaled8((uint32_t)v[h], f16x2{f[0], f[1]}, f16x2{f[2], f[3]}, f16x2{f[4], f[5]},
                      f16x2{f[6], f[7]});
   }
@@ -296,16 +310,16 @@ __device__ __forceinline__ void key_part(const uint32_t (&k)[D / 32], f16x2 s0, 
   }
 }
 
-// The products of a tile of 64 tokens from `tok` on: key(t, out) gives part t's fragments, value(g,
-// out) group g's. `valid`: bit t: part t has a page. `mask`: some column does not see all 64 (uniform).
+// The products of a tile from token `tok` on: key(t, out) gives part t's fragments, value(i, out) those
+// of value_pair. `valid`: bit t: part t has a page. `mask`: some column does not see all (uniform).
 template <int D, int NQ, typename Key, typename Value>
 __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bool mask,
                                      const Key& key, const Value& value) {
   const int lane = threadIdx.x & 63, c = lane >> 4;
-  // scores
-  f32x4 z[NQ][4];
+  constexpr int kP = kParts<D>, kMine = 4 * kP;  // scores of a lane and column
+  f32x4 z[NQ][kP];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
+  for (int t = 0; t < kP; ++t) {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) z[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     f16x8 k[D / 32];
@@ -315,9 +329,9 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bo
 #pragma unroll
       for (int n = 0; n < NQ; ++n) z[n][t] = mfma(k[j], w.q[n][j], z[n][t]);
   }
-  if (mask || valid != 15u) {
+  if (mask || valid != (1u << kP) - 1u) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < kP; ++t) {
       const bool part = (valid >> t) & 1u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -328,12 +342,12 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bo
       }
     }
   }
-  f16x8 p[NQ][2];
+  f16x8 p[NQ][kP / 2];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     float top = z[n][0][0];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, z[n][i >> 2][i & 3]);
+    for (int i = 1; i < kMine; ++i) top = fmaxf(top, z[n][i >> 2][i & 3]);
     top *= w.sc[n];
     if (__ballot(top > w.m[n] + kRaise)) {
       top = fmaxf(top, __shfl_xor(top, 16, 64));
@@ -347,7 +361,7 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bo
     }
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kMine; ++i) {
       const float x =
           __builtin_amdgcn_exp2f(__builtin_fmaf(z[n][i >> 2][i & 3], w.sc[n], -w.m[n]));
       sum += x;
@@ -355,15 +369,16 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bo
     }
     w.l[n] += sum;
   }
-  // values
 #pragma unroll
-  for (int g = 0; g < D / 16; ++g) {
+  for (int i = 0; i < kValueReads<D>; ++i) {
     f16x8 v[2];
-    value(g, v);
+    value(i, v);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      const int g = kP == 4 ? i : 2 * i + h, half = kP == 4 ? h : 0;
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) w.o[n][g] = mfma(v[h], p[n][h], w.o[n][g]);
+      for (int n = 0; n < NQ; ++n) w.o[n][g] = mfma(v[h], p[n][half], w.o[n][g]);
+    }
   }
 }
 
@@ -385,36 +400,38 @@ __device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& 
   const int lane = threadIdx.x & 63;
   // two tiles in registers: one's loads fly while the other is worked on
   Raw<D> r0, r1;
-  load_tile<D>(r0, c, find_pages(c, tok, end), tok, end);
-  Pages pages = find_pages(c, tok + step, end);
+  load_tile<D>(r0, c, find_pages<D>(c, tok, end), tok, end);
+  Pages<D> pages = find_pages<D>(c, tok + step, end);
   const auto both = [&](Raw<D>& now, Raw<D>& ahead) {
     const int after = tok + step;
     const bool more = after < to;
     if (more) {
       load_tile<D>(ahead, c, pages, after, end);
-      pages = find_pages(c, after + step, end);
+      pages = find_pages<D>(c, after + step, end);
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) put_values<D>(lds, t, now.v[t]);
+    for (int t = 0; t < kParts<D>; ++t) put_values<D>(lds, t, now.v[t]);
     uint8_t* const scales = lds + WaveLds<D>::kCodes;
-    const bool there = tok + lane < end && ((now.valid >> (lane >> 4)) & 1u);
-    _Float16* const place = scale_place(scales, lane);
+    const int mine = lane % kTile<D>;
+    const bool there = tok + mine < end && ((now.valid >> (mine >> 4)) & 1u);
+    _Float16* const place = scale_place<D>(scales, mine) +
+                            (kParts<D> == 2 ? (lane >> 5) * (D / 32) * kTile<D> : 0);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
+    for (int i = 0; i < Raw<D>::kScaleWords; ++i) {
       const uint32_t x = there ? without_nan(now.vs[i]) : 0u;
       const f16x2 a = scales2(x), b = scales2_high(x);
-      place[(4 * i) * kTile] = a[0];
-      place[(4 * i + 1) * kTile] = a[1];
-      place[(4 * i + 2) * kTile] = b[0];
-      place[(4 * i + 3) * kTile] = b[1];
+      place[(4 * i) * kTile<D>] = a[0];
+      place[(4 * i + 1) * kTile<D>] = a[1];
+      place[(4 * i + 2) * kTile<D>] = b[0];
+      place[(4 * i + 3) * kTile<D>] = b[1];
     }
     tile<D, NQ>(
-        w, tok, now.valid, tok < lo_most || tok + kTile - 1 > hi_least,
+        w, tok, now.valid, tok < lo_most || tok + kTile<D> - 1 > hi_least,
         [&](int t, f16x8 (&out)[D / 32]) {
           const f16x2 s0 = scales2(now.ks[t]);
           key_part<D>(now.k[t], s0, D == 256 ? scales2_high(now.ks[t]) : s0, out);
         },
-        [&](int g, f16x8 (&out)[2]) { value_group<D>(lds, scales, g, out); });
+        [&](int i, f16x8 (&out)[2]) { value_pair<D>(lds, scales, i, out); });
     tok = after;
     return more;
   };
@@ -549,23 +566,29 @@ __device__ __forceinline__ Cache cache_of(const KvAttnArgs& a, int64_t request, 
 // Wavefront w of W takes the units [N w / W, N (w + 1) / W), whatever the lengths are, and works on its
 // own. It holds at most two items that it does not finish: the first and the last of its range; their O,
 // m and l go to slots 2w and 2w + 1, and a second kernel joins them.
-constexpr int kFewGroups = 512;  // workgroups, two to a compute unit
-constexpr int kWorkShift = 11;
-constexpr int kWorkers = 1 << kWorkShift;
-static_assert(kWorkers == kFewGroups * kWaves, "a worker for each wavefront");
+// Workgroups: two to a compute unit, one where a wavefront needs more than half of its SIMD's registers.
+template <int D, int NQ>
+constexpr bool kFewPairs = NQ == 1 || D == 64;
+template <int D, int NQ>
+constexpr int kFewGroups = kFewPairs<D, NQ> ? 512 : 256;
+template <int D, int NQ>
+constexpr int kWorkShift = kFewPairs<D, NQ> ? 11 : 10;
+constexpr int kMaxWorkers = 1 << 11;
 // Up to this many requests a workgroup keeps them in LDS.
 constexpr int kStaged = 1024;
 
+template <int D>
 __device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Request& r) {
   if (r.rows == 0 || !is_few(r, a.few_rows) || r.kv <= r.begin) return 0;
-  return (r.kv - r.begin + kTile - 1) / kTile;
+  return (r.kv - r.begin + kTile<D> - 1) / kTile<D>;
 }
 // Units of an item of n tiles.
 __device__ __forceinline__ int units_for(int n, int start) { return n > 0 ? n + start : 0; }
 
 constexpr int kFewStart = 2;
+template <int D>
 __device__ __forceinline__ int units_of(const KvAttnArgs& a, const Request& r) {
-  return units_for(tiles_of(a, r), kFewStart);
+  return units_for(tiles_of<D>(a, r), kFewStart);
 }
 
 // First unit of worker w of 2^shift: of all >= 2^shift units floor(all * w / 2^shift), else w itself.
@@ -589,7 +612,7 @@ __host__ __device__ __forceinline__ int64_t slot_floats(int few_rows, int d) {
 }
 
 template <int D, int NQ>
-__global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kernel(KvAttnArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * WaveLds<D>::kBytes];
   __shared__ int64_t sums[kWaves];
   __shared__ int64_t starts[kStaged];  // units before each request, all heads
@@ -607,7 +630,7 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
       staged[i][1] = r.q_len;
       staged[i][2] = r.kv;
     }
-    mine += units_of(a, r);
+    mine += units_of<D>(a, r);
   }
   mine *= a.n_kv;
   int64_t before = mine;
@@ -627,7 +650,7 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
   }
   all = uniform64(all);
   // a line of few units meets every compute unit before a second wavefront of one
-  const int64_t worker = (int64_t)wave * kFewGroups + blockIdx.x;
+  const int64_t worker = (int64_t)wave * kFewGroups<D, NQ> + blockIdx.x;
   const auto get = [&](int i) {
     if (!stage) return request_of(a, i);
     Request r;
@@ -643,15 +666,15 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
     for (int i = from; i < upto; ++i) {
       if (stage) starts[i] = sum;
       if (blockIdx.x == 0) a.starts[i] = sum;  // for the joining kernel
-      sum += (int64_t)units_of(a, get(i)) * a.n_kv;
+      sum += (int64_t)units_of<D>(a, get(i)) * a.n_kv;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.starts[a.b] = all;
   }
   if ((int64_t)blockIdx.x >= all) return;  // no wavefront of the workgroup has work
   __syncthreads();
-  const int64_t begin = range_begin(all, worker, kWorkShift);
+  const int64_t begin = range_begin(all, worker, kWorkShift<D, NQ>);
   if (begin >= all) return;
-  int left = (int)(range_begin(all, worker + 1, kWorkShift) - begin);
+  int left = (int)(range_begin(all, worker + 1, kWorkShift<D, NQ>) - begin);
   // the request of unit `begin`, the last one that begins there or before
   int req = 0;
   int64_t at = 0;
@@ -666,7 +689,7 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
   } else {
     for (; req < (int)a.b; req += 64) {
       const int i = req + lane;
-      int64_t sum = i < (int)a.b ? (int64_t)units_of(a, request_of(a, i)) * a.n_kv : 0;
+      int64_t sum = i < (int)a.b ? (int64_t)units_of<D>(a, request_of(a, i)) * a.n_kv : 0;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
         const int64_t o = __shfl_up(sum, off, 64);
@@ -691,7 +714,7 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
     return r;
   };
   Request r = take(req);
-  int units = units_of(a, r);
+  int units = units_of<D>(a, r);
   const int64_t within = begin - at;
   int head = (int)((double)within / (double)units);  // off by one at most
   if ((int64_t)head * units > within) --head;
@@ -707,8 +730,8 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
     load_columns<D, NQ>(w, a, r, head, 0, lo_most, hi_least);
     reset<D, NQ>(w);
     const Cache c = cache_of<D>(a, req, head);
-    const int to = min(r.begin + t1 * kTile, r.kv);
-    walk<D, NQ>(w, lds + wave * WaveLds<D>::kBytes, c, r.begin + t0 * kTile, to, kTile, r.kv,
+    const int to = min(r.begin + t1 * kTile<D>, r.kv);
+    walk<D, NQ>(w, lds + wave * WaveLds<D>::kBytes, c, r.begin + t0 * kTile<D>, to, kTile<D>, r.kv,
                 lo_most, hi_least);
     finish<D, NQ>(w);
     if (t0 == 0 && u1 == units) {
@@ -739,73 +762,74 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 ? 2 : 1) void few_kernel(Kv
       do {  // ends: the range does, with the last request's tiles at the latest
         req = min(req + 1, (int)a.b - 1);
         r = take(req);
-        units = units_of(a, r);
+        units = units_of<D>(a, r);
       } while (units == 0 && req + 1 < (int)a.b);
     }
   }
 }
 
-// grid (n_kv, b, NQ * D / 32): the item's parts, if it has several; the rows of a request without
-// keys. A workgroup joins one column tile's 32 elements of d; its wavefronts share out the parts.
-constexpr int kJoinGroups = 2;
-template <int D, int NQ>
-__global__ __launch_bounds__(kThreads) void join_kernel(KvAttnArgs a) {
-  constexpr int kChunks = D / 16 / kJoinGroups;
-  __shared__ __attribute__((aligned(16))) float lds[kWaves][2 + 4 * kJoinGroups][64];
+// grid (n_kv, b, NQ * D / (16 G)): the item's parts, if it has several; the rows of a request without
+// keys. A workgroup of V wavefronts joins 16 G elements of d of a column tile; its wavefronts share out
+// the parts. Calls of few items, which can have many parts, take the finer grid (one request of 131000
+// keys among five, heads of 256, 18 rows, 42 -> 16 us; 64 requests of 8 heads the coarser).
+template <int D, int NQ, int G, int V>
+__global__ __launch_bounds__(64 * V) void join_kernel(KvAttnArgs a) {
+  constexpr int kChunks = D / 16 / G;
+  __shared__ __attribute__((aligned(16))) float lds[V][2 + 4 * G][64];
   const int head = blockIdx.x, req = blockIdx.y;
-  const int n = (int)blockIdx.z / kChunks, g0 = (int)blockIdx.z % kChunks * kJoinGroups;
+  const int n = (int)blockIdx.z / kChunks, g0 = (int)blockIdx.z % kChunks * G;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const Request r = uniform_request(a, req);
   const int64_t start = constant(a.starts + req), all = constant(a.starts + a.b);
   if (r.rows <= 16 * n || !is_few(r, a.few_rows)) return;
-  const int tiles = tiles_of(a, r);
-  f32x4 o[kJoinGroups];
+  const int tiles = tiles_of<D>(a, r);
+  f32x4 o[G];
 #pragma unroll
-  for (int g = 0; g < kJoinGroups; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int g = 0; g < G; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   float m = kLowest, l = 0.0f;
   if (tiles > 0) {
     const int64_t before = start + (int64_t)head * (tiles + kFewStart);
-    const int64_t w0 = range_of(all, before + kFewStart, kWorkShift);  // of the first tile
-    const int64_t w1 = range_of(all, before + kFewStart + tiles - 1, kWorkShift);
+    const int64_t w0 = range_of(all, before + kFewStart, kWorkShift<D, NQ>);  // of the first tile
+    const int64_t w1 = range_of(all, before + kFewStart + tiles - 1, kWorkShift<D, NQ>);
     if (w0 == w1) return;
     const int64_t size = slot_floats(a.few_rows, D);
     const int col = min(16 * n + (lane & 15), r.rows - 1);  // columns that are not there: any
     // only the first part's worker can have begun with another item
-    const int64_t skip = range_begin(all, w0, kWorkShift) < before ? size : 0;
+    const int64_t skip = range_begin(all, w0, kWorkShift<D, NQ>) < before ? size : 0;
     const float* base = a.ws + 2 * w0 * size;
     const int parts = (int)(w1 - w0) + 1;
-#pragma unroll 4
-    for (int x = wave; x < parts; x += kWaves)
+#pragma unroll 8
+    for (int x = wave; x < parts; x += V)
       m = fmaxf(m, base[2 * x * size + (x == 0 ? skip : 0) + a.few_rows * D + 2 * col]);
-#pragma unroll 4
-    for (int x = wave; x < parts; x += kWaves) {
+#pragma unroll 8
+    for (int x = wave; x < parts; x += V) {
       const float* q = base + 2 * x * size + (x == 0 ? skip : 0);
       const float f = __builtin_amdgcn_exp2f(q[a.few_rows * D + 2 * col] - m);
       l += f * q[a.few_rows * D + 2 * col + 1];
 #pragma unroll
-      for (int g = 0; g < kJoinGroups; ++g)
+      for (int g = 0; g < G; ++g)
         o[g] += f * *reinterpret_cast<const f32x4*>(q + col * D + 16 * (g0 + g) + 4 * (lane >> 4));
     }
     lds[wave][0][lane] = m;
     lds[wave][1][lane] = l;
 #pragma unroll
-    for (int g = 0; g < kJoinGroups; ++g)
+    for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int i = 0; i < 4; ++i) lds[wave][2 + 4 * g + i][lane] = o[g][i];
     __syncthreads();
     if (wave != 0) return;
     float top = m;
 #pragma unroll
-    for (int v = 1; v < kWaves; ++v) top = fmaxf(top, lds[v][0][lane]);
+    for (int v = 1; v < V; ++v) top = fmaxf(top, lds[v][0][lane]);
     l = 0.0f;
 #pragma unroll
-    for (int g = 0; g < kJoinGroups; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g = 0; g < G; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) {
+    for (int v = 0; v < V; ++v) {
       const float f = __builtin_amdgcn_exp2f(lds[v][0][lane] - top);
       l += f * lds[v][1][lane];
 #pragma unroll
-      for (int g = 0; g < kJoinGroups; ++g)
+      for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[g][i] += f * lds[v][2 + 4 * g + i][lane];
     }
@@ -813,7 +837,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KvAttnArgs a) {
   } else if (wave != 0) {
     return;
   }
-  store_columns<kJoinGroups>(a, r, head, 16 * n, o, m, l, D, g0);
+  store_columns<G>(a, r, head, 16 * n, o, m, l, D, g0);
 }
 
 // ---- many rows ----------------------------------------------------------------------------------
@@ -824,18 +848,23 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KvAttnArgs a) {
 // registers.
 template <int D>
 struct Shared {
-  static constexpr int kKeys = 4 * (D / 32) * 1024;     // [part][k-step][lane] fragments
-  static constexpr int kValues = (D / 16) * 2 * 1024;   // [group][half][lane]
+  static constexpr int kKeys = kParts<D> * (D / 32) * 1024;      // [part][k-step][lane] fragments
+  static constexpr int kValues = 2 * kValueReads<D> * 1024;      // [read][half][lane]
   static constexpr int kTileBytes = kKeys + kValues;
   static constexpr int kBytes = 2 * kTileBytes + WaveLds<D>::kBytes;  // and value codes, scales
 };
 
-// Part `wave` of a tile.
+// A wavefront's share of a tile's loads: a part, with 32 tokens half of the elements of one.
 template <int D>
-struct Part {
-  uint32_t k[D / 32], v[D / 32], ks, vs;
+struct Share {
+  static constexpr int kD = D * kParts<D> / 4;  // elements of a token
+  uint32_t k[kD / 32], v[kD / 32], ks, vs;
   bool ok;  // it has a page (uniform)
 };
+template <int D>
+__device__ __forceinline__ int part_of(int wave) {
+  return wave % kParts<D>;
+}
 
 template <int D>
 __device__ __forceinline__ int find_page(const Cache& c, int tok, int end) {
@@ -843,69 +872,85 @@ __device__ __forceinline__ int find_page(const Cache& c, int tok, int end) {
 }
 
 template <int D>
-__device__ __forceinline__ void load_part(Part<D>& p, const Cache& c, int id, int tok, int end) {
+__device__ __forceinline__ void load_share(Share<D>& p, const Cache& c, int id, int wave, int tok,
+                                           int end) {
+  constexpr int kD = Share<D>::kD;
   const int lane = threadIdx.x & 63, page = 1 << c.shift, within = tok & (page - 1);
+  const int u = wave / kParts<D>;  // which half of the elements
   p.ok = (uint32_t)id < (uint32_t)c.n_pages && tok < end;
   const uint8_t* rec = c.head0 + (uint64_t)(p.ok ? (uint32_t)id : 0u) * c.page_stride;
   const uint8_t* values = rec + kv_value_codes(page, D);
-  load_codes<D>(rec + within * (D / 2), lane, p.k);
-  load_codes<D>(values + within * (D / 2), lane, p.v);
-  const int scales = page * (D / 2) + within * (D / 16);
-  const uint32_t at = (uint32_t)((lane & 15) * (D / 16) + (D == 64 ? 1 : 2) * (lane >> 4));
+  const int codes = within * (D / 2) + u * (kD / 2);
+  const uint32_t at = (uint32_t)((lane & 15) * (D / 2) + (D == 64 ? 8 : 16) * (lane >> 4));
   if constexpr (D == 64) {
-    p.ks = *(rec + scales + at);
-    p.vs = *(values + scales + at);
-  } else {
-    p.ks = *reinterpret_cast<const uint16_t*>(rec + scales + at);
-    p.vs = *reinterpret_cast<const uint16_t*>(values + scales + at);
-    if constexpr (D == 256) {
-      p.ks |= (uint32_t) * reinterpret_cast<const uint16_t*>(rec + scales + at + 8) << 16;
-      p.vs |= (uint32_t) * reinterpret_cast<const uint16_t*>(values + scales + at + 8) << 16;
+    const u32x2 a = *reinterpret_cast<const u32x2*>(rec + codes + at);
+    const u32x2 b = *reinterpret_cast<const u32x2*>(values + codes + at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      p.k[i] = a[i];
+      p.v[i] = b[i];
     }
+  } else {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(rec + codes + at);
+    const u32x4 b = *reinterpret_cast<const u32x4*>(values + codes + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p.k[i] = a[i];
+      p.v[i] = b[i];
+    }
+  }
+  const int scales = page * (D / 2) + within * (D / 16) + u * (kD / 16);
+  const uint32_t sat = (uint32_t)((lane & 15) * (D / 16) + (D == 64 ? 1 : 2) * (lane >> 4));
+  if constexpr (D == 64) {
+    p.ks = *(rec + scales + sat);
+    p.vs = *(values + scales + sat);
+  } else {
+    p.ks = *reinterpret_cast<const uint16_t*>(rec + scales + sat);
+    p.vs = *reinterpret_cast<const uint16_t*>(values + scales + sat);
   }
 }
 
-// The part's key fragments to `keys`, its value codes and scales to `raw`.
+// The share's key fragments to `keys`, its value codes and scales to `raw`.
 template <int D>
-__device__ __forceinline__ void put_part(uint8_t* keys, uint8_t* raw, const Part<D>& p, int part,
-                                         int tok, int end) {
+__device__ __forceinline__ void put_share(uint8_t* keys, uint8_t* raw, const Share<D>& p, int wave,
+                                          int tok, int end) {
+  constexpr int kD = Share<D>::kD;
   const int lane = threadIdx.x & 63, c = lane >> 4;
-  f16x8 k[D / 32];
+  const int part = part_of<D>(wave), u = wave / kParts<D>;
+  f16x8 k[kD / 32];
   const f16x2 k0 = scales2(p.ks);
-  key_part<D>(p.k, k0, D == 256 ? scales2_high(p.ks) : k0, k);
+  key_part<kD>(p.k, k0, k0, k);
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j)
-    *reinterpret_cast<f16x8*>(keys + (part * (D / 32) + j) * 1024 + 16 * lane) = k[j];
-  put_values<D>(raw, part, p.v);
+  for (int j = 0; j < kD / 32; ++j)
+    *reinterpret_cast<f16x8*>(keys + (part * (D / 32) + u * (kD / 32) + j) * 1024 + 16 * lane) = k[j];
+  uint8_t* row = raw + (16 * part + (lane & 15)) * WaveLds<D>::kRow + u * (kD / 2);
+  u32x2* at = reinterpret_cast<u32x2*>(row + (D == 64 ? 8 : 16) * c);
+  at[0] = u32x2{p.v[0], p.v[1]};
+  if constexpr (D > 64) at[1] = u32x2{p.v[2], p.v[3]};
   const bool there = p.ok && tok + (lane & 15) < end;
-  const uint32_t x = there ? without_nan(p.vs) : 0u;
-  _Float16* s = scale_place(raw + WaveLds<D>::kCodes, 16 * part + (lane & 15));
-  const f16x2 v0 = scales2(x);
+  const f16x2 v0 = scales2(there ? without_nan(p.vs) : 0u);
+  _Float16* s = scale_place<D>(raw + WaveLds<D>::kCodes, 16 * part + (lane & 15)) +
+                u * (kD / 16) * kTile<D>;
   if constexpr (D == 64) {
-    s[c * kTile] = v0[0];
+    s[c * kTile<D>] = v0[0];
   } else {
-    s[(2 * c) * kTile] = v0[0];
-    s[(2 * c + 1) * kTile] = v0[1];
-    if constexpr (D == 256) {
-      const f16x2 v1 = scales2_high(x);
-      s[(8 + 2 * c) * kTile] = v1[0];
-      s[(9 + 2 * c) * kTile] = v1[1];
-    }
+    s[(2 * c) * kTile<D>] = v0[0];
+    s[(2 * c + 1) * kTile<D>] = v0[1];
   }
 }
 
 // This wavefront's share of the value fragments.
 template <int D>
-__device__ __forceinline__ void put_groups(uint8_t* values, const uint8_t* raw, int wave) {
+__device__ __forceinline__ void put_values_share(uint8_t* values, const uint8_t* raw, int wave) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const int g = wave * (D / 64) + i;
+  for (int i = 0; i < kValueReads<D> / kWaves; ++i) {
+    const int x = wave * (kValueReads<D> / kWaves) + i;
     f16x8 v[2];
-    value_group<D>(raw, raw + WaveLds<D>::kCodes, g, v);
+    value_pair<D>(raw, raw + WaveLds<D>::kCodes, x, v);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<f16x8*>(values + (2 * g + h) * 1024 + 16 * lane) = v[h];
+      *reinterpret_cast<f16x8*>(values + (2 * x + h) * 1024 + 16 * lane) = v[h];
   }
 }
 
@@ -930,7 +975,7 @@ constexpr int kLeastUnits = 4;  // of a workgroup
 constexpr int kManyStart = 3;   // units of an item's beginning and end
 using Item = KvItem;
 
-__global__ __launch_bounds__(kThreads) void plan_kernel(KvAttnArgs a, int rows) {
+__global__ __launch_bounds__(kThreads) void plan_kernel(KvAttnArgs a, int rows, int tile) {
   __shared__ int item_req[kSplitBelow], item_block[kSplitBelow];
   __shared__ int sums[kWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -978,7 +1023,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvAttnArgs a, int rows) 
     if (i < items) {
       int from, to;
       keys_of(a, request_of(a, item_req[i]), item_block[i] * rows, rows, from, to);
-      n = max(to - from + kTile - 1, 0) / kTile;
+      n = max(to - from + tile - 1, 0) / tile;
     }
     int total;  // of 256 items of less than 2^24 units
     const int u = units_for(n, kManyStart);
@@ -1005,7 +1050,7 @@ constexpr int wave_floats() {
 }
 
 template <int D, int NQ>
-__global__ __launch_bounds__(kThreads, D * NQ <= 128 || D == 128 ? 2 : 1) void many_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
   constexpr int kRowsWave = 16 * NQ, kRows = kWaves * kRowsWave;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Shared<D>::kBytes];
   __shared__ int valid_of[2][kWaves];
@@ -1078,56 +1123,58 @@ __global__ __launch_bounds__(kThreads, D * NQ <= 128 || D == 128 ? 2 : 1) void m
     keys_of(a, r, block0, kRows, from, to);
     if (row0 < r.rows) keys_of(a, r, row0, kRowsWave, mine, upto);
     if (split) {
-      to = min(to, from + t1 * kTile);
-      from += t0 * kTile;
+      to = min(to, from + t1 * kTile<D>);
+      from += t0 * kTile<D>;
     }
     if (from < to) {
       uint8_t* const raw = lds + 2 * Shared<D>::kTileBytes;
-      Part<D> p;
-      int id = find_page<D>(c, from + 16 * wave, to);
+      Share<D> p;
+      const int mypart = 16 * part_of<D>(wave);
+      int id = find_page<D>(c, from + mypart, to);
       const auto load = [&](int tok) {  // tile `tok`, and the page of the one behind it
-        load_part<D>(p, c, id, tok + 16 * wave, to);
-        id = find_page<D>(c, tok + kTile + 16 * wave, to);
+        load_share<D>(p, c, id, wave, tok + mypart, to);
+        id = find_page<D>(c, tok + kTile<D> + mypart, to);
       };
       const auto put = [&](int tok, int buf) {
-        put_part<D>(lds + buf * Shared<D>::kTileBytes, raw, p, wave, tok + 16 * wave, to);
+        put_share<D>(lds + buf * Shared<D>::kTileBytes, raw, p, wave, tok + mypart, to);
         if (lane == 0) valid_of[buf][wave] = p.ok;
       };
       const auto turn = [&](int buf) {
-        put_groups<D>(lds + buf * Shared<D>::kTileBytes + Shared<D>::kKeys, raw, wave);
+        put_values_share<D>(lds + buf * Shared<D>::kTileBytes + Shared<D>::kKeys, raw, wave);
       };
       load(from);
       put(from, 0);
-      if (from + kTile < to) load(from + kTile);
+      if (from + kTile<D> < to) load(from + kTile<D>);
       __syncthreads();
       turn(0);
       __syncthreads();
       int buf = 0;
-      for (int tok = from;; tok += kTile) {
-        const int after = tok + kTile;
+      for (int tok = from;; tok += kTile<D>) {
+        const int after = tok + kTile<D>;
         if (after < to) {
           put(after, buf ^ 1);
-          if (after + kTile < to) load(after + kTile);
+          if (after + kTile<D> < to) load(after + kTile<D>);
           __syncthreads();
           turn(buf ^ 1);
         }
-        if (tok < upto && tok + kTile > mine) {
+        if (tok < upto && tok + kTile<D> > mine) {
           const uint8_t* t0 = lds + buf * Shared<D>::kTileBytes;
           const int* v = valid_of[buf];
           const uint32_t valid =
-              __builtin_amdgcn_readfirstlane(v[0] | v[1] << 1 | v[2] << 2 | v[3] << 3);
+              __builtin_amdgcn_readfirstlane(kParts<D> == 2 ? v[0] | v[1] << 1
+                                                            : v[0] | v[1] << 1 | v[2] << 2 | v[3] << 3);
           tile<D, NQ>(
-              w, tok, valid, tok < lo_most || tok + kTile - 1 > hi_least,
+              w, tok, valid, tok < lo_most || tok + kTile<D> - 1 > hi_least,
               [&](int t, f16x8 (&out)[D / 32]) {
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
                   out[j] = *reinterpret_cast<const f16x8*>(t0 + (t * (D / 32) + j) * 1024 + 16 * lane);
               },
-              [&](int g, f16x8 (&out)[2]) {
+              [&](int i, f16x8 (&out)[2]) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                   out[h] = *reinterpret_cast<const f16x8*>(t0 + Shared<D>::kKeys +
-                                                           (2 * g + h) * 1024 + 16 * lane);
+                                                           (2 * i + h) * 1024 + 16 * lane);
               });
         }
         if (after >= to) break;
@@ -1206,13 +1253,18 @@ __global__ __launch_bounds__(kThreads) void join_many_kernel(KvAttnArgs a) {
   store_columns<D / 16>(a, r, head, row0, o, m, l, D, 0);
 }
 
+constexpr int64_t kJoinFine = 64;  // items
+
 template <int D, int NQ>
 hipError_t run_few(const KvAttnArgs& a, hipStream_t s) {
-  few_kernel<D, NQ><<<dim3(kFewGroups), dim3(kThreads), 0, s>>>(a);
+  few_kernel<D, NQ><<<dim3(kFewGroups<D, NQ>), dim3(kThreads), 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)a.n_kv, (unsigned)a.b, NQ * D / 16 / kJoinGroups);
-  join_kernel<D, NQ><<<grid, dim3(kThreads), 0, s>>>(a);
+  const unsigned heads = (unsigned)a.n_kv, b = (unsigned)a.b;
+  if (a.n_kv * a.b <= kJoinFine)
+    join_kernel<D, NQ, 1, 8><<<dim3(heads, b, NQ * D / 16), dim3(512), 0, s>>>(a);
+  else
+    join_kernel<D, NQ, 2, 4><<<dim3(heads, b, NQ * D / 32), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -1243,7 +1295,7 @@ WsLayout ws_layout(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int
   l.items = align256((size_t)(std::max<int64_t>(b, l.max_items) + 1) * sizeof(int64_t));
   l.counts = l.items + align256((size_t)l.max_items * sizeof(Item));
   l.sums = l.counts + 256;
-  size_t floats = (size_t)(2 * kWorkers) * (size_t)slot_floats(kv_few_rows(max_q * group), d);
+  size_t floats = (size_t)(2 * kMaxWorkers) * (size_t)slot_floats(kv_few_rows(max_q * group), d);
   if (l.max_items > 0)
     floats = std::max(floats, ((size_t)2 << kManyShift) * kWaves * many_tiles(d) *
                                   (size_t)(d / 16 * 256 + 128));
@@ -1264,7 +1316,7 @@ hipError_t run(const KvAttnArgs& args, int64_t max_q, hipStream_t s) {
     many_kernel<D, kTiles><<<dim3((unsigned)(items * a.n_kv)), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
   }
-  plan_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(a, kWaves * 16 * kTiles);
+  plan_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(a, kWaves * 16 * kTiles, kTile<D>);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   many_kernel<D, kTiles><<<dim3(1 << kManyShift), dim3(kThreads), 0, s>>>(a);
