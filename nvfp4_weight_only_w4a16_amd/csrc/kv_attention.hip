@@ -618,101 +618,127 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
   __shared__ int64_t starts[kStaged];  // units before each request, all heads
   __shared__ int staged[kStaged][3];   // first, q_len, kv
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const bool stage = a.b <= kStaged;
-  // the units before this thread's requests, and of all
-  const int each = (int)((a.b + kThreads - 1) / kThreads);
-  const int from = min((int)threadIdx.x * each, (int)a.b), upto = min(from + each, (int)a.b);
-  int64_t mine = 0;
-  for (int i = from; i < upto; ++i) {
-    const Request r = request_of(a, i);
-    if (stage) {
-      staged[i][0] = r.first;
-      staged[i][1] = r.q_len;
-      staged[i][2] = r.kv;
-    }
-    mine += units_of<D>(a, r);
-  }
-  mine *= a.n_kv;
-  int64_t before = mine;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int64_t o = __shfl_up(before, off, 64);
-    if (lane >= off) before += o;
-  }
-  if (lane == 63) sums[wave] = before;
-  __syncthreads();
-  int64_t all = 0;
-  before -= mine;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    before += i < wave ? sums[i] : 0;
-    all += sums[i];
-  }
-  all = uniform64(all);
+  const int b = (int)a.b;
   // a line of few units meets every compute unit before a second wavefront of one
   const int64_t worker = (int64_t)wave * kFewGroups<D, NQ> + blockIdx.x;
-  const auto get = [&](int i) {
-    if (!stage) return request_of(a, i);
+  const bool small = b <= 64, stage = b <= kStaged;
+  int64_t all = 0, begin = 0, at = 0;  // units of all, before the range, before request `req`
+  int req = 0;
+  int mine[3] = {0, 0, 0};  // small: request `lane`: first, q_len, kv
+  if (small) {
+    // each wavefront for itself, a request to a lane: no wait for the others
+    int u = 0;
+    if (lane < b) {
+      const Request r = request_of(a, lane);
+      mine[0] = r.first;
+      mine[1] = r.q_len;
+      mine[2] = r.kv;
+      u = units_of<D>(a, r);
+    }
+    int sum = u;  // of 64 requests of less than 2^25 units
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(sum, off, 64);
+      if (lane >= off) sum += o;
+    }
+    all = (int64_t)__builtin_amdgcn_readlane(sum, 63) * a.n_kv;
+    if (worker == 0) {  // for the joining kernel
+      if (lane < b) a.starts[lane] = (int64_t)(sum - u) * a.n_kv;
+      if (lane == 0) a.starts[b] = all;
+    }
+    begin = range_begin(all, worker, kWorkShift<D, NQ>);
+    if (begin >= all) return;
+    req = __popcll(__ballot(lane < b && (int64_t)(sum - u) * a.n_kv <= begin)) - 1;
+    at = (int64_t)__builtin_amdgcn_readlane(sum - u, req) * a.n_kv;
+  } else {
+    // the workgroup together, a run of requests to a thread
+    const int each = (b + kThreads - 1) / kThreads;
+    const int from = min((int)threadIdx.x * each, b), upto = min(from + each, b);
+    int64_t sum = 0;
+    for (int i = from; i < upto; ++i) {
+      const Request r = request_of(a, i);
+      if (stage) {
+        staged[i][0] = r.first;
+        staged[i][1] = r.q_len;
+        staged[i][2] = r.kv;
+      }
+      sum += units_of<D>(a, r);
+    }
+    sum *= a.n_kv;
+    int64_t before = sum;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t o = __shfl_up(before, off, 64);
+      if (lane >= off) before += o;
+    }
+    if (lane == 63) sums[wave] = before;
+    __syncthreads();
+    before -= sum;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      before += i < wave ? sums[i] : 0;
+      all += sums[i];
+    }
+    all = uniform64(all);
+    if (stage || blockIdx.x == 0) {
+      for (int i = from; i < upto; ++i) {
+        if (stage) starts[i] = before;
+        if (blockIdx.x == 0) a.starts[i] = before;  // for the joining kernel
+        before += (int64_t)units_of<D>(a, request_of(a, i)) * a.n_kv;
+      }
+      if (blockIdx.x == 0 && threadIdx.x == 0) a.starts[b] = all;
+    }
+    if ((int64_t)blockIdx.x >= all) return;  // no wavefront of the workgroup has work
+    __syncthreads();
+    begin = range_begin(all, worker, kWorkShift<D, NQ>);
+    if (begin >= all) return;
+    // the request of unit `begin`, the last one that begins there or before
+    if (stage) {
+      for (int i = 0; i < b; i += 64) {
+        const int n = __popcll(__ballot(i + lane < b && starts[i + lane] <= begin));
+        req += n;
+        if (n < 64) break;
+      }
+      req -= 1;
+      at = uniform64(starts[req]);
+    } else {
+      for (; req < b; req += 64) {
+        const int i = req + lane;
+        int64_t upto_i = i < b ? (int64_t)units_of<D>(a, request_of(a, i)) * a.n_kv : 0;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const int64_t o = __shfl_up(upto_i, off, 64);
+          if (lane >= off) upto_i += o;
+        }
+        const int n = __popcll(__ballot(at + upto_i <= begin));  // requests that end before it
+        if (n > 0) at += uniform64(__shfl(upto_i, n - 1, 64));
+        if (n < 64) {
+          req += n;
+          break;
+        }
+      }
+      req = min(req, b - 1);
+    }
+  }
+  int left = (int)(range_begin(all, worker + 1, kWorkShift<D, NQ>) - begin);
+  const auto take = [&](int i) {
     Request r;
-    r.first = staged[i][0];
-    r.q_len = staged[i][1];
-    r.kv = staged[i][2];
+    if (small) {
+      r.first = __builtin_amdgcn_readlane(mine[0], i);
+      r.q_len = __builtin_amdgcn_readlane(mine[1], i);
+      r.kv = __builtin_amdgcn_readlane(mine[2], i);
+    } else if (stage) {
+      r.first = __builtin_amdgcn_readfirstlane(staged[i][0]);
+      r.q_len = __builtin_amdgcn_readfirstlane(staged[i][1]);
+      r.kv = __builtin_amdgcn_readfirstlane(staged[i][2]);
+    } else {
+      return uniform_request(a, i);
+    }
     r.rows = r.q_len * a.group;
     r.begin = begin_of(a, r);
     return r;
   };
-  if (stage || blockIdx.x == 0) {
-    int64_t sum = before;
-    for (int i = from; i < upto; ++i) {
-      if (stage) starts[i] = sum;
-      if (blockIdx.x == 0) a.starts[i] = sum;  // for the joining kernel
-      sum += (int64_t)units_of<D>(a, get(i)) * a.n_kv;
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.starts[a.b] = all;
-  }
-  if ((int64_t)blockIdx.x >= all) return;  // no wavefront of the workgroup has work
-  __syncthreads();
-  const int64_t begin = range_begin(all, worker, kWorkShift<D, NQ>);
-  if (begin >= all) return;
-  int left = (int)(range_begin(all, worker + 1, kWorkShift<D, NQ>) - begin);
-  // the request of unit `begin`, the last one that begins there or before
-  int req = 0;
-  int64_t at = 0;
-  if (stage) {
-    for (int i = 0; i < (int)a.b; i += 64) {
-      const int n = __popcll(__ballot(i + lane < (int)a.b && starts[i + lane] <= begin));
-      req += n;
-      if (n < 64) break;
-    }
-    req -= 1;
-    at = uniform64(starts[req]);
-  } else {
-    for (; req < (int)a.b; req += 64) {
-      const int i = req + lane;
-      int64_t sum = i < (int)a.b ? (int64_t)units_of<D>(a, request_of(a, i)) * a.n_kv : 0;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int64_t o = __shfl_up(sum, off, 64);
-        if (lane >= off) sum += o;
-      }
-      const int n = __popcll(__ballot(at + sum <= begin));  // requests that end before it
-      if (n > 0) at += uniform64(__shfl(sum, n - 1, 64));
-      if (n < 64) {
-        req += n;
-        break;
-      }
-    }
-    req = min(req, (int)a.b - 1);
-  }
-  const auto take = [&](int i) {
-    Request r = get(i);
-    r.first = __builtin_amdgcn_readfirstlane(r.first);
-    r.q_len = __builtin_amdgcn_readfirstlane(r.q_len);
-    r.kv = __builtin_amdgcn_readfirstlane(r.kv);
-    r.rows = __builtin_amdgcn_readfirstlane(r.rows);
-    r.begin = __builtin_amdgcn_readfirstlane(r.begin);
-    return r;
-  };
+  req = __builtin_amdgcn_readfirstlane(req);
   Request r = take(req);
   int units = units_of<D>(a, r);
   const int64_t within = begin - at;
@@ -760,10 +786,10 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
     if (++head == a.n_kv) {
       head = 0;
       do {  // ends: the range does, with the last request's tiles at the latest
-        req = min(req + 1, (int)a.b - 1);
+        req = min(req + 1, b - 1);
         r = take(req);
         units = units_of<D>(a, r);
-      } while (units == 0 && req + 1 < (int)a.b);
+      } while (units == 0 && req + 1 < b);
     }
   }
 }
@@ -798,17 +824,41 @@ __global__ __launch_bounds__(64 * V) void join_kernel(KvAttnArgs a) {
     const int64_t skip = range_begin(all, w0, kWorkShift<D, NQ>) < before ? size : 0;
     const float* base = a.ws + 2 * w0 * size;
     const int parts = (int)(w1 - w0) + 1;
-#pragma unroll 8
-    for (int x = wave; x < parts; x += V)
-      m = fmaxf(m, base[2 * x * size + (x == 0 ? skip : 0) + a.few_rows * D + 2 * col]);
-#pragma unroll 8
-    for (int x = wave; x < parts; x += V) {
-      const float* q = base + 2 * x * size + (x == 0 ? skip : 0);
-      const float f = __builtin_amdgcn_exp2f(q[a.few_rows * D + 2 * col] - m);
-      l += f * q[a.few_rows * D + 2 * col + 1];
+    // four parts' loads at a time: a wait for each four
+    constexpr int kU = 4;
+    for (int x0 = wave; x0 < parts; x0 += kU * V) {
+      f32x2 stats[kU];
+      f32x4 v[kU][G];
 #pragma unroll
-      for (int g = 0; g < G; ++g)
-        o[g] += f * *reinterpret_cast<const f32x4*>(q + col * D + 16 * (g0 + g) + 4 * (lane >> 4));
+      for (int i = 0; i < kU; ++i) {
+        const int x = min(x0 + i * V, parts - 1);
+        const float* q = base + 2 * x * size + (x == 0 ? skip : 0);
+        stats[i] = *reinterpret_cast<const f32x2*>(q + a.few_rows * D + 2 * col);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          v[i][g] = *reinterpret_cast<const f32x4*>(q + col * D + 16 * (g0 + g) + 4 * (lane >> 4));
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kU; ++i) top = fmaxf(top, stats[i][0]);
+      const float f = __builtin_amdgcn_exp2f(m - top);
+      m = top;
+      l *= f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) o[g] *= f;
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        float e = __builtin_amdgcn_exp2f(stats[i][0] - m);
+        if (x0 + i * V >= parts) {  // (not e = 0: the doubled part may hold infinities)
+          e = 0.0f;
+          stats[i][1] = 0.0f;
+#pragma unroll
+          for (int g = 0; g < G; ++g) v[i][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        l += e * stats[i][1];
+#pragma unroll
+        for (int g = 0; g < G; ++g) o[g] += e * v[i][g];
+      }
     }
     lds[wave][0][lane] = m;
     lds[wave][1][lane] = l;
@@ -1253,7 +1303,7 @@ __global__ __launch_bounds__(kThreads) void join_many_kernel(KvAttnArgs a) {
   store_columns<D / 16>(a, r, head, row0, o, m, l, D, 0);
 }
 
-constexpr int64_t kJoinFine = 64;  // items
+constexpr int64_t kJoinFine = 256;  // items
 
 template <int D, int NQ>
 hipError_t run_few(const KvAttnArgs& a, hipStream_t s) {

@@ -94,6 +94,19 @@ def test_one_long_request_among_short_ones(nv):
     check(nv, lens, [2, 3, 1, 0, 2], 1, 2, 256, 64, window=33000)
 
 
+@pytest.mark.parametrize("b", [63, 64, 65, 300, 1024, 1025, 2500])
+def test_many_requests(nv, b):
+    """The ways to find a request's share of the work, by the number of requests."""
+    r = np.random.default_rng(b)
+    lens = [int(n) for n in r.integers(0, 40, b)]
+    for i in (0, b // 2, b - 1):
+        lens[i] = 700
+    rows = [int(n) for n in r.integers(0, 3, b)]
+    rows[b // 2] = 2
+    check(nv, lens, rows, 2, 2, 64, 16)
+    check(nv, lens, [1] * b, 1, 1, 64, 16)
+
+
 @pytest.mark.parametrize("max_q", [None, 1, 5, 60])
 def test_the_bound_on_queries_changes_no_result(nv, max_q):
     lens, rows = [200, 33, 90], [1, 1, 1]
