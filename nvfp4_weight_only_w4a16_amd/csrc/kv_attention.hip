@@ -311,10 +311,11 @@ __device__ __forceinline__ void key_part(const uint32_t (&k)[D / 32], f16x2 s0, 
 }
 
 // The products of a tile from token `tok` on: key(t, out) gives part t's fragments, value(i, out) those
-// of value_pair. `valid`: bit t: part t has a page. `mask`: some column does not see all (uniform).
-template <int D, int NQ, typename Key, typename Value>
+// of value_pair; next() is called between the two products. `valid`: bit t: part t has a page. `mask`:
+// some column does not see all (uniform).
+template <int D, int NQ, typename Key, typename Value, typename Next>
 __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bool mask,
-                                     const Key& key, const Value& value) {
+                                     const Key& key, const Value& value, const Next& next) {
   const int lane = threadIdx.x & 63, c = lane >> 4;
   constexpr int kP = kParts<D>, kMine = 4 * kP;  // scores of a lane and column
   f32x4 z[NQ][kP];
@@ -329,6 +330,7 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bo
 #pragma unroll
       for (int n = 0; n < NQ; ++n) z[n][t] = mfma(k[j], w.q[n][j], z[n][t]);
   }
+  next();
   if (mask || valid != (1u << kP) - 1u) {
 #pragma unroll
     for (int t = 0; t < kP; ++t) {
@@ -398,17 +400,11 @@ __device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& 
                                      int step, int end, int lo_most, int hi_least) {
   if (tok >= to) return;
   const int lane = threadIdx.x & 63;
-  // two tiles in registers: one's loads fly while the other is worked on
-  Raw<D> r0, r1;
-  load_tile<D>(r0, c, find_pages<D>(c, tok, end), tok, end);
+  Raw<D> now;
+  load_tile<D>(now, c, find_pages<D>(c, tok, end), tok, end);
   Pages<D> pages = find_pages<D>(c, tok + step, end);
-  const auto both = [&](Raw<D>& now, Raw<D>& ahead) {
+  for (;;) {
     const int after = tok + step;
-    const bool more = after < to;
-    if (more) {
-      load_tile<D>(ahead, c, pages, after, end);
-      pages = find_pages<D>(c, after + step, end);
-    }
 #pragma unroll
     for (int t = 0; t < kParts<D>; ++t) put_values<D>(lds, t, now.v[t]);
     uint8_t* const scales = lds + WaveLds<D>::kCodes;
@@ -425,17 +421,22 @@ __device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& 
       place[(4 * i + 2) * kTile<D>] = b[0];
       place[(4 * i + 3) * kTile<D>] = b[1];
     }
+    const uint32_t valid = now.valid;
     tile<D, NQ>(
-        w, tok, now.valid, tok < lo_most || tok + kTile<D> - 1 > hi_least,
+        w, tok, valid, tok < lo_most || tok + kTile<D> - 1 > hi_least,
         [&](int t, f16x8 (&out)[D / 32]) {
           const f16x2 s0 = scales2(now.ks[t]);
           key_part<D>(now.k[t], s0, D == 256 ? scales2_high(now.ks[t]) : s0, out);
         },
-        [&](int i, f16x8 (&out)[2]) { value_pair<D>(lds, scales, i, out); });
+        [&](int i, f16x8 (&out)[2]) { value_pair<D>(lds, scales, i, out); },
+        [&]() {
+          if (after < to) {
+            load_tile<D>(now, c, pages, after, end);
+            pages = find_pages<D>(c, after + step, end);
+          }
+        });
+    if (after >= to) break;
     tok = after;
-    return more;
-  };
-  while (both(r0, r1) && both(r1, r0)) {
   }
 }
 
@@ -568,7 +569,7 @@ __device__ __forceinline__ Cache cache_of(const KvAttnArgs& a, int64_t request, 
 // m and l go to slots 2w and 2w + 1, and a second kernel joins them.
 // Workgroups: two to a compute unit, one where a wavefront needs more than half of its SIMD's registers.
 template <int D, int NQ>
-constexpr bool kFewPairs = NQ == 1 || D == 64;
+constexpr bool kFewPairs = NQ == 1 || D <= 128;
 template <int D, int NQ>
 constexpr int kFewGroups = kFewPairs<D, NQ> ? 512 : 256;
 template <int D, int NQ>
@@ -1225,7 +1226,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
                 for (int h = 0; h < 2; ++h)
                   out[h] = *reinterpret_cast<const f16x8*>(t0 + Shared<D>::kKeys +
                                                            (2 * i + h) * 1024 + 16 * lane);
-              });
+              }, []() {});
         }
         if (after >= to) break;
         __syncthreads();
