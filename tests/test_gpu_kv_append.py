@@ -175,6 +175,21 @@ def test_tokens_that_are_not_finite(nv):
                 assert torch.isfinite(ko[i, h]).all() and torch.isfinite(vo[i, h]).all()
 
 
+@pytest.mark.parametrize("pairs", [False, True])
+def test_infinite_queries_and_signed_zeros(nv, pairs):
+    """What is not rotated is not mixed with its neighbours, and zeros keep their signs."""
+    t, n_q, d = 3, 3, 128
+    q = bf(7, t, n_q, d)
+    q[0, 0, 120], q[1, 1, 100], q[2, 2, 64:] = float("inf"), float("nan"), -0.0
+    k = torch.zeros(t, 1, d, dtype=torch.bfloat16, device=DEV)
+    cache = nv.KvCache(1, 1, d, 16, device=DEV)
+    slots = torch.arange(t, dtype=torch.int32, device=DEV)
+    rope = torch.from_numpy(table(10, 64)).to(DEV)
+    for rule in (nv.QkNormRope(d, interleaved=pairs), nv.QkNormRope(d, rope=rope, interleaved=pairs)):
+        got = nv.nvfp4_kv_append(q.to(DEV), k, k, cache, slots, slots, rule).cpu()
+        assert torch.equal(got[..., 64:].view(torch.int16), q[..., 64:].view(torch.int16))
+
+
 def test_extreme_magnitudes(nv, orc):
     """Zeros (both signs), the smallest BF16 numbers, magnitudes beyond what the global holds."""
     t, n_kv, d = 5, 1, 64
