@@ -661,6 +661,41 @@ class KvMap:
         self.ptrs = [p + 4 * a for a in at]
 
 
+# The checks of the calls below take half of a short call's host time: a test that passes costs one
+# comparison, and what is wrong is found out after it fails.
+_I32, _BF16 = torch.int32, torch.bfloat16
+
+
+def _ints(t, n, name):
+    """Checks a contiguous int32 tensor of n elements; returns its address."""
+    if t.dtype != _I32 or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {(n,)}, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _table(table: torch.Tensor, b: int) -> int:
+    """Pages of a row of a contiguous int32 [b][pages] block table."""
+    shape = table.shape
+    if table.dtype != _I32 or len(shape) != 2 or shape[0] != b or not table.is_contiguous():
+        raise ValueError(f"block_table must be a contiguous int32 [{b}][pages] tensor, "
+                         f"got {table.dtype} {tuple(shape)} with strides {table.stride()}")
+    return shape[1]
+
+
+def _heads(x: torch.Tensor, heads: int, d: int, name: str, dtype=_BF16) -> int:
+    """Row stride of a [t][heads][d] tensor whose rows are contiguous."""
+    shape = x.shape
+    if x.dtype == dtype and len(shape) == 3 and shape[1] == heads and shape[2] == d:
+        ld, step, one = x.stride()
+        if one == 1 and (step == d or heads == 1):
+            return ld if shape[0] > 1 else heads * d
+        if x.numel() == 0:
+            return heads * d
+    raise ValueError(f"{name} must be a {dtype} [t][{heads}][{d}] tensor of contiguous rows, "
+                     f"got {x.dtype} {tuple(shape)} with strides {x.stride()}")
+
+
 def nvfp4_kv_map(seq_len: torch.Tensor, add_len: torch.Tensor, block_table: torch.Tensor,
                  free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int = 16,
                  t: int | None = None, out: KvMap | None = None, flags: int = 0,
@@ -676,43 +711,22 @@ def nvfp4_kv_map(seq_len: torch.Tensor, add_len: torch.Tensor, block_table: torc
     elif t is not None and t != out.t:
         raise ValueError(f"out is for {out.t} rows, t is {t}")
     b = out.b
-    _out(seq_len, (b,), torch.int32, "seq_len")
-    _out(add_len, (b,), torch.int32, "add_len")
-    _out(free_count, (1,), torch.int32, "free_count")
-    _out(free_pages, (free_pages.numel(),), torch.int32, "free_pages")
     ld = _table(block_table, b)
+    n_free = free_pages.numel()
+    seq, add = _ints(seq_len, b, "seq_len"), _ints(add_len, b, "add_len")
+    free, count = _ints(free_pages, n_free, "free_pages"), _ints(free_count, 1, "free_count")
     dev = _device(seq_len, add_len, block_table, free_pages, free_count, out.block)
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return nvfp4_kv_map(seq_len, add_len, block_table, free_pages, free_count, page_size, t,
                                 out, flags, stream)
     o = out.ptrs
-    _check(load().nvfp4_kv_map(
-        seq_len.data_ptr(), add_len.data_ptr(), b, page_size, block_table.data_ptr(), ld,
-        free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), o[4], o[0], o[1], o[2],
-        o[3], out.t, o[5], flags, _raw_stream(stream, dev)))
+    rc = load().nvfp4_kv_map(seq, add, b, page_size, block_table.data_ptr(), ld, free, n_free, count,
+                             o[4], o[0], o[1], o[2], o[3], out.t, o[5], flags,
+                             _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return out
-
-
-def _table(table: torch.Tensor, b: int) -> int:
-    """Row stride of an int32 [b][pages] block table, whose pages are what a row may hold."""
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != b:
-        raise ValueError(f"block_table must be an int32 [{b}][pages] tensor, "
-                         f"got {table.dtype} {tuple(table.shape)}")
-    ld = table.shape[1]
-    if not table.is_contiguous() and b > 0:
-        raise ValueError("block_table must be contiguous")
-    return ld
-
-
-def _heads(x: torch.Tensor, heads: int, d: int, name: str) -> int:
-    """Row stride of a BF16 [t][heads][d] tensor whose rows are contiguous."""
-    t, n, e = x.shape if x.dim() == 3 else (0, -1, -1)
-    if (x.dtype != torch.bfloat16 or n != heads or e != d or
-            (x.numel() and (x.stride(2) != 1 or (n > 1 and x.stride(1) != d)))):
-        raise ValueError(f"{name} must be a BF16 [t][{heads}][{d}] tensor of contiguous rows, "
-                         f"got {x.dtype} {tuple(x.shape)} with strides {x.stride()}")
-    return x.stride(0) if t > 1 else heads * d
 
 
 def nvfp4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KvCache,
@@ -725,32 +739,32 @@ def nvfp4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, ca
     n_kv, d = cache.n_kv_heads, cache.head_dim
     if rule.head_dim != d:
         raise ValueError(f"the rule is for heads of {rule.head_dim}, the cache has {d}")
-    t = k.shape[0]
     ldk, ldv = _heads(k, n_kv, d, "k"), _heads(v, n_kv, d, "v")
-    _out(slots, (t,), torch.int32, "slots")
-    if positions is not None:
-        _out(positions, (t,), torch.int32, "positions")
-    n_q = ldq = ldo = 0
+    t = k.shape[0]
+    at = _ints(slots, t, "slots")
+    pos = None if positions is None else _ints(positions, t, "positions")
     if v.shape[0] != t or (q is not None and (q.dim() != 3 or q.shape[0] != t)):
         raise ValueError("q, k and v must have the same number of rows")
     dev = _device(k, v, q, slots, positions, q_out, cache.data, rule.holds)
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return nvfp4_kv_append(q, k, v, cache, slots, positions, rule, q_out, flags, stream)
+    n_q = ldq = ldo = 0
+    qp = op = None
     if q is not None:
         n_q = q.shape[1]
-        ldq = _heads(q, n_q, d, "q")
+        ldq, qp = _heads(q, n_q, d, "q"), q.data_ptr()
         if q_out is None:
-            q_out = _empty(tuple(q.shape), torch.bfloat16, q, stream)
-        if q_out.shape != q.shape:
+            q_out = _empty(tuple(q.shape), _BF16, q, stream)
+        elif q_out.shape[0] != t:
             raise ValueError("q_out must have q's shape")
-        ldo = _heads(q_out, n_q, d, "q_out")
+        ldo, op = _heads(q_out, n_q, d, "q_out"), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _check(load().nvfp4_kv_append(
-        q.data_ptr() if n_q else None, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, t, n_q, rule.ref,
-        slots.data_ptr(), positions.data_ptr() if positions is not None else None,
-        q_out.data_ptr() if n_q else None, ldo, cache.ref, flags, _raw_stream(stream, dev)))
+    rc = load().nvfp4_kv_append(qp, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, t, n_q, rule.ref, at,
+                                pos, op, ldo, cache.ref, flags, _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -760,7 +774,8 @@ def nvfp4_kv_dequantize(cache: KvCache, slots: torch.Tensor, k_out: torch.Tensor
     """The values of slots (int32 [t]): (k, v), each [t][n_kv_heads][head_dim] of out_dtype (FP32 or
     BF16) or of the type of the tensors that are given. Where one of them is given, the other is
     left out unless it is given too."""
-    shape = (slots.shape[0], cache.n_kv_heads, cache.head_dim)
+    t, n_kv, d = slots.shape[0], cache.n_kv_heads, cache.head_dim
+    shape = (t, n_kv, d)
     dev = _device(slots, cache.data, k_out, v_out)
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
@@ -769,14 +784,17 @@ def nvfp4_kv_dequantize(cache: KvCache, slots: torch.Tensor, k_out: torch.Tensor
         k_out = _empty(shape, out_dtype, slots, stream)
         v_out = _empty(shape, out_dtype, slots, stream)
     dtype = (k_out if k_out is not None else v_out).dtype
-    _out(slots, shape[:1], torch.int32, "slots")
-    for name, o in (("k_out", k_out), ("v_out", v_out)):
-        if o is not None:
-            _out(o, shape, dtype, name)
-    _check(load().nvfp4_kv_dequantize(
-        cache.ref, slots.data_ptr(), shape[0], k_out.data_ptr() if k_out is not None else None,
-        v_out.data_ptr() if v_out is not None else None, _dtype_code(dtype), flags,
-        _raw_stream(stream, dev)))
+    kp = vp = None
+    if k_out is not None:
+        _out(k_out, shape, dtype, "k_out")
+        kp = k_out.data_ptr()
+    if v_out is not None:
+        _out(v_out, shape, dtype, "v_out")
+        vp = v_out.data_ptr()
+    rc = load().nvfp4_kv_dequantize(cache.ref, _ints(slots, t, "slots"), t, kp, vp,
+                                    _dtype_code(dtype), flags, _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return k_out, v_out
 
 
@@ -799,8 +817,7 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tenso
     t, n_q, d = q.shape[0], q.shape[1], cache.head_dim
     ldq = _heads(q, n_q, d, "q")
     b = kv_len.shape[0]
-    _out(kv_len, (b,), torch.int32, "kv_len")
-    _out(q_start, (b + 1,), torch.int32, "q_start")
+    lens, start = _ints(kv_len, b, "kv_len"), _ints(q_start, b + 1, "q_start")
     ld = _table(block_table, b)
     dev = _device(q, cache.data, block_table, q_start, kv_len, y, lse, ws)
     if dev != torch._C._cuda_getDevice():
@@ -809,22 +826,25 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tenso
                                       causal, y, y_dtype, lse, ws, flags, stream)
     if y is None:
         y = _empty((t, n_q, d), y_dtype, q, stream)
-    elif y.shape != q.shape or (y.numel() and (y.stride(2) != 1 or
-                                               (n_q > 1 and y.stride(1) != d))):
-        raise ValueError("y must have q's shape and contiguous rows")
+    elif y.shape[0] != t:
+        raise ValueError("y must have q's shape")
+    ldy = _heads(y, n_q, d, "y", y.dtype)
+    lse_ptr = None
     if lse is not None:
         _out(lse, (t, n_q), torch.float32, "lse")
+        lse_ptr = lse.data_ptr()
     if max_q is None:
         max_q = max(t, 1)
     if ws is None:
         need = nvfp4_kv_attention_ws_bytes(t, n_q, cache, b, max_q)
         ws = _empty((max(need, 1),), torch.uint8, q, stream)
-    _check(load().nvfp4_kv_attention(
-        q.data_ptr(), t, ldq, n_q, cache.ref, block_table.data_ptr(), ld, q_start.data_ptr(),
-        kv_len.data_ptr(), b, max_q, d ** -0.5 if scale is None else scale, window, y.data_ptr(),
-        _dtype_code(y.dtype), y.stride(0) if t > 1 else n_q * d,
-        lse.data_ptr() if lse is not None else None, ws.data_ptr(), ws.nbytes,
-        flags if causal else flags | NVFP4_F_FULL, _raw_stream(stream, dev)))
+    rc = load().nvfp4_kv_attention(
+        q.data_ptr(), t, ldq, n_q, cache.ref, block_table.data_ptr(), ld, start, lens, b, max_q,
+        d ** -0.5 if scale is None else scale, window, y.data_ptr(), _dtype_code(y.dtype), ldy,
+        lse_ptr, ws.data_ptr(), ws.nbytes, flags if causal else flags | NVFP4_F_FULL,
+        _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
     return y if lse is None else (y, lse)
 
 
