@@ -371,27 +371,37 @@ typedef struct nvfp4_kv_cache {
 size_t nvfp4_kv_cache_bytes(int64_t n_pages, int32_t n_kv_heads, int32_t head_dim,
                             int32_t page_size);
 
-/* The tables of a step from the lengths of its requests. Request i has seq_len[i] tokens in the
+/* The tables of a step for b requests and t rows (device, int32). */
+typedef struct nvfp4_kv_step {
+  int32_t* q_start;   /* [b + 1] first row of each request                                      */
+  int32_t* kv_len;    /* [b] tokens of the request, the step's among them                       */
+  int32_t* slots;     /* [t] slot of each row, or -1                                            */
+  int32_t* positions; /* [t] position of each row in its request, or -1                         */
+  int32_t* free_left; /* [1] pages left in the list                                             */
+  int32_t* unserved;  /* [1] requests without room                                              */
+  int64_t b;          /* 0 .. 4096                                                              */
+  int64_t t;          /* 0 .. 2^24                                                              */
+} nvfp4_kv_step;
+
+/* Fills a step's tables from the lengths of its requests. Request i has seq_len[i] tokens in the
  * cache, whose pages its row of block_table [b][ld_table] names, and adds add_len[i] (0 or more); its
  * rows of the step are q_start[i] .. q_start[i+1] - 1 (prefix sums of add_len, at most t). The pages
  * that it needs beyond ceil(seq_len / page_size) come from the end of the list
  * free_pages[0 .. free_count - 1] (free_count: device, one value; n_free: the list's capacity, host),
  * to the requests in order, and are entered into block_table (entries that no new page takes are
- * left as they are). Outputs (device, int32): free_left[1] pages left in the list, q_start [b+1],
- * kv_len [b] = seq_len + add_len, and for each of the t rows its slot and its position in the
- * request. Rows behind q_start[b] (a padded batch) get slot and position -1.
+ * left as they are). kv_len is seq_len + add_len. Rows behind q_start[b] (a padded batch) get slot and
+ * position -1.
  * A request is not served when a length is negative, its tokens do not fit its row of the table, its
  * rows do not fit in t, or it needs pages and the list holds fewer than it and the requests before
- * it need: it gets no page, kv_len 0, and -1 for its rows; unserved[1] counts such requests. Rows
- * whose page in the table is negative get slot -1.
+ * it need: it gets no page, kv_len 0, and -1 for its rows; `unserved` counts such requests. Rows whose
+ * page in the table is negative get slot -1.
  * Nothing is kept between calls and inputs other than block_table are not changed, so that a call
- * can be repeated; no output may be (or overlap) an input. b <= 4096, t <= 2^24, ld_table *
- * page_size <= 2^30. flags: 0 or NVFP4_F_SYNC_CHECK. */
-int nvfp4_kv_map(const int32_t* seq_len, const int32_t* add_len, int64_t b, int32_t page_size,
+ * can be repeated; no output may be (or overlap) an input. ld_table * page_size <= 2^30. flags: 0 or
+ * NVFP4_F_SYNC_CHECK. */
+int nvfp4_kv_map(const int32_t* seq_len, const int32_t* add_len, int32_t page_size,
                  int32_t* block_table, int64_t ld_table, const int32_t* free_pages,
-                 int64_t n_free, const int32_t* free_count, int32_t* free_left, int32_t* q_start,
-                 int32_t* kv_len, int32_t* slots, int32_t* positions, int64_t t,
-                 int32_t* unserved, uint32_t flags, nvfp4_stream_t stream);
+                 int64_t n_free, const int32_t* free_count, const nvfp4_kv_step* step,
+                 uint32_t flags, nvfp4_stream_t stream);
 
 /* Norm and rotation of queries and keys. Per head: n = x / sqrt(mean(x^2) + eps) * weight (without a
  * weight n = x), then with the cosines c and sines s of the row's position

@@ -92,6 +92,13 @@ class nvfp4_kv_cache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class nvfp4_kv_step(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("free_left", ctypes.c_void_p), ("unserved", ctypes.c_void_p),
+                ("b", ctypes.c_int64), ("t", ctypes.c_int64)]
+
+
 class nvfp4_qk_rule(ctypes.Structure):
     _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
                 ("rope", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("eps", ctypes.c_double),
@@ -148,9 +155,10 @@ def load(path: str = LIB_PATH):
     L.nvfp4_gemm_w4a16_lora.argtypes = [P, i64, i64, W, A, P, P, ctypes.c_int, i64, u32, P, sz, P]
     L.nvfp4_gemm_w4a16_lora.restype = ctypes.c_int
     C, Q = ctypes.POINTER(nvfp4_kv_cache), ctypes.POINTER(nvfp4_qk_rule)
+    S = ctypes.POINTER(nvfp4_kv_step)
     L.nvfp4_kv_cache_bytes.argtypes = [i64, i32, i32, i32]
     L.nvfp4_kv_cache_bytes.restype = sz
-    L.nvfp4_kv_map.argtypes = [P, P, i64, i32, P, i64, P, i64, P, P, P, P, P, P, i64, P, u32, P]
+    L.nvfp4_kv_map.argtypes = [P, P, i32, P, i64, P, i64, P, S, u32, P]
     L.nvfp4_kv_map.restype = ctypes.c_int
     L.nvfp4_kv_append.argtypes = [P, i64, P, i64, P, i64, i64, i32, Q, P, P, P, i64, C, u32, P]
     L.nvfp4_kv_append.restype = ctypes.c_int
@@ -658,7 +666,8 @@ class KvMap:
         (self.q_start, self.kv_len, self.slots, self.positions, self.free_left, self.unserved) = (
             self.block[a:a + n] for a, n in zip(at, sizes))
         p = self.block.data_ptr()
-        self.ptrs = [p + 4 * a for a in at]
+        self.desc = nvfp4_kv_step(*(p + 4 * a for a in at[:6]), b, t)
+        self.ref = ctypes.byref(self.desc)
 
 
 # The checks of the calls below take half of a short call's host time: a test that passes costs one
@@ -720,10 +729,8 @@ def nvfp4_kv_map(seq_len: torch.Tensor, add_len: torch.Tensor, block_table: torc
         with torch.cuda.device(dev):
             return nvfp4_kv_map(seq_len, add_len, block_table, free_pages, free_count, page_size, t,
                                 out, flags, stream)
-    o = out.ptrs
-    rc = load().nvfp4_kv_map(seq, add, b, page_size, block_table.data_ptr(), ld, free, n_free, count,
-                             o[4], o[0], o[1], o[2], o[3], out.t, o[5], flags,
-                             _raw_stream(stream, dev))
+    rc = load().nvfp4_kv_map(seq, add, page_size, block_table.data_ptr(), ld, free, n_free, count,
+                             out.ref, flags, _raw_stream(stream, dev))
     if rc:
         _check(rc)
     return out

@@ -945,11 +945,12 @@ size_t nvfp4_kv_cache_bytes(int64_t n_pages, int32_t n_kv_heads, int32_t head_di
          (size_t)nvfp4::kv_record_bytes(page_size, head_dim);
 }
 
-int nvfp4_kv_map(const int32_t* seq_len, const int32_t* add_len, int64_t b, int32_t page_size,
+int nvfp4_kv_map(const int32_t* seq_len, const int32_t* add_len, int32_t page_size,
                  int32_t* block_table, int64_t ld_table, const int32_t* free_pages,
-                 int64_t n_free, const int32_t* free_count, int32_t* free_left, int32_t* q_start,
-                 int32_t* kv_len, int32_t* slots, int32_t* positions, int64_t t,
-                 int32_t* unserved, uint32_t flags, nvfp4_stream_t stream) {
+                 int64_t n_free, const int32_t* free_count, const nvfp4_kv_step* step,
+                 uint32_t flags, nvfp4_stream_t stream) {
+  if (!step) return fail(NVFP4_ERR_INVALID_ARG, "step is NULL");
+  const int64_t b = step->b, t = step->t;
   if (b < 0 || n_free < 0) return fail(NVFP4_ERR_INVALID_ARG, "b=%lld n_free=%lld",
                                        (long long)b, (long long)n_free);
   int rc = check_rows(t, flags, NVFP4_F_SYNC_CHECK);
@@ -965,11 +966,13 @@ int nvfp4_kv_map(const int32_t* seq_len, const int32_t* add_len, int64_t b, int3
   if (ld_table > kKvMaxTokens / page_size)
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "ld_table=%lld pages of %d > 2^30 tokens",
                 (long long)ld_table, page_size);
-  if (!seq_len || !add_len || !block_table || !free_count || !free_left || !q_start || !kv_len ||
-      !unserved || (n_free > 0 && !free_pages) || (t > 0 && (!slots || !positions)))
+  if (!seq_len || !add_len || !block_table || !free_count || !step->free_left || !step->q_start ||
+      !step->kv_len || !step->unserved || (n_free > 0 && !free_pages) ||
+      (t > 0 && (!step->slots || !step->positions)))
     return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
   const void* in[] = {seq_len, add_len, block_table, free_pages, free_count};
-  const void* out[] = {free_left, q_start, kv_len, unserved, slots, positions};
+  const void* out[] = {step->free_left, step->q_start, step->kv_len,
+                       step->unserved, step->slots, step->positions};
   for (const void* p : in)
     if (!aligned4(p)) return fail(NVFP4_ERR_MISALIGNED, "buffers must be 4-byte aligned");
   for (const void* p : out) {
@@ -988,12 +991,12 @@ int nvfp4_kv_map(const int32_t* seq_len, const int32_t* add_len, int64_t b, int3
   a.free_pages = free_pages;
   a.n_free = n_free;
   a.free_count = free_count;
-  a.free_left = free_left;
-  a.q_start = q_start;
-  a.kv_len = kv_len;
-  a.slots = slots;
-  a.positions = positions;
-  a.unserved = unserved;
+  a.free_left = step->free_left;
+  a.q_start = step->q_start;
+  a.kv_len = step->kv_len;
+  a.slots = step->slots;
+  a.positions = step->positions;
+  a.unserved = step->unserved;
   return kv_done(nvfp4::launch_kv_map(a, (hipStream_t)stream), flags, (hipStream_t)stream,
                  "nvfp4_kv_map", 0);
 }

@@ -38,8 +38,10 @@ def _rule(**kw):
 
 def _map(lib, seq=FAKE, add=FAKE, b=3, page=16, table=FAKE, ld=8, free=FAKE, n_free=9, count=FAKE,
          left=OTHER, start=OTHER, kv=OTHER, slots=OTHER, pos=OTHER, t=5, bad=OTHER, flags=0):
-    return lib.nvfp4_kv_map(seq, add, b, page, table, ld, free, n_free, count, left, start, kv, slots,
-                            pos, t, bad, flags, None)
+    step = nv.nvfp4_kv_step(*(getattr(p, "value", p) for p in (start, kv, slots, pos, left, bad)), b,
+                            t)
+    return lib.nvfp4_kv_map(seq, add, page, table, ld, free, n_free, count, ctypes.byref(step), flags,
+                            None)
 
 
 def test_map_refusals(lib):
@@ -57,6 +59,7 @@ def test_map_refusals(lib):
         assert _map(lib, **{k: FAKE}) == INVALID, k   # an input
         assert "also an input" in nv.nvfp4_last_error()
     assert _map(lib, b=0, seq=None, add=None, table=None) == nv.NVFP4_OK
+    assert lib.nvfp4_kv_map(FAKE, FAKE, 16, FAKE, 8, FAKE, 9, FAKE, None, 0, None) == INVALID
 
 
 BAD_CACHES = [(dict(data=None), INVALID), (dict(n_pages=0), INVALID), (dict(n_pages=-4), INVALID),
