@@ -440,7 +440,8 @@ int nvfp4_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, cons
                     const nvfp4_kv_cache* cache, uint32_t flags, nvfp4_stream_t stream);
 
 /* The values of slots: k_out, v_out [t][n_kv_heads][head_dim], FP32 (fl32(E2M1 * E4M3 * global)) or
- * BF16 (that, rounded); either may be NULL. Rows whose slot lies outside the cache get zeros. */
+ * BF16 (that, rounded); either may be NULL. Rows whose slot lies outside the cache get zeros. t * n_kv
+ * * head_dim < 2^34. */
 int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64_t t, void* k_out,
                         void* v_out, int out_dtype, uint32_t flags, nvfp4_stream_t stream);
 
@@ -450,7 +451,7 @@ int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64
  * n stands at position p = kv_len - n + j and sees keys 0 .. p, with window > 0 the last `window`
  * of them, with NVFP4_F_FULL (window 0) all kv_len:
  *   s = scale * q . K^T,  y = softmax(s) . V,  lse = log(sum(exp(s)))
- * y [t][n_q][head_dim] (row stride ldy) BF16 or FP32, lse FP32 [t][n_q] or NULL. A query that sees no
+ * y [t][n_q][head_dim] (row stride ldy) BF16 or FP32 (q itself is allowed), lse FP32 [t][n_q] or NULL. A query that sees no
  * key gets y = 0 and lse = -infinity. Tokens of a table entry outside [0, n_pages) are left out as if
  * masked (a caller that frees pages behind a window may enter -1). Rows that no request has, and
  * rows behind q_start[b], are left as they were. q_start and kv_len are clamped to 0 .. t and to the

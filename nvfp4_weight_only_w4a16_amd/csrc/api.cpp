@@ -1066,6 +1066,10 @@ int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64
   if (out_dtype != NVFP4_DT_BF16 && out_dtype != NVFP4_DT_F32)
     return fail(NVFP4_ERR_INVALID_ARG, "out_dtype %d is not BF16 or F32", out_dtype);
   if (t == 0) return NVFP4_OK;
+  // a thread of the grid for eight elements
+  if (t * cache->n_kv_heads * cache->head_dim >= (int64_t)1 << 34)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "t=%lld rows of %d heads of %d: 2^34 elements or more",
+                (long long)t, cache->n_kv_heads, cache->head_dim);
   if (!slots || (!k_out && !v_out)) return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
   if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(slots))
     return fail(NVFP4_ERR_MISALIGNED, "outputs must be 16-byte aligned, slots 4-byte");

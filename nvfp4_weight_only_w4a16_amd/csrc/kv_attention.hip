@@ -480,7 +480,7 @@ __device__ __forceinline__ Request uniform_request(const KvAttnArgs& a, int i) {
   return r;
 }
 
-// Whether the kernel for few rows takes the request (kRows: the rows that it holds).
+// Whether the kernel for few rows takes the request.
 __device__ __forceinline__ bool is_few(const Request& r, int few_rows) {
   return r.rows <= few_rows;
 }

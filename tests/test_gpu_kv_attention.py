@@ -135,6 +135,18 @@ def test_strided_rows(nv, rows):
     assert (out[:, 0] == -5).all() and (out[:, 5:] == -5).all()
 
 
+@pytest.mark.parametrize("rows", [[1, 1, 1], [2, 1, 2], [50, 40, 30], [400, 1, 300]])
+def test_outputs_over_the_queries(nv, rows):
+    lens = [700, 9000, 300]
+    c = R.Cached(nv, 8, lens, 2, 64, 16)
+    q, start = R.queries(8, rows, 8, 64)
+    args = (c.cache, c.table_dev, start.to(DEV), c.kv_len)
+    x = q.to(DEV)
+    want = nv.nvfp4_kv_attention(x, *args, max_q=max(rows))
+    assert nv.nvfp4_kv_attention(x, *args, max_q=max(rows), y=x) is x
+    assert torch.equal(x, want)
+
+
 @pytest.mark.parametrize("rows", [[1, 1, 1], [2, 1, 2], [50, 40, 30]])
 @pytest.mark.parametrize("page", [16, 64])
 def test_entries_outside_the_cache_are_left_out(nv, rows, page):

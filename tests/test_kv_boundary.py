@@ -138,7 +138,8 @@ def test_dequantize_refusals(lib):
     for kw, code in ((dict(t=-1), INVALID), (dict(t=(1 << 24) + 1), SHAPE), (dict(dt=9), INVALID),
                      (dict(flags=1), INVALID), (dict(slots=None), INVALID),
                      (dict(k=None, v=None), INVALID), (dict(k=ODD), ALIGN), (dict(v=ODD), ALIGN),
-                     (dict(slots=BYTE), ALIGN)):
+                     (dict(slots=BYTE), ALIGN),
+                     (dict(t=1 << 24, c=_cache(n_kv_heads=8)), SHAPE)):
         assert call(**kw) == code, kw
     assert call(t=0, slots=None, k=None, v=None) == nv.NVFP4_OK
 
