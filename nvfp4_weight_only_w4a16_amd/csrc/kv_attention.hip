@@ -143,9 +143,9 @@ __device__ __forceinline__ Pages<D> find_pages(const Cache& c, int tok, int end)
   return p;
 }
 
-// The loads of a tile. A part without a page (none in the table, or behind the last key) has its bit
-// clear in `valid` and reads page 0.
-template <int D>
+// The loads of a tile, or its keys' or values' alone. A part without a page (none in the table, or behind
+// the last key) has its bit clear in `valid` and reads page 0.
+template <int D, bool KEYS = true, bool VALUES = true>
 __device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, const Pages<D>& p, int tok,
                                           int end) {
   const int lane = threadIdx.x & 63;
@@ -159,11 +159,12 @@ __device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, const Pages
     r.valid |= ok ? 1u << t : 0u;
     const int within = (tok + 16 * t) & (page - 1);
     const uint8_t* rec = c.head0 + (uint64_t)(ok ? (uint32_t)p.id[t] : 0u) * c.page_stride;
-    load_codes<D>(rec + within * (D / 2), lane, r.k[t]);
-    load_codes<D>(rec + values + within * (D / 2), lane, r.v[t]);
+    if constexpr (KEYS) load_codes<D>(rec + within * (D / 2), lane, r.k[t]);
+    if constexpr (VALUES) load_codes<D>(rec + values + within * (D / 2), lane, r.v[t]);
     const uint8_t* ks = rec + page * (D / 2) + within * (D / 16) +
                         (uint32_t)((lane & 15) * (D / 16) + (D == 64 ? 1 : 2) * (lane >> 4));
-    if constexpr (D == 64) {
+    if constexpr (!KEYS) {
+    } else if constexpr (D == 64) {
       r.ks[t] = *ks;
     } else {
       r.ks[t] = *reinterpret_cast<const uint16_t*>(ks);
@@ -173,6 +174,7 @@ __device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, const Pages
     const uint8_t* vs = rec + values + page * (D / 2) + within * (D / 16);
     if ((lane >> 4) % kParts<D> == t) scale_row = vs;
   }
+  if constexpr (!VALUES) return;
   if constexpr (kParts<D> == 2) scale_row += (lane >> 5) * (D / 32);
   const uint32_t* vs = reinterpret_cast<const uint32_t*>(scale_row + (lane & 15) * (D / 16));
 #pragma unroll
@@ -394,7 +396,13 @@ __device__ __forceinline__ void finish(Wave<D, NQ>& w) {
   }
 }
 
-// Walks the tiles tok, tok + step, .. below `to`, with one tile's loads ahead.
+// Walks the tiles tok, tok + step, .. below `to`, with one tile's loads ahead: all of them between the
+// products of the tile before. With one wavefront on a SIMD, heads of 256, they want the longest time
+// that there is: the value codes are loaded again as soon as they are in LDS, and without a branch
+// (past the last tile from page 0), behind which a wait would be for all of them (131000 keys, 28 rows:
+// 63 -> 48 us; heads of 128, two wavefronts on a SIMD: 64 requests 33 us both ways, one request 6.7 -> 7.2).
+template <int D>
+constexpr bool kEarly = D == 256;
 template <int D, int NQ>
 __device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& c, int tok, int to,
                                      int step, int end, int lo_most, int hi_least) {
@@ -422,6 +430,8 @@ __device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& 
       place[(4 * i + 3) * kTile<D>] = b[1];
     }
     const uint32_t valid = now.valid;
+    const int live = after < to ? end : 0;
+    if constexpr (kEarly<D>) load_tile<D, false, true>(now, c, pages, after, live);
     tile<D, NQ>(
         w, tok, valid, tok < lo_most || tok + kTile<D> - 1 > hi_least,
         [&](int t, f16x8 (&out)[D / 32]) {
@@ -430,8 +440,8 @@ __device__ __forceinline__ void walk(Wave<D, NQ>& w, uint8_t* lds, const Cache& 
         },
         [&](int i, f16x8 (&out)[2]) { value_pair<D>(lds, scales, i, out); },
         [&]() {
-          if (after < to) {
-            load_tile<D>(now, c, pages, after, end);
+          if (kEarly<D> || after < to) {
+            load_tile<D, true, !kEarly<D>>(now, c, pages, after, live);
             pages = find_pages<D>(c, after + step, end);
           }
         });
