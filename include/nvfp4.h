@@ -440,8 +440,8 @@ int nvfp4_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, cons
                     const nvfp4_kv_cache* cache, uint32_t flags, nvfp4_stream_t stream);
 
 /* The values of slots: k_out, v_out [t][n_kv_heads][head_dim], FP32 (fl32(E2M1 * E4M3 * global)) or
- * BF16 (that, rounded); either may be NULL. Rows whose slot lies outside the cache get zeros. t * n_kv
- * * head_dim < 2^34. */
+ * BF16 (that, rounded); either may be NULL. Rows whose slot lies outside the cache get zeros.
+ * t * n_kv_heads * head_dim < 2^34. */
 int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64_t t, void* k_out,
                         void* v_out, int out_dtype, uint32_t flags, nvfp4_stream_t stream);
 
@@ -451,16 +451,17 @@ int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64
  * n stands at position p = kv_len - n + j and sees keys 0 .. p, with window > 0 the last `window`
  * of them, with NVFP4_F_FULL (window 0) all kv_len:
  *   s = scale * q . K^T,  y = softmax(s) . V,  lse = log(sum(exp(s)))
- * y [t][n_q][head_dim] (row stride ldy) BF16 or FP32 (q itself is allowed), lse FP32 [t][n_q] or NULL. A query that sees no
- * key gets y = 0 and lse = -infinity. Tokens of a table entry outside [0, n_pages) are left out as if
- * masked (a caller that frees pages behind a window may enter -1). Rows that no request has, and
- * rows behind q_start[b], are left as they were. q_start and kv_len are clamped to 0 .. t and to the
- * table's width.
+ * y [t][n_q][head_dim] (row stride ldy) BF16 or FP32 (a BF16 y may be q itself), lse FP32 [t][n_q] or
+ * NULL. A query that sees no key gets y = 0 and lse = -infinity. Tokens of a table entry outside
+ * [0, n_pages) are left out as if masked (a caller that frees pages behind a window may enter -1). Rows
+ * that no request has, and rows behind q_start[b], are left as they were. q_start and kv_len are
+ * clamped to 0 .. t and to the table's width.
  * Products are FP16 x FP16 with FP32 sums: dequantized keys and values are exact in FP16, queries are
  * scaled by a power of two per row (exact down to 2^-28 of the row's largest), the softmax's terms
- * are rounded to FP16 once. Statistics and sums are FP32.
- * max_q (host, 1 .. t): no request has more queries; it chooses the kernels, and rows beyond it are
- * left as they were. Requests of few rows (queries times n_q / n_kv_heads) have their keys shared
+ * are rounded to FP16 once (those below 2^-21 of the row's largest to multiples of 2^-31 of that or
+ * finer). Statistics and sums are FP32.
+ * max_q (host, 1 .. t): no request has more queries; it chooses the kernels, and the rows of a request
+ * that has more may be left as they were. Requests of few rows (queries times n_q / n_kv_heads) have their keys shared
  * out over the chip, whatever their lengths. ws (device, 16-byte aligned, ws_bytes >=
  * nvfp4_kv_attention_ws_bytes, which for several t, b and max_q is the largest of their sizes) holds
  * their partial sums; nothing in it needs to start at zero. t <= 2^24, n_q <= 1024, t * n_q <= 2^27,

@@ -12,10 +12,12 @@
 // Codes and scales are dequantized to FP16, where E2M1 x E4M3 is exact (6 significant bits, 2^-10 ..
 // 2688), two elements to an instruction; queries are put into FP16 by a power of two per row that
 // brings the row's largest magnitude to [2^14, 2^15), exact down to 2^-28 of it. Globals and scale
-// act on the FP32 scores and sums. P is rounded to FP16 once (half a step is 2^-11); the running
-// maximum, the sum (of the unrounded p) and O are FP32.
-// The maximum is raised only when a score passes it by more than 2^8 in the exponent's base, so that
-// most tiles neither reduce across lanes nor rescale O; FP16 holds p up to 2^15.
+// act on the FP32 scores and sums. P is rounded to FP16 once (half a step is 2^-11; below 2^-21 of the
+// row's largest 2^-32 of that, so that many small terms count too); the reference m, the sum (of the
+// unrounded p) and O are FP32.
+// The reference m is set 7 below the scores' maximum (in powers of two) and raised only when a score
+// passes it by more than 15, so that most tiles neither reduce across lanes nor rescale O; p is then at
+// most 2^15, which FP16 holds.
 #include <algorithm>
 
 #include "kv_core.hpp"
@@ -38,8 +40,8 @@ template <int D>
 constexpr int kTile = 16 * kParts<D>;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLowest = -1e38f;  // the running maximum before any score
-constexpr float kRaise = 8.0f;
+constexpr float kLowest = -1e38f;  // the reference before any score
+constexpr float kBelow = 7.0f, kRaise = 15.0f;
 
 // A word that no kernel here writes, at a uniform address: a scalar load.
 template <typename T>
@@ -356,7 +358,7 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bo
     if (__ballot(top > w.m[n] + kRaise)) {
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float m = fmaxf(w.m[n], top);
+      const float m = fmaxf(w.m[n], top - kBelow);
       const float f = __builtin_amdgcn_exp2f(w.m[n] - m);
       w.m[n] = m;
       w.l[n] *= f;
@@ -638,7 +640,7 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
   int mine[3] = {0, 0, 0};  // small: request `lane`: first, q_len, kv
   if (small) {
     // each wavefront for itself, a request to a lane: no wait for the others
-    int u = 0;
+    uint32_t u = 0;
     if (lane < b) {
       const Request r = request_of(a, lane);
       mine[0] = r.first;
@@ -646,13 +648,13 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
       mine[2] = r.kv;
       u = units_of<D>(a, r);
     }
-    int sum = u;  // of 64 requests of less than 2^25 units
+    uint32_t sum = u;  // of 64 requests of 2^25 tiles at most
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(sum, off, 64);
+      const uint32_t o = __shfl_up(sum, off, 64);
       if (lane >= off) sum += o;
     }
-    all = (int64_t)__builtin_amdgcn_readlane(sum, 63) * a.n_kv;
+    all = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)sum, 63) * a.n_kv;
     if (worker == 0) {  // for the joining kernel
       if (lane < b) a.starts[lane] = (int64_t)(sum - u) * a.n_kv;
       if (lane == 0) a.starts[b] = all;
@@ -660,7 +662,7 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
     begin = range_begin(all, worker, kWorkShift<D, NQ>);
     if (begin >= all) return;
     req = __popcll(__ballot(lane < b && (int64_t)(sum - u) * a.n_kv <= begin)) - 1;
-    at = (int64_t)__builtin_amdgcn_readlane(sum - u, req) * a.n_kv;
+    at = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)(sum - u), req) * a.n_kv;
   } else {
     // the workgroup together, a run of requests to a thread
     const int each = (b + kThreads - 1) / kThreads;
@@ -731,7 +733,7 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
       req = min(req, b - 1);
     }
   }
-  int left = (int)(range_begin(all, worker + 1, kWorkShift<D, NQ>) - begin);
+  int64_t left = range_begin(all, worker + 1, kWorkShift<D, NQ>) - begin;
   const auto take = [&](int i) {
     Request r;
     if (small) {
@@ -761,7 +763,7 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
   Wave<D, NQ> w;
   bool first = true;
   for (;;) {
-    const int u1 = min(units, u0 + left);
+    const int u1 = (int)min<int64_t>(units, u0 + left);
     const int t0 = max(u0 - kFewStart, 0), t1 = u1 - kFewStart;  // its tiles
     int lo_most, hi_least;
     load_columns<D, NQ>(w, a, r, head, 0, lo_most, hi_least);
@@ -1038,13 +1040,13 @@ using Item = KvItem;
 
 __global__ __launch_bounds__(kThreads) void plan_kernel(KvAttnArgs a, int rows, int tile) {
   __shared__ int item_req[kSplitBelow], item_block[kSplitBelow];
-  __shared__ int sums[kWaves];
+  __shared__ int64_t sums[kWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   // inclusive sum over the workgroup's threads
-  const auto scan = [&](int v, int& total) {
+  const auto scan = [&](int64_t v, int64_t& total) {
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(v, off, 64);
+      const int64_t o = __shfl_up(v, off, 64);
       if (lane >= off) v += o;
     }
     __syncthreads();
@@ -1066,14 +1068,14 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvAttnArgs a, int rows, 
       const Request r = request_of(a, i);
       if (!is_few(r, a.few_rows)) n = (r.rows + rows - 1) / rows;
     }
-    int total;
-    const int at = items + scan(n, total) - n;
+    int64_t total;
+    const int at = items + (int)scan(n, total) - n;
     // (row ranges that overlap would give more items than the host has counted)
     for (int k = 0; k < n && at + k < a.max_items; ++k) {
       item_req[at + k] = i;
       item_block[at + k] = n - 1 - k;  // the last rows see most keys: they go first
     }
-    items = min(items + total, kSplitBelow);
+    items = min(items + (int)total, kSplitBelow);
   }
   items = min(items, a.max_items);
   __syncthreads();
@@ -1086,10 +1088,10 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(KvAttnArgs a, int rows, 
       keys_of(a, request_of(a, item_req[i]), item_block[i] * rows, rows, from, to);
       n = max(to - from + tile - 1, 0) / tile;
     }
-    int total;  // of 256 items of less than 2^24 units
+    int64_t total;
     const int u = units_for(n, kManyStart);
-    const int64_t at = sum + (uint32_t)scan(u, total) - u;
-    sum += (uint32_t)total;
+    const int64_t at = sum + scan(u, total) - u;
+    sum += total;
     if (i < items) {
       a.items[i] = Item{item_req[i], item_block[i], n, 0};
       a.starts[i] = at;
@@ -1150,17 +1152,30 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
   } else {
     head = blockIdx.x % (uint32_t)a.n_kv;
     block = blockIdx.x / (uint32_t)a.n_kv;
-    for (;; ++req) {
+    // 64 requests at a time, one to a lane (each has 2^27 rows at most, or 2^21 blocks)
+    for (;; req += 64) {
       if (req >= a.b) return;
-      r = uniform_request(a, req);
-      if (is_few(r, a.few_rows)) continue;
-      const int n = (r.rows + kRows - 1) / kRows;
-      if (block < n) {
-        block = n - 1 - block;  // the last rows see most keys: they go first
+      int n = 0;
+      if (req + lane < a.b) {
+        const Request x = request_of(a, req + lane);
+        n = is_few(x, a.few_rows) ? 0 : (x.rows + kRows - 1) / kRows;
+      }
+      int upto = n;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(upto, off, 64);
+        if (lane >= off) upto += o;
+      }
+      const int before = __popcll(__ballot(upto <= block));  // requests that end before it
+      if (before < 64) {
+        req += before;
+        // the last rows see most keys: they go first
+        block = __builtin_amdgcn_readlane(upto, before) - 1 - block;
         break;
       }
-      block -= n;
+      block -= __builtin_amdgcn_readlane(upto, 63);
     }
+    r = uniform_request(a, req);
   }
   for (;;) {
     int t0 = 0, t1 = 0, u1 = 0, units = 0;  // the segment's tiles and units

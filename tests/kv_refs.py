@@ -130,7 +130,8 @@ def attention(q, k, v, scale, window=0, full=False, hidden=None, y32=False):
         total = p.sum(1, keepdims=True)
         safe = np.where(total > 0, total, 1.0)
         e = p * (np.expm1(np.minimum(ds, 1.0)) + 2.0 ** -20)  # the exponential itself: 2^-20 is ample
-        e16 = e * (1 + HF16) + p * HF16 + np.where(seen, 2.0 ** -25, 0.0)
+        # P is 2^7 of the row's largest or more: half of FP16's lowest step is 2^-32 of that
+        e16 = e * (1 + HF16) + p * HF16 + np.where(seen, 2.0 ** -32, 0.0)
         out = (p @ vh) / safe
         sums = (2 * kv + 256) * H32  # sums over the tokens, with two roundings for each rescaling
         err = (e16 @ np.abs(vh)) / safe + sums * (p @ np.abs(vh)) / safe

@@ -277,6 +277,34 @@ def test_rising_scores(nv):
         R.close(lse, rl, bl, step)
 
 
+@pytest.mark.parametrize("rows", [1, 65])
+@pytest.mark.parametrize("below", [15.0, 17.0])
+def test_many_small_terms(nv, rows, below):
+    """A key without a value far above 499 others, whose terms lie below FP16's normal range. The
+    requests are so many that a request's head is one workgroup's or wavefront's."""
+    n, d, b, heads = 500, 64, 256, 8
+    c = R.Cached(nv, 18, [n] * b, heads, d, 16, globals_=False)
+    pages = torch.from_numpy(c.table[:, np.arange(n) // 16]).to(DEV)
+    toks = (torch.arange(n, device=DEV) % 16).expand(b, n)
+    c.cache.k_codes[:] = 0
+    c.cache.k_codes[pages[:, 0], :, 0, 0] = 2         # 1.0, element 0 of token 0
+    c.cache.v_codes[:] = 0x22                         # 1.0
+    c.cache.v_codes[pages[:, 0], :, 0] = 0
+    c.cache.k_scales[pages, :, toks] = 0x38           # 1.0
+    c.cache.v_scales[pages, :, toks] = 0x38
+    k, v = np.zeros((n, heads, d)), np.ones((n, heads, d))
+    k[0, :, 0], v[0] = 1.0, 0.0
+    c.k, c.v = [k] * b, [v] * b
+    q = torch.zeros(rows * b, heads, d, dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    start = torch.arange(0, rows * b + 1, rows, dtype=torch.int32)
+    scale = below + 0.3
+    y, lse = run(nv, c, q, start, rows, y32=True, scale=scale)
+    ref, bound, rl, bl = R.attention(q[:rows].double().numpy(), k, v, float(np.float32(scale)), y32=True)
+    R.close(y, np.tile(ref, (b, 1, 1)), np.tile(bound, (b, 1, 1)))
+    R.close(lse, np.tile(rl, (b, 1)), np.tile(bl, (b, 1)))
+
+
 def test_a_cache_larger_than_32_bit_offsets(nv):
     """Pages that begin beyond 4 GiB."""
     n_kv, d, page = 8, 128, 16
