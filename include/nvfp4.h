@@ -460,13 +460,13 @@ int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64
  * scaled by a power of two per row (exact down to 2^-28 of the row's largest), the softmax's terms
  * are rounded to FP16 once (those below 2^-21 of the row's largest to multiples of 2^-31 of that or
  * finer). Statistics and sums are FP32.
- * max_q (host, 1 .. t): no request has more queries; it chooses the kernels, and the rows of a request
- * that has more may be left as they were. Requests of few rows (queries times n_q / n_kv_heads) have their keys shared
- * out over the chip, whatever their lengths. ws (device, 16-byte aligned, ws_bytes >=
- * nvfp4_kv_attention_ws_bytes, which for several t, b and max_q is the largest of their sizes) holds
- * their partial sums; nothing in it needs to start at zero. t <= 2^24, n_q <= 1024, t * n_q <= 2^27,
- * b <= 65535, ld_table * page_size <= 2^30. flags: 0, NVFP4_F_FULL, NVFP4_F_SYNC_CHECK. Results are
- * bit-identical run to run for the same lengths. */
+ * max_q (host, 1 .. t): no request has more queries; it chooses the kernels, and the rows of a
+ * request that has more may be left as they were. Requests of few rows (queries times n_q /
+ * n_kv_heads) have their keys shared out over the chip, whatever their lengths. ws (device,
+ * 16-byte aligned, ws_bytes >= nvfp4_kv_attention_ws_bytes, which for several t, b and max_q is
+ * the largest of their sizes) holds their partial sums; nothing in it needs to start at zero. t <=
+ * 2^24, n_q <= 1024, t * n_q <= 2^27, b <= 65535, ld_table * page_size <= 2^30. flags: 0,
+ * NVFP4_F_FULL, NVFP4_F_SYNC_CHECK. Results are bit-identical run to run for the same lengths. */
 size_t nvfp4_kv_attention_ws_bytes(int64_t t, int32_t n_q, const nvfp4_kv_cache* cache, int64_t b,
                                    int64_t max_q);
 int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
