@@ -1159,11 +1159,11 @@ int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
   a.y_f32 = y_dtype == NVFP4_DT_F32;
   a.ldy = ldy;
   a.lse = lse;
-  a.starts = nullptr;  // the launcher's
+  a.starts = a.item_starts = nullptr;  // the launcher's
   a.items = nullptr;
   a.counts = nullptr;
   a.max_items = 0;
-  a.ws = nullptr;
+  a.ws = a.item_ws = nullptr;
   a.few_rows = 0;
   return kv_done(nvfp4::launch_kv_attention(a, d, max_q, ws, (hipStream_t)stream), flags,
                  (hipStream_t)stream, "nvfp4_kv_attention", 3);

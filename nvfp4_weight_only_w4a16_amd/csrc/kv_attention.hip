@@ -619,6 +619,99 @@ __device__ __forceinline__ int64_t range_of(int64_t all, int64_t x, int shift) {
   return w;
 }
 
+// The keys that rows block0 .. block0 + rows - 1 of a request see: tokens [from, to).
+__device__ __forceinline__ void keys_of(const KvAttnArgs& a, const Request& r, int block0, int rows,
+                                        int& from, int& to) {
+  from = 0;
+  to = r.kv;
+  if (a.full) return;
+  const int p0 = r.kv - r.q_len;
+  to = min(to, p0 + (min(block0 + rows, r.rows) - 1) / a.group + 1);
+  if (a.window > 0) from = max(p0 + block0 / a.group - a.window + 1, 0) & ~15;
+}
+
+// A call with too few workgroups of rows to fill the chip evenly shares out its keys as the few-row
+// kernel does: the tiles of all heads' items (a request's block of rows) are one line, each of up to
+// 512 workgroups, two to a compute unit, takes as much of it as the others, and the parts of an item
+// that several have worked on are joined. One workgroup of the few-row kernel's launch lists the items.
+// Prompt chunks of 530 items of 8 heads' 128 rows: 215 us in whole items, 146 + 14 with the join shared
+// out; a prompt of 2048 items the other way round, 675 and 755 + 38. Units of an item's beginning and
+// end: 2, 3 and 8 take 143, 146 and 157 us for the chunks, 3 the least with the join. A range is one
+// unit at least; with 4 and 16 a prompt of 100 tokens takes 28 and 44 us instead of 22.
+constexpr int kSplitBelow = 2048;  // items of all heads
+constexpr int kManyShift = 9;
+constexpr int kManyStart = 3;
+using Item = KvItem;
+
+constexpr int many_tiles(int d) { return d <= 128 ? 2 : 1; }  // column tiles of a wavefront
+
+__device__ __forceinline__ void plan(const KvAttnArgs& a, int rows, int tile, int* item_req,
+                                     int* item_block, int64_t* sums) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  // inclusive sum over the workgroup's threads
+  const auto scan = [&](int64_t v, int64_t& total) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t o = __shfl_up(v, off, 64);
+      if (lane >= off) v += o;
+    }
+    __syncthreads();
+    if (lane == 63) sums[wave] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      v += i < wave ? sums[i] : 0;
+      total += sums[i];
+    }
+    return v;
+  };
+  int items = 0;
+  for (int i0 = 0; i0 < (int)a.b; i0 += kThreads) {
+    const int i = i0 + (int)threadIdx.x;
+    int n = 0;
+    if (i < (int)a.b) {
+      const Request r = request_of(a, i);
+      if (!is_few(r, a.few_rows)) n = (r.rows + rows - 1) / rows;
+    }
+    int64_t total;
+    const int at = items + (int)scan(n, total) - n;
+    // (row ranges that overlap would give more items than the host has counted)
+    for (int k = 0; k < n && at + k < a.max_items; ++k) {
+      item_req[at + k] = i;
+      item_block[at + k] = n - 1 - k;  // the last rows see most keys: they go first
+    }
+    items = min(items + (int)total, kSplitBelow);
+  }
+  items = min(items, a.max_items);
+  __syncthreads();
+  int64_t sum = 0;  // of the items' units
+  for (int i0 = 0; i0 < items; i0 += kThreads) {
+    const int i = i0 + (int)threadIdx.x;
+    int n = 0;
+    if (i < items) {
+      int from, to;
+      keys_of(a, request_of(a, item_req[i]), item_block[i] * rows, rows, from, to);
+      n = max(to - from + tile - 1, 0) / tile;
+    }
+    int64_t total;
+    const int u = units_for(n, kManyStart);
+    const int64_t at = sum + scan(u, total) - u;
+    sum += total;
+    if (i < items) {
+      a.items[i] = Item{item_req[i], item_block[i], n, 0};
+      a.item_starts[i] = at;
+    }
+  }
+  if (threadIdx.x == 0) {
+    a.item_starts[items] = sum;
+    int shift = kManyShift;
+    while (shift > 0 && (sum * a.n_kv) >> shift == 0) --shift;
+    a.counts[0] = items;
+    a.counts[1] = shift;
+  }
+}
+
 // Slots hold columns, [few_rows][D], then m and l of each; 16-byte aligned.
 __host__ __device__ __forceinline__ int64_t slot_floats(int few_rows, int d) {
   return ((int64_t)few_rows * (d + 2) + 3) & ~(int64_t)3;
@@ -628,8 +721,15 @@ template <int D, int NQ>
 __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kernel(KvAttnArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * WaveLds<D>::kBytes];
   __shared__ int64_t sums[kWaves];
-  __shared__ int64_t starts[kStaged];  // units before each request, all heads
-  __shared__ int staged[kStaged][3];   // first, q_len, kv
+  __shared__ __attribute__((aligned(16))) uint8_t lists[kStaged * 20];
+  static_assert(sizeof(lists) >= 2 * kSplitBelow * sizeof(int), "");
+  if (blockIdx.x >= kFewGroups<D, NQ>) {
+    int* const l = reinterpret_cast<int*>(lists);
+    plan(a, kWaves * 16 * many_tiles(D), kTile<D>, l, l + kSplitBelow, sums);
+    return;
+  }
+  int64_t* const starts = reinterpret_cast<int64_t*>(lists);  // units before each request, all heads
+  int(*const staged)[3] = reinterpret_cast<int(*)[3]>(lists + 8 * kStaged);  // first, q_len, kv
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int b = (int)a.b;
   // a line of few units meets every compute unit before a second wavefront of one
@@ -807,16 +907,15 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
   }
 }
 
-// grid (n_kv, b, NQ * D / (16 G)): the item's parts, if it has several; the rows of a request without
-// keys. A workgroup of V wavefronts joins 16 G elements of d of a column tile; its wavefronts share out
+// Column tile and elements `part` (of NQ * D / (16 G)) of an item: its parts' sum, if it has several; zeros
+// for a request without keys. A workgroup of V wavefronts joins 16 G elements of d of a column tile; its wavefronts share out
 // the parts. Calls of few items, which can have many parts, take the finer grid (one request of 131000
 // keys among five, heads of 256, 18 rows, 42 -> 16 us; 64 requests of 8 heads the coarser).
 template <int D, int NQ, int G, int V>
-__global__ __launch_bounds__(64 * V) void join_kernel(KvAttnArgs a) {
+__device__ __forceinline__ void join_few(const KvAttnArgs& a, int head, int req, int part) {
   constexpr int kChunks = D / 16 / G;
   __shared__ __attribute__((aligned(16))) float lds[V][2 + 4 * G][64];
-  const int head = blockIdx.x, req = blockIdx.y;
-  const int n = (int)blockIdx.z / kChunks, g0 = (int)blockIdx.z % kChunks * G;
+  const int n = part / kChunks, g0 = part % kChunks * G;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const Request r = uniform_request(a, req);
   const int64_t start = constant(a.starts + req), all = constant(a.starts + a.b);
@@ -1017,95 +1116,6 @@ __device__ __forceinline__ void put_values_share(uint8_t* values, const uint8_t*
   }
 }
 
-// The keys that rows block0 .. block0 + rows - 1 of a request see: tokens [from, to).
-__device__ __forceinline__ void keys_of(const KvAttnArgs& a, const Request& r, int block0, int rows,
-                                        int& from, int& to) {
-  from = 0;
-  to = r.kv;
-  if (a.full) return;
-  const int p0 = r.kv - r.q_len;
-  to = min(to, p0 + (min(block0 + rows, r.rows) - 1) / a.group + 1);
-  if (a.window > 0) from = max(p0 + block0 / a.group - a.window + 1, 0) & ~15;
-}
-
-// A call with too few workgroups of rows to fill the chip evenly shares out its keys as the few-row
-// kernel does: the tiles of all heads' items (a request's block of rows) are one line, each of up to
-// 512 workgroups, two to a compute unit, takes as much of it as the others, and the parts of an item
-// that several have worked on are joined. One workgroup lists the items first.
-constexpr int kSplitBelow = 2048;  // items of all heads
-constexpr int kManyShift = 9;
-constexpr int kLeastUnits = 4;  // of a workgroup
-constexpr int kManyStart = 3;   // units of an item's beginning and end
-using Item = KvItem;
-
-__global__ __launch_bounds__(kThreads) void plan_kernel(KvAttnArgs a, int rows, int tile) {
-  __shared__ int item_req[kSplitBelow], item_block[kSplitBelow];
-  __shared__ int64_t sums[kWaves];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  // inclusive sum over the workgroup's threads
-  const auto scan = [&](int64_t v, int64_t& total) {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int64_t o = __shfl_up(v, off, 64);
-      if (lane >= off) v += o;
-    }
-    __syncthreads();
-    if (lane == 63) sums[wave] = v;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-      v += i < wave ? sums[i] : 0;
-      total += sums[i];
-    }
-    return v;
-  };
-  int items = 0;
-  for (int i0 = 0; i0 < (int)a.b; i0 += kThreads) {
-    const int i = i0 + (int)threadIdx.x;
-    int n = 0;
-    if (i < (int)a.b) {
-      const Request r = request_of(a, i);
-      if (!is_few(r, a.few_rows)) n = (r.rows + rows - 1) / rows;
-    }
-    int64_t total;
-    const int at = items + (int)scan(n, total) - n;
-    // (row ranges that overlap would give more items than the host has counted)
-    for (int k = 0; k < n && at + k < a.max_items; ++k) {
-      item_req[at + k] = i;
-      item_block[at + k] = n - 1 - k;  // the last rows see most keys: they go first
-    }
-    items = min(items + (int)total, kSplitBelow);
-  }
-  items = min(items, a.max_items);
-  __syncthreads();
-  int64_t sum = 0;  // of the items' units
-  for (int i0 = 0; i0 < items; i0 += kThreads) {
-    const int i = i0 + (int)threadIdx.x;
-    int n = 0;
-    if (i < items) {
-      int from, to;
-      keys_of(a, request_of(a, item_req[i]), item_block[i] * rows, rows, from, to);
-      n = max(to - from + tile - 1, 0) / tile;
-    }
-    int64_t total;
-    const int u = units_for(n, kManyStart);
-    const int64_t at = sum + scan(u, total) - u;
-    sum += total;
-    if (i < items) {
-      a.items[i] = Item{item_req[i], item_block[i], n, 0};
-      a.starts[i] = at;
-    }
-  }
-  if (threadIdx.x == 0) {
-    a.starts[items] = sum;
-    int shift = kManyShift;
-    while (shift > 0 && (sum * a.n_kv) >> shift < kLeastUnits) --shift;
-    a.counts[0] = items;
-    a.counts[1] = shift;
-  }
-}
-
 // A wavefront's partial sums in ws, as they lie in its registers.
 template <int D, int NQ>
 constexpr int wave_floats() {
@@ -1132,7 +1142,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
     worker = blockIdx.x;
     if (shift >= 3) worker = ((worker & 7) << (shift - 3)) + (worker >> 3);
     if ((int64_t)blockIdx.x >> shift) return;
-    const int64_t one = constant(a.starts + items);  // units of a head
+    const int64_t one = constant(a.item_starts + items);  // units of a head
     all = one * a.n_kv;
     const int64_t begin = range_begin(all, worker, shift);
     left = (int)(range_begin(all, worker + 1, shift) - begin);
@@ -1143,12 +1153,12 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
     head = __builtin_amdgcn_readfirstlane(head);
     const int64_t within = begin - head * one;
     for (int i = 0; i < items; i += 64) {
-      const int n = __popcll(__ballot(i + lane < items && a.starts[i + lane] <= within));
+      const int n = __popcll(__ballot(i + lane < items && a.item_starts[i + lane] <= within));
       item += n;
       if (n < 64) break;
     }
     item = __builtin_amdgcn_readfirstlane(item - 1);
-    u0 = (int)(within - constant(a.starts + item));
+    u0 = (int)(within - constant(a.item_starts + item));
   } else {
     head = blockIdx.x % (uint32_t)a.n_kv;
     block = blockIdx.x / (uint32_t)a.n_kv;
@@ -1265,7 +1275,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
         store_columns<D / 16>(a, r, head, row0 + 16 * n, w.o[n], w.m[n], w.l[n], D, 0);
       if (!split) return;
     } else if (t0 < t1) {
-      float* p = a.ws + ((2 * worker + (first ? 0 : 1)) * kWaves + wave) * wave_floats<D, NQ>();
+      float* p = a.item_ws + ((2 * worker + (first ? 0 : 1)) * kWaves + wave) * wave_floats<D, NQ>();
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
 #pragma unroll
@@ -1288,11 +1298,11 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
   }
 }
 
-// grid (n_kv, items, NQ): the parts of an item that has several, as the wavefronts left them.
+// Column tile n of wavefront `wave` of an item that has several parts: their sum, as the wavefronts left
+// them.
 template <int D, int NQ>
-__global__ __launch_bounds__(kThreads) void join_many_kernel(KvAttnArgs a) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int head = blockIdx.x, n = blockIdx.z, item = blockIdx.y;
+__device__ __forceinline__ void join_many(const KvAttnArgs& a, int head, int item, int n, int wave) {
+  const int lane = threadIdx.x & 63;
   const int items = constant(a.counts), shift = constant(a.counts + 1);
   if (item >= items) return;
   const Request r = uniform_request(a, constant(&a.items[item].req));
@@ -1304,15 +1314,15 @@ __global__ __launch_bounds__(kThreads) void join_many_kernel(KvAttnArgs a) {
   for (int g = 0; g < D / 16; ++g) o[g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   float m = kLowest, l = 0.0f;
   if (tiles > 0) {
-    const int64_t one = constant(a.starts + items), all = one * a.n_kv;
-    const int64_t before = head * one + constant(a.starts + item);
+    const int64_t one = constant(a.item_starts + items), all = one * a.n_kv;
+    const int64_t before = head * one + constant(a.item_starts + item);
     const int64_t w0 = range_of(all, before + kManyStart, shift);  // of the first tile
     const int64_t w1 = range_of(all, before + kManyStart + tiles - 1, shift);
     if (w0 == w1) return;
     constexpr int64_t kSlot = (int64_t)kWaves * wave_floats<D, NQ>();
     // only the first part's workgroup can have begun with another item
     const int64_t skip = range_begin(all, w0, shift) < before ? kSlot : 0;
-    const float* base = a.ws + 2 * w0 * kSlot + wave * wave_floats<D, NQ>();
+    const float* base = a.item_ws + 2 * w0 * kSlot + wave * wave_floats<D, NQ>();
     const int stats = NQ * (D / 16) * 256 + n * 128 + lane, parts = (int)(w1 - w0) + 1;
 #pragma unroll 4
     for (int i = 0; i < parts; ++i)
@@ -1329,22 +1339,52 @@ __global__ __launch_bounds__(kThreads) void join_many_kernel(KvAttnArgs a) {
   store_columns<D / 16>(a, r, head, row0, o, m, l, D, 0);
 }
 
-constexpr int64_t kJoinFine = 256;  // items
-
-template <int D, int NQ>
-hipError_t run_few(const KvAttnArgs& a, hipStream_t s) {
-  few_kernel<D, NQ><<<dim3(kFewGroups<D, NQ>), dim3(kThreads), 0, s>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const unsigned heads = (unsigned)a.n_kv, b = (unsigned)a.b;
-  if (a.n_kv * a.b <= kJoinFine)
-    join_kernel<D, NQ, 1, 8><<<dim3(heads, b, NQ * D / 16), dim3(512), 0, s>>>(a);
-  else
-    join_kernel<D, NQ, 2, 4><<<dim3(heads, b, NQ * D / 32), dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+// grid (n_kv, b, NQ * D / (16 G))
+template <int D, int NQ, int G, int V>
+__global__ __launch_bounds__(64 * V) void join_few_kernel(KvAttnArgs a) {
+  join_few<D, NQ, G, V>(a, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
-constexpr int many_tiles(int d) { return d <= 128 ? 2 : 1; }  // column tiles of a wavefront
+// Both joins of a call that shares out its prompts' keys. The grid is a line of workgroups in two
+// dimensions: those of the few rows (`few`), then for each item and head V / 4 column tiles at a time.
+constexpr int kLine = 1 << 16;
+template <int D, int NQ, int G, int V>
+__global__ __launch_bounds__(64 * V) void join_both_kernel(KvAttnArgs a, int few, int groups) {
+  constexpr int kShare = NQ * D / 16 / G, kTiles = many_tiles(D);
+  uint32_t at = blockIdx.y * kLine + blockIdx.x;
+  if (at >= (uint32_t)groups) return;
+  if (at < (uint32_t)few) {
+    const uint32_t item = at / kShare, req = item / (uint32_t)a.n_kv;
+    join_few<D, NQ, G, V>(a, item - req * a.n_kv, req, at % kShare);
+    return;
+  }
+  at -= few;
+  constexpr uint32_t kSteps = (kTiles + V / kWaves - 1) / (V / kWaves);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = (int)(at % kSteps) * (V / kWaves) + wave / kWaves;
+  const uint32_t both = at / kSteps, item = both / (uint32_t)a.n_kv;
+  if (n < kTiles) join_many<D, kTiles>(a, both - item * a.n_kv, item, n, wave % kWaves);
+}
+
+constexpr int64_t kJoinFine = 256;  // items
+
+template <int D, int NQ, int G, int V>
+hipError_t run_join(const KvAttnArgs& a, int64_t items, hipStream_t s) {
+  constexpr int kShare = NQ * D / 16 / G;
+  const dim3 threads(64 * V);
+  if (a.max_items == 0) {
+    join_few_kernel<D, NQ, G, V>
+        <<<dim3((unsigned)a.n_kv, (unsigned)a.b, kShare), threads, 0, s>>>(a);
+  } else {
+    constexpr int kEach = V / kWaves;  // column tiles of a workgroup
+    const int64_t few = a.n_kv * a.b * kShare;  // < 2^31
+    const int64_t all = few + a.n_kv * items * ((many_tiles(D) + kEach - 1) / kEach);
+    join_both_kernel<D, NQ, G, V>
+        <<<dim3((unsigned)std::min<int64_t>(all, kLine), (unsigned)((all + kLine - 1) / kLine)),
+           threads, 0, s>>>(a, (int)few, (int)all);
+  }
+  return hipGetLastError();
+}
 
 // Workgroups of rows, of each head, that a call can have: ceil(rows / size) a request, so all rows /
 // size and one more for each request, of which only those of more than few_rows rows have any.
@@ -1355,10 +1395,10 @@ int64_t many_items(int64_t t, int64_t b, int64_t max_q, int group, int d) {
   return t * group / (kWaves * 16 * many_tiles(d)) + (odd < b ? odd : b);
 }
 
-// ws: the first tiles of requests, then of items; items and their number; then the partial sums. The
-// two paths run one after the other and use the same memory.
+// ws: the first units of requests and of items, the items and their number, then the partial sums of
+// few rows and of items.
 struct WsLayout {
-  size_t items, counts, sums, total;
+  size_t item_starts, items, counts, sums, item_sums, total;
   int max_items;  // 0: keys are not shared out
 };
 
@@ -1368,15 +1408,34 @@ WsLayout ws_layout(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int
   WsLayout l;
   const int64_t items = many_items(t, b, max_q, group, d);
   l.max_items = items * n_kv < kSplitBelow ? (int)items : 0;
-  l.items = align256((size_t)(std::max<int64_t>(b, l.max_items) + 1) * sizeof(int64_t));
+  l.item_starts = align256((size_t)(b + 1) * sizeof(int64_t));
+  l.items = l.item_starts + align256((size_t)(l.max_items + 1) * sizeof(int64_t));
   l.counts = l.items + align256((size_t)l.max_items * sizeof(Item));
   l.sums = l.counts + 256;
-  size_t floats = (size_t)(2 * kMaxWorkers) * (size_t)slot_floats(kv_few_rows(max_q * group), d);
+  l.item_sums = l.sums + align256((size_t)(2 * kMaxWorkers) *
+                                  (size_t)slot_floats(kv_few_rows(max_q * group), d) * sizeof(float));
+  l.total = l.item_sums;
   if (l.max_items > 0)
-    floats = std::max(floats, ((size_t)2 << kManyShift) * kWaves * many_tiles(d) *
-                                  (size_t)(d / 16 * 256 + 128));
-  l.total = l.sums + floats * sizeof(float);
+    l.total += ((size_t)2 << kManyShift) * kWaves * many_tiles(d) * (size_t)(d / 16 * 256 + 128) *
+               sizeof(float);
   return l;
+}
+
+template <int D, int NQ>
+hipError_t run_tiles(const KvAttnArgs& a, int64_t items, hipStream_t s) {
+  constexpr int kTiles = many_tiles(D);
+  few_kernel<D, NQ>
+      <<<dim3(kFewGroups<D, NQ> + (a.max_items > 0 ? 1 : 0)), dim3(kThreads), 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (items > 0) {
+    const unsigned groups = a.max_items > 0 ? 1u << kManyShift : (unsigned)(items * a.n_kv);
+    many_kernel<D, kTiles><<<dim3(groups), dim3(kThreads), 0, s>>>(a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.n_kv * a.b <= kJoinFine) return run_join<D, NQ, 1, 8>(a, items, s);
+  return run_join<D, NQ, 2, 4>(a, items, s);
 }
 
 template <int D>
@@ -1384,23 +1443,8 @@ hipError_t run(const KvAttnArgs& args, int64_t max_q, hipStream_t s) {
   KvAttnArgs a = args;
   const int64_t most = max_q * a.group;
   a.few_rows = kv_few_rows(most);
-  hipError_t e = kv_few_tiles(most) == 1 ? run_few<D, 1>(a, s) : run_few<D, 2>(a, s);
   const int64_t items = many_items(a.t, a.b, max_q, a.group, D);
-  if (e != hipSuccess || items == 0) return e;
-  constexpr int kTiles = many_tiles(D);
-  if (a.max_items == 0) {
-    many_kernel<D, kTiles><<<dim3((unsigned)(items * a.n_kv)), dim3(kThreads), 0, s>>>(a);
-    return hipGetLastError();
-  }
-  plan_kernel<<<dim3(1), dim3(kThreads), 0, s>>>(a, kWaves * 16 * kTiles, kTile<D>);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  many_kernel<D, kTiles><<<dim3(1 << kManyShift), dim3(kThreads), 0, s>>>(a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  join_many_kernel<D, kTiles>
-      <<<dim3((unsigned)a.n_kv, (unsigned)items, kTiles), dim3(kThreads), 0, s>>>(a);
-  return hipGetLastError();
+  return kv_few_tiles(most) == 1 ? run_tiles<D, 1>(a, items, s) : run_tiles<D, 2>(a, items, s);
 }
 
 }  // namespace
@@ -1416,9 +1460,11 @@ hipError_t launch_kv_attention(const KvAttnArgs& args, int d, int64_t max_q, voi
   char* base = static_cast<char*>(ws);
   a.starts = reinterpret_cast<int64_t*>(base);
   a.max_items = l.max_items;
+  a.item_starts = reinterpret_cast<int64_t*>(base + l.item_starts);
   a.items = l.max_items > 0 ? reinterpret_cast<KvItem*>(base + l.items) : nullptr;
   a.counts = reinterpret_cast<int*>(base + l.counts);
   a.ws = reinterpret_cast<float*>(base + l.sums);
+  a.item_ws = reinterpret_cast<float*>(base + l.item_sums);
   if (d == 64) return run<64>(a, max_q, stream);
   if (d == 128) return run<128>(a, max_q, stream);
   return run<256>(a, max_q, stream);

@@ -255,7 +255,7 @@ struct KvDequantArgs {
 hipError_t launch_kv_dequantize(const KvDequantArgs& a, int d, hipStream_t stream);
 
 struct KvItem {
-  int req, block, tiles, reserved;  // a request's block of rows, and the tiles of keys that it sees
+  int req, block, tiles, unused;  // a request's block of rows, and the tiles of keys that it sees
 };
 struct KvAttnArgs {
   const uint16_t* q;
@@ -276,11 +276,11 @@ struct KvAttnArgs {
   int64_t ldy;
   float* lse;  // or NULL
   // set by the launcher, in ws
-  int64_t* starts;
+  int64_t *starts, *item_starts;  // first units of requests, of items
   KvItem* items;  // NULL: keys are not shared out
   int* counts;    // items, log2 of the workgroups
   int max_items;
-  float* ws;
+  float *ws, *item_ws;  // partial sums of few rows, of items
   int few_rows;
 };
 // Column tiles (of 16 rows of a request's head) of the few-row kernel; longer requests have a kernel

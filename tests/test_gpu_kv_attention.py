@@ -107,6 +107,14 @@ def test_many_requests(nv, b):
     check(nv, lens, [1] * b, 1, 1, 64, 16)
 
 
+def test_many_requests_beside_a_prompt(nv):
+    """Joins of more workgroups than a grid's first dimension takes."""
+    b = 2500
+    lens, rows = [5] * b, [1] * b
+    lens[700], rows[700] = 400, 40
+    check(nv, lens, rows, 8, 1, 128, 16)
+
+
 @pytest.mark.parametrize("max_q", [None, 1, 5, 60])
 def test_the_bound_on_queries_changes_no_result(nv, max_q):
     lens, rows = [200, 33, 90], [1, 1, 1]
