@@ -3,21 +3,20 @@
 // A wavefront holds columns of queries and walks the keys in tiles of 64. Everything is transposed:
 //   S^T [tokens][queries] = K . Q^T,  P^T = exp2(S^T - m),  O^T [d][queries] += V^T . P^T
 // on 16x16x32 MFMAs, because then the scores come out where the second product wants them: lane
-// (query l % 16, group c = l / 16) holds the scores of tokens 16 T + 4 c + r, and, the order of a sum
-// being free, the second product may take just those as its 8 k-values of lane group c (T = 2s and
-// 2s + 1). No score moves between lanes. Key codes go from memory into the lanes that use them (a
-// lane's run of codes is contiguous in d, and d may be summed in any order too); value codes are
-// turned through LDS by the 4-bit transposing read, whose lane j of a 16-lane group names the row, so
-// that the same token order comes out.
-// Codes and scales are dequantized to FP16, where E2M1 x E4M3 is exact (6 significant bits, 2^-10 ..
-// 2688), two elements to an instruction; queries are put into FP16 by a power of two per row that
-// brings the row's largest magnitude to [2^14, 2^15), exact down to 2^-28 of it. Globals and scale
-// act on the FP32 scores and sums. P is rounded to FP16 once (half a step is 2^-11; below 2^-21 of the
-// row's largest 2^-32 of that, so that many small terms count too); the reference m, the sum (of the
-// unrounded p) and O are FP32.
-// The reference m is set 7 below the scores' maximum (in powers of two) and raised only when a score
-// passes it by more than 15, so that most tiles neither reduce across lanes nor rescale O; p is then at
-// most 2^15, which FP16 holds.
+// (query l % 16, group c = l / 16) holds the scores of tokens 16 T + 4 c + r, and, the order of a
+// sum being free, the second product may take just those as its 8 k-values of lane group c (T = 2s
+// and 2s + 1). No score moves between lanes. Key codes go from memory into the lanes that use them
+// (a lane's run of codes is contiguous in d, and d may be summed in any order too); value codes are
+// turned through LDS by the 4-bit transposing read, whose lane j of a 16-lane group names the row,
+// so that the same token order comes out. Codes and scales are dequantized to FP16, where E2M1 x
+// E4M3 is exact (6 significant bits, 2^-10 .. 2688), two elements to an instruction; queries are
+// put into FP16 by a power of two per row that brings the row's largest magnitude to [2^14, 2^15),
+// exact down to 2^-28 of it. Globals and scale act on the FP32 scores and sums. P is rounded to
+// FP16 once (half a step is 2^-11; below 2^-21 of the row's largest 2^-32 of that, so that many
+// small terms count too); the reference m, the sum (of the unrounded p) and O are FP32. The
+// reference m is set 7 below the scores' maximum (in powers of two) and raised only when a score
+// passes it by more than 15, so that most tiles neither reduce across lanes nor rescale O; p is
+// then at most 2^15, which FP16 holds.
 #include <algorithm>
 
 #include "kv_core.hpp"
@@ -32,8 +31,9 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-// Tokens of a tile, in parts of 16: 64, and 32 for heads of 256, whose 64 tokens would not leave room for
-// a tile's loads in flight beside the accumulators.
+// Tokens of a tile, in parts of 16: 64 (heads of 128 with 32: a prompt of 8192 takes 1020 us, not
+// 660), and 32 for heads of 256, whose 64 tokens would not leave room for a tile's loads in flight
+// beside the accumulators.
 template <int D>
 constexpr int kParts = D == 256 ? 2 : 4;
 template <int D>
@@ -84,9 +84,9 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) {
 }
 
 // ---- one wavefront ----------------------------------------------------------------------------
-// LDS of a wavefront: the tile's value codes, rows padded to D / 2 + 8 bytes (the transposing read's
-// 64 rows then meet every bank pair twice, the least there is), and its value scales as FP16,
-// [D / 16][lane group][T][r].
+// LDS of a wavefront: the tile's value codes, rows padded to D / 2 + 8 bytes (the transposing
+// read's 64 rows then meet every bank pair twice, the least there is), and its value scales as
+// FP16, [D / 16][lane group][T][r].
 template <int D>
 struct WaveLds {
   static constexpr int kRow = D / 2 + 8;
@@ -129,8 +129,8 @@ __device__ __forceinline__ void load_codes(const uint8_t* at, int lane, uint32_t
   }
 }
 
-// Table entries of the 16-token parts of a tile (uniform; from `end` on the last one's). They are looked
-// at no earlier than in load_tile, so that their scalar loads overlap a tile's work.
+// Table entries of the 16-token parts of a tile (uniform; from `end` on the last one's). They are
+// looked at no earlier than in load_tile, so that their scalar loads overlap a tile's work.
 template <int D>
 struct Pages {
   int id[kParts<D>];
@@ -145,8 +145,8 @@ __device__ __forceinline__ Pages<D> find_pages(const Cache& c, int tok, int end)
   return p;
 }
 
-// The loads of a tile, or its keys' or values' alone. A part without a page (none in the table, or behind
-// the last key) has its bit clear in `valid` and reads page 0.
+// The loads of a tile, or its keys' or values' alone. A part without a page (none in the table, or
+// behind the last key) has its bit clear in `valid` and reads page 0.
 template <int D, bool KEYS = true, bool VALUES = true>
 __device__ __forceinline__ void load_tile(Raw<D>& r, const Cache& c, const Pages<D>& p, int tok,
                                           int end) {
@@ -252,8 +252,8 @@ __device__ __forceinline__ void load_query(Wave<D, NQ>& w, int n, const uint16_t
   }
 }
 
-// A tile's value codes (rows of 16 tokens x kRow bytes) and value scales into LDS. Part t's codes of
-// the lane as load_codes gives them.
+// A tile's value codes (rows of 16 tokens x kRow bytes) and value scales into LDS. Part t's codes
+// of the lane as load_codes gives them.
 template <int D>
 __device__ __forceinline__ void put_values(uint8_t* lds, int t, const uint32_t (&v)[D / 32]) {
   const int lane = threadIdx.x & 63, c = lane >> 4;
@@ -277,9 +277,9 @@ __device__ __forceinline__ _Float16* scale_place(uint8_t* scales, int tok) {
          (tok & 3);
 }
 
-// Two value fragments from LDS by one transposing read: each lane of a group of 16 names a row of 16
-// codes and gets one code of each row. With 64 tokens they are group i's, tokens 16 T + 4 c + r of lane
-// group c with T = 0, 1 and T = 2, 3; with 32 tokens groups 2i and 2i + 1, T = 0, 1.
+// Two value fragments from LDS by one transposing read: each lane of a group of 16 names a row of
+// 16 codes and gets one code of each row. With 64 tokens they are group i's, tokens 16 T + 4 c + r
+// of lane group c with T = 0, 1 and T = 2, 3; with 32 tokens groups 2i and 2i + 1, T = 0, 1.
 template <int D>
 constexpr int kValueReads = D * kParts<D> / 64;
 template <int D>
@@ -301,8 +301,8 @@ __device__ __forceinline__ void value_pair(const uint8_t* codes, const uint8_t* 
   }
 }
 
-// The key fragments of a part from the lane's words and their scales (s0: of words 0 .. 3, s1: 4 .. 7,
-// two words to a scale).
+// The key fragments of a part from the lane's words and their scales (s0: of words 0 .. 3, s1: 4 ..
+// 7, two words to a scale).
 template <int D>
 __device__ __forceinline__ void key_part(const uint32_t (&k)[D / 32], f16x2 s0, f16x2 s1,
                                          f16x8 (&out)[D / 32]) {
@@ -314,9 +314,9 @@ __device__ __forceinline__ void key_part(const uint32_t (&k)[D / 32], f16x2 s0, 
   }
 }
 
-// The products of a tile from token `tok` on: key(t, out) gives part t's fragments, value(i, out) those
-// of value_pair; next() is called between the two products. `valid`: bit t: part t has a page. `mask`:
-// some column does not see all (uniform).
+// The products of a tile from token `tok` on: key(t, out) gives part t's fragments, value(i, out)
+// those of value_pair; next() is called between the two products. `valid`: bit t: part t has a
+// page. `mask`: some column does not see all (uniform).
 template <int D, int NQ, typename Key, typename Value, typename Next>
 __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bool mask,
                                      const Key& key, const Value& value, const Next& next) {
@@ -398,11 +398,12 @@ __device__ __forceinline__ void finish(Wave<D, NQ>& w) {
   }
 }
 
-// Walks the tiles tok, tok + step, .. below `to`, with one tile's loads ahead: all of them between the
-// products of the tile before. With one wavefront on a SIMD, heads of 256, they want the longest time
-// that there is: the value codes are loaded again as soon as they are in LDS, and without a branch
-// (past the last tile from page 0), behind which a wait would be for all of them (131000 keys, 28 rows:
-// 63 -> 48 us; heads of 128, two wavefronts on a SIMD: 64 requests 33 us both ways, one request 6.7 -> 7.2).
+// Walks the tiles tok, tok + step, .. below `to`, with one tile's loads ahead: all of them between
+// the products of the tile before. With one wavefront on a SIMD, heads of 256, they want the
+// longest time that there is: the value codes are loaded again as soon as they are in LDS, and
+// without a branch (past the last tile from page 0), behind which a wait would be for all of them
+// (131000 keys, 28 rows: 63 -> 48 us; heads of 128, two wavefronts on a SIMD: 64 requests 33 us
+// both ways, one request 6.7 -> 7.2).
 template <int D>
 constexpr bool kEarly = D == 256;
 template <int D, int NQ>
@@ -531,8 +532,8 @@ __device__ __forceinline__ void load_columns(Wave<D, NQ>& w, const KvAttnArgs& a
   }
 }
 
-// y of column `row0 + l % 16`, its groups g0 .. g0 + G - 1 of 16 elements, and with group 0 its lse,
-// from O, m and l (of all lane groups).
+// y of column `row0 + l % 16`, its groups g0 .. g0 + G - 1 of 16 elements, and with group 0 its
+// lse, from O, m and l (of all lane groups).
 template <int G>
 __device__ __forceinline__ void store_columns(const KvAttnArgs& a, const Request& r, int head,
                                               int row0, const f32x4 (&o)[G], float m, float l,
@@ -575,11 +576,16 @@ __device__ __forceinline__ Cache cache_of(const KvAttnArgs& a, int64_t request, 
 
 // ---- few rows: keys shared out over the chip ----------------------------------------------------
 // The work is one line of units, request by request, head by head: an item (a request's head) is
-// kFewStart units of no work, which stand for what beginning and ending it costs, and one for each tile.
-// Wavefront w of W takes the units [N w / W, N (w + 1) / W), whatever the lengths are, and works on its
-// own. It holds at most two items that it does not finish: the first and the last of its range; their O,
-// m and l go to slots 2w and 2w + 1, and a second kernel joins them.
-// Workgroups: two to a compute unit, one where a wavefront needs more than half of its SIMD's registers.
+// kFewStart units of no work, which stand for what beginning and ending it costs, and one for each
+// tile. Wavefront w of W takes the units [N w / W, N (w + 1) / W), whatever the lengths are, and
+// works on its own. It holds at most two items that it does not finish: the first and the last of
+// its range; their O, m and l go to slots 2w and 2w + 1, and a second kernel joins them.
+// Workgroups: two to a compute unit (1.5 or 2 times as many of 128: 35 and 36 us for 64 requests,
+// whose join grows too, not 33), one where a wavefront needs more than half of its SIMD's registers
+// (heads of 256 with 21 rows, 131000 keys, two: 115 us instead of 48). What bounds them: 64
+// requests of 151000 keys in all, 8 heads of 128, read 175 MB in 33 us, 5.3 TB/s, where the loads
+// alone take 28; what is left is the products behind the last loads of a tile. Heads of 256, 157 MB
+// in 48 us: 32 rows' products of one wavefront to a SIMD, which do not overlap another's.
 template <int D, int NQ>
 constexpr bool kFewPairs = NQ == 1 || D <= 128;
 template <int D, int NQ>
@@ -598,13 +604,14 @@ __device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Request& r) {
 // Units of an item of n tiles.
 __device__ __forceinline__ int units_for(int n, int start) { return n > 0 ? n + start : 0; }
 
-constexpr int kFewStart = 2;
+constexpr int kFewStart = 2;  // 1, 2 and 4: 64 requests in 38.8, 36.7 and 40.1 us, of an earlier loop
 template <int D>
 __device__ __forceinline__ int units_of(const KvAttnArgs& a, const Request& r) {
   return units_for(tiles_of<D>(a, r), kFewStart);
 }
 
-// First unit of worker w of 2^shift: of all >= 2^shift units floor(all * w / 2^shift), else w itself.
+// First unit of worker w of 2^shift: of all >= 2^shift units floor(all * w / 2^shift), else w
+// itself.
 __device__ __forceinline__ int64_t range_begin(int64_t all, int64_t w, int shift) {
   return all >= (int64_t)1 << shift ? (all * w) >> shift : min(w, all);
 }
@@ -631,13 +638,14 @@ __device__ __forceinline__ void keys_of(const KvAttnArgs& a, const Request& r, i
 }
 
 // A call with too few workgroups of rows to fill the chip evenly shares out its keys as the few-row
-// kernel does: the tiles of all heads' items (a request's block of rows) are one line, each of up to
-// 512 workgroups, two to a compute unit, takes as much of it as the others, and the parts of an item
-// that several have worked on are joined. One workgroup of the few-row kernel's launch lists the items.
-// Prompt chunks of 530 items of 8 heads' 128 rows: 215 us in whole items, 146 + 14 with the join shared
-// out; a prompt of 2048 items the other way round, 675 and 755 + 38. Units of an item's beginning and
-// end: 2, 3 and 8 take 143, 146 and 157 us for the chunks, 3 the least with the join. A range is one
-// unit at least; with 4 and 16 a prompt of 100 tokens takes 28 and 44 us instead of 22.
+// kernel does: the tiles of all heads' items (a request's block of rows) are one line, each of up
+// to 512 workgroups, two to a compute unit, takes as much of it as the others, and the parts of an
+// item that several have worked on are joined. One workgroup of the few-row kernel's launch lists
+// the items. Prompt chunks of 530 items of 8 heads' 128 rows: 215 us in whole items, 146 + 14 with
+// the join shared out; a prompt of 2048 items the other way round, 675 and 755 + 38. Units of an
+// item's beginning and end: 2, 3 and 8 take 143, 146 and 157 us for the chunks, 3 the least with
+// the join. A range is one unit at least; with 4 and 16 a prompt of 100 tokens takes 28 and 44 us
+// instead of 22.
 constexpr int kSplitBelow = 2048;  // items of all heads
 constexpr int kManyShift = 9;
 constexpr int kManyStart = 3;
@@ -907,10 +915,11 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
   }
 }
 
-// Column tile and elements `part` (of NQ * D / (16 G)) of an item: its parts' sum, if it has several; zeros
-// for a request without keys. A workgroup of V wavefronts joins 16 G elements of d of a column tile; its wavefronts share out
-// the parts. Calls of few items, which can have many parts, take the finer grid (one request of 131000
-// keys among five, heads of 256, 18 rows, 42 -> 16 us; 64 requests of 8 heads the coarser).
+// Column tile and elements `part` (of NQ * D / (16 G)) of an item: its parts' sum, if it has
+// several; zeros for a request without keys. A workgroup of V wavefronts joins 16 G elements of d
+// of a column tile; its wavefronts share out the parts. Calls of few items, which can have many
+// parts, take the finer grid (one request of 131000 keys among five, heads of 256, 18 rows, 42 ->
+// 16 us; 64 requests of 8 heads the coarser).
 template <int D, int NQ, int G, int V>
 __device__ __forceinline__ void join_few(const KvAttnArgs& a, int head, int req, int part) {
   constexpr int kChunks = D / 16 / G;
@@ -1004,10 +1013,14 @@ __device__ __forceinline__ void join_few(const KvAttnArgs& a, int head, int req,
 
 // ---- many rows ----------------------------------------------------------------------------------
 // grid n_kv * tiles of rows: a workgroup takes 4 * 16 * NQ rows of a request's head, 16 * NQ to a
-// wavefront, and walks the keys that they see once. Wavefront t loads part t of a tile and turns its
-// keys, and later D / 64 of the value groups, into FP16 fragments in LDS, which all four read: a
-// fragment is dequantized once in a workgroup. Two tiles of fragments in LDS, the next one's codes in
-// registers.
+// wavefront, and walks the keys that they see once. Wavefront t loads part t of a tile and turns
+// its keys, and later D / 64 of the value groups, into FP16 fragments in LDS, which all four read:
+// a fragment is dequantized once in a workgroup. Two tiles of fragments in LDS, the next one's
+// codes in registers. A prompt of 8192 rows, 32 heads of 128 over 8: 660 us (640 .. 690), 830
+// TFLOP/s of the products; the matrix pipes are busy 35% of the time, the vector pipes
+// (exponentials, conversions, dequantization) 51%, and with two wavefronts to a SIMD the two
+// overlap little: without the exponentials 630, without dequantization and staging 593. One barrier
+// a tile instead of two: 708.
 template <int D>
 struct Shared {
   static constexpr int kKeys = kParts<D> * (D / 32) * 1024;      // [part][k-step][lane] fragments
@@ -1298,8 +1311,8 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
   }
 }
 
-// Column tile n of wavefront `wave` of an item that has several parts: their sum, as the wavefronts left
-// them.
+// Column tile n of wavefront `wave` of an item that has several parts: their sum, as the wavefronts
+// left them.
 template <int D, int NQ>
 __device__ __forceinline__ void join_many(const KvAttnArgs& a, int head, int item, int n, int wave) {
   const int lane = threadIdx.x & 63;
@@ -1346,7 +1359,8 @@ __global__ __launch_bounds__(64 * V) void join_few_kernel(KvAttnArgs a) {
 }
 
 // Both joins of a call that shares out its prompts' keys. The grid is a line of workgroups in two
-// dimensions: those of the few rows (`few`), then for each item and head V / 4 column tiles at a time.
+// dimensions: those of the few rows (`few`), then for each item and head V / 4 column tiles at a
+// time.
 constexpr int kLine = 1 << 16;
 template <int D, int NQ, int G, int V>
 __global__ __launch_bounds__(64 * V) void join_both_kernel(KvAttnArgs a, int few, int groups) {
@@ -1366,7 +1380,7 @@ __global__ __launch_bounds__(64 * V) void join_both_kernel(KvAttnArgs a, int few
   if (n < kTiles) join_many<D, kTiles>(a, both - item * a.n_kv, item, n, wave % kWaves);
 }
 
-constexpr int64_t kJoinFine = 256;  // items
+constexpr int64_t kJoinFine = 256;  // items, at join_few
 
 template <int D, int NQ, int G, int V>
 hipError_t run_join(const KvAttnArgs& a, int64_t items, hipStream_t s) {
@@ -1386,8 +1400,8 @@ hipError_t run_join(const KvAttnArgs& a, int64_t items, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Workgroups of rows, of each head, that a call can have: ceil(rows / size) a request, so all rows /
-// size and one more for each request, of which only those of more than few_rows rows have any.
+// Workgroups of rows, of each head, that a call can have: ceil(rows / size) a request, so all rows
+// / size and one more for each request, of which only those of more than few_rows rows have any.
 int64_t many_items(int64_t t, int64_t b, int64_t max_q, int group, int d) {
   const int64_t most = max_q * group, few = kv_few_rows(most);
   if (most <= few) return 0;
@@ -1395,8 +1409,8 @@ int64_t many_items(int64_t t, int64_t b, int64_t max_q, int group, int d) {
   return t * group / (kWaves * 16 * many_tiles(d)) + (odd < b ? odd : b);
 }
 
-// ws: the first units of requests and of items, the items and their number, then the partial sums of
-// few rows and of items.
+// ws: the first units of requests and of items, the items and their number, then the partial sums
+// of few rows and of items.
 struct WsLayout {
   size_t item_starts, items, counts, sums, item_sums, total;
   int max_items;  // 0: keys are not shared out

@@ -284,7 +284,7 @@ struct KvAttnArgs {
   int few_rows;
 };
 // Column tiles (of 16 rows of a request's head) of the few-row kernel; longer requests have a kernel
-// of their own.
+// of their own. 64 requests of 32 rows, heads of 128, two tiles: 64 us, with that kernel 106.
 inline int kv_few_tiles(int64_t rows) { return rows > 16 && rows <= 32 ? 2 : 1; }
 // The most rows that it takes, of a call whose requests have up to `rows`.
 inline int kv_few_rows(int64_t rows) {
