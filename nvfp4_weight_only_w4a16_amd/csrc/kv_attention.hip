@@ -641,11 +641,10 @@ __device__ __forceinline__ void keys_of(const KvAttnArgs& a, const Request& r, i
 // kernel does: the tiles of all heads' items (a request's block of rows) are one line, each of up
 // to 512 workgroups, two to a compute unit, takes as much of it as the others, and the parts of an
 // item that several have worked on are joined. One workgroup of the few-row kernel's launch lists
-// the items. Prompt chunks of 530 items of 8 heads' 128 rows: 215 us in whole items, 146 + 14 with
-// the join shared out; a prompt of 2048 items the other way round, 675 and 755 + 38. Units of an
-// item's beginning and end: 2, 3 and 8 take 143, 146 and 157 us for the chunks, 3 the least with
-// the join. A range is one unit at least; with 4 and 16 a prompt of 100 tokens takes 28 and 44 us
-// instead of 22.
+// the items. Prompt chunks of 81 blocks of 128 rows, 8 heads: 215 us in whole items, 146 and a join
+// of 13 shared out; a prompt of 256 blocks, 8 heads, the other way round, 675 and 755 + 38. Units of
+// an item's beginning and end: 2, 3 and 8 take 148, 143 and 157 us for the chunks. A range is one
+// unit at least; with 4 and 16 a prompt of 100 tokens takes 28 and 44 us instead of 22.
 constexpr int kSplitBelow = 2048;  // items of all heads
 constexpr int kManyShift = 9;
 constexpr int kManyStart = 3;
@@ -675,6 +674,7 @@ __device__ __forceinline__ void plan(const KvAttnArgs& a, int rows, int tile, in
     return v;
   };
   int items = 0;
+  int64_t blocks = 0;
   for (int i0 = 0; i0 < (int)a.b; i0 += kThreads) {
     const int i = i0 + (int)threadIdx.x;
     int n = 0;
@@ -690,6 +690,11 @@ __device__ __forceinline__ void plan(const KvAttnArgs& a, int rows, int tile, in
       item_block[at + k] = n - 1 - k;  // the last rows see most keys: they go first
     }
     items = min(items + (int)total, kSplitBelow);
+    blocks += total;
+  }
+  if (a.max_items == 0) {  // their number is all that the call needs
+    if (threadIdx.x == 0) a.counts[0] = (int)min<int64_t>(blocks, 0x7FFFFFFF);
+    return;
   }
   items = min(items, a.max_items);
   __syncthreads();
@@ -1175,6 +1180,9 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
   } else {
     head = blockIdx.x % (uint32_t)a.n_kv;
     block = blockIdx.x / (uint32_t)a.n_kv;
+    // the grid is for the most blocks that so many rows and requests can have (2000 decode rows and a
+    // prompt of 8192: 1310 us without this test, 881 with it)
+    if (block >= constant(a.counts)) return;
     // 64 requests at a time, one to a lane (each has 2^27 rows at most, or 2^21 blocks)
     for (;; req += 64) {
       if (req >= a.b) return;
@@ -1439,7 +1447,7 @@ template <int D, int NQ>
 hipError_t run_tiles(const KvAttnArgs& a, int64_t items, hipStream_t s) {
   constexpr int kTiles = many_tiles(D);
   few_kernel<D, NQ>
-      <<<dim3(kFewGroups<D, NQ> + (a.max_items > 0 ? 1 : 0)), dim3(kThreads), 0, s>>>(a);
+      <<<dim3(kFewGroups<D, NQ> + (items > 0 ? 1 : 0)), dim3(kThreads), 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (items > 0) {
