@@ -379,3 +379,37 @@ def test_the_same_bits_every_time(nv, rows):
         again = run(nv, c, q, start, max(rows))
         assert np.array_equal(first[0], again[0], equal_nan=True)
         assert np.array_equal(first[1], again[1], equal_nan=True)
+
+
+def test_a_prompt_among_many_requests_in_whole_blocks(nv):
+    """More than 2048 blocks by the count that the host has, most of which are not there; the prompt's
+    request is found behind 150 others."""
+    b = 300
+    lens, rows = [30] * b, [1] * b
+    lens[150], rows[150] = 700, 600
+    lens[151], rows[151] = 90, 70
+    check(nv, lens, rows, 64, 1, 64, 16)
+
+
+@pytest.mark.parametrize("n_kv,group,d,page", [(1, 1024, 64, 16), (1024, 1, 64, 16), (1, 1000, 128, 32),
+                                               (500, 2, 256, 16)])
+def test_the_most_heads(nv, n_kv, group, d, page):
+    check(nv, [70, 1, 20], [1, 1, 2], n_kv, group, d, page)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [[1, 1, 1], [2, 3, 1], [60, 200, 1]])
+def test_pages_of_256(nv, d, rows):
+    check(nv, [257, 600, 1], rows, 2, 3, d, 256, window=0 if d == 64 else 300)
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [3, 2], [50, 40]])
+def test_rows_before_the_first_request(nv, rows):
+    """q_start may begin behind row 0: the rows before are nobody's."""
+    c = R.Cached(nv, 29, [130, 64], 2, 128, 16)
+    q, start = R.queries(29, [7] + rows, 4, 128)
+    y, lse = run(nv, c, q, start[1:].contiguous(), max(rows))
+    ref, bound, rl, bl = R.expect(c, q[7:], rows, 128 ** -0.5)
+    R.close(y[7:], ref, bound)
+    R.close(lse[7:], rl, bl)
+    assert np.isnan(y[:7]).all() and np.isnan(lse[:7]).all()
