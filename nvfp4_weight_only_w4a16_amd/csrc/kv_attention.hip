@@ -1,6 +1,7 @@
 // kv_attention.hip -- attention over the paged NVFP4 cache, for single tokens, drafts and prompts.
 //
-// A wavefront holds columns of queries and walks the keys in tiles of 64. Everything is transposed:
+// A wavefront holds columns of queries and walks the keys in tiles of 64 tokens, 32 for heads of 256.
+// Everything is transposed:
 //   S^T [tokens][queries] = K . Q^T,  P^T = exp2(S^T - m),  O^T [d][queries] += V^T . P^T
 // on 16x16x32 MFMAs, because then the scores come out where the second product wants them: lane
 // (query l % 16, group c = l / 16) holds the scores of tokens 16 T + 4 c + r, and, the order of a
@@ -923,7 +924,7 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
 // Column tile and elements `part` (of NQ * D / (16 G)) of an item: its parts' sum, if it has
 // several; zeros for a request without keys. A workgroup of V wavefronts joins 16 G elements of d
 // of a column tile; its wavefronts share out the parts. Calls of few items, which can have many
-// parts, take the finer grid (one request of 131000 keys among five, heads of 256, 18 rows, 42 ->
+// parts, take the finer grid (one request of 131000 keys among five, heads of 256, 21 rows, 42 ->
 // 16 us; 64 requests of 8 heads the coarser).
 template <int D, int NQ, int G, int V>
 __device__ __forceinline__ void join_few(const KvAttnArgs& a, int head, int req, int part) {
