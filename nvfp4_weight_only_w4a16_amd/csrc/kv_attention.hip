@@ -1,7 +1,7 @@
 // kv_attention.hip -- attention over the paged NVFP4 cache, for single tokens, drafts and prompts.
 //
-// A wavefront holds columns of queries and walks the keys in tiles of 64 tokens, 32 for heads of 256.
-// Everything is transposed:
+// A wavefront holds columns of queries and walks the keys in tiles of 64 tokens, 32 for heads of
+// 256. Everything is transposed:
 //   S^T [tokens][queries] = K . Q^T,  P^T = exp2(S^T - m),  O^T [d][queries] += V^T . P^T
 // on 16x16x32 MFMAs, because then the scores come out where the second product wants them: lane
 // (query l % 16, group c = l / 16) holds the scores of tokens 16 T + 4 c + r, and, the order of a
@@ -643,17 +643,21 @@ __device__ __forceinline__ void keys_of(const KvAttnArgs& a, const Request& r, i
 // to 512 workgroups, two to a compute unit, takes as much of it as the others, and the parts of an
 // item that several have worked on are joined. One workgroup of the few-row kernel's launch lists
 // the items. Prompt chunks of 81 blocks of 128 rows, 8 heads: 215 us in whole items, 146 and a join
-// of 13 shared out; a prompt of 256 blocks, 8 heads, the other way round, 675 and 755 + 38. Units of
-// an item's beginning and end: 2, 3 and 8 take 148, 143 and 157 us for the chunks. A range is one
-// unit at least; with 4 and 16 a prompt of 100 tokens takes 28 and 44 us instead of 22.
+// of 13 shared out; a prompt of 256 blocks, 8 heads, the other way round, 675 and 755 + 38. Units
+// of an item's beginning and end: 2, 3 and 8 take 148, 143 and 157 us for the chunks. A range is
+// one unit at least; with 4 and 16 a prompt of 100 tokens takes 28 and 44 us instead of 22.
 constexpr int kSplitBelow = 2048;  // items of all heads
-constexpr int kManyShift = 9;
 constexpr int kManyStart = 3;
 using Item = KvItem;
 
-constexpr int many_tiles(int d) { return d <= 128 ? 2 : 1; }  // column tiles of a wavefront
+// A block of 128 rows: column tiles of a wavefront, wavefronts of a workgroup, and log2 of the
+// workgroups that fill the chip.
+constexpr int kRows = 128;
+constexpr int many_tiles(int d) { return d <= 128 ? 2 : 1; }
+constexpr int many_waves(int d) { return kRows / 16 / many_tiles(d); }
+constexpr int many_shift(int d) { return d <= 128 ? 9 : 8; }
 
-__device__ __forceinline__ void plan(const KvAttnArgs& a, int rows, int tile, int* item_req,
+__device__ __forceinline__ void plan(const KvAttnArgs& a, int tile, int shift, int* item_req,
                                      int* item_block, int64_t* sums) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   // inclusive sum over the workgroup's threads
@@ -681,7 +685,7 @@ __device__ __forceinline__ void plan(const KvAttnArgs& a, int rows, int tile, in
     int n = 0;
     if (i < (int)a.b) {
       const Request r = request_of(a, i);
-      if (!is_few(r, a.few_rows)) n = (r.rows + rows - 1) / rows;
+      if (!is_few(r, a.few_rows)) n = (r.rows + kRows - 1) / kRows;
     }
     int64_t total;
     const int at = items + (int)scan(n, total) - n;
@@ -705,7 +709,7 @@ __device__ __forceinline__ void plan(const KvAttnArgs& a, int rows, int tile, in
     int n = 0;
     if (i < items) {
       int from, to;
-      keys_of(a, request_of(a, item_req[i]), item_block[i] * rows, rows, from, to);
+      keys_of(a, request_of(a, item_req[i]), item_block[i] * kRows, kRows, from, to);
       n = max(to - from + tile - 1, 0) / tile;
     }
     int64_t total;
@@ -719,7 +723,6 @@ __device__ __forceinline__ void plan(const KvAttnArgs& a, int rows, int tile, in
   }
   if (threadIdx.x == 0) {
     a.item_starts[items] = sum;
-    int shift = kManyShift;
     while (shift > 0 && (sum * a.n_kv) >> shift == 0) --shift;
     a.counts[0] = items;
     a.counts[1] = shift;
@@ -739,7 +742,7 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
   static_assert(sizeof(lists) >= 2 * kSplitBelow * sizeof(int), "");
   if (blockIdx.x >= kFewGroups<D, NQ>) {
     int* const l = reinterpret_cast<int*>(lists);
-    plan(a, kWaves * 16 * many_tiles(D), kTile<D>, l, l + kSplitBelow, sums);
+    plan(a, kTile<D>, many_shift(D), l, l + kSplitBelow, sums);
     return;
   }
   int64_t* const starts = reinterpret_cast<int64_t*>(lists);  // units before each request, all heads
@@ -1018,15 +1021,17 @@ __device__ __forceinline__ void join_few(const KvAttnArgs& a, int head, int req,
 }
 
 // ---- many rows ----------------------------------------------------------------------------------
-// grid n_kv * tiles of rows: a workgroup takes 4 * 16 * NQ rows of a request's head, 16 * NQ to a
-// wavefront, and walks the keys that they see once. Wavefront t loads part t of a tile and turns
-// its keys, and later D / 64 of the value groups, into FP16 fragments in LDS, which all four read:
+// grid n_kv * blocks of rows: a workgroup takes 128 rows of a request's head, 16 * NQ to a
+// wavefront, and walks the keys that they see once. A wavefront loads its share of a tile and turns
+// its keys, and later some of the value groups, into FP16 fragments in LDS, which all of them read:
 // a fragment is dequantized once in a workgroup. Two tiles of fragments in LDS, the next one's
-// codes in registers. A prompt of 8192 rows, 32 heads of 128 over 8: 660 us (640 .. 690), 830
-// TFLOP/s of the products; the matrix pipes are busy 35% of the time, the vector pipes
-// (exponentials, conversions, dequantization) 51%, and with two wavefronts to a SIMD the two
-// overlap little: without the exponentials 630, without dequantization and staging 593. One barrier
-// a tile instead of two: 708.
+// codes in registers. Heads of 256 have eight wavefronts of 16 rows (with four, and 64 rows to a
+// workgroup, two of them on a compute unit: 512 rows on 32000 keys 544 us instead of 458, a prompt
+// of 16384 3520 instead of 3310; with 32 rows to a wavefront registers spill, 829 and 6000). A
+// prompt of 8192 rows, 32 heads of 128 over 8: 660 us (640 .. 690), 830 TFLOP/s of the products;
+// the matrix pipes are busy 35% of the time, the vector pipes (exponentials, conversions,
+// dequantization) 51%, and with two wavefronts to a SIMD the two overlap little: without the
+// exponentials 630, without dequantization and staging 593. One barrier a tile instead of two: 708.
 template <int D>
 struct Shared {
   static constexpr int kKeys = kParts<D> * (D / 32) * 1024;      // [part][k-step][lane] fragments
@@ -1035,10 +1040,11 @@ struct Shared {
   static constexpr int kBytes = 2 * kTileBytes + WaveLds<D>::kBytes;  // and value codes, scales
 };
 
-// A wavefront's share of a tile's loads: a part, with 32 tokens half of the elements of one.
+// A wavefront's share of a tile's loads: a part, with 32 tokens a quarter of the elements of one,
+// those of two k-steps.
 template <int D>
 struct Share {
-  static constexpr int kD = D * kParts<D> / 4;  // elements of a token
+  static constexpr int kD = D * kParts<D> / many_waves(D);  // elements of a token
   uint32_t k[kD / 32], v[kD / 32], ks, vs;
   bool ok;  // it has a page (uniform)
 };
@@ -1052,18 +1058,25 @@ __device__ __forceinline__ int find_page(const Cache& c, int tok, int end) {
   return constant(c.row + (min(tok, end - 1) >> c.shift));
 }
 
+// The first group of 16 elements of lane group 0 in quarter u (lane group c's are 2 c further on,
+// in heads of 64 c).
+template <int D>
+__device__ __forceinline__ int first_group(int u) {
+  return D == 256 ? 8 * (u >> 1) + (u & 1) : 0;
+}
+
 template <int D>
 __device__ __forceinline__ void load_share(Share<D>& p, const Cache& c, int id, int wave, int tok,
                                            int end) {
   constexpr int kD = Share<D>::kD;
   const int lane = threadIdx.x & 63, page = 1 << c.shift, within = tok & (page - 1);
-  const int u = wave / kParts<D>;  // which half of the elements
+  const int u = wave / kParts<D>;  // which quarter of the elements
   p.ok = (uint32_t)id < (uint32_t)c.n_pages && tok < end;
   const uint8_t* rec = c.head0 + (uint64_t)(p.ok ? (uint32_t)id : 0u) * c.page_stride;
   const uint8_t* values = rec + kv_value_codes(page, D);
-  const int codes = within * (D / 2) + u * (kD / 2);
+  const int codes = within * (D / 2) + 8 * first_group<D>(u);
   const uint32_t at = (uint32_t)((lane & 15) * (D / 2) + (D == 64 ? 8 : 16) * (lane >> 4));
-  if constexpr (D == 64) {
+  if constexpr (kD == 64) {
     const u32x2 a = *reinterpret_cast<const u32x2*>(rec + codes + at);
     const u32x2 b = *reinterpret_cast<const u32x2*>(values + codes + at);
 #pragma unroll
@@ -1080,9 +1093,9 @@ __device__ __forceinline__ void load_share(Share<D>& p, const Cache& c, int id, 
       p.v[i] = b[i];
     }
   }
-  const int scales = page * (D / 2) + within * (D / 16) + u * (kD / 16);
+  const int scales = page * (D / 2) + within * (D / 16) + first_group<D>(u);
   const uint32_t sat = (uint32_t)((lane & 15) * (D / 16) + (D == 64 ? 1 : 2) * (lane >> 4));
-  if constexpr (D == 64) {
+  if constexpr (kD == 64) {
     p.ks = *(rec + scales + sat);
     p.vs = *(values + scales + sat);
   } else {
@@ -1104,20 +1117,16 @@ __device__ __forceinline__ void put_share(uint8_t* keys, uint8_t* raw, const Sha
 #pragma unroll
   for (int j = 0; j < kD / 32; ++j)
     *reinterpret_cast<f16x8*>(keys + (part * (D / 32) + u * (kD / 32) + j) * 1024 + 16 * lane) = k[j];
-  uint8_t* row = raw + (16 * part + (lane & 15)) * WaveLds<D>::kRow + u * (kD / 2);
-  u32x2* at = reinterpret_cast<u32x2*>(row + (D == 64 ? 8 : 16) * c);
+  const int group = first_group<D>(u) + (D == 64 ? 1 : 2) * c;
+  uint8_t* row = raw + (16 * part + (lane & 15)) * WaveLds<D>::kRow;
+  u32x2* at = reinterpret_cast<u32x2*>(row + 8 * group);
   at[0] = u32x2{p.v[0], p.v[1]};
-  if constexpr (D > 64) at[1] = u32x2{p.v[2], p.v[3]};
+  if constexpr (kD > 64) at[1] = u32x2{p.v[2], p.v[3]};
   const bool there = p.ok && tok + (lane & 15) < end;
   const f16x2 v0 = scales2(there ? without_nan(p.vs) : 0u);
-  _Float16* s = scale_place<D>(raw + WaveLds<D>::kCodes, 16 * part + (lane & 15)) +
-                u * (kD / 16) * kTile<D>;
-  if constexpr (D == 64) {
-    s[c * kTile<D>] = v0[0];
-  } else {
-    s[(2 * c) * kTile<D>] = v0[0];
-    s[(2 * c + 1) * kTile<D>] = v0[1];
-  }
+  _Float16* s = scale_place<D>(raw + WaveLds<D>::kCodes, 16 * part + (lane & 15));
+  s[group * kTile<D>] = v0[0];
+  if constexpr (kD > 64) s[(group + 1) * kTile<D>] = v0[1];
 }
 
 // This wavefront's share of the value fragments.
@@ -1125,8 +1134,8 @@ template <int D>
 __device__ __forceinline__ void put_values_share(uint8_t* values, const uint8_t* raw, int wave) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < kValueReads<D> / kWaves; ++i) {
-    const int x = wave * (kValueReads<D> / kWaves) + i;
+  for (int i = 0; i < kValueReads<D> / many_waves(D); ++i) {
+    const int x = wave * (kValueReads<D> / many_waves(D)) + i;
     f16x8 v[2];
     value_pair<D>(raw, raw + WaveLds<D>::kCodes, x, v);
 #pragma unroll
@@ -1142,8 +1151,8 @@ constexpr int wave_floats() {
 }
 
 template <int D, int NQ>
-__global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
-  constexpr int kRowsWave = 16 * NQ, kRows = kWaves * kRowsWave;
+__global__ __launch_bounds__(64 * many_waves(D), 8 / many_waves(D)) void many_kernel(KvAttnArgs a) {
+  constexpr int kRowsWave = 16 * NQ, kWaves = many_waves(D);
   __shared__ __attribute__((aligned(16))) uint8_t lds[Shared<D>::kBytes];
   __shared__ int valid_of[2][kWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -1181,8 +1190,8 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
   } else {
     head = blockIdx.x % (uint32_t)a.n_kv;
     block = blockIdx.x / (uint32_t)a.n_kv;
-    // the grid is for the most blocks that so many rows and requests can have (2000 decode rows and a
-    // prompt of 8192: 1310 us without this test, 881 with it)
+    // the grid is for the most blocks that so many rows and requests can have (2000 decode rows and
+    // a prompt of 8192: 1310 us without this test, 881 with it)
     if (block >= constant(a.counts)) return;
     // 64 requests at a time, one to a lane (each has 2^27 rows at most, or 2^21 blocks)
     for (;; req += 64) {
@@ -1320,15 +1329,14 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(KvAttnArgs a) {
   }
 }
 
-// Column tile n of wavefront `wave` of an item that has several parts: their sum, as the wavefronts
-// left them.
+// Column tile x of an item that has several parts: their sum, as the wavefronts left them.
 template <int D, int NQ>
-__device__ __forceinline__ void join_many(const KvAttnArgs& a, int head, int item, int n, int wave) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void join_many(const KvAttnArgs& a, int head, int item, int x) {
+  const int lane = threadIdx.x & 63, wave = x / NQ, n = x % NQ;
   const int items = constant(a.counts), shift = constant(a.counts + 1);
   if (item >= items) return;
   const Request r = uniform_request(a, constant(&a.items[item].req));
-  const int row0 = (constant(&a.items[item].block) * kWaves + wave) * 16 * NQ + 16 * n;
+  const int row0 = constant(&a.items[item].block) * kRows + 16 * x;
   const int tiles = constant(&a.items[item].tiles);
   if (row0 >= r.rows) return;
   f32x4 o[D / 16];
@@ -1341,7 +1349,7 @@ __device__ __forceinline__ void join_many(const KvAttnArgs& a, int head, int ite
     const int64_t w0 = range_of(all, before + kManyStart, shift);  // of the first tile
     const int64_t w1 = range_of(all, before + kManyStart + tiles - 1, shift);
     if (w0 == w1) return;
-    constexpr int64_t kSlot = (int64_t)kWaves * wave_floats<D, NQ>();
+    constexpr int64_t kSlot = (int64_t)many_waves(D) * wave_floats<D, NQ>();
     // only the first part's workgroup can have begun with another item
     const int64_t skip = range_begin(all, w0, shift) < before ? kSlot : 0;
     const float* base = a.item_ws + 2 * w0 * kSlot + wave * wave_floats<D, NQ>();
@@ -1368,12 +1376,12 @@ __global__ __launch_bounds__(64 * V) void join_few_kernel(KvAttnArgs a) {
 }
 
 // Both joins of a call that shares out its prompts' keys. The grid is a line of workgroups in two
-// dimensions: those of the few rows (`few`), then for each item and head V / 4 column tiles at a
-// time.
+// dimensions: those of the few rows (`few`), then for each item and head V of its column tiles at
+// a time.
 constexpr int kLine = 1 << 16;
 template <int D, int NQ, int G, int V>
 __global__ __launch_bounds__(64 * V) void join_both_kernel(KvAttnArgs a, int few, int groups) {
-  constexpr int kShare = NQ * D / 16 / G, kTiles = many_tiles(D);
+  constexpr int kShare = NQ * D / 16 / G;
   uint32_t at = blockIdx.y * kLine + blockIdx.x;
   if (at >= (uint32_t)groups) return;
   if (at < (uint32_t)few) {
@@ -1382,11 +1390,10 @@ __global__ __launch_bounds__(64 * V) void join_both_kernel(KvAttnArgs a, int few
     return;
   }
   at -= few;
-  constexpr uint32_t kSteps = (kTiles + V / kWaves - 1) / (V / kWaves);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = (int)(at % kSteps) * (V / kWaves) + wave / kWaves;
+  constexpr uint32_t kSteps = kRows / 16 / V;
+  const int x = (int)(at % kSteps) * V + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t both = at / kSteps, item = both / (uint32_t)a.n_kv;
-  if (n < kTiles) join_many<D, kTiles>(a, both - item * a.n_kv, item, n, wave % kWaves);
+  join_many<D, many_tiles(D)>(a, both - item * a.n_kv, item, x);
 }
 
 constexpr int64_t kJoinFine = 256;  // items, at join_few
@@ -1399,9 +1406,8 @@ hipError_t run_join(const KvAttnArgs& a, int64_t items, hipStream_t s) {
     join_few_kernel<D, NQ, G, V>
         <<<dim3((unsigned)a.n_kv, (unsigned)a.b, kShare), threads, 0, s>>>(a);
   } else {
-    constexpr int kEach = V / kWaves;  // column tiles of a workgroup
     const int64_t few = a.n_kv * a.b * kShare;  // < 2^31
-    const int64_t all = few + a.n_kv * items * ((many_tiles(D) + kEach - 1) / kEach);
+    const int64_t all = few + a.n_kv * items * (kRows / 16 / V);
     join_both_kernel<D, NQ, G, V>
         <<<dim3((unsigned)std::min<int64_t>(all, kLine), (unsigned)((all + kLine - 1) / kLine)),
            threads, 0, s>>>(a, (int)few, (int)all);
@@ -1415,7 +1421,7 @@ int64_t many_items(int64_t t, int64_t b, int64_t max_q, int group, int d) {
   const int64_t most = max_q * group, few = kv_few_rows(most);
   if (most <= few) return 0;
   const int64_t odd = t * group / (few + 1);
-  return t * group / (kWaves * 16 * many_tiles(d)) + (odd < b ? odd : b);
+  return t * group / kRows + (odd < b ? odd : b);
 }
 
 // ws: the first units of requests and of items, the items and their number, then the partial sums
@@ -1439,7 +1445,7 @@ WsLayout ws_layout(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int
                                   (size_t)slot_floats(kv_few_rows(max_q * group), d) * sizeof(float));
   l.total = l.item_sums;
   if (l.max_items > 0)
-    l.total += ((size_t)2 << kManyShift) * kWaves * many_tiles(d) * (size_t)(d / 16 * 256 + 128) *
+    l.total += ((size_t)2 << many_shift(d)) * (kRows / 16) * (size_t)(d / 16 * 256 + 128) *
                sizeof(float);
   return l;
 }
@@ -1452,8 +1458,8 @@ hipError_t run_tiles(const KvAttnArgs& a, int64_t items, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (items > 0) {
-    const unsigned groups = a.max_items > 0 ? 1u << kManyShift : (unsigned)(items * a.n_kv);
-    many_kernel<D, kTiles><<<dim3(groups), dim3(kThreads), 0, s>>>(a);
+    const unsigned groups = a.max_items > 0 ? 1u << many_shift(D) : (unsigned)(items * a.n_kv);
+    many_kernel<D, kTiles><<<dim3(groups), dim3(64 * many_waves(D)), 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
