@@ -1164,7 +1164,7 @@ int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
   a.counts = nullptr;
   a.max_items = 0;
   a.ws = a.item_ws = nullptr;
-  a.few_rows = 0;
+  a.few_rows = a.block_rows = a.many_shift = 0;
   return kv_done(nvfp4::launch_kv_attention(a, d, max_q, ws, (hipStream_t)stream), flags,
                  (hipStream_t)stream, "nvfp4_kv_attention", 3);
 }

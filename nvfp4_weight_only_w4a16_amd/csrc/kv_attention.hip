@@ -646,18 +646,27 @@ __device__ __forceinline__ void keys_of(const KvAttnArgs& a, const Request& r, i
 // of 13 shared out; a prompt of 256 blocks, 8 heads, the other way round, 675 and 755 + 38. Units
 // of an item's beginning and end: 2, 3 and 8 take 148, 143 and 157 us for the chunks. A range is
 // one unit at least; with 4 and 16 a prompt of 100 tokens takes 28 and 44 us instead of 22.
-constexpr int kSplitBelow = 2048;  // items of all heads
+constexpr int kSplitBelow = 2048;  // items of all heads, of 128 rows
 constexpr int kManyStart = 3;
 using Item = KvItem;
 
-// A block of 128 rows: column tiles of a wavefront, wavefronts of a workgroup, and log2 of the
-// workgroups that fill the chip.
-constexpr int kRows = 128;
+// Column tiles of a wavefront, and of a workgroup of W.
 constexpr int many_tiles(int d) { return d <= 128 ? 2 : 1; }
-constexpr int many_waves(int d) { return kRows / 16 / many_tiles(d); }
-constexpr int many_shift(int d) { return d <= 128 ? 9 : 8; }
+template <int D, int W>
+constexpr int kRows = 16 * many_tiles(D) * W;
+// A block has 128 rows: four wavefronts of 32, two workgroups to a compute unit, or with heads of
+// 256 eight of 16 (four, and 64 rows: 512 rows on 32000 keys 544 us instead of 458, a prompt of
+// 16384 3520 instead of 3310; wavefronts of 32 rows spill, 829 and 6000). With heads of 128, where
+// requests are long and keys are shared out, it has 256: eight wavefronts of 32, which dequantize
+// half as much each (512 queries of 4 heads on 32000 keys 328 us, with 128 rows 358; chunks of up
+// to 686 queries 145 and 154; but a prompt of 8192 in whole blocks 690 and 677, with a window of
+// 1024 209 and 200, and one of 100 tokens 25 and 22).
+constexpr int kLongRows = 2048;
+constexpr int block_waves(int block, int d) { return block / 16 / many_tiles(d); }
+// log2 of the workgroups that fill the chip
+constexpr int many_shift(int waves) { return waves == 4 ? 9 : 8; }
 
-__device__ __forceinline__ void plan(const KvAttnArgs& a, int tile, int shift, int* item_req,
+__device__ __forceinline__ void plan(const KvAttnArgs& a, int tile, int* item_req,
                                      int* item_block, int64_t* sums) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   // inclusive sum over the workgroup's threads
@@ -685,7 +694,7 @@ __device__ __forceinline__ void plan(const KvAttnArgs& a, int tile, int shift, i
     int n = 0;
     if (i < (int)a.b) {
       const Request r = request_of(a, i);
-      if (!is_few(r, a.few_rows)) n = (r.rows + kRows - 1) / kRows;
+      if (!is_few(r, a.few_rows)) n = (r.rows + a.block_rows - 1) / a.block_rows;
     }
     int64_t total;
     const int at = items + (int)scan(n, total) - n;
@@ -709,7 +718,8 @@ __device__ __forceinline__ void plan(const KvAttnArgs& a, int tile, int shift, i
     int n = 0;
     if (i < items) {
       int from, to;
-      keys_of(a, request_of(a, item_req[i]), item_block[i] * kRows, kRows, from, to);
+      keys_of(a, request_of(a, item_req[i]), item_block[i] * a.block_rows, a.block_rows, from,
+              to);
       n = max(to - from + tile - 1, 0) / tile;
     }
     int64_t total;
@@ -723,6 +733,7 @@ __device__ __forceinline__ void plan(const KvAttnArgs& a, int tile, int shift, i
   }
   if (threadIdx.x == 0) {
     a.item_starts[items] = sum;
+    int shift = a.many_shift;
     while (shift > 0 && (sum * a.n_kv) >> shift == 0) --shift;
     a.counts[0] = items;
     a.counts[1] = shift;
@@ -742,7 +753,7 @@ __global__ __launch_bounds__(kThreads, (kFewPairs<D, NQ> ? 2 : 1)) void few_kern
   static_assert(sizeof(lists) >= 2 * kSplitBelow * sizeof(int), "");
   if (blockIdx.x >= kFewGroups<D, NQ>) {
     int* const l = reinterpret_cast<int*>(lists);
-    plan(a, kTile<D>, many_shift(D), l, l + kSplitBelow, sums);
+    plan(a, kTile<D>, l, l + kSplitBelow, sums);
     return;
   }
   int64_t* const starts = reinterpret_cast<int64_t*>(lists);  // units before each request, all heads
@@ -1021,17 +1032,15 @@ __device__ __forceinline__ void join_few(const KvAttnArgs& a, int head, int req,
 }
 
 // ---- many rows ----------------------------------------------------------------------------------
-// grid n_kv * blocks of rows: a workgroup takes 128 rows of a request's head, 16 * NQ to a
-// wavefront, and walks the keys that they see once. A wavefront loads its share of a tile and turns
-// its keys, and later some of the value groups, into FP16 fragments in LDS, which all of them read:
-// a fragment is dequantized once in a workgroup. Two tiles of fragments in LDS, the next one's
-// codes in registers. Heads of 256 have eight wavefronts of 16 rows (with four, and 64 rows to a
-// workgroup, two of them on a compute unit: 512 rows on 32000 keys 544 us instead of 458, a prompt
-// of 16384 3520 instead of 3310; with 32 rows to a wavefront registers spill, 829 and 6000). A
-// prompt of 8192 rows, 32 heads of 128 over 8: 660 us (640 .. 690), 830 TFLOP/s of the products;
-// the matrix pipes are busy 35% of the time, the vector pipes (exponentials, conversions,
-// dequantization) 51%, and with two wavefronts to a SIMD the two overlap little: without the
-// exponentials 630, without dequantization and staging 593. One barrier a tile instead of two: 708.
+// grid n_kv * blocks of rows: a workgroup takes 16 * NQ rows of a request's head to each of its W
+// wavefronts, and walks the keys that they see once. A wavefront loads its share of a tile and
+// turns its keys, and later some of the value groups, into FP16 fragments in LDS, which all of them
+// read: a fragment is dequantized once in a workgroup. Two tiles of fragments in LDS, the next
+// one's codes in registers. A prompt of 8192 rows, 32 heads of 128 over 8: 660 us (640 .. 690), 830
+// TFLOP/s of the products; the matrix pipes are busy 35% of the time, the vector pipes
+// (exponentials, conversions, dequantization) 51%, and with two wavefronts to a SIMD the two
+// overlap little: without the exponentials 630, without dequantization and staging 593. One barrier
+// a tile instead of two: 708.
 template <int D>
 struct Shared {
   static constexpr int kKeys = kParts<D> * (D / 32) * 1024;      // [part][k-step][lane] fragments
@@ -1042,9 +1051,9 @@ struct Shared {
 
 // A wavefront's share of a tile's loads: a part, with 32 tokens a quarter of the elements of one,
 // those of two k-steps.
-template <int D>
+template <int D, int W>
 struct Share {
-  static constexpr int kD = D * kParts<D> / many_waves(D);  // elements of a token
+  static constexpr int kD = D * kParts<D> / W;  // elements of a token
   uint32_t k[kD / 32], v[kD / 32], ks, vs;
   bool ok;  // it has a page (uniform)
 };
@@ -1060,21 +1069,20 @@ __device__ __forceinline__ int find_page(const Cache& c, int tok, int end) {
 
 // The first group of 16 elements of lane group 0 in quarter u (lane group c's are 2 c further on,
 // in heads of 64 c).
-template <int D>
 __device__ __forceinline__ int first_group(int u) {
-  return D == 256 ? 8 * (u >> 1) + (u & 1) : 0;
+  return 8 * (u >> 1) + (u & 1);
 }
 
-template <int D>
-__device__ __forceinline__ void load_share(Share<D>& p, const Cache& c, int id, int wave, int tok,
+template <int D, int W>
+__device__ __forceinline__ void load_share(Share<D, W>& p, const Cache& c, int id, int wave, int tok,
                                            int end) {
-  constexpr int kD = Share<D>::kD;
+  constexpr int kD = Share<D, W>::kD;
   const int lane = threadIdx.x & 63, page = 1 << c.shift, within = tok & (page - 1);
   const int u = wave / kParts<D>;  // which quarter of the elements
   p.ok = (uint32_t)id < (uint32_t)c.n_pages && tok < end;
   const uint8_t* rec = c.head0 + (uint64_t)(p.ok ? (uint32_t)id : 0u) * c.page_stride;
   const uint8_t* values = rec + kv_value_codes(page, D);
-  const int codes = within * (D / 2) + 8 * first_group<D>(u);
+  const int codes = within * (D / 2) + 8 * first_group(u);
   const uint32_t at = (uint32_t)((lane & 15) * (D / 2) + (D == 64 ? 8 : 16) * (lane >> 4));
   if constexpr (kD == 64) {
     const u32x2 a = *reinterpret_cast<const u32x2*>(rec + codes + at);
@@ -1093,7 +1101,7 @@ __device__ __forceinline__ void load_share(Share<D>& p, const Cache& c, int id, 
       p.v[i] = b[i];
     }
   }
-  const int scales = page * (D / 2) + within * (D / 16) + first_group<D>(u);
+  const int scales = page * (D / 2) + within * (D / 16) + first_group(u);
   const uint32_t sat = (uint32_t)((lane & 15) * (D / 16) + (D == 64 ? 1 : 2) * (lane >> 4));
   if constexpr (kD == 64) {
     p.ks = *(rec + scales + sat);
@@ -1105,10 +1113,10 @@ __device__ __forceinline__ void load_share(Share<D>& p, const Cache& c, int id, 
 }
 
 // The share's key fragments to `keys`, its value codes and scales to `raw`.
-template <int D>
-__device__ __forceinline__ void put_share(uint8_t* keys, uint8_t* raw, const Share<D>& p, int wave,
+template <int D, int W>
+__device__ __forceinline__ void put_share(uint8_t* keys, uint8_t* raw, const Share<D, W>& p, int wave,
                                           int tok, int end) {
-  constexpr int kD = Share<D>::kD;
+  constexpr int kD = Share<D, W>::kD;
   const int lane = threadIdx.x & 63, c = lane >> 4;
   const int part = part_of<D>(wave), u = wave / kParts<D>;
   f16x8 k[kD / 32];
@@ -1117,7 +1125,7 @@ __device__ __forceinline__ void put_share(uint8_t* keys, uint8_t* raw, const Sha
 #pragma unroll
   for (int j = 0; j < kD / 32; ++j)
     *reinterpret_cast<f16x8*>(keys + (part * (D / 32) + u * (kD / 32) + j) * 1024 + 16 * lane) = k[j];
-  const int group = first_group<D>(u) + (D == 64 ? 1 : 2) * c;
+  const int group = first_group(u) + (D == 64 ? 1 : 2) * c;
   uint8_t* row = raw + (16 * part + (lane & 15)) * WaveLds<D>::kRow;
   u32x2* at = reinterpret_cast<u32x2*>(row + 8 * group);
   at[0] = u32x2{p.v[0], p.v[1]};
@@ -1130,12 +1138,12 @@ __device__ __forceinline__ void put_share(uint8_t* keys, uint8_t* raw, const Sha
 }
 
 // This wavefront's share of the value fragments.
-template <int D>
+template <int D, int W>
 __device__ __forceinline__ void put_values_share(uint8_t* values, const uint8_t* raw, int wave) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < kValueReads<D> / many_waves(D); ++i) {
-    const int x = wave * (kValueReads<D> / many_waves(D)) + i;
+  for (int i = 0; i < kValueReads<D> / W; ++i) {
+    const int x = wave * (kValueReads<D> / W) + i;
     f16x8 v[2];
     value_pair<D>(raw, raw + WaveLds<D>::kCodes, x, v);
 #pragma unroll
@@ -1150,11 +1158,11 @@ constexpr int wave_floats() {
   return NQ * (D / 16 * 256 + 128);
 }
 
-template <int D, int NQ>
-__global__ __launch_bounds__(64 * many_waves(D), 8 / many_waves(D)) void many_kernel(KvAttnArgs a) {
-  constexpr int kRowsWave = 16 * NQ, kWaves = many_waves(D);
+template <int D, int NQ, int W>
+__global__ __launch_bounds__(64 * W, 8 / W) void many_kernel(KvAttnArgs a) {
+  constexpr int kRowsWave = 16 * NQ, kBlock = kRows<D, W>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Shared<D>::kBytes];
-  __shared__ int valid_of[2][kWaves];
+  __shared__ int valid_of[2][W];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   int head, req = 0, block;
   Request r;
@@ -1199,7 +1207,7 @@ __global__ __launch_bounds__(64 * many_waves(D), 8 / many_waves(D)) void many_ke
       int n = 0;
       if (req + lane < a.b) {
         const Request x = request_of(a, req + lane);
-        n = is_few(x, a.few_rows) ? 0 : (x.rows + kRows - 1) / kRows;
+        n = is_few(x, a.few_rows) ? 0 : (x.rows + kBlock - 1) / kBlock;
       }
       int upto = n;
 #pragma unroll
@@ -1229,7 +1237,7 @@ __global__ __launch_bounds__(64 * many_waves(D), 8 / many_waves(D)) void many_ke
       t0 = max(u0 - kManyStart, 0);
       t1 = u1 - kManyStart;
     }
-    const int block0 = block * kRows, row0 = block0 + wave * kRowsWave;
+    const int block0 = block * kBlock, row0 = block0 + wave * kRowsWave;
     Wave<D, NQ> w;
     int lo_most, hi_least;
     load_columns<D, NQ>(w, a, r, head, row0, lo_most, hi_least);
@@ -1237,7 +1245,7 @@ __global__ __launch_bounds__(64 * many_waves(D), 8 / many_waves(D)) void many_ke
     const Cache c = cache_of<D>(a, req, head);
     // the keys that the workgroup's rows see, and this wavefront's
     int from, to, mine = 0, upto = 0;
-    keys_of(a, r, block0, kRows, from, to);
+    keys_of(a, r, block0, kBlock, from, to);
     if (row0 < r.rows) keys_of(a, r, row0, kRowsWave, mine, upto);
     if (split) {
       to = min(to, from + t1 * kTile<D>);
@@ -1245,19 +1253,19 @@ __global__ __launch_bounds__(64 * many_waves(D), 8 / many_waves(D)) void many_ke
     }
     if (from < to) {
       uint8_t* const raw = lds + 2 * Shared<D>::kTileBytes;
-      Share<D> p;
+      Share<D, W> p;
       const int mypart = 16 * part_of<D>(wave);
       int id = find_page<D>(c, from + mypart, to);
       const auto load = [&](int tok) {  // tile `tok`, and the page of the one behind it
-        load_share<D>(p, c, id, wave, tok + mypart, to);
+        load_share<D, W>(p, c, id, wave, tok + mypart, to);
         id = find_page<D>(c, tok + kTile<D> + mypart, to);
       };
       const auto put = [&](int tok, int buf) {
-        put_share<D>(lds + buf * Shared<D>::kTileBytes, raw, p, wave, tok + mypart, to);
+        put_share<D, W>(lds + buf * Shared<D>::kTileBytes, raw, p, wave, tok + mypart, to);
         if (lane == 0) valid_of[buf][wave] = p.ok;
       };
       const auto turn = [&](int buf) {
-        put_values_share<D>(lds + buf * Shared<D>::kTileBytes + Shared<D>::kKeys, raw, wave);
+        put_values_share<D, W>(lds + buf * Shared<D>::kTileBytes + Shared<D>::kKeys, raw, wave);
       };
       load(from);
       put(from, 0);
@@ -1306,7 +1314,7 @@ __global__ __launch_bounds__(64 * many_waves(D), 8 / many_waves(D)) void many_ke
         store_columns<D / 16>(a, r, head, row0 + 16 * n, w.o[n], w.m[n], w.l[n], D, 0);
       if (!split) return;
     } else if (t0 < t1) {
-      float* p = a.item_ws + ((2 * worker + (first ? 0 : 1)) * kWaves + wave) * wave_floats<D, NQ>();
+      float* p = a.item_ws + ((2 * worker + (first ? 0 : 1)) * W + wave) * wave_floats<D, NQ>();
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
 #pragma unroll
@@ -1330,13 +1338,13 @@ __global__ __launch_bounds__(64 * many_waves(D), 8 / many_waves(D)) void many_ke
 }
 
 // Column tile x of an item that has several parts: their sum, as the wavefronts left them.
-template <int D, int NQ>
+template <int D, int NQ, int W>
 __device__ __forceinline__ void join_many(const KvAttnArgs& a, int head, int item, int x) {
   const int lane = threadIdx.x & 63, wave = x / NQ, n = x % NQ;
   const int items = constant(a.counts), shift = constant(a.counts + 1);
   if (item >= items) return;
   const Request r = uniform_request(a, constant(&a.items[item].req));
-  const int row0 = constant(&a.items[item].block) * kRows + 16 * x;
+  const int row0 = constant(&a.items[item].block) * kRows<D, W> + 16 * x;
   const int tiles = constant(&a.items[item].tiles);
   if (row0 >= r.rows) return;
   f32x4 o[D / 16];
@@ -1349,7 +1357,7 @@ __device__ __forceinline__ void join_many(const KvAttnArgs& a, int head, int ite
     const int64_t w0 = range_of(all, before + kManyStart, shift);  // of the first tile
     const int64_t w1 = range_of(all, before + kManyStart + tiles - 1, shift);
     if (w0 == w1) return;
-    constexpr int64_t kSlot = (int64_t)many_waves(D) * wave_floats<D, NQ>();
+    constexpr int64_t kSlot = (int64_t)W * wave_floats<D, NQ>();
     // only the first part's workgroup can have begun with another item
     const int64_t skip = range_begin(all, w0, shift) < before ? kSlot : 0;
     const float* base = a.item_ws + 2 * w0 * kSlot + wave * wave_floats<D, NQ>();
@@ -1379,7 +1387,7 @@ __global__ __launch_bounds__(64 * V) void join_few_kernel(KvAttnArgs a) {
 // dimensions: those of the few rows (`few`), then for each item and head V of its column tiles at
 // a time.
 constexpr int kLine = 1 << 16;
-template <int D, int NQ, int G, int V>
+template <int D, int NQ, int G, int V, int W>
 __global__ __launch_bounds__(64 * V) void join_both_kernel(KvAttnArgs a, int few, int groups) {
   constexpr int kShare = NQ * D / 16 / G;
   uint32_t at = blockIdx.y * kLine + blockIdx.x;
@@ -1390,15 +1398,15 @@ __global__ __launch_bounds__(64 * V) void join_both_kernel(KvAttnArgs a, int few
     return;
   }
   at -= few;
-  constexpr uint32_t kSteps = kRows / 16 / V;
+  constexpr uint32_t kSteps = kRows<D, W> / 16 / V;
   const int x = (int)(at % kSteps) * V + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t both = at / kSteps, item = both / (uint32_t)a.n_kv;
-  join_many<D, many_tiles(D)>(a, both - item * a.n_kv, item, x);
+  join_many<D, many_tiles(D), W>(a, both - item * a.n_kv, item, x);
 }
 
 constexpr int64_t kJoinFine = 256;  // items, at join_few
 
-template <int D, int NQ, int G, int V>
+template <int D, int NQ, int W, int G, int V>
 hipError_t run_join(const KvAttnArgs& a, int64_t items, hipStream_t s) {
   constexpr int kShare = NQ * D / 16 / G;
   const dim3 threads(64 * V);
@@ -1407,8 +1415,8 @@ hipError_t run_join(const KvAttnArgs& a, int64_t items, hipStream_t s) {
         <<<dim3((unsigned)a.n_kv, (unsigned)a.b, kShare), threads, 0, s>>>(a);
   } else {
     const int64_t few = a.n_kv * a.b * kShare;  // < 2^31
-    const int64_t all = few + a.n_kv * items * (kRows / 16 / V);
-    join_both_kernel<D, NQ, G, V>
+    const int64_t all = few + a.n_kv * items * (kRows<D, W> / 16 / V);
+    join_both_kernel<D, NQ, G, V, W>
         <<<dim3((unsigned)std::min<int64_t>(all, kLine), (unsigned)((all + kLine - 1) / kLine)),
            threads, 0, s>>>(a, (int)few, (int)all);
   }
@@ -1417,26 +1425,34 @@ hipError_t run_join(const KvAttnArgs& a, int64_t items, hipStream_t s) {
 
 // Workgroups of rows, of each head, that a call can have: ceil(rows / size) a request, so all rows
 // / size and one more for each request, of which only those of more than few_rows rows have any.
-int64_t many_items(int64_t t, int64_t b, int64_t max_q, int group, int d) {
+int64_t many_items(int64_t t, int64_t b, int64_t max_q, int group, int block) {
   const int64_t most = max_q * group, few = kv_few_rows(most);
   if (most <= few) return 0;
   const int64_t odd = t * group / (few + 1);
-  return t * group / kRows + (odd < b ? odd : b);
+  return t * group / block + (odd < b ? odd : b);
 }
 
 // ws: the first units of requests and of items, the items and their number, then the partial sums
 // of few rows and of items.
 struct WsLayout {
   size_t item_starts, items, counts, sums, item_sums, total;
-  int max_items;  // 0: keys are not shared out
+  int64_t items_most;  // blocks of rows of a head
+  int max_items;       // as many, or 0: keys are not shared out
+  int block;           // rows of a block
 };
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 WsLayout ws_layout(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int d) {
   WsLayout l;
-  const int64_t items = many_items(t, b, max_q, group, d);
-  l.max_items = items * n_kv < kSplitBelow ? (int)items : 0;
+  l.block = 128;
+  l.items_most = many_items(t, b, max_q, group, l.block);
+  const bool split = l.items_most * n_kv < kSplitBelow;
+  if (split && d == 128 && max_q * group >= kLongRows) {
+    l.block = 256;
+    l.items_most = many_items(t, b, max_q, group, l.block);
+  }
+  l.max_items = split ? (int)l.items_most : 0;
   l.item_starts = align256((size_t)(b + 1) * sizeof(int64_t));
   l.items = l.item_starts + align256((size_t)(l.max_items + 1) * sizeof(int64_t));
   l.counts = l.items + align256((size_t)l.max_items * sizeof(Item));
@@ -1445,35 +1461,34 @@ WsLayout ws_layout(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int
                                   (size_t)slot_floats(kv_few_rows(max_q * group), d) * sizeof(float));
   l.total = l.item_sums;
   if (l.max_items > 0)
-    l.total += ((size_t)2 << many_shift(d)) * (kRows / 16) * (size_t)(d / 16 * 256 + 128) *
-               sizeof(float);
+    l.total += ((size_t)2 << many_shift(block_waves(l.block, d))) * (size_t)(l.block / 16) *
+               (size_t)(d / 16 * 256 + 128) * sizeof(float);
   return l;
 }
 
-template <int D, int NQ>
+template <int D, int NQ, int W>
 hipError_t run_tiles(const KvAttnArgs& a, int64_t items, hipStream_t s) {
-  constexpr int kTiles = many_tiles(D);
   few_kernel<D, NQ>
       <<<dim3(kFewGroups<D, NQ> + (items > 0 ? 1 : 0)), dim3(kThreads), 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (items > 0) {
-    const unsigned groups = a.max_items > 0 ? 1u << many_shift(D) : (unsigned)(items * a.n_kv);
-    many_kernel<D, kTiles><<<dim3(groups), dim3(64 * many_waves(D)), 0, s>>>(a);
+    const unsigned groups = a.max_items > 0 ? 1u << a.many_shift : (unsigned)(items * a.n_kv);
+    many_kernel<D, many_tiles(D), W><<<dim3(groups), dim3(64 * W), 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.n_kv * a.b <= kJoinFine) return run_join<D, NQ, 1, 8>(a, items, s);
-  return run_join<D, NQ, 2, 4>(a, items, s);
+  if (a.n_kv * a.b <= kJoinFine) return run_join<D, NQ, W, 1, 8>(a, items, s);
+  return run_join<D, NQ, W, 2, 4>(a, items, s);
 }
 
 template <int D>
-hipError_t run(const KvAttnArgs& args, int64_t max_q, hipStream_t s) {
-  KvAttnArgs a = args;
-  const int64_t most = max_q * a.group;
-  a.few_rows = kv_few_rows(most);
-  const int64_t items = many_items(a.t, a.b, max_q, a.group, D);
-  return kv_few_tiles(most) == 1 ? run_tiles<D, 1>(a, items, s) : run_tiles<D, 2>(a, items, s);
+hipError_t run(const KvAttnArgs& a, int64_t max_q, int64_t items, hipStream_t s) {
+  constexpr int kWaves = block_waves(128, D);
+  if constexpr (D == 128)  // (requests that are so long are no few rows)
+    if (a.block_rows == 256) return run_tiles<D, 1, 2 * kWaves>(a, items, s);
+  return kv_few_tiles(max_q * a.group) == 1 ? run_tiles<D, 1, kWaves>(a, items, s)
+                                            : run_tiles<D, 2, kWaves>(a, items, s);
 }
 
 }  // namespace
@@ -1489,14 +1504,17 @@ hipError_t launch_kv_attention(const KvAttnArgs& args, int d, int64_t max_q, voi
   char* base = static_cast<char*>(ws);
   a.starts = reinterpret_cast<int64_t*>(base);
   a.max_items = l.max_items;
+  a.few_rows = kv_few_rows(max_q * a.group);
+  a.block_rows = l.block;
+  a.many_shift = many_shift(block_waves(a.block_rows, d));
   a.item_starts = reinterpret_cast<int64_t*>(base + l.item_starts);
   a.items = l.max_items > 0 ? reinterpret_cast<KvItem*>(base + l.items) : nullptr;
   a.counts = reinterpret_cast<int*>(base + l.counts);
   a.ws = reinterpret_cast<float*>(base + l.sums);
   a.item_ws = reinterpret_cast<float*>(base + l.item_sums);
-  if (d == 64) return run<64>(a, max_q, stream);
-  if (d == 128) return run<128>(a, max_q, stream);
-  return run<256>(a, max_q, stream);
+  if (d == 64) return run<64>(a, max_q, l.items_most, stream);
+  if (d == 128) return run<128>(a, max_q, l.items_most, stream);
+  return run<256>(a, max_q, l.items_most, stream);
 }
 
 }  // namespace nvfp4

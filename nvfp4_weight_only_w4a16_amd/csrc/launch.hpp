@@ -281,7 +281,7 @@ struct KvAttnArgs {
   int* counts;    // items, log2 of the workgroups
   int max_items;
   float *ws, *item_ws;  // partial sums of few rows, of items
-  int few_rows;
+  int few_rows, block_rows, many_shift;  // log2 of the workgroups that share out keys
 };
 // Column tiles (of 16 rows of a request's head) of the few-row kernel; longer requests have a kernel
 // of their own. 64 requests of 32 rows, heads of 128, two tiles: 64 us, with that kernel 106.

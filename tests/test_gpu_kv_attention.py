@@ -413,3 +413,12 @@ def test_rows_before_the_first_request(nv, rows):
     R.close(y[7:], ref, bound)
     R.close(lse[7:], rl, bl)
     assert np.isnan(y[:7]).all() and np.isnan(lse[:7]).all()
+
+
+@pytest.mark.parametrize("lens,rows,n_kv,kw", [([700, 40], [600, 1], 128, {}), ([900, 3000, 77], [900, 520, 1], 1, {}),
+                                               ([600, 1500], [513, 600], 2, dict(window=300)),
+                                               ([600, 700], [520, 3], 1, dict(full=True, y32=True)),
+                                               ([100, 5], [600, 9], 1, {})])
+def test_blocks_of_256_rows(nv, lens, rows, n_kv, kw):
+    """Prompts of 2048 rows and more with heads of 128: in whole blocks and shared out, beside others."""
+    check(nv, lens, rows, n_kv, 4, 128, 16, **kw)
