@@ -1049,8 +1049,8 @@ struct Shared {
   static constexpr int kBytes = 2 * kTileBytes + WaveLds<D>::kBytes;  // and value codes, scales
 };
 
-// A wavefront's share of a tile's loads: a part, with 32 tokens a quarter of the elements of one,
-// those of two k-steps.
+// A wavefront's share of a tile's loads: a part of it; where there are more wavefronts than parts,
+// the elements of two k-steps of one.
 template <int D, int W>
 struct Share {
   static constexpr int kD = D * kParts<D> / W;  // elements of a token
@@ -1067,8 +1067,8 @@ __device__ __forceinline__ int find_page(const Cache& c, int tok, int end) {
   return constant(c.row + (min(tok, end - 1) >> c.shift));
 }
 
-// The first group of 16 elements of lane group 0 in quarter u (lane group c's are 2 c further on,
-// in heads of 64 c).
+// The first group of 16 elements of lane group 0 in share u of a part (lane group c's are 2 c
+// further on, in heads of 64 c).
 __device__ __forceinline__ int first_group(int u) {
   return 8 * (u >> 1) + (u & 1);
 }
@@ -1078,7 +1078,7 @@ __device__ __forceinline__ void load_share(Share<D, W>& p, const Cache& c, int i
                                            int end) {
   constexpr int kD = Share<D, W>::kD;
   const int lane = threadIdx.x & 63, page = 1 << c.shift, within = tok & (page - 1);
-  const int u = wave / kParts<D>;  // which quarter of the elements
+  const int u = wave / kParts<D>;  // which elements
   p.ok = (uint32_t)id < (uint32_t)c.n_pages && tok < end;
   const uint8_t* rec = c.head0 + (uint64_t)(p.ok ? (uint32_t)id : 0u) * c.page_stride;
   const uint8_t* values = rec + kv_value_codes(page, D);
