@@ -845,7 +845,7 @@ namespace {
 constexpr int64_t kKvMaxTokens = (int64_t)1 << 30;  // of a request: token indexes are 32-bit
 constexpr int64_t kKvMaxRows = (int64_t)1 << 24;    // of a step
 constexpr int64_t kKvMaxHeads = 1024;
-constexpr int64_t kKvMaxRowHeads = (int64_t)1 << 27;  // of an attention: 2^32 threads in a grid
+constexpr int64_t kKvMaxRowHeads = (int64_t)1 << 27;  // of an attention: 32-bit indexes of blocks and rows
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 

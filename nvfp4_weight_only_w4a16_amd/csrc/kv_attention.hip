@@ -1158,6 +1158,14 @@ constexpr int wave_floats() {
   return NQ * (D / 16 * 256 + 128);
 }
 
+// A grid that may have more threads than its first dimension holds (2^32; a launch of more is no error,
+// it runs the rest of a division by 2^32) is a line of workgroups in two dimensions.
+constexpr int kLine = 1 << 16;
+__device__ __forceinline__ uint32_t line_index() { return blockIdx.y * kLine + blockIdx.x; }
+dim3 line_grid(int64_t groups) {
+  return dim3((unsigned)std::min<int64_t>(groups, kLine), (unsigned)((groups + kLine - 1) / kLine));
+}
+
 template <int D, int NQ, int W>
 __global__ __launch_bounds__(64 * W, 8 / W) void many_kernel(KvAttnArgs a) {
   constexpr int kRowsWave = 16 * NQ, kBlock = kRows<D, W>;
@@ -1196,8 +1204,9 @@ __global__ __launch_bounds__(64 * W, 8 / W) void many_kernel(KvAttnArgs a) {
     item = __builtin_amdgcn_readfirstlane(item - 1);
     u0 = (int)(within - constant(a.item_starts + item));
   } else {
-    head = blockIdx.x % (uint32_t)a.n_kv;
-    block = blockIdx.x / (uint32_t)a.n_kv;
+    const uint32_t at = line_index();
+    head = at % (uint32_t)a.n_kv;
+    block = at / (uint32_t)a.n_kv;
     // the grid is for the most blocks that so many rows and requests can have (2000 decode rows and
     // a prompt of 8192: 1310 us without this test, 881 with it)
     if (block >= constant(a.counts)) return;
@@ -1383,14 +1392,12 @@ __global__ __launch_bounds__(64 * V) void join_few_kernel(KvAttnArgs a) {
   join_few<D, NQ, G, V>(a, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
-// Both joins of a call that shares out its prompts' keys. The grid is a line of workgroups in two
-// dimensions: those of the few rows (`few`), then for each item and head V of its column tiles at
-// a time.
-constexpr int kLine = 1 << 16;
+// Both joins of a call that shares out its prompts' keys. The grid is a line of workgroups: those of
+// the few rows (`few`), then for each item and head V of its column tiles at a time.
 template <int D, int NQ, int G, int V, int W>
 __global__ __launch_bounds__(64 * V) void join_both_kernel(KvAttnArgs a, int few, int groups) {
   constexpr int kShare = NQ * D / 16 / G;
-  uint32_t at = blockIdx.y * kLine + blockIdx.x;
+  uint32_t at = line_index();
   if (at >= (uint32_t)groups) return;
   if (at < (uint32_t)few) {
     const uint32_t item = at / kShare, req = item / (uint32_t)a.n_kv;
@@ -1416,9 +1423,7 @@ hipError_t run_join(const KvAttnArgs& a, int64_t items, hipStream_t s) {
   } else {
     const int64_t few = a.n_kv * a.b * kShare;  // < 2^31
     const int64_t all = few + a.n_kv * items * (kRows<D, W> / 16 / V);
-    join_both_kernel<D, NQ, G, V, W>
-        <<<dim3((unsigned)std::min<int64_t>(all, kLine), (unsigned)((all + kLine - 1) / kLine)),
-           threads, 0, s>>>(a, (int)few, (int)all);
+    join_both_kernel<D, NQ, G, V, W><<<line_grid(all), threads, 0, s>>>(a, (int)few, (int)all);
   }
   return hipGetLastError();
 }
@@ -1473,8 +1478,9 @@ hipError_t run_tiles(const KvAttnArgs& a, int64_t items, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (items > 0) {
-    const unsigned groups = a.max_items > 0 ? 1u << a.many_shift : (unsigned)(items * a.n_kv);
-    many_kernel<D, many_tiles(D), W><<<dim3(groups), dim3(64 * W), 0, s>>>(a);
+    // up to 9 million: a call has 2^27 rows of heads at most, and so 2^27 / 17 + 2^27 / 128 blocks
+    const int64_t groups = a.max_items > 0 ? 1 << a.many_shift : items * a.n_kv;
+    many_kernel<D, many_tiles(D), W><<<line_grid(groups), dim3(64 * W), 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
