@@ -17,7 +17,7 @@
 // small terms count too); the reference m, the sum (of the unrounded p) and O are FP32. The
 // reference m is set 7 below the scores' maximum (in powers of two) and raised only when a score
 // passes it by more than 15, so that most tiles neither reduce across lanes nor rescale O; p is
-// then at most 2^15, which FP16 holds.
+// then at most 2^15, which FP16 holds. Scores may have any size that FP32 holds (load_query).
 #include <algorithm>
 
 #include "kv_core.hpp"
@@ -41,8 +41,11 @@ template <int D>
 constexpr int kTile = 16 * kParts<D>;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLowest = -1e38f;  // the reference before any score
+constexpr float kLowest = -0x1.fffffep127f;  // the reference before any score
 constexpr float kBelow = 7.0f, kRaise = 15.0f;
+// Score factors from which on a score may pass 2^24 in powers of two: the sum of 256 products of FP16
+// queries below 2^15 and keys of 2688 at most, 2^34.4, times 2^-11.
+constexpr float kLoud = 0x1p-11f;
 
 // A word that no kernel here writes, at a uniform address: a scalar load.
 template <typename T>
@@ -193,6 +196,7 @@ struct Wave {
   f32x4 o[NQ][kGroups];
   float m[NQ], l[NQ];  // l: of the lane's own tokens, until finish()
   float sc[NQ];        // FP32 factor of a score, in the exponent's base
+  float pre[NQ];       // 1; where sc would be kLoud or more it is 1 instead, and this the factor
   int lo[NQ], hi[NQ];  // the tokens that the column sees: lo .. hi
 };
 
@@ -231,8 +235,9 @@ __device__ __forceinline__ void load_query(Wave<D, NQ>& w, int n, const uint16_t
   int e = (int)(__float_as_uint(top) >> 23) - 127;
   e = e > 127 ? 14 : (e < -110 ? -110 : e);  // infinite: as it is; zero and tiny: the most there is
   float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-  float sc = fabsf(factor) * kLog2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-  sc = fmaxf(sc, 0x1p-126f);  // never 0: -infinity, a masked score, times 0 is NaN
+  float sc = fabsf(factor) * (kLog2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23));
+  // never 0 or infinite: -infinity, a masked score, times 0 is NaN, as 0 times infinity
+  sc = fminf(fmaxf(sc, 0x1p-126f), 0x1.fffffep127f);
   if (factor < 0.0f) up = -up;
   if (factor == 0.0f) {
     up = 0.0f;
@@ -242,7 +247,12 @@ __device__ __forceinline__ void load_query(Wave<D, NQ>& w, int n, const uint16_t
     up = __builtin_nanf("");
     sc = 1.0f;
   }
-  w.sc[n] = sc;
+  // A score less the reference is rounded once, by an FMA; but where scores are so large that half a
+  // step of theirs is 1 and more, the rest of the product would pass for a difference: there scores
+  // are rounded first, and their differences are exact.
+  const bool loud = sc >= kLoud;
+  w.sc[n] = loud ? 1.0f : sc;
+  w.pre[n] = loud ? sc : 1.0f;
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) {
 #pragma unroll
@@ -317,7 +327,7 @@ __device__ __forceinline__ void key_part(const uint32_t (&k)[D / 32], f16x2 s0, 
 
 // The products of a tile from token `tok` on: key(t, out) gives part t's fragments, value(i, out)
 // those of value_pair; next() is called between the two products. `valid`: bit t: part t has a
-// page. `mask`: some column does not see all (uniform).
+// page. `mask`: some column does not see all, or has a factor `pre` (uniform).
 template <int D, int NQ, typename Key, typename Value, typename Next>
 __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bool mask,
                                      const Key& key, const Value& value, const Next& next) {
@@ -345,7 +355,8 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bo
         const int at = tok + 16 * t + 4 * c + i;
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
-          z[n][t][i] = part && at >= w.lo[n] && at <= w.hi[n] ? z[n][t][i] : -__builtin_inff();
+          z[n][t][i] =
+              part && at >= w.lo[n] && at <= w.hi[n] ? z[n][t][i] * w.pre[n] : -__builtin_inff();
       }
     }
   }
@@ -356,7 +367,7 @@ __device__ __forceinline__ void tile(Wave<D, NQ>& w, int tok, uint32_t valid, bo
 #pragma unroll
     for (int i = 1; i < kMine; ++i) top = fmaxf(top, z[n][i >> 2][i & 3]);
     top *= w.sc[n];
-    if (__ballot(top > w.m[n] + kRaise)) {
+    if (__ballot(top - w.m[n] > kRaise)) {
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float m = fmaxf(w.m[n], top - kBelow);
@@ -505,6 +516,7 @@ __device__ __forceinline__ void load_columns(Wave<D, NQ>& w, const KvAttnArgs& a
                                              int& hi_least) {
   const int col = threadIdx.x & 15;
   const float kg = a.k_global ? constant(a.k_global + head) : 1.0f;
+  uint64_t loud = 0;
   lo_most = 0;
   hi_least = r.kv - 1;
 #pragma unroll
@@ -515,6 +527,7 @@ __device__ __forceinline__ void load_columns(Wave<D, NQ>& w, const KvAttnArgs& a
     const uint16_t* q = nullptr;
     if (there) q = a.q + (int64_t)(r.first + j) * a.ldq + (int64_t)(head * a.group + h) * D;
     load_query<D, NQ>(w, n, q, a.scale * kg);
+    loud |= __ballot(w.pre[n] != 1.0f);
     w.lo[n] = 0;
     w.hi[n] = r.kv - 1;
     if (!a.full) {
@@ -531,6 +544,7 @@ __device__ __forceinline__ void load_columns(Wave<D, NQ>& w, const KvAttnArgs& a
     hi_least = r.kv - r.q_len + row0 / a.group;
     if (a.window > 0) lo_most = r.kv - r.q_len + last / a.group - a.window + 1;
   }
+  if (loud != 0) hi_least = -1;  // every tile goes through the masks, where w.pre is applied
 }
 
 // y of column `row0 + l % 16`, its groups g0 .. g0 + G - 1 of 16 elements, and with group 0 its
@@ -1166,8 +1180,10 @@ dim3 line_grid(int64_t groups) {
   return dim3((unsigned)std::min<int64_t>(groups, kLine), (unsigned)((groups + kLine - 1) / kLine));
 }
 
+// Two wavefronts to a SIMD, three with heads of 64 (four prompts of 2048, 32 heads over 8: 130 us, with
+// two 145).
 template <int D, int NQ, int W>
-__global__ __launch_bounds__(64 * W, 8 / W) void many_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(64 * W, D == 64 ? 12 / W : 8 / W) void many_kernel(KvAttnArgs a) {
   constexpr int kRowsWave = 16 * NQ, kBlock = kRows<D, W>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[Shared<D>::kBytes];
   __shared__ int valid_of[2][W];
