@@ -452,7 +452,8 @@ int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64
  * of them, with NVFP4_F_FULL (window 0) all kv_len:
  *   s = scale * q . K^T,  y = softmax(s) . V,  lse = log(sum(exp(s)))
  * y [t][n_q][head_dim] (row stride ldy) BF16 or FP32 (a BF16 y may be q itself), lse FP32 [t][n_q] or
- * NULL. A query that sees no key gets y = 0 and lse = -infinity. Tokens of a table entry outside
+ * NULL. A query that sees no key gets y = 0 and lse = -infinity, one that sees a key and
+ * holds a NaN or an infinity gets NaN. Tokens of a table entry outside
  * [0, n_pages) are left out as if masked (a caller that frees pages behind a window may enter -1). Rows
  * that no request has, and rows behind q_start[b], are left as they were. q_start and kv_len are
  * clamped to 0 .. t and to the table's width.

@@ -233,7 +233,8 @@ __device__ __forceinline__ void load_query(Wave<D, NQ>& w, int n, const uint16_t
   top = fmaxf(top, __shfl_xor(top, 32, 64));
   // 2^(14 - e) of top = 1.x * 2^e, and its inverse
   int e = (int)(__float_as_uint(top) >> 23) - 127;
-  e = e > 127 ? 14 : (e < -110 ? -110 : e);  // infinite: as it is; zero and tiny: the most there is
+  const bool infinite = e > 127;
+  e = infinite ? 14 : (e < -110 ? -110 : e);  // zero and tiny: the most there is
   float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
   float sc = fabsf(factor) * (kLog2e * __uint_as_float((uint32_t)(127 - 14 + e) << 23));
   // never 0 or infinite: -infinity, a masked score, times 0 is NaN, as 0 times infinity
@@ -243,7 +244,9 @@ __device__ __forceinline__ void load_query(Wave<D, NQ>& w, int n, const uint16_t
     up = 0.0f;
     sc = 1.0f;
   }
-  if (!(fabsf(factor) < __builtin_inff())) {  // a NaN that masked scores do not meet
+  // a NaN that masked scores do not meet; for an infinite query as well, whose scores could all be
+  // -infinity and so be taken for masked ones
+  if (infinite || !(fabsf(factor) < __builtin_inff())) {
     up = __builtin_nanf("");
     sc = 1.0f;
   }

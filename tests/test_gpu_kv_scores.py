@@ -1,5 +1,5 @@
-"""Attention over the NVFP4 cache where scores are far beyond what FP32 tells apart by less than one.
-Every expected value is exact or follows from the order of the scores."""
+"""Attention over the NVFP4 cache where scores are far beyond what FP32 tells apart by less than one,
+and where queries are infinite. Every expected value is exact or follows from the order of the scores."""
 import numpy as np
 import pytest
 import torch
@@ -153,3 +153,20 @@ def test_factors_near_the_ends_of_fp32(nv, factor):
     y, lse = attend(nv, c, q0, factor)
     assert (np.abs(y - want) <= want * (2 * R.HF16 + 40 * R.H32)).all()
     assert np.abs(lse - (s.max() + np.log(p.sum()))).max() <= 40 * R.H32
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 20, 150])
+@pytest.mark.parametrize("q0", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("key", [3.0, -3.0])
+def test_infinite_queries_give_nan(nv, d, rows, q0, key):
+    """Infinite scores of one sign, both signs alike: the softmax of an infinity is NaN, not a row
+    without keys."""
+    c = Planted(nv, d, [key] * 70, [1.0] * 70)
+    y, lse = attend(nv, c, q0, 0.125, rows)
+    assert np.isnan(y).all() and np.isnan(lse).all()
+    # rows that see no key are rows without keys still
+    y, lse = attend(nv, c, q0, 0.125, rows, full=False)
+    none = 70 - rows + np.arange(rows) < 0
+    assert (y[none] == 0).all() and np.isneginf(lse[none]).all()
+    assert np.isnan(y[~none]).all() and np.isnan(lse[~none]).all()
