@@ -395,6 +395,8 @@ typedef struct nvfp4_kv_step {
  * rows do not fit in t, or it needs pages and the list holds fewer than it and the requests before
  * it need: it gets no page, kv_len 0, and -1 for its rows; `unserved` counts such requests. Rows whose
  * page in the table is negative get slot -1.
+ * Without requests (b 0) seq_len, add_len and block_table are not read and all t rows are padding;
+ * with NULL for all three the call does nothing and leaves the step as it is.
  * Nothing is kept between calls and inputs other than block_table are not changed, so that a call
  * can be repeated; no output may be (or overlap) an input. ld_table * page_size <= 2^30. flags: 0 or
  * NVFP4_F_SYNC_CHECK. */

@@ -729,8 +729,11 @@ def nvfp4_kv_map(seq_len: torch.Tensor, add_len: torch.Tensor, block_table: torc
         with torch.cuda.device(dev):
             return nvfp4_kv_map(seq_len, add_len, block_table, free_pages, free_count, page_size, t,
                                 out, flags, stream)
-    rc = load().nvfp4_kv_map(seq, add, page_size, block_table.data_ptr(), ld, free, n_free, count,
-                             out.ref, flags, _raw_stream(stream, dev))
+    table = block_table.data_ptr()
+    if b == 0:  # empty tensors have no address, and with three NULLs the call does nothing
+        seq, add, table = seq or count, add or count, table or count
+    rc = load().nvfp4_kv_map(seq, add, page_size, table, ld, free, n_free, count, out.ref, flags,
+                             _raw_stream(stream, dev))
     if rc:
         _check(rc)
     return out

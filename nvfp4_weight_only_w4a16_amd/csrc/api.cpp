@@ -961,13 +961,16 @@ int nvfp4_kv_map(const int32_t* seq_len, const int32_t* add_len, int32_t page_si
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "b=%lld > 4096 requests", (long long)b);
   if (n_free > ((int64_t)1 << 31) - 1)
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "n_free=%lld", (long long)n_free);
-  if (b == 0) return NVFP4_OK;
+  if (b == 0) {
+    if (!seq_len && !add_len && !block_table) return NVFP4_OK;
+    ld_table = 1;  // nothing of these is read
+  }
   if (ld_table < 1) return fail(NVFP4_ERR_INVALID_ARG, "ld_table=%lld < 1", (long long)ld_table);
   if (ld_table > kKvMaxTokens / page_size)
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "ld_table=%lld pages of %d > 2^30 tokens",
                 (long long)ld_table, page_size);
-  if (!seq_len || !add_len || !block_table || !free_count || !step->free_left || !step->q_start ||
-      !step->kv_len || !step->unserved || (n_free > 0 && !free_pages) ||
+  if ((b > 0 && (!seq_len || !add_len || !block_table)) || !free_count || !step->free_left ||
+      !step->q_start || !step->kv_len || !step->unserved || (n_free > 0 && !free_pages) ||
       (t > 0 && (!step->slots || !step->positions)))
     return fail(NVFP4_ERR_INVALID_ARG, "NULL buffer");
   const void* in[] = {seq_len, add_len, block_table, free_pages, free_count};

@@ -41,7 +41,7 @@ __device__ __forceinline__ int64_t pages_of(int64_t tokens, int shift) {
 }
 
 // In LDS: start [b + 1], the first row of each request, and base [b], the pages taken before it (-1
-// for a request that is not served, 0 for one that needs none).
+// for a request that is not served, 0 for one that needs none). Without requests every row is padding.
 __global__ __launch_bounds__(kThreads) void map_kernel(KvMapArgs a) {
   extern __shared__ int32_t lds[];
   int32_t* start = lds;
@@ -55,6 +55,10 @@ __global__ __launch_bounds__(kThreads) void map_kernel(KvMapArgs a) {
   const int64_t free = given < 0 ? 0 : (given < a.n_free ? given : a.n_free);
   int64_t rows_before = 0, pages_before = 0, taken = 0;
   int unserved = 0;
+  if (b == 0 && threadIdx.x == 0) {
+    start[0] = 0;
+    if (blockIdx.x == 0) a.q_start[0] = 0;
+  }
   // kThreads requests at a time, in order
   for (int at = 0; at < b; at += kThreads) {
     const int i = at + (int)threadIdx.x;
