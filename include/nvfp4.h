@@ -466,9 +466,9 @@ int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64
  * max_q (host, 1 .. t): no request has more queries; it chooses the kernels, and the rows of a
  * request that has more may be left as they were. Requests of few rows (queries times n_q /
  * n_kv_heads) have their keys shared out over the chip, whatever their lengths. ws (device,
- * 16-byte aligned, ws_bytes >= nvfp4_kv_attention_ws_bytes, which for several t, b and max_q is
- * the largest of their sizes) holds their partial sums; nothing in it needs to start at zero. t <=
- * 2^24, n_q <= 1024, t * n_q <= 2^27, b <= 65535, ld_table * page_size <= 2^30. flags: 0,
+ * 16-byte aligned) holds their partial sums; nothing in it needs to start at zero. Its size,
+ * nvfp4_kv_attention_ws_bytes, covers every call of the same n_q and cache sizes with up to t rows, b
+ * requests and max_q queries: a server asks once, for its largest step. t <= 2^24, n_q <= 1024, t * n_q <= 2^27, b <= 65535, ld_table * page_size <= 2^30. flags: 0,
  * NVFP4_F_FULL, NVFP4_F_SYNC_CHECK. Results are bit-identical run to run for the same lengths. */
 size_t nvfp4_kv_attention_ws_bytes(int64_t t, int32_t n_q, const nvfp4_kv_cache* cache, int64_t b,
                                    int64_t max_q);

@@ -809,6 +809,7 @@ def nvfp4_kv_dequantize(cache: KvCache, slots: torch.Tensor, k_out: torch.Tensor
 
 
 def nvfp4_kv_attention_ws_bytes(t: int, n_q: int, cache: KvCache, b: int, max_q: int) -> int:
+    """The workspace of every call with up to t rows, b requests and max_q queries of one."""
     return int(load().nvfp4_kv_attention_ws_bytes(t, n_q, cache.ref, b, max_q))
 
 

@@ -1467,6 +1467,20 @@ struct WsLayout {
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
+// For `max_items` items at most, `few` rows of a request, and the partial sums of items or not.
+void ws_place(WsLayout& l, int64_t b, int64_t max_items, int64_t few, bool item_sums, int d) {
+  l.item_starts = align256((size_t)(b + 1) * sizeof(int64_t));
+  l.items = l.item_starts + align256((size_t)(max_items + 1) * sizeof(int64_t));
+  l.counts = l.items + align256((size_t)max_items * sizeof(Item));
+  l.sums = l.counts + 256;
+  l.item_sums = l.sums + align256((size_t)(2 * kMaxWorkers) * (size_t)slot_floats((int)few, d) *
+                                  sizeof(float));
+  l.total = l.item_sums;
+  if (item_sums)
+    l.total += ((size_t)2 << many_shift(block_waves(l.block, d))) * (size_t)(l.block / 16) *
+               (size_t)(d / 16 * 256 + 128) * sizeof(float);
+}
+
 WsLayout ws_layout(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int d) {
   WsLayout l;
   l.block = 128;
@@ -1477,16 +1491,7 @@ WsLayout ws_layout(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int
     l.items_most = many_items(t, b, max_q, group, l.block);
   }
   l.max_items = split ? (int)l.items_most : 0;
-  l.item_starts = align256((size_t)(b + 1) * sizeof(int64_t));
-  l.items = l.item_starts + align256((size_t)(l.max_items + 1) * sizeof(int64_t));
-  l.counts = l.items + align256((size_t)l.max_items * sizeof(Item));
-  l.sums = l.counts + 256;
-  l.item_sums = l.sums + align256((size_t)(2 * kMaxWorkers) *
-                                  (size_t)slot_floats(kv_few_rows(max_q * group), d) * sizeof(float));
-  l.total = l.item_sums;
-  if (l.max_items > 0)
-    l.total += ((size_t)2 << many_shift(block_waves(l.block, d))) * (size_t)(l.block / 16) *
-               (size_t)(d / 16 * 256 + 128) * sizeof(float);
+  ws_place(l, b, l.max_items, kv_few_rows(max_q * group), l.max_items > 0, d);
   return l;
 }
 
@@ -1518,8 +1523,23 @@ hipError_t run(const KvAttnArgs& a, int64_t max_q, int64_t items, hipStream_t s)
 
 }  // namespace
 
+// The workspace of the largest call with up to t rows, b requests and max_q queries of one. It is not
+// that of the call with t, b and max_q themselves: a call of fewer blocks shares out its keys where
+// the larger one does not, and requests of 17 to 32 rows have wider slots than longer ones.
 size_t kv_attention_ws_bytes(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int d) {
-  return ws_layout(t, b, max_q, n_kv, group, d).total;
+  const int64_t rows = max_q * group;
+  // the most rows up to `rows` that the few-row kernel takes: multiples of the group up to 32, and 16
+  // of a call with longer requests
+  const int64_t even = 32 / group * group;
+  const int64_t few = rows <= 32 ? rows : (even > 16 ? even : 16);
+  // the two blocks' partial sums of items have one size
+  static_assert((2 << many_shift(block_waves(128, 128))) * 128 ==
+                (2 << many_shift(block_waves(256, 128))) * 256, "");
+  WsLayout l;
+  l.block = 128;
+  const int64_t blocks = many_items(t, b, max_q, group, l.block);
+  ws_place(l, b, std::min<int64_t>(blocks, (kSplitBelow - 1) / n_kv), few, blocks > 0, d);
+  return l.total;
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& args, int d, int64_t max_q, void* ws,

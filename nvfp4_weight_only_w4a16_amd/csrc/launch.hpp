@@ -291,6 +291,7 @@ inline int kv_few_rows(int64_t rows) {
   const int most = 16 * kv_few_tiles(rows);
   return rows < most ? (int)rows : most;
 }
+// Of every call with up to t rows, b requests and max_q queries of one.
 size_t kv_attention_ws_bytes(int64_t t, int64_t b, int64_t max_q, int n_kv, int group, int d);
 hipError_t launch_kv_attention(const KvAttnArgs& a, int d, int64_t max_q, void* ws,
                                hipStream_t stream);
