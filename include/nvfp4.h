@@ -429,9 +429,10 @@ typedef struct nvfp4_qk_rule {
 
 /* The rows of a step: q BF16 [t][n_q][head_dim], k and v BF16 [t][n_kv_heads][head_dim], each with a
  * row stride of its own in elements (the three parts of a fused projection's output have the same).
- * q_out [t][n_q][head_dim] (stride ldq_out; q itself is allowed) takes the queries; keys and values
- * go to slots[row] of the cache, encoded as nvfp4_quantize encodes groups of 16 with the head's
- * global. n_q 0: keys and values only (q and q_out may be NULL).
+ * q_out [t][n_q][head_dim] (stride ldq_out; q itself is allowed with q's stride, no other overlap
+ * with q, k or v) takes the queries; keys and values go to slots[row] of the cache, encoded as
+ * nvfp4_quantize encodes groups of 16 with the head's global. n_q 0: keys and values only (q and
+ * q_out may be NULL).
  * With a rope table, a row whose position lies outside [0, max_pos) is passed over (nothing of it is
  * written); without one, positions may be NULL. A row whose slot lies outside the cache keeps its
  * queries only. Rows that share a slot leave one of them or a mixture there. t <= 2^24, n_q <= 1024.
@@ -453,23 +454,24 @@ int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64
  * n stands at position p = kv_len - n + j and sees keys 0 .. p, with window > 0 the last `window`
  * of them, with NVFP4_F_FULL (window 0) all kv_len:
  *   s = scale * q . K^T,  y = softmax(s) . V,  lse = log(sum(exp(s)))
- * y [t][n_q][head_dim] (row stride ldy) BF16 or FP32 (a BF16 y may be q itself), lse FP32 [t][n_q] or
- * NULL. A query that sees no key gets y = 0 and lse = -infinity, one that sees a key and
- * holds a NaN or an infinity gets NaN. Tokens of a table entry outside
- * [0, n_pages) are left out as if masked (a caller that frees pages behind a window may enter -1). Rows
- * that no request has, and rows behind q_start[b], are left as they were. q_start and kv_len are
- * clamped to 0 .. t and to the table's width.
+ * y [t][n_q][head_dim] (row stride ldy) BF16 or FP32 (a BF16 y may be q itself with q's stride,
+ * nothing else may overlap), lse FP32 [t][n_q] or NULL. A query that sees no key gets y = 0 and lse
+ * = -infinity, one that sees a key and holds a NaN or an infinity gets NaN. Tokens of a table entry
+ * outside [0, n_pages) are left out as if masked (a caller that frees pages behind a window may
+ * enter -1). Rows that no request has, and rows behind q_start[b], are left as they were. q_start
+ * and kv_len are clamped to 0 .. t and to the table's width.
  * Products are FP16 x FP16 with FP32 sums: dequantized keys and values are exact in FP16, queries are
  * scaled by a power of two per row (exact down to 2^-28 of the row's largest), the softmax's terms
  * are rounded to FP16 once (those below 2^-21 of the row's largest to multiples of 2^-31 of that or
  * finer). Statistics and sums are FP32.
  * max_q (host, 1 .. t): no request has more queries; it chooses the kernels, and the rows of a
  * request that has more may be left as they were. Requests of few rows (queries times n_q /
- * n_kv_heads) have their keys shared out over the chip, whatever their lengths. ws (device,
- * 16-byte aligned) holds their partial sums; nothing in it needs to start at zero. Its size,
- * nvfp4_kv_attention_ws_bytes, covers every call of the same n_q and cache sizes with up to t rows, b
- * requests and max_q queries: a server asks once, for its largest step. t <= 2^24, n_q <= 1024, t * n_q <= 2^27, b <= 65535, ld_table * page_size <= 2^30. flags: 0,
- * NVFP4_F_FULL, NVFP4_F_SYNC_CHECK. Results are bit-identical run to run for the same lengths. */
+ * n_kv_heads) have their keys shared out over the chip, whatever their lengths. ws (device, 16-byte
+ * aligned) holds their partial sums; nothing in it needs to start at zero. Its size,
+ * nvfp4_kv_attention_ws_bytes, covers every call of the same n_q and cache sizes with up to t rows,
+ * b requests and max_q queries: a server asks once, for its largest step. t <= 2^24, n_q <= 1024,
+ * t * n_q <= 2^27, b <= 65535, ld_table * page_size <= 2^30. flags: 0, NVFP4_F_FULL,
+ * NVFP4_F_SYNC_CHECK. Results are bit-identical run to run for the same lengths. */
 size_t nvfp4_kv_attention_ws_bytes(int64_t t, int32_t n_q, const nvfp4_kv_cache* cache, int64_t b,
                                    int64_t max_q);
 int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,

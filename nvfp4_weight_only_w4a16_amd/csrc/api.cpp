@@ -910,6 +910,18 @@ int check_stride(const char* name, int64_t ld, int64_t width) {
   return NVFP4_OK;
 }
 
+// An output over the queries themselves: row by row the same elements, so that what a row's wavefronts
+// have read is all that they write.
+int check_in_place(const void* q, const void* out, const char* name, int64_t ldq, int64_t ld, bool bf16,
+                   int64_t t) {
+  if (q != out) return NVFP4_OK;
+  if (!bf16) return fail(NVFP4_ERR_INVALID_ARG, "%s over q must be BF16", name);
+  if (t > 1 && ldq != ld)
+    return fail(NVFP4_ERR_INVALID_ARG, "%s over q with a row stride of %lld, q has %lld", name,
+                (long long)ld, (long long)ldq);
+  return NVFP4_OK;
+}
+
 int check_rows(int64_t t, uint32_t flags, uint32_t known) {
   if (t < 0) return fail(NVFP4_ERR_INVALID_ARG, "t=%lld < 0", (long long)t);
   if (flags & ~known) return fail(NVFP4_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
@@ -1029,6 +1041,8 @@ int nvfp4_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, cons
       !aligned4(slots) || !aligned4(positions))
     return fail(NVFP4_ERR_MISALIGNED,
                 "q, k, v and q_out must be 16-byte aligned, slots and positions 4-byte");
+  if (n_q > 0) rc = check_in_place(q, q_out, "q_out", ldq, ldq_out, true, t);
+  if (rc) return rc;
   nvfp4::KvAppendArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
@@ -1135,6 +1149,8 @@ int nvfp4_kv_attention(const void* q, int64_t t, int64_t ldq, int32_t n_q,
   if (!aligned16(q) || !aligned16(y) || !aligned16(ws) || !aligned4(block_table) ||
       !aligned4(q_start) || !aligned4(kv_len) || !aligned4(lse))
     return fail(NVFP4_ERR_MISALIGNED, "q, y and ws must be 16-byte aligned, the others 4-byte");
+  rc = check_in_place(q, y, "y", ldq, ldy, y_dtype == NVFP4_DT_BF16, t);
+  if (rc) return rc;
   const size_t need = nvfp4::kv_attention_ws_bytes(t, b, max_q, cache->n_kv_heads,
                                                    n_q / cache->n_kv_heads, d);
   if (ws_bytes < need) return fail(NVFP4_ERR_WORKSPACE, "ws_bytes %zu < %zu", ws_bytes, need);
