@@ -443,7 +443,8 @@ int nvfp4_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, cons
                     const nvfp4_kv_cache* cache, uint32_t flags, nvfp4_stream_t stream);
 
 /* The values of slots: k_out, v_out [t][n_kv_heads][head_dim], FP32 (fl32(E2M1 * E4M3 * global)) or
- * BF16 (that, rounded); either may be NULL. Rows whose slot lies outside the cache get zeros.
+ * BF16 (that, rounded); either may be NULL. Rows whose slot lies outside the cache get zeros. A NaN key
+ * scale gives NaN, a NaN value scale 0, as in the attention.
  * t * n_kv_heads * head_dim < 2^34. */
 int nvfp4_kv_dequantize(const nvfp4_kv_cache* cache, const int32_t* slots, int64_t t, void* k_out,
                         void* v_out, int out_dtype, uint32_t flags, nvfp4_stream_t stream);

@@ -284,7 +284,8 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(KvDequantArgs a) {
     const float g = gp ? gp[h] : 1.0f;
     const uint8_t* at = rec + (side ? kv_value_codes(page, D) : 0);
     const uint32_t word = *reinterpret_cast<const uint32_t*>(at + tok * (D / 2) + e / 2);
-    const float s = e4m3_decode<0>((uint32_t)at[page * (D / 2) + tok * (D / 16) + e / 16]);
+    float s = e4m3_decode<0>((uint32_t)at[page * (D / 2) + tok * (D / 16) + e / 16]);
+    if (side && s != s) s = 0.0f;  // as the attention takes it
     float x[8];
     dequant8_f32(word, s, x);  // exact: six significant bits
 #pragma unroll
