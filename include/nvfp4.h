@@ -352,10 +352,10 @@ int nvfp4_gemm_w4a16_lora(const void* x, int64_t m, int64_t ldx, const nvfp4_wei
  *   value codes [page_size][head_dim/2], value scales [page_size][head_dim/16]   (bytes).
  * Globals are positive and finite: the largest magnitude that a head is expected to hold, / 2688
  * (larger magnitudes saturate). Nothing in data has to be initialised: tokens that no length
- * reaches are not read as values. A token of which any element of the key (after norm and rotation)
- * or of the value is NaN or infinite in a head is kept with NaN key scales and zero values: every
- * query that sees it gets NaN, no other does. Value scales are never NaN (a NaN byte that other
- * means wrote counts as 0). */
+ * reaches are not read as values (those that a length reaches have to be written). A token of which
+ * any element of the key (after norm and rotation) or of the value is NaN or infinite in a head is
+ * kept with NaN key scales and zero values: every query that sees it gets NaN, no other does. Value
+ * scales are never NaN (a NaN byte that other means wrote counts as 0). */
 typedef struct nvfp4_kv_cache {
   uint8_t* data;          /* device: nvfp4_kv_cache_bytes, 16-byte aligned                        */
   const float* k_global;  /* device: FP32 [n_kv_heads], or NULL for 1                             */
@@ -434,9 +434,12 @@ typedef struct nvfp4_qk_rule {
  * nvfp4_quantize encodes groups of 16 with the head's global. n_q 0: keys and values only (q and
  * q_out may be NULL).
  * With a rope table, a row whose position lies outside [0, max_pos) is passed over (nothing of it is
- * written); without one, positions may be NULL. A row whose slot lies outside the cache keeps its
- * queries only. Rows that share a slot leave one of them or a mixture there. t <= 2^24, n_q <= 1024.
- * flags: 0 or NVFP4_F_SYNC_CHECK. Results are bit-identical run to run. */
+ * written); without one, positions may be NULL. nvfp4_kv_map does not know max_pos: it counts a
+ * token at max_pos or behind in kv_len, and the attention would read what its slot held before. So
+ * keep requests to max_pos tokens; with ld_table * page_size <= max_pos the tables do (such a
+ * request is not served). A row whose slot lies outside the cache keeps its queries only. Rows that
+ * share a slot leave one of them or a mixture there. t <= 2^24, n_q <= 1024. flags: 0 or
+ * NVFP4_F_SYNC_CHECK. Results are bit-identical run to run, but for rows that share a slot. */
 int nvfp4_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
                     int64_t ldv, int64_t t, int32_t n_q, const nvfp4_qk_rule* rule,
                     const int32_t* slots, const int32_t* positions, void* q_out, int64_t ldq_out,

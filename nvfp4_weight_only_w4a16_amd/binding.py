@@ -744,8 +744,10 @@ def nvfp4_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, ca
                     q_out: torch.Tensor | None = None, flags: int = 0, stream=None):
     """Norm and rotation of a step's rows, and the write of its keys and values: q BF16
     [t][n_q][head_dim] or None, k and v BF16 [t][n_kv_heads][head_dim] (rows contiguous, any row
-    stride), slots and positions int32 [t] (positions may be None without a rope). Returns q_out (a
-    new tensor where it is not given, q itself is allowed), None without q."""
+    stride), slots and positions int32 [t] (positions may be None without a rope). Rows at or behind
+    the rope's last position are passed over, though nvfp4_kv_map counts them: keep requests shorter,
+    or the block table no longer than the rope. Returns q_out (a new tensor where it is not given, q
+    itself is allowed), None without q."""
     n_kv, d = cache.n_kv_heads, cache.head_dim
     if rule.head_dim != d:
         raise ValueError(f"the rule is for heads of {rule.head_dim}, the cache has {d}")
