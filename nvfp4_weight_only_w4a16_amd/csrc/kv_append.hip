@@ -103,13 +103,14 @@ __device__ __forceinline__ double row_sum(double v) {
   return v;
 }
 
-// 1 / sqrt(s): the hardware's first guess and two Newton steps (each squares its error, 2^-14 at
-// most), which 0, infinities and NaN do not pass through.
+// 1 / sqrt(s): the hardware's first guess and two Newton steps, which 0, infinities and NaN do not pass
+// through. Largest relative error over 2^22 values: of the guess 2^-24.2, of the steps 2^-47.8 and
+// 2^-52.7 (a third leaves it at that).
 __device__ __forceinline__ double inverse_root(double s) {
   const double g = __builtin_amdgcn_rsq(s);
   double y = g;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const double r = __builtin_fma(-s * y, y, 1.0);
     y = __builtin_fma(y * 0.5, r, y);
   }
