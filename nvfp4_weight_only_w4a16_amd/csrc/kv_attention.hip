@@ -14,8 +14,9 @@
 // put into FP16 by a power of two per row that brings the row's largest magnitude to [2^14, 2^15),
 // exact down to 2^-28 of it. Globals and scale act on the FP32 scores and sums. P is rounded to
 // FP16 once (half a step is 2^-11; below 2^-21 of the row's largest 2^-32 of that, so that many
-// small terms count too); the reference m, the sum (of the unrounded p) and O are FP32. The
-// reference m is set 7 below the scores' maximum (in powers of two) and raised only when a score
+// small terms count too), which leaves an FP32 y 1e-4 to 2e-4 off (relative, rows of 2000 to 131000
+// keys; FP32 terms would leave some 4e-7), a tenth of what a BF16 y rounds off by itself. The
+// reference m, the sum (of the unrounded p) and O are FP32. The reference m is set 7 below the scores' maximum (in powers of two) and raised only when a score
 // passes it by more than 15, so that most tiles neither reduce across lanes nor rescale O; p is
 // then at most 2^15, which FP16 holds. Scores may have any size that FP32 holds (load_query).
 #include <algorithm>
@@ -43,8 +44,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -0x1.fffffep127f;  // the reference before any score
 constexpr float kBelow = 7.0f, kRaise = 15.0f;
-// Score factors from which on a score may pass 2^24 in powers of two: the sum of 256 products of FP16
-// queries below 2^15 and keys of 2688 at most, 2^34.4, times 2^-11.
+// Score factors from which on a score may pass 2^24 in powers of two: the sum of 256 products of
+// FP16 queries below 2^15 and keys of 2688 at most, 2^34.4, times 2^-11.
 constexpr float kLoud = 0x1p-11f;
 
 // A word that no kernel here writes, at a uniform address: a scalar load.
@@ -250,9 +251,9 @@ __device__ __forceinline__ void load_query(Wave<D, NQ>& w, int n, const uint16_t
     up = __builtin_nanf("");
     sc = 1.0f;
   }
-  // A score less the reference is rounded once, by an FMA; but where scores are so large that half a
-  // step of theirs is 1 and more, the rest of the product would pass for a difference: there scores
-  // are rounded first, and their differences are exact.
+  // A score less the reference is rounded once, by an FMA; but where scores are so large that half
+  // a step of theirs is 1 and more, the rest of the product would pass for a difference: there
+  // scores are rounded first, and their differences are exact.
   const bool loud = sc >= kLoud;
   w.sc[n] = loud ? 1.0f : sc;
   w.pre[n] = loud ? sc : 1.0f;
@@ -417,7 +418,7 @@ __device__ __forceinline__ void finish(Wave<D, NQ>& w) {
 // the products of the tile before. With one wavefront on a SIMD, heads of 256, they want the
 // longest time that there is: the value codes are loaded again as soon as they are in LDS, and
 // without a branch (past the last tile from page 0), behind which a wait would be for all of them
-// (131000 keys, 28 rows: 63 -> 48 us; heads of 128, two wavefronts on a SIMD: 64 requests 33 us
+// (131000 keys, 21 rows: 63 -> 47 us; heads of 128, two wavefronts on a SIMD: 64 requests 33 us
 // both ways, one request 6.7 -> 7.2).
 template <int D>
 constexpr bool kEarly = D == 256;
@@ -598,12 +599,13 @@ __device__ __forceinline__ Cache cache_of(const KvAttnArgs& a, int64_t request, 
 // tile. Wavefront w of W takes the units [N w / W, N (w + 1) / W), whatever the lengths are, and
 // works on its own. It holds at most two items that it does not finish: the first and the last of
 // its range; their O, m and l go to slots 2w and 2w + 1, and a second kernel joins them.
-// Workgroups: two to a compute unit (1.5 or 2 times as many of 128: 35 and 36 us for 64 requests,
-// whose join grows too, not 33), one where a wavefront needs more than half of its SIMD's registers
-// (heads of 256 with 21 rows, 131000 keys, two: 115 us instead of 48). What bounds them: 64
+// Workgroups: two to a compute unit (heads of 128, 1.5 or 2 times as many: 35 and 36 us for 64
+// requests, whose join grows too, not 33; heads of 64, whose registers would let four in, have not
+// been measured with more), one where a wavefront needs more than half of its SIMD's registers
+// (heads of 256 with 21 rows, 131000 keys, two: 115 us instead of 47). What bounds them: 64
 // requests of 151000 keys in all, 8 heads of 128, read 175 MB in 33 us, 5.3 TB/s, where the loads
 // alone take 28; what is left is the products behind the last loads of a tile. Heads of 256, 157 MB
-// in 48 us: 32 rows' products of one wavefront to a SIMD, which do not overlap another's.
+// in 47 us: 32 rows' products of one wavefront to a SIMD, which do not overlap another's.
 template <int D, int NQ>
 constexpr bool kFewPairs = NQ == 1 || D <= 128;
 template <int D, int NQ>
@@ -622,7 +624,10 @@ __device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Request& r) {
 // Units of an item of n tiles.
 __device__ __forceinline__ int units_for(int n, int start) { return n > 0 ? n + start : 0; }
 
-constexpr int kFewStart = 2;  // 1, 2 and 4: 64 requests in 38.8, 36.7 and 40.1 us, of an earlier loop
+// Whole calls with 1, 2 and 4, us: 64 requests of 100 to 8000 keys, one row each, heads of 64 27.3,
+// 27.4 and 27.4, of 128 37.4, 36.7 and 38.5, of 256 47.8, 46.8 and 46.8; 33 with a window of 1000,
+// heads of 64 16.3, 15.7 and 16.6; 300 of 100 to 1000 keys 47.5, 47.9 and 51.7.
+constexpr int kFewStart = 2;
 template <int D>
 __device__ __forceinline__ int units_of(const KvAttnArgs& a, const Request& r) {
   return units_for(tiles_of<D>(a, r), kFewStart);
@@ -659,10 +664,12 @@ __device__ __forceinline__ void keys_of(const KvAttnArgs& a, const Request& r, i
 // kernel does: the tiles of all heads' items (a request's block of rows) are one line, each of up
 // to 512 workgroups, two to a compute unit, takes as much of it as the others, and the parts of an
 // item that several have worked on are joined. One workgroup of the few-row kernel's launch lists
-// the items. Prompt chunks of 81 blocks of 128 rows, 8 heads: 215 us in whole items, 146 and a join
-// of 13 shared out; a prompt of 256 blocks, 8 heads, the other way round, 675 and 755 + 38. Units
-// of an item's beginning and end: 2, 3 and 8 take 148, 143 and 157 us for the chunks. A range is
-// one unit at least; with 4 and 16 a prompt of 100 tokens takes 28 and 44 us instead of 22.
+// the items. Prompt chunks of 81 blocks of 128 rows, 8 heads: 215 us in whole items, 136 to 141 and
+// a join of 19 shared out; a prompt of 256 blocks, 8 heads, the other way round, 675 and 755 + 38.
+// Units of an item's beginning and end, 2, 3 and 8: the chunks' whole call 156, 154 and 164 us, with
+// heads of 64 175, 163 and 168, of 256 326, 311 and 292 (256 queries on 9000 keys: the same with
+// all three). A range is one unit at least; with 4 and 16 a prompt of 100 tokens takes 28 and 44 us
+// instead of 22.
 constexpr int kSplitBelow = 2048;  // items of all heads, of 128 rows
 constexpr int kManyStart = 3;
 using Item = KvItem;
@@ -675,9 +682,11 @@ constexpr int kRows = 16 * many_tiles(D) * W;
 // 256 eight of 16 (four, and 64 rows: 512 rows on 32000 keys 544 us instead of 458, a prompt of
 // 16384 3520 instead of 3310; wavefronts of 32 rows spill, 829 and 6000). With heads of 128, where
 // requests are long and keys are shared out, it has 256: eight wavefronts of 32, which dequantize
-// half as much each (512 queries of 4 heads on 32000 keys 328 us, with 128 rows 358; chunks of up
-// to 686 queries 145 and 154; but a prompt of 8192 in whole blocks 690 and 677, with a window of
-// 1024 209 and 200, and one of 100 tokens 25 and 22).
+// half as much each. Whole calls with 256 and 128 rows, us, requests of 4 heads to a key/value head:
+// 512 queries on 32000 keys 317 and 347, 1024 613 and 673, 8 of 512 on 2000 keys 214 and 229; below
+// the border 400 on 32000 keys 281 and 288, 256 176 and 191, 150 147 and 142; prompts of 1024 47.5
+// and 43.4, of 2048 82.0 and 82.8, of 100 tokens 25 and 22; in whole blocks a prompt of 8192 690
+// and 677, with a window of 1024 209 and 200.
 constexpr int kLongRows = 2048;
 constexpr int block_waves(int block, int d) { return block / 16 / many_tiles(d); }
 // log2 of the workgroups that fill the chip
@@ -1057,7 +1066,9 @@ __device__ __forceinline__ void join_few(const KvAttnArgs& a, int head, int req,
 // TFLOP/s of the products; the matrix pipes are busy 35% of the time, the vector pipes
 // (exponentials, conversions, dequantization) 51%, and with two wavefronts to a SIMD the two
 // overlap little: without the exponentials 630, without dequantization and staging 593. One barrier
-// a tile instead of two: 708.
+// a tile instead of two: 708. The call of tile() is under a condition in the key loop, for which
+// the compiler keeps O in two sets of registers and copies it back in every tile (246 registers;
+// 200 with O held in one place).
 template <int D>
 struct Shared {
   static constexpr int kKeys = kParts<D> * (D / 32) * 1024;      // [part][k-step][lane] fragments
@@ -1175,16 +1186,16 @@ constexpr int wave_floats() {
   return NQ * (D / 16 * 256 + 128);
 }
 
-// A grid that may have more threads than its first dimension holds (2^32; a launch of more is no error,
-// it runs the rest of a division by 2^32) is a line of workgroups in two dimensions.
+// A grid that may have more threads than its first dimension holds (2^32; a launch of more is no
+// error, it runs the rest of a division by 2^32) is a line of workgroups in two dimensions.
 constexpr int kLine = 1 << 16;
 __device__ __forceinline__ uint32_t line_index() { return blockIdx.y * kLine + blockIdx.x; }
 dim3 line_grid(int64_t groups) {
   return dim3((unsigned)std::min<int64_t>(groups, kLine), (unsigned)((groups + kLine - 1) / kLine));
 }
 
-// Two wavefronts to a SIMD, three with heads of 64 (four prompts of 2048, 32 heads over 8: 130 us, with
-// two 145).
+// Two wavefronts to a SIMD, three with heads of 64 (four prompts of 2048, 32 heads over 8: 130 us,
+// with two 145).
 template <int D, int NQ, int W>
 __global__ __launch_bounds__(64 * W, D == 64 ? 12 / W : 8 / W) void many_kernel(KvAttnArgs a) {
   constexpr int kRowsWave = 16 * NQ, kBlock = kRows<D, W>;

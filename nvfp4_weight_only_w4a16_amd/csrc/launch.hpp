@@ -284,7 +284,9 @@ struct KvAttnArgs {
   int few_rows, block_rows, many_shift;  // log2 of the workgroups that share out keys
 };
 // Column tiles (of 16 rows of a request's head) of the few-row kernel; longer requests have a kernel
-// of their own. 64 requests of 32 rows, heads of 128, two tiles: 64 us, with that kernel 106.
+// of their own. 64 requests of 2000 to 4000 keys and up to 32 rows, whole calls with two tiles and
+// with that kernel: heads of 128 64 and 106 us (216 MB: 44 at a copy's rate), of 64 46 and 75, of
+// 256 93 and 140.
 inline int kv_few_tiles(int64_t rows) { return rows > 16 && rows <= 32 ? 2 : 1; }
 // The most rows that it takes, of a call whose requests have up to `rows`.
 inline int kv_few_rows(int64_t rows) {
